@@ -50,7 +50,7 @@ EXPORTS = ["dsa_api_version", "dsa_status_string", "dsa_last_cuda_error", "dsa_k
            "dsa_decode_step_bf16",
            "dsa_topk_workspace_size", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_force_multipass", "dsa_topk_paged",
            "dsa_dcp_topk_workspace_size", "dsa_dcp_topk", "sparse_mla_workspace_size",
-           "sparse_mla_decode", "dsa_dcp_sparse_mla_workspace_size", "dsa_dcp_sparse_mla", "dsa_batch_invariant",
+           "sparse_mla_decode", "dense_mla_workspace_size", "dense_mla_decode", "dsa_dcp_sparse_mla_workspace_size", "dsa_dcp_sparse_mla", "dsa_batch_invariant",
            "dsa_workspace_size", "dsa_decode_step", "dsa_cache_append", "dsa_quantize_index_query",
            "dsa_index_frontend", "dsa_frontend_workspace_size", "dsa_decode_step_frontend",
            "dsa_selftest_wait_timeout"]
@@ -81,6 +81,8 @@ def lib():
             "dsa_dcp_topk": (i32, [P, i64, P, i32, i32, i32, i32, P, P, P, sz, P, P]),
             "sparse_mla_workspace_size": (sz, [i32, i32]),
             "sparse_mla_decode": (i32, [pc, pb, P, P, i32, f32, P, P, P, sz, P, P]),
+            "dense_mla_workspace_size": (sz, [i32, i32]),
+            "dense_mla_decode": (i32, [pc, pb, P, f32, P, P, P, sz, P, P]),
             "dsa_dcp_sparse_mla_workspace_size": (sz, [i32, i32, i32]),
             "dsa_batch_invariant": (i32, [i32]),
             "dsa_dcp_sparse_mla": (i32, [pc, pb, P, P, i32, i32, f32, P, P, P, P, P, sz, P, P]),
@@ -250,6 +252,19 @@ def sparse_mla_decode(cache: PagedCache, batch: Batch, q_mla, idx, sm_scale: flo
                                    float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
            "sparse_mla_decode")
+
+
+def dense_mla_workspace_size(rows: int, max_seq_len: int) -> int:
+    return int(lib().dense_mla_workspace_size(rows, max_seq_len))
+
+
+def dense_mla_decode(cache: PagedCache, batch: Batch, q_mla, sm_scale: float, out, lse, workspace, status,
+                     stream=None):
+    """Exact MLA over every token each row sees (no selection): out [rows, 96, 512] bf16 bits, lse fp32 [rows, 96]."""
+    c, b = cache.struct(), batch.struct()
+    _check(lib().dense_mla_decode(ctypes.byref(c), ctypes.byref(b), _ptr(q_mla), float(sm_scale), _ptr(out), _ptr(lse),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+                                  _stream(stream)), "dense_mla_decode")
 
 
 def batch_invariant(on: bool) -> bool:

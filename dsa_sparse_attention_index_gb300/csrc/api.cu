@@ -296,6 +296,27 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
                            static_cast<cudaStream_t>(stream));
 }
 
+size_t dense_mla_workspace_size(int32_t rows, int32_t max_seq_len) {
+  if (rows < 0 || max_seq_len < 0) return 0;
+  return dense_mla_workspace_bytes(rows, max_seq_len);
+}
+
+dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
+                              float sm_scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream) {
+  dsa_status_t s;
+  if ((s = check_cache(cache)) != DSA_OK) return s;
+  if ((s = check_batch(batch)) != DSA_OK) return s;
+  if (!dev_status) return DSA_ERR_INVALID_ARG;
+  const int rows = batch->batch * batch->queries_per_seq;
+  if (rows == 0) return DSA_OK;
+  if (!q_mla || !out || !lse || !aligned(q_mla, 16) || !aligned(out, 8) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_mla_workspace_bytes(rows, batch->max_seq_len))
+    return DSA_ERR_WORKSPACE;
+  return launch_dense_mla(*cache, *batch, q_mla, sm_scale, out, lse, workspace, dev_status,
+                          static_cast<cudaStream_t>(stream));
+}
+
 size_t dsa_workspace_size(const dsa_batch_t* batch, int32_t k) {
   if (!batch || batch->batch < 0 || k < 1 || k > DSA_MAX_TOPK) return 0;
   const int rows = batch->batch * std::max(1, batch->queries_per_seq);

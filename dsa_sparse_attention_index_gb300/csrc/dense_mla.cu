@@ -1,0 +1,836 @@
+// dense_mla.cu — exact MLA over every token a row sees in the paged cache.
+//
+// The same attention as the sparse kernel (absorbed MLA, 96 heads, keys = all
+// 576 columns of a latent, values = its first 512), without a selection: for
+// layers that have no indexer, contexts too short to select from, caches that
+// eviction holds at a budget, and prefill chunks whose rows see the whole
+// prefix.  For row r, head h and its visible tokens t:
+//   l_t = sm_scale * latent_scale * (q[r][h] . c_t)
+//   O   = latent_scale * sum_t softmax(l)_t c_t[0:512],  LSE = ln sum_t exp(l_t)
+// with c_t the unscaled E4M3 or NVFP4 latent.
+//
+// GB300 design (persistent, one CTA per SM, 10 warps):
+//   * All (row, 64-token page) tiles form one line; CTA c takes an equal run
+//     of it, so ragged batches, one long context and a prefill chunk all fill
+//     every SM to within a tile.  A row that lies in one CTA's run is written
+//     at once; one that crosses runs leaves a partial (normalised fp16 O, max,
+//     sums) per CTA, merged through the log-sum-exp by the combine kernel.
+//   * A tile is one page, read as it lies: warps 4..7 load a page's records
+//     with 16-byte loads a whole tile ahead (in registers), widen them exactly
+//     to bf16 and store 64-dim blocks, 128-byte swizzled, into a ring of 14
+//     value blocks and 2 key-only blocks.  A block is the B operand of QK^T
+//     (K-major, N = 64 tokens) and the A operand of P V (MN-major, M = 128
+//     dims over two blocks); it is freed as soon as its part of PV has run.
+//   * S = Q K^T has the heads on M = 128 rows (96 used).  Q dims 0..447 sit in
+//     shared memory, 448..575 in TMEM, O^T [512 dims x 96 heads] in 384 TMEM
+//     columns, S in 64.
+//   * warp 8 issues QK^T, warp 9 P V; warps 0..3 run the online softmax, one
+//     thread per head, as the sparse kernel does: P rounded to bf16 (the value
+//     products' operand type; the normaliser sums the rounded values, the LSE
+//     the exact ones), O^T rescaled only when a head's maximum grows by more
+//     than 2^8.
+// What bounds it: the shared-memory port.  Per tile QK^T reads 28 x (4 KB of Q
+// + 2 KB of keys) + 8 x 2 KB, PV 16 x (4 KB of values + 3 KB of P), and the
+// widened tile is written once: 370 KB, 2,900 cycles at 128 B a cycle, against
+// 1,630 cycles of tensor time for the 96 used rows.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kTile = kBlock;                          // tokens per tile: one page
+constexpr int kDB = kLatent / 64;                      // 9 blocks of 64 dims
+constexpr int kVB = kValue / 64;                       // 8 of them are values
+constexpr int kQTmemBlocks = 2;                        // Q dims 448..575 in TMEM
+constexpr int kQSmemBlocks = kDB - kQTmemBlocks;       // Q dims 0..447 in shared memory
+constexpr int kQBlockBytes = kHeads * 128;             // 12,288
+constexpr int kBlkBytes = kTile * 128;                 // 8,192: 64 tokens x 64 dims of bf16
+constexpr int kVSlots = 14;                            // ring of value blocks (a tile has 8)
+constexpr int kKSlots = 2;                             // ring of key-only blocks (a tile has 1)
+constexpr int kPBytes = kHeads * 128;                  // 12,288: 64 tokens of bf16 per head
+constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);  // 352 B
+constexpr int kThreads = 320;  // softmax 0-3, loaders 4-7, QK issuer 8, PV issuer 9
+constexpr int kLoadWarp0 = 4;
+constexpr int kLoadWarps = 4;
+constexpr int kQkWarp = 8;
+constexpr int kPvWarp = 9;
+constexpr int kOCols = 4 * kHeads;                     // 384
+constexpr int kSCol = kOCols;                          // 384..447
+constexpr int kQ8Col = kSCol + kTile;                  // 448..511
+static_assert(kQ8Col + 32 * kQTmemBlocks <= 512, "TMEM columns");
+constexpr float kRescaleThreshold = 8.0f;              // log2 units
+constexpr int kMinTiles = 2;                           // tiles per CTA before more CTAs are used
+constexpr int kMaxGrid = 256;                          // CTAs the workspace is sized for
+constexpr int kInvariantTiles = 64;                    // tiles per part in the batch-invariant mode
+
+constexpr int kOffQ = 0;
+constexpr int kOffV = kOffQ + kQSmemBlocks * kQBlockBytes;     // 86,016
+constexpr int kOffK = kOffV + kVSlots * kBlkBytes;             // 200,704
+constexpr int kOffP = kOffK + kKSlots * kBlkBytes;             // 217,088
+constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
+constexpr int kOffBars = kOffAlpha + 512;
+constexpr int kNumBars = 2 * kVSlots + 2 * kKSlots + 8;
+constexpr int kOffMisc = kOffBars + kNumBars * 8;              // TMEM slot, abort flag, scan scratch
+constexpr size_t kSmemBytes = 1024 + kOffMisc + 256;
+static_assert(kOffV % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+constexpr size_t kPartO = (size_t)kHeads * kValue;             // fp16 values of a partial
+
+struct DenseParams {
+  const uint8_t* latent_base;
+  int64_t row_stride;
+  int32_t num_blocks;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  int32_t nq, cap, rows;
+  float logit_scale_log2;  // sm_scale * latent_scale * log2(e)
+  float latent_scale;
+  const uint16_t* q_mla;
+  uint16_t* out;
+  float* lse;
+  uint16_t* opart;  // fp16 [slots][96][512]
+  float* ml;        // [slots][96][4]: max (log2), sum of bf16(p), sum of p
+  int2* row_info;   // [rows]: first slot key, number of parts (0: no token, 1: written by the kernel)
+  int32_t unit;     // tiles of a fixed part in the batch-invariant mode, else 0
+  int32_t* status;
+};
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool bar_or_softmax(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// A part of a row: tiles [t0, t1) of `row`, written to `slot` (< 0: the whole
+// row, written to the outputs).
+struct Segment {
+  int row, vis, t0, t1, slot;
+};
+
+// Walks the CTA's parts.  Every role walks on its own and meets the same parts.
+//   plain:      the CTA's run [pos, hi) of the line of all rows' tiles.  A row
+//               that began before the run, or fills all of it, goes to slot
+//               2 cta, one that goes on behind it to slot 2 cta + 1.
+//   invariant:  parts of `unit` tiles counted over all rows, CTA c taking every
+//               gridDim-th; a part's slot is its number.
+struct Walk {
+  const DenseParams& p;
+  int row;        // next row
+  int64_t start;  // first tile (or part) of `row` on the line
+  int64_t pos, hi;
+
+  __device__ int visible(int r) const {
+    int len = p.seq_lens[r / p.nq];
+    len = len < 0 ? 0 : (len > p.cap ? p.cap : len);
+    return visible_len(len, p.nq, r % p.nq);
+  }
+  __device__ bool next(Segment& s) {
+    while (pos < hi && row < p.rows) {
+      const int vis = visible(row);
+      const int tiles = (vis + kTile - 1) / kTile;
+      const int64_t n = p.unit ? (tiles + p.unit - 1) / p.unit : tiles;
+      if (pos >= start + n) {
+        start += n;
+        ++row;
+        continue;
+      }
+      s.row = row;
+      s.vis = vis;
+      if (p.unit) {
+        const int u = (int)(pos - start);
+        s.t0 = u * p.unit;
+        s.t1 = min(tiles, s.t0 + p.unit);
+        s.slot = n == 1 ? -1 : (int)pos;
+        pos += gridDim.x;
+      } else {
+        s.t0 = (int)(pos - start);
+        s.t1 = (int)min((int64_t)tiles, hi - start);
+        const bool ends = start + n <= hi;
+        s.slot = s.t0 > 0 ? 2 * (int)blockIdx.x : (ends ? -1 : 2 * (int)blockIdx.x + 1);
+        pos = start + s.t1;
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// The line's length and this CTA's place on it, by all threads.  CTA 0 also
+// writes row_info.  `scratch`: 16 int64 of shared memory.
+__device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
+  Walk w{p, 0, 0, 0, 0};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kThreads / 32;
+  auto count = [&](int r) -> int64_t {
+    if (r >= p.rows) return 0;
+    const int tiles = (w.visible(r) + kTile - 1) / kTile;
+    return p.unit ? (tiles + p.unit - 1) / p.unit : tiles;
+  };
+  int64_t sum = 0;
+  for (int r = threadIdx.x; r < p.rows; r += kThreads) sum += count(r);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < kWarps; ++i) total += scratch[i];
+  __syncthreads();
+  const int64_t per = p.unit ? 1 : max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kMinTiles);
+  w.pos = (int64_t)blockIdx.x * per;
+  w.hi = p.unit ? total : min(w.pos + per, total);
+  // the row that holds w.pos: a block scan over the rows, kThreads at a time
+  if (threadIdx.x == 0) scratch[12] = p.rows;
+  int64_t base = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kThreads) {
+    const int r = r0 + threadIdx.x;
+    const int64_t n = count(r);
+    int64_t inc = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int64_t before = base;
+    for (int i = 0; i < warp; ++i) before += scratch[i];
+    const int64_t first = before + inc - n;
+    if (n > 0 && w.pos >= first && w.pos < first + n) {
+      scratch[12] = r;
+      scratch[13] = first;
+    }
+    if (blockIdx.x == 0 && r < p.rows) {
+      if (p.unit) {
+        p.row_info[r] = make_int2((int)first, (int)n);
+      } else {
+        const int64_t c0 = first / per;
+        p.row_info[r] = make_int2((int)c0, n == 0 ? 0 : (int)((first + n - 1) / per - c0 + 1));
+      }
+    }
+    for (int i = 0; i < kWarps; ++i) base += scratch[i];
+    if (blockIdx.x != 0 && base > w.pos) break;  // uniform: base and w.pos are the block's
+  }
+  __syncthreads();
+  w.row = (int)scratch[12];
+  w.start = scratch[13];
+  return w;
+}
+
+// 16 E4M3 bytes -> 16 bf16, exactly.
+__device__ __forceinline__ void widen_e4m3(const uint4& v, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) e4m3x4_to_bf16x4(w[q], o[2 * q], o[2 * q + 1]);
+}
+
+template <bool kNV>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ DenseParams p) {
+  constexpr int kRec = kNV ? kNvRec : kLatent;
+  constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, kFmtBF16, 0, 0, 128, kTile);
+  constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, kFmtBF16, 1, 0, 128, kHeads);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + kOffBars;
+  auto vfull = [&](int s) { return bars + 8u * s; };
+  auto vempty = [&](int s) { return bars + 8u * (kVSlots + s); };
+  auto kfull = [&](int s) { return bars + 8u * (2 * kVSlots + s); };
+  auto kempty = [&](int s) { return bars + 8u * (2 * kVSlots + kKSlots + s); };
+  const uint32_t bars2 = bars + 8u * (2 * kVSlots + 2 * kKSlots);
+  const uint32_t q_full = bars2, q8_full = bars2 + 8, s_full = bars2 + 16, s_empty = bars2 + 24, p_full = bars2 + 32,
+                 pv_done = bars2 + 40, o_free = bars2 + 48, drain = bars2 + 56;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
+  float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kVSlots; ++s) {
+      mbar_init(vfull(s), kLoadWarps);
+      mbar_init(vempty(s), 1);
+    }
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(kfull(s), kLoadWarps);
+      mbar_init(kempty(s), 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q8_full, 4);
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 1);
+    mbar_init(o_free, 4);
+    mbar_init(drain, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmap_q);
+  }
+  if (warp == kQkWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  grid_dep_wait();  // the lengths and the cache may come from the previous kernel
+  Walk walk = make_walk(p, scratch);
+  grid_dep_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Segment sg;
+
+  if (warp == kQkWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------ QK issuer
+      const uint64_t q_desc = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSw128);
+      const uint32_t q_lo = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
+      const uint32_t v_lo0 = (uint32_t)smem_desc(sbase + kOffV, 16, 1024, kLayoutSw128);
+      const uint32_t k_lo0 = (uint32_t)smem_desc(sbase + kOffK, 16, 1024, kLayoutSw128);
+      uint32_t it = 0, seg = 0;
+      bool ok = true, q_pending = false;
+      const uint32_t d = tmem + kSCol;
+      while (ok && walk.next(sg)) {
+        // the previous part's last S tile has been read by the softmax, so its QK^T has completed: Q may go
+        if (seg > 0) ok = mbar_wait(s_empty, (it & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(q_full, kQSmemBlocks * kQBlockBytes);
+        for (int kb = 0; kb < kQSmemBlocks; ++kb)
+          tma_load_2d(sbase + kOffQ + kb * kQBlockBytes, &tmap_q, kb * 64, sg.row * kHeads, q_full);
+        q_pending = true;
+        ok = mbar_wait(q_full, seg & 1, abort_flag, p.status) && mbar_wait(q8_full, seg & 1, abort_flag, p.status);
+        if (!ok) break;
+        q_pending = false;
+        ++seg;
+        for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
+          ok = mbar_wait(s_empty, (it & 1) ^ 1, abort_flag, p.status) &&
+               mbar_wait(kfull(it % kKSlots), (it / kKSlots) & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_lo = k_lo0 + (it % kKSlots) * (kBlkBytes / 16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // dims 512..575: A from TMEM
+            mma_bf16_tmem_a(d, tmem + kQ8Col + 32 + 8 * kk, desc64(k_lo + 2 * kk, hi), kIdescQK, kk ? 1u : 0u);
+          mma_commit(kempty(it % kKSlots));
+          uint32_t n = it * kVB;
+#pragma unroll 1
+          for (int kb = 0; kb < kVB; ++kb, ++n) {
+            const uint32_t slot = n % kVSlots;
+            ok = mbar_wait(vfull(slot), (n / kVSlots) & 1, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v_lo = v_lo0 + slot * (kBlkBytes / 16);
+            if (kb < kQSmemBlocks) {
+              const uint32_t a_lo = q_lo + kb * (kQBlockBytes / 16);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(d, desc64(a_lo + 2 * kk, hi), desc64(v_lo + 2 * kk, hi), kIdescQK, 1u);
+            } else {  // dims 448..511: A from TMEM
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_tmem_a(d, tmem + kQ8Col + 8 * kk, desc64(v_lo + 2 * kk, hi), kIdescQK, 1u);
+            }
+          }
+          if (ok) mma_commit(s_full);
+        }
+      }
+      if (q_pending) mbar_wait_drain(q_full, seg & 1, 10000000ull);
+      // both issuers' MMAs complete before TMEM is released
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0, 10000000ull);
+    }
+  } else if (warp == kPvWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------ PV issuer
+      const uint64_t a_desc = smem_desc(sbase + kOffV, kBlkBytes, 1024, kLayoutSw128);
+      const uint32_t a_lo0 = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
+      const uint64_t p_desc = smem_desc(sbase + kOffP, 16, 1024, kLayoutSw128);
+      const uint32_t p_lo = (uint32_t)p_desc, p_hi = (uint32_t)(p_desc >> 32);
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      while (ok && walk.next(sg)) {
+        // the previous part's O^T has been read
+        if (seg > 0) ok = mbar_wait(o_free, (seg - 1) & 1, abort_flag, p.status);
+        ++seg;
+        for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
+          ok = mbar_wait(p_full, it & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb) {
+            const uint32_t slot = (it * kVB + 2 * mb) % kVSlots;  // even: the pair does not wrap
+            const uint32_t a_lo = a_lo0 + slot * (kBlkBytes / 16);
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_bf16(tmem + mb * kHeads, desc64(a_lo + 2 * ks * 64, a_hi), desc64(p_lo + 2 * ks, p_hi), kIdescPV,
+                       (t > sg.t0 || ks > 0) ? 1u : 0u);
+            mma_commit(vempty(slot));
+            mma_commit(vempty(slot + 1));
+          }
+          mma_commit(pv_done);
+        }
+      }
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0, 10000000ull);
+    }
+  } else if (warp >= kLoadWarp0) {
+    // ------------------------------------------------ loaders: page -> bf16 blocks
+    // Thread (token, half): 32 dims of each block.  Its 16 code bytes of a block
+    // (32 for E4M3) are loaded a whole tile before they are widened and stored.
+    constexpr int kW = kNV ? 1 : 2;  // 16-byte words per block and thread
+    const int lt = threadIdx.x - kLoadWarp0 * 32;
+    const int tok = lt >> 1, half = lt & 1;
+    uint4 buf[kVB][kW], tail[2], sc[2];
+    const uint8_t* rec = nullptr;  // null: a bad table entry
+    int row = -1, t = 0, t1 = 0;
+    // the next tile of the walk
+    auto advance = [&]() -> bool {
+      if (t >= t1) {
+        if (!walk.next(sg)) return false;
+        row = sg.row;
+        t = sg.t0;
+        t1 = sg.t1;
+      }
+      const int r = p.block_table[(int64_t)(row / p.nq) * p.max_blocks + t];
+      ++t;
+      rec = nullptr;
+      if (r >= 0 && r < p.num_blocks)
+        rec = p.latent_base + (int64_t)r * p.row_stride + tok * kRec;
+      else
+        report(p.status, DSA_ERR_BOUNDS);
+      return true;
+    };
+    auto ld = [&](int off) {
+      return rec ? __ldg(reinterpret_cast<const uint4*>(rec + off)) : make_uint4(0, 0, 0, 0);
+    };
+    auto load_tail = [&]() {
+      constexpr int kTailOff = kNV ? kValue / 2 + kValue / 16 : kValue;
+      tail[0] = ld(kTailOff + 32 * half);
+      tail[1] = ld(kTailOff + 32 * half + 16);
+      if (kNV) {
+        sc[0] = ld(kValue / 2);
+        sc[1] = ld(kValue / 2 + 16);
+      }
+    };
+    auto load_block = [&](int kb) {
+      if (kNV) {
+        buf[kb][0] = ld(32 * kb + 16 * half);
+      } else {
+        buf[kb][0] = ld(64 * kb + 32 * half);
+        buf[kb][kW - 1] = ld(64 * kb + 32 * half + 16);
+      }
+    };
+    auto store_unit = [&](uint8_t* blk, int u, const uint32_t (&o)[8]) {
+      const uint32_t off = (uint32_t)(tok * 128 + half * 64 + u * 32);
+      *reinterpret_cast<uint4*>(blk + swz128(off)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(blk + swz128(off + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    auto publish = [&](uint32_t bar) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    bool have = advance();
+    if (have) {
+      load_tail();
+#pragma unroll
+      for (int kb = 0; kb < kVB; ++kb) load_block(kb);
+    }
+    uint32_t it = 0;
+    while (have) {
+      uint32_t o[8];
+      bool ok = mbar_wait(kempty(it % kKSlots), ((it / kKSlots) & 1) ^ 1, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      uint8_t* kblk = smem + kOffK + (it % kKSlots) * kBlkBytes;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        widen_e4m3(tail[u], o);
+        store_unit(kblk, u, o);
+      }
+      publish(kfull(it % kKSlots));
+      // this tile's scales: units 4 kb + 2 half + u, as bytes of the 32
+      uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
+      const bool more = advance();
+      if (more) load_tail();
+      uint32_t n = it * kVB;
+#pragma unroll
+      for (int kb = 0; kb < kVB; ++kb, ++n) {
+        const uint32_t slot = n % kVSlots;
+        ok = mbar_wait(vempty(slot), ((n / kVSlots) & 1) ^ 1, abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        uint8_t* blk = smem + kOffV + slot * kBlkBytes;
+        if (kNV) {
+          const uint32_t pair = half ? scw[kb] >> 16 : scw[kb];
+          nvfp4x16_to_bf16x16(buf[kb][0].x, buf[kb][0].y, pair & 0xFFu, o);
+          store_unit(blk, 0, o);
+          nvfp4x16_to_bf16x16(buf[kb][0].z, buf[kb][0].w, (pair >> 8) & 0xFFu, o);
+          store_unit(blk, 1, o);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            widen_e4m3(buf[kb][u * (kW - 1)], o);
+            store_unit(blk, u, o);
+          }
+        }
+        publish(vfull(slot));
+        if (more) load_block(kb);
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++it;
+      have = more;
+    }
+  } else {
+    // ------------------------------------------------ softmax (thread = head) and the parts' outputs
+    const int h = threadIdx.x;
+    const bool live = h < kHeads;
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      {
+        // Q dims 448..575 into TMEM (every QK^T of the previous part has completed)
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q_mla + ((int64_t)sg.row * kHeads + (live ? h : 0)) * kLatent + 64 * kQSmemBlocks);
+        uint4 v[8 * kQTmemBlocks];
+#pragma unroll
+        for (int c = 0; c < 8 * kQTmemBlocks; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 8 * kQTmemBlocks; ++c)
+          tmem_st4(lane_base + kQ8Col + 4 * c, v[c].x, v[c].y, v[c].z, v[c].w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q8_full);
+      }
+      float m_used = -INFINITY, l_round = 0.f, l_exact = 0.f;
+      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
+        ok = mbar_wait(s_full, it & 1, abort_flag, p.status);
+        if (bar_or_softmax(!ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t r[kTile];
+        tmem_ld32(lane_base + kSCol, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_ld32(lane_base + kSCol + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+        const int valid = sg.vis - t * kTile;
+        float x[kTile];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (valid >= kTile) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) {
+            x[j] = __uint_as_float(r[j]) * p.logit_scale_log2;
+            mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) {
+            x[j] = j < valid ? __uint_as_float(r[j]) * p.logit_scale_log2 : -INFINITY;
+            mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          }
+        }
+        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = live && m_tile > m_used + kRescaleThreshold;
+        if (bar_or_softmax(grow)) {
+          const float m_new = grow ? m_tile : m_used;
+          const float alpha = (m_used == -INFINITY) ? 0.f : ex2f(m_used - m_new);
+          if (live) alpha_s[h] = alpha;
+          l_round *= alpha;
+          l_exact *= alpha;
+          m_used = m_new;
+          if (t > sg.t0) {
+            ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+            if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 12; ++c) {
+              uint32_t o[32];
+              const uint32_t ta = lane_base + (c / 3) * kHeads + (c % 3) * 32;
+              tmem_ld32(ta, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha_s[(c % 3) * 32 + j]);
+              tmem_st32(ta, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        uint32_t pk[kTile / 2];
+        if (m_used != -INFINITY) {
+          float sr[2] = {0.f, 0.f}, se[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < kTile; j += 2) {
+            const float p0 = ex2f(x[j] - m_used), p1 = ex2f(x[j + 1] - m_used);
+            const __nv_bfloat162 bb = __floats2bfloat162_rn(p0, p1);
+            const float2 back = __bfloat1622float2(bb);
+            sr[0] += back.x;
+            sr[1] += back.y;
+            se[0] += p0;
+            se[1] += p1;
+            pk[j >> 1] = *reinterpret_cast<const uint32_t*>(&bb);
+          }
+          l_round += sr[0] + sr[1];
+          l_exact += se[0] + se[1];
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTile / 2; ++j) pk[j] = 0;
+        }
+        // the P buffer was last read by the PV of the tile before
+        ok = it == 0 || mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+        if (bar_or_softmax(!ok)) { ok = false; break; }
+        if (live) {
+          uint8_t* prow = smem + kOffP;
+#pragma unroll
+          for (int c = 0; c < kTile / 8; ++c)
+            *reinterpret_cast<uint4*>(prow + swz128(h * 128 + c * 16)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      if (ok) ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+      // ---- the part's O^T: lanes are dims of a 128-dim block, columns heads
+      const bool direct = sg.slot < 0;
+      alpha_s[h] = (live && l_round > 0.f) ? (direct ? p.latent_scale : 1.f) / l_round : 0.f;
+      if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
+      tc_fence_after();
+      if (live) {
+        if (direct)
+          p.lse[(int64_t)sg.row * kHeads + h] =
+              l_exact > 0.f || l_exact != l_exact ? (m_used + log2f(l_exact)) * 0.69314718055994531f : -INFINITY;
+        else
+          reinterpret_cast<float4*>(p.ml)[(int64_t)sg.slot * kHeads + h] = make_float4(m_used, l_round, l_exact, 0.f);
+      }
+      uint16_t* dst = direct ? p.out + (int64_t)sg.row * kPartO : p.opart + (int64_t)sg.slot * kPartO;
+#pragma unroll 1
+      for (int c = 0; c < 12; ++c) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + (c / 3) * kHeads + (c % 3) * 32, o);
+        tmem_ld_wait();
+        uint16_t* col = dst + (int64_t)((c % 3) * 32) * kValue + (c / 3) * 128 + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float v = __uint_as_float(o[j]) * alpha_s[(c % 3) * 32 + j];
+          col[j * kValue] = direct ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+        }
+      }
+      tc_fence_before();
+      bar_or_softmax(false);  // alpha_s is read: the next part may write it
+      if (lane == 0) mbar_arrive(o_free);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kQkWarp) tmem_dealloc(tmem, 512);
+}
+
+// Merge the parts of the rows that crossed CTAs, and fill the rows that see no
+// token.  CTA (row, group): kHpc heads, 64 threads (8 dims each) a head, and
+// 4 / kHpc groups of threads that take every such part, joined in a fixed order.
+template <int kHpc>
+__global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __restrict__ opart,
+                                                            const float* __restrict__ ml,
+                                                            const int2* __restrict__ row_info, int inv,
+                                                            float latent_scale, uint16_t* out, float* lse) {
+  constexpr int kGroups = 4 / kHpc;
+  __shared__ float acc_s[kGroups > 1 ? kGroups - 1 : 1][64][8];
+  grid_dep_wait();  // the parts come from the previous kernel
+  const int row = blockIdx.x, w = threadIdx.x >> 6, th = threadIdx.x & 63;
+  const int h = blockIdx.y * kHpc + w % kHpc, grp = w / kHpc;
+  const int2 info = row_info[row];
+  const int parts = info.y;
+  if (parts == 1) return;
+  uint16_t* dst = out + ((int64_t)row * kHeads + h) * kValue + th * 8;
+  if (parts == 0) {
+    if (grp == 0) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(0, 0);
+      *reinterpret_cast<uint2*>(dst + 4) = make_uint2(0, 0);
+      if (th == 0) lse[(int64_t)row * kHeads + h] = -INFINITY;
+    }
+    return;
+  }
+  auto slot_of = [&](int s) -> int64_t {
+    return inv ? (int64_t)info.x + s : (s == 0 ? 2 * (int64_t)info.x + 1 : 2 * ((int64_t)info.x + s));
+  };
+  const float4* ml4 = reinterpret_cast<const float4*>(ml);
+  float M = -INFINITY;
+  for (int s = th & 31; s < parts; s += 32) M = fmaxf(M, ml4[slot_of(s) * kHeads + h].x);
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float den = 0.f, ex = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int kU = 4;
+  for (int s0 = grp; s0 < parts; s0 += kU * kGroups) {
+    float4 v[kU];
+    uint4 x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int s = s0 + u * kGroups;
+      v[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (s < parts) {
+        const int64_t slot = slot_of(s);
+        v[u] = ml4[slot * kHeads + h];
+        x[u] = *reinterpret_cast<const uint4*>(opart + (slot * kHeads + h) * kValue + th * 8);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const float e = v[u].x == -INFINITY ? 0.f : ex2f(v[u].x - M);
+      const float wt = e * v[u].y;  // a part is normalised by its own sum
+      den += wt;
+      ex += e * v[u].z;
+      const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&xs[i]));
+        a[2 * i] = fmaf(wt, f.x, a[2 * i]);
+        a[2 * i + 1] = fmaf(wt, f.y, a[2 * i + 1]);
+      }
+    }
+  }
+  if constexpr (kGroups > 1) {
+    __shared__ float2 sum_s[kGroups - 1];
+    if (grp > 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc_s[grp - 1][th][i] = a[i];
+      if (th == 0) sum_s[grp - 1] = make_float2(den, ex);
+    }
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int g = 0; g < kGroups - 1; ++g) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] += acc_s[g][th][i];
+      den += sum_s[g].x;
+      ex += sum_s[g].y;
+    }
+  }
+  const float inv_den = latent_scale / den;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(a[2 * i] * inv_den, a[2 * i + 1] * inv_den);
+    o[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+  *reinterpret_cast<uint2*>(dst + 4) = make_uint2(o[2], o[3]);
+  if (th == 0) lse[(int64_t)row * kHeads + h] = (M + log2f(ex)) * 0.69314718055994531f;
+}
+
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int64_t max_tiles(int rows, int max_len) { return (int64_t)rows * ((std::max(max_len, 0) + kTile - 1) / kTile); }
+
+// Partial slots for `rows` rows of at most max_len tokens.
+int64_t dense_slots(int rows, int max_len, bool inv) {
+  if (inv) {
+    const int64_t tiles = (std::max(max_len, 0) + kTile - 1) / kTile;
+    return std::max<int64_t>(1, rows * ((tiles + kInvariantTiles - 1) / kInvariantTiles));
+  }
+  return 2 * std::max<int64_t>(1, std::min<int64_t>(kMaxGrid, max_tiles(rows, max_len)));
+}
+
+}  // namespace
+
+size_t dense_mla_workspace_bytes(int rows, int max_len) {
+  const int64_t slots = dense_slots(rows, max_len, mla_batch_invariant_on());
+  return al256((size_t)rows * sizeof(int2)) + al256((size_t)slots * kPartO * 2) + al256((size_t)slots * kHeads * 16);
+}
+
+dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,
+                              uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st) {
+  const int rows = bt.batch * bt.queries_per_seq;
+  const bool inv = mla_batch_invariant_on();  // read once: the parts and the workspace layout agree
+  const int64_t slots = dense_slots(rows, bt.max_seq_len, inv);
+  const bool nv = c.latent_format == DSA_LATENT_NVFP4;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    if (cuda_status(cudaFuncSetAttribute(dense_mla_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemBytes)) != DSA_OK ||
+        cuda_status(cudaFuncSetAttribute(dense_mla_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemBytes)) != DSA_OK)
+      return DSA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  CUtensorMap qmap;
+  const uint64_t dims[2] = {(uint64_t)kLatent, (uint64_t)rows * kHeads};
+  const uint64_t strides[1] = {(uint64_t)kLatent * 2};
+  const uint32_t box[2] = {64, (uint32_t)kHeads};
+  if (!encode_tmap(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_mla, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return DSA_ERR_CUDA;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  DenseParams p = {};
+  p.row_info = reinterpret_cast<int2*>(w);
+  w += al256((size_t)rows * sizeof(int2));
+  p.opart = reinterpret_cast<uint16_t*>(w);
+  w += al256((size_t)slots * kPartO * 2);
+  p.ml = reinterpret_cast<float*>(w);
+  p.latent_base = static_cast<const uint8_t*>(c.base) + c.latent_off;
+  p.row_stride = c.row_stride;
+  p.num_blocks = c.num_blocks;
+  p.block_table = bt.block_table;
+  p.max_blocks = bt.max_blocks_per_seq;
+  p.seq_lens = bt.seq_lens;
+  p.nq = bt.queries_per_seq;
+  p.cap = (int)std::min<int64_t>((int64_t)bt.max_blocks_per_seq * kBlock, bt.max_seq_len);
+  p.rows = rows;
+  p.logit_scale_log2 = sm_scale * c.latent_scale * 1.4426950408889634f;
+  p.latent_scale = c.latent_scale;
+  p.q_mla = q_mla;
+  p.out = out;
+  p.lse = lse;
+  p.unit = inv ? kInvariantTiles : 0;
+  p.status = status;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(max_tiles(rows, p.cap), std::min(num_sms(), kMaxGrid)));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)want);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  if (cuda_status(cudaLaunchKernelEx(&cfg, nv ? dense_mla_kernel<true> : dense_mla_kernel<false>, qmap, p)) != DSA_OK)
+    return DSA_ERR_CUDA;
+  // few rows: a CTA a head, its parts over four groups of threads; many rows: four heads a CTA
+  const bool few = rows <= 64;
+  cfg.gridDim = dim3((unsigned)rows, (unsigned)(few ? kHeads : kHeads / 4));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  count_launches(1);
+  if (cuda_status(cudaLaunchKernelEx(&cfg, few ? dense_combine_kernel<1> : dense_combine_kernel<4>,
+                                     (const uint16_t*)p.opart, (const float*)p.ml, (const int2*)p.row_info, inv ? 1 : 0,
+                                     c.latent_scale, out, lse)) != DSA_OK)
+    return DSA_ERR_CUDA;
+  return launch_status();
+}
+
+}  // namespace dsa

@@ -77,6 +77,7 @@ dsa_status_t launch_dcp_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t
 size_t mla_workspace_bytes(int rows, int k);
 // Process-wide batch-invariant mode of the MLA chunking; returns the previous setting.
 int mla_batch_invariant(int on);
+bool mla_batch_invariant_on();
 // Tokens of idx one MLA chunk may hold.
 int mla_max_chunk();
 // The MLA kernel alone over per-row chunk tables: nseg chunks per row,
@@ -92,6 +93,10 @@ dsa_status_t launch_sparse_mla_partials(const dsa_paged_cache_t& c, const dsa_ba
 dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
                                const int32_t* idx, int k, float sm_scale, uint16_t* out, float* lse,
                                void* workspace, int32_t* status, cudaStream_t st, const int32_t* phys = nullptr);
+// Attention over every visible token (dense_mla.cu).
+size_t dense_mla_workspace_bytes(int rows, int max_len);
+dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,
+                              uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st);
 dsa_status_t launch_wait_selftest(int64_t limit_ns, int32_t* status, cudaStream_t st);
 dsa_status_t launch_cache_append(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* new_latent,
                                  const uint16_t* new_key, int32_t* status, cudaStream_t st);

@@ -808,6 +808,7 @@ std::atomic<int> g_batch_invariant{0};
 }  // namespace
 
 int mla_batch_invariant(int on) { return g_batch_invariant.exchange(on ? 1 : 0); }
+bool mla_batch_invariant_on() { return g_batch_invariant.load(std::memory_order_relaxed) != 0; }
 
 // Token chunks per row: enough CTAs for one wave over the SMs (one CTA per SM
 // fits), at most 16; the workspace is sized for up to 256 SMs.  In the
@@ -822,7 +823,7 @@ static int mla_nsplit(int rows, int k, bool inv) {
   return std::max((k + kMaxChunk - 1) / kMaxChunk,
                   std::min(mla_nsplit_max(rows, k, false), num_sms() / std::max(1, rows)));
 }
-static bool batch_invariant() { return g_batch_invariant.load(std::memory_order_relaxed) != 0; }
+static bool batch_invariant() { return mla_batch_invariant_on(); }
 
 size_t mla_workspace_bytes(int rows, int k) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };

@@ -23,6 +23,7 @@
  *   dsa_topk(_bf16, _noalloc) top-k per row, ties to the lower index
  *   dsa_topk_paged           the step's top-k, with the selected tokens' physical KV rows
  *   sparse_mla_decode        exact sparse MLA over the selected tokens
+ *   dense_mla_decode         exact MLA over every visible token
  *   dsa_decode_step(_bf16)   the three stages fused on one stream
  *   dsa_cache_append, dsa_quantize_index_query   the step's front end
  *   dsa_index_frontend       the fused indexer front end (norm, projection,
@@ -292,6 +293,33 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
                                float sm_scale, uint16_t* out, float* lse,
                                void* workspace, size_t workspace_bytes,
                                int32_t* dev_status, void* stream);
+
+/*
+ * Exact MLA over the whole context (no counterpart on the source pages beyond
+ * the definition of the attention itself): sparse_mla_decode's attention with
+ * every visible token selected, for layers without an indexer, contexts too
+ * short to select from, caches that dsa_cache_evict holds at a budget, and
+ * prefill chunks.  For row r, head h and every token t that row r sees:
+ *   c_t       = latent_scale * latent of token t      (576 values, either latent format)
+ *   l_t       = sm_scale * (q[r][h] . c_t)
+ *   out[r][h] = sum_t softmax(l)_t * c_t[0:512]        (bf16, round-to-nearest)
+ *   lse[r][h] = ln sum_t exp(l_t)                       (fp32)
+ * A row that sees no token gets out = 0 and lse = -inf.  A length above
+ * min(max_blocks_per_seq * 64, max_seq_len) is read as that bound, a negative
+ * one as 0.  Any number of rows per sequence up to DSA_MAX_QUERIES_PER_SEQ.
+ *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned
+ *   out       device bf16 bits [rows][96][512], 8-byte aligned;  lse device fp32 [rows][96]
+ *   workspace >= dense_mla_workspace_size(rows, batch->max_seq_len) bytes, 256-B aligned
+ * A table entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS in *dev_status.
+ * Two launches.  The tokens of all rows are split evenly over the SMs, so the
+ * order of a row's sums depends on the batch; in the batch-invariant mode
+ * (dsa_batch_invariant) rows are split every 4,096 tokens instead, and the
+ * workspace size follows the mode at the time of the query.
+ */
+size_t dense_mla_workspace_size(int32_t rows, int32_t max_seq_len);
+dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
+                              float sm_scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
 
 /*
  * Batch-invariant mode (Day-0 post, section "day 0 的零失配 RL", zero-mismatch

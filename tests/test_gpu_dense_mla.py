@@ -1,0 +1,158 @@
+"""dense_mla_decode (exact MLA over every visible token) against a plain
+64-bit form, at lengths around pages and runs, both latent formats, ragged
+batches, draft rows and prefill chunks, offsets and strides of the pool, and
+its device-side refusals.
+
+Tolerances, from the roundings on the way (half a step of bf16 is 2^-8
+relative, of fp16 2^-11, of fp32 2^-24):
+  logits   fp32 sums of 576 exact products: |dl| <= 576 * 2^-24 * Sum |q c| * sm_scale
+           =: e (plus 2^-22 * |l| for the scaling and the exponential's argument,
+           inside e as Sum |q c| >= |l|)
+  P        rounded to bf16 on both sides of the quotient, which is normalised by the
+           sum of the rounded values: Sum p |v - o| * 2^-8 * (1 + 2^-7)
+  logits   move the quotient by at most 2 e * Sum p |v|
+  sums     fp32 over n tokens, n * 2^-24 * Sum p |v| twice (values, normaliser)
+  parts    fp16, 2^-11 * Sum p |v|;  output bf16, 2^-8 |o|
+  LSE      e + n * 2^-24 + 2^-20 * (1 + |lse|)
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import plain64
+from dsa_sparse_attention_index_gb300 import binding, synth
+
+pytestmark = pytest.mark.gpu
+
+FP8, NV = synth.LATENT_FP8, synth.LATENT_NVFP4
+
+
+def run_dense(case, dc, stream=None, ws=None):
+    rows = case.rows
+    out = torch.full((rows, 96, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, 96), float("nan"), dtype=torch.float32, device="cuda")
+    if ws is None:
+        ws = binding.workspace(binding.dense_mla_workspace_size(rows, dc.batch.max_seq_len))
+        ws.fill_(255)   # NaN patterns wherever a part is read that was not written
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.dense_mla_decode(dc.cache, dc.batch, dc.q_mla, case.sm_scale, out, lse, ws, st, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse, st.item()
+
+
+def check_rows(case, out, lse, rows=None):
+    o, l = out.double().cpu(), lse.double().cpu()
+    cached = {}
+    for row in range(case.rows) if rows is None else rows:
+        b = row // case.nq
+        if b not in cached:
+            cached = {b: plain64.latents(case, b)}
+        ro, rl, av, spread, bound = plain64.attend(case, row, c=cached[b])
+        n = max(0, int(case.seq_lens[b]) - (case.nq - 1) + row % case.nq)
+        if n == 0:
+            assert torch.all(o[row] == 0) and torch.all(torch.isneginf(l[row]))
+            continue
+        e = (576 * 2.0 ** -24 * bound)[:, None]
+        tol = 2.0 ** -8 * (1 + 2.0 ** -7) * spread + (2 * e + 2 * n * 2.0 ** -24 + 2.0 ** -11) * av + 2.0 ** -8 * ro.abs()
+        excess = ((o[row] - ro).abs() - tol).max().item()
+        assert excess <= 0, f"row {row}, {n} tokens: out off by {excess} more than {tol.max().item()}"
+        ltol = e[:, 0] + n * 2.0 ** -24 + 2.0 ** -20 * (1 + rl.abs())
+        assert torch.all((l[row] - rl).abs() <= ltol), f"row {row}: lse"
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("lens,nq", [([1], 1), ([64], 1), ([65], 1), ([63, 0, 1, 130], 1), ([997], 1),
+                                     ([129, 700, 2049], 4), ([2, 5, 66], 3), ([5000, 64, 20001, 1], 1),
+                                     ([400], 64), ([100, 31], 32)])
+def test_dense_mla_matches_plain(fmt, lens, nq):
+    case = synth.make_case("dense", seq_lens=lens, nq=nq, seed=100 + len(lens) + nq, latent_format=fmt)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check_rows(case, out, lse)
+
+
+def test_dense_mla_many_sequences():
+    """More sequences than SMs, so a CTA's run holds several rows and a row crosses CTAs."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 400, 333)
+    case = synth.make_case("dense_many", seq_lens=lens, seed=7, latent_format=NV)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check_rows(case, out, lse)
+
+
+def test_dense_mla_prefill_chunk():
+    case = synth.make_case("dense_chunk", seq_lens=[1500], nq=512, seed=8, latent_format=NV)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check_rows(case, out, lse, rows=[0, 1, 63, 64, 255, 256, 300, 510, 511])
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+def test_dense_mla_sharp_heads(fmt):
+    """Logits that grow along the context (the running maximum moves many times) and heads that one token takes."""
+    case = synth.make_case("dense_sharp", seq_lens=[3000], seed=9, latent_format=fmt)
+    q = torch.randn((1, 96, 576), generator=torch.Generator().manual_seed(1)) * torch.linspace(0.0, 60.0, 96)[None, :, None]
+    case = dataclasses.replace(case, q_mla=q.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16))
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check_rows(case, out, lse)
+
+
+def test_dense_mla_layout_and_filler():
+    """Index pages before the latent pages, padding between rows, and NaN codes in every slot behind a context."""
+    case = synth.make_case("dense_layout", seq_lens=[70, 129], seed=10, key_format=synth.KEY_MXFP4, latent_format=NV,
+                           spare_blocks=2)
+    n, rec = case.num_blocks, 64 * 352
+    pool = np.full((n, 384 + rec + 64 * 68 + 256), 0x7F, dtype=np.uint8)
+    pool[:, 256 + 64 * 68 + 128:256 + 64 * 68 + 128 + rec] = case.pool[:, :rec]
+    for b, L in enumerate([70, 129]):
+        r = case.block_table[b, (L - 1) // 64]
+        pool[r, 256 + 64 * 68 + 128 + (L % 64) * 352:256 + 64 * 68 + 128 + rec] = 0x7F
+    moved = dataclasses.replace(case, pool=pool, row_stride=pool.shape[1], latent_off=256 + 64 * 68 + 128, index_off=256)
+    out, lse, st = run_dense(moved, synth.device_case(moved))
+    assert st == 0
+    check_rows(moved, out, lse)
+
+
+def test_dense_mla_invariant_mode():
+    """In the batch-invariant mode a row's bits do not depend on its batch, and stay within the tolerance."""
+    lens = [9000, 4097, 300]
+    case = synth.make_case("dense_inv", seq_lens=lens, seed=11, latent_format=NV)
+    prev = binding.batch_invariant(True)
+    try:
+        out, lse, st = run_dense(case, synth.device_case(case))
+        assert st == 0
+        check_rows(case, out, lse)
+        for b in range(3):
+            one = dataclasses.replace(case, batch=1, seq_lens=case.seq_lens[b:b + 1].copy(),
+                                      block_table=case.block_table[b:b + 1].copy(), q_mla=case.q_mla[b:b + 1].copy(),
+                                      q_index=case.q_index[b:b + 1].copy(), head_w=case.head_w[b:b + 1].copy())
+            o1, l1, st = run_dense(one, synth.device_case(one))
+            assert st == 0
+            assert torch.equal(o1[0], out[b]) and torch.equal(l1[0], lse[b])
+    finally:
+        binding.batch_invariant(prev)
+
+
+def test_dense_mla_bad_page_is_reported():
+    case = synth.make_case("dense_bad", seq_lens=[500, 300], seed=12)
+    for bad in (case.num_blocks, -1, 1 << 30):
+        table = case.block_table.copy()
+        table[1, 2] = bad
+        broken = dataclasses.replace(case, block_table=table)
+        _, _, st = run_dense(broken, synth.device_case(broken))
+        assert st == binding.ERR_BOUNDS
+
+
+def test_dense_mla_lengths_outside_the_table():
+    """A length above the table reads as the table's bound, a negative one as 0."""
+    case = synth.make_case("dense_len", seq_lens=[128, 64], seed=13)
+    dc = synth.device_case(case)
+    dc.batch.seq_lens.copy_(torch.tensor([1 << 30, -5], dtype=torch.int32))
+    out, lse, st = run_dense(case, dc)
+    assert st == 0
+    check_rows(case, out, lse, rows=[0])
+    assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
