@@ -169,7 +169,7 @@ def prepare(case, seed):
         st["mass"] = torch.zeros((batch, ld), dtype=torch.float32, device=dev)
         st["lse"] = torch.stack([plain_logits(st, r)[0].logsumexp(1) for r in range(rows)])
         if own:
-            st["ws"] = binding.workspace(binding.attention_mass_workspace_size(rows, k))
+            st["ws"] = binding.workspace(binding.attention_mass_workspace_size(rows, max(lens), k))
     else:
         keep = case["keep"]
         st.update(keep=keep, sink=case["sink"], recent=case["recent"])
