@@ -50,7 +50,9 @@ EXPORTS = ["dsa_api_version", "dsa_status_string", "dsa_last_cuda_error", "dsa_k
            "dsa_decode_step_bf16",
            "dsa_topk_workspace_size", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_force_multipass", "dsa_topk_paged",
            "dsa_dcp_topk_workspace_size", "dsa_dcp_topk", "sparse_mla_workspace_size",
-           "sparse_mla_decode", "dense_mla_workspace_size", "dense_mla_decode", "dsa_dcp_sparse_mla_workspace_size", "dsa_dcp_sparse_mla", "dsa_batch_invariant",
+           "sparse_mla_decode", "dense_mla_workspace_size", "dense_mla_decode",
+           "dsa_attention_mass_workspace_size", "dsa_attention_mass", "dsa_cache_evict_workspace_size",
+           "dsa_cache_evict", "dsa_dcp_sparse_mla_workspace_size", "dsa_dcp_sparse_mla", "dsa_batch_invariant",
            "dsa_workspace_size", "dsa_decode_step", "dsa_cache_append", "dsa_quantize_index_query",
            "dsa_index_frontend", "dsa_frontend_workspace_size", "dsa_decode_step_frontend",
            "dsa_selftest_wait_timeout"]
@@ -83,6 +85,10 @@ def lib():
             "sparse_mla_decode": (i32, [pc, pb, P, P, i32, f32, P, P, P, sz, P, P]),
             "dense_mla_workspace_size": (sz, [i32, i32]),
             "dense_mla_decode": (i32, [pc, pb, P, f32, P, P, P, sz, P, P]),
+            "dsa_attention_mass_workspace_size": (sz, [i32, i32, i32]),
+            "dsa_attention_mass": (i32, [pc, pb, P, P, P, i32, f32, P, P, i64, P, sz, P, P]),
+            "dsa_cache_evict_workspace_size": (sz, [i32, i32, i32]),
+            "dsa_cache_evict": (i32, [pc, pb, P, i64, i32, i32, i32, pc, P, i32, P, P, i64, P, P, sz, P, P]),
             "dsa_dcp_sparse_mla_workspace_size": (sz, [i32, i32, i32]),
             "dsa_batch_invariant": (i32, [i32]),
             "dsa_dcp_sparse_mla": (i32, [pc, pb, P, P, i32, i32, f32, P, P, P, P, P, sz, P, P]),
@@ -265,6 +271,43 @@ def dense_mla_decode(cache: PagedCache, batch: Batch, q_mla, sm_scale: float, ou
     _check(lib().dense_mla_decode(ctypes.byref(c), ctypes.byref(b), _ptr(q_mla), float(sm_scale), _ptr(out), _ptr(lse),
                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
                                   _stream(stream)), "dense_mla_decode")
+
+
+def attention_mass_workspace_size(rows: int, max_seq_len: int, k: int = 0) -> int:
+    return int(lib().dsa_attention_mass_workspace_size(rows, max_seq_len, k))
+
+
+def attention_mass(cache: PagedCache, batch: Batch, q_mla, lse, sm_scale: float, mass_in, mass_out, workspace, status,
+                   idx=None, stream=None):
+    """mass_out = mass_in (or 0) + every token's attention weight, summed over the rows of its sequence and the heads:
+    fp32 [batch, ld]; over every visible token, or over the top-k's entries when idx is given."""
+    c, b = cache.struct(), batch.struct()
+    if mass_in is not None and mass_in.shape != mass_out.shape:
+        raise ValueError("mass_in and mass_out must have the same shape")
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().dsa_attention_mass(ctypes.byref(c), ctypes.byref(b), _ptr(q_mla), _ptr(lse), _ptr(idx),
+                                    int(idx.shape[1]) if idx is not None else 0, float(sm_scale), _ptr(mass_in),
+                                    _ptr(mass_out), int(mass_out.shape[1]), _ptr(workspace), nbytes, _ptr(status),
+                                    _stream(stream)), "dsa_attention_mass")
+
+
+def cache_evict_workspace_size(batch: int, max_seq_len: int, keep: int) -> int:
+    return int(lib().dsa_cache_evict_workspace_size(batch, max_seq_len, keep))
+
+
+def cache_evict(cache: PagedCache, batch: Batch, mass, keep: int, sink: int, recent: int, dst_cache: PagedCache,
+                dst_block_table, kept_idx, mass_out, new_lens, workspace, status, stream=None):
+    """Keep each sequence's first `sink`, last `recent` and, between them, heaviest tokens (`keep` in all) and move
+    their records into the pages of dst_block_table.  kept_idx int32 [batch, keep], mass_out fp32 [batch, >= keep]
+    or None, new_lens int32 [batch]."""
+    c, b, d = cache.struct(), batch.struct(), dst_cache.struct()
+    if tuple(kept_idx.shape) != (batch.batch, int(keep)):
+        raise ValueError("kept_idx must be [batch, keep]")
+    _check(lib().dsa_cache_evict(ctypes.byref(c), ctypes.byref(b), _ptr(mass), int(mass.shape[1]), int(keep), int(sink),
+                                 int(recent), ctypes.byref(d), _ptr(dst_block_table), int(dst_block_table.shape[1]),
+                                 _ptr(kept_idx), _ptr(mass_out), int(mass_out.shape[1]) if mass_out is not None else 0,
+                                 _ptr(new_lens), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 _ptr(status), _stream(stream)), "dsa_cache_evict")
 
 
 def batch_invariant(on: bool) -> bool:

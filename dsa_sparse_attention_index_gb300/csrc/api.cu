@@ -317,6 +317,76 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
                           static_cast<cudaStream_t>(stream));
 }
 
+size_t dsa_attention_mass_workspace_size(int32_t rows, int32_t max_seq_len, int32_t k) {
+  if (rows < 0 || max_seq_len < 0 || k < 0 || k > DSA_MAX_TOPK) return 0;
+  return mass_workspace_bytes(rows, max_seq_len, k);
+}
+
+dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
+                                const float* lse, const int32_t* idx, int32_t k, float sm_scale, const float* mass_in,
+                                float* mass_out, int64_t ld_mass, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream) {
+  dsa_status_t s;
+  if ((s = check_cache(cache)) != DSA_OK) return s;
+  if ((s = check_batch(batch)) != DSA_OK) return s;
+  if (!dev_status) return DSA_ERR_INVALID_ARG;
+  if (idx ? (k < 1 || k > DSA_MAX_TOPK) : k != 0) return DSA_ERR_INVALID_ARG;
+  const int rows = batch->batch * batch->queries_per_seq;
+  if (rows == 0) return DSA_OK;
+  if (!q_mla || !lse || !mass_out || !aligned(q_mla, 16) || !aligned(lse, 4) || !aligned(idx, 4) ||
+      !aligned(mass_in, 4) || !aligned(mass_out, 4) || ld_mass < batch->max_seq_len)
+    return DSA_ERR_INVALID_ARG;
+  const bool needs = idx || batch->queries_per_seq > 1;
+  if (needs && (!workspace || !aligned(workspace, 256) ||
+                workspace_bytes < mass_workspace_bytes(rows, batch->max_seq_len, k)))
+    return DSA_ERR_WORKSPACE;
+  return launch_attention_mass(*cache, *batch, q_mla, lse, idx, k, sm_scale, mass_in, mass_out, ld_mass, workspace,
+                               dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_cache_evict_workspace_size(int32_t batch, int32_t max_seq_len, int32_t keep) {
+  if (batch < 0 || max_seq_len < 0 || keep < 1) return 0;
+  return evict_workspace_bytes(batch, keep);
+}
+
+dsa_status_t dsa_cache_evict(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const float* mass,
+                             int64_t ld_mass, int32_t keep, int32_t sink, int32_t recent,
+                             const dsa_paged_cache_t* dst_cache, const int32_t* dst_block_table,
+                             int32_t dst_max_blocks, int32_t* kept_idx, float* mass_out, int64_t ld_mass_out,
+                             int32_t* new_lens, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             void* stream) {
+  dsa_status_t s;
+  if ((s = check_cache(cache)) != DSA_OK) return s;
+  if ((s = check_cache(dst_cache)) != DSA_OK) return s;
+  if ((s = check_batch(batch)) != DSA_OK) return s;
+  if (!dev_status) return DSA_ERR_INVALID_ARG;
+  if (keep < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > keep || dst_max_blocks < 1 ||
+      (int64_t)keep > (int64_t)dst_max_blocks * kBlock)
+    return DSA_ERR_INVALID_ARG;
+  // records move as they are: the same formats and the same layer scale on both sides
+  const bool keys8 = cache->key_format == DSA_KEY_FP8_E4M3, dst8 = dst_cache->key_format == DSA_KEY_FP8_E4M3;
+  if (keys8 != dst8 || cache->latent_format != dst_cache->latent_format ||
+      cache->latent_scale != dst_cache->latent_scale)
+    return DSA_ERR_UNSUPPORTED;
+  if (((int64_t)keep + kBlock - 1) / kBlock * batch->batch > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  if (batch->batch == 0) return DSA_OK;
+  if (!mass || !dst_block_table || !kept_idx || !new_lens || new_lens == batch->seq_lens || !aligned(mass, 4) || !aligned(mass_out, 4) ||
+      !aligned(kept_idx, 4) || !aligned(new_lens, 4) || !aligned(dst_block_table, 4) || ld_mass < batch->max_seq_len)
+    return DSA_ERR_INVALID_ARG;
+  if (mass_out) {
+    if (ld_mass_out < keep) return DSA_ERR_INVALID_ARG;
+    // the totals are read while the kept ones are written: no overlap
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(mass), a1 = a0 + (uintptr_t)batch->batch * ld_mass * 4;
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(mass_out), b1 = b0 + (uintptr_t)batch->batch * ld_mass_out * 4;
+    if (a0 < b1 && b0 < a1) return DSA_ERR_INVALID_ARG;
+  }
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < evict_workspace_bytes(batch->batch, keep))
+    return DSA_ERR_WORKSPACE;
+  return launch_cache_evict(*cache, *batch, mass, ld_mass, keep, sink, recent, *dst_cache, dst_block_table,
+                            dst_max_blocks, kept_idx, mass_out, ld_mass_out, new_lens, workspace, dev_status,
+                            static_cast<cudaStream_t>(stream));
+}
+
 size_t dsa_workspace_size(const dsa_batch_t* batch, int32_t k) {
   if (!batch || batch->batch < 0 || k < 1 || k > DSA_MAX_TOPK) return 0;
   const int rows = batch->batch * std::max(1, batch->queries_per_seq);

@@ -39,6 +39,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "run.cuh"
 
 namespace dsa {
 
@@ -173,63 +174,26 @@ struct Walk {
   }
 };
 
-// The line's length and this CTA's place on it, by all threads.  CTA 0 also
-// writes row_info.  `scratch`: 16 int64 of shared memory.
+// This CTA's place on the line, by all threads; CTA 0 also writes row_info.
 __device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
   Walk w{p, 0, 0, 0, 0};
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kWarps = kThreads / 32;
   auto count = [&](int r) -> int64_t {
-    if (r >= p.rows) return 0;
     const int tiles = (w.visible(r) + kTile - 1) / kTile;
     return p.unit ? (tiles + p.unit - 1) / p.unit : tiles;
   };
-  int64_t sum = 0;
-  for (int r = threadIdx.x; r < p.rows; r += kThreads) sum += count(r);
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  for (int i = 0; i < kWarps; ++i) total += scratch[i];
-  __syncthreads();
-  const int64_t per = p.unit ? 1 : max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kMinTiles);
-  w.pos = (int64_t)blockIdx.x * per;
-  w.hi = p.unit ? total : min(w.pos + per, total);
-  // the row that holds w.pos: a block scan over the rows, kThreads at a time
-  if (threadIdx.x == 0) scratch[12] = p.rows;
-  int64_t base = 0;
-  for (int r0 = 0; r0 < p.rows; r0 += kThreads) {
-    const int r = r0 + threadIdx.x;
-    const int64_t n = count(r);
-    int64_t inc = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+  auto each = [&](int r, int64_t first, int64_t n, int64_t per) {
+    if (p.unit) {
+      p.row_info[r] = make_int2((int)first, (int)n);
+    } else {
+      const int64_t c0 = first / per;
+      p.row_info[r] = make_int2((int)c0, n == 0 ? 0 : (int)((first + n - 1) / per - c0 + 1));
     }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    int64_t before = base;
-    for (int i = 0; i < warp; ++i) before += scratch[i];
-    const int64_t first = before + inc - n;
-    if (n > 0 && w.pos >= first && w.pos < first + n) {
-      scratch[12] = r;
-      scratch[13] = first;
-    }
-    if (blockIdx.x == 0 && r < p.rows) {
-      if (p.unit) {
-        p.row_info[r] = make_int2((int)first, (int)n);
-      } else {
-        const int64_t c0 = first / per;
-        p.row_info[r] = make_int2((int)c0, n == 0 ? 0 : (int)((first + n - 1) / per - c0 + 1));
-      }
-    }
-    for (int i = 0; i < kWarps; ++i) base += scratch[i];
-    if (blockIdx.x != 0 && base > w.pos) break;  // uniform: base and w.pos are the block's
-  }
-  __syncthreads();
-  w.row = (int)scratch[12];
-  w.start = scratch[13];
+  };
+  const Run run = find_run<kThreads>(p.rows, kMinTiles, p.unit ? 1 : 0, scratch, count, each);
+  w.row = run.row;
+  w.start = run.start;
+  w.pos = run.pos;
+  w.hi = run.hi;
   return w;
 }
 

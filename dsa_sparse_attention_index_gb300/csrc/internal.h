@@ -97,6 +97,17 @@ dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt
 size_t dense_mla_workspace_bytes(int rows, int max_len);
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,
                               uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st);
+// Attention weights per cached token (mass.cu).  k = 0: every visible token.
+size_t mass_workspace_bytes(int rows, int max_len, int k);
+dsa_status_t launch_attention_mass(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
+                                   const float* lse, const int32_t* idx, int k, float sm_scale, const float* mass_in,
+                                   float* mass_out, int64_t ld, void* workspace, int32_t* status, cudaStream_t st);
+// Eviction by those weights into fresh pages (evict.cu).
+size_t evict_workspace_bytes(int batch, int keep);
+dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t& bt, const float* mass, int64_t ld_mass,
+                                int keep, int sink, int recent, const dsa_paged_cache_t& dst, const int32_t* dst_table,
+                                int dst_max_blocks, int32_t* kept, float* mass_out, int64_t ld_out, int32_t* new_lens,
+                                void* workspace, int32_t* status, cudaStream_t st);
 dsa_status_t launch_wait_selftest(int64_t limit_ns, int32_t* status, cudaStream_t st);
 dsa_status_t launch_cache_append(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* new_latent,
                                  const uint16_t* new_key, int32_t* status, cudaStream_t st);

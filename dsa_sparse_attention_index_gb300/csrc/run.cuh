@@ -1,0 +1,70 @@
+// run.cuh — an equal share of a line of work for every CTA of a persistent
+// grid.  The rows' items (tiles, or parts) lie on one line, row after row; CTA
+// c takes the run [c per, (c + 1) per).  Row lengths are read on the device, so
+// a ragged batch balances without the host knowing its lengths.
+#pragma once
+
+#include <stdint.h>
+
+namespace dsa {
+
+struct Run {
+  int64_t pos, hi;   // this CTA's run
+  int row;           // the row that holds pos (rows if none does)
+  int64_t start;     // that row's first item
+};
+
+// By all kThreads threads of the CTA: count(r) items of row r; at least
+// min_items a CTA (fixed_per > 0: exactly that many, and hi is the line's end).
+// each(r, first, n, per) is called once for every row by CTA 0.  `scratch`: 16
+// int64 of shared memory.
+template <int kThreads, class Count, class Each>
+__device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, int64_t* scratch, Count count, Each each) {
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps <= 14, "scratch");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  for (int r = threadIdx.x; r < rows; r += kThreads) sum += count(r);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < kWarps; ++i) total += scratch[i];
+  __syncthreads();
+  const int64_t even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
+  const int64_t per = fixed_per ? fixed_per : (even > min_items ? even : min_items);
+  Run w;
+  w.pos = (int64_t)blockIdx.x * per;
+  w.hi = fixed_per ? total : (w.pos + per < total ? w.pos + per : total);
+  // the row that holds w.pos: a block scan over the rows, kThreads at a time
+  if (threadIdx.x == 0) scratch[14] = rows;
+  int64_t base = 0;
+  for (int r0 = 0; r0 < rows; r0 += kThreads) {
+    const int r = r0 + threadIdx.x;
+    const int64_t n = r < rows ? count(r) : 0;
+    int64_t inc = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int64_t before = base;
+    for (int i = 0; i < warp; ++i) before += scratch[i];
+    const int64_t first = before + inc - n;
+    if (n > 0 && w.pos >= first && w.pos < first + n) {
+      scratch[14] = r;
+      scratch[15] = first;
+    }
+    if (blockIdx.x == 0 && r < rows) each(r, first, n, per);
+    for (int i = 0; i < kWarps; ++i) base += scratch[i];
+    if (blockIdx.x != 0 && base > w.pos) break;  // the same in every thread
+  }
+  __syncthreads();
+  w.row = (int)scratch[14];
+  w.start = scratch[15];
+  return w;
+}
+
+}  // namespace dsa

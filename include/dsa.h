@@ -24,6 +24,8 @@
  *   dsa_topk_paged           the step's top-k, with the selected tokens' physical KV rows
  *   sparse_mla_decode        exact sparse MLA over the selected tokens
  *   dense_mla_decode         exact MLA over every visible token
+ *   dsa_attention_mass       attention weight per cached token, added to a running total
+ *   dsa_cache_evict          eviction by that total into fresh pages
  *   dsa_decode_step(_bf16)   the three stages fused on one stream
  *   dsa_cache_append, dsa_quantize_index_query   the step's front end
  *   dsa_index_frontend       the fused indexer front end (norm, projection,
@@ -320,6 +322,70 @@ size_t dense_mla_workspace_size(int32_t rows, int32_t max_seq_len);
 dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
                               float sm_scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                               int32_t* dev_status, void* stream);
+
+/*
+ * The attention weight that each cached token received (no counterpart on the
+ * source pages), added to a running total: what dsa_cache_evict ranks tokens by.
+ * For sequence b, its rows r = b * queries_per_seq + j in order of j, and the
+ * tokens t that row r attended to (idx NULL: every token it sees, as in
+ * dense_mla_decode; else the entries >= 0 of idx[r], as in sparse_mla_decode;
+ * an entry listed twice counts twice):
+ *   mass_out[b][t] = mass_in[b][t] + sum_j sum_h exp(sm_scale * (q[r][h] . c_t) - lse[r][h])
+ * with c_t as for the attention.  With the LSE of that attention the exponentials
+ * are its softmax weights; an LSE of -inf (a row that attended to nothing) adds
+ * nothing.  Written for every t < seq_len_b and nothing else; fp32 sums in a
+ * fixed order, so the result is the same on every run.
+ *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned;  lse device fp32 [rows][96]
+ *   idx       device int32 [rows][k] with k in 1..DSA_MAX_TOPK, or NULL with k = 0; an entry
+ *             that its row does not see raises DSA_ERR_BOUNDS
+ *   mass_in   device fp32 [batch][ld_mass] or NULL (zeros);  mass_out likewise, mass_in itself
+ *             (adding in place) or a buffer that does not overlap it;  ld_mass >= max_seq_len
+ *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B
+ *             aligned; not needed (NULL) with one row per sequence and idx NULL
+ * One launch without a workspace, two with one.  Lengths as for dense_mla_decode.
+ */
+size_t dsa_attention_mass_workspace_size(int32_t rows, int32_t max_seq_len, int32_t k);
+dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
+                                const float* lse, const int32_t* idx, int32_t k, float sm_scale, const float* mass_in,
+                                float* mass_out, int64_t ld_mass, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream);
+
+/*
+ * Eviction from the cache by accumulated attention weight (no counterpart on
+ * the source pages).  Sequence b of L tokens keeps
+ *   all of them if L <= keep, else
+ *   the tokens [0, sink) and [L - recent, L), and of those between the
+ *   keep - sink - recent with the largest mass[b][t] (equal totals: the lower
+ *   index; -0 = +0; NaN below every number),
+ * and the records of its n = min(L, keep) kept tokens, latents and index keys,
+ * move in ascending order into the pages of dst_block_table: kept token i
+ * becomes token i of a context of n tokens.  The attention and the indexer
+ * carry no position encoding, so both give the same on the moved tokens as on
+ * the kept ones where they were.  Slots behind the n tokens are not written.
+ *   mass        device fp32 [batch][ld_mass], ld_mass >= batch->max_seq_len
+ *   keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep <= dst_max_blocks * 64
+ *   dst_cache   the pool that receives the records: `cache` itself or another with the same
+ *               latent format, latent scale and key page layout (else DSA_ERR_UNSUPPORTED)
+ *   dst_block_table  device int32 [batch][dst_max_blocks]: ceil(min(L, keep) / 64) pages a
+ *               sequence, all different and none of them a page of `batch` (its pages are only
+ *               read, so pages that several sequences share stay valid)
+ *   kept_idx    device int32 [batch][keep]: the kept tokens' old indices, then -1
+ *   mass_out    device fp32 [batch][ld_mass_out], ld_mass_out >= keep, or NULL: the kept tokens'
+ *               totals, the rest of the row 0; it must not overlap mass
+ *   new_lens    device int32 [batch]: n; another buffer than batch->seq_lens
+ *   workspace   >= dsa_cache_evict_workspace_size(batch, max_seq_len, keep) bytes, 256-B aligned
+ * batch->queries_per_seq plays no part.  A length outside the table or above
+ * max_seq_len, or negative, raises DSA_ERR_BOUNDS and the sequence comes out
+ * empty; so does a table entry outside its pool, and its record or page is not
+ * moved.  Two launches.
+ */
+size_t dsa_cache_evict_workspace_size(int32_t batch, int32_t max_seq_len, int32_t keep);
+dsa_status_t dsa_cache_evict(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const float* mass,
+                             int64_t ld_mass, int32_t keep, int32_t sink, int32_t recent,
+                             const dsa_paged_cache_t* dst_cache, const int32_t* dst_block_table,
+                             int32_t dst_max_blocks, int32_t* kept_idx, float* mass_out, int64_t ld_mass_out,
+                             int32_t* new_lens, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             void* stream);
 
 /*
  * Batch-invariant mode (Day-0 post, section "day 0 的零失配 RL", zero-mismatch
