@@ -35,10 +35,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxShare = 48 * 1024;  // tokens whose keys a CTA holds in shared memory (192 KB)
 
 struct SelectParams {
   const float* mass;
@@ -64,30 +65,29 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sh, uint32_
     const uint32_t u = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += u;
   }
+  __syncthreads();  // sh may still be read by the scan before
   if (lane == 31) sh[wid] = x;
   __syncthreads();
-  if (wid == 0) {
-    uint32_t w = sh[lane];
+  uint32_t before = 0;
+  total = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w += u;
-    }
-    sh[lane] = w;
+  for (int w = 0; w < kSelWarps; ++w) {
+    const uint32_t s = sh[w];
+    if (w < wid) before += s;
+    total += s;
   }
-  __syncthreads();
-  const uint32_t before = wid ? sh[wid - 1] : 0u;
-  total = sh[kSelWarps - 1];
-  __syncthreads();
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectParams p) {
+// kResident: the CTA's keys stay in shared memory; else every pass reads the weights again (L2).
+template <bool kResident>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[kBins];   // this CTA's counts
   __shared__ uint32_t total[kBins];  // the cluster's
   __shared__ uint32_t sh[kSelWarps];
   __shared__ uint32_t found[2];
-  __shared__ uint32_t counts[2];     // this CTA's tokens above and at the threshold
+  __shared__ uint32_t counts[2];     // this CTA's tokens kept whatever their rank, and at the threshold
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x;
@@ -125,82 +125,115 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
   const uint32_t m = (uint32_t)(p.keep - p.sink - p.recent);
   const int share = (((L + C - 1) / C) + 3) & ~3;  // tokens a CTA, a multiple of 4
   const int t0 = min(L, rank * share), t1 = min(L, t0 + share);
+  const int a0 = max(t0, lo), a1 = min(t1, hi);    // its part of the middle
+  auto key_at = [&](int t) { return kResident ? keys[t - t0] : score_key(mass[t]); };
   uint32_t prefix = 0, mask = 0, want = m;         // key & mask == prefix: the keys still in question
   if (m > 0) {
-    const int shifts[3] = {21, 10, 0};
+#pragma unroll
     for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
       const uint32_t dmask = d < 2 ? 2047u : 1023u;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kBins / kSelThreads; ++i) hist[tid + i * kSelThreads] = 0;
       __syncthreads();
-      for (int t = max(t0, lo) + tid; t < min(t1, hi); t += kSelThreads) {
-        const uint32_t key = score_key(mass[t]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shifts[d]) & dmask], 1u);
+      constexpr int kU = 4;
+      for (int tb = a0 + tid; tb < a1; tb += kU * kSelThreads) {
+        uint32_t key[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int t = tb + u * kSelThreads;
+          if (t >= a1) continue;
+          if (kResident && d == 0)
+            key[u] = __float_as_uint(mass[t]);
+          else
+            key[u] = key_at(t);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int t = tb + u * kSelThreads;
+          if (t >= a1) continue;
+          if (kResident && d == 0) keys[t - t0] = key[u] = score_key(__uint_as_float(key[u]));
+          if ((key[u] & mask) == prefix) atomicAdd(&hist[(key[u] >> shift) & dmask], 1u);
+        }
       }
       cl.sync();
-      // bins rank, rank + C, ... summed over the cluster, the sums written to every CTA
-      for (int i = rank + C * tid; i < kBins; i += C * kSelThreads) {
+      // bins [rank, rank + 1) * kBins / C summed over the cluster, the sums written to every CTA
+      for (int i = tid; i < kBins / C; i += kSelThreads) {
+        const int bin = rank * (kBins / C) + i;
         uint32_t s = 0;
-        for (int c = 0; c < C; ++c) s += cl.map_shared_rank(hist, c)[i];
-        for (int c = 0; c < C; ++c) cl.map_shared_rank(total, c)[i] = s;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < C) s += cl.map_shared_rank(hist, c)[bin];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < C) cl.map_shared_rank(total, c)[bin] = s;
       }
       cl.sync();
       // the digit: bins from the top until `want` keys are covered
-      const int i0 = kBins - 1 - 2 * tid;
-      const uint32_t a = total[i0], c = total[i0 - 1];
-      uint32_t all;
-      const uint32_t before = block_scan(a + c, sh, all);
-      if (want > before && want <= before + a) {
-        found[0] = (uint32_t)i0;
-        found[1] = before;
-      } else if (want > before + a && want <= before + a + c) {
-        found[0] = (uint32_t)(i0 - 1);
-        found[1] = before + a;
+      constexpr int kPer = kBins / kSelThreads;
+      uint32_t v[kPer], sum = 0, all;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += v[i] = total[kBins - 1 - kPer * tid - i];
+      uint32_t before = block_scan(sum, sh, all);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (want > before && want <= before + v[i]) {
+          found[0] = (uint32_t)(kBins - 1 - kPer * tid - i);
+          found[1] = before;
+        }
+        before += v[i];
       }
       __syncthreads();
-      prefix |= found[0] << shifts[d];
-      mask |= dmask << shifts[d];
+      prefix |= found[0] << shift;
+      mask |= dmask << shift;
       want -= found[1];
-      __syncthreads();
     }
   }
-  // `want` of the keys equal to `prefix` stay, those of the lowest indices; with m = 0 none does
-  uint32_t gt = 0, eq = 0;
-  if (m > 0)
-    for (int t = max(t0, lo) + tid; t < min(t1, hi); t += kSelThreads) {
-      const uint32_t key = score_key(mass[t]);
-      gt += key > prefix;
-      eq += key == prefix;
-    }
-  uint32_t tg, te;
-  block_scan(gt, sh, tg);
-  block_scan(eq, sh, te);
+  // `want` of the keys equal to `prefix` stay, those of the lowest indices; with m = 0 none does.
+  // Low half: a token that stays whatever its rank among the equals; high half: one of the equals.
+  auto kind = [&](int t) -> uint32_t {
+    if (t >= t1) return 0u;
+    if (t < lo || t >= hi) return 1u;
+    if (m == 0) return 0u;
+    const uint32_t key = key_at(t);
+    return key > prefix ? 1u : key == prefix ? 1u << 16 : 0u;
+  };
+  uint32_t hard = 0, equal = 0;
+  for (int t = t0 + tid; t < t1; t += kSelThreads) {
+    const uint32_t k = kind(t);
+    hard += k & 0xffffu;
+    equal += k >> 16;
+  }
+  uint32_t th, te;
+  block_scan(hard, sh, th);
+  block_scan(equal, sh, te);
   if (tid == 0) {
-    counts[0] = tg;
+    counts[0] = th;
     counts[1] = te;
   }
   cl.sync();
-  // kept tokens and equal keys of the CTAs before this one
-  uint32_t eq_before = 0, pos = 0;
+  uint32_t hard_before = 0, eq_before = 0;  // of the CTAs before this one
   for (int c = 0; c < rank; ++c) {
     const uint32_t* o = cl.map_shared_rank(counts, c);
-    const int s0 = min(L, c * share), s1 = min(L, s0 + share);
-    const uint32_t e = o[1], left = want > eq_before ? want - eq_before : 0u;
-    pos += o[0] + min(e, left) + (uint32_t)max(0, min(s1, lo) - s0) + (uint32_t)max(0, s1 - max(s0, hi));
-    eq_before += e;
+    hard_before += o[0];
+    eq_before += o[1];
   }
   cl.sync();  // the counts have been read: a CTA may exit
-  for (int tb = t0; tb < t1; tb += kSelThreads) {
-    const int t = tb + tid;
-    const bool in = t < t1, middle = in && t >= lo && t < hi && m > 0;
-    const uint32_t key = middle ? score_key(mass[t]) : 0u;
-    const bool is_eq = middle && key == prefix;
-    uint32_t eqs, kepts;
-    const uint32_t er = block_scan(is_eq ? 1u : 0u, sh, eqs);
-    const bool stay = in && ((t < lo || t >= hi) || (middle && (key > prefix || (is_eq && eq_before + er < want))));
-    const uint32_t kr = block_scan(stay ? 1u : 0u, sh, kepts);
-    if (stay) put((int)(pos + kr), t);
-    pos += kepts;
-    eq_before += eqs;
+  for (int tb = t0; tb < t1; tb += 4 * kSelThreads) {
+    const int t = tb + 4 * tid;
+    uint32_t k[4], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += k[i] = kind(t + i);
+    const uint32_t r = block_scan(sum, sh, all);
+    uint32_t hb = hard_before + (r & 0xffffu), eb = eq_before + (r >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k[i] == 1u || (k[i] && eb < want)) put((int)(hb + min(eb, want)), t + i);
+      hb += k[i] & 0xffffu;
+      eb += k[i] >> 16;
+    }
+    hard_before += all & 0xffffu;
+    eq_before += all >> 16;
   }
 }
 
@@ -209,63 +242,59 @@ struct MoveParams {
   uint8_t* dst;
   int64_t src_stride, dst_stride;
   int64_t src_lat, src_idx, dst_lat, dst_idx;  // page offsets in a block row
-  int32_t rec, code;                           // latent record and index-key code bytes, multiples of 16
   const int32_t* new_lens;
   const int32_t* phys;
-  int32_t keep;
+  int32_t keep, pages;
   const int32_t* dst_table;
   int32_t dst_max_blocks, dst_num_blocks;
   int32_t* status;
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
 
+// kRec, kCode: bytes of a latent record and of an index key's codes (its 4-byte scales lie behind the page's codes).
+template <int kRec, int kCode>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveParams p) {
-  __shared__ int32_t src_s[kBlock];
+  constexpr int kLu = kRec / 16, kKu = kCode / 16, kUnits = kLu + kKu;  // 16-byte units of a token
+  constexpr int kPer = (kBlock * kUnits + kMoveThreads - 1) / kMoveThreads;
+  __shared__ int32_t src_s[kBlock];  // kept token's slot, block row * 64 + slot; -1: none, or a bad page (reported)
   grid_dep_wait();
-  const int pages = (p.keep + kBlock - 1) / kBlock;
-  const int b = blockIdx.x / pages, page = blockIdx.x % pages, tid = threadIdx.x;
+  const int b = blockIdx.x / p.pages, page = blockIdx.x % p.pages, tid = threadIdx.x;
   const int n = min(p.new_lens[b] - page * kBlock, kBlock);
-  if (n <= 0) return;
   const int dr = p.dst_table[(int64_t)b * p.dst_max_blocks + page];
+  const int at = page * kBlock + tid;
+  const int s = tid < kBlock && at < p.keep ? p.phys[(int64_t)b * p.keep + at] : -1;
+  if (n <= 0) return;
   if (dr < 0 || dr >= p.dst_num_blocks) {
     if (tid == 0) report(p.status, DSA_ERR_BOUNDS);
     return;
   }
-  if (tid < n) src_s[tid] = p.phys[(int64_t)b * p.keep + page * kBlock + tid];
+  if (tid < kBlock) src_s[tid] = at < page * kBlock + n ? s : -1;
   __syncthreads();
   uint8_t* row = p.dst + (int64_t)dr * p.dst_stride;
-  const int lu = p.rec / 16, ku = p.code / 16;
-  const int units = n * lu, all = units + n * ku;
-  for (int u0 = tid; u0 < all; u0 += kMoveThreads * kMoveUnroll) {
-    uint4 v[kMoveUnroll];
-    uint8_t* to[kMoveUnroll];
+  uint4 v[kPer];
 #pragma unroll
-    for (int i = 0; i < kMoveUnroll; ++i) {
-      const int u = u0 + i * kMoveThreads;
-      to[i] = nullptr;
-      if (u >= all) continue;
-      const bool lat = u < units;
-      const int w = lat ? u : u - units, per = lat ? lu : ku;
-      const int tok = w / per, c = w % per, s = src_s[tok];
-      if (s < 0) continue;  // a bad page of the source, reported
-      const uint8_t* from = p.src + (int64_t)(s / kBlock) * p.src_stride + (lat ? p.src_lat : p.src_idx) +
-                            (s % kBlock) * (per * 16) + c * 16;
-      to[i] = row + (lat ? p.dst_lat : p.dst_idx) + tok * (per * 16) + c * 16;
-      v[i] = *reinterpret_cast<const uint4*>(from);
-    }
+  for (int i = 0; i < kPer; ++i) {
+    const int u = tid + i * kMoveThreads, tok = u / kUnits, c = u % kUnits;
+    if (u >= kBlock * kUnits) continue;
+    const int32_t q = src_s[tok];
+    if (q < 0) continue;
+    const int slot = q % kBlock;
+    v[i] = *reinterpret_cast<const uint4*>(p.src + (int64_t)(q / kBlock) * p.src_stride +
+                                           (c < kLu ? p.src_lat + slot * kRec + c * 16
+                                                    : p.src_idx + slot * kCode + (c - kLu) * 16));
+  }
 #pragma unroll
-    for (int i = 0; i < kMoveUnroll; ++i)
-      if (to[i]) *reinterpret_cast<uint4*>(to[i]) = v[i];
+  for (int i = 0; i < kPer; ++i) {
+    const int u = tid + i * kMoveThreads, tok = u / kUnits, c = u % kUnits;
+    if (u >= kBlock * kUnits || src_s[tok] < 0) continue;
+    uint8_t* to = row + (c < kLu ? p.dst_lat + tok * kRec + c * 16 : p.dst_idx + tok * kCode + (c - kLu) * 16);
+    *reinterpret_cast<uint4*>(to) = v[i];
   }
-  // the 4-byte key scales behind the codes
-  if (tid < n && src_s[tid] >= 0) {
-    const int s = src_s[tid];
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p.src + (int64_t)(s / kBlock) * p.src_stride + p.src_idx +
-                                                          kBlock * p.code + (s % kBlock) * 4);
-    *reinterpret_cast<uint32_t*>(row + p.dst_idx + kBlock * p.code + tid * 4) = v;
-  }
+  if (tid < n && s >= 0)
+    *reinterpret_cast<uint32_t*>(row + p.dst_idx + kBlock * kCode + tid * 4) =
+        *reinterpret_cast<const uint32_t*>(p.src + (int64_t)(s / kBlock) * p.src_stride + p.src_idx + kBlock * kCode +
+                                           (s % kBlock) * 4);
 }
 
 }  // namespace
@@ -276,8 +305,7 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
                                 int keep, int sink, int recent, const dsa_paged_cache_t& dst, const int32_t* dst_table,
                                 int dst_max_blocks, int32_t* kept, float* mass_out, int64_t ld_out, int32_t* new_lens,
                                 void* workspace, int32_t* status, cudaStream_t st) {
-  const int rec = src.latent_format == DSA_LATENT_NVFP4 ? 352 : kLatent;
-  const int code = src.key_format == DSA_KEY_FP8_E4M3 ? kIdxDim : kIdxDim / 2;
+  const bool nv = src.latent_format == DSA_LATENT_NVFP4, key8 = src.key_format == DSA_KEY_FP8_E4M3;
   SelectParams s = {};
   s.mass = mass;
   s.ld_mass = ld_mass;
@@ -295,9 +323,21 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
   s.new_lens = new_lens;
   s.phys = static_cast<int32_t*>(workspace);
   s.status = status;
-  // CTAs a sequence: one up to 4,096 tokens, then one more for every 4,096
+  // CTAs a sequence: enough that a CTA's share is at most 2,048 tokens, but no more than fill the SMs twice
+  // (one sequence of 5,001 tokens and 32 of 16K to 49K measured: see the kernel's comment)
   int C = 1;
-  while (C < kMaxCluster && C * 4096 < bt.max_seq_len) C *= 2;
+  while (C < kMaxCluster && C * 2048 < bt.max_seq_len && 2 * C * bt.batch <= 2 * num_sms()) C *= 2;
+  const int64_t share = ((((int64_t)bt.max_seq_len + C - 1) / C) + 3) & ~int64_t(3);
+  const bool resident = share <= kMaxShare;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    if (cuda_status(cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMaxShare * 4)) != DSA_OK)
+      return DSA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -308,11 +348,12 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(bt.batch * C));
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = resident ? (size_t)share * 4 : 0;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launches(1);
-  if (cuda_status(cudaLaunchKernelEx(&cfg, evict_select_kernel, s)) != DSA_OK) return DSA_ERR_CUDA;
+  if (cuda_status(cudaLaunchKernelEx(&cfg, resident ? evict_select_kernel<true> : evict_select_kernel<false>, s)) != DSA_OK) return DSA_ERR_CUDA;
   MoveParams m = {};
   m.src = static_cast<const uint8_t*>(src.base);
   m.dst = static_cast<uint8_t*>(dst.base);
@@ -322,20 +363,23 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
   m.src_idx = src.index_off;
   m.dst_lat = dst.latent_off;
   m.dst_idx = dst.index_off;
-  m.rec = rec;
-  m.code = code;
   m.new_lens = new_lens;
   m.phys = s.phys;
   m.keep = keep;
+  m.pages = (keep + kBlock - 1) / kBlock;
   m.dst_table = dst_table;
   m.dst_max_blocks = dst_max_blocks;
   m.dst_num_blocks = dst.num_blocks;
   m.status = status;
-  cfg.gridDim = dim3((unsigned)(bt.batch * ((keep + kBlock - 1) / kBlock)));
+  cfg.gridDim = dim3((unsigned)(bt.batch * m.pages));
   cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   count_launches(1);
-  if (cuda_status(cudaLaunchKernelEx(&cfg, evict_move_kernel, m)) != DSA_OK) return DSA_ERR_CUDA;
+  constexpr int kNv = kValue / 2 + kValue / 16 + (kLatent - kValue);
+  auto move = nv ? (key8 ? evict_move_kernel<kNv, kIdxDim> : evict_move_kernel<kNv, kIdxDim / 2>)
+                 : (key8 ? evict_move_kernel<kLatent, kIdxDim> : evict_move_kernel<kLatent, kIdxDim / 2>);
+  if (cuda_status(cudaLaunchKernelEx(&cfg, move, m)) != DSA_OK) return DSA_ERR_CUDA;
   return launch_status();
 }
 
