@@ -302,7 +302,7 @@ __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return ((
 
 // Instruction descriptor (kind::f16 and kind::f8f6f4): fp32 accumulator,
 // operand formats, K-major (0) / MN-major (1) per operand, N >> 3, M >> 4.
-enum : uint32_t { kFmtE4M3 = 0, kFmtE2M1 = 5, kFmtBF16 = 1 };
+enum : uint32_t { kFmtE4M3 = 0, kFmtE2M1 = 5, kFmtBF16 = 1, kFmtF16 = 0 };
 // E2M1 in the operand-format field of kind::mxf4 (the only format of that kind)
 constexpr uint32_t kFmtMxf4E2M1 = 1;
 // Instruction descriptor of kind::mxf8f6f4.block_scale (fp32 accumulator
@@ -375,6 +375,54 @@ __device__ __forceinline__ void nvfp4x16_to_bf16x16(uint32_t w0, uint32_t w1, ui
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(f), "r"(0x7E807E80u));  // 2^126
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(v), "r"(s2));
   }
+}
+
+// The same widenings to fp16 with the conversion instructions: exact too (E4M3
+// has 4 significant bits and reaches down to 2^-9; the product of an E2M1 value
+// and an E4M3 scale has 6 and lies in [2^-10, 2688]), in less than half the
+// instructions.  The NaN codes become NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  uint32_t o;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o) : "h"(v));
+  return o;
+}
+__device__ __forceinline__ void e4m3x16_to_f16x16(const uint4& v, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    o[2 * q] = e4m3x2_to_f16x2((uint16_t)w[q]);
+    o[2 * q + 1] = e4m3x2_to_f16x2((uint16_t)(w[q] >> 16));
+  }
+}
+__device__ __forceinline__ void nvfp4x16_to_f16x16(uint32_t w0, uint32_t w1, uint32_t scale_byte, uint32_t (&o)[8]) {
+  const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(scale_byte * 0x0101u));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t* d = o + 4 * h;
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(h ? w1 : w0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d[i]) : "r"(s2));
+  }
+}
+// A head's bf16 query as fp16: times 2^e with e such that its largest magnitude
+// lands in [2^14, 2^15).  What falls below fp16's normal range is at most 2^-28
+// of that, and its rounding (2^-39 of it) far below the fp32 sums' own.
+__device__ __forceinline__ uint32_t bf16x2_abs_max(uint32_t a, uint32_t b) {  // per 16-bit half, of magnitudes as integers
+  return __vmaxu2(a, b & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ int f16_shift_of(uint32_t abs_max2) {
+  const uint32_t m = max(abs_max2 & 0xFFFFu, abs_max2 >> 16);
+  const int e = (int)(m >> 7);  // bf16's exponent field; 0 and 255 (no finite value) clamp
+  return max(-126, min(126, 14 + 127 - e));
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
+  const float lo = __uint_as_float(v << 16) * scale, hi = __uint_as_float(v & 0xFFFF0000u) * scale;
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Two E4M3 bytes (low byte = first element) -> two bf16 (low half = first).

@@ -45,41 +45,43 @@ namespace dsa {
 
 namespace {
 
-constexpr int kTile = kBlock;                          // tokens per tile: one page
+constexpr int kTile = 48;                              // tokens per tile
 constexpr int kDB = kLatent / 64;                      // 9 blocks of 64 dims
 constexpr int kVB = kValue / 64;                       // 8 of them are values
 constexpr int kQTmemBlocks = 2;                        // Q dims 448..575 in TMEM
 constexpr int kQSmemBlocks = kDB - kQTmemBlocks;       // Q dims 0..447 in shared memory
 constexpr int kQBlockBytes = kHeads * 128;             // 12,288
-constexpr int kBlkBytes = kTile * 128;                 // 8,192: 64 tokens x 64 dims of bf16
-constexpr int kVSlots = 14;                            // ring of value blocks (a tile has 8)
-constexpr int kKSlots = 2;                             // ring of key-only blocks (a tile has 1)
-constexpr int kPBytes = kHeads * 128;                  // 12,288: 64 tokens of bf16 per head
+constexpr int kBlkBytes = kTile * 128;                 // 6,144: 48 tokens x 64 dims of bf16
+constexpr int kPairs = kVB / 2;                        // a pair of blocks: the 128 dims of one PV product
+constexpr int kTileBytes = kDB * kBlkBytes;            // 55,296; block 8 holds the key-only dims
+constexpr int kBufs = 2;                               // tile buffers, each filled and freed in two halves
+constexpr int kPBytes = kHeads * 128;                  // 12,288: a head's 48 bf16 in a 128-byte row
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);  // 352 B
-constexpr int kThreads = 320;  // softmax 0-3, loaders 4-7, QK issuer 8, PV issuer 9
+constexpr int kThreads = 12 * 32;  // softmax 0-3, loaders 4-9, QK issuer 10, PV issuer 11
 constexpr int kLoadWarp0 = 4;
-constexpr int kLoadWarps = 4;
-constexpr int kQkWarp = 8;
-constexpr int kPvWarp = 9;
+constexpr int kLoadWarps = 6;   // 8 tokens a warp
+constexpr int kQkWarp = 10;
+constexpr int kPvWarp = 11;
+static_assert(kLoadWarps * 8 == kTile, "loader split");
 constexpr int kOCols = 4 * kHeads;                     // 384
 constexpr int kSCol = kOCols;                          // 384..447
-constexpr int kQ8Col = kSCol + kTile;                  // 448..511
-static_assert(kQ8Col + 32 * kQTmemBlocks <= 512, "TMEM columns");
+constexpr int kQ8Col = 448;                            // 448..511
+static_assert(kSCol + kTile <= kQ8Col && kQ8Col + 32 * kQTmemBlocks <= 512, "TMEM columns");
 constexpr float kRescaleThreshold = 8.0f;              // log2 units
+constexpr float kPShift = 7.0f;                        // P is stored times 2^7, at most 2^15
 constexpr int kMinTiles = 2;                           // tiles per CTA before more CTAs are used
 constexpr int kMaxGrid = 256;                          // CTAs the workspace is sized for
-constexpr int kInvariantTiles = 64;                    // tiles per part in the batch-invariant mode
+constexpr int kInvariantTiles = 80;                    // tiles per part in the batch-invariant mode
 
 constexpr int kOffQ = 0;
-constexpr int kOffV = kOffQ + kQSmemBlocks * kQBlockBytes;     // 86,016
-constexpr int kOffK = kOffV + kVSlots * kBlkBytes;             // 200,704
-constexpr int kOffP = kOffK + kKSlots * kBlkBytes;             // 217,088
-constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
+constexpr int kOffTile = kOffQ + kQSmemBlocks * kQBlockBytes;  // 86,016
+constexpr int kOffP = kOffTile + kBufs * kTileBytes;           // 196,608
+constexpr int kOffAlpha = kOffP + 2 * kPBytes;                     // 229,376
 constexpr int kOffBars = kOffAlpha + 512;
-constexpr int kNumBars = 2 * kVSlots + 2 * kKSlots + 8;
-constexpr int kOffMisc = kOffBars + kNumBars * 8;              // TMEM slot, abort flag, scan scratch
+constexpr int kNumBars = 4 * kBufs + 11;
+constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;              // TMEM slot, abort flag, scan scratch
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 256;
-static_assert(kOffV % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+static_assert(kOffTile % 1024 == 0 && kOffP % 1024 == 0 && kBlkBytes % 1024 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 constexpr size_t kPartO = (size_t)kHeads * kValue;             // fp16 values of a partial
@@ -98,7 +100,7 @@ struct DenseParams {
   uint16_t* out;
   float* lse;
   uint16_t* opart;  // fp16 [slots][96][512]
-  float* ml;        // [slots][96][4]: max (log2), sum of bf16(p), sum of p
+  float* ml;        // [slots][96][2]: reference (log2), sum of 2^(l - reference)
   int2* row_info;   // [rows]: first slot key, number of parts (0: no token, 1: written by the kernel)
   int32_t unit;     // tiles of a fixed part in the batch-invariant mode, else 0
   int32_t* status;
@@ -197,31 +199,24 @@ __device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
   return w;
 }
 
-// 16 E4M3 bytes -> 16 bf16, exactly.
-__device__ __forceinline__ void widen_e4m3(const uint4& v, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) e4m3x4_to_bf16x4(w[q], o[2 * q], o[2 * q + 1]);
-}
-
 template <bool kNV>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ DenseParams p) {
   constexpr int kRec = kNV ? kNvRec : kLatent;
-  constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, kFmtBF16, 0, 0, 128, kTile);
-  constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, kFmtBF16, 1, 0, 128, kHeads);
+  constexpr uint32_t kIdescQK = make_idesc(kFmtF16, kFmtF16, 0, 0, 128, kTile);
+  constexpr uint32_t kIdescPV = make_idesc(kFmtF16, kFmtF16, 1, 0, 128, kHeads);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + kOffBars;
-  auto vfull = [&](int s) { return bars + 8u * s; };
-  auto vempty = [&](int s) { return bars + 8u * (kVSlots + s); };
-  auto kfull = [&](int s) { return bars + 8u * (2 * kVSlots + s); };
-  auto kempty = [&](int s) { return bars + 8u * (2 * kVSlots + kKSlots + s); };
-  const uint32_t bars2 = bars + 8u * (2 * kVSlots + 2 * kKSlots);
-  const uint32_t q_full = bars2, q8_full = bars2 + 8, s_full = bars2 + 16, s_empty = bars2 + 24, p_full = bars2 + 32,
-                 pv_done = bars2 + 40, o_free = bars2 + 48, drain = bars2 + 56;
+  auto full = [&](uint32_t buf, int half) { return bars + 8u * (2 * buf + half); };
+  auto empty = [&](uint32_t buf, int half) { return bars + 8u * (2 * kBufs + 2 * buf + half); };
+  const uint32_t bars2 = bars + 8u * (4 * kBufs);
+  const uint32_t q_full = bars2, q_ready = bars2 + 8, s_full = bars2 + 16, s_empty = bars2 + 24, o_free = bars2 + 32,
+                 drain = bars2 + 40;
+  auto p_full = [&](uint32_t b) { return bars2 + 48 + 8 * b; };
+  auto pv_done = [&](uint32_t b) { return bars2 + 64 + 8 * b; };  // PV of the tiles that use P buffer b
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
@@ -229,20 +224,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kVSlots; ++s) {
-      mbar_init(vfull(s), kLoadWarps);
-      mbar_init(vempty(s), 1);
-    }
-    for (int s = 0; s < kKSlots; ++s) {
-      mbar_init(kfull(s), kLoadWarps);
-      mbar_init(kempty(s), 1);
-    }
+    for (int s = 0; s < kBufs; ++s)
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(full(s, h), kLoadWarps);
+        mbar_init(empty(s, h), 1);
+      }
     mbar_init(q_full, 1);
-    mbar_init(q8_full, 4);
+    mbar_init(q_ready, 4);
     mbar_init(s_full, 1);
     mbar_init(s_empty, 4);
-    mbar_init(p_full, 4);
-    mbar_init(pv_done, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(p_full(b), 4);
+      mbar_init(pv_done(b), 1);
+    }
     mbar_init(o_free, 4);
     mbar_init(drain, 2);
     *abort_flag = 0;
@@ -267,10 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ QK issuer
       const uint64_t q_desc = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSw128);
       const uint32_t q_lo = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
-      const uint32_t v_lo0 = (uint32_t)smem_desc(sbase + kOffV, 16, 1024, kLayoutSw128);
-      const uint32_t k_lo0 = (uint32_t)smem_desc(sbase + kOffK, 16, 1024, kLayoutSw128);
+      const uint32_t t_lo0 = (uint32_t)smem_desc(sbase + kOffTile, 16, 1024, kLayoutSw128);
       uint32_t it = 0, seg = 0;
-      bool ok = true, q_pending = false;
+      bool ok = true;
       const uint32_t d = tmem + kSCol;
       while (ok && walk.next(sg)) {
         // the previous part's last S tile has been read by the softmax, so its QK^T has completed: Q may go
@@ -279,44 +272,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(q_full, kQSmemBlocks * kQBlockBytes);
         for (int kb = 0; kb < kQSmemBlocks; ++kb)
           tma_load_2d(sbase + kOffQ + kb * kQBlockBytes, &tmap_q, kb * 64, sg.row * kHeads, q_full);
-        q_pending = true;
-        ok = mbar_wait(q_full, seg & 1, abort_flag, p.status) && mbar_wait(q8_full, seg & 1, abort_flag, p.status);
-        if (!ok) break;
-        q_pending = false;
+        // the softmax warps wait for it, turn it into fp16 where it lies and say so
+        ok = mbar_wait(q_ready, seg & 1, abort_flag, p.status);
         ++seg;
         for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
-          ok = mbar_wait(s_empty, (it & 1) ^ 1, abort_flag, p.status) &&
-               mbar_wait(kfull(it % kKSlots), (it / kKSlots) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t k_lo = k_lo0 + (it % kKSlots) * (kBlkBytes / 16);
+          ok = mbar_wait(s_empty, (it & 1) ^ 1, abort_flag, p.status);
+          const uint32_t buf = it % kBufs, t_lo = t_lo0 + buf * (kTileBytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // dims 512..575: A from TMEM
-            mma_bf16_tmem_a(d, tmem + kQ8Col + 32 + 8 * kk, desc64(k_lo + 2 * kk, hi), kIdescQK, kk ? 1u : 0u);
-          mma_commit(kempty(it % kKSlots));
-          uint32_t n = it * kVB;
-#pragma unroll 1
-          for (int kb = 0; kb < kVB; ++kb, ++n) {
-            const uint32_t slot = n % kVSlots;
-            ok = mbar_wait(vfull(slot), (n / kVSlots) & 1, abort_flag, p.status);
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && mbar_wait(full(buf, half), (it / kBufs) & 1, abort_flag, p.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v_lo = v_lo0 + slot * (kBlkBytes / 16);
-            if (kb < kQSmemBlocks) {
-              const uint32_t a_lo = q_lo + kb * (kQBlockBytes / 16);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(d, desc64(a_lo + 2 * kk, hi), desc64(v_lo + 2 * kk, hi), kIdescQK, 1u);
-            } else {  // dims 448..511: A from TMEM
+            for (int kb = half * (kVB / 2); kb < (half ? kDB : kVB / 2); ++kb) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_tmem_a(d, tmem + kQ8Col + 8 * kk, desc64(v_lo + 2 * kk, hi), kIdescQK, 1u);
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t bd = desc64(t_lo + kb * (kBlkBytes / 16) + 2 * kk, hi);
+                if (kb < kQSmemBlocks)
+                  mma_bf16(d, desc64(q_lo + kb * (kQBlockBytes / 16) + 2 * kk, hi), bd, kIdescQK, (kb | kk) ? 1u : 0u);
+                else  // dims 448..575: A from TMEM
+                  mma_bf16_tmem_a(d, tmem + kQ8Col + 32 * (kb - kQSmemBlocks) + 8 * kk, bd, kIdescQK, 1u);
+              }
             }
           }
           if (ok) mma_commit(s_full);
         }
       }
-      if (q_pending) mbar_wait_drain(q_full, seg & 1, 10000000ull);
+      if (seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, 10000000ull);  // no copy is in flight at the exit
       // both issuers' MMAs complete before TMEM is released
       mma_commit(drain);
       mbar_wait_drain(drain, 0, 10000000ull);
@@ -324,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kPvWarp) {
     if (lane == 0) {
       // ------------------------------------------------ PV issuer
-      const uint64_t a_desc = smem_desc(sbase + kOffV, kBlkBytes, 1024, kLayoutSw128);
+      const uint64_t a_desc = smem_desc(sbase + kOffTile, kBlkBytes, 1024, kLayoutSw128);
       const uint32_t a_lo0 = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
       const uint64_t p_desc = smem_desc(sbase + kOffP, 16, 1024, kLayoutSw128);
       const uint32_t p_lo = (uint32_t)p_desc, p_hi = (uint32_t)(p_desc >> 32);
@@ -335,21 +317,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (seg > 0) ok = mbar_wait(o_free, (seg - 1) & 1, abort_flag, p.status);
         ++seg;
         for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
-          ok = mbar_wait(p_full, it & 1, abort_flag, p.status);
+          ok = mbar_wait(p_full(it & 1), (it >> 1) & 1, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
-            const uint32_t slot = (it * kVB + 2 * mb) % kVSlots;  // even: the pair does not wrap
-            const uint32_t a_lo = a_lo0 + slot * (kBlkBytes / 16);
+            const uint32_t a_lo = a_lo0 + (it % kBufs) * (kTileBytes / 16) + 2 * mb * (kBlkBytes / 16);
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_bf16(tmem + mb * kHeads, desc64(a_lo + 2 * ks * 64, a_hi), desc64(p_lo + 2 * ks, p_hi), kIdescPV,
+              mma_bf16(tmem + mb * kHeads, desc64(a_lo + 2 * ks * 64, a_hi), desc64(p_lo + (it & 1) * (kPBytes / 16) + 2 * ks, p_hi), kIdescPV,
                        (t > sg.t0 || ks > 0) ? 1u : 0u);
-            mma_commit(vempty(slot));
-            mma_commit(vempty(slot + 1));
+            if (mb & 1) mma_commit(empty(it % kBufs, mb >> 1));  // QK^T of this tile completed before its P existed
           }
-          mma_commit(pv_done);
+          mma_commit(pv_done(it & 1));
         }
       }
       mma_commit(drain);
@@ -357,141 +337,181 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------ loaders: page -> bf16 blocks
-    // Thread (token, half): 32 dims of each block.  Its 16 code bytes of a block
-    // (32 for E4M3) are loaded a whole tile before they are widened and stored.
-    constexpr int kW = kNV ? 1 : 2;  // 16-byte words per block and thread
-    const int lt = threadIdx.x - kLoadWarp0 * 32;
-    const int tok = lt >> 1, half = lt & 1;
-    uint4 buf[kVB][kW], tail[2], sc[2];
-    const uint8_t* rec = nullptr;  // null: a bad table entry
-    int row = -1, t = 0, t1 = 0;
-    // the next tile of the walk
-    auto advance = [&]() -> bool {
-      if (t >= t1) {
-        if (!walk.next(sg)) return false;
+    // Warp w: tokens 8 w .. 8 w + 7, four lanes a token, a lane 32 dims of each
+    // pair (block `blk`, its half `half`) and 16 dims of the key-only block.  The
+    // lanes are numbered so that eight neighbours store 16 bytes each to all 32
+    // banks.  A pair's codes are loaded a whole tile before they are stored, and a
+    // token's page is looked up two tiles ahead.
+    constexpr int kW = kNV ? 1 : 2;  // 16-byte words of a pair and lane
+    const int half = lane & 1, blk = (lane >> 3) & 1;
+    const int tok = (warp - kLoadWarp0) * 8 + ((lane >> 1) & 3) + ((lane >> 4) & 1) * 4;
+    const uint32_t off = (uint32_t)(tok * 128 + half * 64);
+    const uint32_t o0 = blk * kBlkBytes + swz128(off), o1 = blk * kBlkBytes + swz128(off + 16),
+                   o2 = blk * kBlkBytes + swz128(off + 32), o3 = blk * kBlkBytes + swz128(off + 48);
+    const uint32_t ot = (uint32_t)(tok * 128 + blk * 64 + half * 32);
+    const uint32_t ot0 = (kDB - 1) * kBlkBytes + swz128(ot), ot1 = (kDB - 1) * kBlkBytes + swz128(ot + 16);
+    uint4 buf[kPairs][kW], tail;
+    uint32_t sc[kPairs];
+    const uint8_t* rec = nullptr;  // null: no such token, or a bad table entry
+    int row = -1, t = 0, t1 = 0, page = -1, slot_b = 0;
+    bool have_page = false, live_b = false, have = false;
+    auto step_page = [&]() {  // the next tile's page
+      have_page = t < t1;
+      if (!have_page && walk.next(sg)) {
         row = sg.row;
         t = sg.t0;
         t1 = sg.t1;
+        have_page = true;
       }
-      const int r = p.block_table[(int64_t)(row / p.nq) * p.max_blocks + t];
-      ++t;
+      if (!have_page) return;
+      const int token = t++ * kTile + tok;
+      live_b = token < sg.vis;
+      page = live_b ? p.block_table[(int64_t)(row / p.nq) * p.max_blocks + token / kBlock] : -1;
+      slot_b = token % kBlock;
+    };
+    auto step_record = [&]() {
+      have = have_page;
       rec = nullptr;
-      if (r >= 0 && r < p.num_blocks)
-        rec = p.latent_base + (int64_t)r * p.row_stride + tok * kRec;
+      if (!have || !live_b) return;
+      if (page >= 0 && page < p.num_blocks)
+        rec = p.latent_base + (int64_t)page * p.row_stride + slot_b * kRec;
       else
         report(p.status, DSA_ERR_BOUNDS);
-      return true;
     };
     auto ld = [&](int off) {
       return rec ? __ldg(reinterpret_cast<const uint4*>(rec + off)) : make_uint4(0, 0, 0, 0);
     };
-    auto load_tail = [&]() {
-      constexpr int kTailOff = kNV ? kValue / 2 + kValue / 16 : kValue;
-      tail[0] = ld(kTailOff + 32 * half);
-      tail[1] = ld(kTailOff + 32 * half + 16);
+    auto load_tail = [&]() { tail = ld((kNV ? kValue / 2 + kValue / 16 : kValue) + 32 * blk + 16 * half); };
+    auto load_pair = [&](int mb) {
       if (kNV) {
-        sc[0] = ld(kValue / 2);
-        sc[1] = ld(kValue / 2 + 16);
-      }
-    };
-    auto load_block = [&](int kb) {
-      if (kNV) {
-        buf[kb][0] = ld(32 * kb + 16 * half);
+        buf[mb][0] = ld(64 * mb + 32 * blk + 16 * half);
+        sc[mb] = rec ? __ldg(reinterpret_cast<const uint16_t*>(rec + kValue / 2 + 8 * mb + 4 * blk + 2 * half)) : 0u;
       } else {
-        buf[kb][0] = ld(64 * kb + 32 * half);
-        buf[kb][kW - 1] = ld(64 * kb + 32 * half + 16);
+        buf[mb][0] = ld(128 * mb + 64 * blk + 32 * half);
+        buf[mb][kW - 1] = ld(128 * mb + 64 * blk + 32 * half + 16);
       }
     };
-    auto store_unit = [&](uint8_t* blk, int u, const uint32_t (&o)[8]) {
-      const uint32_t off = (uint32_t)(tok * 128 + half * 64 + u * 32);
-      *reinterpret_cast<uint4*>(blk + swz128(off)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(blk + swz128(off + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+    auto store = [&](uint8_t* a0, uint8_t* a1, const uint32_t (&o)[8]) {
+      *reinterpret_cast<uint4*>(a0) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(a1) = make_uint4(o[4], o[5], o[6], o[7]);
     };
-    auto publish = [&](uint32_t bar) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    bool have = advance();
+    step_page();
+    step_record();
+    step_page();
     if (have) {
       load_tail();
 #pragma unroll
-      for (int kb = 0; kb < kVB; ++kb) load_block(kb);
+      for (int mb = 0; mb < kPairs; ++mb) load_pair(mb);
     }
     uint32_t it = 0;
     while (have) {
-      uint32_t o[8];
-      bool ok = mbar_wait(kempty(it % kKSlots), ((it / kKSlots) & 1) ^ 1, abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t* kblk = smem + kOffK + (it % kKSlots) * kBlkBytes;
+      uint8_t* tile = smem + kOffTile + (it % kBufs) * kTileBytes;
+      const uint4 tail_now = tail;
+      step_record();
+      step_page();
+      if (have) load_tail();
+      bool ok = true;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        widen_e4m3(tail[u], o);
-        store_unit(kblk, u, o);
-      }
-      publish(kfull(it % kKSlots));
-      // this tile's scales: units 4 kb + 2 half + u, as bytes of the 32
-      uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
-      const bool more = advance();
-      if (more) load_tail();
-      uint32_t n = it * kVB;
-#pragma unroll
-      for (int kb = 0; kb < kVB; ++kb, ++n) {
-        const uint32_t slot = n % kVSlots;
-        ok = mbar_wait(vempty(slot), ((n / kVSlots) & 1) ^ 1, abort_flag, p.status);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        uint8_t* blk = smem + kOffV + slot * kBlkBytes;
-        if (kNV) {
-          const uint32_t pair = half ? scw[kb] >> 16 : scw[kb];
-          nvfp4x16_to_bf16x16(buf[kb][0].x, buf[kb][0].y, pair & 0xFFu, o);
-          store_unit(blk, 0, o);
-          nvfp4x16_to_bf16x16(buf[kb][0].z, buf[kb][0].w, (pair >> 8) & 0xFFu, o);
-          store_unit(blk, 1, o);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            widen_e4m3(buf[kb][u * (kW - 1)], o);
-            store_unit(blk, u, o);
-          }
+      for (int h = 0; h < 2; ++h) {
+        ok = mbar_wait(empty(it % kBufs, h), ((it / kBufs) & 1) ^ 1, abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
         }
-        publish(vfull(slot));
-        if (more) load_block(kb);
+        uint32_t o[8];
+#pragma unroll
+        for (int mb = 2 * h; mb < 2 * h + 2; ++mb) {
+          uint8_t* at = tile + 2 * mb * kBlkBytes;
+          if (kNV) {
+            nvfp4x16_to_f16x16(buf[mb][0].x, buf[mb][0].y, sc[mb] & 0xFFu, o);
+            store(at + o0, at + o1, o);
+            nvfp4x16_to_f16x16(buf[mb][0].z, buf[mb][0].w, sc[mb] >> 8, o);
+            store(at + o2, at + o3, o);
+          } else {
+            e4m3x16_to_f16x16(buf[mb][0], o);
+            store(at + o0, at + o1, o);
+            e4m3x16_to_f16x16(buf[mb][kW - 1], o);
+            store(at + o2, at + o3, o);
+          }
+          if (have) load_pair(mb);
+        }
+        if (h) {
+          e4m3x16_to_f16x16(tail_now, o);
+          store(tile + ot0, tile + ot1, o);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(it % kBufs, h));
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!ok) break;
       ++it;
-      have = more;
     }
   } else {
     // ------------------------------------------------ softmax (thread = head) and the parts' outputs
     const int h = threadIdx.x;
     const bool live = h < kHeads;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t it = 0;
+    uint32_t it = 0, seg = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
+      // ---- Q of head h to fp16 (every QK^T of the previous part has completed): dims 0..447 where TMA put them,
+      // 448..575 into TMEM
+      float c_log2;  // logits in log2 units per unit of S
       {
-        // Q dims 448..575 into TMEM (every QK^T of the previous part has completed)
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q_mla + ((int64_t)sg.row * kHeads + (live ? h : 0)) * kLatent + 64 * kQSmemBlocks);
         uint4 v[8 * kQTmemBlocks];
 #pragma unroll
         for (int c = 0; c < 8 * kQTmemBlocks; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        uint32_t am = 0;
+        auto more = [&](const uint4& w) {
+          am = bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(am, w.x), w.y), w.z), w.w);
+        };
+#pragma unroll
+        for (int c = 0; c < 8 * kQTmemBlocks; ++c) more(v[c]);
+        ok = mbar_wait(q_full, seg & 1, abort_flag, p.status);
+        if (bar_or_softmax(!ok)) { ok = false; break; }
+        uint8_t* q_row = smem + kOffQ;
+        if (live) {
+#pragma unroll 1
+          for (int kb = 0; kb < kQSmemBlocks; ++kb)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              more(*reinterpret_cast<const uint4*>(q_row + kb * kQBlockBytes + swz128(h * 128 + c * 16)));
+        }
+        const int e = f16_shift_of(am);
+        const float scale = __int_as_float((127 + e) << 23);
+        c_log2 = p.logit_scale_log2 * __int_as_float((127 - e) << 23);
+        if (live) {
+#pragma unroll 1
+          for (int kb = 0; kb < kQSmemBlocks; ++kb)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(q_row + kb * kQBlockBytes + swz128(h * 128 + c * 16));
+              const uint4 w = *at;
+              *at = make_uint4(bf16x2_to_f16x2(w.x, scale), bf16x2_to_f16x2(w.y, scale), bf16x2_to_f16x2(w.z, scale),
+                               bf16x2_to_f16x2(w.w, scale));
+            }
+        }
 #pragma unroll
         for (int c = 0; c < 8 * kQTmemBlocks; ++c)
-          tmem_st4(lane_base + kQ8Col + 4 * c, v[c].x, v[c].y, v[c].z, v[c].w);
+          tmem_st4(lane_base + kQ8Col + 4 * c, bf16x2_to_f16x2(v[c].x, scale), bf16x2_to_f16x2(v[c].y, scale),
+                   bf16x2_to_f16x2(v[c].z, scale), bf16x2_to_f16x2(v[c].w, scale));
         tmem_st_wait();
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q8_full);
+        if (lane == 0) mbar_arrive(q_ready);
+        ++seg;
       }
-      float m_used = -INFINITY, l_round = 0.f, l_exact = 0.f;
+      float m_used = -INFINITY, l_sum = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         ok = mbar_wait(s_full, it & 1, abort_flag, p.status);
         if (bar_or_softmax(!ok)) { ok = false; break; }
         tc_fence_after();
         uint32_t r[kTile];
         tmem_ld32(lane_base + kSCol, *reinterpret_cast<uint32_t(*)[32]>(r));
-        tmem_ld32(lane_base + kSCol + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tmem_ld16(lane_base + kSCol + 32, r + 32);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
@@ -502,27 +522,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid >= kTile) {
 #pragma unroll
           for (int j = 0; j < kTile; ++j) {
-            x[j] = __uint_as_float(r[j]) * p.logit_scale_log2;
+            x[j] = __uint_as_float(r[j]) * c_log2;
             mx[j & 3] = fmaxf(mx[j & 3], x[j]);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < kTile; ++j) {
-            x[j] = j < valid ? __uint_as_float(r[j]) * p.logit_scale_log2 : -INFINITY;
+            x[j] = j < valid ? __uint_as_float(r[j]) * c_log2 : -INFINITY;
             mx[j & 3] = fmaxf(mx[j & 3], x[j]);
           }
         }
         const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (x[0] != x[0]) m_used = x[0];  // NaN logits (a NaN in the query) give a NaN row
         const bool grow = live && m_tile > m_used + kRescaleThreshold;
         if (bar_or_softmax(grow)) {
           const float m_new = grow ? m_tile : m_used;
           const float alpha = (m_used == -INFINITY) ? 0.f : ex2f(m_used - m_new);
           if (live) alpha_s[h] = alpha;
-          l_round *= alpha;
-          l_exact *= alpha;
+          l_sum *= alpha;
           m_used = m_new;
           if (t > sg.t0) {
-            ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+            ok = mbar_wait(pv_done((it - 1) & 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
             if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
             tc_fence_after();
 #pragma unroll 1
@@ -541,29 +561,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t pk[kTile / 2];
         if (m_used != -INFINITY) {
-          float sr[2] = {0.f, 0.f}, se[2] = {0.f, 0.f};
+          // times 2^7: fp16 keeps its 11 bits for weights down to 2^-21 of the largest
+          const float m_ref = m_used - kPShift;
+          float se[2] = {0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < kTile; j += 2) {
-            const float p0 = ex2f(x[j] - m_used), p1 = ex2f(x[j + 1] - m_used);
-            const __nv_bfloat162 bb = __floats2bfloat162_rn(p0, p1);
-            const float2 back = __bfloat1622float2(bb);
-            sr[0] += back.x;
-            sr[1] += back.y;
+            const float p0 = ex2f(x[j] - m_ref), p1 = ex2f(x[j + 1] - m_ref);
+            const __half2 bb = __floats2half2_rn(p0, p1);
             se[0] += p0;
             se[1] += p1;
             pk[j >> 1] = *reinterpret_cast<const uint32_t*>(&bb);
           }
-          l_round += sr[0] + sr[1];
-          l_exact += se[0] + se[1];
+          l_sum += se[0] + se[1];
         } else {
 #pragma unroll
           for (int j = 0; j < kTile / 2; ++j) pk[j] = 0;
         }
-        // the P buffer was last read by the PV of the tile before
-        ok = it == 0 || mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+        // the P buffer was last read by the PV of the tile before the last
+        ok = mbar_wait(pv_done(it & 1), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
         if (bar_or_softmax(!ok)) { ok = false; break; }
         if (live) {
-          uint8_t* prow = smem + kOffP;
+          uint8_t* prow = smem + kOffP + (it & 1) * kPBytes;
 #pragma unroll
           for (int c = 0; c < kTile / 8; ++c)
             *reinterpret_cast<uint4*>(prow + swz128(h * 128 + c * 16)) =
@@ -572,20 +590,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(p_full(it & 1));
       }
-      if (ok) ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+      if (ok) ok = mbar_wait(pv_done((it - 1) & 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
       // ---- the part's O^T: lanes are dims of a 128-dim block, columns heads
       const bool direct = sg.slot < 0;
-      alpha_s[h] = (live && l_round > 0.f) ? (direct ? p.latent_scale : 1.f) / l_round : 0.f;
+      alpha_s[h] = live && m_used != -INFINITY ? (direct ? p.latent_scale : 1.f) / l_sum : 0.f;
       if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
       tc_fence_after();
       if (live) {
         if (direct)
           p.lse[(int64_t)sg.row * kHeads + h] =
-              l_exact > 0.f || l_exact != l_exact ? (m_used + log2f(l_exact)) * 0.69314718055994531f : -INFINITY;
+              m_used == -INFINITY ? -INFINITY : (m_used - kPShift + log2f(l_sum)) * 0.69314718055994531f;
         else
-          reinterpret_cast<float4*>(p.ml)[(int64_t)sg.slot * kHeads + h] = make_float4(m_used, l_round, l_exact, 0.f);
+          reinterpret_cast<float2*>(p.ml)[(int64_t)sg.slot * kHeads + h] = make_float2(m_used - kPShift, l_sum);
       }
       uint16_t* dst = direct ? p.out + (int64_t)sg.row * kPartO : p.opart + (int64_t)sg.slot * kPartO;
 #pragma unroll 1
@@ -640,32 +658,30 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
   auto slot_of = [&](int s) -> int64_t {
     return inv ? (int64_t)info.x + s : (s == 0 ? 2 * (int64_t)info.x + 1 : 2 * ((int64_t)info.x + s));
   };
-  const float4* ml4 = reinterpret_cast<const float4*>(ml);
+  const float2* ml2 = reinterpret_cast<const float2*>(ml);
   float M = -INFINITY;
-  for (int s = th & 31; s < parts; s += 32) M = fmaxf(M, ml4[slot_of(s) * kHeads + h].x);
+  for (int s = th & 31; s < parts; s += 32) M = fmaxf(M, ml2[slot_of(s) * kHeads + h].x);
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float den = 0.f, ex = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float den = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   constexpr int kU = 4;
   for (int s0 = grp; s0 < parts; s0 += kU * kGroups) {
-    float4 v[kU];
+    float2 v[kU];
     uint4 x[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int s = s0 + u * kGroups;
-      v[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      v[u] = make_float2(-INFINITY, 0.f);
       x[u] = make_uint4(0, 0, 0, 0);
       if (s < parts) {
         const int64_t slot = slot_of(s);
-        v[u] = ml4[slot * kHeads + h];
+        v[u] = ml2[slot * kHeads + h];
         x[u] = *reinterpret_cast<const uint4*>(opart + (slot * kHeads + h) * kValue + th * 8);
       }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const float e = v[u].x == -INFINITY ? 0.f : ex2f(v[u].x - M);
-      const float wt = e * v[u].y;  // a part is normalised by its own sum
+      const float wt = v[u].x == -INFINITY ? 0.f : ex2f(v[u].x - M) * v[u].y;  // a part is normalised by its own sum
       den += wt;
-      ex += e * v[u].z;
       const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -676,11 +692,11 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
     }
   }
   if constexpr (kGroups > 1) {
-    __shared__ float2 sum_s[kGroups - 1];
+    __shared__ float sum_s[kGroups - 1];
     if (grp > 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc_s[grp - 1][th][i] = a[i];
-      if (th == 0) sum_s[grp - 1] = make_float2(den, ex);
+      if (th == 0) sum_s[grp - 1] = den;
     }
     __syncthreads();
     if (grp > 0) return;
@@ -688,11 +704,10 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
     for (int g = 0; g < kGroups - 1; ++g) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) a[i] += acc_s[g][th][i];
-      den += sum_s[g].x;
-      ex += sum_s[g].y;
+      den += sum_s[g];
     }
   }
-  const float inv_den = latent_scale / den;
+  const float inv_den = M == -INFINITY ? 0.f : latent_scale / den;
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -701,7 +716,7 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
   }
   *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
   *reinterpret_cast<uint2*>(dst + 4) = make_uint2(o[2], o[3]);
-  if (th == 0) lse[(int64_t)row * kHeads + h] = (M + log2f(ex)) * 0.69314718055994531f;
+  if (th == 0) lse[(int64_t)row * kHeads + h] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
 }
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -721,7 +736,7 @@ int64_t dense_slots(int rows, int max_len, bool inv) {
 
 size_t dense_mla_workspace_bytes(int rows, int max_len) {
   const int64_t slots = dense_slots(rows, max_len, mla_batch_invariant_on());
-  return al256((size_t)rows * sizeof(int2)) + al256((size_t)slots * kPartO * 2) + al256((size_t)slots * kHeads * 16);
+  return al256((size_t)rows * sizeof(int2)) + al256((size_t)slots * kPartO * 2) + al256((size_t)slots * kHeads * 8);
 }
 
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,

@@ -101,6 +101,32 @@ def test_dense_mla_sharp_heads(fmt):
     check_rows(case, out, lse)
 
 
+@pytest.mark.parametrize("fmt", [FP8, NV])
+def test_dense_mla_single_tokens_are_bit_exact(fmt):
+    """One token a row: out is its value rounded to bf16, for every E2M1 code under every E4M3 block scale (each in
+    some sequence), and every E4M3 code."""
+    n = 32
+    case = synth.make_case("dense_one", seq_lens=[1] * n, seed=22, latent_format=fmt)
+    rec = case.latent_bytes()
+    codes = [c for c in range(256) if c & 0x7F != 0x7F]
+    for b in range(n):
+        if fmt == NV:
+            r = np.zeros(352, dtype=np.uint8)
+            r[:256] = [((i + b) % 16) | (((5 * i + 2) % 16) << 4) for i in range(256)]
+            r[256:288] = [codes[(8 * b + i) % len(codes)] for i in range(32)]
+            r[288:] = [codes[(3 * i + b) % len(codes)] for i in range(64)]
+        else:
+            r = np.array([codes[(i + 7 * b) % len(codes)] for i in range(576)], dtype=np.uint8)
+        case.pool[case.block_table[b, 0], case.latent_off:case.latent_off + rec] = r
+    for scale in (1.0, 0.75):
+        one = dataclasses.replace(case, latent_scale=scale)
+        out, lse, st = run_dense(one, synth.device_case(one))
+        assert st == 0
+        for b in range(n):
+            v = (plain64.latents(case, b)[0, :512] / case.latent_scale).float() * np.float32(scale)
+            assert torch.equal(out[b].float().cpu(), v.to(torch.bfloat16).float().expand(96, 512)), b
+
+
 def test_dense_mla_layout_and_filler():
     """Index pages before the latent pages, padding between rows, and NaN codes in every slot behind a context."""
     case = synth.make_case("dense_layout", seq_lens=[70, 129], seed=10, key_format=synth.KEY_MXFP4, latent_format=NV,
