@@ -232,25 +232,14 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// The same two, issued by the lane whose `leader` is not 0 of a warp that runs
-// converged.  Where one lane alone runs the issuing loop, the compiler cannot
-// keep descriptors in uniform registers, and moving them there costs more than
-// the multiplication of a small tile (36 of N = 48: 1.6 us instead of 0.7).
-__device__ __forceinline__ void mma_f16_by(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_tmem_a_by(uint32_t leader, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                                  uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-      ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
+// True in one lane of a converged warp, always the same one.  An issuing warp
+// runs its loops and waits as a whole and only its MMAs and commits under this:
+// a lone lane's loop, or a per-lane predicate on each MMA, costs more than the
+// multiplication of a small tile.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r) :: "memory");
+  return r != 0;
 }
 // mbar_wait by a whole warp, with the same answer in every lane.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {

@@ -48,8 +48,8 @@ namespace {
 constexpr int kTile = 48;                              // tokens per tile
 constexpr int kDB = kLatent / 64;                      // 9 blocks of 64 dims
 constexpr int kVB = kValue / 64;                       // 8 of them are values
-constexpr int kQTmemBlocks = 2;                        // Q dims 448..575 in TMEM
-constexpr int kQSmemBlocks = kDB - kQTmemBlocks;       // Q dims 0..447 in shared memory
+constexpr int kQTmemBlocks = 1;                        // Q dims 512..575 in TMEM
+constexpr int kQSmemBlocks = kDB - kQTmemBlocks;       // Q dims 0..511 in shared memory
 constexpr int kQBlockBytes = kHeads * 128;             // 12,288
 constexpr int kBlkBytes = kTile * 128;                 // 6,144: 48 tokens x 64 dims of bf16
 constexpr int kPairs = kVB / 2;                        // a pair of blocks: the 128 dims of one PV product
@@ -64,9 +64,9 @@ constexpr int kQkWarp = 10;
 constexpr int kPvWarp = 11;
 static_assert(kLoadWarps * 8 == kTile, "loader split");
 constexpr int kOCols = 4 * kHeads;                     // 384
-constexpr int kSCol = kOCols;                          // 384..447
-constexpr int kQ8Col = 448;                            // 448..511
-static_assert(kSCol + kTile <= kQ8Col && kQ8Col + 32 * kQTmemBlocks <= 512, "TMEM columns");
+constexpr int kSCol = kOCols;                          // two S tiles: 384..479
+constexpr int kQ8Col = kSCol + 2 * kTile;              // 480..511
+static_assert(kQ8Col + 32 * kQTmemBlocks <= 512, "TMEM columns");
 constexpr float kRescaleThreshold = 8.0f;              // log2 units
 constexpr float kPShift = 7.0f;                        // P is stored times 2^7, at most 2^15
 constexpr int kMinTiles = 2;                           // tiles per CTA before more CTAs are used
@@ -76,9 +76,9 @@ constexpr int kInvariantTiles = 80;                    // tiles per part in the 
 constexpr int kOffQ = 0;
 constexpr int kOffTile = kOffQ + kQSmemBlocks * kQBlockBytes;  // 86,016
 constexpr int kOffP = kOffTile + kBufs * kTileBytes;           // 196,608
-constexpr int kOffAlpha = kOffP + 2 * kPBytes;                     // 229,376
+constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
 constexpr int kOffBars = kOffAlpha + 512;
-constexpr int kNumBars = 4 * kBufs + 11;
+constexpr int kNumBars = 4 * kBufs + 10;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;              // TMEM slot, abort flag, scan scratch
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 256;
 static_assert(kOffTile % 1024 == 0 && kOffP % 1024 == 0 && kBlkBytes % 1024 == 0, "swizzle atoms");
@@ -213,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto full = [&](uint32_t buf, int half) { return bars + 8u * (2 * buf + half); };
   auto empty = [&](uint32_t buf, int half) { return bars + 8u * (2 * kBufs + 2 * buf + half); };
   const uint32_t bars2 = bars + 8u * (4 * kBufs);
-  const uint32_t q_full = bars2, q_ready = bars2 + 8, s_full = bars2 + 16, s_empty = bars2 + 24, o_free = bars2 + 32,
-                 drain = bars2 + 40;
-  auto p_full = [&](uint32_t b) { return bars2 + 48 + 8 * b; };
-  auto pv_done = [&](uint32_t b) { return bars2 + 64 + 8 * b; };  // PV of the tiles that use P buffer b
+  const uint32_t q_full = bars2, q_ready = bars2 + 8, o_free = bars2 + 16, drain = bars2 + 24, p_full = bars2 + 32,
+                 pv_done = bars2 + 40;
+  auto s_full = [&](uint32_t b) { return bars2 + 48 + 8 * b; };
+  auto s_empty = [&](uint32_t b) { return bars2 + 64 + 8 * b; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
@@ -231,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     mbar_init(q_full, 1);
     mbar_init(q_ready, 4);
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(p_full(b), 4);
-      mbar_init(pv_done(b), 1);
+      mbar_init(s_full(b), 1);
+      mbar_init(s_empty(b), 4);
     }
     mbar_init(o_free, 4);
     mbar_init(drain, 2);
@@ -253,23 +253,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Segment sg;
+  // walk.next by a whole warp, with values that the compiler knows to be the same in every lane
+  auto next_uniform = [&](Segment& s) -> bool {
+    const bool more = __all_sync(0xffffffffu, walk.next(s));
+    s.row = __shfl_sync(0xffffffffu, s.row, 0);
+    s.t0 = __shfl_sync(0xffffffffu, s.t0, 0);
+    s.t1 = __shfl_sync(0xffffffffu, s.t1, 0);
+    return more;
+  };
 
   if (warp == kQkWarp) {
-    // ------------------------------------------------ QK issuer (the whole warp runs, lane 0 issues)
-    const uint32_t leader = lane == 0;
+    // ------------------------------------------------ QK issuer (the whole warp runs, one lane issues)
     const uint64_t q_desc = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSw128);
     const uint32_t q_lo = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
     const uint32_t t_lo0 = (uint32_t)smem_desc(sbase + kOffTile, 16, 1024, kLayoutSw128);
     uint32_t it = 0, seg = 0;
     bool ok = true;
-    const uint32_t d = tmem + kSCol;
-    while (ok && walk.next(sg)) {
-      // the previous part's last S tile has been read by the softmax, so its QK^T has completed: Q may go
-      if (seg > 0) ok = mbar_wait_warp(s_empty, (it & 1) ^ 1, abort_flag, p.status);
+    while (ok && next_uniform(sg)) {
+      // the previous part's last QK^T has completed: Q may go
+      if (it > 0) ok = mbar_wait_warp(s_full((it - 1) & 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
       if (!ok) break;
-      if (leader) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(q_full, kQSmemBlocks * kQBlockBytes);
         for (int kb = 0; kb < kQSmemBlocks; ++kb)
           tma_load_2d(sbase + kOffQ + kb * kQBlockBytes, &tmap_q, kb * 64, sg.row * kHeads, q_full);
@@ -279,38 +285,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(q_ready, seg & 1, abort_flag, p.status);
       ++seg;
       for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
-        ok = mbar_wait_warp(s_empty, (it & 1) ^ 1, abort_flag, p.status);
+        ok = mbar_wait_warp(s_empty(it & 1), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+        const uint32_t d = tmem + kSCol + (it & 1) * kTile;
         const uint32_t buf = it % kBufs, t_lo = t_lo0 + buf * (kTileBytes / 16);
-        // rolled loops: issued once a tile each, 36 instructions in a row would be
-        // fetched anew every time (3.0 against 2.2 ms on the 512-row chunk)
         int kb = 0;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           ok = ok && mbar_wait_warp(full(buf, half), (it / kBufs) & 1, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
-          const int end = half ? kQSmemBlocks : kVB / 2;
+          if (elect_one()) {
+            const int end = half ? kQSmemBlocks : kVB / 2;
 #pragma unroll 1
-          for (; kb < end; ++kb) {
-            const uint32_t a_lo = q_lo + kb * (kQBlockBytes / 16), b_lo = t_lo + kb * (kBlkBytes / 16);
+            for (; kb < end; ++kb) {
+              const uint32_t a_lo = q_lo + kb * (kQBlockBytes / 16), b_lo = t_lo + kb * (kBlkBytes / 16);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_by(leader, d, desc64(a_lo + 2 * kk, hi), desc64(b_lo + 2 * kk, hi), kIdescQK, (kb | kk) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(d, desc64(a_lo + 2 * kk, hi), desc64(b_lo + 2 * kk, hi), kIdescQK, (kb | kk) ? 1u : 0u);
+            }
+            if (half) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // dims 512..575: A from TMEM
+                mma_bf16_tmem_a(d, tmem + kQ8Col + 8 * kk, desc64(t_lo + kQSmemBlocks * (kBlkBytes / 16) + 2 * kk, hi), kIdescQK, 1u);
+              mma_commit(s_full(it & 1));
+            }
           }
+          __syncwarp();
+          kb = kVB / 2;
         }
         if (!ok) break;
-#pragma unroll 1
-        for (; kb < kDB; ++kb) {  // dims 448..575: A from TMEM
-          const uint32_t a_t = tmem + kQ8Col + 32 * (kb - kQSmemBlocks), b_lo = t_lo + kb * (kBlkBytes / 16);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_tmem_a_by(leader, d, a_t + 8 * kk, desc64(b_lo + 2 * kk, hi), kIdescQK, 1u);
-        }
-        if (leader) mma_commit(s_full);
         __syncwarp();
       }
     }
-    if (leader) {
+    if (elect_one()) {
       if (seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, 10000000ull);  // no copy is in flight at the exit
       // both issuers' MMAs complete before TMEM is released
       mma_commit(drain);
@@ -318,38 +325,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kPvWarp) {
     // ------------------------------------------------ PV issuer (likewise)
-    const uint32_t leader = lane == 0;
     const uint64_t a_desc = smem_desc(sbase + kOffTile, kBlkBytes, 1024, kLayoutSw128);
     const uint32_t a_lo0 = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
     const uint64_t p_desc = smem_desc(sbase + kOffP, 16, 1024, kLayoutSw128);
-    const uint32_t p_lo0 = (uint32_t)p_desc, p_hi = (uint32_t)(p_desc >> 32);
+    const uint32_t p_lo = (uint32_t)p_desc, p_hi = (uint32_t)(p_desc >> 32);
     uint32_t it = 0, seg = 0;
     bool ok = true;
-    while (ok && walk.next(sg)) {
+    while (ok && next_uniform(sg)) {
       // the previous part's O^T has been read
       if (seg > 0) ok = mbar_wait_warp(o_free, (seg - 1) & 1, abort_flag, p.status);
       ++seg;
       for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
-        ok = mbar_wait_warp(p_full(it & 1), (it >> 1) & 1, abort_flag, p.status);
+        ok = mbar_wait_warp(p_full, it & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t more = t > sg.t0;
-        const uint32_t p_lo = p_lo0 + (it & 1) * (kPBytes / 16);
         const uint32_t a_lo = a_lo0 + (it % kBufs) * (kTileBytes / 16);
+        if (elect_one()) {
 #pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
+          for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_f16_by(leader, tmem + mb * kHeads, desc64(a_lo + 2 * mb * (kBlkBytes / 16) + 2 * ks * 64, a_hi),
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_bf16(tmem + mb * kHeads, desc64(a_lo + 2 * mb * (kBlkBytes / 16) + 2 * ks * 64, a_hi),
                        desc64(p_lo + 2 * ks, p_hi), kIdescPV, ks > 0 ? 1u : more);
-          // QK^T of this tile completed before its P existed, so half the tile is free after these
-          if ((mb & 1) && leader) mma_commit(empty(it % kBufs, mb >> 1));
+            // QK^T of this tile completed before its P existed, so half the tile is free after these
+            if (mb & 1) mma_commit(empty(it % kBufs, mb >> 1));
+          }
+          mma_commit(pv_done);
         }
-        if (leader) mma_commit(pv_done(it & 1));
         __syncwarp();
       }
     }
-    if (leader) {
+    if (elect_one()) {
       mma_commit(drain);
       mbar_wait_drain(drain, 0, 10000000ull);
     }
@@ -431,32 +438,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        // widened before the wait: from the half's release to its being full is
+        // then a few stores (a buffer's round of load, QK^T, softmax and PV is
+        // what paces two tile buffers)
+        uint32_t o[5][8];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int mb = 2 * h + m;
+          if (kNV) {
+            nvfp4x16_to_f16x16(buf[mb][0].x, buf[mb][0].y, sc[mb] & 0xFFu, o[2 * m]);
+            nvfp4x16_to_f16x16(buf[mb][0].z, buf[mb][0].w, sc[mb] >> 8, o[2 * m + 1]);
+          } else {
+            e4m3x16_to_f16x16(buf[mb][0], o[2 * m]);
+            e4m3x16_to_f16x16(buf[mb][kW - 1], o[2 * m + 1]);
+          }
+          if (have) load_pair(mb);
+        }
+        if (h) e4m3x16_to_f16x16(tail_now, o[4]);
         ok = mbar_wait(empty(it % kBufs, h), ((it / kBufs) & 1) ^ 1, abort_flag, p.status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        uint32_t o[8];
 #pragma unroll
-        for (int mb = 2 * h; mb < 2 * h + 2; ++mb) {
-          uint8_t* at = tile + 2 * mb * kBlkBytes;
-          if (kNV) {
-            nvfp4x16_to_f16x16(buf[mb][0].x, buf[mb][0].y, sc[mb] & 0xFFu, o);
-            store(at + o0, at + o1, o);
-            nvfp4x16_to_f16x16(buf[mb][0].z, buf[mb][0].w, sc[mb] >> 8, o);
-            store(at + o2, at + o3, o);
-          } else {
-            e4m3x16_to_f16x16(buf[mb][0], o);
-            store(at + o0, at + o1, o);
-            e4m3x16_to_f16x16(buf[mb][kW - 1], o);
-            store(at + o2, at + o3, o);
-          }
-          if (have) load_pair(mb);
+        for (int m = 0; m < 2; ++m) {
+          uint8_t* at = tile + (4 * h + 2 * m) * kBlkBytes;
+          store(at + o0, at + o1, o[2 * m]);
+          store(at + o2, at + o3, o[2 * m + 1]);
         }
-        if (h) {
-          e4m3x16_to_f16x16(tail_now, o);
-          store(tile + ot0, tile + ot1, o);
-        }
+        if (h) store(tile + ot0, tile + ot1, o[4]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full(it % kBufs, h));
@@ -472,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, seg = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
-      // ---- Q of head h to fp16 (every QK^T of the previous part has completed): dims 0..447 where TMA put them,
-      // 448..575 into TMEM
+      // ---- Q of head h to fp16 (every QK^T of the previous part has completed): dims 0..511 where TMA put them,
+      // 512..575 into TMEM
       float c_log2;  // logits in log2 units per unit of S
       {
         const uint4* src = reinterpret_cast<const uint4*>(
@@ -524,16 +534,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m_used = -INFINITY, l_sum = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        ok = mbar_wait(s_full, it & 1, abort_flag, p.status);
-        if (bar_or_softmax(!ok)) { ok = false; break; }
+        ok = ok && mbar_wait(s_full(it & 1), (it >> 1) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         uint32_t r[kTile];
-        tmem_ld32(lane_base + kSCol, *reinterpret_cast<uint32_t(*)[32]>(r));
-        tmem_ld16(lane_base + kSCol + 32, r + 32);
+        const uint32_t s_col = lane_base + kSCol + (it & 1) * kTile;
+        tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_ld16(s_col + 32, r + 32);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty);
+        if (lane == 0) mbar_arrive(s_empty(it & 1));
         const int valid = sg.vis - t * kTile;
         float x[kTile];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -553,14 +564,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (x[0] != x[0]) m_used = x[0];  // NaN logits (a NaN in the query) give a NaN row
         const bool grow = live && m_tile > m_used + kRescaleThreshold;
-        if (bar_or_softmax(grow)) {
+        // one barrier a tile: any head that grew, and any warp whose wait ran out
+        if (bar_or_softmax(grow || !ok)) {
+          if (bar_or_softmax(!ok)) { ok = false; break; }
           const float m_new = grow ? m_tile : m_used;
           const float alpha = (m_used == -INFINITY) ? 0.f : ex2f(m_used - m_new);
           if (live) alpha_s[h] = alpha;
           l_sum *= alpha;
           m_used = m_new;
           if (t > sg.t0) {
-            ok = mbar_wait(pv_done((it - 1) & 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
+            ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
             if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
             tc_fence_after();
 #pragma unroll 1
@@ -595,11 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kTile / 2; ++j) pk[j] = 0;
         }
-        // the P buffer was last read by the PV of the tile before the last
-        ok = mbar_wait(pv_done(it & 1), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
-        if (bar_or_softmax(!ok)) { ok = false; break; }
-        if (live) {
-          uint8_t* prow = smem + kOffP + (it & 1) * kPBytes;
+        // the PV of the tile before has read the P buffer; a wait that runs out is
+        // told to the other warps at the next barrier
+        ok = it == 0 || mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (live && ok) {
+          uint8_t* prow = smem + kOffP;
 #pragma unroll
           for (int c = 0; c < kTile / 8; ++c)
             *reinterpret_cast<uint4*>(prow + swz128(h * 128 + c * 16)) =
@@ -608,9 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(it & 1));
+        if (ok && lane == 0) mbar_arrive(p_full);
       }
-      if (ok) ok = mbar_wait(pv_done((it - 1) & 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
+      if (ok) ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
       // ---- the part's O^T: lanes are dims of a 128-dim block, columns heads
       const bool direct = sg.slot < 0;
       alpha_s[h] = live && m_used != -INFINITY ? (direct ? p.latent_scale : 1.f) / l_sum : 0.f;
