@@ -57,12 +57,11 @@ constexpr int kTileBytes = kDB * kBlkBytes;            // 55,296; block 8 holds 
 constexpr int kBufs = 2;                               // tile buffers, each filled and freed in two halves
 constexpr int kPBytes = kHeads * 128;                  // 12,288: a head's 48 bf16 in a 128-byte row
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);  // 352 B
-constexpr int kThreads = 12 * 32;  // softmax 0-3, loaders 4-9, QK issuer 10, PV issuer 11
+constexpr int kThreads = 15 * 32;  // softmax 0-3, loaders 4-12 (one 64-dim block each), QK issuer 13, PV issuer 14
 constexpr int kLoadWarp0 = 4;
-constexpr int kLoadWarps = 6;   // 8 tokens a warp
-constexpr int kQkWarp = 10;
-constexpr int kPvWarp = 11;
-static_assert(kLoadWarps * 8 == kTile, "loader split");
+constexpr int kQkWarp = 13;
+constexpr int kPvWarp = 14;
+static_assert(kLoadWarp0 + kDB == kQkWarp, "a loader warp a block");
 constexpr int kOCols = 4 * kHeads;                     // 384
 constexpr int kSCol = kOCols;                          // two S tiles: 384..479
 constexpr int kQ8Col = kSCol + 2 * kTile;              // 480..511
@@ -80,7 +79,7 @@ constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
 constexpr int kOffBars = kOffAlpha + 512;
 constexpr int kNumBars = 4 * kBufs + 10;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;              // TMEM slot, abort flag, scan scratch
-constexpr size_t kSmemBytes = 1024 + kOffMisc + 256;
+constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
 static_assert(kOffTile % 1024 == 0 && kOffP % 1024 == 0 && kBlkBytes % 1024 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 232448, "shared memory");
 
@@ -199,6 +198,9 @@ __device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
   return w;
 }
 
+// What a lane without a token reads: zeros take no part in the products.
+__device__ const uint4 zero_record[kLatent / 16] = {};
+
 template <bool kNV>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ DenseParams p) {
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kBufs; ++s)
       for (int h = 0; h < 2; ++h) {
-        mbar_init(full(s, h), kLoadWarps);
+        mbar_init(full(s, h), h ? kDB - kVB / 2 : kVB / 2);
         mbar_init(empty(s, h), 1);
       }
     mbar_init(q_full, 1);
@@ -360,121 +362,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(drain);
       mbar_wait_drain(drain, 0, 10000000ull);
     }
-  } else if (warp >= kLoadWarp0) {
+  } else if (warp >= kLoadWarp0 && warp < kQkWarp) {
     // ------------------------------------------------ loaders: page -> bf16 blocks
-    // Warp w: tokens 8 w .. 8 w + 7, four lanes a token, a lane 32 dims of each
-    // pair (block `blk`, its half `half`) and 16 dims of the key-only block.  The
-    // lanes are numbered so that eight neighbours store 16 bytes each to all 32
-    // banks.  A pair's codes are loaded a whole tile before they are stored, and a
-    // token's page is looked up two tiles ahead.
-    constexpr int kW = kNV ? 1 : 2;  // 16-byte words of a pair and lane
-    const int half = lane & 1, blk = (lane >> 3) & 1;
-    const int tok = (warp - kLoadWarp0) * 8 + ((lane >> 1) & 3) + ((lane >> 4) & 1) * 4;
-    const uint32_t off = (uint32_t)(tok * 128 + half * 64);
-    const uint32_t o0 = blk * kBlkBytes + swz128(off), o1 = blk * kBlkBytes + swz128(off + 16),
-                   o2 = blk * kBlkBytes + swz128(off + 32), o3 = blk * kBlkBytes + swz128(off + 48);
-    const uint32_t ot = (uint32_t)(tok * 128 + blk * 64 + half * 32);
-    const uint32_t ot0 = (kDB - 1) * kBlkBytes + swz128(ot), ot1 = (kDB - 1) * kBlkBytes + swz128(ot + 16);
-    uint4 buf[kPairs][kW], tail;
-    uint32_t sc[kPairs];
-    const uint8_t* rec = nullptr;  // null: no such token, or a bad table entry
-    int row = -1, t = 0, t1 = 0, page = -1, slot_b = 0;
-    bool have_page = false, live_b = false, have = false;
-    auto step_page = [&]() {  // the next tile's page
+    // Warp kb: the 64 dims of block kb, two lanes a token, 16 tokens at a time.
+    // Eight neighbouring lanes store 16 bytes each to all 32 banks.  Codes are
+    // loaded a whole tile before they are stored, a token's page is looked up two
+    // tiles ahead, and codes are widened before the wait for the buffer.
+    constexpr int kTt = kTile / 16;  // tokens of a lane
+    const int kb = warp - kLoadWarp0, h = kb >= kVB / 2;
+    const bool four = kNV && kb < kVB;  // E2M1 codes with block scales; else E4M3 codes
+    const int sub = lane & 1, tok0 = lane >> 1;
+    const uint32_t off = (uint32_t)(kb * kBlkBytes + tok0 * 128 + sub * 64);
+    uint32_t o0 = swz128(off), o1 = swz128(off + 16), o2 = swz128(off + 32), o3 = swz128(off + 48);
+    // byte offsets in a record of this lane's codes and scales
+    const int c0 = four ? 32 * kb + 16 * sub : (kNV ? kValue / 2 + kValue / 16 : 64 * kb) + 32 * sub;
+    const int s0 = kValue / 2 + 4 * kb + 2 * sub;
+    uint4 buf[kTt][2];
+    uint32_t sc[kTt];
+    const uint8_t* none = reinterpret_cast<const uint8_t*>(zero_record);
+    const uint8_t* rec[kTt];
+    const int32_t* table = nullptr;
+    int t = 0, t1 = 0, page[kTt], first = 0, vis = 0;
+    bool have_page = false, have = false;
+    auto step_page = [&]() {  // the next tile's pages
       have_page = t < t1;
       if (!have_page && walk.next(sg)) {
-        row = sg.row;
+        table = p.block_table + (int64_t)(sg.row / p.nq) * p.max_blocks;
+        vis = sg.vis;
         t = sg.t0;
         t1 = sg.t1;
         have_page = true;
       }
       if (!have_page) return;
-      const int token = t++ * kTile + tok;
-      live_b = token < sg.vis;
-      page = live_b ? p.block_table[(int64_t)(row / p.nq) * p.max_blocks + token / kBlock] : -1;
-      slot_b = token % kBlock;
+      first = t++ * kTile + tok0;
+#pragma unroll
+      for (int i = 0; i < kTt; ++i)
+        if (first + 16 * i < vis) page[i] = table[(first + 16 * i) / kBlock];
     };
     auto step_record = [&]() {
       have = have_page;
-      rec = nullptr;
-      if (!have || !live_b) return;
-      if (page >= 0 && page < p.num_blocks)
-        rec = p.latent_base + (int64_t)page * p.row_stride + slot_b * kRec;
-      else
-        report(p.status, DSA_ERR_BOUNDS);
-    };
-    auto ld = [&](int off) {
-      return rec ? __ldg(reinterpret_cast<const uint4*>(rec + off)) : make_uint4(0, 0, 0, 0);
-    };
-    auto load_tail = [&]() { tail = ld((kNV ? kValue / 2 + kValue / 16 : kValue) + 32 * blk + 16 * half); };
-    auto load_pair = [&](int mb) {
-      if (kNV) {
-        buf[mb][0] = ld(64 * mb + 32 * blk + 16 * half);
-        sc[mb] = rec ? __ldg(reinterpret_cast<const uint16_t*>(rec + kValue / 2 + 8 * mb + 4 * blk + 2 * half)) : 0u;
-      } else {
-        buf[mb][0] = ld(128 * mb + 64 * blk + 32 * half);
-        buf[mb][kW - 1] = ld(128 * mb + 64 * blk + 32 * half + 16);
+#pragma unroll
+      for (int i = 0; i < kTt; ++i) {
+        rec[i] = none;  // no such token, or a bad table entry: zeros
+        const int token = first + 16 * i;
+        if (!have || token >= vis) continue;
+        if ((uint32_t)page[i] < (uint32_t)p.num_blocks)
+          rec[i] = p.latent_base + (int64_t)page[i] * p.row_stride + token % kBlock * kRec;
+        else
+          report(p.status, DSA_ERR_BOUNDS);
       }
     };
-    auto store = [&](uint8_t* a0, uint8_t* a1, const uint32_t (&o)[8]) {
-      *reinterpret_cast<uint4*>(a0) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(a1) = make_uint4(o[4], o[5], o[6], o[7]);
+    auto load = [&]() {
+#pragma unroll
+      for (int i = 0; i < kTt; ++i) {
+        buf[i][0] = __ldg(reinterpret_cast<const uint4*>(rec[i] + c0));
+        if (four)
+          sc[i] = __ldg(reinterpret_cast<const uint16_t*>(rec[i] + s0));
+        else
+          buf[i][1] = __ldg(reinterpret_cast<const uint4*>(rec[i] + c0 + 16));
+      }
     };
     step_page();
     step_record();
     step_page();
-    if (have) {
-      load_tail();
-#pragma unroll
-      for (int mb = 0; mb < kPairs; ++mb) load_pair(mb);
-    }
+    if (have) load();
     uint32_t it = 0;
     while (have) {
-      uint8_t* tile = smem + kOffTile + (it % kBufs) * kTileBytes;
-      const uint4 tail_now = tail;
+      uint32_t o[2 * kTt][8];
+#pragma unroll
+      for (int i = 0; i < kTt; ++i) {
+        if (four) {
+          nvfp4x16_to_f16x16(buf[i][0].x, buf[i][0].y, sc[i] & 0xFFu, o[2 * i]);
+          nvfp4x16_to_f16x16(buf[i][0].z, buf[i][0].w, sc[i] >> 8, o[2 * i + 1]);
+        } else {
+          e4m3x16_to_f16x16(buf[i][0], o[2 * i]);
+          e4m3x16_to_f16x16(buf[i][1], o[2 * i + 1]);
+        }
+      }
       step_record();
       step_page();
-      if (have) load_tail();
-      bool ok = true;
+      if (have) load();
+      if (!mbar_wait_warp(empty(it % kBufs, h), ((it / kBufs) & 1) ^ 1, abort_flag, p.status)) break;
+      uint8_t* tile = smem + kOffTile + (it % kBufs) * kTileBytes;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // widened before the wait: from the half's release to its being full is
-        // then a few stores (a buffer's round of load, QK^T, softmax and PV is
-        // what paces two tile buffers)
-        uint32_t o[5][8];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int mb = 2 * h + m;
-          if (kNV) {
-            nvfp4x16_to_f16x16(buf[mb][0].x, buf[mb][0].y, sc[mb] & 0xFFu, o[2 * m]);
-            nvfp4x16_to_f16x16(buf[mb][0].z, buf[mb][0].w, sc[mb] >> 8, o[2 * m + 1]);
-          } else {
-            e4m3x16_to_f16x16(buf[mb][0], o[2 * m]);
-            e4m3x16_to_f16x16(buf[mb][kW - 1], o[2 * m + 1]);
-          }
-          if (have) load_pair(mb);
-        }
-        if (h) e4m3x16_to_f16x16(tail_now, o[4]);
-        ok = mbar_wait(empty(it % kBufs, h), ((it / kBufs) & 1) ^ 1, abort_flag, p.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint8_t* at = tile + (4 * h + 2 * m) * kBlkBytes;
-          store(at + o0, at + o1, o[2 * m]);
-          store(at + o2, at + o3, o[2 * m + 1]);
-        }
-        if (h) store(tile + ot0, tile + ot1, o[4]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(it % kBufs, h));
+      for (int i = 0; i < kTt; ++i) {
+        uint8_t* at = tile + 2048 * i;  // 16 tokens on: two swizzle atoms
+        *reinterpret_cast<uint4*>(at + o0) = make_uint4(o[2 * i][0], o[2 * i][1], o[2 * i][2], o[2 * i][3]);
+        *reinterpret_cast<uint4*>(at + o1) = make_uint4(o[2 * i][4], o[2 * i][5], o[2 * i][6], o[2 * i][7]);
+        *reinterpret_cast<uint4*>(at + o2) = make_uint4(o[2 * i + 1][0], o[2 * i + 1][1], o[2 * i + 1][2], o[2 * i + 1][3]);
+        *reinterpret_cast<uint4*>(at + o3) = make_uint4(o[2 * i + 1][4], o[2 * i + 1][5], o[2 * i + 1][6], o[2 * i + 1][7]);
       }
-      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(it % kBufs, h));
       ++it;
     }
-  } else {
+  } else if (warp < kLoadWarp0) {
     // ------------------------------------------------ softmax (thread = head) and the parts' outputs
     const int h = threadIdx.x;
     const bool live = h < kHeads;

@@ -10,11 +10,13 @@
 // tiles of 128 tokens lie on one line, equal runs of it to every CTA.
 //   * S^T = K Q^T with the tokens on M = 128 rows and the heads on N = 96: the
 //     sum over heads then stays inside a thread, and no MMA row is wasted.  Q
-//     (110 KB) stays in shared memory while a CTA works on a row; the tiles
-//     stream past it in stages of three 64-dim blocks (two stages).
-//   * warps 4..11 load the tiles' records a whole tile ahead in registers (two
-//     lanes a token, 16-byte loads, contiguous or gathered alike), widen them
-//     exactly to bf16 and store them 128-byte swizzled, as the attention does.
+//     (110 KB, turned into fp16 in place) stays in shared memory while a CTA
+//     works on a row; 64-dim blocks of keys pass through a ring of 7.
+//   * warp 12 resolves tokens to records (index, page, slot) three tiles ahead.
+//   * warps 4..10 each fill one slot of the ring, so a warp takes every seventh
+//     block of the stream: the records' 64 dims, two lanes a token, loaded seven
+//     blocks ahead in registers, widened exactly to fp16 and stored 128-byte
+//     swizzled.
 //   * warps 0..3, one thread a token: sum over heads of 2^(s c - lse c'), from
 //     one of two S tiles in TMEM while the next is computed.
 // With one row per sequence and no selection the kernel adds the running total
@@ -40,26 +42,26 @@ constexpr int kTok = 128;                        // tokens per tile
 constexpr int kDB = kLatent / 64;                // 9 blocks of 64 dims
 constexpr int kQBlockBytes = kHeads * 128;       // 12,288
 constexpr int kBlkBytes = kTok * 128;            // 16,384
-constexpr int kStageBlocks = 3;
-constexpr int kStagesPerTile = kDB / kStageBlocks;
-constexpr int kStages = 2;
-constexpr int kStageBytes = kStageBlocks * kBlkBytes;  // 49,152
+constexpr int kSlots = 7;                        // ring of blocks
+constexpr int kInfos = 4;                        // tiles whose records are resolved
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);
-constexpr int kThreads = 13 * 32;                // epilogue 0-3, loaders 4-11, MMA issuer 12
+constexpr int kThreads = 13 * 32;                // epilogue 0-3, loaders 4-10 (a ring slot each), MMA issuer 11, lookup 12
 constexpr int kLoadWarp0 = 4;
-constexpr int kLoadWarps = 8;
-constexpr int kMmaWarp = 12;
+constexpr int kMmaWarp = 11;
+constexpr int kLookupWarp = 12;
+static_assert(kLoadWarp0 + kSlots == kMmaWarp, "a loader warp a slot");
 constexpr int kSCols = 128;                      // columns between the two S tiles
 constexpr int kTmemCols = 256;
 
 constexpr int kOffQ = 0;
-constexpr int kOffStage = kDB * kQBlockBytes;                  // 110,592
-constexpr int kOffLse = kOffStage + kStages * kStageBytes;     // 208,896
-constexpr int kOffBars = kOffLse + kHeads * 4;
-constexpr int kNumBars = 2 * kStages + 6;
+constexpr int kOffRing = kDB * kQBlockBytes;                   // 110,592
+constexpr int kOffInfo = kOffRing + kSlots * kBlkBytes;        // 225,280
+constexpr int kOffHead = kOffInfo + kInfos * kTok * 4;         // per head: scale of S, its LSE (log2)
+constexpr int kOffBars = kOffHead + kHeads * 8;
+constexpr int kNumBars = 2 * kSlots + 2 * kInfos + 7;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
-constexpr size_t kSmemBytes = 1024 + kOffMisc + 256;
-static_assert(kOffStage % 1024 == 0 && kOffBars % 8 == 0, "alignment");
+constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
+static_assert(kOffRing % 1024 == 0 && kOffBars % 8 == 0, "alignment");
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct MassParams {
@@ -86,19 +88,27 @@ __device__ __forceinline__ float ex2f(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool bar_or_epilogue(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
 
 struct Tiles {  // a run's tiles, one after another
   const MassParams& p;
   int row, limit;  // limit: tokens (or entries) of `row`
   int64_t start, pos, hi;
 
-  __device__ int items(int r) const {
-    if (p.idx) return p.k;
+  __device__ int visible(int r) const {
     int len = p.seq_lens[r / p.nq];
     len = len < 0 ? 0 : (len > p.cap ? p.cap : len);
     return visible_len(len, p.nq, r % p.nq);
   }
+  __device__ int items(int r) const { return p.idx ? p.k : visible(r); }
   // The next tile: its row and first token (or entry); false behind the run.
   __device__ bool next(int& r, int& first, int& count) {
     if (pos >= hi) return false;
@@ -115,36 +125,48 @@ struct Tiles {  // a run's tiles, one after another
   }
 };
 
+// What a lane without a token reads.
+__device__ const uint4 zero_record[kLatent / 16] = {};
+
 template <bool kNV>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ MassParams p) {
   constexpr int kRec = kNV ? kNvRec : kLatent;
-  constexpr uint32_t kIdesc = make_idesc(kFmtBF16, kFmtBF16, 0, 0, kTok, kHeads);
+  constexpr uint32_t kIdesc = make_idesc(kFmtF16, kFmtF16, 0, 0, kTok, kHeads);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + kOffBars;
-  auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
-  auto s_full = [&](int s) { return bars + 8u * (2 * kStages + s); };
-  auto s_empty = [&](int s) { return bars + 8u * (2 * kStages + 2 + s); };
-  const uint32_t q_full = bars + 8u * (2 * kStages + 4), drain = bars + 8u * (2 * kStages + 5);
+  auto full = [&](uint32_t s) { return bars + 8u * s; };
+  auto empty = [&](uint32_t s) { return bars + 8u * (kSlots + s); };
+  auto info_full = [&](uint32_t s) { return bars + 8u * (2 * kSlots + s); };
+  auto info_empty = [&](uint32_t s) { return bars + 8u * (2 * kSlots + kInfos + s); };
+  const uint32_t bars2 = bars + 8u * (2 * kSlots + 2 * kInfos);
+  auto s_full = [&](uint32_t s) { return bars2 + 8u * s; };
+  auto s_empty = [&](uint32_t s) { return bars2 + 16 + 8u * s; };
+  const uint32_t q_full = bars2 + 32, q_ready = bars2 + 40, drain = bars2 + 48;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
-  float* lse_s = reinterpret_cast<float*>(smem + kOffLse);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float2* head_s = reinterpret_cast<float2*>(smem + kOffHead);
+  int32_t* info = reinterpret_cast<int32_t*>(smem + kOffInfo);
+  const int warp = warp_number(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), kLoadWarps);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < kInfos; ++s) {
+      mbar_init(info_full(s), 1);
+      mbar_init(info_empty(s), kDB);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
       mbar_init(s_empty(s), 4);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_ready, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -169,204 +191,214 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  int row, first, count;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  int row = -1, first = 0, count = 0;
 
   if (warp == kMmaWarp) {
-    if (lane == 0) {
-      // ------------------------------------------------ MMA issuer
-      const uint64_t q_desc = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSw128);
-      const uint32_t q_lo = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
-      const uint32_t st_lo = (uint32_t)smem_desc(sbase + kOffStage, 16, 1024, kLayoutSw128);
-      uint32_t it = 0, stage = 0, segs = 0;
-      int cur = -1;
-      bool ok = true, q_pending = false;
-      while (ok && tiles.next(row, first, count)) {
-        const int b = it & 1;
-        if (row != cur) {
-          // Q may go once the previous row's last S tile is complete
-          if (it > 0) ok = mbar_wait(s_full(b ^ 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
-          if (!ok) break;
+    // ------------------------------------------------ MMA issuer (the whole warp runs, one lane issues)
+    const uint64_t q_desc = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSw128);
+    const uint32_t q_lo = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
+    const uint32_t r_lo = (uint32_t)smem_desc(sbase + kOffRing, 16, 1024, kLayoutSw128);
+    uint32_t it = 0, n = 0, segs = 0;
+    int cur = -1;
+    bool ok = true;
+    while (ok) {
+      if (!__all_sync(0xffffffffu, tiles.next(row, first, count))) break;
+      row = __shfl_sync(0xffffffffu, row, 0);
+      const uint32_t b = it & 1;
+      if (row != cur) {
+        // Q may go once the previous row's last S tile is complete
+        if (it > 0) ok = mbar_wait_warp(s_full(b ^ 1), ((it - 1) >> 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(q_full, kDB * kQBlockBytes);
           for (int kb = 0; kb < kDB; ++kb)
             tma_load_2d(sbase + kOffQ + kb * kQBlockBytes, &tmap_q, kb * 64, row * kHeads, q_full);
-          q_pending = true;
-          ok = mbar_wait(q_full, segs & 1, abort_flag, p.status);
-          if (!ok) break;
-          q_pending = false;
-          ++segs;
-          cur = row;
         }
-        ok = mbar_wait(s_empty(b), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
-        for (int g = 0; ok && g < kStagesPerTile; ++g, ++stage) {
-          const uint32_t slot = stage % kStages;
-          ok = mbar_wait(full(slot), (stage / kStages) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a_lo = st_lo + slot * (kStageBytes / 16);
-          const uint32_t b_lo = q_lo + g * (kStageBlocks * kQBlockBytes / 16);
-#pragma unroll
-          for (int j = 0; j < kStageBlocks; ++j)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(tmem + b * kSCols, desc64(a_lo + j * (kBlkBytes / 16) + 2 * kk, hi),
-                       desc64(b_lo + j * (kQBlockBytes / 16) + 2 * kk, hi), kIdesc, (g | j | kk) ? 1u : 0u);
-          mma_commit(empty(slot));
-        }
-        if (!ok) break;
-        mma_commit(s_full(b));
-        ++it;
+        __syncwarp();
+        // the epilogue warps wait for it, turn it into fp16 where it lies and say so
+        ok = mbar_wait_warp(q_ready, segs & 1, abort_flag, p.status);
+        ++segs;
+        cur = row;
       }
-      if (q_pending) mbar_wait_drain(q_full, segs & 1, 10000000ull);
-      // every MMA completes before TMEM is released
-      mma_commit(drain);
+      ok = ok && mbar_wait_warp(s_empty(b), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+#pragma unroll 1
+      for (int kb = 0; ok && kb < kDB; ++kb, ++n) {
+        const uint32_t slot = n % kSlots;
+        ok = mbar_wait_warp(full(slot), (n / kSlots) & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a_lo = r_lo + slot * (kBlkBytes / 16), b_lo = q_lo + kb * (kQBlockBytes / 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(tmem + b * kSCols, desc64(a_lo + 2 * kk, hi), desc64(b_lo + 2 * kk, hi), kIdesc, (kb | kk) ? 1u : 0u);
+          mma_commit(empty(slot));
+          if (kb == kDB - 1) mma_commit(s_full(b));
+        }
+        __syncwarp();
+      }
+      ++it;
+    }
+    if (elect_one()) {
+      if (segs > 0) mbar_wait_drain(q_full, (segs - 1) & 1, 10000000ull);  // no copy is in flight at the exit
+      mma_commit(drain);  // every MMA completes before TMEM is released
       mbar_wait_drain(drain, 0, 10000000ull);
     }
-  } else if (warp >= kLoadWarp0) {
-    // ------------------------------------------------ loaders: records -> bf16 stages
-    // Lane (token, half) of 16 tokens a warp: 32 dims of each block.
-    constexpr int kW = kNV ? 1 : 2;
-    const int tok = (warp - kLoadWarp0) * 16 + (lane >> 1), half = lane & 1;
-    uint4 buf[kDB - 1][kW], tail[2], sc[2];
-    const uint8_t* rec = nullptr;
-    // Three steps, each a tile ahead of the next: the token, its page, its record.
-    int tok_a = -1, row_b = 0, tok_b = -1, page_b = -1;
-    bool have_a = false, have_b = false, have = false;
+  } else if (warp == kLookupWarp) {
+    // ------------------------------------------------ lookup: block row * 64 + slot of each token, -1 for none
+    // The tokens of the next tile are fetched before this tile's pages are.
+    int tok[kTok / 32];
+    bool have;
     auto step_token = [&]() {
-      have_a = tiles.next(row, first, count);
-      tok_a = -1;
-      if (have_a && tok < count) tok_a = p.idx ? p.idx[(int64_t)row * p.k + first + tok] : first + tok;
-    };
-    auto step_page = [&]() {
-      have_b = have_a;
-      tok_b = tok_a;
-      page_b = -1;
-      if (!have_b) return;
-      row_b = row;
-      if (tok_b >= 0) {
-        if (tok_b >= p.cap || (p.idx && tok_b >= [&] {
-              int len = p.seq_lens[row_b / p.nq];
-              len = len < 0 ? 0 : (len > p.cap ? p.cap : len);
-              return visible_len(len, p.nq, row_b % p.nq);
-            }())) {
-          report(p.status, DSA_ERR_BOUNDS);
-          tok_b = -1;
-        } else {
-          page_b = p.block_table[(int64_t)(row_b / p.nq) * p.max_blocks + tok_b / kBlock];
-        }
-      }
-    };
-    auto step_record = [&]() {
-      have = have_b;
-      rec = nullptr;
-      if (have && tok_b >= 0) {
-        if (page_b >= 0 && page_b < p.num_blocks)
-          rec = p.latent_base + (int64_t)page_b * p.row_stride + (tok_b % kBlock) * kRec;
-        else
-          report(p.status, DSA_ERR_BOUNDS);
-      }
-    };
-    auto advance = [&]() {
-      step_record();
-      step_page();
-      step_token();
-    };
-    auto ld = [&](int off) {
-      return rec ? __ldg(reinterpret_cast<const uint4*>(rec + off)) : make_uint4(0, 0, 0, 0);
-    };
-    auto load_block = [&](int kb) {
-      if (kb == kDB - 1) {
-        constexpr int kTailOff = kNV ? kValue / 2 + kValue / 16 : kValue;
-        tail[0] = ld(kTailOff + 32 * half);
-        tail[1] = ld(kTailOff + 32 * half + 16);
-      } else if (kNV) {
-        buf[kb][0] = ld(32 * kb + 16 * half);
-      } else {
-        buf[kb][0] = ld(64 * kb + 32 * half);
-        buf[kb][kW - 1] = ld(64 * kb + 32 * half + 16);
-      }
-    };
-    auto load_scales = [&]() {
-      if (kNV) {
-        sc[0] = ld(kValue / 2);
-        sc[1] = ld(kValue / 2 + 16);
-      }
-    };
-    auto store_unit = [&](uint8_t* blk, int u, const uint32_t (&o)[8]) {
-      const uint32_t off = (uint32_t)(tok * 128 + half * 64 + u * 32);
-      *reinterpret_cast<uint4*>(blk + swz128(off)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(blk + swz128(off + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-    };
-    step_token();
-    step_page();
-    step_token();
-    advance();
-    if (have) {
-      load_scales();
+      have = tiles.next(row, first, count);
 #pragma unroll
-      for (int kb = 0; kb < kDB; ++kb) load_block(kb);
-    }
-    uint32_t stage = 0;
+      for (int i = 0; i < kTok / 32; ++i) {
+        const int e = lane + 32 * i;
+        tok[i] = -1;
+        if (have && e < count) tok[i] = p.idx ? p.idx[(int64_t)row * p.k + first + e] : first + e;
+      }
+    };
+    step_token();
+    uint32_t it = 0;
     while (have) {
-      const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
-      advance();
-      if (have) load_scales();
-      bool ok = true;
+      int t[kTok / 32], page[kTok / 32];
+      const int limit = p.idx ? tiles.visible(row) : p.cap;
+      const int32_t* table = p.block_table + (int64_t)(row / p.nq) * p.max_blocks;
 #pragma unroll
-      for (int g = 0; g < kStagesPerTile; ++g, ++stage) {
-        const uint32_t slot = stage % kStages;
-        ok = mbar_wait(empty(slot), ((stage / kStages) & 1) ^ 1, abort_flag, p.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+      for (int i = 0; i < kTok / 32; ++i) {
+        t[i] = tok[i];
+        if (t[i] >= limit) {
+          report(p.status, DSA_ERR_BOUNDS);
+          t[i] = -1;
         }
-#pragma unroll
-        for (int j = 0; j < kStageBlocks; ++j) {
-          const int kb = g * kStageBlocks + j;
-          uint8_t* blk = smem + kOffStage + slot * kStageBytes + j * kBlkBytes;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t o[8];
-            if (kNV && kb < kDB - 1) {
-              const uint32_t pair = half ? scw[kb & 7] >> 16 : scw[kb & 7];
-              const uint4 w = buf[kb < kDB - 1 ? kb : 0][0];
-              nvfp4x16_to_bf16x16(u ? w.z : w.x, u ? w.w : w.y, (pair >> (8 * u)) & 0xFFu, o);
-            } else {
-              const uint4 w = kb == kDB - 1 ? tail[u] : buf[kb < kDB - 1 ? kb : 0][u * (kW - 1)];
-              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) e4m3x4_to_bf16x4(ws[q], o[2 * q], o[2 * q + 1]);
-            }
-            store_unit(blk, u, o);
-          }
-          if (have) load_block(kb);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(slot));
+        page[i] = t[i] >= 0 ? table[t[i] / kBlock] : -1;
       }
+      step_token();
+      if (!mbar_wait_warp(info_empty(it % kInfos), ((it / kInfos) & 1) ^ 1, abort_flag, p.status)) break;
+#pragma unroll
+      for (int i = 0; i < kTok / 32; ++i) {
+        const bool good = (uint32_t)page[i] < (uint32_t)p.num_blocks;
+        if (t[i] >= 0 && !good) report(p.status, DSA_ERR_BOUNDS);
+        info[(it % kInfos) * kTok + lane + 32 * i] = t[i] >= 0 && good ? page[i] * kBlock + t[i] % kBlock : -1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(info_full(it % kInfos));
+      ++it;
+    }
+  } else if (warp >= kLoadWarp0) {
+    // ------------------------------------------------ loaders: records -> fp16 blocks
+    // Warp w takes the blocks n = w, w + 7, ... of the run's stream (block n % 9 of
+    // tile n / 9), always into slot w: a slot's waits then belong to one warp and
+    // cannot run a phase ahead.  Lane: 32 dims of 8 tokens.
+    constexpr int kTt = kTok / 16;
+    const int w = warp - kLoadWarp0;
+    const int sub = lane & 1, tok0 = lane >> 1;
+    const uint32_t off = (uint32_t)(tok0 * 128 + sub * 64);
+    uint8_t* blk = smem + kOffRing + w * kBlkBytes;
+    uint8_t *p0 = blk + swz128(off), *p1 = blk + swz128(off + 16), *p2 = blk + swz128(off + 32), *p3 = blk + swz128(off + 48);
+    uint4 buf[kTt][2];
+    uint32_t sc[kTt];
+    const int64_t mine = max(tiles.hi - tiles.pos, (int64_t)0) * kDB;  // this run's blocks
+    bool four = false;  // the loaded block: E2M1 codes with block scales; else E4M3 codes
+    // block n's records into registers
+    auto load = [&](uint32_t n) -> bool {
+      const uint32_t tile = n / kDB, kb = n % kDB;
+      if (!mbar_wait_warp(info_full(tile % kInfos), (tile / kInfos) & 1, abort_flag, p.status)) return false;
+      four = kNV && kb < kDB - 1;
+      const int c0 = four ? 32 * kb + 16 * sub : (kNV ? kValue / 2 + kValue / 16 : 64 * kb) + 32 * sub;
+      const int s0 = kValue / 2 + 4 * kb + 2 * sub;
+      const int32_t* list = info + (tile % kInfos) * kTok + tok0;
+#pragma unroll
+      for (int i = 0; i < kTt; ++i) {
+        const int32_t ph = list[16 * i];
+        const uint8_t* rec = ph < 0 ? reinterpret_cast<const uint8_t*>(zero_record)
+                                    : p.latent_base + (int64_t)(ph / kBlock) * p.row_stride + ph % kBlock * kRec;
+        buf[i][0] = __ldg(reinterpret_cast<const uint4*>(rec + c0));
+        if (four)
+          sc[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + s0));
+        else
+          buf[i][1] = __ldg(reinterpret_cast<const uint4*>(rec + c0 + 16));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(info_empty(tile % kInfos));
+      return true;
+    };
+    bool ok = w < mine && load(w);
+    uint32_t use = 0;  // of the slot
+    for (uint32_t n = w; ok && n < mine; n += kSlots, ++use) {
+      ok = mbar_wait_warp(empty(w), (use & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < kTt; ++i) {
+        uint32_t u0[8], u1[8];
+        if (four) {
+          nvfp4x16_to_f16x16(buf[i][0].x, buf[i][0].y, sc[i] & 0xFFu, u0);
+          nvfp4x16_to_f16x16(buf[i][0].z, buf[i][0].w, sc[i] >> 8, u1);
+        } else {
+          e4m3x16_to_f16x16(buf[i][0], u0);
+          e4m3x16_to_f16x16(buf[i][1], u1);
+        }
+        const int at = 2048 * i;  // 16 tokens on: two swizzle atoms
+        *reinterpret_cast<uint4*>(p0 + at) = make_uint4(u0[0], u0[1], u0[2], u0[3]);
+        *reinterpret_cast<uint4*>(p1 + at) = make_uint4(u0[4], u0[5], u0[6], u0[7]);
+        *reinterpret_cast<uint4*>(p2 + at) = make_uint4(u1[0], u1[1], u1[2], u1[3]);
+        *reinterpret_cast<uint4*>(p3 + at) = make_uint4(u1[4], u1[5], u1[6], u1[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(w));
+      if (n + kSlots < mine) ok = load(n + kSlots);
     }
   } else {
-    // ------------------------------------------------ weights (thread = token)
+    // ------------------------------------------------ weights (thread = token; thread h turns head h's query into fp16)
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const int tid = threadIdx.x;
-    uint32_t it = 0;
+    uint32_t it = 0, segs = 0;
     int cur = -1;
     bool ok = true;
     while (tiles.next(row, first, count)) {
-      const int b = it & 1;
+      const uint32_t b = it & 1;
       if (row != cur) {
-        bar_epilogue();  // the previous row's values have been read
-        if (tid < kHeads) {
+        // Every warp meets these barriers at the same rows, also after a wait that ran out.
+        ok = ok && mbar_wait_warp(q_full, segs & 1, abort_flag, p.status);
+        ok = !bar_or_epilogue(!ok);  // and the previous row's values have been read
+        uint8_t* q = smem + kOffQ;
+        uint32_t am = 0;
+        if (ok && tid < kHeads) {
+#pragma unroll 1
+          for (int kb = 0; kb < kDB; ++kb)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(q + kb * kQBlockBytes + swz128(tid * 128 + c * 16));
+              am = bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(am, w.x), w.y), w.z), w.w);
+            }
+          const int e = f16_shift_of(am);
+          const float scale = __int_as_float((127 + e) << 23);
+#pragma unroll 1
+          for (int kb = 0; kb < kDB; ++kb)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(q + kb * kQBlockBytes + swz128(tid * 128 + c * 16));
+              const uint4 w = *at;
+              *at = make_uint4(bf16x2_to_f16x2(w.x, scale), bf16x2_to_f16x2(w.y, scale), bf16x2_to_f16x2(w.z, scale),
+                               bf16x2_to_f16x2(w.w, scale));
+            }
           const float l = p.lse[(int64_t)row * kHeads + tid];
-          lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no token attended: no weight
+          // an LSE of -inf (no token attended) gives no weight
+          head_s[tid] = make_float2(p.scale_log2 * __int_as_float((127 - e) << 23),
+                                    l == -INFINITY ? INFINITY : l * 1.4426950408889634f);
         }
-        bar_epilogue();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+        bar_or_epilogue(false);  // head_s is written
+        ++segs;
         cur = row;
       }
-      ok = mbar_wait(s_full(b), (it >> 1) & 1, abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = ok && mbar_wait_warp(s_full(b), (it >> 1) & 1, abort_flag, p.status);
+      ++it;
+      if (!ok) continue;
       tc_fence_after();
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -380,12 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(s_empty(b));
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(lse_s + 32 * c + j);
-          sum[0] += ex2f(fmaf(__uint_as_float(r[j]), p.scale_log2, -l.x));
-          sum[1] += ex2f(fmaf(__uint_as_float(r[j + 1]), p.scale_log2, -l.y));
-          sum[2] += ex2f(fmaf(__uint_as_float(r[j + 2]), p.scale_log2, -l.z));
-          sum[3] += ex2f(fmaf(__uint_as_float(r[j + 3]), p.scale_log2, -l.w));
+        for (int j = 0; j < 32; j += 2) {
+          const float4 v = *reinterpret_cast<const float4*>(head_s + 32 * c + j);
+          sum[j & 2] += ex2f(fmaf(__uint_as_float(r[j]), v.x, -v.y));
+          sum[(j & 2) + 1] += ex2f(fmaf(__uint_as_float(r[j + 1]), v.z, -v.w));
         }
       }
       float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -397,7 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           w = 0.f;
         p.out[at] = w;
       }
-      ++it;
     }
   }
   __syncwarp();

@@ -16,12 +16,12 @@ struct Run {
 
 // By all kThreads threads of the CTA: count(r) items of row r; at least
 // min_items a CTA (fixed_per > 0: exactly that many, and hi is the line's end).
-// each(r, first, n, per) is called once for every row by CTA 0.  `scratch`: 16
+// each(r, first, n, per) is called once for every row by CTA 0.  `scratch`: 32
 // int64 of shared memory.
 template <int kThreads, class Count, class Each>
 __device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, int64_t* scratch, Count count, Each each) {
   constexpr int kWarps = kThreads / 32;
-  static_assert(kWarps <= 14, "scratch");
+  static_assert(kWarps <= 30, "scratch");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
   for (int r = threadIdx.x; r < rows; r += kThreads) sum += count(r);
@@ -37,7 +37,7 @@ __device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, 
   w.pos = (int64_t)blockIdx.x * per;
   w.hi = fixed_per ? total : (w.pos + per < total ? w.pos + per : total);
   // the row that holds w.pos: a block scan over the rows, kThreads at a time
-  if (threadIdx.x == 0) scratch[14] = rows;
+  if (threadIdx.x == 0) scratch[30] = rows;
   int64_t base = 0;
   for (int r0 = 0; r0 < rows; r0 += kThreads) {
     const int r = r0 + threadIdx.x;
@@ -54,16 +54,16 @@ __device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, 
     for (int i = 0; i < warp; ++i) before += scratch[i];
     const int64_t first = before + inc - n;
     if (n > 0 && w.pos >= first && w.pos < first + n) {
-      scratch[14] = r;
-      scratch[15] = first;
+      scratch[30] = r;
+      scratch[31] = first;
     }
     if (blockIdx.x == 0 && r < rows) each(r, first, n, per);
     for (int i = 0; i < kWarps; ++i) base += scratch[i];
     if (blockIdx.x != 0 && base > w.pos) break;  // the same in every thread
   }
   __syncthreads();
-  w.row = (int)scratch[14];
-  w.start = scratch[15];
+  w.row = (int)scratch[30];
+  w.start = scratch[31];
   return w;
 }
 
