@@ -6,16 +6,18 @@
 // LSE), or those its top-k selected (the sparse attention's).  The running total
 // is what cache eviction ranks tokens by.
 //
-// attention_weights_kernel (persistent, one CTA per SM, 13 warps): the rows'
+// attention_weights_kernel (persistent, one CTA per SM, 14 warps): the rows'
 // tiles of 128 tokens lie on one line, equal runs of it to every CTA.
 //   * S^T = K Q^T with the tokens on M = 128 rows and the heads on N = 96: the
 //     sum over heads then stays inside a thread, and no MMA row is wasted.  Q
 //     (110 KB, turned into fp16 in place) stays in shared memory while a CTA
-//     works on a row; 64-dim blocks of keys pass through a ring of 7.
-//   * warp 12 resolves tokens to records (index, page, slot) three tiles ahead.
-//   * warps 4..10 each fill one slot of the ring, so a warp takes every seventh
-//     block of the stream: the records' 64 dims, two lanes a token, loaded seven
-//     blocks ahead in registers, widened exactly to fp16 and stored 128-byte
+//     works on a row; the keys pass through a ring of three 128-dim pairs of
+//     blocks and one slot for the last 64 dims.
+//   * warp 13 resolves tokens to records (index, page, slot) three tiles ahead.
+//   * warps 4..11 load 16 tokens' records each, a whole tile ahead in registers
+//     (four lanes a token and 16 bytes a lane: a load touches 8 lines; with two
+//     lanes a token it touched 16, and the load pipe, not the tensor cores,
+//     paced the kernel), widen them exactly to fp16 and store them 128-byte
 //     swizzled.
 //   * warps 0..3, one thread a token: sum over heads of 2^(s c - lse c'), from
 //     one of two S tiles in TMEM while the next is computed.
@@ -42,23 +44,27 @@ constexpr int kTok = 128;                        // tokens per tile
 constexpr int kDB = kLatent / 64;                // 9 blocks of 64 dims
 constexpr int kQBlockBytes = kHeads * 128;       // 12,288
 constexpr int kBlkBytes = kTok * 128;            // 16,384
-constexpr int kSlots = 7;                        // ring of blocks
+constexpr int kPairs = 4;                        // pairs of blocks a tile (dims 0..511), then the last block
+constexpr int kPairBytes = 2 * kBlkBytes;
+constexpr int kSlots = 3;                        // ring of pairs
 constexpr int kInfos = 4;                        // tiles whose records are resolved
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);
-constexpr int kThreads = 13 * 32;                // epilogue 0-3, loaders 4-10 (a ring slot each), MMA issuer 11, lookup 12
+constexpr int kThreads = 14 * 32;                // epilogue 0-3, loaders 4-11, MMA issuer 12, lookup 13
 constexpr int kLoadWarp0 = 4;
-constexpr int kMmaWarp = 11;
-constexpr int kLookupWarp = 12;
-static_assert(kLoadWarp0 + kSlots == kMmaWarp, "a loader warp a slot");
+constexpr int kLoadWarps = 8;                    // 16 tokens each
+constexpr int kMmaWarp = 12;
+constexpr int kLookupWarp = 13;
+static_assert(kLoadWarps * 16 == kTok, "loader split");
 constexpr int kSCols = 128;                      // columns between the two S tiles
 constexpr int kTmemCols = 256;
 
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kDB * kQBlockBytes;                   // 110,592
-constexpr int kOffInfo = kOffRing + kSlots * kBlkBytes;        // 225,280
+constexpr int kOffLast = kOffRing + kSlots * kPairBytes;       // dims 512..575
+constexpr int kOffInfo = kOffLast + kBlkBytes;                 // 225,280
 constexpr int kOffHead = kOffInfo + kInfos * kTok * 4;         // per head: scale of S, its LSE (log2)
 constexpr int kOffBars = kOffHead + kHeads * 8;
-constexpr int kNumBars = 2 * kSlots + 2 * kInfos + 7;
+constexpr int kNumBars = 2 * (kSlots + 1) + 2 * kInfos + 7;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
 static_assert(kOffRing % 1024 == 0 && kOffBars % 8 == 0, "alignment");
@@ -137,11 +143,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + kOffBars;
+  // ring slots 0 .. kSlots - 1, and the last block's slot kSlots
   auto full = [&](uint32_t s) { return bars + 8u * s; };
-  auto empty = [&](uint32_t s) { return bars + 8u * (kSlots + s); };
-  auto info_full = [&](uint32_t s) { return bars + 8u * (2 * kSlots + s); };
-  auto info_empty = [&](uint32_t s) { return bars + 8u * (2 * kSlots + kInfos + s); };
-  const uint32_t bars2 = bars + 8u * (2 * kSlots + 2 * kInfos);
+  auto empty = [&](uint32_t s) { return bars + 8u * (kSlots + 1 + s); };
+  auto info_full = [&](uint32_t s) { return bars + 8u * (2 * (kSlots + 1) + s); };
+  auto info_empty = [&](uint32_t s) { return bars + 8u * (2 * (kSlots + 1) + kInfos + s); };
+  const uint32_t bars2 = bars + 8u * (2 * (kSlots + 1) + 2 * kInfos);
   auto s_full = [&](uint32_t s) { return bars2 + 8u * s; };
   auto s_empty = [&](uint32_t s) { return bars2 + 16 + 8u * s; };
   const uint32_t q_full = bars2 + 32, q_ready = bars2 + 40, drain = bars2 + 48;
@@ -153,13 +160,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(full(s), 1);
+    for (int s = 0; s <= kSlots; ++s) {
+      mbar_init(full(s), kLoadWarps);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kInfos; ++s) {
       mbar_init(info_full(s), 1);
-      mbar_init(info_empty(s), kDB);
+      mbar_init(info_empty(s), kLoadWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
@@ -223,20 +230,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = ok && mbar_wait_warp(s_empty(b), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
 #pragma unroll 1
-      for (int kb = 0; ok && kb < kDB; ++kb, ++n) {
-        const uint32_t slot = n % kSlots;
-        ok = mbar_wait_warp(full(slot), (n / kSlots) & 1, abort_flag, p.status);
+      for (int mb = 0; ok && mb <= kPairs; ++mb) {
+        const bool last = mb == kPairs;
+        const uint32_t slot = last ? kSlots : n % kSlots;
+        ok = mbar_wait_warp(full(slot), last ? it & 1 : (n / kSlots) & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a_lo = r_lo + slot * (kBlkBytes / 16), b_lo = q_lo + kb * (kQBlockBytes / 16);
+        const uint32_t a_lo = r_lo + slot * (kPairBytes / 16), b_lo = q_lo + mb * (2 * kQBlockBytes / 16);
         if (elect_one()) {
+#pragma unroll 1
+          for (int j = 0; j < (last ? 1 : 2); ++j)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(tmem + b * kSCols, desc64(a_lo + 2 * kk, hi), desc64(b_lo + 2 * kk, hi), kIdesc, (kb | kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(tmem + b * kSCols, desc64(a_lo + j * (kBlkBytes / 16) + 2 * kk, hi),
+                       desc64(b_lo + j * (kQBlockBytes / 16) + 2 * kk, hi), kIdesc, (mb | j | kk) ? 1u : 0u);
           mma_commit(empty(slot));
-          if (kb == kDB - 1) mma_commit(s_full(b));
+          if (last) mma_commit(s_full(b));
         }
         __syncwarp();
+        if (!last) ++n;
       }
       ++it;
     }
@@ -288,67 +300,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------ loaders: records -> fp16 blocks
-    // Warp w takes the blocks n = w, w + 7, ... of the run's stream (block n % 9 of
-    // tile n / 9), always into slot w: a slot's waits then belong to one warp and
-    // cannot run a phase ahead.  Lane: 32 dims of 8 tokens.
-    constexpr int kTt = kTok / 16;
+    // Warp w: tokens 16 w .. 16 w + 15, eight at a time, four lanes a token: lane
+    // (token, block `blk` of the pair, its half `half`), numbered so that eight
+    // neighbours store 16 bytes each to all 32 banks.  A pair's records of the next
+    // tile go into registers as this tile's are widened out of them.
     const int w = warp - kLoadWarp0;
-    const int sub = lane & 1, tok0 = lane >> 1;
-    const uint32_t off = (uint32_t)(tok0 * 128 + sub * 64);
-    uint8_t* blk = smem + kOffRing + w * kBlkBytes;
-    uint8_t *p0 = blk + swz128(off), *p1 = blk + swz128(off + 16), *p2 = blk + swz128(off + 32), *p3 = blk + swz128(off + 48);
-    uint4 buf[kTt][2];
-    uint32_t sc[kTt];
-    const int64_t mine = max(tiles.hi - tiles.pos, (int64_t)0) * kDB;  // this run's blocks
-    bool four = false;  // the loaded block: E2M1 codes with block scales; else E4M3 codes
-    // block n's records into registers
-    auto load = [&](uint32_t n) -> bool {
-      const uint32_t tile = n / kDB, kb = n % kDB;
+    const int half = lane & 1, blk = (lane >> 3) & 1, quarter = 2 * blk + half;
+    const int tok0 = w * 16 + ((lane >> 1) & 3) + ((lane >> 4) & 1) * 4;
+    const uint32_t off = (uint32_t)(tok0 * 128 + half * 64);
+    const uint32_t o0 = swz128(off), o1 = swz128(off + 16), o2 = swz128(off + 32), o3 = swz128(off + 48);
+    const uint32_t ot = (uint32_t)(tok0 * 128 + quarter * 32), ot0 = swz128(ot), ot1 = swz128(ot + 16);
+    uint4 buf[kPairs][2][kNV ? 1 : 2], last[2];
+    uint2 sc[2];  // the block scales of pair `quarter` of the lane's two tokens
+    const uint8_t* rec[2];
+    const int64_t mine = tiles.hi - tiles.pos;  // this run's tiles, as the lookup warp resolves them
+    auto resolve = [&](uint32_t tile) -> bool {
       if (!mbar_wait_warp(info_full(tile % kInfos), (tile / kInfos) & 1, abort_flag, p.status)) return false;
-      four = kNV && kb < kDB - 1;
-      const int c0 = four ? 32 * kb + 16 * sub : (kNV ? kValue / 2 + kValue / 16 : 64 * kb) + 32 * sub;
-      const int s0 = kValue / 2 + 4 * kb + 2 * sub;
-      const int32_t* list = info + (tile % kInfos) * kTok + tok0;
 #pragma unroll
-      for (int i = 0; i < kTt; ++i) {
-        const int32_t ph = list[16 * i];
-        const uint8_t* rec = ph < 0 ? reinterpret_cast<const uint8_t*>(zero_record)
-                                    : p.latent_base + (int64_t)(ph / kBlock) * p.row_stride + ph % kBlock * kRec;
-        buf[i][0] = __ldg(reinterpret_cast<const uint4*>(rec + c0));
-        if (four)
-          sc[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + s0));
-        else
-          buf[i][1] = __ldg(reinterpret_cast<const uint4*>(rec + c0 + 16));
+      for (int e = 0; e < 2; ++e) {
+        const int32_t ph = info[(tile % kInfos) * kTok + tok0 + 8 * e];
+        rec[e] = ph < 0 ? reinterpret_cast<const uint8_t*>(zero_record)
+                        : p.latent_base + (int64_t)(ph / kBlock) * p.row_stride + ph % kBlock * kRec;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(info_empty(tile % kInfos));
       return true;
     };
-    bool ok = w < mine && load(w);
-    uint32_t use = 0;  // of the slot
-    for (uint32_t n = w; ok && n < mine; n += kSlots, ++use) {
-      ok = mbar_wait_warp(empty(w), (use & 1) ^ 1, abort_flag, p.status);
-      if (!ok) break;
+    auto load_pair = [&](int mb) {
 #pragma unroll
-      for (int i = 0; i < kTt; ++i) {
-        uint32_t u0[8], u1[8];
-        if (four) {
-          nvfp4x16_to_f16x16(buf[i][0].x, buf[i][0].y, sc[i] & 0xFFu, u0);
-          nvfp4x16_to_f16x16(buf[i][0].z, buf[i][0].w, sc[i] >> 8, u1);
+      for (int e = 0; e < 2; ++e) {
+        if (kNV) {
+          buf[mb][e][0] = __ldg(reinterpret_cast<const uint4*>(rec[e] + 64 * mb + 16 * quarter));
         } else {
-          e4m3x16_to_f16x16(buf[i][0], u0);
-          e4m3x16_to_f16x16(buf[i][1], u1);
+#pragma unroll
+          for (int x = 0; x < (kNV ? 1 : 2); ++x)
+            buf[mb][e][x] = __ldg(reinterpret_cast<const uint4*>(rec[e] + 128 * mb + 32 * quarter + 16 * x));
         }
-        const int at = 2048 * i;  // 16 tokens on: two swizzle atoms
-        *reinterpret_cast<uint4*>(p0 + at) = make_uint4(u0[0], u0[1], u0[2], u0[3]);
-        *reinterpret_cast<uint4*>(p1 + at) = make_uint4(u0[4], u0[5], u0[6], u0[7]);
-        *reinterpret_cast<uint4*>(p2 + at) = make_uint4(u1[0], u1[1], u1[2], u1[3]);
-        *reinterpret_cast<uint4*>(p3 + at) = make_uint4(u1[4], u1[5], u1[6], u1[7]);
       }
+    };
+    auto load_last = [&]() {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        last[e] = __ldg(reinterpret_cast<const uint4*>(rec[e] + (kNV ? kValue / 2 + kValue / 16 : kValue) + 16 * quarter));
+    };
+    auto load_scales = [&]() {
+      if (kNV) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sc[e] = __ldg(reinterpret_cast<const uint2*>(rec[e] + kValue / 2 + 8 * quarter));
+      }
+    };
+    auto store = [&](uint8_t* a0, uint8_t* a1, const uint32_t (&u)[8]) {
+      *reinterpret_cast<uint4*>(a0) = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(a1) = make_uint4(u[4], u[5], u[6], u[7]);
+    };
+    bool ok = mine > 0 && resolve(0);
+    if (ok) {
+      load_scales();
+#pragma unroll
+      for (int mb = 0; mb < kPairs; ++mb) load_pair(mb);
+      load_last();
+    }
+    uint32_t n = 0;
+    for (uint32_t it = 0; ok && it < mine; ++it) {
+      const bool next = it + 1 < mine;
+      const uint2 sn[2] = {sc[0], sc[1]};
+      ok = !next || resolve(it + 1);
+      if (!ok) break;
+      if (next) load_scales();
+#pragma unroll
+      for (int mb = 0; mb < kPairs; ++mb, ++n) {
+        const uint32_t slot = n % kSlots;
+        ok = mbar_wait_warp(empty(slot), ((n / kSlots) & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        uint8_t* at = smem + kOffRing + slot * kPairBytes + blk * kBlkBytes;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t u[8];
+          if (kNV) {
+            // pair mb's scales lie with the lane of quarter mb: its word `blk`, the half's two bytes
+            const int src = (lane & ~9) | (mb & 1) | ((mb >> 1) << 3);
+            const uint32_t x = __shfl_sync(0xffffffffu, sn[e].x, src), y = __shfl_sync(0xffffffffu, sn[e].y, src);
+            const uint32_t two = (blk ? y : x) >> (16 * half);
+            nvfp4x16_to_f16x16(buf[mb][e][0].x, buf[mb][e][0].y, two & 0xFFu, u);
+            store(at + o0 + 1024 * e, at + o1 + 1024 * e, u);
+            nvfp4x16_to_f16x16(buf[mb][e][0].z, buf[mb][e][0].w, (two >> 8) & 0xFFu, u);
+            store(at + o2 + 1024 * e, at + o3 + 1024 * e, u);
+          } else {
+            e4m3x16_to_f16x16(buf[mb][e][0], u);
+            store(at + o0 + 1024 * e, at + o1 + 1024 * e, u);
+            e4m3x16_to_f16x16(buf[mb][e][kNV ? 0 : 1], u);
+            store(at + o2 + 1024 * e, at + o3 + 1024 * e, u);
+          }
+        }
+        if (next) load_pair(mb);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(slot));
+      }
+      if (!ok) break;
+      ok = mbar_wait_warp(empty(kSlots), (it & 1) ^ 1, abort_flag, p.status);
+      if (!ok) break;
+      uint8_t* at = smem + kOffLast;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t u[8];
+        e4m3x16_to_f16x16(last[e], u);
+        store(at + ot0 + 1024 * e, at + ot1 + 1024 * e, u);
+      }
+      if (next) load_last();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(w));
-      if (n + kSlots < mine) ok = load(n + kSlots);
+      if (lane == 0) mbar_arrive(full(kSlots));
     }
   } else {
     // ------------------------------------------------ weights (thread = token; thread h turns head h's query into fp16)
