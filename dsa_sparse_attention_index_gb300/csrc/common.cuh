@@ -159,6 +159,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
+// Asks L2 for the line of one address.
+__device__ __forceinline__ void prefetch_l2_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Make this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tensor core / TMA) before signalling the consumer.
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -62,8 +62,8 @@ constexpr int kOffQ = 0;
 constexpr int kOffRing = kDB * kQBlockBytes;                   // 110,592
 constexpr int kOffLast = kOffRing + kSlots * kPairBytes;       // dims 512..575
 constexpr int kOffInfo = kOffLast + kBlkBytes;                 // 225,280
-constexpr int kOffHead = kOffInfo + kInfos * kTok * 4;         // per head: scale of S, its LSE (log2)
-constexpr int kOffBars = kOffHead + kHeads * 8;
+constexpr int kOffHead = kOffInfo + kInfos * kTok * 4;         // per head: its LSE (log2); per warp: a maximum
+constexpr int kOffBars = kOffHead + kHeads * 4 + 16;
 constexpr int kNumBars = 2 * (kSlots + 1) + 2 * kInfos + 7;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
-  float2* head_s = reinterpret_cast<float2*>(smem + kOffHead);
+  float* lse_s = reinterpret_cast<float*>(smem + kOffHead);
+  uint32_t* max_s = reinterpret_cast<uint32_t*>(smem + kOffHead + kHeads * 4);
   int32_t* info = reinterpret_cast<int32_t*>(smem + kOffInfo);
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
@@ -293,6 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool good = (uint32_t)page[i] < (uint32_t)p.num_blocks;
         if (t[i] >= 0 && !good) report(p.status, DSA_ERR_BOUNDS);
         info[(it % kInfos) * kTok + lane + 32 * i] = t[i] >= 0 && good ? page[i] * kBlock + t[i] % kBlock : -1;
+        if (t[i] >= 0 && good) {
+          const uint8_t* rec = p.latent_base + (int64_t)page[i] * p.row_stride + t[i] % kBlock * kRec;
+#pragma unroll
+          for (int o = 0; o < kRec; o += 128) prefetch_l2_line(rec + o);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(info_full(it % kInfos));
@@ -360,6 +366,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int mb = 0; mb < kPairs; ++mb) load_pair(mb);
       load_last();
     }
+    // A step widens its data, then publishes the step before (whose stores have
+    // landed by then, so the fence is short), then waits for its slot and stores.
+    uint32_t pending = 0;  // the barrier of the step before
+    auto publish = [&]() {
+      if (pending) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pending);
+      }
+    };
     uint32_t n = 0;
     for (uint32_t it = 0; ok && it < mine; ++it) {
       const bool next = it + 1 < mine;
@@ -369,55 +385,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (next) load_scales();
 #pragma unroll
       for (int mb = 0; mb < kPairs; ++mb, ++n) {
+        uint32_t u[2][2][8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (kNV) {
+            // pair mb's scales lie with the lane of quarter mb: its word `blk`, the half's two bytes
+            const int src = (lane & ~9) | (mb & 1) | ((mb >> 1) << 3);
+            const uint32_t x = __shfl_sync(0xffffffffu, sn[e].x, src), y = __shfl_sync(0xffffffffu, sn[e].y, src);
+            const uint32_t two = (blk ? y : x) >> (16 * half);
+            nvfp4x16_to_f16x16(buf[mb][e][0].x, buf[mb][e][0].y, two & 0xFFu, u[e][0]);
+            nvfp4x16_to_f16x16(buf[mb][e][0].z, buf[mb][e][0].w, (two >> 8) & 0xFFu, u[e][1]);
+          } else {
+            e4m3x16_to_f16x16(buf[mb][e][0], u[e][0]);
+            e4m3x16_to_f16x16(buf[mb][e][kNV ? 0 : 1], u[e][1]);
+          }
+        }
+        if (next) load_pair(mb);
+        publish();
         const uint32_t slot = n % kSlots;
         ok = mbar_wait_warp(empty(slot), ((n / kSlots) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         uint8_t* at = smem + kOffRing + slot * kPairBytes + blk * kBlkBytes;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          uint32_t u[8];
-          if (kNV) {
-            // pair mb's scales lie with the lane of quarter mb: its word `blk`, the half's two bytes
-            const int src = (lane & ~9) | (mb & 1) | ((mb >> 1) << 3);
-            const uint32_t x = __shfl_sync(0xffffffffu, sn[e].x, src), y = __shfl_sync(0xffffffffu, sn[e].y, src);
-            const uint32_t two = (blk ? y : x) >> (16 * half);
-            nvfp4x16_to_f16x16(buf[mb][e][0].x, buf[mb][e][0].y, two & 0xFFu, u);
-            store(at + o0 + 1024 * e, at + o1 + 1024 * e, u);
-            nvfp4x16_to_f16x16(buf[mb][e][0].z, buf[mb][e][0].w, (two >> 8) & 0xFFu, u);
-            store(at + o2 + 1024 * e, at + o3 + 1024 * e, u);
-          } else {
-            e4m3x16_to_f16x16(buf[mb][e][0], u);
-            store(at + o0 + 1024 * e, at + o1 + 1024 * e, u);
-            e4m3x16_to_f16x16(buf[mb][e][kNV ? 0 : 1], u);
-            store(at + o2 + 1024 * e, at + o3 + 1024 * e, u);
-          }
+          store(at + o0 + 1024 * e, at + o1 + 1024 * e, u[e][0]);
+          store(at + o2 + 1024 * e, at + o3 + 1024 * e, u[e][1]);
         }
-        if (next) load_pair(mb);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(slot));
+        pending = full(slot);
       }
       if (!ok) break;
+      uint32_t u[2][8];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) e4m3x16_to_f16x16(last[e], u[e]);
+      if (next) load_last();
+      publish();
       ok = mbar_wait_warp(empty(kSlots), (it & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
       uint8_t* at = smem + kOffLast;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t u[8];
-        e4m3x16_to_f16x16(last[e], u);
-        store(at + ot0 + 1024 * e, at + ot1 + 1024 * e, u);
-      }
-      if (next) load_last();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(kSlots));
+      for (int e = 0; e < 2; ++e) store(at + ot0 + 1024 * e, at + ot1 + 1024 * e, u[e]);
+      pending = full(kSlots);
     }
+    publish();
   } else {
     // ------------------------------------------------ weights (thread = token; thread h turns head h's query into fp16)
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const int tid = threadIdx.x;
     uint32_t it = 0, segs = 0;
     int cur = -1;
+    float c_log2 = 0.f;  // logits in log2 units per unit of S
     bool ok = true;
     while (tiles.next(row, first, count)) {
       const uint32_t b = it & 1;
@@ -427,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = !bar_or_epilogue(!ok);  // and the previous row's values have been read
         uint8_t* q = smem + kOffQ;
         uint32_t am = 0;
+        // one power of two for the whole row: a logit's error is then at most 2^-39 of the row's largest products
         if (ok && tid < kHeads) {
 #pragma unroll 1
           for (int kb = 0; kb < kDB; ++kb)
@@ -435,7 +452,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint4 w = *reinterpret_cast<const uint4*>(q + kb * kQBlockBytes + swz128(tid * 128 + c * 16));
               am = bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(am, w.x), w.y), w.z), w.w);
             }
-          const int e = f16_shift_of(am);
+          const float l = p.lse[(int64_t)row * kHeads + tid];
+          lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no token attended: no weight
+        }
+        am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+        if (lane == 0) max_s[warp] = am;
+        bar_or_epilogue(false);  // lse_s and max_s are written
+        const int e = f16_shift_of(max(max(max_s[0], max_s[1]), max(max_s[2], max_s[3])));
+        c_log2 = p.scale_log2 * __int_as_float((127 - e) << 23);
+        if (ok && tid < kHeads) {
           const float scale = __int_as_float((127 + e) << 23);
 #pragma unroll 1
           for (int kb = 0; kb < kDB; ++kb)
@@ -446,15 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               *at = make_uint4(bf16x2_to_f16x2(w.x, scale), bf16x2_to_f16x2(w.y, scale), bf16x2_to_f16x2(w.z, scale),
                                bf16x2_to_f16x2(w.w, scale));
             }
-          const float l = p.lse[(int64_t)row * kHeads + tid];
-          // an LSE of -inf (no token attended) gives no weight
-          head_s[tid] = make_float2(p.scale_log2 * __int_as_float((127 - e) << 23),
-                                    l == -INFINITY ? INFINITY : l * 1.4426950408889634f);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        bar_or_epilogue(false);  // head_s is written
         ++segs;
         cur = row;
       }
@@ -474,10 +494,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(s_empty(b));
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float4 v = *reinterpret_cast<const float4*>(head_s + 32 * c + j);
-          sum[j & 2] += ex2f(fmaf(__uint_as_float(r[j]), v.x, -v.y));
-          sum[(j & 2) + 1] += ex2f(fmaf(__uint_as_float(r[j + 1]), v.z, -v.w));
+        for (int j = 0; j < 32; j += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(lse_s + 32 * c + j);
+          sum[0] += ex2f(fmaf(__uint_as_float(r[j]), c_log2, -l.x));
+          sum[1] += ex2f(fmaf(__uint_as_float(r[j + 1]), c_log2, -l.y));
+          sum[2] += ex2f(fmaf(__uint_as_float(r[j + 2]), c_log2, -l.z));
+          sum[3] += ex2f(fmaf(__uint_as_float(r[j + 3]), c_log2, -l.w));
         }
       }
       float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
