@@ -6,19 +6,21 @@
 // LSE), or those its top-k selected (the sparse attention's).  The running total
 // is what cache eviction ranks tokens by.
 //
-// attention_weights_kernel (persistent, one CTA per SM, 14 warps): the rows'
+// attention_weights_kernel (persistent, one CTA per SM, 15 warps): the rows'
 // tiles of 128 tokens lie on one line, equal runs of it to every CTA.
 //   * S^T = K Q^T with the tokens on M = 128 rows and the heads on N = 96: the
 //     sum over heads then stays inside a thread, and no MMA row is wasted.  Q
 //     (110 KB, turned into fp16 in place) stays in shared memory while a CTA
-//     works on a row; the keys pass through a ring of three 128-dim pairs of
-//     blocks and one slot for the last 64 dims.
-//   * warp 13 resolves tokens to records (index, page, slot) three tiles ahead.
-//   * warps 4..11 load 16 tokens' records each, a whole tile ahead in registers
-//     (four lanes a token and 16 bytes a lane: a load touches 8 lines; with two
-//     lanes a token it touched 16, and the load pipe, not the tensor cores,
-//     paced the kernel), widen them exactly to fp16 and store them 128-byte
-//     swizzled.
+//     works on a row.
+//   * The widened keys, the A operand, go to TMEM (288 columns; two S tiles take
+//     192 more), not to shared memory: storing 147 KB a tile there and reading
+//     it back took most of the shared-memory port's cycles.
+//   * warps 12, 13 find the tokens' records (index, page, slot; two stages ahead)
+//     and copy them raw, 16 bytes a lane, into a ring of 64-token stages; a record
+//     is padded by 16 bytes there, so that 32 lanes reading one 16-byte piece of
+//     32 records meet all banks.
+//   * warps 4..11 (thread = token, the TMEM lane; 4..7 dims 0..255, 8..11 dims
+//     256..575) widen them exactly to fp16, block by block.
 //   * warps 0..3, one thread a token: sum over heads of 2^(s c - lse c'), from
 //     one of two S tiles in TMEM while the next is computed.
 // With one row per sequence and no selection the kernel adds the running total
@@ -26,9 +28,6 @@
 // adds them, row after row, so the order of the sums is fixed:
 // weights_reduce_kernel (every visible token) or weights_scatter_kernel (the
 // selected ones: a CTA owns 4,096 tokens of a sequence in shared memory).
-// What bounds it: the shared-memory port (per tile 36 x (4 KB of keys + 3 KB of
-// Q) read and 147 KB written: 3,200 cycles at 128 B a cycle, against 1,730
-// cycles of tensor time).
 #include <algorithm>
 #include <atomic>
 
@@ -43,31 +42,36 @@ namespace {
 constexpr int kTok = 128;                        // tokens per tile
 constexpr int kDB = kLatent / 64;                // 9 blocks of 64 dims
 constexpr int kQBlockBytes = kHeads * 128;       // 12,288
-constexpr int kBlkBytes = kTok * 128;            // 16,384
-constexpr int kPairs = 4;                        // pairs of blocks a tile (dims 0..511), then the last block
-constexpr int kPairBytes = 2 * kBlkBytes;
-constexpr int kSlots = 3;                        // ring of pairs
-constexpr int kInfos = 4;                        // tiles whose records are resolved
+constexpr int kStageTok = 64;                    // tokens per stage of raw records
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);
-constexpr int kThreads = 14 * 32;                // epilogue 0-3, loaders 4-11, MMA issuer 12, lookup 13
-constexpr int kLoadWarp0 = 4;
-constexpr int kLoadWarps = 8;                    // 16 tokens each
-constexpr int kMmaWarp = 12;
-constexpr int kLookupWarp = 13;
-static_assert(kLoadWarps * 16 == kTok, "loader split");
-constexpr int kSCols = 128;                      // columns between the two S tiles
-constexpr int kTmemCols = 256;
+constexpr int kThreads = 15 * 32;                // epilogue 0-3, converters 4-11, producers 12-13, MMA issuer 14
+constexpr int kConvWarp0 = 4;
+constexpr int kProdWarp0 = 12;
+constexpr int kMmaWarp = 14;
+constexpr int kSplit = 4;                        // blocks below it: warps 4..7, from it: warps 8..11
+constexpr int kSCols = kHeads;                   // TMEM: two S tiles, then nine blocks of keys
+constexpr int kKCol = 2 * kSCols;
+constexpr int kTmemCols = 512;
+static_assert(kKCol + 32 * kDB <= kTmemCols, "TMEM columns");
+
+template <bool kNV>
+struct Raw {
+  static constexpr int kRec = kNV ? kNvRec : kLatent;
+  static constexpr int kStride = kRec + 16;
+  static constexpr int kBytes = kStageTok * kStride;  // 23,552 or 37,888
+  static constexpr int kStages = kNV ? 4 : 3;
+};
 
 constexpr int kOffQ = 0;
-constexpr int kOffRing = kDB * kQBlockBytes;                   // 110,592
-constexpr int kOffLast = kOffRing + kSlots * kPairBytes;       // dims 512..575
-constexpr int kOffInfo = kOffLast + kBlkBytes;                 // 225,280
-constexpr int kOffHead = kOffInfo + kInfos * kTok * 4;         // per head: its LSE (log2); per warp: a maximum
+constexpr int kOffRaw = kDB * kQBlockBytes;                    // 110,592
+constexpr int kRawBytes = Raw<false>::kStages * Raw<false>::kBytes;  // 113,664
+static_assert(Raw<true>::kStages * Raw<true>::kBytes <= kRawBytes, "raw ring");
+constexpr int kOffHead = kOffRaw + kRawBytes;                  // per head: its LSE (log2); per warp: a maximum
 constexpr int kOffBars = kOffHead + kHeads * 4 + 16;
-constexpr int kNumBars = 2 * (kSlots + 1) + 2 * kInfos + 7;
+constexpr int kNumBars = 2 * 4 + 2 * kDB + 7;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
-static_assert(kOffRing % 1024 == 0 && kOffBars % 8 == 0, "alignment");
+static_assert(kOffBars % 8 == 0, "alignment");
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct MassParams {
@@ -137,18 +141,18 @@ __device__ const uint4 zero_record[kLatent / 16] = {};
 template <bool kNV>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ MassParams p) {
-  constexpr int kRec = kNV ? kNvRec : kLatent;
+  using R = Raw<kNV>;
+  constexpr int kRec = R::kRec, kStages = R::kStages;
   constexpr uint32_t kIdesc = make_idesc(kFmtF16, kFmtF16, 0, 0, kTok, kHeads);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + kOffBars;
-  // ring slots 0 .. kSlots - 1, and the last block's slot kSlots
-  auto full = [&](uint32_t s) { return bars + 8u * s; };
-  auto empty = [&](uint32_t s) { return bars + 8u * (kSlots + 1 + s); };
-  auto info_full = [&](uint32_t s) { return bars + 8u * (2 * (kSlots + 1) + s); };
-  auto info_empty = [&](uint32_t s) { return bars + 8u * (2 * (kSlots + 1) + kInfos + s); };
-  const uint32_t bars2 = bars + 8u * (2 * (kSlots + 1) + 2 * kInfos);
+  auto raw_full = [&](uint32_t s) { return bars + 8u * s; };
+  auto raw_empty = [&](uint32_t s) { return bars + 8u * (4 + s); };
+  auto k_full = [&](uint32_t kb) { return bars + 8u * (8 + kb); };
+  auto k_empty = [&](uint32_t kb) { return bars + 8u * (8 + kDB + kb); };
+  const uint32_t bars2 = bars + 8u * (8 + 2 * kDB);
   auto s_full = [&](uint32_t s) { return bars2 + 8u * s; };
   auto s_empty = [&](uint32_t s) { return bars2 + 16 + 8u * s; };
   const uint32_t q_full = bars2 + 32, q_ready = bars2 + 40, drain = bars2 + 48;
@@ -157,17 +161,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
   float* lse_s = reinterpret_cast<float*>(smem + kOffHead);
   uint32_t* max_s = reinterpret_cast<uint32_t*>(smem + kOffHead + kHeads * 4);
-  int32_t* info = reinterpret_cast<int32_t*>(smem + kOffInfo);
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s <= kSlots; ++s) {
-      mbar_init(full(s), kLoadWarps);
-      mbar_init(empty(s), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(raw_full(s), 64);  // both producer warps' lanes
+      mbar_init(raw_empty(s), 4);  // the converters of 64 tokens
     }
-    for (int s = 0; s < kInfos; ++s) {
-      mbar_init(info_full(s), 1);
-      mbar_init(info_empty(s), kLoadWarps);
+    for (int kb = 0; kb < kDB; ++kb) {
+      mbar_init(k_full(kb), 4);
+      mbar_init(k_empty(kb), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
@@ -206,8 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ MMA issuer (the whole warp runs, one lane issues)
     const uint64_t q_desc = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSw128);
     const uint32_t q_lo = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
-    const uint32_t r_lo = (uint32_t)smem_desc(sbase + kOffRing, 16, 1024, kLayoutSw128);
-    uint32_t it = 0, n = 0, segs = 0;
+    uint32_t it = 0, segs = 0;
     int cur = -1;
     bool ok = true;
     while (ok) {
@@ -231,25 +233,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = ok && mbar_wait_warp(s_empty(b), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
 #pragma unroll 1
-      for (int mb = 0; ok && mb <= kPairs; ++mb) {
-        const bool last = mb == kPairs;
-        const uint32_t slot = last ? kSlots : n % kSlots;
-        ok = mbar_wait_warp(full(slot), last ? it & 1 : (n / kSlots) & 1, abort_flag, p.status);
+      for (int kb = 0; ok && kb < kDB; ++kb) {
+        ok = mbar_wait_warp(k_full(kb), it & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a_lo = r_lo + slot * (kPairBytes / 16), b_lo = q_lo + mb * (2 * kQBlockBytes / 16);
+        const uint32_t a_t = tmem + kKCol + 32 * kb, b_lo = q_lo + kb * (kQBlockBytes / 16);
         if (elect_one()) {
-#pragma unroll 1
-          for (int j = 0; j < (last ? 1 : 2); ++j)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(tmem + b * kSCols, desc64(a_lo + j * (kBlkBytes / 16) + 2 * kk, hi),
-                       desc64(b_lo + j * (kQBlockBytes / 16) + 2 * kk, hi), kIdesc, (mb | j | kk) ? 1u : 0u);
-          mma_commit(empty(slot));
-          if (last) mma_commit(s_full(b));
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_tmem_a(tmem + b * kSCols, a_t + 8 * kk, desc64(b_lo + 2 * kk, hi), kIdesc, (kb | kk) ? 1u : 0u);
+          mma_commit(k_empty(kb));
+          if (kb == kDB - 1) mma_commit(s_full(b));
         }
         __syncwarp();
-        if (!last) ++n;
       }
       ++it;
     }
@@ -258,175 +254,114 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(drain);  // every MMA completes before TMEM is released
       mbar_wait_drain(drain, 0, 10000000ull);
     }
-  } else if (warp == kLookupWarp) {
-    // ------------------------------------------------ lookup: block row * 64 + slot of each token, -1 for none
-    // The tokens of the next tile are fetched before this tile's pages are.
-    int tok[kTok / 32];
-    bool have;
+  } else if (warp >= kProdWarp0) {
+    // ------------------------------------------------ producers: raw records into the ring
+    // Lane: one of the warp's 32 tokens of a stage; a token's index is read two
+    // stages ahead, its page one.
+    const int pw = warp - kProdWarp0;
+    const uint8_t* rec = nullptr;
+    int part = 0, row_a = 0, tok_a = -1, tok_b = -1, page_b = -1, limit = 0, limit_row = -1;
+    bool have_t = false, have_a = false, have_b = false, have = false;
     auto step_token = [&]() {
-      have = tiles.next(row, first, count);
-#pragma unroll
-      for (int i = 0; i < kTok / 32; ++i) {
-        const int e = lane + 32 * i;
-        tok[i] = -1;
-        if (have && e < count) tok[i] = p.idx ? p.idx[(int64_t)row * p.k + first + e] : first + e;
+      if (part == 0) have_t = tiles.next(row, first, count);
+      have_a = have_t;
+      row_a = row;
+      tok_a = -1;
+      const int e = part * kStageTok + pw * 32 + lane;
+      if (have_a && e < count) tok_a = p.idx ? p.idx[(int64_t)row * p.k + first + e] : first + e;
+      part ^= 1;
+    };
+    auto step_page = [&]() {
+      have_b = have_a;
+      tok_b = -1;
+      page_b = -1;
+      if (!have_b) return;
+      if (row_a != limit_row) {
+        limit_row = row_a;
+        limit = tiles.visible(row_a);
       }
+      if (tok_a >= 0 && tok_a < limit) {
+        tok_b = tok_a;
+        page_b = p.block_table[(int64_t)(row_a / p.nq) * p.max_blocks + tok_a / kBlock];
+      } else if (tok_a >= 0) {
+        report(p.status, DSA_ERR_BOUNDS);  // an entry that its row does not see
+      }
+    };
+    auto step_record = [&]() {
+      have = have_b;
+      rec = reinterpret_cast<const uint8_t*>(zero_record);  // no token: zeros
+      if (tok_b < 0) return;
+      if ((uint32_t)page_b < (uint32_t)p.num_blocks)
+        rec = p.latent_base + (int64_t)page_b * p.row_stride + tok_b % kBlock * kRec;
+      else
+        report(p.status, DSA_ERR_BOUNDS);
     };
     step_token();
-    uint32_t it = 0;
-    while (have) {
-      int t[kTok / 32], page[kTok / 32];
-      const int limit = p.idx ? tiles.visible(row) : p.cap;
-      const int32_t* table = p.block_table + (int64_t)(row / p.nq) * p.max_blocks;
-#pragma unroll
-      for (int i = 0; i < kTok / 32; ++i) {
-        t[i] = tok[i];
-        if (t[i] >= limit) {
-          report(p.status, DSA_ERR_BOUNDS);
-          t[i] = -1;
-        }
-        page[i] = t[i] >= 0 ? table[t[i] / kBlock] : -1;
-      }
+    step_page();
+    step_token();
+    bool ok = true;
+    for (uint32_t n = 0;; ++n) {
+      step_record();
+      if (!have) break;
+      step_page();
       step_token();
-      if (!mbar_wait_warp(info_empty(it % kInfos), ((it / kInfos) & 1) ^ 1, abort_flag, p.status)) break;
+      const uint32_t slot = n % kStages;
+      ok = mbar_wait_warp(raw_empty(slot), ((n / kStages) & 1) ^ 1, abort_flag, p.status);
+      if (!ok) break;
+      const uint32_t dst = sbase + kOffRaw + slot * R::kBytes + pw * 32 * R::kStride;
+      const uint64_t mine = reinterpret_cast<uint64_t>(rec);
+#pragma unroll 8
+      for (int t = 0; t < 32; ++t) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, t));
 #pragma unroll
-      for (int i = 0; i < kTok / 32; ++i) {
-        const bool good = (uint32_t)page[i] < (uint32_t)p.num_blocks;
-        if (t[i] >= 0 && !good) report(p.status, DSA_ERR_BOUNDS);
-        info[(it % kInfos) * kTok + lane + 32 * i] = t[i] >= 0 && good ? page[i] * kBlock + t[i] % kBlock : -1;
-        if (t[i] >= 0 && good) {
-          const uint8_t* rec = p.latent_base + (int64_t)page[i] * p.row_stride + t[i] % kBlock * kRec;
-#pragma unroll
-          for (int o = 0; o < kRec; o += 128) prefetch_l2_line(rec + o);
-        }
+        for (int u = 0; u < (kRec + 511) / 512; ++u)
+          if (lane + 32 * u < kRec / 16) cp_async16(dst + t * R::kStride + 16 * (lane + 32 * u), src + 16 * (lane + 32 * u));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(info_full(it % kInfos));
-      ++it;
+      cp_async_arrive(raw_full(slot));
     }
-  } else if (warp >= kLoadWarp0) {
-    // ------------------------------------------------ loaders: records -> fp16 blocks
-    // Warp w: tokens 16 w .. 16 w + 15, eight at a time, four lanes a token: lane
-    // (token, block `blk` of the pair, its half `half`), numbered so that eight
-    // neighbours store 16 bytes each to all 32 banks.  A pair's records of the next
-    // tile go into registers as this tile's are widened out of them.
-    const int w = warp - kLoadWarp0;
-    const int half = lane & 1, blk = (lane >> 3) & 1, quarter = 2 * blk + half;
-    const int tok0 = w * 16 + ((lane >> 1) & 3) + ((lane >> 4) & 1) * 4;
-    const uint32_t off = (uint32_t)(tok0 * 128 + half * 64);
-    const uint32_t o0 = swz128(off), o1 = swz128(off + 16), o2 = swz128(off + 32), o3 = swz128(off + 48);
-    const uint32_t ot = (uint32_t)(tok0 * 128 + quarter * 32), ot0 = swz128(ot), ot1 = swz128(ot + 16);
-    uint4 buf[kPairs][2][kNV ? 1 : 2], last[2];
-    uint2 sc[2];  // the block scales of pair `quarter` of the lane's two tokens
-    const uint8_t* rec[2];
-    const int64_t mine = tiles.hi - tiles.pos;  // this run's tiles, as the lookup warp resolves them
-    auto resolve = [&](uint32_t tile) -> bool {
-      if (!mbar_wait_warp(info_full(tile % kInfos), (tile / kInfos) & 1, abort_flag, p.status)) return false;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int32_t ph = info[(tile % kInfos) * kTok + tok0 + 8 * e];
-        rec[e] = ph < 0 ? reinterpret_cast<const uint8_t*>(zero_record)
-                        : p.latent_base + (int64_t)(ph / kBlock) * p.row_stride + ph % kBlock * kRec;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(info_empty(tile % kInfos));
-      return true;
-    };
-    auto load_pair = [&](int mb) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (kNV) {
-          buf[mb][e][0] = __ldg(reinterpret_cast<const uint4*>(rec[e] + 64 * mb + 16 * quarter));
+    cp_async_wait_all();  // no copy is in flight at the exit
+  } else if (warp >= kConvWarp0) {
+    // ------------------------------------------------ converters: raw records -> fp16 keys in TMEM (thread = token)
+    const int q = warp & 3, group = (warp - kConvWarp0) >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + kKCol;
+    const uint8_t* mine = smem + kOffRaw + ((q & 1) * 32 + lane) * R::kStride;
+    const int64_t todo = tiles.hi - tiles.pos;
+    bool ok = true;
+    for (uint32_t it = 0; ok && (int64_t)it < todo; ++it) {
+      const uint32_t st = 2 * it + (q >> 1), slot = st % kStages;
+      ok = mbar_wait_warp(raw_full(slot), (st / kStages) & 1, abort_flag, p.status);
+      if (!ok) break;
+      const uint8_t* rec = mine + slot * R::kBytes;
+      uint4 sc = make_uint4(0, 0, 0, 0);
+      if (kNV) sc = *reinterpret_cast<const uint4*>(rec + kValue / 2 + 16 * group);
+#pragma unroll 1
+      for (int kb = group ? kSplit : 0; kb < (group ? kDB : kSplit); ++kb) {
+        uint32_t o[32];
+        if (kNV && kb < kDB - 1) {
+          const uint4 a = *reinterpret_cast<const uint4*>(rec + 32 * kb), b = *reinterpret_cast<const uint4*>(rec + 32 * kb + 16);
+          const uint32_t s = sc.x;  // four units' scales; the next block's follow
+          sc = make_uint4(sc.y, sc.z, sc.w, 0);
+          nvfp4x16_to_f16x16(a.x, a.y, s & 0xFFu, *reinterpret_cast<uint32_t(*)[8]>(o));
+          nvfp4x16_to_f16x16(a.z, a.w, (s >> 8) & 0xFFu, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
+          nvfp4x16_to_f16x16(b.x, b.y, (s >> 16) & 0xFFu, *reinterpret_cast<uint32_t(*)[8]>(o + 16));
+          nvfp4x16_to_f16x16(b.z, b.w, s >> 24, *reinterpret_cast<uint32_t(*)[8]>(o + 24));
         } else {
+          const uint8_t* c = rec + (kNV ? kValue / 2 + kValue / 16 : 64 * kb);
 #pragma unroll
-          for (int x = 0; x < (kNV ? 1 : 2); ++x)
-            buf[mb][e][x] = __ldg(reinterpret_cast<const uint4*>(rec[e] + 128 * mb + 32 * quarter + 16 * x));
+          for (int u = 0; u < 4; ++u)
+            e4m3x16_to_f16x16(*reinterpret_cast<const uint4*>(c + 16 * u), *reinterpret_cast<uint32_t(*)[8]>(o + 8 * u));
         }
-      }
-    };
-    auto load_last = [&]() {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        last[e] = __ldg(reinterpret_cast<const uint4*>(rec[e] + (kNV ? kValue / 2 + kValue / 16 : kValue) + 16 * quarter));
-    };
-    auto load_scales = [&]() {
-      if (kNV) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) sc[e] = __ldg(reinterpret_cast<const uint2*>(rec[e] + kValue / 2 + 8 * quarter));
-      }
-    };
-    auto store = [&](uint8_t* a0, uint8_t* a1, const uint32_t (&u)[8]) {
-      *reinterpret_cast<uint4*>(a0) = make_uint4(u[0], u[1], u[2], u[3]);
-      *reinterpret_cast<uint4*>(a1) = make_uint4(u[4], u[5], u[6], u[7]);
-    };
-    bool ok = mine > 0 && resolve(0);
-    if (ok) {
-      load_scales();
-#pragma unroll
-      for (int mb = 0; mb < kPairs; ++mb) load_pair(mb);
-      load_last();
-    }
-    // A step widens its data, then publishes the step before (whose stores have
-    // landed by then, so the fence is short), then waits for its slot and stores.
-    uint32_t pending = 0;  // the barrier of the step before
-    auto publish = [&]() {
-      if (pending) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pending);
-      }
-    };
-    uint32_t n = 0;
-    for (uint32_t it = 0; ok && it < mine; ++it) {
-      const bool next = it + 1 < mine;
-      const uint2 sn[2] = {sc[0], sc[1]};
-      ok = !next || resolve(it + 1);
-      if (!ok) break;
-      if (next) load_scales();
-#pragma unroll
-      for (int mb = 0; mb < kPairs; ++mb, ++n) {
-        uint32_t u[2][2][8];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (kNV) {
-            // pair mb's scales lie with the lane of quarter mb: its word `blk`, the half's two bytes
-            const int src = (lane & ~9) | (mb & 1) | ((mb >> 1) << 3);
-            const uint32_t x = __shfl_sync(0xffffffffu, sn[e].x, src), y = __shfl_sync(0xffffffffu, sn[e].y, src);
-            const uint32_t two = (blk ? y : x) >> (16 * half);
-            nvfp4x16_to_f16x16(buf[mb][e][0].x, buf[mb][e][0].y, two & 0xFFu, u[e][0]);
-            nvfp4x16_to_f16x16(buf[mb][e][0].z, buf[mb][e][0].w, (two >> 8) & 0xFFu, u[e][1]);
-          } else {
-            e4m3x16_to_f16x16(buf[mb][e][0], u[e][0]);
-            e4m3x16_to_f16x16(buf[mb][e][kNV ? 0 : 1], u[e][1]);
-          }
-        }
-        if (next) load_pair(mb);
-        publish();
-        const uint32_t slot = n % kSlots;
-        ok = mbar_wait_warp(empty(slot), ((n / kSlots) & 1) ^ 1, abort_flag, p.status);
+        ok = mbar_wait_warp(k_empty(kb), (it & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
-        uint8_t* at = smem + kOffRing + slot * kPairBytes + blk * kBlkBytes;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          store(at + o0 + 1024 * e, at + o1 + 1024 * e, u[e][0]);
-          store(at + o2 + 1024 * e, at + o3 + 1024 * e, u[e][1]);
-        }
-        pending = full(slot);
+        tc_fence_after();
+        tmem_st32(lane_base + 32 * kb, o);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full(kb));
       }
-      if (!ok) break;
-      uint32_t u[2][8];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) e4m3x16_to_f16x16(last[e], u[e]);
-      if (next) load_last();
-      publish();
-      ok = mbar_wait_warp(empty(kSlots), (it & 1) ^ 1, abort_flag, p.status);
-      if (!ok) break;
-      uint8_t* at = smem + kOffLast;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) store(at + ot0 + 1024 * e, at + ot1 + 1024 * e, u[e]);
-      pending = full(kSlots);
+      if (ok && lane == 0) mbar_arrive(raw_empty(slot));
     }
-    publish();
   } else {
     // ------------------------------------------------ weights (thread = token; thread h turns head h's query into fp16)
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
