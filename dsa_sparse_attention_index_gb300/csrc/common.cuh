@@ -250,9 +250,25 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r) :: "memory");
   return r != 0;
 }
-// mbar_wait by a whole warp, with the same answer in every lane.
+// mbar_wait by a whole converged warp, with the same answer in every lane.  Every
+// branch of it is on a vote: a per-lane loop (or one lane's wait and a broadcast)
+// makes the warp diverge and reconverge, which costs hundreds of cycles a wait.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+  uint32_t tries = 0;
+  uint64_t t0 = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if ((++tries & 63u) == 0) {
+      if (__any_sync(0xffffffffu, *abort != 0)) return false;
+      const uint64_t now = __shfl_sync(0xffffffffu, globaltimer(), 0);
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        *abort = 1;
+        report(status, DSA_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 // This warp's number in the CTA, known to the compiler to be the same in every lane.
 __device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
