@@ -448,9 +448,8 @@ __device__ __forceinline__ void nvfp4x16_to_f16x16(uint32_t w0, uint32_t w1, uin
     for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d[i]) : "r"(s2));
   }
 }
-// A head's bf16 query as fp16: times 2^e with e such that its largest magnitude
-// lands in [2^14, 2^15).  What falls below fp16's normal range is at most 2^-28
-// of that, and its rounding (2^-39 of it) far below the fp32 sums' own.
+// bf16 queries as fp16 times 2^e, with e such that the largest magnitude lands in
+// [2^14, 2^15).
 __device__ __forceinline__ uint32_t bf16x2_abs_max(uint32_t a, uint32_t b) {  // per 16-bit half, of magnitudes as integers
   return __vmaxu2(a, b & 0x7FFF7FFFu);
 }

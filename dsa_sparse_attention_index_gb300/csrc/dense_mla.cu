@@ -95,7 +95,8 @@ struct DenseParams {
   int32_t nq, cap, rows;
   float logit_scale_log2;  // sm_scale * latent_scale * log2(e)
   float latent_scale;
-  const uint16_t* q_mla;
+  const uint16_t* q16;     // the queries in fp16 times a power of two a row
+  const float* q_inv;      // its inverse, [rows]
   uint16_t* out;
   float* lse;
   uint16_t* opart;  // fp16 [slots][96][512]
@@ -111,6 +112,7 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool bar_or_softmax(bool v) {
   uint32_t r;
   asm volatile(
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto full = [&](uint32_t buf, int half) { return bars + 8u * (2 * buf + half); };
   auto empty = [&](uint32_t buf, int half) { return bars + 8u * (2 * kBufs + 2 * buf + half); };
   const uint32_t bars2 = bars + 8u * (4 * kBufs);
-  const uint32_t q_full = bars2, q_ready = bars2 + 8, o_free = bars2 + 16, drain = bars2 + 24, p_full = bars2 + 32,
+  const uint32_t q_full = bars2, q8_full = bars2 + 8, o_free = bars2 + 16, drain = bars2 + 24, p_full = bars2 + 32,
                  pv_done = bars2 + 40;
   auto s_full = [&](uint32_t b) { return bars2 + 48 + 8 * b; };
   auto s_empty = [&](uint32_t b) { return bars2 + 64 + 8 * b; };
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(empty(s, h), 1);
       }
     mbar_init(q_full, 1);
-    mbar_init(q_ready, 4);
+    mbar_init(q8_full, 4);
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     for (int b = 0; b < 2; ++b) {
@@ -249,8 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  grid_dep_wait();  // the lengths and the cache may come from the previous kernel
+  // The queries come from the previous kernel, which let this one start only when
+  // all before it had completed: the lengths can be read before the wait.
   Walk walk = make_walk(p, scratch);
+  grid_dep_wait();
   grid_dep_launch();
   tc_fence_before();
   __syncthreads();
@@ -283,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(sbase + kOffQ + kb * kQBlockBytes, &tmap_q, kb * 64, sg.row * kHeads, q_full);
       }
       __syncwarp();
-      // the softmax warps wait for it, turn it into fp16 where it lies and say so
-      ok = mbar_wait_warp(q_ready, seg & 1, abort_flag, p.status);
+      ok = mbar_wait_warp(q_full, seg & 1, abort_flag, p.status);
+      ok = ok && mbar_wait_warp(q8_full, seg & 1, abort_flag, p.status);
       ++seg;
       for (int t = sg.t0; ok && t < sg.t1; ++t, ++it) {
         ok = mbar_wait_warp(s_empty(it & 1), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
@@ -462,58 +466,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = threadIdx.x;
     const bool live = h < kHeads;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t it = 0, seg = 0;
+    uint32_t it = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
-      // ---- Q of head h to fp16 (every QK^T of the previous part has completed): dims 0..511 where TMA put them,
-      // 512..575 into TMEM
-      float c_log2;  // logits in log2 units per unit of S
+      // ---- Q dims 512..575 of head h into TMEM (every QK^T of the previous part has completed)
+      // logits in log2 units per unit of S
+      const float c_log2 = p.logit_scale_log2 * p.q_inv[sg.row];
       {
         const uint4* src = reinterpret_cast<const uint4*>(
-            p.q_mla + ((int64_t)sg.row * kHeads + (live ? h : 0)) * kLatent + 64 * kQSmemBlocks);
+            p.q16 + ((int64_t)sg.row * kHeads + (live ? h : 0)) * kLatent + 64 * kQSmemBlocks);
         uint4 v[8 * kQTmemBlocks];
 #pragma unroll
-        for (int c = 0; c < 8 * kQTmemBlocks; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        uint32_t am = 0;
-        auto more = [&](const uint4& w) {
-          am = bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(am, w.x), w.y), w.z), w.w);
-        };
-#pragma unroll
-        for (int c = 0; c < 8 * kQTmemBlocks; ++c) more(v[c]);
-        ok = mbar_wait(q_full, seg & 1, abort_flag, p.status);
-        if (bar_or_softmax(!ok)) { ok = false; break; }
-        uint8_t* q_row = smem + kOffQ;
-        if (live) {
-#pragma unroll 1
-          for (int kb = 0; kb < kQSmemBlocks; ++kb)
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              more(*reinterpret_cast<const uint4*>(q_row + kb * kQBlockBytes + swz128(h * 128 + c * 16)));
-        }
-        const int e = f16_shift_of(am);
-        const float scale = __int_as_float((127 + e) << 23);
-        c_log2 = p.logit_scale_log2 * __int_as_float((127 - e) << 23);
-        if (live) {
-#pragma unroll 1
-          for (int kb = 0; kb < kQSmemBlocks; ++kb)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(q_row + kb * kQBlockBytes + swz128(h * 128 + c * 16));
-              const uint4 w = *at;
-              *at = make_uint4(bf16x2_to_f16x2(w.x, scale), bf16x2_to_f16x2(w.y, scale), bf16x2_to_f16x2(w.z, scale),
-                               bf16x2_to_f16x2(w.w, scale));
-            }
-        }
+        for (int c = 0; c < 8 * kQTmemBlocks; ++c) v[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < 8 * kQTmemBlocks; ++c)
-          tmem_st4(lane_base + kQ8Col + 4 * c, bf16x2_to_f16x2(v[c].x, scale), bf16x2_to_f16x2(v[c].y, scale),
-                   bf16x2_to_f16x2(v[c].z, scale), bf16x2_to_f16x2(v[c].w, scale));
+          tmem_st4(lane_base + kQ8Col + 4 * c, v[c].x, v[c].y, v[c].z, v[c].w);
         tmem_st_wait();
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
-        ++seg;
+        if (lane == 0) mbar_arrive(q8_full);
       }
       float m_used = -INFINITY, l_sum = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
@@ -621,20 +592,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<float2*>(p.ml)[(int64_t)sg.slot * kHeads + h] = make_float2(m_used - kPShift, l_sum);
       }
       uint16_t* dst = direct ? p.out + (int64_t)sg.row * kPartO : p.opart + (int64_t)sg.slot * kPartO;
+      // turned in the P buffer (free: every PV has completed), 32 heads x 128 dims at a
+      // time, so that the stores are 16 bytes a lane and whole lines (2-byte stores
+      // straight from the lanes took 10 us)
+      uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kOffP);
+      static_assert(32 * 128 * 2 <= kPBytes, "the turned chunk fits");
 #pragma unroll 1
       for (int c = 0; c < 12; ++c) {
+        const int hg = (c % 3) * 32, d0 = (c / 3) * 128;
         uint32_t o[32];
-        tmem_ld32(lane_base + (c / 3) * kHeads + (c % 3) * 32, o);
+        tmem_ld32(lane_base + (c / 3) * kHeads + hg, o);
         tmem_ld_wait();
-        uint16_t* col = dst + (int64_t)((c % 3) * 32) * kValue + (c / 3) * 128 + threadIdx.x;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float v = __uint_as_float(o[j]) * alpha_s[(c % 3) * 32 + j];
-          col[j * kValue] = direct ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+          const float v = __uint_as_float(o[j]) * alpha_s[hg + j];
+          turn[j * 128 + threadIdx.x] = direct ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
         }
+        bar_softmax();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = threadIdx.x + 128 * u, j = i >> 4, d = (i & 15) * 8;
+          const uint4 v = *reinterpret_cast<const uint4*>(turn + j * 128 + d);
+          uint2* to = reinterpret_cast<uint2*>(dst + (int64_t)(hg + j) * kValue + d0 + d);  // out is 8-byte aligned
+          to[0] = make_uint2(v.x, v.y);
+          to[1] = make_uint2(v.z, v.w);
+        }
+        bar_softmax();
       }
       tc_fence_before();
-      bar_or_softmax(false);  // alpha_s is read: the next part may write it
       if (lane == 0) mbar_arrive(o_free);
     }
   }
@@ -751,7 +736,7 @@ int64_t dense_slots(int rows, int max_len, bool inv) {
 
 size_t dense_mla_workspace_bytes(int rows, int max_len) {
   const int64_t slots = dense_slots(rows, max_len, mla_batch_invariant_on());
-  return al256((size_t)rows * sizeof(int2)) + al256((size_t)slots * kPartO * 2) + al256((size_t)slots * kHeads * 8);
+  return query_f16_bytes(rows) + al256((size_t)rows * sizeof(int2)) + al256((size_t)slots * kPartO * 2) + al256((size_t)slots * kHeads * 8);
 }
 
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,
@@ -771,13 +756,16 @@ dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt,
       return DSA_ERR_CUDA;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
+  uint16_t* q16 = nullptr;
+  float* q_inv = nullptr;
+  if (launch_query_f16(q_mla, rows, workspace, &q16, &q_inv, st) != DSA_OK) return DSA_ERR_CUDA;
   CUtensorMap qmap;
   const uint64_t dims[2] = {(uint64_t)kLatent, (uint64_t)rows * kHeads};
   const uint64_t strides[1] = {(uint64_t)kLatent * 2};
   const uint32_t box[2] = {64, (uint32_t)kHeads};
-  if (!encode_tmap(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_mla, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_tmap(&qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_CUDA;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
+  uint8_t* w = static_cast<uint8_t*>(workspace) + query_f16_bytes(rows);
   DenseParams p = {};
   p.row_info = reinterpret_cast<int2*>(w);
   w += al256((size_t)rows * sizeof(int2));
@@ -795,7 +783,8 @@ dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt,
   p.rows = rows;
   p.logit_scale_log2 = sm_scale * c.latent_scale * 1.4426950408889634f;
   p.latent_scale = c.latent_scale;
-  p.q_mla = q_mla;
+  p.q16 = q16;
+  p.q_inv = q_inv;
   p.out = out;
   p.lse = lse;
   p.unit = inv ? kInvariantTiles : 0;

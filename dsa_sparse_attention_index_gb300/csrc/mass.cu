@@ -10,8 +10,8 @@
 // tiles of 128 tokens lie on one line, equal runs of it to every CTA.
 //   * S^T = K Q^T with the tokens on M = 128 rows and the heads on N = 96: the
 //     sum over heads then stays inside a thread, and no MMA row is wasted.  Q
-//     (110 KB, turned into fp16 in place) stays in shared memory while a CTA
-//     works on a row.
+//     (110 KB, fp16 from query.cu) stays in shared memory while a CTA works on a
+//     row.
 //   * The widened keys, the A operand, go to TMEM (288 columns; two S tiles take
 //     192 more), not to shared memory: storing 147 KB a tile there and reading
 //     it back took most of the shared-memory port's cycles.
@@ -66,9 +66,9 @@ constexpr int kOffQ = 0;
 constexpr int kOffRaw = kDB * kQBlockBytes;                    // 110,592
 constexpr int kRawBytes = Raw<false>::kStages * Raw<false>::kBytes;  // 113,664
 static_assert(Raw<true>::kStages * Raw<true>::kBytes <= kRawBytes, "raw ring");
-constexpr int kOffHead = kOffRaw + kRawBytes;                  // per head: its LSE (log2); per warp: a maximum
-constexpr int kOffBars = kOffHead + kHeads * 4 + 16;
-constexpr int kNumBars = 2 * 4 + 2 * kDB + 7;
+constexpr int kOffHead = kOffRaw + kRawBytes;                  // per head: its LSE (log2)
+constexpr int kOffBars = kOffHead + kHeads * 4;
+constexpr int kNumBars = 2 * 4 + 2 * kDB + 6;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
 static_assert(kOffBars % 8 == 0, "alignment");
@@ -85,6 +85,7 @@ struct MassParams {
   const int32_t* idx;   // [rows][k] or null: every visible token
   int32_t k;
   float scale_log2;     // sm_scale * latent_scale * log2(e)
+  const float* q_inv;   // [rows]: the inverse of the power of two in the fp16 queries
   const float* lse;     // [rows][96]
   const float* mass_in; // [batch][ld] (direct only)
   float* out;           // direct: mass_out [batch][ld]; else the rows' weights [rows][ld]
@@ -98,15 +99,7 @@ __device__ __forceinline__ float ex2f(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ bool bar_or_epilogue(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
+__device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 struct Tiles {  // a run's tiles, one after another
   const MassParams& p;
@@ -155,12 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars2 = bars + 8u * (8 + 2 * kDB);
   auto s_full = [&](uint32_t s) { return bars2 + 8u * s; };
   auto s_empty = [&](uint32_t s) { return bars2 + 16 + 8u * s; };
-  const uint32_t q_full = bars2 + 32, q_ready = bars2 + 40, drain = bars2 + 48;
+  const uint32_t q_full = bars2 + 32, drain = bars2 + 40;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
   float* lse_s = reinterpret_cast<float*>(smem + kOffHead);
-  uint32_t* max_s = reinterpret_cast<uint32_t*>(smem + kOffHead + kHeads * 4);
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -177,7 +169,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_empty(s), 4);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_ready, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -187,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  grid_dep_wait();  // the LSE, the indices and the lengths may come from the previous kernel
+  // The queries come from the previous kernel, which let this one start only when
+  // all before it had completed: the lengths can be read before the wait.
   Tiles tiles{p, 0, -1, 0, 0, 0};
   {
     const Run run = find_run<kThreads>(
@@ -198,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tiles.pos = run.pos;
     tiles.hi = run.hi;
   }
+  grid_dep_wait();
   grid_dep_launch();
   tc_fence_before();
   __syncthreads();
@@ -226,8 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(sbase + kOffQ + kb * kQBlockBytes, &tmap_q, kb * 64, row * kHeads, q_full);
         }
         __syncwarp();
-        // the epilogue warps wait for it, turn it into fp16 where it lies and say so
-        ok = mbar_wait_warp(q_ready, segs & 1, abort_flag, p.status);
+        ok = mbar_wait_warp(q_full, segs & 1, abort_flag, p.status);
         ++segs;
         cur = row;
       }
@@ -363,54 +355,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && lane == 0) mbar_arrive(raw_empty(slot));
     }
   } else {
-    // ------------------------------------------------ weights (thread = token; thread h turns head h's query into fp16)
+    // ------------------------------------------------ weights (thread = token)
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const int tid = threadIdx.x;
-    uint32_t it = 0, segs = 0;
+    uint32_t it = 0;
     int cur = -1;
     float c_log2 = 0.f;  // logits in log2 units per unit of S
     bool ok = true;
     while (tiles.next(row, first, count)) {
       const uint32_t b = it & 1;
       if (row != cur) {
-        // Every warp meets these barriers at the same rows, also after a wait that ran out.
-        ok = ok && mbar_wait_warp(q_full, segs & 1, abort_flag, p.status);
-        ok = !bar_or_epilogue(!ok);  // and the previous row's values have been read
-        uint8_t* q = smem + kOffQ;
-        uint32_t am = 0;
-        // one power of two for the whole row: a logit's error is then at most 2^-39 of the row's largest products
-        if (ok && tid < kHeads) {
-#pragma unroll 1
-          for (int kb = 0; kb < kDB; ++kb)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 w = *reinterpret_cast<const uint4*>(q + kb * kQBlockBytes + swz128(tid * 128 + c * 16));
-              am = bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(bf16x2_abs_max(am, w.x), w.y), w.z), w.w);
-            }
+        bar_epilogue();  // the previous row's values have been read
+        if (tid < kHeads) {
           const float l = p.lse[(int64_t)row * kHeads + tid];
           lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no token attended: no weight
         }
-        am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
-        if (lane == 0) max_s[warp] = am;
-        bar_or_epilogue(false);  // lse_s and max_s are written
-        const int e = f16_shift_of(max(max(max_s[0], max_s[1]), max(max_s[2], max_s[3])));
-        c_log2 = p.scale_log2 * __int_as_float((127 - e) << 23);
-        if (ok && tid < kHeads) {
-          const float scale = __int_as_float((127 + e) << 23);
-#pragma unroll 1
-          for (int kb = 0; kb < kDB; ++kb)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(q + kb * kQBlockBytes + swz128(tid * 128 + c * 16));
-              const uint4 w = *at;
-              *at = make_uint4(bf16x2_to_f16x2(w.x, scale), bf16x2_to_f16x2(w.y, scale), bf16x2_to_f16x2(w.z, scale),
-                               bf16x2_to_f16x2(w.w, scale));
-            }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
-        ++segs;
+        c_log2 = p.scale_log2 * p.q_inv[row];
+        bar_epilogue();
         cur = row;
       }
       ok = ok && mbar_wait_warp(s_full(b), (it >> 1) & 1, abort_flag, p.status);
@@ -514,9 +475,10 @@ int64_t round4(int64_t x) { return (x + 3) & ~int64_t(3); }
 }  // namespace
 
 size_t mass_workspace_bytes(int rows, int max_len, int k) {
-  // the rows' weights; one row per sequence without a selection needs none, but the query does not know the batch
+  // the fp16 queries and the rows' weights (one row per sequence without a selection needs none, but the query
+  // does not know the batch)
   const int64_t ld = k > 0 ? k : round4(std::max(max_len, 1));
-  return ((size_t)rows * ld * 4 + 255) & ~size_t(255);
+  return query_f16_bytes(rows) + (((size_t)rows * ld * 4 + 255) & ~size_t(255));
 }
 
 dsa_status_t launch_attention_mass(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
@@ -535,11 +497,14 @@ dsa_status_t launch_attention_mass(const dsa_paged_cache_t& c, const dsa_batch_t
       return DSA_ERR_CUDA;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
+  uint16_t* q16 = nullptr;
+  float* q_inv = nullptr;
+  if (launch_query_f16(q_mla, rows, workspace, &q16, &q_inv, st) != DSA_OK) return DSA_ERR_CUDA;
   CUtensorMap qmap;
   const uint64_t dims[2] = {(uint64_t)kLatent, (uint64_t)rows * kHeads};
   const uint64_t strides[1] = {(uint64_t)kLatent * 2};
   const uint32_t box[2] = {64, (uint32_t)kHeads};
-  if (!encode_tmap(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q_mla, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_tmap(&qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_CUDA;
   MassParams p = {};
   p.latent_base = static_cast<const uint8_t*>(c.base) + c.latent_off;
@@ -557,7 +522,8 @@ dsa_status_t launch_attention_mass(const dsa_paged_cache_t& c, const dsa_batch_t
   p.lse = lse;
   p.mass_in = mass_in;
   p.direct = !idx && p.nq == 1;
-  p.out = p.direct ? mass_out : static_cast<float*>(workspace);
+  p.q_inv = q_inv;
+  p.out = p.direct ? mass_out : reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + query_f16_bytes(rows));
   p.ld = p.direct ? ld : (idx ? k : round4(std::max(bt.max_seq_len, 1)));
   p.status = status;
   const int64_t most = (int64_t)rows * (((idx ? k : p.cap) + kTok - 1) / kTok);

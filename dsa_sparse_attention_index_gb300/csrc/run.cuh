@@ -23,44 +23,59 @@ __device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, 
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps <= 30, "scratch");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t sum = 0;
-  for (int r = threadIdx.x; r < rows; r += kThreads) sum += count(r);
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  for (int i = 0; i < kWarps; ++i) total += scratch[i];
-  __syncthreads();
-  const int64_t even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
-  const int64_t per = fixed_per ? fixed_per : (even > min_items ? even : min_items);
+  // up to kThreads rows, one scan gives the total and every row's place
+  const bool small = rows <= kThreads;
+  int64_t total = 0, n = 0;
+  if (!small) {
+    int64_t sum = 0;
+    for (int r = threadIdx.x; r < rows; r += kThreads) sum += count(r);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) scratch[warp] = sum;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) total += scratch[i];
+    __syncthreads();
+  }
   Run w;
-  w.pos = (int64_t)blockIdx.x * per;
-  w.hi = fixed_per ? total : (w.pos + per < total ? w.pos + per : total);
-  // the row that holds w.pos: a block scan over the rows, kThreads at a time
+  int64_t per = 0;
+  auto place = [&]() {
+    const int64_t even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
+    per = fixed_per ? fixed_per : (even > min_items ? even : min_items);
+    w.pos = (int64_t)blockIdx.x * per;
+    w.hi = fixed_per ? total : (w.pos + per < total ? w.pos + per : total);
+  };
+  if (!small) place();
   if (threadIdx.x == 0) scratch[30] = rows;
   int64_t base = 0;
   for (int r0 = 0; r0 < rows; r0 += kThreads) {
     const int r = r0 + threadIdx.x;
-    const int64_t n = r < rows ? count(r) : 0;
+    n = r < rows ? count(r) : 0;
     int64_t inc = n;
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    __syncthreads();
+    if (r0 > 0) __syncthreads();
     if (lane == 31) scratch[warp] = inc;
     __syncthreads();
     int64_t before = base;
-    for (int i = 0; i < warp; ++i) before += scratch[i];
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t v = scratch[i];
+      if (i < warp) before += v;
+      base += v;
+    }
+    if (small) {
+      total = base;
+      place();
+    }
     const int64_t first = before + inc - n;
     if (n > 0 && w.pos >= first && w.pos < first + n) {
       scratch[30] = r;
       scratch[31] = first;
     }
     if (blockIdx.x == 0 && r < rows) each(r, first, n, per);
-    for (int i = 0; i < kWarps; ++i) base += scratch[i];
     if (blockIdx.x != 0 && base > w.pos) break;  // the same in every thread
   }
+  if (rows == 0) place();
   __syncthreads();
   w.row = (int)scratch[30];
   w.start = scratch[31];

@@ -313,9 +313,9 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
  *   out       device bf16 bits [rows][96][512], 8-byte aligned;  lse device fp32 [rows][96]
  *   workspace >= dense_mla_workspace_size(rows, batch->max_seq_len) bytes, 256-B aligned
  * A table entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS in *dev_status.
- * Two launches.  The tokens of all rows are split evenly over the SMs, so the
+ * Three launches.  The tokens of all rows are split evenly over the SMs, so the
  * order of a row's sums depends on the batch; in the batch-invariant mode
- * (dsa_batch_invariant) rows are split every 4,096 tokens instead, and the
+ * (dsa_batch_invariant) rows are split every 3,840 tokens instead, and the
  * workspace size follows the mode at the time of the query.
  */
 size_t dense_mla_workspace_size(int32_t rows, int32_t max_seq_len);
@@ -340,9 +340,9 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
  *             that its row does not see raises DSA_ERR_BOUNDS
  *   mass_in   device fp32 [batch][ld_mass] or NULL (zeros);  mass_out likewise, mass_in itself
  *             (adding in place) or a buffer that does not overlap it;  ld_mass >= max_seq_len
- *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B
- *             aligned; not needed (NULL) with one row per sequence and idx NULL
- * One launch without a workspace, two with one.  Lengths as for dense_mla_decode.
+ *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B aligned
+ * Two launches with one row per sequence and idx NULL, else three.  Lengths as for
+ * dense_mla_decode.
  */
 size_t dsa_attention_mass_workspace_size(int32_t rows, int32_t max_seq_len, int32_t k);
 dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
