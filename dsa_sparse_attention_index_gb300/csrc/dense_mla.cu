@@ -112,7 +112,6 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool bar_or_softmax(bool v) {
   uint32_t r;
   asm volatile(
@@ -198,6 +197,64 @@ __device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
   w.pos = run.pos;
   w.hi = run.hi;
   return w;
+}
+
+// O^T of a part from TMEM (lanes: dims of a 128-dim block, columns: heads), times
+// alpha per head, to dst [96][512] as bf16 or fp16, by the four softmax warps: each
+// turns 32 heads x 32 dims at a time in 2 KB of its own, the next 32 on the way
+// from TMEM meanwhile, and writes 64 bytes a head.
+template <bool kBf16>
+__device__ __forceinline__ void write_part(uint32_t lane_base, const float* alpha, uint8_t* turn, uint16_t* dst) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint16_t* col = reinterpret_cast<uint16_t*>(turn + warp * 2048) + lane;
+  const uint4* rows = reinterpret_cast<const uint4*>(turn + warp * 2048) + lane;
+  uint16_t* to = dst + (lane >> 2) * kValue + warp * 32 + (lane & 3) * 8;
+  auto fetch = [&](int c, uint32_t (&o)[32]) { tmem_ld32(lane_base + (c / 3) * kHeads + (c % 3) * 32, o); };
+  auto put = [&](int c, const uint32_t (&o)[32]) {
+    const int hg = (c % 3) * 32, d0 = (c / 3) * 128;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(alpha + hg + j);
+      const float v0 = __uint_as_float(o[j]) * a.x, v1 = __uint_as_float(o[j + 1]) * a.y,
+                  v2 = __uint_as_float(o[j + 2]) * a.z, v3 = __uint_as_float(o[j + 3]) * a.w;
+      uint32_t x, y;
+      if (kBf16) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v0, v1), q = __floats2bfloat162_rn(v2, v3);
+        x = *reinterpret_cast<const uint32_t*>(&p);
+        y = *reinterpret_cast<const uint32_t*>(&q);
+      } else {
+        const __half2 p = __floats2half2_rn(v0, v1), q = __floats2half2_rn(v2, v3);
+        x = *reinterpret_cast<const uint32_t*>(&p);
+        y = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      col[j * 32] = (uint16_t)x;
+      col[(j + 1) * 32] = (uint16_t)(x >> 16);
+      col[(j + 2) * 32] = (uint16_t)y;
+      col[(j + 3) * 32] = (uint16_t)(y >> 16);
+    }
+    __syncwarp();
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = rows[32 * u];  // heads 8 u + lane / 4
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint2* p = reinterpret_cast<uint2*>(to + (hg + 8 * u) * kValue + d0);  // out is 8-byte aligned
+      p[0] = make_uint2(v[u].x, v[u].y);
+      p[1] = make_uint2(v[u].z, v[u].w);
+    }
+    __syncwarp();
+  };
+  uint32_t o0[32], o1[32];
+  fetch(0, o0);
+#pragma unroll 1
+  for (int c = 0; c < 12; c += 2) {
+    tmem_ld_wait();
+    fetch(c + 1, o1);
+    put(c, o0);
+    tmem_ld_wait();
+    if (c + 2 < 12) fetch(c + 2, o0);
+    put(c + 1, o1);
+  }
 }
 
 // What a lane without a token reads: zeros take no part in the products.
@@ -591,35 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           reinterpret_cast<float2*>(p.ml)[(int64_t)sg.slot * kHeads + h] = make_float2(m_used - kPShift, l_sum);
       }
-      uint16_t* dst = direct ? p.out + (int64_t)sg.row * kPartO : p.opart + (int64_t)sg.slot * kPartO;
-      // turned in the P buffer (free: every PV has completed), 32 heads x 128 dims at a
-      // time, so that the stores are 16 bytes a lane and whole lines (2-byte stores
-      // straight from the lanes took 10 us)
-      uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kOffP);
-      static_assert(32 * 128 * 2 <= kPBytes, "the turned chunk fits");
-#pragma unroll 1
-      for (int c = 0; c < 12; ++c) {
-        const int hg = (c % 3) * 32, d0 = (c / 3) * 128;
-        uint32_t o[32];
-        tmem_ld32(lane_base + (c / 3) * kHeads + hg, o);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float v = __uint_as_float(o[j]) * alpha_s[hg + j];
-          turn[j * 128 + threadIdx.x] = direct ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-        }
-        bar_softmax();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = threadIdx.x + 128 * u, j = i >> 4, d = (i & 15) * 8;
-          const uint4 v = *reinterpret_cast<const uint4*>(turn + j * 128 + d);
-          uint2* to = reinterpret_cast<uint2*>(dst + (int64_t)(hg + j) * kValue + d0 + d);  // out is 8-byte aligned
-          to[0] = make_uint2(v.x, v.y);
-          to[1] = make_uint2(v.z, v.w);
-        }
-        bar_softmax();
-      }
+      // turned in the P buffer (free: every PV has completed): 2-byte stores straight
+      // from the lanes took 12 us a part
+      uint8_t* turn = smem + kOffP;
+      if (direct)
+        write_part<true>(lane_base, alpha_s, turn, p.out + (int64_t)sg.row * kPartO);
+      else
+        write_part<false>(lane_base, alpha_s, turn, p.opart + (int64_t)sg.slot * kPartO);
       tc_fence_before();
+      bar_or_softmax(false);  // alpha_s and the P buffer are free for the next part
       if (lane == 0) mbar_arrive(o_free);
     }
   }
