@@ -9,14 +9,15 @@
 // encoding (keys and queries carry none), so a token may change its slot.
 //
 // evict_select_kernel: a cluster of C CTAs per sequence, each over a C-th of
-// its tokens.  The C-th largest key is found with three radix digits (11, 11,
-// 10 bits of an order-preserving key): a histogram per CTA in shared memory,
-// summed over the cluster through distributed shared memory (CTA r sums a C-th
-// of the bins and writes the totals to all), then a suffix scan in every CTA.
-// A last pass ranks the kept tokens (the CTAs' counts give each its first
-// position) and writes their indices, weights and physical rows.  The weights
-// are read from L2 on every pass but the first: 4 bytes a token against the
-// several hundred of a kept record.
+// its tokens, whose order-preserving keys it loads once into shared memory.  The
+// threshold is found with three radix digits (11, 11, 10 bits): a histogram per
+// CTA, summed over the cluster through distributed shared memory (CTA r sums a
+// C-th of the bins and writes the totals to all; every CTA reading all C
+// histograms took twice as long), then a scan from the top.  Tokens of total 0,
+// often a large part, are counted apart instead of all on one bin.  At last each
+// warp ranks a run of the CTA's tokens (the CTAs' and warps' counts give its first
+// position) and writes the kept ones' indices, totals and physical rows.  Bound
+// by latency: the barriers and dependent loads of about ten steps.
 //
 // evict_move_kernel: one CTA per destination page, its 64 records copied in
 // 16-byte units with every load of a thread in flight before its first store.
@@ -38,8 +39,11 @@ namespace cg = cooperative_groups;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
-constexpr int kMaxShare = 48 * 1024;  // tokens whose keys a CTA holds in shared memory (192 KB)
+constexpr uint32_t kZeroKey = 0x80000000u;  // score_key(0)
+constexpr int kUnroll = 4;            // tokens of a lane in flight
+constexpr int kCtaTokens = 2048;      // a CTA's share before a sequence takes more of them
+constexpr int kMaxCluster = 16;       // (8 where the device cannot schedule 16)
+constexpr int kMaxShare = 44 * 1024;  // tokens whose keys a CTA holds in shared memory (176 KB)
 
 struct SelectParams {
   const float* mass;
@@ -79,18 +83,24 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sh, uint32_
   return before + x - v;
 }
 
-// kResident: the CTA's keys stay in shared memory; else every pass reads the weights again (L2).
+// The total whose key this is (-0 as +0, a NaN as the canonical one).
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return key == 0 ? __uint_as_float(0x7FC00000u) : __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+// kResident: the CTA's keys stay in shared memory; else every pass reads the totals again (L2).
 template <bool kResident>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ uint32_t hist[kBins];   // this CTA's counts
-  __shared__ uint32_t total[kBins];  // the cluster's
+  __shared__ __align__(16) uint32_t hist[kBins];   // this CTA's counts
+  __shared__ __align__(16) uint32_t total[kBins];  // the cluster's
   __shared__ uint32_t sh[kSelWarps];
   __shared__ uint32_t found[2];
-  __shared__ uint32_t counts[2];     // this CTA's tokens kept whatever their rank, and at the threshold
+  __shared__ uint32_t counts[2];  // this CTA's tokens kept whatever their rank, and at the threshold
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x;
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
   grid_dep_wait();
   int L = p.seq_lens[b];
   if (L < 0 || L > p.cap) {
@@ -103,82 +113,92 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   int32_t* phys = p.phys + (int64_t)b * p.keep;
   float* mass_out = p.mass_out ? p.mass_out + (int64_t)b * p.ld_out : nullptr;
   const int n = min(L, p.keep);
-  auto put = [&](int pos, int t) {
-    const int r = table[t / kBlock];
+  auto put = [&](int pos, int t, int r, float x) {  // token t of block row r and total x is kept as token pos
     const bool ok = r >= 0 && r < p.num_blocks;
     if (!ok) report(p.status, DSA_ERR_BOUNDS);
     kept[pos] = t;
     phys[pos] = ok ? r * kBlock + t % kBlock : -1;
-    if (mass_out) mass_out[pos] = mass[t];
+    if (mass_out) mass_out[pos] = x;
   };
   if (rank == 0 && tid == 0) p.new_lens[b] = n;
   for (int i = n + rank * kSelThreads + tid; i < p.keep; i += C * kSelThreads) kept[i] = phys[i] = -1;
   if (mass_out)
     for (int64_t i = n + rank * kSelThreads + tid; i < p.ld_out; i += C * kSelThreads) mass_out[i] = 0.f;
   if (L <= p.keep) {  // uniform over the cluster
-    for (int t = rank * kSelThreads + tid; t < L; t += C * kSelThreads) put(t, t);
+    for (int t = rank * kSelThreads + tid; t < L; t += C * kSelThreads) put(t, t, table[t / kBlock], mass[t]);
     return;
   }
 
   // ---- the threshold: the m-th largest key of the middle [sink, L - recent)
   const int lo = p.sink, hi = L - p.recent;
   const uint32_t m = (uint32_t)(p.keep - p.sink - p.recent);
-  const int share = (((L + C - 1) / C) + 3) & ~3;  // tokens a CTA, a multiple of 4
+  const int share = (L + C - 1) / C;             // tokens a CTA
   const int t0 = min(L, rank * share), t1 = min(L, t0 + share);
-  const int a0 = max(t0, lo), a1 = min(t1, hi);    // its part of the middle
+  const int a0 = max(t0, lo), a1 = min(t1, hi);  // its part of the middle
   auto key_at = [&](int t) { return kResident ? keys[t - t0] : score_key(mass[t]); };
-  uint32_t prefix = 0, mask = 0, want = m;         // key & mask == prefix: the keys still in question
-  if (m > 0) {
+  if (kResident) {
+    constexpr int kU = 12;  // loads of a thread in flight
+    for (int tb = t0 + tid; tb < t1; tb += kU * kSelThreads) {
+      float x[kU];
 #pragma unroll
+      for (int u = 0; u < kU; ++u) x[u] = tb + u * kSelThreads < t1 ? mass[tb + u * kSelThreads] : 0.f;
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (tb + u * kSelThreads < t1) keys[tb + u * kSelThreads - t0] = score_key(x[u]);
+    }
+  }
+  __syncthreads();
+  uint32_t prefix = 0, mask = 0, want = m;  // key & mask == prefix: the keys still in question
+  if (m > 0) {
+#pragma unroll 1
     for (int d = 0; d < 3; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
       const uint32_t dmask = d < 2 ? 2047u : 1023u;
+      uint32_t zeros = 0;
+      for (int tb = a0 + tid; tb < a1; tb += kUnroll * kSelThreads) {
+        uint32_t key[kUnroll];
+        bool in[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kBins / kSelThreads; ++i) hist[tid + i * kSelThreads] = 0;
-      __syncthreads();
-      constexpr int kU = 4;
-      for (int tb = a0 + tid; tb < a1; tb += kU * kSelThreads) {
-        uint32_t key[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
           const int t = tb + u * kSelThreads;
-          if (t >= a1) continue;
-          if (kResident && d == 0)
-            key[u] = __float_as_uint(mass[t]);
-          else
-            key[u] = key_at(t);
+          key[u] = t < a1 ? key_at(t) : 0u;
+          in[u] = t < a1 && (key[u] & mask) == prefix;
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int t = tb + u * kSelThreads;
-          if (t >= a1) continue;
-          if (kResident && d == 0) keys[t - t0] = key[u] = score_key(__uint_as_float(key[u]));
-          if ((key[u] & mask) == prefix) atomicAdd(&hist[(key[u] >> shift) & dmask], 1u);
+        for (int u = 0; u < kUnroll; ++u) {
+          if (key[u] == kZeroKey)
+            zeros += in[u];
+          else if (in[u])
+            atomicAdd(&hist[(key[u] >> shift) & dmask], 1u);
         }
       }
+      zeros = __reduce_add_sync(0xffffffffu, zeros);
+      if (zeros && (tid & 31) == 0) atomicAdd(&hist[(kZeroKey >> shift) & dmask], zeros);
       cl.sync();
       // bins [rank, rank + 1) * kBins / C summed over the cluster, the sums written to every CTA
       for (int i = tid; i < kBins / C; i += kSelThreads) {
         const int bin = rank * (kBins / C) + i;
-        uint32_t s = 0;
+        uint32_t x[kMaxCluster], s = 0;
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < C) s += cl.map_shared_rank(hist, c)[bin];
+        for (int c = 0; c < kMaxCluster; ++c) x[c] = c < C ? cl.map_shared_rank(hist, c)[bin] : 0u;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) s += x[c];
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
           if (c < C) cl.map_shared_rank(total, c)[bin] = s;
       }
       cl.sync();
-      // the digit: bins from the top until `want` keys are covered
-      constexpr int kPer = kBins / kSelThreads;
-      uint32_t v[kPer], sum = 0, all;
+      // the digit: bins from the top, four a thread, until `want` keys are covered
+      static_assert(kBins == 4 * kSelThreads, "four bins a thread");
+      const int bin = kBins - 4 - 4 * tid;
+      const uint4 x = *reinterpret_cast<const uint4*>(total + bin);
+      const uint32_t v[4] = {x.w, x.z, x.y, x.x};
+      *reinterpret_cast<uint4*>(hist + bin) = make_uint4(0, 0, 0, 0);  // read by every CTA before the barrier
+      uint32_t all, before = block_scan(v[0] + v[1] + v[2] + v[3], sh, all);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += v[i] = total[kBins - 1 - kPer * tid - i];
-      uint32_t before = block_scan(sum, sh, all);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
+      for (int i = 0; i < 4; ++i) {
         if (want > before && want <= before + v[i]) {
-          found[0] = (uint32_t)(kBins - 1 - kPer * tid - i);
+          found[0] = (uint32_t)(bin + 3 - i);
           found[1] = before;
         }
         before += v[i];
@@ -187,53 +207,62 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       prefix |= found[0] << shift;
       mask |= dmask << shift;
       want -= found[1];
+      __syncthreads();
     }
   }
   // `want` of the keys equal to `prefix` stay, those of the lowest indices; with m = 0 none does.
-  // Low half: a token that stays whatever its rank among the equals; high half: one of the equals.
-  auto kind = [&](int t) -> uint32_t {
-    if (t >= t1) return 0u;
-    if (t < lo || t >= hi) return 1u;
-    if (m == 0) return 0u;
-    const uint32_t key = key_at(t);
-    return key > prefix ? 1u : key == prefix ? 1u << 16 : 0u;
+  // 1: a token that stays whatever its rank among the equals; 2: one of the equals.
+  auto kind = [&](int t, uint32_t key) {
+    return t < lo || t >= hi ? 1 : m == 0 ? 0 : key > prefix ? 1 : key == prefix ? 2 : 0;
   };
+  // Each warp ranks a run of the CTA's tokens: first its counts, then, from its first position, the tokens.
+  const int lane = tid & 31, wid = tid >> 5;
+  const int run = (t1 - t0 + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+  const int w0 = min(t1, t0 + wid * run), w1 = min(t1, w0 + run);
   uint32_t hard = 0, equal = 0;
-  for (int t = t0 + tid; t < t1; t += kSelThreads) {
-    const uint32_t k = kind(t);
-    hard += k & 0xffffu;
-    equal += k >> 16;
+  for (int tb = w0; tb < w1; tb += 32 * kUnroll) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int t = tb + 32 * u + lane;
+      const int k = t < w1 ? kind(t, key_at(t)) : 0;
+      hard += k == 1;
+      equal += k == 2;
+    }
   }
+  hard = __reduce_add_sync(0xffffffffu, hard);
+  equal = __reduce_add_sync(0xffffffffu, equal);
   uint32_t th, te;
-  block_scan(hard, sh, th);
-  block_scan(equal, sh, te);
+  const uint32_t hs = block_scan(lane == 0 ? hard : 0u, sh, th), es = block_scan(lane == 0 ? equal : 0u, sh, te);
+  uint32_t hard_before = __shfl_sync(0xffffffffu, hs, 0), eq_before = __shfl_sync(0xffffffffu, es, 0);
   if (tid == 0) {
     counts[0] = th;
     counts[1] = te;
   }
   cl.sync();
-  uint32_t hard_before = 0, eq_before = 0;  // of the CTAs before this one
-  for (int c = 0; c < rank; ++c) {
-    const uint32_t* o = cl.map_shared_rank(counts, c);
-    hard_before += o[0];
-    eq_before += o[1];
-  }
+  // of the CTAs before this one: lane c asks CTA c
+  const uint32_t* o = lane < rank ? cl.map_shared_rank(counts, lane) : nullptr;
+  hard_before += __reduce_add_sync(0xffffffffu, o ? o[0] : 0u);
+  eq_before += __reduce_add_sync(0xffffffffu, o ? o[1] : 0u);
   cl.sync();  // the counts have been read: a CTA may exit
-  for (int tb = t0; tb < t1; tb += 4 * kSelThreads) {
-    const int t = tb + 4 * tid;
-    uint32_t k[4], sum = 0, all;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int tb = w0; tb < w1; tb += 32 * kUnroll) {
+    uint32_t key[kUnroll];
+    int r[kUnroll], k[kUnroll];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += k[i] = kind(t + i);
-    const uint32_t r = block_scan(sum, sh, all);
-    uint32_t hb = hard_before + (r & 0xffffu), eb = eq_before + (r >> 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (k[i] == 1u || (k[i] && eb < want)) put((int)(hb + min(eb, want)), t + i);
-      hb += k[i] & 0xffffu;
-      eb += k[i] >> 16;
+    for (int u = 0; u < kUnroll; ++u) {
+      const int t = tb + 32 * u + lane;
+      key[u] = t < w1 ? key_at(t) : 0u;
+      r[u] = t < w1 ? table[t / kBlock] : -1;
+      k[u] = t < w1 ? kind(t, key[u]) : 0;
     }
-    hard_before += all & 0xffffu;
-    eq_before += all >> 16;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t hm = __ballot_sync(0xffffffffu, k[u] == 1), em = __ballot_sync(0xffffffffu, k[u] == 2);
+      const uint32_t hb = hard_before + __popc(hm & below), eb = eq_before + __popc(em & below);
+      if (k[u] == 1 || (k[u] == 2 && eb < want)) put((int)(hb + min(eb, want)), tb + 32 * u + lane, r[u], key_value(key[u]));
+      hard_before += __popc(hm);
+      eq_before += __popc(em);
+    }
   }
 }
 
@@ -299,6 +328,32 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MovePara
 
 }  // namespace
 
+// Whether clusters of C of the largest select CTAs can be resident on this device (asked once per device).
+static bool cluster_ok(int C) {
+  static std::atomic<int> known[64];  // 0 unknown, 1 yes, 2 no
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return false;
+  if (known[dev] == 0) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kMaxShare * 4;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok = cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<true>, &cfg) == cudaSuccess && n > 0;
+    cudaGetLastError();  // a refused query leaves no error behind
+    known[dev] = ok ? 1 : 2;
+  }
+  return known[dev] == 1;
+}
+
 size_t evict_workspace_bytes(int batch, int keep) { return ((size_t)batch * keep * 4 + 255) & ~size_t(255); }
 
 dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t& bt, const float* mass, int64_t ld_mass,
@@ -323,21 +378,26 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
   s.new_lens = new_lens;
   s.phys = static_cast<int32_t*>(workspace);
   s.status = status;
-  // CTAs a sequence: enough that a CTA's share is at most 2,048 tokens, but no more than fill the SMs twice
-  // (one sequence of 5,001 tokens and 32 of 16K to 49K measured: see the kernel's comment)
-  int C = 1;
-  while (C < kMaxCluster && C * 2048 < bt.max_seq_len && 2 * C * bt.batch <= 2 * num_sms()) C *= 2;
-  const int64_t share = ((((int64_t)bt.max_seq_len + C - 1) / C) + 3) & ~int64_t(3);
-  const bool resident = share <= kMaxShare;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     if (cuda_status(cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMaxShare * 4)) != DSA_OK)
+                                         kMaxShare * 4)) != DSA_OK ||
+        cuda_status(cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
+            DSA_OK ||
+        cuda_status(cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                         1)) != DSA_OK)
       return DSA_ERR_CUDA;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
+  // CTAs a sequence: a share of kCtaTokens each, while all fit the SMs at once (two an SM)
+  int most = kMaxCluster;
+  while (most > 8 && !cluster_ok(most)) most /= 2;
+  int C = 1;
+  while (C < most && C * kCtaTokens < bt.max_seq_len && C * bt.batch <= num_sms()) C *= 2;
+  const int64_t share = ((int64_t)bt.max_seq_len + C - 1) / C;
+  const bool resident = share <= kMaxShare;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -348,7 +408,7 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(bt.batch * C));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = resident ? (size_t)share * 4 : 0;
+  cfg.dynamicSmemBytes = resident ? (size_t)std::max<int64_t>(share, 1) * 4 : 0;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
