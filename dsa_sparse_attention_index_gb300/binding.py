@@ -143,8 +143,31 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle, without building a Stream object (3 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+_BITS16 = (torch.int16, torch.uint16, torch.bfloat16)
+_I32, _F32 = (torch.int32,), (torch.float32,)
+
+
+def _want(name: str, t, shape, dtypes) -> int | None:
+    """The address of a tensor that must have this shape (-1: any size from 1) and one of these types, or of None."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or len(t.shape) != len(shape) or any(w != n and w != -1 for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected {list(shape)} of {dtypes[0]}, got {list(t.shape)} of {t.dtype}")
+    return _ptr(t)
+
+
+def _one_device(*tensors) -> None:
+    """Every tensor on the current device: the library launches there."""
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != at:
+            raise ValueError(f"tensors must be on the current device (cuda:{at}), got {t.device}")
 
 
 @dataclass
@@ -266,11 +289,16 @@ def dense_mla_workspace_size(rows: int, max_seq_len: int) -> int:
 
 def dense_mla_decode(cache: PagedCache, batch: Batch, q_mla, sm_scale: float, out, lse, workspace, status,
                      stream=None):
-    """Exact MLA over every token each row sees (no selection): out [rows, 96, 512] bf16 bits, lse fp32 [rows, 96]."""
-    c, b = cache.struct(), batch.struct()
-    _check(lib().dense_mla_decode(ctypes.byref(c), ctypes.byref(b), _ptr(q_mla), float(sm_scale), _ptr(out), _ptr(lse),
-                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-                                  _stream(stream)), "dense_mla_decode")
+    """Exact MLA over every token each row sees (no selection): q_mla bf16 bits [rows, 96, 576], out bf16 bits
+    [rows, 96, 512], lse fp32 [rows, 96]."""
+    c, b, rows = cache.struct(), batch.struct(), batch.rows
+    _one_device(cache.pool, batch.block_table, batch.seq_lens, q_mla, out, lse, workspace, status)
+    _check(lib().dense_mla_decode(ctypes.byref(c), ctypes.byref(b),
+                                  _want("q_mla", q_mla, (rows, MLA_HEADS, LATENT), _BITS16), float(sm_scale),
+                                  _want("out", out, (rows, MLA_HEADS, VALUE), _BITS16),
+                                  _want("lse", lse, (rows, MLA_HEADS), _F32), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
+           "dense_mla_decode")
 
 
 def attention_mass_workspace_size(rows: int, max_seq_len: int, k: int = 0) -> int:
@@ -280,15 +308,17 @@ def attention_mass_workspace_size(rows: int, max_seq_len: int, k: int = 0) -> in
 def attention_mass(cache: PagedCache, batch: Batch, q_mla, lse, sm_scale: float, mass_in, mass_out, workspace, status,
                    idx=None, stream=None):
     """mass_out = mass_in (or 0) + every token's attention weight, summed over the rows of its sequence and the heads:
-    fp32 [batch, ld]; over every visible token, or over the top-k's entries when idx is given."""
-    c, b = cache.struct(), batch.struct()
-    if mass_in is not None and mass_in.shape != mass_out.shape:
-        raise ValueError("mass_in and mass_out must have the same shape")
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().dsa_attention_mass(ctypes.byref(c), ctypes.byref(b), _ptr(q_mla), _ptr(lse), _ptr(idx),
-                                    int(idx.shape[1]) if idx is not None else 0, float(sm_scale), _ptr(mass_in),
-                                    _ptr(mass_out), int(mass_out.shape[1]), _ptr(workspace), nbytes, _ptr(status),
-                                    _stream(stream)), "dsa_attention_mass")
+    fp32 [batch, ld]; over every visible token, or over the top-k's entries when idx (int32 [rows, k]) is given."""
+    c, b, rows = cache.struct(), batch.struct(), batch.rows
+    _one_device(cache.pool, batch.block_table, batch.seq_lens, q_mla, lse, mass_in, mass_out, workspace, status, idx)
+    out = _want("mass_out", mass_out, (batch.batch, -1), _F32)
+    _check(lib().dsa_attention_mass(ctypes.byref(c), ctypes.byref(b),
+                                    _want("q_mla", q_mla, (rows, MLA_HEADS, LATENT), _BITS16),
+                                    _want("lse", lse, (rows, MLA_HEADS), _F32), _want("idx", idx, (rows, -1), _I32),
+                                    int(idx.shape[1]) if idx is not None else 0, float(sm_scale),
+                                    _want("mass_in", mass_in, tuple(mass_out.shape), _F32), out,
+                                    int(mass_out.shape[1]), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _ptr(status), _stream(stream)), "dsa_attention_mass")
 
 
 def cache_evict_workspace_size(batch: int, max_seq_len: int, keep: int) -> int:
@@ -300,14 +330,18 @@ def cache_evict(cache: PagedCache, batch: Batch, mass, keep: int, sink: int, rec
     """Keep each sequence's first `sink`, last `recent` and, between them, heaviest tokens (`keep` in all) and move
     their records into the pages of dst_block_table.  kept_idx int32 [batch, keep], mass_out fp32 [batch, >= keep]
     or None, new_lens int32 [batch]."""
-    c, b, d = cache.struct(), batch.struct(), dst_cache.struct()
-    if tuple(kept_idx.shape) != (batch.batch, int(keep)):
-        raise ValueError("kept_idx must be [batch, keep]")
-    _check(lib().dsa_cache_evict(ctypes.byref(c), ctypes.byref(b), _ptr(mass), int(mass.shape[1]), int(keep), int(sink),
-                                 int(recent), ctypes.byref(d), _ptr(dst_block_table), int(dst_block_table.shape[1]),
-                                 _ptr(kept_idx), _ptr(mass_out), int(mass_out.shape[1]) if mass_out is not None else 0,
-                                 _ptr(new_lens), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 _ptr(status), _stream(stream)), "dsa_cache_evict")
+    c, b, d, n = cache.struct(), batch.struct(), dst_cache.struct(), batch.batch
+    _one_device(cache.pool, batch.block_table, batch.seq_lens, mass, dst_cache.pool, dst_block_table, kept_idx, mass_out,
+                new_lens, workspace, status)
+    _check(lib().dsa_cache_evict(ctypes.byref(c), ctypes.byref(b), _want("mass", mass, (n, -1), _F32),
+                                 int(mass.shape[1]), int(keep), int(sink), int(recent), ctypes.byref(d),
+                                 _want("dst_block_table", dst_block_table, (n, -1), _I32), int(dst_block_table.shape[1]),
+                                 _want("kept_idx", kept_idx, (n, int(keep)), _I32),
+                                 _want("mass_out", mass_out, (n, -1), _F32),
+                                 int(mass_out.shape[1]) if mass_out is not None else 0,
+                                 _want("new_lens", new_lens, (n,), _I32), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
+           "dsa_cache_evict")
 
 
 def batch_invariant(on: bool) -> bool:

@@ -41,7 +41,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr uint32_t kZeroKey = 0x80000000u;  // score_key(0)
 constexpr int kUnroll = 4;            // tokens of a lane in flight
-constexpr int kCtaTokens = 2048;      // a CTA's share before a sequence takes more of them
+constexpr int kCtaTokens = 1024;      // a CTA's share before a sequence takes more of them
 constexpr int kMaxCluster = 16;       // (8 where the device cannot schedule 16)
 constexpr int kMaxShare = 44 * 1024;  // tokens whose keys a CTA holds in shared memory (176 KB)
 
