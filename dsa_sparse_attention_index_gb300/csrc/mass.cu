@@ -6,7 +6,7 @@
 // LSE), or those its top-k selected (the sparse attention's).  The running total
 // is what cache eviction ranks tokens by.
 //
-// attention_weights_kernel (persistent, one CTA per SM, 15 warps): the rows'
+// attention_weights_kernel (persistent, one CTA per SM, 19 warps): the rows'
 // tiles of 128 tokens lie on one line, equal runs of it to every CTA.
 //   * S^T = K Q^T with the tokens on M = 128 rows and the heads on N = 96: the
 //     sum over heads then stays inside a thread, and no MMA row is wasted.  Q
@@ -15,12 +15,13 @@
 //   * The widened keys, the A operand, go to TMEM (288 columns; two S tiles take
 //     192 more), not to shared memory: storing 147 KB a tile there and reading
 //     it back took most of the shared-memory port's cycles.
-//   * warps 12, 13 find the tokens' records (index, page, slot; two stages ahead)
+//   * warps 16, 17 find the tokens' records (index, page, slot; two stages ahead)
 //     and copy them raw, 16 bytes a lane, into a ring of 64-token stages; a record
 //     is padded by 16 bytes there, so that 32 lanes reading one 16-byte piece of
 //     32 records meet all banks.
-//   * warps 4..11 (thread = token, the TMEM lane; 4..7 dims 0..255, 8..11 dims
-//     256..575) widen them exactly to fp16, block by block.
+//   * warps 4..15 (thread = token, the TMEM lane; three sets of four warps, 192
+//     dims each) widen them exactly to fp16; a set's three blocks are one step of
+//     the MMA issuer (a step a block, or two sets, left it waiting).
 //   * warps 0..3, one thread a token: sum over heads of 2^(s c - lse c'), from
 //     one of two S tiles in TMEM while the next is computed.
 // With one row per sequence and no selection the kernel adds the running total
@@ -44,11 +45,13 @@ constexpr int kDB = kLatent / 64;                // 9 blocks of 64 dims
 constexpr int kQBlockBytes = kHeads * 128;       // 12,288
 constexpr int kStageTok = 64;                    // tokens per stage of raw records
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);
-constexpr int kThreads = 15 * 32;                // epilogue 0-3, converters 4-11, producers 12-13, MMA issuer 14
+constexpr int kThreads = 19 * 32;                // epilogue 0-3, converters 4-15, producers 16-17, MMA issuer 18
 constexpr int kConvWarp0 = 4;
-constexpr int kProdWarp0 = 12;
-constexpr int kMmaWarp = 14;
-constexpr int kSplit = 4;                        // blocks below it: warps 4..7, from it: warps 8..11
+constexpr int kProdWarp0 = 16;
+constexpr int kMmaWarp = 18;
+constexpr int kSets = 3;                         // of converters, four warps each
+constexpr int kSetBlocks = kDB / kSets;          // blocks of a set
+static_assert(kSets * kSetBlocks == kDB && kConvWarp0 + 4 * kSets == kProdWarp0, "converter split");
 constexpr int kSCols = kHeads;                   // TMEM: two S tiles, then nine blocks of keys
 constexpr int kKCol = 2 * kSCols;
 constexpr int kTmemCols = 512;
@@ -68,7 +71,7 @@ constexpr int kRawBytes = Raw<false>::kStages * Raw<false>::kBytes;  // 113,664
 static_assert(Raw<true>::kStages * Raw<true>::kBytes <= kRawBytes, "raw ring");
 constexpr int kOffHead = kOffRaw + kRawBytes;                  // per head: its LSE (log2)
 constexpr int kOffBars = kOffHead + kHeads * 4;
-constexpr int kNumBars = 2 * 4 + 2 * kDB + 6;
+constexpr int kNumBars = 2 * 4 + 2 * kSets + 6;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
 static_assert(kOffBars % 8 == 0, "alignment");
@@ -143,9 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = sbase + kOffBars;
   auto raw_full = [&](uint32_t s) { return bars + 8u * s; };
   auto raw_empty = [&](uint32_t s) { return bars + 8u * (4 + s); };
-  auto k_full = [&](uint32_t kb) { return bars + 8u * (8 + kb); };
-  auto k_empty = [&](uint32_t kb) { return bars + 8u * (8 + kDB + kb); };
-  const uint32_t bars2 = bars + 8u * (8 + 2 * kDB);
+  auto k_full = [&](uint32_t g) { return bars + 8u * (8 + g); };
+  auto k_empty = [&](uint32_t g) { return bars + 8u * (8 + kSets + g); };
+  const uint32_t bars2 = bars + 8u * (8 + 2 * kSets);
   auto s_full = [&](uint32_t s) { return bars2 + 8u * s; };
   auto s_empty = [&](uint32_t s) { return bars2 + 16 + 8u * s; };
   const uint32_t q_full = bars2 + 32, drain = bars2 + 40;
@@ -158,11 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(raw_full(s), 64);  // both producer warps' lanes
-      mbar_init(raw_empty(s), 4);  // the converters of 64 tokens
+      mbar_init(raw_empty(s), 2 * kSets);  // the converters of 64 tokens
     }
-    for (int kb = 0; kb < kDB; ++kb) {
-      mbar_init(k_full(kb), 4);
-      mbar_init(k_empty(kb), 1);
+    for (int g = 0; g < kSets; ++g) {
+      mbar_init(k_full(g), 4);
+      mbar_init(k_empty(g), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
@@ -225,17 +228,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = ok && mbar_wait_warp(s_empty(b), ((it >> 1) & 1) ^ 1, abort_flag, p.status);
 #pragma unroll 1
-      for (int kb = 0; ok && kb < kDB; ++kb) {
-        ok = mbar_wait_warp(k_full(kb), it & 1, abort_flag, p.status);
+      for (int g = 0; ok && g < kSets; ++g) {
+        ok = mbar_wait_warp(k_full(g), it & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a_t = tmem + kKCol + 32 * kb, b_lo = q_lo + kb * (kQBlockBytes / 16);
         if (elect_one()) {
+#pragma unroll 1
+          for (int kb = g * kSetBlocks; kb < (g + 1) * kSetBlocks; ++kb) {
+            const uint32_t a_t = tmem + kKCol + 32 * kb, b_lo = q_lo + kb * (kQBlockBytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_tmem_a(tmem + b * kSCols, a_t + 8 * kk, desc64(b_lo + 2 * kk, hi), kIdesc, (kb | kk) ? 1u : 0u);
-          mma_commit(k_empty(kb));
-          if (kb == kDB - 1) mma_commit(s_full(b));
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_tmem_a(tmem + b * kSCols, a_t + 8 * kk, desc64(b_lo + 2 * kk, hi), kIdesc, (kb | kk) ? 1u : 0u);
+          }
+          mma_commit(k_empty(g));
+          if (g == kSets - 1) mma_commit(s_full(b));
         }
         __syncwarp();
       }
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cp_async_wait_all();  // no copy is in flight at the exit
   } else if (warp >= kConvWarp0) {
     // ------------------------------------------------ converters: raw records -> fp16 keys in TMEM (thread = token)
-    const int q = warp & 3, group = (warp - kConvWarp0) >> 2;
+    const int q = warp & 3, g = (warp - kConvWarp0) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + kKCol;
     const uint8_t* mine = smem + kOffRaw + ((q & 1) * 32 + lane) * R::kStride;
     const int64_t todo = tiles.hi - tiles.pos;
@@ -324,15 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(raw_full(slot), (st / kStages) & 1, abort_flag, p.status);
       if (!ok) break;
       const uint8_t* rec = mine + slot * R::kBytes;
-      uint4 sc = make_uint4(0, 0, 0, 0);
-      if (kNV) sc = *reinterpret_cast<const uint4*>(rec + kValue / 2 + 16 * group);
 #pragma unroll 1
-      for (int kb = group ? kSplit : 0; kb < (group ? kDB : kSplit); ++kb) {
+      for (int kb = g * kSetBlocks; kb < (g + 1) * kSetBlocks; ++kb) {
         uint32_t o[32];
         if (kNV && kb < kDB - 1) {
           const uint4 a = *reinterpret_cast<const uint4*>(rec + 32 * kb), b = *reinterpret_cast<const uint4*>(rec + 32 * kb + 16);
-          const uint32_t s = sc.x;  // four units' scales; the next block's follow
-          sc = make_uint4(sc.y, sc.z, sc.w, 0);
+          const uint32_t s = *reinterpret_cast<const uint32_t*>(rec + kValue / 2 + 4 * kb);  // four units' scales
           nvfp4x16_to_f16x16(a.x, a.y, s & 0xFFu, *reinterpret_cast<uint32_t(*)[8]>(o));
           nvfp4x16_to_f16x16(a.z, a.w, (s >> 8) & 0xFFu, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
           nvfp4x16_to_f16x16(b.x, b.y, (s >> 16) & 0xFFu, *reinterpret_cast<uint32_t(*)[8]>(o + 16));
@@ -343,16 +346,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 4; ++u)
             e4m3x16_to_f16x16(*reinterpret_cast<const uint4*>(c + 16 * u), *reinterpret_cast<uint32_t(*)[8]>(o + 8 * u));
         }
-        ok = mbar_wait_warp(k_empty(kb), (it & 1) ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
+        if (kb == g * kSetBlocks) {
+          ok = mbar_wait_warp(k_empty(g), (it & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
         tmem_st32(lane_base + 32 * kb, o);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(kb));
       }
-      if (ok && lane == 0) mbar_arrive(raw_empty(slot));
+      if (!ok) break;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(k_full(g));
+        mbar_arrive(raw_empty(slot));
+      }
     }
   } else {
     // ------------------------------------------------ weights (thread = token)
