@@ -76,7 +76,7 @@ constexpr int kOffQ = 0;
 constexpr int kOffTile = kOffQ + kQSmemBlocks * kQBlockBytes;  // 86,016
 constexpr int kOffP = kOffTile + kBufs * kTileBytes;           // 196,608
 constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
-constexpr int kOffBars = kOffAlpha + 512;
+constexpr int kOffBars = kOffAlpha + 512 + 16;
 constexpr int kNumBars = 4 * kBufs + 10;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;              // TMEM slot, abort flag, scan scratch
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
-  float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
+  float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);  // 128 factors, then per softmax warp whether a head grew
+  volatile int* grew_s = reinterpret_cast<volatile int*>(smem + kOffAlpha + 512);
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -528,7 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(sg)) {
       // ---- Q dims 512..575 of head h into TMEM (every QK^T of the previous part has completed)
       // logits in log2 units per unit of S
-      const float c_log2 = p.logit_scale_log2 * p.q_inv[sg.row];
+      const float c_raw = p.logit_scale_log2 * p.q_inv[sg.row];
+      // its magnitude; a scale of 0 becomes one that still sends a masked token's -inf to -inf
+      const float c_log2 = fmaxf(fabsf(c_raw), 1e-38f);
       {
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q16 + ((int64_t)sg.row * kHeads + (live ? h : 0)) * kLatent + 64 * kQSmemBlocks);
@@ -545,8 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m_used = -INFINITY, l_sum = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        ok = ok && mbar_wait(s_full(it & 1), (it >> 1) & 1, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && mbar_wait_warp(s_full(it & 1), (it >> 1) & 1, abort_flag, p.status);
         tc_fence_after();
         uint32_t r[kTile];
         const uint32_t s_col = lane_base + kSCol + (it & 1) * kTile;
@@ -557,46 +559,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty(it & 1));
         const int valid = sg.vis - t * kTile;
-        float x[kTile];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (valid >= kTile) {
+        if (c_raw < 0.f) {  // a negative scale: the largest logit is that of the smallest product
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) {
-            x[j] = __uint_as_float(r[j]) * c_log2;
-            mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kTile; ++j) {
-            x[j] = j < valid ? __uint_as_float(r[j]) * c_log2 : -INFINITY;
-            mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-          }
+          for (int j = 0; j < kTile; ++j) r[j] ^= 0x80000000u;
         }
-        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (x[0] != x[0]) m_used = x[0];  // NaN logits (a NaN in the query) give a NaN row
+        if (valid < kTile) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) r[j] = j < valid ? r[j] : 0xFF800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < kTile; j += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[j + 2 * i])), __uint_as_float(r[j + 2 * i + 1]));
+        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c_log2;
+        const float first = __uint_as_float(r[0]);
+        if (first != first) m_used = first;  // NaN logits (a NaN in the query) give a NaN row
         const bool grow = live && m_tile > m_used + kRescaleThreshold;
         // one barrier a tile: any head that grew, and any warp whose wait ran out
         if (bar_or_softmax(grow || !ok)) {
-          if (bar_or_softmax(!ok)) { ok = false; break; }
           const float m_new = grow ? m_tile : m_used;
           const float alpha = (m_used == -INFINITY) ? 0.f : ex2f(m_used - m_new);
-          if (live) alpha_s[h] = alpha;
+          alpha_s[h] = alpha;
+          if (lane == 0) grew_s[warp] = 0;
+          __syncwarp();
+          if (grow) grew_s[warp] = 1;
           l_sum *= alpha;
           m_used = m_new;
+          if (t > sg.t0) ok = ok && mbar_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status);
+          if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s and grew_s
           if (t > sg.t0) {
-            ok = mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
-            if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 12; ++c) {
-              uint32_t o[32];
-              const uint32_t ta = lane_base + (c / 3) * kHeads + (c % 3) * 32;
-              tmem_ld32(ta, o);
-              tmem_ld_wait();
+            for (int g = 0; g < kHeads / 32; ++g) {
+              if (!grew_s[g]) continue;  // the 32 heads of warp g
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                const int col = g * 32 + (c & 1) * 16;
+                const uint32_t ta = lane_base + (c >> 1) * kHeads + col;
+                tmem_ld16(ta, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha_s[(c % 3) * 32 + j]);
-              tmem_st32(ta, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha_s[col + j]);
+                tmem_st16(ta, o);
+              }
             }
             tmem_st_wait();
           }
@@ -604,11 +612,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[kTile / 2];
         if (m_used != -INFINITY) {
           // times 2^7: fp16 keeps its 11 bits for weights down to 2^-21 of the largest
-          const float m_ref = m_used - kPShift;
+          const float m_ref = kPShift - m_used;
           float se[2] = {0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < kTile; j += 2) {
-            const float p0 = ex2f(x[j] - m_ref), p1 = ex2f(x[j + 1] - m_ref);
+            const float p0 = ex2f(fmaf(__uint_as_float(r[j]), c_log2, m_ref)),
+                        p1 = ex2f(fmaf(__uint_as_float(r[j + 1]), c_log2, m_ref));
             const __half2 bb = __floats2half2_rn(p0, p1);
             se[0] += p0;
             se[1] += p1;
@@ -621,8 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the PV of the tile before has read the P buffer; a wait that runs out is
         // told to the other warps at the next barrier
-        ok = it == 0 || mbar_wait(pv_done, (it - 1) & 1, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = it == 0 || mbar_wait_warp(pv_done, (it - 1) & 1, abort_flag, p.status);
         if (live && ok) {
           uint8_t* prow = smem + kOffP;
 #pragma unroll
@@ -697,8 +705,14 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
   };
   const float2* ml2 = reinterpret_cast<const float2*>(ml);
   float M = -INFINITY;
-  for (int s = th & 31; s < parts; s += 32) M = fmaxf(M, ml2[slot_of(s) * kHeads + h].x);
+  bool bad = false;  // NaN logits in a part
+  for (int s = th & 31; s < parts; s += 32) {
+    const float x = ml2[slot_of(s) * kHeads + h].x;
+    bad |= x != x;
+    M = fmaxf(M, x);
+  }
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (__any_sync(0xffffffffu, bad)) M = __int_as_float(0x7FC00000);
   float den = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   constexpr int kU = 4;
   for (int s0 = grp; s0 < parts; s0 += kU * kGroups) {

@@ -182,3 +182,43 @@ def test_dense_mla_lengths_outside_the_table():
     assert st == 0
     check_rows(case, out, lse, rows=[0])
     assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
+
+
+@pytest.mark.parametrize("scale", [-1.0 / 24, 0.0, 3.0])
+def test_dense_mla_scales(scale):
+    """A negative scale (the smallest products weigh most), none at all (uniform weights), and a large one."""
+    case = dataclasses.replace(synth.make_case("dense_scale", seq_lens=[1000, 47, 49], seed=23, latent_format=NV),
+                               sm_scale=scale)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check_rows(case, out, lse)
+
+
+def test_dense_mla_rising_logits():
+    """Tokens sorted by one head's logit, so that its maximum grows along the whole context and the others' do not."""
+    case = synth.make_case("dense_rising", seq_lens=[2500], seed=24, latent_format=FP8)
+    c = plain64.latents(case, 0)
+    q = plain64.queries(case, 0) * 8
+    case = dataclasses.replace(case, q_mla=q.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)[None].copy())
+    for head in (0, 50, 95):
+        order = torch.argsort(c @ q[head]).numpy()
+        pool = case.pool.copy()
+        flat = pool[case.block_table[0], :64 * 576].reshape(-1, 576)
+        flat[:2500] = flat[:2500][order]
+        pool[case.block_table[0], :64 * 576] = flat.reshape(-1, 64 * 576)
+        sorted_case = dataclasses.replace(case, pool=pool)
+        out, lse, st = run_dense(sorted_case, synth.device_case(sorted_case))
+        assert st == 0
+        check_rows(sorted_case, out, lse)
+
+
+def test_dense_mla_nan_query_gives_a_nan_row():
+    """A NaN in one head's query leaves NaN in that head and nothing in the others or in the other rows."""
+    case = synth.make_case("dense_nan", seq_lens=[500, 300], seed=25, latent_format=NV)
+    q = case.q_mla.copy()
+    q[0, 5, 17] = 0x7FC0
+    out, lse, st = run_dense(dataclasses.replace(case, q_mla=q), synth.device_case(dataclasses.replace(case, q_mla=q)))
+    assert st == 0
+    assert bool(torch.isnan(out[0, 5].float()).all()) and bool(torch.isnan(lse[0, 5]))
+    assert bool(torch.isfinite(out[1].float()).all()) and bool(torch.isfinite(lse[1]).all())
+    check_rows(case, out, lse, rows=[1])
