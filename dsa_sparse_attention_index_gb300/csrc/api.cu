@@ -336,6 +336,7 @@ dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_
   if (!q_mla || !lse || !mass_out || !aligned(q_mla, 16) || !aligned(lse, 4) || !aligned(idx, 4) ||
       !aligned(mass_in, 4) || !aligned(mass_out, 4) || ld_mass < batch->max_seq_len)
     return DSA_ERR_INVALID_ARG;
+  if (batch->max_seq_len > (1 << 23)) return DSA_ERR_UNSUPPORTED;  // one grid dimension counts runs of 256 tokens
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < mass_workspace_bytes(rows, batch->max_seq_len, k))
     return DSA_ERR_WORKSPACE;
   return launch_attention_mass(*cache, *batch, q_mla, lse, idx, k, sm_scale, mass_in, mass_out, ld_mass, workspace,

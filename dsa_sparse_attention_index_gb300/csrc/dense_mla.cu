@@ -9,30 +9,35 @@
 //   O   = latent_scale * sum_t softmax(l)_t c_t[0:512],  LSE = ln sum_t exp(l_t)
 // with c_t the unscaled E4M3 or NVFP4 latent.
 //
-// GB300 design (persistent, one CTA per SM, 10 warps):
-//   * All (row, 64-token page) tiles form one line; CTA c takes an equal run
-//     of it, so ragged batches, one long context and a prefill chunk all fill
-//     every SM to within a tile.  A row that lies in one CTA's run is written
-//     at once; one that crosses runs leaves a partial (normalised fp16 O, max,
-//     sums) per CTA, merged through the log-sum-exp by the combine kernel.
-//   * A tile is one page, read as it lies: warps 4..7 load a page's records
-//     with 16-byte loads a whole tile ahead (in registers), widen them exactly
-//     to bf16 and store 64-dim blocks, 128-byte swizzled, into a ring of 14
-//     value blocks and 2 key-only blocks.  A block is the B operand of QK^T
-//     (K-major, N = 64 tokens) and the A operand of P V (MN-major, M = 128
-//     dims over two blocks); it is freed as soon as its part of PV has run.
-//   * S = Q K^T has the heads on M = 128 rows (96 used).  Q dims 0..447 sit in
-//     shared memory, 448..575 in TMEM, O^T [512 dims x 96 heads] in 384 TMEM
-//     columns, S in 64.
-//   * warp 8 issues QK^T, warp 9 P V; warps 0..3 run the online softmax, one
-//     thread per head, as the sparse kernel does: P rounded to bf16 (the value
-//     products' operand type; the normaliser sums the rounded values, the LSE
-//     the exact ones), O^T rescaled only when a head's maximum grows by more
-//     than 2^8.
-// What bounds it: the shared-memory port.  Per tile QK^T reads 28 x (4 KB of Q
-// + 2 KB of keys) + 8 x 2 KB, PV 16 x (4 KB of values + 3 KB of P), and the
-// widened tile is written once: 370 KB, 2,900 cycles at 128 B a cycle, against
-// 1,630 cycles of tensor time for the 96 used rows.
+// GB300 design (persistent, one CTA per SM, 15 warps):
+//   * All rows' 48-token tiles form one line; CTA c takes an equal run of it
+//     (run.cuh), so ragged batches, one long context and a prefill chunk all fill
+//     every SM to within a tile.  A row that lies in one CTA's run is written at
+//     once; one that crosses runs leaves a partial (normalised fp16 O, reference
+//     and sum) per CTA, merged through the log-sum-exp by the combine kernel.
+//   * Operands are fp16, not bf16: E4M3 values and E2M1 x E4M3 products are exact
+//     in it, the conversion instructions widen to it in a third of the
+//     instructions that bf16 takes, and P keeps 11 bits.  query.cu turns Q into
+//     fp16 times a power of two.
+//   * warps 4..12, one per 64-dim block: two lanes a token, 16-byte loads a whole
+//     tile ahead in registers, a token's page looked up two tiles ahead; widened,
+//     stored 128-byte swizzled into one of two tile buffers, which are filled and
+//     freed in halves.  A tile is the B operand of QK^T (K-major, N = 48 tokens)
+//     and the A operand of P V (MN-major, M = 128 dims over two blocks).
+//   * S = Q K^T has the heads on M = 128 rows (96 used).  Q dims 0..511 sit in
+//     shared memory, 512..575 in TMEM, O^T [512 dims x 96 heads] in 384 TMEM
+//     columns, two S tiles in 96.
+//   * warp 13 issues QK^T, warp 14 P V, each as a whole with its MMAs under
+//     elect.sync; warps 0..3 run the online softmax, one thread per head: P is
+//     2^7 exp(l - reference) in fp16 (full precision down to 2^-21 of a head's
+//     largest weight), its fp32 sum the normaliser; O^T is rescaled, 32 heads at a
+//     time, only where a maximum grew by more than 2^8.
+// What bounds it: the shared-memory port.  A tile's MMAs read 272 KB (QK^T 32 x
+// (4 KB of Q + 1.5 KB of keys) + 4 x 1.5 KB, PV 12 x (4 KB of values + 3 KB of
+// P)) and its stores and polls take about 85 KB: 2,800 cycles at 128 B a cycle,
+// of which the measured 1.6 us use 88 % (32 contexts of 8K to 64K tokens, NVFP4:
+// 276 us, 893 TFLOP/s, 0.47 of the measured bf16 burst rate).  The tensor pipe is
+// active 47 % of the time.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -51,11 +56,10 @@ constexpr int kVB = kValue / 64;                       // 8 of them are values
 constexpr int kQTmemBlocks = 1;                        // Q dims 512..575 in TMEM
 constexpr int kQSmemBlocks = kDB - kQTmemBlocks;       // Q dims 0..511 in shared memory
 constexpr int kQBlockBytes = kHeads * 128;             // 12,288
-constexpr int kBlkBytes = kTile * 128;                 // 6,144: 48 tokens x 64 dims of bf16
-constexpr int kPairs = kVB / 2;                        // a pair of blocks: the 128 dims of one PV product
+constexpr int kBlkBytes = kTile * 128;                 // 6,144: 48 tokens x 64 dims of fp16
 constexpr int kTileBytes = kDB * kBlkBytes;            // 55,296; block 8 holds the key-only dims
 constexpr int kBufs = 2;                               // tile buffers, each filled and freed in two halves
-constexpr int kPBytes = kHeads * 128;                  // 12,288: a head's 48 bf16 in a 128-byte row
+constexpr int kPBytes = kHeads * 128;                  // 12,288: a head's 48 fp16 in a 128-byte row
 constexpr int kNvRec = kValue / 2 + kValue / 16 + (kLatent - kValue);  // 352 B
 constexpr int kThreads = 15 * 32;  // softmax 0-3, loaders 4-12 (one 64-dim block each), QK issuer 13, PV issuer 14
 constexpr int kLoadWarp0 = 4;
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(drain, 0, 10000000ull);
     }
   } else if (warp >= kLoadWarp0 && warp < kQkWarp) {
-    // ------------------------------------------------ loaders: page -> bf16 blocks
+    // ------------------------------------------------ loaders: records -> fp16 blocks
     // Warp kb: the 64 dims of block kb, two lanes a token, 16 tokens at a time.
     // Eight neighbouring lanes store 16 bytes each to all 32 banks.  Codes are
     // loaded a whole tile before they are stored, a token's page is looked up two

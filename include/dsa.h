@@ -306,7 +306,7 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
  *   l_t       = sm_scale * (q[r][h] . c_t)
  *   out[r][h] = sum_t softmax(l)_t * c_t[0:512]        (bf16, round-to-nearest)
  *   lse[r][h] = ln sum_t exp(l_t)                       (fp32)
- * A row that sees no token gets out = 0 and lse = -inf.  A length above
+ * A row that sees no token gets out = 0 and lse = -inf, a head whose logits are NaN NaN.  A length above
  * min(max_blocks_per_seq * 64, max_seq_len) is read as that bound, a negative
  * one as 0.  Any number of rows per sequence up to DSA_MAX_QUERIES_PER_SEQ.
  *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned
@@ -342,7 +342,7 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
  *             (adding in place) or a buffer that does not overlap it;  ld_mass >= max_seq_len
  *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B aligned
  * Two launches with one row per sequence and idx NULL, else three.  Lengths as for
- * dense_mla_decode.
+ * dense_mla_decode; max_seq_len up to 2^23, else DSA_ERR_UNSUPPORTED.
  */
 size_t dsa_attention_mass_workspace_size(int32_t rows, int32_t max_seq_len, int32_t k);
 dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
