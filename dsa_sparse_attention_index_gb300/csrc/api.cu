@@ -96,6 +96,18 @@ dsa_status_t check_index_rows(const dsa_paged_cache_t* c, const dsa_batch_t* b) 
   return DSA_OK;
 }
 
+// The kernels below count tokens, and tokens past the last tile, in 32 bits.
+bool too_long(const dsa_batch_t* b) {
+  return std::min<int64_t>((int64_t)b->max_blocks_per_seq * kBlock, b->max_seq_len) > (1 << 30);
+}
+
+// Whether the rows [batch][ld_a] and [batch][ld_b] of fp32 overlap.
+bool overlap(const float* a, int64_t ld_a, const float* b, int64_t ld_b, int batch) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), a1 = a0 + (uintptr_t)batch * ld_a * 4;
+  const uintptr_t b0 = reinterpret_cast<uintptr_t>(b), b1 = b0 + (uintptr_t)batch * ld_b * 4;
+  return a0 < b1 && b0 < a1;
+}
+
 int64_t round_ld(int max_len) { return ((int64_t)std::max(max_len, 1) + 7) & ~int64_t(7); }
 
 }  // namespace
@@ -311,6 +323,7 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
   const int rows = batch->batch * batch->queries_per_seq;
   if (rows == 0) return DSA_OK;
   if (!q_mla || !out || !lse || !aligned(q_mla, 16) || !aligned(out, 8) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
+  if (too_long(batch)) return DSA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_mla_workspace_bytes(rows, batch->max_seq_len))
     return DSA_ERR_WORKSPACE;
   return launch_dense_mla(*cache, *batch, q_mla, sm_scale, out, lse, workspace, dev_status,
@@ -335,6 +348,8 @@ dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_
   if (rows == 0) return DSA_OK;
   if (!q_mla || !lse || !mass_out || !aligned(q_mla, 16) || !aligned(lse, 4) || !aligned(idx, 4) ||
       !aligned(mass_in, 4) || !aligned(mass_out, 4) || ld_mass < batch->max_seq_len)
+    return DSA_ERR_INVALID_ARG;
+  if (mass_in && mass_in != mass_out && overlap(mass_in, ld_mass, mass_out, ld_mass, batch->batch))
     return DSA_ERR_INVALID_ARG;
   if (batch->max_seq_len > (1 << 23)) return DSA_ERR_UNSUPPORTED;  // one grid dimension counts runs of 256 tokens
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < mass_workspace_bytes(rows, batch->max_seq_len, k))
@@ -369,16 +384,14 @@ dsa_status_t dsa_cache_evict(const dsa_paged_cache_t* cache, const dsa_batch_t* 
     return DSA_ERR_UNSUPPORTED;
   if (((int64_t)keep + kBlock - 1) / kBlock * batch->batch > (1 << 24)) return DSA_ERR_UNSUPPORTED;
   if (batch->batch == 0) return DSA_OK;
-  if (!mass || !dst_block_table || !kept_idx || !new_lens || new_lens == batch->seq_lens || !aligned(mass, 4) || !aligned(mass_out, 4) ||
-      !aligned(kept_idx, 4) || !aligned(new_lens, 4) || !aligned(dst_block_table, 4) || ld_mass < batch->max_seq_len)
+  if (!mass || !dst_block_table || !kept_idx || !new_lens || new_lens == batch->seq_lens || !aligned(mass, 4) ||
+      !aligned(mass_out, 4) || !aligned(kept_idx, 4) || !aligned(new_lens, 4) || !aligned(dst_block_table, 4) ||
+      ld_mass < batch->max_seq_len)
     return DSA_ERR_INVALID_ARG;
-  if (mass_out) {
-    if (ld_mass_out < keep) return DSA_ERR_INVALID_ARG;
-    // the totals are read while the kept ones are written: no overlap
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(mass), a1 = a0 + (uintptr_t)batch->batch * ld_mass * 4;
-    const uintptr_t b0 = reinterpret_cast<uintptr_t>(mass_out), b1 = b0 + (uintptr_t)batch->batch * ld_mass_out * 4;
-    if (a0 < b1 && b0 < a1) return DSA_ERR_INVALID_ARG;
-  }
+  // the totals are read while the kept ones are written: no overlap
+  if (mass_out && (ld_mass_out < keep || overlap(mass, ld_mass, mass_out, ld_mass_out, batch->batch)))
+    return DSA_ERR_INVALID_ARG;
+  if (too_long(batch)) return DSA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < evict_workspace_bytes(batch->batch, keep))
     return DSA_ERR_WORKSPACE;
   return launch_cache_evict(*cache, *batch, mass, ld_mass, keep, sink, recent, *dst_cache, dst_block_table,

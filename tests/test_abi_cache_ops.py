@@ -132,3 +132,17 @@ def test_binding_checks_shapes_and_types():
     with pytest.raises(ValueError):
         B._want("lse", x, (2, 96), B._F32)       # a host tensor
     assert B._want("mass_in", None, (2, 96), B._F32) is None
+
+
+def test_contexts_beyond_32_bit_tiles_and_overlapping_totals(lib):
+    far = batch(max_blocks_per_seq=1 << 25, max_seq_len=(1 << 30) + 1)
+    assert dense(lib, b=far) == B.ERR_UNSUPPORTED
+    assert evict(lib, b=far, ld=1 << 31, mo=None) == B.ERR_UNSUPPORTED
+    # a loose bound over a short table is none
+    loose = batch(max_seq_len=(1 << 31) - 1)
+    assert dense(lib, b=loose, ws=None) == B.ERR_WORKSPACE
+    assert evict(lib, b=loose, ld=1 << 31, mo=None, ws=None) == B.ERR_WORKSPACE
+    for mi in (FAKE + 4 * 900, FAKE - 4 * 900):
+        assert mass(lib, mi=mi) == B.ERR_INVALID_ARG
+    for mi in (FAKE, FAKE + 4 * 1000, FAKE - 4 * 1000):
+        assert mass(lib, mi=mi, ws=None) == B.ERR_WORKSPACE

@@ -250,6 +250,74 @@ def test_evict_long_sequences(kind):
         check_evict(case, mass, keep, sink, recent, r)
 
 
+@pytest.mark.parametrize("lens,width", [([800_001], 800_001), ([50_000] + [70, 0, 300] * 53, 50_000),
+                                        ([200_000, 7, 150_001], 720_897)])
+def test_evict_with_totals_too_many_for_shared_memory(lens, width):
+    """Contexts (or bounds) whose shares a CTA does not keep on chip: one sequence over the largest cluster, and more
+    sequences than SMs.  The table lists a few pages over and over."""
+    case = synth.make_case("evict_wide", seq_lens=[640] * len(lens), seed=30, key_format=synth.KEY_MXFP4, latent_format=NV)
+    table = np.take(case.block_table, np.arange(-(-width // 64)) % 10, axis=1)
+    case = dataclasses.replace(case, seq_lens=np.array(lens, dtype=np.int32), block_table=np.ascontiguousarray(table))
+    dc = synth.device_case(case)
+    dc.batch.max_seq_len = width
+    mass = totals(case.batch, width, "ties", 7)
+    r = evict(case, dc, mass, 1000, 9, 130)
+    assert r["status"] == 0
+    check_evict(case, mass, 1000, 9, 130, r)
+
+
+def test_two_calls_at_once():
+    """The three calls of two batches on two streams at the same time, each with its own workspaces."""
+    cases = [synth.make_case("at_once", seq_lens=[9000, 400, 2500], nq=nq, seed=31 + nq, latent_format=fmt)
+             for nq, fmt in ((1, NV), (3, FP8))]
+    steps, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for case in cases:
+        rows, keep = case.rows, 500
+        dc = synth.device_case(case)
+        rec, key = case.latent_bytes(), case.token_bytes()
+        pool = torch.zeros((24, 64 * (rec + key)), dtype=torch.uint8, device="cuda")
+        dst = binding.PagedCache(pool, pool.shape[1], 0, 64 * rec, case.key_format, case.latent_scale, case.latent_format)
+        steps.append(dict(case=case, dc=dc, dst=dst, pool=pool, keep=keep,
+                          out=torch.zeros((rows, 96, 512), dtype=torch.bfloat16, device="cuda"),
+                          lse=torch.zeros((rows, 96), device="cuda"), mass=torch.zeros((3, 9000), device="cuda"),
+                          table=torch.arange(24, dtype=torch.int32, device="cuda").view(3, 8),
+                          kept=torch.zeros((3, keep), dtype=torch.int32, device="cuda"),
+                          lens=torch.zeros(3, dtype=torch.int32, device="cuda"),
+                          st=torch.zeros(1, dtype=torch.int32, device="cuda"),
+                          w=[binding.workspace(n) for n in (binding.dense_mla_workspace_size(rows, 9000),
+                                                            binding.attention_mass_workspace_size(rows, 9000, 0),
+                                                            binding.cache_evict_workspace_size(3, 9000, keep))]))
+
+    def run(s, stream):
+        dc, scale = s["dc"], s["case"].sm_scale
+        binding.dense_mla_decode(dc.cache, dc.batch, dc.q_mla, scale, s["out"], s["lse"], s["w"][0], s["st"], stream=stream)
+        binding.attention_mass(dc.cache, dc.batch, dc.q_mla, s["lse"], scale, None, s["mass"], s["w"][1], s["st"],
+                               stream=stream)
+        binding.cache_evict(dc.cache, dc.batch, s["mass"], s["keep"], 2, 30, s["dst"], s["table"], s["kept"], None,
+                            s["lens"], s["w"][2], s["st"], stream=stream)
+
+    def results(s):
+        assert s["st"].item() == 0
+        return [s[n].clone() for n in ("out", "lse", "mass", "kept", "lens", "pool")]
+
+    alone = []
+    for s in steps:
+        run(s, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        alone.append(results(s))
+    for s in steps:
+        for n in ("out", "lse", "mass", "kept", "lens", "pool"):
+            s[n].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, stream in zip(steps, streams):
+            run(s, stream)
+    torch.cuda.synchronize()
+    for s, want in zip(steps, alone):
+        for a, b in zip(results(s), want):
+            assert torch.equal(a, b)
+
+
 def test_evict_into_spare_pages_of_the_same_pool():
     case = synth.make_case("evict_same", seq_lens=[300, 500], seed=18, spare_blocks=6)
     dc = synth.device_case(case)
