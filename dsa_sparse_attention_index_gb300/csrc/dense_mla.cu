@@ -81,7 +81,7 @@ constexpr int kOffTile = kOffQ + kQSmemBlocks * kQBlockBytes;  // 86,016
 constexpr int kOffP = kOffTile + kBufs * kTileBytes;           // 196,608
 constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
 constexpr int kOffBars = kOffAlpha + 512 + 16;
-constexpr int kNumBars = 4 * kBufs + 10;
+constexpr int kNumBars = 4 * kBufs + 11;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;              // TMEM slot, abort flag, scan scratch
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
 static_assert(kOffTile % 1024 == 0 && kOffP % 1024 == 0 && kBlkBytes % 1024 == 0, "swizzle atoms");
@@ -204,14 +204,16 @@ __device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
 }
 
 // O^T of a part from TMEM (lanes: dims of a 128-dim block, columns: heads), times
-// alpha per head, to dst [96][512] as bf16 or fp16, by the four softmax warps: each
-// turns 32 heads x 32 dims at a time in 2 KB of its own, the next 32 on the way
-// from TMEM meanwhile, and writes 64 bytes a head.
+// alpha per head, to dst [96][512] as bf16 or fp16, by sets of four warps, each set
+// the pieces [c, end) of 12 (a piece: 32 heads of a 128-dim block): a warp turns
+// 32 heads x 32 dims at a time in 2 KB of its own, the next 32 on the way from TMEM
+// meanwhile, and writes 64 bytes a head.
 template <bool kBf16>
-__device__ __forceinline__ void write_part(uint32_t lane_base, const float* alpha, uint8_t* turn, uint16_t* dst) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint16_t* col = reinterpret_cast<uint16_t*>(turn + warp * 2048) + lane;
-  const uint4* rows = reinterpret_cast<const uint4*>(turn + warp * 2048) + lane;
+__device__ __forceinline__ void write_part(int c, int end, uint32_t lane_base, const float* alpha, uint8_t* turn,
+                                           uint16_t* dst) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  uint16_t* col = reinterpret_cast<uint16_t*>(turn) + lane;
+  const uint4* rows = reinterpret_cast<const uint4*>(turn) + lane;
   uint16_t* to = dst + (lane >> 2) * kValue + warp * 32 + (lane & 3) * 8;
   auto fetch = [&](int c, uint32_t (&o)[32]) { tmem_ld32(lane_base + (c / 3) * kHeads + (c % 3) * 32, o); };
   auto put = [&](int c, const uint32_t (&o)[32]) {
@@ -249,14 +251,14 @@ __device__ __forceinline__ void write_part(uint32_t lane_base, const float* alph
     __syncwarp();
   };
   uint32_t o0[32], o1[32];
-  fetch(0, o0);
+  fetch(c, o0);
 #pragma unroll 1
-  for (int c = 0; c < 12; c += 2) {
+  for (; c < end; c += 2) {
     tmem_ld_wait();
     fetch(c + 1, o1);
     put(c, o0);
     tmem_ld_wait();
-    if (c + 2 < 12) fetch(c + 2, o0);
+    if (c + 2 < end) fetch(c + 2, o0);
     put(c + 1, o1);
   }
 }
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  pv_done = bars2 + 40;
   auto s_full = [&](uint32_t b) { return bars2 + 48 + 8 * b; };
   auto s_empty = [&](uint32_t b) { return bars2 + 64 + 8 * b; };
+  const uint32_t o_last = bars2 + 80;  // the CTA's last O^T is complete and its factors are in alpha_s
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
@@ -304,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_empty(b), 4);
     }
     mbar_init(o_free, 4);
+    mbar_init(o_last, 4);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -523,6 +527,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(full(it % kBufs, h));
       ++it;
     }
+    // The CTA's last part: eight of these warps write two thirds of it (the softmax
+    // warps alone: 21.1 instead of 19.9 us for one row of 997 tokens, 57.0 instead of
+    // 55.6 for 32 draft rows); the tile buffers are free when it is complete.
+    if (it > 0 && !have && kb < kVB && mbar_wait_warp(o_last, 0, abort_flag, p.status)) {
+      tc_fence_after();
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      uint8_t* turn = smem + kOffTile + kb * 2048;
+      const int c = 4 + 4 * h;
+      if (sg.slot < 0)
+        write_part<true>(c, c + 4, lane_base, alpha_s, turn, p.out + (int64_t)sg.row * kPartO);
+      else
+        write_part<false>(c, c + 4, lane_base, alpha_s, turn, p.opart + (int64_t)sg.slot * kPartO);
+    }
   } else if (warp < kLoadWarp0) {
     // ------------------------------------------------ softmax (thread = head) and the parts' outputs
     const int h = threadIdx.x;
@@ -652,6 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool direct = sg.slot < 0;
       alpha_s[h] = live && m_used != -INFINITY ? (direct ? p.latent_scale : 1.f) / l_sum : 0.f;
       if (bar_or_softmax(!ok)) { ok = false; break; }  // also publishes alpha_s
+      const bool last = walk.pos >= walk.hi;
+      if (last) {
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(o_last);
+      }
       tc_fence_after();
       if (live) {
         if (direct)
@@ -662,11 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // turned in the P buffer (free: every PV has completed): 2-byte stores straight
       // from the lanes took 12 us a part
-      uint8_t* turn = smem + kOffP;
+      uint8_t* turn = smem + kOffP + warp * 2048;
+      const int end = last ? 4 : 12;  // the loaders write the rest of the last part
       if (direct)
-        write_part<true>(lane_base, alpha_s, turn, p.out + (int64_t)sg.row * kPartO);
+        write_part<true>(0, end, lane_base, alpha_s, turn, p.out + (int64_t)sg.row * kPartO);
       else
-        write_part<false>(lane_base, alpha_s, turn, p.opart + (int64_t)sg.slot * kPartO);
+        write_part<false>(0, end, lane_base, alpha_s, turn, p.opart + (int64_t)sg.slot * kPartO);
       tc_fence_before();
       bar_or_softmax(false);  // alpha_s and the P buffer are free for the next part
       if (lane == 0) mbar_arrive(o_free);
