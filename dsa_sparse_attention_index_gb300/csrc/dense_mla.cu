@@ -884,7 +884,8 @@ dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt,
   // Few rows have many parts each: a CTA a head, the parts over four groups of threads; else four heads a CTA.
   // Whole call with a head and with four (us): 1 row of 60,000 tokens 54 and 80, 16 rows of 6,000 52 and 55,
   // 32 rows of 8,000 90 and 87, 128 rows of 3,500 146 and 130.
-  const bool few = rows <= 16;
+  // (one kernel whatever the batch in the batch-invariant mode: the groups' order of a row's sum differs)
+  const bool few = inv || rows <= 16;
   cfg.gridDim = dim3((unsigned)rows, (unsigned)(few ? kHeads : kHeads / 4));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

@@ -163,6 +163,26 @@ def test_dense_mla_invariant_mode():
         binding.batch_invariant(prev)
 
 
+def test_dense_mla_invariant_mode_over_the_batch_size():
+    """Bit for bit the same row alone, among a few and among many, with several parts a row."""
+    case = synth.make_case("dense_inv", seq_lens=[20000, 12000, 3841], seed=33, latent_format=NV)
+    try:
+        binding.batch_invariant(True)
+        alone = run_dense(case, synth.device_case(case))
+        assert alone[2] == 0
+        for copies in (6, 30):
+            many = dataclasses.replace(case, batch=3 * copies, q_mla=np.tile(case.q_mla, (copies, 1, 1)),
+                                       seq_lens=np.tile(case.seq_lens, copies),
+                                       block_table=np.tile(case.block_table, (copies, 1)))
+            dc = synth.device_case(many)
+            out, lse, st = run_dense(many, dc)
+            assert st == 0
+            for i in range(copies):
+                assert torch.equal(out[3 * i:3 * i + 3], alone[0]) and torch.equal(lse[3 * i:3 * i + 3], alone[1]), i
+    finally:
+        binding.batch_invariant(False)
+
+
 def test_dense_mla_bad_page_is_reported():
     case = synth.make_case("dense_bad", seq_lens=[500, 300], seed=12)
     for bad in (case.num_blocks, -1, 1 << 30):
