@@ -72,7 +72,6 @@ constexpr int kQ8Col = kSCol + 2 * kTile;              // 480..511
 static_assert(kQ8Col + 32 * kQTmemBlocks <= 512, "TMEM columns");
 constexpr float kRescaleThreshold = 8.0f;              // log2 units
 constexpr float kPShift = 7.0f;                        // P is stored times 2^7, at most 2^15
-constexpr int kMinTiles = 2;                           // tiles per CTA before more CTAs are used
 constexpr int kMaxGrid = 256;                          // CTAs the workspace is sized for
 constexpr int kInvariantTiles = 80;                    // tiles per part in the batch-invariant mode
 
@@ -195,7 +194,7 @@ __device__ Walk make_walk(const DenseParams& p, int64_t* scratch) {
       p.row_info[r] = make_int2((int)c0, n == 0 ? 0 : (int)((first + n - 1) / per - c0 + 1));
     }
   };
-  const Run run = find_run<kThreads>(p.rows, kMinTiles, p.unit ? 1 : 0, scratch, count, each);
+  const Run run = find_run<kThreads>(p.rows, p.unit ? 1 : 0, scratch, count, each);
   w.row = run.row;
   w.start = run.start;
   w.pos = run.pos;
@@ -702,22 +701,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kQkWarp) tmem_dealloc(tmem, 512);
 }
 
-// Merge the parts of the rows that crossed CTAs, and fill the rows that see no
-// token.  CTA (row, group): kHpc heads, 64 threads (8 dims each) a head, and
-// 4 / kHpc groups of threads that take every such part, joined in a fixed order.
-template <int kHpc>
-__global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __restrict__ opart,
-                                                            const float* __restrict__ ml,
-                                                            const int2* __restrict__ row_info, int inv,
-                                                            float latent_scale, uint16_t* out, float* lse) {
-  constexpr int kGroups = 4 / kHpc;
+// 16 bytes, loaded where it is written: the compiler otherwise puts a round's loads
+// behind one another to save registers (four rows of 20,000 tokens: 47.7 instead of
+// 44.9 us; with one group, at two parts a row, the free order is as fast).
+__device__ __forceinline__ uint4 ld_now(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Merge the parts of a row that crossed CTAs, or fill a row that sees no token:
+// kHpc heads a CTA, 64 threads (8 dims each) a head, and kGroups groups of threads
+// that take every such part, joined in a fixed order.
+template <int kHpc, int kGroups>
+__device__ __forceinline__ void combine_row(int row, const uint16_t* __restrict__ opart, const float* __restrict__ ml,
+                                            int2 info, int inv, float latent_scale, uint16_t* out, float* lse) {
   __shared__ float acc_s[kGroups > 1 ? kGroups - 1 : 1][64][8];
-  grid_dep_wait();  // the parts come from the previous kernel
-  const int row = blockIdx.x, w = threadIdx.x >> 6, th = threadIdx.x & 63;
+  const int w = threadIdx.x >> 6, th = threadIdx.x & 63;
   const int h = blockIdx.y * kHpc + w % kHpc, grp = w / kHpc;
-  const int2 info = row_info[row];
   const int parts = info.y;
-  if (parts == 1) return;
   uint16_t* dst = out + ((int64_t)row * kHeads + h) * kValue + th * 8;
   if (parts == 0) {
     if (grp == 0) {
@@ -753,7 +755,11 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
       if (s < parts) {
         const int64_t slot = slot_of(s);
         v[u] = ml2[slot * kHeads + h];
-        x[u] = *reinterpret_cast<const uint4*>(opart + (slot * kHeads + h) * kValue + th * 8);
+        const uint16_t* from = opart + (slot * kHeads + h) * kValue + th * 8;
+        if (kGroups > 1)
+          x[u] = ld_now(from);
+        else
+          x[u] = *reinterpret_cast<const uint4*>(from);
       }
     }
 #pragma unroll
@@ -797,14 +803,25 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const uint16_t* __re
   if (th == 0) lse[(int64_t)row * kHeads + h] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
 }
 
+template <int kHpc, int kGroups>
+__global__ void __launch_bounds__(64 * kHpc * kGroups) dense_combine_kernel(
+    const uint16_t* __restrict__ opart, const float* __restrict__ ml, const int2* __restrict__ row_info, int inv,
+    float latent_scale, uint16_t* out, float* lse) {
+  grid_dep_wait();  // the parts come from the previous kernel
+  const int row = blockIdx.x;
+  const int2 info = row_info[row];
+  if (info.y == 1) return;  // written already
+  combine_row<kHpc, kGroups>(row, opart, ml, info, inv, latent_scale, out, lse);
+}
+
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-int64_t max_tiles(int rows, int max_len) { return (int64_t)rows * ((std::max(max_len, 0) + kTile - 1) / kTile); }
+int64_t max_tiles(int rows, int max_len) { return (int64_t)rows * (((int64_t)std::max(max_len, 0) + kTile - 1) / kTile); }
 
 // Partial slots for `rows` rows of at most max_len tokens.
 int64_t dense_slots(int rows, int max_len, bool inv) {
   if (inv) {
-    const int64_t tiles = (std::max(max_len, 0) + kTile - 1) / kTile;
+    const int64_t tiles = max_tiles(1, max_len);
     return std::max<int64_t>(1, rows * ((tiles + kInvariantTiles - 1) / kInvariantTiles));
   }
   return 2 * std::max<int64_t>(1, std::min<int64_t>(kMaxGrid, max_tiles(rows, max_len)));
@@ -881,18 +898,20 @@ dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt,
   count_launches(1);
   if (cuda_status(cudaLaunchKernelEx(&cfg, nv ? dense_mla_kernel<true> : dense_mla_kernel<false>, qmap, p)) != DSA_OK)
     return DSA_ERR_CUDA;
-  // Few rows have many parts each: a CTA a head, the parts over four groups of threads; else four heads a CTA.
-  // Whole call with a head and with four (us): 1 row of 60,000 tokens 54 and 80, 16 rows of 6,000 52 and 55,
-  // 32 rows of 8,000 90 and 87, 128 rows of 3,500 146 and 130.
-  // (one kernel whatever the batch in the batch-invariant mode: the groups' order of a row's sum differs)
-  const bool few = inv || rows <= 16;
-  cfg.gridDim = dim3((unsigned)rows, (unsigned)(few ? kHeads : kHeads / 4));
-  cfg.blockDim = dim3(256);
+  // Few rows have many parts each: a CTA a head, the parts over 16 or 4 groups of threads; else four heads a CTA.
+  // The whole call with 16 groups, 4 groups and four heads, us: one row of 60,000 tokens 36, 54 and 80; two of 3,000
+  // 25 and 29; four of 20,000 50 and 49; 16 of 6,000 71, 51 and 55; 32 of 8,000: 4 groups 90, four heads 87.
+  // The groups' order of a row's sum differs, so the batch-invariant mode takes one whatever the batch.
+  const bool wide = !inv && rows <= 2, one = inv || rows <= 16;
+  auto combine = wide  ? dense_combine_kernel<1, 16>
+                 : one ? dense_combine_kernel<1, 4>
+                       : dense_combine_kernel<4, 1>;
+  cfg.gridDim = dim3((unsigned)rows, (unsigned)(one ? kHeads : kHeads / 4));
+  cfg.blockDim = dim3(wide ? 1024 : 256);
   cfg.dynamicSmemBytes = 0;
   count_launches(1);
-  if (cuda_status(cudaLaunchKernelEx(&cfg, few ? dense_combine_kernel<1> : dense_combine_kernel<4>,
-                                     (const uint16_t*)p.opart, (const float*)p.ml, (const int2*)p.row_info, inv ? 1 : 0,
-                                     c.latent_scale, out, lse)) != DSA_OK)
+  if (cuda_status(cudaLaunchKernelEx(&cfg, combine, (const uint16_t*)p.opart, (const float*)p.ml,
+                                     (const int2*)p.row_info, inv ? 1 : 0, c.latent_scale, out, lse)) != DSA_OK)
     return DSA_ERR_CUDA;
   return launch_status();
 }

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Tiles tiles{p, 0, -1, 0, 0, 0};
   {
     const Run run = find_run<kThreads>(
-        p.rows, 1, 0, scratch, [&](int r) -> int64_t { return (tiles.items(r) + kTok - 1) / kTok; },
+        p.rows, 0, scratch, [&](int r) -> int64_t { return (tiles.items(r) + kTok - 1) / kTok; },
         [](int, int64_t, int64_t, int64_t) {});
     tiles.row = run.row;
     tiles.start = run.start;

@@ -14,12 +14,12 @@ struct Run {
   int64_t start;     // that row's first item
 };
 
-// By all kThreads threads of the CTA: count(r) items of row r; at least
-// min_items a CTA (fixed_per > 0: exactly that many, and hi is the line's end).
+// By all kThreads threads of the CTA: count(r) items of row r
+// (fixed_per > 0: that many a CTA, and hi is the line's end).
 // each(r, first, n, per) is called once for every row by CTA 0.  `scratch`: 32
 // int64 of shared memory.
 template <int kThreads, class Count, class Each>
-__device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, int64_t* scratch, Count count, Each each) {
+__device__ __forceinline__ Run find_run(int rows, int fixed_per, int64_t* scratch, Count count, Each each) {
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps <= 30, "scratch");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -39,7 +39,7 @@ __device__ __forceinline__ Run find_run(int rows, int min_items, int fixed_per, 
   int64_t per = 0;
   auto place = [&]() {
     const int64_t even = (total + gridDim.x - 1) / (int64_t)gridDim.x;
-    per = fixed_per ? fixed_per : (even > min_items ? even : min_items);
+    per = fixed_per ? fixed_per : (even > 1 ? even : 1);
     w.pos = (int64_t)blockIdx.x * per;
     w.hi = fixed_per ? total : (w.pos + per < total ? w.pos + per : total);
   };

@@ -142,6 +142,8 @@ def test_contexts_beyond_32_bit_tiles_and_overlapping_totals(lib):
     loose = batch(max_seq_len=(1 << 31) - 1)
     assert dense(lib, b=loose, ws=None) == B.ERR_WORKSPACE
     assert evict(lib, b=loose, ld=1 << 31, mo=None, ws=None) == B.ERR_WORKSPACE
+    for rows in (1, 3):   # and takes as many partial results as any long one
+        assert lib.dense_mla_workspace_size(rows, (1 << 31) - 1) == lib.dense_mla_workspace_size(rows, 1 << 20)
     for mi in (FAKE + 4 * 900, FAKE - 4 * 900):
         assert mass(lib, mi=mi) == B.ERR_INVALID_ARG
     for mi in (FAKE, FAKE + 4 * 1000, FAKE - 4 * 1000):
