@@ -154,10 +154,10 @@ _I32, _F32 = (torch.int32,), (torch.float32,)
 
 
 def _want(name: str, t, shape, dtypes) -> int | None:
-    """The address of a tensor that must have this shape (-1: any size from 1) and one of these types, or of None."""
+    """The address of a tensor that must have this shape and one of these types, or of None."""
     if t is None:
         return None
-    if t.dtype not in dtypes or len(t.shape) != len(shape) or any(w != n and w != -1 for w, n in zip(shape, t.shape)):
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {list(shape)} of {dtypes[0]}, got {list(t.shape)} of {t.dtype}")
     return _ptr(t)
 
@@ -166,7 +166,7 @@ def _one_device(*tensors) -> None:
     """Every tensor on the current device: the library launches there."""
     at = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != at:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"tensors must be on the current device (cuda:{at}), got {t.device}")
 
 
@@ -297,7 +297,7 @@ def dense_mla_decode(cache: PagedCache, batch: Batch, q_mla, sm_scale: float, ou
                                   _want("q_mla", q_mla, (rows, MLA_HEADS, LATENT), _BITS16), float(sm_scale),
                                   _want("out", out, (rows, MLA_HEADS, VALUE), _BITS16),
                                   _want("lse", lse, (rows, MLA_HEADS), _F32), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
+                                  workspace.nbytes, _ptr(status), _stream(stream)),
            "dense_mla_decode")
 
 
@@ -311,14 +311,14 @@ def attention_mass(cache: PagedCache, batch: Batch, q_mla, lse, sm_scale: float,
     fp32 [batch, ld]; over every visible token, or over the top-k's entries when idx (int32 [rows, k]) is given."""
     c, b, rows = cache.struct(), batch.struct(), batch.rows
     _one_device(cache.pool, batch.block_table, batch.seq_lens, q_mla, lse, mass_in, mass_out, workspace, status, idx)
-    out = _want("mass_out", mass_out, (batch.batch, -1), _F32)
+    ld, k = mass_out.shape[-1], 0 if idx is None else idx.shape[-1]
+    totals = (batch.batch, ld)
     _check(lib().dsa_attention_mass(ctypes.byref(c), ctypes.byref(b),
                                     _want("q_mla", q_mla, (rows, MLA_HEADS, LATENT), _BITS16),
-                                    _want("lse", lse, (rows, MLA_HEADS), _F32), _want("idx", idx, (rows, -1), _I32),
-                                    int(idx.shape[1]) if idx is not None else 0, float(sm_scale),
-                                    _want("mass_in", mass_in, tuple(mass_out.shape), _F32), out,
-                                    int(mass_out.shape[1]), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _ptr(status), _stream(stream)), "dsa_attention_mass")
+                                    _want("lse", lse, (rows, MLA_HEADS), _F32), _want("idx", idx, (rows, k), _I32), k,
+                                    float(sm_scale), _want("mass_in", mass_in, totals, _F32),
+                                    _want("mass_out", mass_out, totals, _F32), ld, _ptr(workspace),
+                                    workspace.nbytes, _ptr(status), _stream(stream)), "dsa_attention_mass")
 
 
 def cache_evict_workspace_size(batch: int, max_seq_len: int, keep: int) -> int:
@@ -331,16 +331,16 @@ def cache_evict(cache: PagedCache, batch: Batch, mass, keep: int, sink: int, rec
     their records into the pages of dst_block_table.  kept_idx int32 [batch, keep], mass_out fp32 [batch, >= keep]
     or None, new_lens int32 [batch]."""
     c, b, d, n = cache.struct(), batch.struct(), dst_cache.struct(), batch.batch
+    ld, blocks, ld_out = mass.shape[-1], dst_block_table.shape[-1], 0 if mass_out is None else mass_out.shape[-1]
     _one_device(cache.pool, batch.block_table, batch.seq_lens, mass, dst_cache.pool, dst_block_table, kept_idx, mass_out,
                 new_lens, workspace, status)
-    _check(lib().dsa_cache_evict(ctypes.byref(c), ctypes.byref(b), _want("mass", mass, (n, -1), _F32),
-                                 int(mass.shape[1]), int(keep), int(sink), int(recent), ctypes.byref(d),
-                                 _want("dst_block_table", dst_block_table, (n, -1), _I32), int(dst_block_table.shape[1]),
+    _check(lib().dsa_cache_evict(ctypes.byref(c), ctypes.byref(b), _want("mass", mass, (n, ld), _F32),
+                                 ld, int(keep), int(sink), int(recent), ctypes.byref(d),
+                                 _want("dst_block_table", dst_block_table, (n, blocks), _I32), blocks,
                                  _want("kept_idx", kept_idx, (n, int(keep)), _I32),
-                                 _want("mass_out", mass_out, (n, -1), _F32),
-                                 int(mass_out.shape[1]) if mass_out is not None else 0,
+                                 _want("mass_out", mass_out, (n, ld_out), _F32), ld_out,
                                  _want("new_lens", new_lens, (n,), _I32), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
+                                 workspace.nbytes, _ptr(status), _stream(stream)),
            "dsa_cache_evict")
 
 
