@@ -36,7 +36,7 @@
 // (4 KB of Q + 1.5 KB of keys) + 4 x 1.5 KB, PV 12 x (4 KB of values + 3 KB of
 // P)) and its stores and polls take about 85 KB: 2,800 cycles at 128 B a cycle,
 // of which the measured 1.6 us use 88 % (32 contexts of 8K to 64K tokens, NVFP4:
-// 276 us, 893 TFLOP/s, 0.47 of the measured bf16 burst rate).  The tensor pipe is
+// 272 us, 906 TFLOP/s, 0.47 of the measured bf16 burst rate).  The tensor pipe is
 // active 47 % of the time.
 #include <algorithm>
 #include <atomic>

@@ -2,7 +2,7 @@
 // widened to fp16 (dense_mla.cu, mass.cu).
 //
 // bf16 reaches further than fp16, so a row's 96 x 576 values are multiplied by
-// one power of two 2^e that brings its largest magnitude into [2^14, 2^15); the
+// one power of two 2^e that brings the largest finite one into [2^14, 2^15); the
 // kernels multiply the logits by 2^-e.  bf16's 8 significant bits fit fp16's 11
 // down to 2^-28 of the row's largest value, and what lies below loses at most
 // 2^-39 of it: far below the error of the fp32 sums it goes into.
