@@ -853,7 +853,7 @@ dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt,
   }
   uint16_t* q16 = nullptr;
   float* q_inv = nullptr;
-  if (launch_query_f16(q_mla, rows, workspace, &q16, &q_inv, st) != DSA_OK) return DSA_ERR_CUDA;
+  if (launch_query_f16(q_mla, nullptr, rows, workspace, &q16, &q_inv, st) != DSA_OK) return DSA_ERR_CUDA;
   CUtensorMap qmap;
   const uint64_t dims[2] = {(uint64_t)kLatent, (uint64_t)rows * kHeads};
   const uint64_t strides[1] = {(uint64_t)kLatent * 2};

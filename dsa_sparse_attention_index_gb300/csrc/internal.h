@@ -96,7 +96,8 @@ dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt
 // The rows' queries as fp16 times a power of two, and its inverse per row, in
 // `workspace` (query_f16_bytes(rows) bytes, 256-byte aligned; query.cu).
 size_t query_f16_bytes(int rows);
-dsa_status_t launch_query_f16(const uint16_t* q, int rows, void* workspace, uint16_t** q16, float** inv, cudaStream_t st);
+dsa_status_t launch_query_f16(const uint16_t* q, const float* lse, int rows, void* workspace, uint16_t** q16,
+                              float** inv, cudaStream_t st);
 // Attention over every visible token (dense_mla.cu).
 size_t dense_mla_workspace_bytes(int rows, int max_len);
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,

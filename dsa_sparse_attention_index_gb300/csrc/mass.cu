@@ -511,7 +511,7 @@ dsa_status_t launch_attention_mass(const dsa_paged_cache_t& c, const dsa_batch_t
   }
   uint16_t* q16 = nullptr;
   float* q_inv = nullptr;
-  if (launch_query_f16(q_mla, rows, workspace, &q16, &q_inv, st) != DSA_OK) return DSA_ERR_CUDA;
+  if (launch_query_f16(q_mla, lse, rows, workspace, &q16, &q_inv, st) != DSA_OK) return DSA_ERR_CUDA;
   CUtensorMap qmap;
   const uint64_t dims[2] = {(uint64_t)kLatent, (uint64_t)rows * kHeads};
   const uint64_t strides[1] = {(uint64_t)kLatent * 2};

@@ -7,6 +7,9 @@
 // down to 2^-28 of the row's largest value, and what lies below loses at most
 // 2^-39 of it: far below the error of the fp32 sums it goes into.
 //
+// For the attention weights a head whose LSE is -inf (it attended to nothing) counts
+// as zeros, so that NaN or infinities in a masked row's query stay out of the sums.
+//
 // One CTA a row, nine 16-byte pieces a thread, all loaded before the maximum is
 // taken; the kernel that follows sets itself up meanwhile.  (Converting inside
 // that kernel cost its softmax warps 5 us for every row a CTA touched.)
@@ -21,8 +24,9 @@ constexpr int kPieces = 9;
 constexpr int kThreads = kHeads * kLatent / 8 / kPieces;  // 768
 static_assert(kThreads * kPieces * 8 == kHeads * kLatent && kThreads % 32 == 0, "pieces");
 
-__global__ void __launch_bounds__(kThreads) query_f16_kernel(const uint4* __restrict__ q, uint4* __restrict__ out,
-                                                             float* __restrict__ inv) {
+__global__ void __launch_bounds__(kThreads) query_f16_kernel(const uint4* __restrict__ q,
+                                                             const float* __restrict__ lse,  // or null
+                                                             uint4* __restrict__ out, float* __restrict__ inv) {
   __shared__ uint32_t max_s[kThreads / 32];
   grid_dep_wait();    // the queries may come from the previous kernel
   grid_dep_launch();  // so what the next one reads before its own wait is in place too
@@ -30,6 +34,12 @@ __global__ void __launch_bounds__(kThreads) query_f16_kernel(const uint4* __rest
   uint4 v[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) v[i] = q[base + i * kThreads + threadIdx.x];
+  if (lse) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (lse[blockIdx.x * (int64_t)kHeads + (i * kThreads + threadIdx.x) / (kLatent / 8)] == -INFINITY)
+        v[i] = make_uint4(0, 0, 0, 0);
+  }
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i)
@@ -55,7 +65,8 @@ size_t query_f16_bytes(int rows) {
   return al((size_t)rows * kHeads * kLatent * 2) + al((size_t)rows * 4);
 }
 
-dsa_status_t launch_query_f16(const uint16_t* q, int rows, void* workspace, uint16_t** q16, float** inv, cudaStream_t st) {
+dsa_status_t launch_query_f16(const uint16_t* q, const float* lse, int rows, void* workspace, uint16_t** q16,
+                              float** inv, cudaStream_t st) {
   *q16 = static_cast<uint16_t*>(workspace);
   *inv = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                   (((size_t)rows * kHeads * kLatent * 2 + 255) & ~size_t(255)));
@@ -69,7 +80,7 @@ dsa_status_t launch_query_f16(const uint16_t* q, int rows, void* workspace, uint
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   count_launches(1);
-  return cuda_status(cudaLaunchKernelEx(&cfg, query_f16_kernel, reinterpret_cast<const uint4*>(q),
+  return cuda_status(cudaLaunchKernelEx(&cfg, query_f16_kernel, reinterpret_cast<const uint4*>(q), lse,
                                         reinterpret_cast<uint4*>(*q16), *inv));
 }
 

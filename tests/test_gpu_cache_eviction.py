@@ -123,6 +123,23 @@ def test_mass_without_a_total_and_with_empty_rows():
         assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L])
 
 
+@pytest.mark.parametrize("fmt", [FP8, NV])
+def test_mass_keeps_masked_queries_out(fmt):
+    """NaN and infinities in the query of a row, or of one head, whose LSE is -inf add nothing and disturb nothing."""
+    case = synth.make_case("mass_masked", seq_lens=[300, 200], nq=2, seed=34, latent_format=fmt)
+    lse = plain_lse(case)
+    lse[1] = lse[2, 7] = lse[2, 95] = -float("inf")
+    none = lse.masked_fill(torch.isneginf(lse), 1e30)   # whose weights vanish in the plain form
+    want, tol = plain_mass(case, torch.zeros((2, case.max_len + 3)), none)
+    q = case.q_mla.copy()
+    q[1, ::2], q[1, 1::2], q[2, 7], q[2, 95, 575] = 0x7FC0, 0xFF80, 0x7F80, 0x7FC0
+    masked = dataclasses.replace(case, q_mla=q)
+    got, st = run_mass(masked, synth.device_case(masked), lse, None)
+    assert st == 0
+    for b, L in enumerate([300, 200]):
+        assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L])
+
+
 def test_mass_reports_bad_entries_and_pages():
     case = synth.make_case("mass_bad", seq_lens=[500], seed=15)
     lse = torch.zeros((1, 96))
