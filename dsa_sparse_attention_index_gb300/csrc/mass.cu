@@ -31,8 +31,8 @@
 // selected ones: a CTA owns 4,096 tokens of a sequence in shared memory).
 // What bounds it: issue and latency in the converters and the MMA issuer (per
 // tile about 7,700 warp instructions, 42 % of the issue slots; the tensor pipe is
-// active 37 % of the time).  16 contexts of 16K to 64K tokens, NVFP4: 87 us, 834
-// TFLOP/s, 2.7 TB/s; 64 rows of one 32,770-token context: 249 us, 928 TFLOP/s.
+// active 37 % of the time).  16 contexts of 16K to 64K tokens, NVFP4: 89 us, 815
+// TFLOP/s, 2.6 TB/s; 64 rows of one 32,770-token context: 251 us, 921 TFLOP/s.
 #include <algorithm>
 #include <atomic>
 
