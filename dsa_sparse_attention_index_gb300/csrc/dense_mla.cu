@@ -594,8 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i)
             mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[j + 2 * i])), __uint_as_float(r[j + 2 * i + 1]));
         const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c_log2;
-        const float first = __uint_as_float(r[0]);
-        if (first != first) m_used = first;  // NaN logits (a NaN in the query) give a NaN row
+        // Every tile has a token.  A maximum of -inf is that of logits that are all -inf or NaN (fmaxf drops
+        // NaN): an infinity or a NaN in the head's query, which gives a NaN row
+        if (m_tile == -INFINITY) m_used = __int_as_float(0x7FC00000);
         const bool grow = live && m_tile > m_used + kRescaleThreshold;
         // one barrier a tile: any head that grew, and any warp whose wait ran out
         if (bar_or_softmax(grow || !ok)) {

@@ -1,0 +1,98 @@
+"""dense_mla_decode and dsa_attention_mass where single heads, rows, pages or
+entries are out of the ordinary: what is wrong with one of them stays there.
+
+Tolerance of the attention, from the roundings on the way (half a step of bf16
+is 2^-8 relative, of fp16 2^-11, of fp32 2^-24; p is normalised, sums over the
+row's n tokens):
+  logits   fp32 sums of 576 exact products and the scaled argument of the
+           exponential, 576 * 2^-24 * Sum |q c| * sm_scale =: e; they move the
+           quotient by at most 2 e * Sum p |v|
+  P        fp16 in the numerator only, 2^-11 * Sum p |v|; below 2^-14 its step is
+           fixed, half of it 2^-25 against a normaliser of at least 2^7 (the
+           largest weight is stored as 2^7 or more): 2^-32 * Sum |v|
+  sums     fp32, n * 2^-24 * Sum p |v| for the values and as much for the normaliser
+  parts    fp16, 2^-11 * Sum p |v|, and 2^-25 of a latent unit below 2^-14
+  output   bf16, 2^-8 of the computed value
+  LSE      e + n * 2^-24 + 2^-20 * (1 + |lse|)
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import plain64
+from dsa_sparse_attention_index_gb300 import binding, synth
+from test_gpu_cache_eviction import plain_lse, plain_mass, run_mass
+from test_gpu_dense_mla import run_dense
+
+pytestmark = pytest.mark.gpu
+
+FP8, NV = synth.LATENT_FP8, synth.LATENT_NVFP4
+HEAD = 5   # the head that is out of the ordinary
+
+
+def bf16_bits(x):
+    return x.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+
+
+def check(case, out, lse, heads=None, rows=None, tokens=None):
+    """Rows of the attention against 64 bits; tokens(row) lists what a row attends to (None: all it sees)."""
+    heads = torch.arange(96) if heads is None else torch.as_tensor(heads)
+    o, l = out.double().cpu(), lse.double().cpu()
+    cached = {}
+    for row in range(case.rows) if rows is None else rows:
+        b = row // case.nq
+        if b not in cached:
+            cached = {b: plain64.latents(case, b)}
+        vis = max(0, int(case.seq_lens[b]) - (case.nq - 1) + row % case.nq)
+        see = torch.arange(vis) if tokens is None else tokens(row)
+        n = len(see)
+        if n == 0:
+            assert torch.all(o[row] == 0) and torch.all(torch.isneginf(l[row])), row
+            continue
+        ro, rl, av, _, bound = plain64.attend(case, row, see, c=cached[b])
+        sum_v = cached[b][see][:, :512].abs().sum(0)[None, :]
+        e = (576 * 2.0 ** -24 * bound)[:, None]
+        err = ((2 * e + 2 * n * 2.0 ** -24 + 2 * 2.0 ** -11) * av + 2.0 ** -32 * sum_v
+               + 2.0 ** -25 * case.latent_scale)
+        tol = err + 2.0 ** -8 * (ro.abs() + err)
+        bad = ((o[row] - ro).abs() - tol)[heads]
+        assert not torch.isnan(bad).any() and bad.max().item() <= 0, f"row {row}, {n} tokens: out off by {bad.max().item()}"
+        ltol = e[:, 0] + n * 2.0 ** -24 + 2.0 ** -20 * (1 + rl.abs())
+        assert torch.all(((l[row] - rl).abs() <= ltol)[heads]), f"row {row}: lse"
+
+
+OTHERS = [h for h in range(96) if h != HEAD]
+
+
+# ---------------------------------------------------------------- infinities and NaN
+def constant_dim(case, kind):
+    """Latent dimension 550 (E4M3 in either format) of every token: 1.0; "first": 1.0 in each tile's first token
+    and 0 in the others."""
+    rec = case.latent_bytes()
+    pool = case.pool.copy()
+    at = case.latent_off + (550 if rec == 576 else 288 + 550 - 512)
+    for b in range(case.batch):
+        for t in range(int(case.seq_lens[b])):
+            one = kind == "same" or t % 48 == 0
+            pool[case.block_table[b, t // 64], at + t % 64 * rec] = 0x38 if one else 0
+    return dataclasses.replace(case, pool=pool)
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("kind", ["same", "first"])
+@pytest.mark.parametrize("bits,sign", [(0x7F80, 1), (0xFF80, 1), (0x7F80, -1), (0xFF80, -1), (0x7FC0, 1)])
+def test_dense_infinite_query_whose_products_share_a_sign(fmt, kind, bits, sign):
+    """inf - inf is NaN whatever the sign: one token, one tile, several tiles and several parts."""
+    lens = [1, 2, 48, 60, 7000]
+    case = constant_dim(synth.make_case("edge_inf", seq_lens=lens, seed=501, latent_format=fmt), kind)
+    q = case.q_mla.copy()
+    q[:, HEAD, 550] = bits
+    case = dataclasses.replace(case, q_mla=q, sm_scale=sign * case.sm_scale)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    assert bool(torch.isnan(out[:, HEAD].float()).all()) and bool(torch.isnan(lse[:, HEAD]).all())
+    clean = case.q_mla.copy()
+    clean[:, HEAD, 550] = 0
+    check(dataclasses.replace(case, q_mla=clean), out, lse, heads=OTHERS)
