@@ -550,8 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- Q dims 512..575 of head h into TMEM (every QK^T of the previous part has completed)
       // logits in log2 units per unit of S
       const float c_raw = p.logit_scale_log2 * p.q_inv[sg.row];
-      // its magnitude; a scale of 0 becomes one that still sends a masked token's -inf to -inf
-      const float c_log2 = fmaxf(fabsf(c_raw), 1e-38f);
+      // its magnitude; a scale of 0 becomes one that still sends a masked token's -inf to -inf, and one that
+      // is no number makes every logit NaN
+      const float c_log2 = fabsf(c_raw) < INFINITY ? fmaxf(fabsf(c_raw), 1e-38f) : __int_as_float(0x7FC00000);
       {
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q16 + ((int64_t)sg.row * kHeads + (live ? h : 0)) * kLatent + 64 * kQSmemBlocks);
@@ -595,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[j + 2 * i])), __uint_as_float(r[j + 2 * i + 1]));
         const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c_log2;
         // Every tile has a token.  A maximum of -inf is that of logits that are all -inf or NaN (fmaxf drops
-        // NaN): an infinity or a NaN in the head's query, which gives a NaN row
-        if (m_tile == -INFINITY) m_used = __int_as_float(0x7FC00000);
+        // NaN).  That, a NaN and +inf come from a query, a scale or a logit that is no fp32 number: a NaN row
+        if (!(fabsf(m_tile) < INFINITY)) m_used = __int_as_float(0x7FC00000);
         const bool grow = live && m_tile > m_used + kRescaleThreshold;
         // one barrier a tile: any head that grew, and any warp whose wait ran out
         if (bar_or_softmax(grow || !ok)) {

@@ -307,9 +307,10 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
  *   out[r][h] = sum_t softmax(l)_t * c_t[0:512]        (bf16, round-to-nearest)
  *   lse[r][h] = ln sum_t exp(l_t)                       (fp32)
  * A row that sees no token gets out = 0 and lse = -inf; a NaN or an infinity in a
- * head's query gives that head NaN.  A length above min(max_blocks_per_seq * 64,
- * max_seq_len) is read as that bound, a negative one as 0; a bound above 2^30 is
- * DSA_ERR_UNSUPPORTED.  Any number of rows per sequence up to DSA_MAX_QUERIES_PER_SEQ.
+ * head's query or in the scale, or a largest logit beyond fp32, gives that head NaN.
+ * A length above min(max_blocks_per_seq * 64, max_seq_len) is read as that bound, a
+ * negative one as 0; a bound above 2^30 is DSA_ERR_UNSUPPORTED.  Any number of rows
+ * per sequence up to DSA_MAX_QUERIES_PER_SEQ.
  *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned
  *   out       device bf16 bits [rows][96][512], 8-byte aligned;  lse device fp32 [rows][96]
  *   workspace >= dense_mla_workspace_size(rows, batch->max_seq_len) bytes, 256-B aligned

@@ -96,3 +96,14 @@ def test_dense_infinite_query_whose_products_share_a_sign(fmt, kind, bits, sign)
     clean = case.q_mla.copy()
     clean[:, HEAD, 550] = 0
     check(dataclasses.replace(case, q_mla=clean), out, lse, heads=OTHERS)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_dense_scale_that_is_no_number(scale):
+    """NaN for every row that sees a token; a row that sees none stays as documented."""
+    case = dataclasses.replace(synth.make_case("edge_scale", seq_lens=[300, 0, 1], seed=502, latent_format=NV), sm_scale=scale)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    for row in (0, 2):
+        assert bool(torch.isnan(out[row].float()).all()) and bool(torch.isnan(lse[row]).all())
+    assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
