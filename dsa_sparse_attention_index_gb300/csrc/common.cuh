@@ -456,19 +456,19 @@ __device__ __forceinline__ void nvfp4x16_to_f16x16(uint32_t w0, uint32_t w1, uin
     for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d[i]) : "r"(s2));
   }
 }
-// bf16 queries as fp16 times 2^e, with e such that the largest magnitude lands in
-// [2^14, 2^15).
 // The larger finite magnitude (as integers) of each 16-bit half; infinities and
 // NaN, which no power of two brings into range, count as 0.
 __device__ __forceinline__ uint32_t bf16x2_abs_max(uint32_t a, uint32_t b) {
   const uint32_t m = b & 0x7FFF7FFFu;
   return __vmaxu2(a, m & ~__vcmpgeu2(m, 0x7F807F80u));
 }
+// e of the power of two that brings the largest magnitude into [2^14, 2^15).
 __device__ __forceinline__ int f16_shift_of(uint32_t abs_max2) {
   const uint32_t m = max(abs_max2 & 0xFFFFu, abs_max2 >> 16);
   const int e = (int)(m >> 7);  // bf16's exponent field
   return max(-126, min(126, 14 + 127 - e));
 }
+// Two bf16 times 2^e (`scale`) as fp16.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
   const float lo = __uint_as_float(v << 16) * scale, hi = __uint_as_float(v & 0xFFFF0000u) * scale;
   const __half2 h = __floats2half2_rn(lo, hi);

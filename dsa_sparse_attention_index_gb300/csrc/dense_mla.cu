@@ -18,7 +18,7 @@
 //   * Operands are fp16, not bf16: E4M3 values and E2M1 x E4M3 products are exact
 //     in it, the conversion instructions widen to it in a third of the
 //     instructions that bf16 takes, and P keeps 11 bits.  query.cu turns Q into
-//     fp16 times a power of two.
+//     fp16 times a power of two a head.
 //   * warps 4..12, one per 64-dim block: two lanes a token, 16-byte loads a whole
 //     tile ahead in registers, a token's page looked up two tiles ahead; widened,
 //     stored 128-byte swizzled into one of two tile buffers, which are filled and
@@ -98,8 +98,8 @@ struct DenseParams {
   int32_t nq, cap, rows;
   float logit_scale_log2;  // sm_scale * latent_scale * log2(e)
   float latent_scale;
-  const uint16_t* q16;     // the queries in fp16 times a power of two a row
-  const float* q_inv;      // its inverse, [rows]
+  const uint16_t* q16;     // the queries in fp16 times a power of two a head
+  const float* q_inv;      // its inverse, [rows][96]
   uint16_t* out;
   float* lse;
   uint16_t* opart;  // fp16 [slots][96][512]
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(sg)) {
       // ---- Q dims 512..575 of head h into TMEM (every QK^T of the previous part has completed)
       // logits in log2 units per unit of S
-      const float c_raw = p.logit_scale_log2 * p.q_inv[sg.row];
+      const float c_raw = p.logit_scale_log2 * p.q_inv[(int64_t)sg.row * kHeads + (live ? h : 0)];
       // its magnitude; a scale of 0 becomes one that still sends a masked token's -inf to -inf, and one that
       // is no number makes every logit NaN
       const float c_log2 = fabsf(c_raw) < INFINITY ? fmaxf(fabsf(c_raw), 1e-38f) : __int_as_float(0x7FC00000);

@@ -93,7 +93,7 @@ dsa_status_t launch_sparse_mla_partials(const dsa_paged_cache_t& c, const dsa_ba
 dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
                                const int32_t* idx, int k, float sm_scale, uint16_t* out, float* lse,
                                void* workspace, int32_t* status, cudaStream_t st, const int32_t* phys = nullptr);
-// The rows' queries as fp16 times a power of two, and its inverse per row, in
+// The rows' queries as fp16 times a power of two per head, and its inverse, fp32 [rows][96], in
 // `workspace` (query_f16_bytes(rows) bytes, 256-byte aligned; query.cu).
 size_t query_f16_bytes(int rows);
 dsa_status_t launch_query_f16(const uint16_t* q, const float* lse, int rows, void* workspace, uint16_t** q16,

@@ -73,12 +73,12 @@ constexpr int kOffQ = 0;
 constexpr int kOffRaw = kDB * kQBlockBytes;                    // 110,592
 constexpr int kRawBytes = Raw<false>::kStages * Raw<false>::kBytes;  // 113,664
 static_assert(Raw<true>::kStages * Raw<true>::kBytes <= kRawBytes, "raw ring");
-constexpr int kOffHead = kOffRaw + kRawBytes;                  // per head: its LSE (log2)
-constexpr int kOffBars = kOffHead + kHeads * 4;
+constexpr int kOffHead = kOffRaw + kRawBytes;                  // the heads' LSE (log2), then log2 units per unit of S
+constexpr int kOffBars = kOffHead + 2 * kHeads * 4;
 constexpr int kNumBars = 2 * 4 + 2 * kSets + 6;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
 constexpr size_t kSmemBytes = 1024 + kOffMisc + 16 + 32 * 8;
-static_assert(kOffBars % 8 == 0, "alignment");
+static_assert(kOffHead % 16 == 0 && kHeads % 4 == 0 && kOffBars % 8 == 0, "alignment");
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct MassParams {
@@ -92,7 +92,7 @@ struct MassParams {
   const int32_t* idx;   // [rows][k] or null: every visible token
   int32_t k;
   float scale_log2;     // sm_scale * latent_scale * log2(e)
-  const float* q_inv;   // [rows]: the inverse of the power of two in the fp16 queries
+  const float* q_inv;   // [rows][96]: the inverse of the power of two in the fp16 queries
   const float* lse;     // [rows][96]
   const float* mass_in; // [batch][ld] (direct only)
   float* out;           // direct: mass_out [batch][ld]; else the rows' weights [rows][ld]
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffMisc + 16);
   float* lse_s = reinterpret_cast<float*>(smem + kOffHead);
+  float* unit_s = lse_s + kHeads;  // logits in log2 units per unit of S
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -372,7 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x;
     uint32_t it = 0;
     int cur = -1;
-    float c_log2 = 0.f;  // logits in log2 units per unit of S
     bool ok = true;
     while (tiles.next(row, first, count)) {
       const uint32_t b = it & 1;
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid < kHeads) {
           const float l = p.lse[(int64_t)row * kHeads + tid];
           lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no token attended: no weight
+          unit_s[tid] = p.scale_log2 * p.q_inv[(int64_t)row * kHeads + tid];
         }
-        c_log2 = p.scale_log2 * p.q_inv[row];
         bar_epilogue();
         cur = row;
       }
@@ -404,10 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 l = *reinterpret_cast<const float4*>(lse_s + 32 * c + j);
-          sum[0] += ex2f(fmaf(__uint_as_float(r[j]), c_log2, -l.x));
-          sum[1] += ex2f(fmaf(__uint_as_float(r[j + 1]), c_log2, -l.y));
-          sum[2] += ex2f(fmaf(__uint_as_float(r[j + 2]), c_log2, -l.z));
-          sum[3] += ex2f(fmaf(__uint_as_float(r[j + 3]), c_log2, -l.w));
+          const float4 u = *reinterpret_cast<const float4*>(unit_s + 32 * c + j);
+          sum[0] += ex2f(fmaf(__uint_as_float(r[j]), u.x, -l.x));
+          sum[1] += ex2f(fmaf(__uint_as_float(r[j + 1]), u.y, -l.y));
+          sum[2] += ex2f(fmaf(__uint_as_float(r[j + 2]), u.z, -l.z));
+          sum[3] += ex2f(fmaf(__uint_as_float(r[j + 3]), u.w, -l.w));
         }
       }
       float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);

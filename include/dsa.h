@@ -310,7 +310,10 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
  * head's query or in the scale, or a largest logit beyond fp32, gives that head NaN.
  * A length above min(max_blocks_per_seq * 64, max_seq_len) is read as that bound, a
  * negative one as 0; a bound above 2^30 is DSA_ERR_UNSUPPORTED.  Any number of rows
- * per sequence up to DSA_MAX_QUERIES_PER_SEQ.
+ * per sequence up to DSA_MAX_QUERIES_PER_SEQ.  A head's query enters the products as
+ * fp16 times a power of two of its own: with m the head's largest finite magnitude (at
+ * least 2^-112), elements down to 2^-28 m are exact and smaller ones off by at most
+ * 2^-39 m; what a head holds does not touch another.
  *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned
  *   out       device bf16 bits [rows][96][512], 8-byte aligned;  lse device fp32 [rows][96]
  *   workspace >= dense_mla_workspace_size(rows, batch->max_seq_len) bytes, 256-B aligned
@@ -333,7 +336,7 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
  * dense_mla_decode; else the entries >= 0 of idx[r], as in sparse_mla_decode;
  * an entry listed twice counts twice):
  *   mass_out[b][t] = mass_in[b][t] + sum_j sum_h exp(sm_scale * (q[r][h] . c_t) - lse[r][h])
- * with c_t as for the attention.  With the LSE of that attention the exponentials
+ * with c_t and q as for the attention.  With the LSE of that attention the exponentials
  * are its softmax weights; an LSE of -inf (a row that attended to nothing) adds
  * nothing, whatever its query holds.  Written for every t < seq_len_b and nothing else; fp32 sums in a
  * fixed order, so the result is the same on every run.

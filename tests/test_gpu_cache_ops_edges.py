@@ -14,6 +14,8 @@ row's n tokens):
   parts    fp16, 2^-11 * Sum p |v|, and 2^-25 of a latent unit below 2^-14
   output   bf16, 2^-8 of the computed value
   LSE      e + n * 2^-24 + 2^-20 * (1 + |lse|)
+A head's query is bf16 times a power of two of its own: exact down to 2^-28 of the
+head's largest element.
 """
 import dataclasses
 
@@ -107,3 +109,42 @@ def test_dense_scale_that_is_no_number(scale):
     for row in (0, 2):
         assert bool(torch.isnan(out[row].float()).all()) and bool(torch.isnan(lse[row]).all())
     assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
+
+
+# ---------------------------------------------------------------- heads of very different size
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("power", [28, 34, 45, 60, 100])
+def test_dense_one_head_far_above_the_others(fmt, power):
+    """A finite outlier in one head takes nothing from the other heads of its row."""
+    case = synth.make_case("edge_far", seq_lens=[700, 48, 6000], seed=503, latent_format=fmt)
+    q = torch.randn((3, 96, 576), generator=torch.Generator().manual_seed(power))
+    q[:, HEAD, 17] = 2.0 ** power
+    case = dataclasses.replace(case, q_mla=bf16_bits(q))
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check(case, out, lse, heads=OTHERS)
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("power", [28, 34, 45, 60, 100])
+@pytest.mark.parametrize("nq,k", [(1, 0), (3, 0), (1, 200)])
+def test_mass_one_head_far_above_the_others(fmt, power, nq, k):
+    """The same for the weights; the outlier's own LSE is set so high that it adds nothing."""
+    case = synth.make_case("edge_mass_far", seq_lens=[700, 140], nq=nq, seed=504, latent_format=fmt)
+    idx = None
+    if k:
+        g = torch.Generator().manual_seed(k)
+        idx = torch.full((case.rows, k), -1, dtype=torch.int32)
+        for r, vis in enumerate(case.row_lens()):
+            idx[r, :min(k, int(vis))] = torch.randperm(int(vis), generator=g)[:k].to(torch.int32)
+    q = torch.randn((case.rows, 96, 576), generator=torch.Generator().manual_seed(power))
+    q[:, HEAD, 17] = 2.0 ** power
+    case = dataclasses.replace(case, q_mla=bf16_bits(q))
+    lse = plain_lse(case, idx)
+    lse[:, HEAD] = 1e38
+    before = torch.rand((2, case.max_len + 3), generator=torch.Generator().manual_seed(3))
+    want, tol = plain_mass(case, before, lse, idx)
+    got, st = run_mass(case, synth.device_case(case), lse, before, idx)
+    assert st == 0
+    for b, L in enumerate(case.seq_lens):
+        assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
