@@ -126,6 +126,30 @@ def test_dense_one_head_far_above_the_others(fmt, power):
 
 
 @pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("power", [16, 24, 30, 45, 60, 100])
+def test_dense_logits_beyond_the_steps_of_fp32(fmt, power):
+    """Logits whose fp32 steps exceed 1, up to 2^100: one token takes a head, and it is the largest one's value."""
+    case = synth.make_case("edge_steep", seq_lens=[700, 48, 6000], seed=509, latent_format=fmt)
+    q = torch.randn((3, 96, 576), generator=torch.Generator().manual_seed(power)) * 2.0 ** power
+    case = dataclasses.replace(case, q_mla=bf16_bits(q))
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check(case, out, lse)   # this tolerance grows with the logits
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(lse).all())
+    for b in range(3):
+        c = plain64.latents(case, b)
+        x = plain64.queries(case, b) @ c.T * case.sm_scale
+        top, runner = x.topk(2, 1).values.T
+        # where the runner-up is further behind than the logits' error, and 6,000 of its weight vanish
+        bound = (plain64.queries(case, b).abs() @ c.abs().T * case.sm_scale).amax(1)
+        clear = top - runner > 2 * 576 * 2.0 ** -24 * bound + 30
+        assert bool(clear.any())
+        v = c[x.argmax(1)][:, :512]
+        tol = 2.0 ** -8 * v.abs() + 2.0 ** -11 * v.abs() + 2.0 ** -20 * c.abs().max()
+        assert torch.all(((out[b].double().cpu() - v).abs() <= tol)[clear]), b
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
 @pytest.mark.parametrize("power", [28, 34, 45, 60, 100])
 @pytest.mark.parametrize("nq,k", [(1, 0), (3, 0), (1, 200)])
 def test_mass_one_head_far_above_the_others(fmt, power, nq, k):
