@@ -574,6 +574,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q8_full);
       }
+      // Whether a page of the part lies outside the pool (the loaders report it), by all lanes while the first S is
+      // on its way: looked up in every tile, two entries cost 1 % of a decode batch and 4 % of one long context
+      auto hole = [&](int page) {
+        return (uint32_t)p.block_table[(int64_t)(sg.row / p.nq) * p.max_blocks + page] >= (uint32_t)p.num_blocks;
+      };
+      bool holes = false;
+#pragma unroll 4
+      for (int g = sg.t0 * kTile / kBlock + lane; g <= (min(sg.t1 * kTile, sg.vis) - 1) / kBlock; g += 32)
+        holes |= hole(g);
+      holes = __any_sync(0xffffffffu, holes);
       // the reference, in units of S
       float m_used = -INFINITY, l_sum = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
@@ -587,14 +597,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty(it & 1));
-        const int valid = sg.vis - t * kTile;
+        int lo = 0, up = sg.vis - t * kTile;  // the tile's tokens [lo, up) take part
+        if (holes) {  // those of a page outside the pool do not; a tile lies on at most two pages
+          up = min(up, kTile);
+          const int split = min(kBlock - t * kTile % kBlock, up);  // tokens on the first
+          const bool hole1 = hole((t * kTile + up - 1) / kBlock);
+          if (hole(t * kTile / kBlock)) lo = split;
+          if (hole1) up = split;
+        }
         if (c_raw < 0.f) {  // a negative scale: the largest logit is that of the smallest product
 #pragma unroll
           for (int j = 0; j < kTile; ++j) r[j] ^= 0x80000000u;
         }
-        if (valid < kTile) {
+        if (lo > 0 || up < kTile) {
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) r[j] = j < valid ? r[j] : 0xFF800000u;  // -inf
+          for (int j = 0; j < kTile; ++j) r[j] = j >= lo && j < up ? r[j] : 0xFF800000u;  // -inf
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -603,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i)
             mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[j + 2 * i])), __uint_as_float(r[j + 2 * i + 1]));
         const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // Every tile has a token.  A maximum of -inf is that of logits that are all -inf or NaN (fmaxf drops
-        // NaN).  That, a NaN and +inf come from a query, a scale or a logit that is no fp32 number: a NaN row
-        if (!(fabsf(m_tile * c_log2) < INFINITY)) m_used = __int_as_float(0x7FC00000);
+        // A maximum of -inf over a tile's tokens is that of logits that are all -inf or NaN (fmaxf drops NaN).
+        // That, a NaN and +inf come from a query, a scale or a logit that is no fp32 number: a NaN row
+        if (lo < up && !(fabsf(m_tile * c_log2) < INFINITY)) m_used = __int_as_float(0x7FC00000);
         const bool grow =
             live && (m_used == -INFINITY ? m_tile > -INFINITY : (m_tile - m_used) * c_log2 > kRescaleThreshold);
         // one barrier a tile: any head that grew, and any warp whose wait ran out

@@ -317,7 +317,8 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
  *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned
  *   out       device bf16 bits [rows][96][512], 8-byte aligned;  lse device fp32 [rows][96]
  *   workspace >= dense_mla_workspace_size(rows, batch->max_seq_len) bytes, 256-B aligned
- * A table entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS in *dev_status.
+ * A table entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS in *dev_status, and the
+ * tokens of its page take no part.
  * Three launches.  The tokens of all rows are split evenly over the SMs, so the
  * order of a row's sums depends on the batch; in the batch-invariant mode
  * (dsa_batch_invariant) rows are split every 3,840 tokens instead, and the

@@ -172,3 +172,28 @@ def test_mass_one_head_far_above_the_others(fmt, power, nq, k):
     assert st == 0
     for b, L in enumerate(case.seq_lens):
         assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
+
+
+# ---------------------------------------------------------------- bad pages and entries
+def seen(case, table):
+    def tokens(row):
+        b = row // case.nq
+        t = torch.arange(max(0, int(case.seq_lens[b]) - (case.nq - 1) + row % case.nq))
+        page = torch.from_numpy(table[b].astype(np.int64))[t // 64]
+        return t[(page >= 0) & (page < case.num_blocks)]
+    return tokens
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("bad", [-1, 1 << 30, None])
+def test_dense_bad_pages_take_no_part(fmt, bad):
+    """The tokens of a page outside the pool are masked, in the first, an inner, the last and every page."""
+    case = synth.make_case("edge_page", seq_lens=[40, 500, 300, 130, 6000, 64, 190], nq=2, seed=505, latent_format=fmt)
+    table = case.block_table.copy()
+    bad = case.num_blocks if bad is None else bad
+    table[0, 0] = table[1, 0] = table[2, 2] = table[3, 2] = bad
+    table[4, 5:9] = table[4, 40] = table[4, 93] = bad
+    table[6, :3] = bad
+    out, lse, st = run_dense(case, synth.device_case(dataclasses.replace(case, block_table=table)))
+    assert st == binding.ERR_BOUNDS
+    check(case, out, lse, tokens=seen(case, table))
