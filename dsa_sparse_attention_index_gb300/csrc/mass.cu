@@ -411,13 +411,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum[3] += ex2f(fmaf(__uint_as_float(r[j + 3]), u.w, -l.w));
         }
       }
-      float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (tid < count) {
+        // an entry of -1, one that the row does not see and a page outside the pool (the producers report the last
+        // two) have no weight, whatever the products of their zeros give
         const int64_t at = (int64_t)row * p.ld + first + tid;  // direct: one row per sequence
-        if (p.direct)
-          w += p.mass_in ? p.mass_in[at] : 0.f;
-        else if (p.idx && p.idx[at] < 0)
-          w = 0.f;
+        const int tok = p.idx ? p.idx[at] : first + tid;
+        bool seen = tok >= 0 && (!p.idx || tok < tiles.visible(row));
+        if (seen) seen = (uint32_t)p.block_table[(int64_t)(row / p.nq) * p.max_blocks + tok / kBlock] < (uint32_t)p.num_blocks;
+        float w = seen ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+        if (p.direct && p.mass_in) w += p.mass_in[at];
         p.out[at] = w;
       }
     }

@@ -343,7 +343,8 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
  * fixed order, so the result is the same on every run.
  *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned;  lse device fp32 [rows][96]
  *   idx       device int32 [rows][k] with k in 1..DSA_MAX_TOPK, or NULL with k = 0; an entry
- *             that its row does not see raises DSA_ERR_BOUNDS
+ *             that its row does not see raises DSA_ERR_BOUNDS and adds nothing, and so does a
+ *             table entry outside 0..num_blocks-1 for the tokens of its page
  *   mass_in   device fp32 [batch][ld_mass] or NULL (zeros);  mass_out likewise, mass_in itself
  *             (adding in place) or a buffer that does not overlap it;  ld_mass >= max_seq_len
  *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B aligned

@@ -197,3 +197,45 @@ def test_dense_bad_pages_take_no_part(fmt, bad):
     out, lse, st = run_dense(case, synth.device_case(dataclasses.replace(case, block_table=table)))
     assert st == binding.ERR_BOUNDS
     check(case, out, lse, tokens=seen(case, table))
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("nq", [1, 3])
+def test_mass_bad_pages_add_nothing(fmt, nq):
+    case = synth.make_case("edge_mass_page", seq_lens=[40, 500, 1300], nq=nq, seed=506, latent_format=fmt)
+    table = case.block_table.copy()
+    table[0, 0], table[1, 3], table[2, 20] = -1, case.num_blocks, 1 << 30
+    tokens = seen(case, table)
+    lse = torch.stack([plain64.attend(case, r, tokens(r))[1] for r in range(case.rows)]).float()
+    lse[:nq] = 0.0   # nothing attended; a finite LSE all the same
+    before = torch.rand((3, case.max_len + 3), generator=torch.Generator().manual_seed(5))
+    listed = torch.full((case.rows, case.max_len), -1, dtype=torch.int32)
+    for r in range(case.rows):
+        listed[r, :len(tokens(r))] = tokens(r).to(torch.int32)
+    want, tol = plain_mass(case, before, lse, listed)
+    got, st = run_mass(case, synth.device_case(dataclasses.replace(case, block_table=table)), lse, before)
+    assert st == binding.ERR_BOUNDS
+    for b, L in enumerate(case.seq_lens):
+        assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+def test_mass_bad_entries_add_nothing(fmt):
+    """Entries behind what their row sees, below and above the sequence's length, and on a bad page."""
+    case = synth.make_case("edge_entries", seq_lens=[500, 200], nq=2, seed=507, latent_format=fmt)
+    table = case.block_table.copy()
+    table[1, 1] = -1
+    idx = torch.full((4, 150), -1, dtype=torch.int32)
+    for r, vis in enumerate(case.row_lens()):
+        idx[r, :120] = torch.randperm(int(vis), generator=torch.Generator().manual_seed(r))[:120].to(torch.int32)
+    good = idx.clone()
+    idx[0, 3], idx[0, 130], idx[1, 149], idx[2, 7] = 499, 499, 1 << 30, 199   # row 0 sees 499 tokens, row 2 199
+    good[0, 3], good[2, 7] = -1, -1
+    good[2:][(good[2:] >= 64) & (good[2:] < 128)] = -1
+    lse = plain_lse(case, good)
+    before = torch.rand((2, case.max_len + 3), generator=torch.Generator().manual_seed(6))
+    want, tol = plain_mass(case, before, lse, good)
+    got, st = run_mass(case, synth.device_case(dataclasses.replace(case, block_table=table)), lse, before, idx)
+    assert st == binding.ERR_BOUNDS
+    for b, L in enumerate(case.seq_lens):
+        assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
