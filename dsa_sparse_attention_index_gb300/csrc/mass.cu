@@ -107,6 +107,15 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 __device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool bar_or_epilogue(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
 
 struct Tiles {  // a run's tiles, one after another
   const MassParams& p;
@@ -373,17 +382,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x;
     uint32_t it = 0;
     int cur = -1;
-    bool ok = true;
+    bool ok = true, attended = false;  // attended: a head of the row has an LSE above -inf
     while (tiles.next(row, first, count)) {
       const uint32_t b = it & 1;
       if (row != cur) {
         bar_epilogue();  // the previous row's values have been read
+        attended = false;
         if (tid < kHeads) {
           const float l = p.lse[(int64_t)row * kHeads + tid];
           lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no token attended: no weight
           unit_s[tid] = p.scale_log2 * p.q_inv[(int64_t)row * kHeads + tid];
+          attended = l != -INFINITY;
         }
-        bar_epilogue();
+        attended = bar_or_epilogue(attended);
         cur = row;
       }
       ok = ok && mbar_wait_warp(s_full(b), (it >> 1) & 1, abort_flag, p.status);
@@ -413,10 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid < count) {
         // an entry of -1, one that the row does not see and a page outside the pool (the producers report the last
-        // two) have no weight, whatever the products of their zeros give
+        // two) have no weight, whatever the products of their zeros give; nor has any token of a row that attended
+        // to nothing, though its pages may never have been written (NaN codes)
         const int64_t at = (int64_t)row * p.ld + first + tid;  // direct: one row per sequence
         const int tok = p.idx ? p.idx[at] : first + tid;
-        bool seen = tok >= 0 && (!p.idx || tok < tiles.visible(row));
+        bool seen = attended && tok >= 0 && (!p.idx || tok < tiles.visible(row));
         if (seen) seen = (uint32_t)p.block_table[(int64_t)(row / p.nq) * p.max_blocks + tok / kBlock] < (uint32_t)p.num_blocks;
         float w = seen ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
         if (p.direct && p.mass_in) w += p.mass_in[at];

@@ -338,8 +338,9 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
  * an entry listed twice counts twice):
  *   mass_out[b][t] = mass_in[b][t] + sum_j sum_h exp(sm_scale * (q[r][h] . c_t) - lse[r][h])
  * with c_t and q as for the attention.  With the LSE of that attention the exponentials
- * are its softmax weights; an LSE of -inf (a row that attended to nothing) adds
- * nothing, whatever its query holds.  Written for every t < seq_len_b and nothing else; fp32 sums in a
+ * are its softmax weights; a head's LSE of -inf (it attended to nothing) adds
+ * nothing, whatever its query holds, and a row of such heads adds nothing, whatever
+ * its pages hold.  Written for every t < seq_len_b and nothing else; fp32 sums in a
  * fixed order, so the result is the same on every run.
  *   q_mla     device bf16 bits [rows][96][576], 16-byte aligned;  lse device fp32 [rows][96]
  *   idx       device int32 [rows][k] with k in 1..DSA_MAX_TOPK, or NULL with k = 0; an entry

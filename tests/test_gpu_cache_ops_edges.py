@@ -239,3 +239,22 @@ def test_mass_bad_entries_add_nothing(fmt):
     assert st == binding.ERR_BOUNDS
     for b, L in enumerate(case.seq_lens):
         assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("nq", [1, 2])
+def test_mass_rows_that_attended_to_nothing_over_unwritten_pages(fmt, nq):
+    """A row whose LSEs are all -inf adds nothing, whatever lies in its pages (NaN codes here)."""
+    case = synth.make_case("edge_unwritten", seq_lens=[300, 200], nq=nq, seed=508, latent_format=fmt)
+    lse = plain_lse(case)
+    pool = case.pool.copy()
+    for page in case.block_table[1][case.block_table[1] >= 0]:
+        pool[page, case.latent_off:case.latent_off + 64 * case.latent_bytes()] = 0x7F
+    lse[nq:] = -float("inf")
+    before = torch.rand((2, case.max_len + 3), generator=torch.Generator().manual_seed(7))
+    want, tol = plain_mass(case, before, lse)
+    got, st = run_mass(dataclasses.replace(case, pool=pool), synth.device_case(dataclasses.replace(case, pool=pool)), lse,
+                       before)
+    assert st == 0
+    assert torch.equal(got[1, :200], before[1, :200])
+    assert torch.all((got[0, :300].double() - want[0, :300]).abs() <= tol[0, :300])
