@@ -310,7 +310,7 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
 
 size_t dense_mla_workspace_size(int32_t rows, int32_t max_seq_len) {
   if (rows < 0 || max_seq_len < 0) return 0;
-  return dense_mla_workspace_bytes(rows, max_seq_len);
+  return dense_mla_workspace_bytes(rows, max_seq_len, mla_batch_invariant_on());
 }
 
 dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
@@ -324,9 +324,11 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
   if (rows == 0) return DSA_OK;
   if (!q_mla || !out || !lse || !aligned(q_mla, 16) || !aligned(out, 8) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
   if (too_long(batch)) return DSA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_mla_workspace_bytes(rows, batch->max_seq_len))
+  const bool inv = mla_batch_invariant_on();  // read once: the workspace that is checked is the one laid out
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < dense_mla_workspace_bytes(rows, batch->max_seq_len, inv))
     return DSA_ERR_WORKSPACE;
-  return launch_dense_mla(*cache, *batch, q_mla, sm_scale, out, lse, workspace, dev_status,
+  return launch_dense_mla(*cache, *batch, q_mla, sm_scale, inv, out, lse, workspace, dev_status,
                           static_cast<cudaStream_t>(stream));
 }
 

@@ -855,15 +855,14 @@ int64_t dense_slots(int rows, int max_len, bool inv) {
 
 }  // namespace
 
-size_t dense_mla_workspace_bytes(int rows, int max_len) {
-  const int64_t slots = dense_slots(rows, max_len, mla_batch_invariant_on());
+size_t dense_mla_workspace_bytes(int rows, int max_len, bool inv) {
+  const int64_t slots = dense_slots(rows, max_len, inv);
   return query_f16_bytes(rows) + al256((size_t)rows * sizeof(int2)) + al256((size_t)slots * kPartO * 2) + al256((size_t)slots * kHeads * 8);
 }
 
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,
-                              uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st) {
+                              bool inv, uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st) {
   const int rows = bt.batch * bt.queries_per_seq;
-  const bool inv = mla_batch_invariant_on();  // read once: the parts and the workspace layout agree
   const int64_t slots = dense_slots(rows, bt.max_seq_len, inv);
   const bool nv = c.latent_format == DSA_LATENT_NVFP4;
   static std::atomic<bool> attr_set[64];

@@ -98,10 +98,11 @@ dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt
 size_t query_f16_bytes(int rows);
 dsa_status_t launch_query_f16(const uint16_t* q, const float* lse, int rows, void* workspace, uint16_t** q16,
                               float** inv, cudaStream_t st);
-// Attention over every visible token (dense_mla.cu).
-size_t dense_mla_workspace_bytes(int rows, int max_len);
+// Attention over every visible token (dense_mla.cu).  inv: the batch-invariant mode, which the caller reads once:
+// another thread may switch it between the check of a workspace's size and its layout.
+size_t dense_mla_workspace_bytes(int rows, int max_len, bool inv);
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla, float sm_scale,
-                              uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st);
+                              bool inv, uint16_t* out, float* lse, void* workspace, int32_t* status, cudaStream_t st);
 // Attention weights per cached token (mass.cu).  k = 0: every visible token.
 size_t mass_workspace_bytes(int rows, int max_len, int k);
 dsa_status_t launch_attention_mass(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
