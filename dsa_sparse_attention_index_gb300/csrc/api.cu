@@ -289,7 +289,7 @@ int32_t dsa_batch_invariant(int32_t on) { return dsa::mla_batch_invariant(on); }
 
 size_t sparse_mla_workspace_size(int32_t rows, int32_t k) {
   if (rows < 0 || k < 1 || k > DSA_MAX_TOPK) return 0;
-  return mla_workspace_bytes(rows, k);
+  return mla_workspace_bytes(rows, k, mla_batch_invariant_on());
 }
 
 dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t* batch, const uint16_t* q_mla,
@@ -302,9 +302,10 @@ dsa_status_t sparse_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t
   const int rows = batch->batch * batch->queries_per_seq;
   if (rows == 0) return DSA_OK;
   if (!q_mla || !idx || !out || !lse || !aligned(q_mla, 16) || !aligned(out, 8)) return DSA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < mla_workspace_bytes(rows, k))
+  const bool inv = mla_batch_invariant_on();  // read once: the workspace that is checked is the one laid out
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < mla_workspace_bytes(rows, k, inv))
     return DSA_ERR_WORKSPACE;
-  return launch_sparse_mla(*cache, *batch, q_mla, idx, k, sm_scale, out, lse, workspace, dev_status,
+  return launch_sparse_mla(*cache, *batch, q_mla, idx, k, sm_scale, inv, out, lse, workspace, dev_status,
                            static_cast<cudaStream_t>(stream));
 }
 
@@ -401,11 +402,19 @@ dsa_status_t dsa_cache_evict(const dsa_paged_cache_t* cache, const dsa_batch_t* 
                             static_cast<cudaStream_t>(stream));
 }
 
-size_t dsa_workspace_size(const dsa_batch_t* batch, int32_t k) {
-  if (!batch || batch->batch < 0 || k < 1 || k > DSA_MAX_TOPK) return 0;
+namespace {
+
+size_t step_workspace_bytes(const dsa_batch_t* batch, int32_t k, bool inv) {
   const int rows = batch->batch * std::max(1, batch->queries_per_seq);
   return al256((size_t)rows * round_ld(batch->max_seq_len) * 4) + al256((size_t)rows * k * 4) +
-         al256(topk_workspace_bytes(rows, batch->max_seq_len, k)) + al256(mla_workspace_bytes(rows, k));
+         al256(topk_workspace_bytes(rows, batch->max_seq_len, k)) + al256(mla_workspace_bytes(rows, k, inv));
+}
+
+}  // namespace
+
+size_t dsa_workspace_size(const dsa_batch_t* batch, int32_t k) {
+  if (!batch || batch->batch < 0 || k < 1 || k > DSA_MAX_TOPK) return 0;
+  return step_workspace_bytes(batch, k, mla_batch_invariant_on());
 }
 
 namespace {
@@ -425,7 +434,8 @@ dsa_status_t decode_step_impl(const dsa_paged_cache_t* cache, const dsa_batch_t*
   if (!q_index || !head_w || !q_mla || !out || !lse) return DSA_ERR_INVALID_ARG;
   if (!aligned(q_index, 16) || !aligned(head_w, 16) || !aligned(q_mla, 16) || !aligned(out, 8))
     return DSA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < dsa_workspace_size(batch, k))
+  const bool inv = mla_batch_invariant_on();  // read once, as above
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < step_workspace_bytes(batch, k, inv))
     return DSA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -464,7 +474,7 @@ dsa_status_t decode_step_impl(const dsa_paged_cache_t* cache, const dsa_batch_t*
     s = launch_topk(static_cast<const float*>(scores), ld, nullptr, batch->seq_lens, batch->queries_per_seq, rows,
                     cap, k, idx, topk_ws, dev_status, st, po);
   if (s != DSA_OK) return s;
-  return launch_sparse_mla(*cache, *batch, q_mla, idx, k, sm_scale, out, lse, mla_ws, dev_status, st, phys);
+  return launch_sparse_mla(*cache, *batch, q_mla, idx, k, sm_scale, inv, out, lse, mla_ws, dev_status, st, phys);
 }
 
 }  // namespace

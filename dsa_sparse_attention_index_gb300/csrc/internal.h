@@ -74,7 +74,8 @@ dsa_status_t launch_dcp_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t
                                    const int32_t* idx, int k, int shards, float sm_scale, uint16_t* out, float* lse,
                                    uint16_t* part_out, float* part_lse, void* workspace, int32_t* status,
                                    cudaStream_t st);
-size_t mla_workspace_bytes(int rows, int k);
+// inv: the batch-invariant mode, which the caller reads once (see dense_mla_workspace_bytes).
+size_t mla_workspace_bytes(int rows, int k, bool inv);
 // Process-wide batch-invariant mode of the MLA chunking; returns the previous setting.
 int mla_batch_invariant(int on);
 bool mla_batch_invariant_on();
@@ -91,7 +92,7 @@ dsa_status_t launch_sparse_mla_partials(const dsa_paged_cache_t& c, const dsa_ba
 // phys: the top-k's physical KV rows for idx ([rows][k], -1 padding, already
 // bounds-checked and visible) or nullptr: the kernel translates idx itself.
 dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
-                               const int32_t* idx, int k, float sm_scale, uint16_t* out, float* lse,
+                               const int32_t* idx, int k, float sm_scale, bool inv, uint16_t* out, float* lse,
                                void* workspace, int32_t* status, cudaStream_t st, const int32_t* phys = nullptr);
 // The rows' queries as fp16 times a power of two per head, and its inverse, fp32 [rows][96], in
 // `workspace` (query_f16_bytes(rows) bytes, 256-byte aligned; query.cu).

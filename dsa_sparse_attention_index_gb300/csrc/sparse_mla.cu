@@ -823,11 +823,10 @@ static int mla_nsplit(int rows, int k, bool inv) {
   return std::max((k + kMaxChunk - 1) / kMaxChunk,
                   std::min(mla_nsplit_max(rows, k, false), num_sms() / std::max(1, rows)));
 }
-static bool batch_invariant() { return mla_batch_invariant_on(); }
 
-size_t mla_workspace_bytes(int rows, int k) {
+size_t mla_workspace_bytes(int rows, int k, bool inv) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t parts = (size_t)rows * mla_nsplit_max(rows, k, batch_invariant());
+  const size_t parts = (size_t)rows * mla_nsplit_max(rows, k, inv);
   return al(parts * kHeads * kValue * 2) + al(parts * kHeads * 16);
 }
 
@@ -918,11 +917,10 @@ dsa_status_t launch_sparse_mla_partials(const dsa_paged_cache_t& c, const dsa_ba
 }
 
 dsa_status_t launch_sparse_mla(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* q_mla,
-                               const int32_t* idx, int k, float sm_scale, uint16_t* out, float* lse,
+                               const int32_t* idx, int k, float sm_scale, bool inv, uint16_t* out, float* lse,
                                void* workspace, int32_t* status, cudaStream_t st, const int32_t* phys) {
   const int rows = bt.batch * bt.queries_per_seq;
   if (rows == 0) return DSA_OK;
-  const bool inv = batch_invariant();  // read once: the split and the workspace layout agree
   const int nsplit0 = mla_nsplit(rows, k, inv);
   const int tiles = (k + kTileTok - 1) / kTileTok;
   const int chunk = ((tiles + nsplit0 - 1) / nsplit0) * kTileTok;

@@ -17,6 +17,17 @@ static size_t size_of(bool inv) { checked = inv; return 1024; }
 size_t dense_mla_workspace_bytes(int, int, bool inv) { return size_of(inv); }
 dsa_status_t launch_dense_mla(const dsa_paged_cache_t&, const dsa_batch_t&, const uint16_t*, float, bool inv, uint16_t*,
                               float*, void*, int32_t*, cudaStream_t) { launched = inv; return DSA_OK; }
+size_t mla_workspace_bytes(int, int, bool inv) { return size_of(inv); }
+dsa_status_t launch_sparse_mla(const dsa_paged_cache_t&, const dsa_batch_t&, const uint16_t*, const int32_t*, int, float,
+                               bool inv, uint16_t*, float*, void*, int32_t*, cudaStream_t, const int32_t*) {
+  launched = inv;
+  return DSA_OK;
+}
+size_t topk_workspace_bytes(int, int, int) { return 0; }
+dsa_status_t launch_index_scores(const dsa_paged_cache_t&, const dsa_batch_t&, const uint8_t*, const float*, void*, bool,
+                                 int64_t, int32_t*, cudaStream_t) { return DSA_OK; }
+dsa_status_t launch_topk(const float*, int64_t, const int32_t*, const int32_t*, int, int, int, int, int32_t*, void*, int32_t*,
+                         cudaStream_t, const TopkPhys&) { return DSA_OK; }
 }  // namespace dsa
 using namespace dsa;
 int main() {
@@ -33,6 +44,9 @@ int main() {
   if (reads != 1 || checked != launched || launched != start)                                 \
     return printf("%s: %d reads, checked %d, launched %d\n", #name, reads, checked, launched), 1;
     CALL(dense_mla_decode, &c, &b, u, 1.0f, u, f, at, 1024, i, nullptr)
+    CALL(sparse_mla_decode, &c, &b, u, i, 64, 1.0f, u, f, at, 1024, i, nullptr)
+    CALL(dsa_decode_step, &c, &b, static_cast<uint8_t*>(at), f, u, 64, 1.0f, u, f, nullptr, 0, nullptr, nullptr, at, 1 << 20, i,
+         nullptr)
   }
   return 0;
 }
