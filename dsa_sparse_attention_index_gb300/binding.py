@@ -211,6 +211,25 @@ class Batch:
                       self.queries_per_seq, int(self.max_seq_len))
 
 
+def _structs(batch: Batch, *caches: PagedCache):
+    """The descriptors of a batch and caches whose tensors hold all that the library reads through them."""
+    table, lens = batch.block_table, batch.seq_lens
+    if (table.dtype not in _I32 or lens.dtype not in _I32 or table.dim() != 2 or lens.dim() != 1
+            or table.shape[0] < lens.shape[0]):
+        raise ValueError(f"block_table and seq_lens: expected int32 [batch, max_blocks] and [batch], got "
+                         f"{list(table.shape)} of {table.dtype} and {list(lens.shape)} of {lens.dtype}")
+    for c in caches:
+        if c.pool.nbytes < c.pool.shape[0] * c.row_stride:
+            raise ValueError(f"pool: {c.pool.nbytes} bytes for {c.pool.shape[0]} rows of {c.row_stride}")
+    return batch.struct(), *(c.struct() for c in caches)
+
+
+def _status(status) -> int | None:
+    if status.dtype not in _I32 or status.numel() < 1:
+        raise ValueError(f"status: expected one int32, got {list(status.shape)} of {status.dtype}")
+    return _ptr(status)
+
+
 def translate_pages(cache: PagedCache, batch: Batch, latent_pages, index_pages, status, stream=None):
     c, b = cache.struct(), batch.struct()
     _check(lib().dsa_translate_pages(ctypes.byref(c), ctypes.byref(b), _ptr(latent_pages), _ptr(index_pages),
@@ -291,13 +310,14 @@ def dense_mla_decode(cache: PagedCache, batch: Batch, q_mla, sm_scale: float, ou
                      stream=None):
     """Exact MLA over every token each row sees (no selection): q_mla bf16 bits [rows, 96, 576], out bf16 bits
     [rows, 96, 512], lse fp32 [rows, 96]."""
-    c, b, rows = cache.struct(), batch.struct(), batch.rows
+    b, c = _structs(batch, cache)
+    rows = batch.rows
     _one_device(cache.pool, batch.block_table, batch.seq_lens, q_mla, out, lse, workspace, status)
     _check(lib().dense_mla_decode(ctypes.byref(c), ctypes.byref(b),
                                   _want("q_mla", q_mla, (rows, MLA_HEADS, LATENT), _BITS16), float(sm_scale),
                                   _want("out", out, (rows, MLA_HEADS, VALUE), _BITS16),
                                   _want("lse", lse, (rows, MLA_HEADS), _F32), _ptr(workspace),
-                                  workspace.nbytes, _ptr(status), _stream(stream)),
+                                  workspace.nbytes, _status(status), _stream(stream)),
            "dense_mla_decode")
 
 
@@ -309,7 +329,8 @@ def attention_mass(cache: PagedCache, batch: Batch, q_mla, lse, sm_scale: float,
                    idx=None, stream=None):
     """mass_out = mass_in (or 0) + every token's attention weight, summed over the rows of its sequence and the heads:
     fp32 [batch, ld]; over every visible token, or over the top-k's entries when idx (int32 [rows, k]) is given."""
-    c, b, rows = cache.struct(), batch.struct(), batch.rows
+    b, c = _structs(batch, cache)
+    rows = batch.rows
     _one_device(cache.pool, batch.block_table, batch.seq_lens, q_mla, lse, mass_in, mass_out, workspace, status, idx)
     ld, k = mass_out.shape[-1], 0 if idx is None else idx.shape[-1]
     totals = (batch.batch, ld)
@@ -318,7 +339,7 @@ def attention_mass(cache: PagedCache, batch: Batch, q_mla, lse, sm_scale: float,
                                     _want("lse", lse, (rows, MLA_HEADS), _F32), _want("idx", idx, (rows, k), _I32), k,
                                     float(sm_scale), _want("mass_in", mass_in, totals, _F32),
                                     _want("mass_out", mass_out, totals, _F32), ld, _ptr(workspace),
-                                    workspace.nbytes, _ptr(status), _stream(stream)), "dsa_attention_mass")
+                                    workspace.nbytes, _status(status), _stream(stream)), "dsa_attention_mass")
 
 
 def cache_evict_workspace_size(batch: int, max_seq_len: int, keep: int) -> int:
@@ -330,7 +351,8 @@ def cache_evict(cache: PagedCache, batch: Batch, mass, keep: int, sink: int, rec
     """Keep each sequence's first `sink`, last `recent` and, between them, heaviest tokens (`keep` in all) and move
     their records into the pages of dst_block_table.  kept_idx int32 [batch, keep], mass_out fp32 [batch, >= keep]
     or None, new_lens int32 [batch]."""
-    c, b, d, n = cache.struct(), batch.struct(), dst_cache.struct(), batch.batch
+    b, c, d = _structs(batch, cache, dst_cache)
+    n = batch.batch
     ld, blocks, ld_out = mass.shape[-1], dst_block_table.shape[-1], 0 if mass_out is None else mass_out.shape[-1]
     _one_device(cache.pool, batch.block_table, batch.seq_lens, mass, dst_cache.pool, dst_block_table, kept_idx, mass_out,
                 new_lens, workspace, status)
@@ -340,7 +362,7 @@ def cache_evict(cache: PagedCache, batch: Batch, mass, keep: int, sink: int, rec
                                  _want("kept_idx", kept_idx, (n, int(keep)), _I32),
                                  _want("mass_out", mass_out, (n, ld_out), _F32), ld_out,
                                  _want("new_lens", new_lens, (n,), _I32), _ptr(workspace),
-                                 workspace.nbytes, _ptr(status), _stream(stream)),
+                                 workspace.nbytes, _status(status), _stream(stream)),
            "dsa_cache_evict")
 
 
