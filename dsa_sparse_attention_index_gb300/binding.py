@@ -333,6 +333,8 @@ def attention_mass(cache: PagedCache, batch: Batch, q_mla, lse, sm_scale: float,
     rows = batch.rows
     _one_device(cache.pool, batch.block_table, batch.seq_lens, q_mla, lse, mass_in, mass_out, workspace, status, idx)
     ld, k = mass_out.shape[-1], 0 if idx is None else idx.shape[-1]
+    if idx is not None and k < 1:
+        raise ValueError("idx: expected at least one entry a row; None stands for every visible token")
     totals = (batch.batch, ld)
     _check(lib().dsa_attention_mass(ctypes.byref(c), ctypes.byref(b),
                                     _want("q_mla", q_mla, (rows, MLA_HEADS, LATENT), _BITS16),

@@ -116,3 +116,8 @@ def test_pools_smaller_than_their_rows(lib):
 def test_status_words(lib, shape, dtype):
     for call in calls(status=Tensor(shape, dtype)):
         refused(lib, call)
+
+
+def test_a_selection_of_no_entries(lib):
+    """An empty idx has no address, which the library would take for "every visible token"."""
+    refused(lib, calls(idx=Tensor((6, 0), torch.int32))[2])
