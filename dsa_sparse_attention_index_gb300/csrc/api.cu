@@ -346,9 +346,10 @@ dsa_status_t dsa_attention_mass(const dsa_paged_cache_t* cache, const dsa_batch_
   if ((s = check_cache(cache)) != DSA_OK) return s;
   if ((s = check_batch(batch)) != DSA_OK) return s;
   if (!dev_status) return DSA_ERR_INVALID_ARG;
-  if (idx ? (k < 1 || k > DSA_MAX_TOPK) : k != 0) return DSA_ERR_INVALID_ARG;
+  if (k < 0 || k > DSA_MAX_TOPK) return DSA_ERR_INVALID_ARG;
   const int rows = batch->batch * batch->queries_per_seq;
-  if (rows == 0) return DSA_OK;
+  if (rows == 0) return DSA_OK;  // idx of an empty batch has no address
+  if ((k > 0) != (idx != nullptr)) return DSA_ERR_INVALID_ARG;
   if (!q_mla || !lse || !mass_out || !aligned(q_mla, 16) || !aligned(lse, 4) || !aligned(idx, 4) ||
       !aligned(mass_in, 4) || !aligned(mass_out, 4) || ld_mass < batch->max_seq_len)
     return DSA_ERR_INVALID_ARG;

@@ -148,3 +148,13 @@ def test_contexts_beyond_32_bit_tiles_and_overlapping_totals(lib):
         assert mass(lib, mi=mi) == B.ERR_INVALID_ARG
     for mi in (FAKE, FAKE + 4 * 1000, FAKE - 4 * 1000):
         assert mass(lib, mi=mi, ws=None) == B.ERR_WORKSPACE
+
+
+def test_an_empty_batch_has_nothing_to_do_whatever_the_selection(lib):
+    """No sequence, so no row of idx, whose tensor then has no address."""
+    none = batch(batch=0, block_table=None, seq_lens=None)
+    assert mass(lib, b=none, idx=None, k=64, q=None, lse=None, mo=None, ws=None, n=0) == B.OK
+    assert mass(lib, b=none, q=None, lse=None, mo=None, ws=None, n=0) == B.OK
+    assert dense(lib, b=none, q=None, out=None, lse=None, ws=None, n=0) == B.OK
+    assert evict(lib, b=none, m=None, table=None, kept=None, mo=None, lens=None, ws=None, n=0) == B.OK
+    assert mass(lib, b=none, idx=None, k=2049) == B.ERR_INVALID_ARG
