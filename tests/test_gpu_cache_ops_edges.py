@@ -68,6 +68,43 @@ def check(case, out, lse, heads=None, rows=None, tokens=None):
 OTHERS = [h for h in range(96) if h != HEAD]
 
 
+# ---------------------------------------------------------------- the tolerance itself
+@pytest.mark.parametrize("fmt", [FP8, NV])
+@pytest.mark.parametrize("lens,nq", [([1, 47, 48, 49, 0], 1), ([3000, 130], 1), ([20001], 1), ([700, 2049], 4)])
+def test_dense_within_the_roundings_of_its_own_arithmetic(fmt, lens, nq):
+    case = synth.make_case("edge_tol", seq_lens=lens, nq=nq, seed=500 + len(lens) + nq, latent_format=fmt)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check(case, out, lse)
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+def test_dense_weights_keep_eleven_bits(fmt):
+    """Two tokens of opposite values and nearly equal weights: the output is the weights' small difference, and a
+    weight held in bf16's 8 bits would be seen."""
+    case = synth.make_case("edge_bits", seq_lens=[2], seed=515, latent_format=fmt)
+    rec, at = case.latent_bytes(), case.latent_off
+    pool = case.pool.copy()
+    row = pool[case.block_table[0, 0], at:at + 2 * rec].reshape(2, rec)
+    row[:, rec - 64:] = 0                      # no key-only dimensions
+    row[1] = row[0]
+    row[1, :512 if fmt == FP8 else 256] ^= 0x80 if fmt == FP8 else 0x88
+    pool[case.block_table[0, 0], at:at + 2 * rec] = row.reshape(-1)
+    q = 0.05 * torch.randn((1, 96, 576), generator=torch.Generator().manual_seed(4))
+    case = dataclasses.replace(case, pool=pool, q_mla=bf16_bits(q))
+    c = plain64.latents(case, 0)
+    ro, rl, av, _, bound = plain64.attend(case, 0, c=c)
+    err = (2 * 576 * 2.0 ** -24 * bound[:, None] + 4 * 2.0 ** -24 + 2.0 ** -11) * av + 2.0 ** -31 * c.abs().max()
+    tol = err + 2.0 ** -8 * (ro.abs() + err)   # one part, so no rounding of parts
+    x = plain64.queries(case, 0) @ c.T * case.sm_scale
+    p = torch.exp(x - x.amax(1, keepdim=True))
+    in8 = (p * 128).to(torch.bfloat16).double() / 128 @ c[:, :512] / p.sum(1, keepdim=True)
+    assert bool(((in8 - ro).abs() > tol).any())
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    assert torch.all((out[0].double().cpu() - ro).abs() <= tol)
+
+
 # ---------------------------------------------------------------- infinities and NaN
 def constant_dim(case, kind):
     """Latent dimension 550 (E4M3 in either format) of every token: 1.0; "first": 1.0 in each tile's first token
@@ -258,3 +295,81 @@ def test_mass_rows_that_attended_to_nothing_over_unwritten_pages(fmt, nq):
     assert st == 0
     assert torch.equal(got[1, :200], before[1, :200])
     assert torch.all((got[0, :300].double() - want[0, :300]).abs() <= tol[0, :300])
+
+
+# ---------------------------------------------------------------- sizes and bounds
+def loose(dc, blocks):
+    """The same batch under a table and a bound far beyond its lengths, as a captured graph has them."""
+    table = torch.full((dc.batch.batch, blocks), -1, dtype=torch.int32, device="cuda")
+    table[:, :dc.batch.block_table.shape[1]] = dc.batch.block_table
+    dc.batch.block_table, dc.batch.max_seq_len = table, 64 * blocks
+    return dc
+
+
+@pytest.mark.parametrize("invariant", [False, True])
+def test_dense_prompt_chunk_of_2048_rows(invariant):
+    case = synth.make_case("edge_chunk", seq_lens=[4300], nq=2048, seed=510, latent_format=NV)
+    prev = binding.batch_invariant(invariant)
+    try:
+        out, lse, st = run_dense(case, synth.device_case(case))
+    finally:
+        binding.batch_invariant(prev)
+    assert st == 0
+    check(case, out, lse, rows=[0, 1, 479, 480, 1023, 1587, 1588, 2047])
+
+
+@pytest.mark.parametrize("fmt", [FP8, NV])
+def test_dense_context_of_150001_tokens(fmt):
+    case = synth.make_case("edge_long", seq_lens=[150_001], seed=511, latent_format=fmt)
+    out, lse, st = run_dense(case, synth.device_case(case))
+    assert st == 0
+    check(case, out, lse)
+
+
+@pytest.mark.parametrize("invariant", [False, True])
+def test_dense_under_a_loose_bound(invariant):
+    case = synth.make_case("edge_loose", seq_lens=[700, 0, 4100], nq=2, seed=512, latent_format=NV)
+    prev = binding.batch_invariant(invariant)
+    try:
+        out, lse, st = run_dense(case, loose(synth.device_case(case), 2048))
+    finally:
+        binding.batch_invariant(prev)
+    assert st == 0
+    check(case, out, lse)
+
+
+@pytest.mark.parametrize("nq,k", [(1, 0), (3, 0), (1, 150), (3, 150)])
+def test_mass_under_a_loose_bound(nq, k):
+    case = synth.make_case("edge_mass_loose", seq_lens=[700, 5, 4100], nq=nq, seed=513, latent_format=NV)
+    idx = None
+    if k:
+        idx = torch.full((case.rows, k), -1, dtype=torch.int32)
+        for r, vis in enumerate(case.row_lens()):
+            n = min(k, int(vis))
+            idx[r, :n] = torch.randperm(int(vis), generator=torch.Generator().manual_seed(r))[:n].to(torch.int32)
+    lse = plain_lse(case, idx)
+    before = torch.rand((3, 64 * 2048 + 5), generator=torch.Generator().manual_seed(8))
+    want, tol = plain_mass(case, before, lse, idx)
+    got, st = run_mass(case, loose(synth.device_case(case), 2048), lse, before, idx, in_place=True)
+    assert st == 0
+    for b, L in enumerate(case.seq_lens):
+        assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
+        assert torch.equal(got[b, L:], before[b, L:])
+
+
+@pytest.mark.parametrize("nq,k", [(512, 0), (300, 40)])
+def test_mass_of_a_prompt_chunk(nq, k):
+    case = synth.make_case("edge_mass_chunk", seq_lens=[900, 310], nq=nq, seed=514, latent_format=NV)
+    idx = None
+    if k:
+        idx = torch.full((case.rows, k), -1, dtype=torch.int32)
+        for r, vis in enumerate(case.row_lens()):
+            n = min(k, int(vis))
+            idx[r, :n] = torch.randperm(int(vis), generator=torch.Generator().manual_seed(r))[:n].to(torch.int32)
+    lse = plain_lse(case, idx)
+    before = torch.rand((2, case.max_len + 3), generator=torch.Generator().manual_seed(9))
+    want, tol = plain_mass(case, before, lse, idx)
+    got, st = run_mass(case, synth.device_case(case), lse, before, idx)
+    assert st == 0
+    for b, L in enumerate(case.seq_lens):
+        assert torch.all((got[b, :L].double() - want[b, :L]).abs() <= tol[b, :L]), b
