@@ -225,7 +225,7 @@ def _structs(batch: Batch, *caches: PagedCache):
 
 
 def _status(status) -> int | None:
-    if status.dtype not in _I32 or status.numel() < 1:
+    if status is not None and (status.dtype not in _I32 or status.numel() < 1):
         raise ValueError(f"status: expected one int32, got {list(status.shape)} of {status.dtype}")
     return _ptr(status)
 

@@ -121,3 +121,11 @@ def test_status_words(lib, shape, dtype):
 def test_a_selection_of_no_entries(lib):
     """An empty idx has no address, which the library would take for "every visible token"."""
     refused(lib, calls(idx=Tensor((6, 0), torch.int32))[2])
+
+
+def test_no_status_word_is_left_to_the_library(lib):
+    """Which refuses it by its own code."""
+    none = {**arguments(), "status": None}
+    for call in calls(**none):
+        call()
+    assert lib.calls == 4
