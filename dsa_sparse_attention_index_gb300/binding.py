@@ -369,7 +369,8 @@ def cache_evict(cache: PagedCache, batch: Batch, mass, keep: int, sink: int, rec
 
 
 def batch_invariant(on: bool) -> bool:
-    """Switch the process-wide batch-invariant mode (fixed 512-token MLA chunks); returns the previous one."""
+    """Switch the process-wide batch-invariant mode (MLA chunks of 512 selected tokens, dense parts of 3,840 tokens);
+    returns the previous one."""
     return bool(lib().dsa_batch_invariant(1 if on else 0))
 
 

@@ -19,6 +19,11 @@
 //     in it, the conversion instructions widen to it in a third of the
 //     instructions that bf16 takes, and P keeps 11 bits.  query.cu turns Q into
 //     fp16 times a power of two a head.
+//   * Two roundings to fp16 are choices: P's as an operand (its sum, the
+//     normaliser, is taken in fp32 before) and a partial's.  Each is off by 2^-11 of
+//     the weighted mean of |c| at most, where the bf16 output's own rounding takes
+//     2^-8 of the value; a partial in fp32 would double the workspace and what the
+//     merge reads.  Below 2^-14 of a latent's unit a partial's step is 2^-24.
 //   * warps 4..12, one per 64-dim block: two lanes a token, 16-byte loads a whole
 //     tile ahead in registers, a token's page looked up two tiles ahead; widened,
 //     stored 128-byte swizzled into one of two tile buffers, which are filled and
@@ -31,11 +36,12 @@
 //     elect.sync; warps 0..3 run the online softmax, one thread per head: P is
 //     2^7 exp(l - reference) in fp16 (full precision down to 2^-21 of a head's
 //     largest weight), its fp32 sum the normaliser; O^T is rescaled, 32 heads at a
-//     time, only where a maximum grew by more than 2^8.
+//     time, only where a maximum grew by more than 2^8.  Tokens behind a row's last and
+//     those of a page outside the pool are masked.
 // What bounds it: the shared-memory port.  A tile's MMAs read 272 KB (QK^T 32 x
 // (4 KB of Q + 1.5 KB of keys) + 4 x 1.5 KB, PV 12 x (4 KB of values + 3 KB of
 // P)) and its stores and polls take about 85 KB: 2,800 cycles at 128 B a cycle,
-// of which the measured 1.6 us use 88 % (32 contexts of 8K to 64K tokens, NVFP4:
+// of which the measured 1.6 us use 86 % (32 contexts of 8K to 64K tokens, NVFP4:
 // 272 us, 906 TFLOP/s, 0.47 of the measured bf16 burst rate).  The tensor pipe is
 // active 47 % of the time.
 #include <algorithm>
@@ -76,9 +82,9 @@ constexpr int kMaxGrid = 256;                          // CTAs the workspace is 
 constexpr int kInvariantTiles = 80;                    // tiles per part in the batch-invariant mode
 
 constexpr int kOffQ = 0;
-constexpr int kOffTile = kOffQ + kQSmemBlocks * kQBlockBytes;  // 86,016
-constexpr int kOffP = kOffTile + kBufs * kTileBytes;           // 196,608
-constexpr int kOffAlpha = kOffP + kPBytes;                     // 229,376
+constexpr int kOffTile = kOffQ + kQSmemBlocks * kQBlockBytes;  // 98,304
+constexpr int kOffP = kOffTile + kBufs * kTileBytes;           // 208,896
+constexpr int kOffAlpha = kOffP + kPBytes;                     // 221,184
 constexpr int kOffBars = kOffAlpha + 512 + 16;
 constexpr int kNumBars = 4 * kBufs + 11;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;              // TMEM slot, abort flag, scan scratch

@@ -22,17 +22,21 @@
 //   * warps 4..15 (thread = token, the TMEM lane; three sets of four warps, 192
 //     dims each) widen them exactly to fp16; a set's three blocks are one step of
 //     the MMA issuer (a step a block, or two sets, left it waiting).
-//   * warps 0..3, one thread a token: sum over heads of 2^(s c - lse c'), from
-//     one of two S tiles in TMEM while the next is computed.
+//   * warps 0..3, one thread a token: sum over heads of 2^(s c_h - lse_h log2 e), from
+//     one of two S tiles in TMEM while the next is computed (c_h: log2 units per unit
+//     of S, a factor a head).  The exponential is ex2.approx, right to 2^-22, in whose
+//     argument the fp32 products' sum is the larger error.  A token that the row does
+//     not see, or whose page lies outside the pool, gets 0.
 // With one row per sequence and no selection the kernel adds the running total
 // itself; otherwise the rows' weights go to the workspace and a second kernel
 // adds them, row after row, so the order of the sums is fixed:
 // weights_reduce_kernel (every visible token) or weights_scatter_kernel (the
 // selected ones: a CTA owns 4,096 tokens of a sequence in shared memory).
-// What bounds it: issue and latency in the converters and the MMA issuer (per
-// tile about 7,700 warp instructions, 42 % of the issue slots; the tensor pipe is
-// active 37 % of the time).  16 contexts of 16K to 64K tokens, NVFP4: 89 us, 815
-// TFLOP/s, 2.6 TB/s; 64 rows of one 32,770-token context: 251 us, 921 TFLOP/s.
+// What bounds it: a set's three key blocks exist once, so its converters and its
+// MMAs take turns (per tile about 8,000 warp instructions, 42 % of the issue slots;
+// the tensor pipe is active 36 % of the time).  16 contexts of 16K to 64K tokens,
+// NVFP4: 89 us, 815 TFLOP/s, 2.7 TB/s; 64 rows of one 32,770-token context: 254 us,
+// 912 TFLOP/s.
 #include <algorithm>
 #include <atomic>
 

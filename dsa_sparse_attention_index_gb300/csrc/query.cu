@@ -13,8 +13,11 @@
 // as zeros, so that NaN or infinities in a masked row's query stay out of the sums.
 //
 // A warp a head and no barrier: 72 16-byte pieces, all loaded before the maximum is
-// taken; the kernel that follows sets itself up meanwhile.  (Converting inside
-// that kernel cost its softmax warps 5 us for every row a CTA touched.)
+// taken; the kernel that follows sets itself up meanwhile.  Bound by latency: 32
+// rows take 5.3 us with cold caches.  A whole call over one row of 997 tokens takes
+// 16.5 us with it and took 19.5 with a CTA, a barrier and one scale a row; converting
+// inside the kernel that follows cost its softmax warps 5 us for every row a CTA
+// touched.
 #include "common.cuh"
 #include "internal.h"
 

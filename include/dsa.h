@@ -348,7 +348,9 @@ dsa_status_t dense_mla_decode(const dsa_paged_cache_t* cache, const dsa_batch_t*
  *             table entry outside 0..num_blocks-1 for the tokens of its page
  *   mass_in   device fp32 [batch][ld_mass] or NULL (zeros);  mass_out likewise, mass_in itself
  *             (adding in place) or a buffer that does not overlap it;  ld_mass >= max_seq_len
- *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B aligned
+ *   workspace >= dsa_attention_mass_workspace_size(rows, batch->max_seq_len, k) bytes, 256-B aligned:
+ *             the fp16 queries, 108 KB a row, and an fp32 weight for each of the row's k entries or,
+ *             with idx NULL, max_seq_len tokens (2,048 rows of a 153,600-token bound: 0.23 + 1.26 GB)
  * Two launches with one row per sequence and idx NULL, else three.  Lengths as for
  * dense_mla_decode; max_seq_len up to 2^23, else DSA_ERR_UNSUPPORTED.
  */
@@ -402,12 +404,14 @@ dsa_status_t dsa_cache_evict(const dsa_paged_cache_t* cache, const dsa_batch_t* 
  * each row the same result whatever the batch; the sparse MLA splits a row's
  * tokens into chunks whose number depends on the number of rows (to fill the
  * SMs), and the merge of the chunks rounds differently for a different split.
- * on != 0 fixes the chunks at 512 tokens for every later call in this process
- * (all threads and devices), so out and lse of a row are bitwise the same in
- * any batch, at the cost of fewer CTAs for small batches.  The workspace
- * sizes reported by sparse_mla_workspace_size and dsa_workspace_size follow
+ * on != 0 fixes the chunks at 512 selected tokens, and the dense attention's parts
+ * at 3,840 tokens, for every later call in this process (all threads and devices),
+ * so out and lse of a row are bitwise the same in any batch, at the cost of fewer
+ * CTAs for small batches.  The workspace sizes reported by
+ * sparse_mla_workspace_size, dsa_workspace_size and dense_mla_workspace_size follow
  * the mode at the time of the query: set the mode first, and do not change it
- * while other threads launch.  Returns the previous setting; never fails.
+ * while other threads launch (a call that needs more than it was given refuses
+ * its workspace).  Returns the previous setting; never fails.
  */
 int32_t dsa_batch_invariant(int32_t on);
 
