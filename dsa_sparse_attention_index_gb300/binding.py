@@ -20,6 +20,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_BOUNDS, ERR_TIMEOUT, ERR_CUDA, ERR_WOR
 KEY_FP8_E4M3, KEY_MXFP4, KEY_MXFP4_NATIVE = 0, 1, 2
 LATENT_FP8_E4M3, LATENT_NVFP4 = 0, 1
 BLOCK, IDX_HEADS, IDX_DIM, MLA_HEADS, LATENT, VALUE, MAX_TOPK = 64, 32, 128, 96, 576, 512, 2048
+DELTA_DIM = 128
 
 
 class DsaError(RuntimeError):
@@ -43,6 +44,17 @@ class BatchT(ctypes.Structure):
                 ("queries_per_seq", ctypes.c_int32), ("max_seq_len", ctypes.c_int32)]
 
 
+class StatePoolT(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("slot_stride", ctypes.c_int64), ("num_slots", ctypes.c_int32),
+                ("heads", ctypes.c_int32)]
+
+
+class DeltaRowsT(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "gate", "beta")] + [
+        (n, ctypes.c_int64) for n in ("ld_q", "ld_k", "ld_v", "ld_gate", "ld_beta")] + [
+        ("qk_heads", ctypes.c_int32), ("gate_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 EXPORTS = ["dsa_api_version", "dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launches",
@@ -55,7 +67,8 @@ EXPORTS = ["dsa_api_version", "dsa_status_string", "dsa_last_cuda_error", "dsa_k
            "dsa_cache_evict", "dsa_dcp_sparse_mla_workspace_size", "dsa_dcp_sparse_mla", "dsa_batch_invariant",
            "dsa_workspace_size", "dsa_decode_step", "dsa_cache_append", "dsa_quantize_index_query",
            "dsa_index_frontend", "dsa_frontend_workspace_size", "dsa_decode_step_frontend",
-           "dsa_selftest_wait_timeout"]
+           "dsa_assign_slots", "dsa_cache_append_slots", "gated_delta_decode", "gated_delta_prefill_workspace_size",
+           "gated_delta_prefill", "dsa_selftest_wait_timeout"]
 
 
 def lib():
@@ -68,6 +81,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         pc, pb = ctypes.POINTER(PagedCacheT), ctypes.POINTER(BatchT)
+        ps, pd = ctypes.POINTER(StatePoolT), ctypes.POINTER(DeltaRowsT)
         sig = {
             "dsa_api_version": (i32, []),
             "dsa_status_string": (ctypes.c_char_p, [i32]),
@@ -104,6 +118,11 @@ def lib():
             "dsa_frontend_workspace_size": (sz, [pb, i32]),
             "dsa_decode_step_frontend": (i32, [pc, pb, P, i32, P, f32, P, P, P, P, P, i32, f32, P, P, P, i64, P, P,
                                                P, sz, P, P]),
+            "dsa_assign_slots": (i32, [P, P, i32, P, i32, P, P, i32, P, i32, P, P, P, P, i32, P, P]),
+            "dsa_cache_append_slots": (i32, [pc, P, i32, P, P, P, P]),
+            "gated_delta_decode": (i32, [ps, pd, i32, i32, P, P, P, P, P]),
+            "gated_delta_prefill_workspace_size": (sz, [i32, i32, i32]),
+            "gated_delta_prefill": (i32, [ps, pd, P, i32, i32, P, P, P, P, sz, P, P]),
             "dsa_selftest_wait_timeout": (i32, [i64, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -436,6 +455,128 @@ def cache_append(cache: PagedCache, batch: Batch, new_latent, new_index_key, sta
     c, b = cache.struct(), batch.struct()
     _check(lib().dsa_cache_append(ctypes.byref(c), ctypes.byref(b), _ptr(new_latent), _ptr(new_index_key),
                                   _ptr(status), _stream(stream)), "dsa_cache_append")
+
+
+def assign_slots(cached_lens, new_lens, free_blocks, free_count, num_blocks: int, block_table, seq_lens, row_starts,
+                 positions, slots, free_left, status, stream=None):
+    """Pages off the free stack and cache slots for every request's new tokens: cached_lens and new_lens int32 [batch],
+    free_blocks int32 [n] with its count in free_count; fills in block_table int32 [batch, max_blocks], seq_lens
+    [batch], row_starts [batch + 1], positions and slots [max_rows] (-1 behind the last row) and free_left."""
+    n, blocks, rows = cached_lens.shape[0], block_table.shape[-1], slots.shape[0]
+    _one_device(cached_lens, new_lens, free_blocks, free_count, block_table, seq_lens, row_starts, positions, slots,
+                free_left, status)
+    _check(lib().dsa_assign_slots(_want("cached_lens", cached_lens, (n,), _I32), _want("new_lens", new_lens, (n,), _I32),
+                                  n, _want("free_blocks", free_blocks, (free_blocks.shape[0],), _I32),
+                                  free_blocks.shape[0], _want("free_count", free_count, (1,), _I32),
+                                  _want("free_left", free_left, (1,), _I32), int(num_blocks),
+                                  _want("block_table", block_table, (n, blocks), _I32), blocks,
+                                  _want("seq_lens", seq_lens, (n,), _I32),
+                                  _want("row_starts", row_starts, (n + 1,), _I32),
+                                  _want("positions", positions, (rows,), _I32), _want("slots", slots, (rows,), _I32),
+                                  rows, _status(status), _stream(stream)), "dsa_assign_slots")
+
+
+def cache_append_slots(cache: PagedCache, slots, new_latent, new_index_key, status, stream=None):
+    """Write new tokens (bf16 bits, [rows, 576] and [rows, 128]) into the cache rows slots [rows]; -1: none."""
+    rows = slots.shape[0]
+    if cache.pool.nbytes < cache.pool.shape[0] * cache.row_stride:
+        raise ValueError(f"pool: {cache.pool.nbytes} bytes for {cache.pool.shape[0]} rows of {cache.row_stride}")
+    c = cache.struct()
+    _one_device(cache.pool, slots, new_latent, new_index_key, status)
+    _check(lib().dsa_cache_append_slots(ctypes.byref(c), _want("slots", slots, (rows,), _I32), rows,
+                                        _want("new_latent", new_latent, (rows, LATENT), _BITS16),
+                                        _want("new_index_key", new_index_key, (rows, IDX_DIM), _BITS16),
+                                        _status(status), _stream(stream)), "dsa_cache_append_slots")
+
+
+@dataclass
+class StatePool:
+    """The recurrent layers' states, fp32 [slots, heads, 128 values, 128 keys] on the GPU: a tensor of its own, or a
+    view into the packed cache's block rows (slots may lie apart)."""
+
+    states: torch.Tensor
+
+    def struct(self) -> StatePoolT:
+        t = self.states
+        if t.dtype not in _F32 or t.dim() != 4 or t.shape[2:] != (DELTA_DIM, DELTA_DIM) or not t.is_cuda or (
+                t.shape[0] and not t[0].is_contiguous()):
+            raise ValueError(f"states: expected float32 [slots, heads, {DELTA_DIM}, {DELTA_DIM}] on the GPU, each slot "
+                             f"contiguous, got {list(t.shape)} of {t.dtype}")
+        stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * DELTA_DIM * DELTA_DIM
+        return StatePoolT(t.data_ptr(), 4 * stride, t.shape[0], t.shape[1])
+
+
+def _strided(name: str, t, shape, dtypes):
+    """The address and the row stride of a tensor whose rows are contiguous but may lie apart."""
+    if t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {list(shape)} of {dtypes[0]}, got {list(t.shape)} of {t.dtype}")
+    if not t.is_cuda or (t.shape[0] and not t[0].is_contiguous()):
+        raise ValueError(f"{name}: expected a CUDA tensor with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else 1 << 40
+
+
+@dataclass
+class DeltaRows:
+    """The rows of a gated delta layer: q and k bf16 bits [rows, qk_heads, 128], v [rows, heads, 128], the log decays
+    gate fp32 [rows, heads, 128] (per key channel) or [rows, heads], beta fp32 [rows, heads].  Rows may lie apart."""
+
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    gate: torch.Tensor
+    beta: torch.Tensor
+    scale: float
+
+    @property
+    def rows(self) -> int:
+        return int(self.v.shape[0])
+
+    def struct(self, heads: int) -> DeltaRowsT:
+        rows, qk = self.rows, self.q.shape[1] if self.q.dim() == 3 else 0
+        wide = self.gate.dim() == 3
+        got = [_strided("q", self.q, (rows, qk, DELTA_DIM), _BITS16), _strided("k", self.k, (rows, qk, DELTA_DIM), _BITS16),
+               _strided("v", self.v, (rows, heads, DELTA_DIM), _BITS16),
+               _strided("gate", self.gate, (rows, heads, DELTA_DIM) if wide else (rows, heads), _F32),
+               _strided("beta", self.beta, (rows, heads), _F32)]
+        return DeltaRowsT(*(p for p, _ in got), *(ld for _, ld in got), qk, DELTA_DIM if wide else 1, float(self.scale))
+
+
+def _delta(pool: StatePool, x: DeltaRows, *others):
+    p = pool.struct()
+    _one_device(pool.states, x.q, x.k, x.v, x.gate, x.beta, *others)
+    return p, x.struct(p.heads)
+
+
+def gated_delta_decode(pool: StatePool, x: DeltaRows, queries_per_seq: int, slots_in, slots_out, out, status,
+                       stream=None):
+    """The gated delta rule for queries_per_seq rows a sequence: states from slots_in int32 [batch] (-1: zeros), the
+    state after each row to slots_out int32 [batch, queries_per_seq] (-1: nowhere); out bf16 bits [rows, heads, 128]."""
+    p, r = _delta(pool, x, slots_in, slots_out, out, status)
+    batch, nq = slots_in.shape[0], int(queries_per_seq)
+    if x.rows != batch * nq:
+        raise ValueError(f"{x.rows} rows for {batch} sequences of {nq}")
+    _check(lib().gated_delta_decode(ctypes.byref(p), ctypes.byref(r), batch, nq, _want("slots_in", slots_in, (batch,), _I32),
+                                    _want("slots_out", slots_out, (batch, nq), _I32),
+                                    _want("out", out, (x.rows, p.heads, DELTA_DIM), _BITS16), _status(status),
+                                    _stream(stream)), "gated_delta_decode")
+
+
+def gated_delta_prefill_workspace_size(rows: int, batch: int, heads: int) -> int:
+    return int(lib().gated_delta_prefill_workspace_size(rows, batch, heads))
+
+
+def gated_delta_prefill(pool: StatePool, x: DeltaRows, row_starts, slots_in, slots_out, out, workspace, status,
+                        stream=None):
+    """The gated delta rule over ragged prompts: sequence b has the rows row_starts[b] .. row_starts[b + 1] - 1 (int32
+    [batch + 1]); its state comes from slots_in[b] (-1: zeros) and goes to slots_out[b] (-1: nowhere)."""
+    p, r = _delta(pool, x, row_starts, slots_in, slots_out, out, workspace, status)
+    batch = slots_in.shape[0]
+    _check(lib().gated_delta_prefill(ctypes.byref(p), ctypes.byref(r),
+                                     _want("row_starts", row_starts, (batch + 1,), _I32), batch, x.rows,
+                                     _want("slots_in", slots_in, (batch,), _I32),
+                                     _want("slots_out", slots_out, (batch,), _I32),
+                                     _want("out", out, (x.rows, p.heads, DELTA_DIM), _BITS16), _ptr(workspace),
+                                     workspace.nbytes, _status(status), _stream(stream)), "gated_delta_prefill")
 
 
 def quantize_index_query(q_bf16, head_w, q_index, head_w_out, stream=None):

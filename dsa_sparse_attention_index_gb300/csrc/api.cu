@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "delta.cuh"
 #include "internal.h"
 
 namespace dsa {
@@ -531,6 +532,109 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_batch_t*
     return DSA_ERR_INVALID_ARG;
   return launch_cache_append(*cache, *batch, new_latent, new_index_key, dev_status,
                              static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_cache_append_slots(const dsa_paged_cache_t* cache, const int32_t* slots, int32_t rows,
+                                    const uint16_t* new_latent, const uint16_t* new_index_key, int32_t* dev_status,
+                                    void* stream) {
+  dsa_status_t s;
+  if ((s = check_cache(cache)) != DSA_OK) return s;
+  if (rows < 0 || !dev_status) return DSA_ERR_INVALID_ARG;
+  if (rows > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  if (rows == 0) return DSA_OK;
+  if (!slots || !new_latent || !new_index_key || !aligned(slots, 4) || !aligned(new_latent, 16) ||
+      !aligned(new_index_key, 16))
+    return DSA_ERR_INVALID_ARG;
+  return launch_cache_append_slots(*cache, slots, rows, new_latent, new_index_key, dev_status,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                              const int32_t* free_blocks, int32_t free_capacity, const int32_t* free_count,
+                              int32_t* free_left, int32_t num_blocks, int32_t* block_table, int32_t max_blocks,
+                              int32_t* seq_lens, int32_t* row_starts, int32_t* positions, int32_t* slots,
+                              int32_t max_rows, int32_t* dev_status, void* stream) {
+  if (batch < 0 || max_rows < 0 || free_capacity < 0 || num_blocks < 1 || max_blocks < 1 || !dev_status)
+    return DSA_ERR_INVALID_ARG;
+  // positions and slots are counted in 32 bits
+  if (batch > (1 << 24) || max_rows > (1 << 30) || max_blocks > (1 << 24) || num_blocks > (1 << 25))
+    return DSA_ERR_UNSUPPORTED;
+  if (!free_count || !free_left || !row_starts || (free_capacity > 0 && !free_blocks) ||
+      (max_rows > 0 && (!positions || !slots)))
+    return DSA_ERR_INVALID_ARG;
+  if (batch > 0 && (!cached_lens || !new_lens || !block_table || !seq_lens || seq_lens == new_lens))
+    return DSA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)cached_lens, (const void*)new_lens, (const void*)free_blocks,
+                        (const void*)free_count, (const void*)free_left, (const void*)block_table,
+                        (const void*)seq_lens, (const void*)row_starts, (const void*)positions, (const void*)slots})
+    if (!aligned(p, 4)) return DSA_ERR_INVALID_ARG;
+  return launch_assign_slots(cached_lens, new_lens, batch, free_blocks, free_capacity, free_count, free_left, num_blocks,
+                             block_table, max_blocks, seq_lens, row_starts, positions, slots, max_rows, dev_status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+dsa_status_t check_delta(const dsa_state_pool_t* pool, const dsa_delta_rows_t* x, int64_t rows, int32_t batch,
+                         const int32_t* slots_in, const int32_t* slots_out, const uint16_t* out) {
+  if (!pool || !x || rows < 0 || batch < 0) return DSA_ERR_INVALID_ARG;
+  if (pool->heads < 1 || pool->num_slots < 1 || !pool->base || !aligned(pool->base, 128) || pool->slot_stride % 128 ||
+      pool->slot_stride < (int64_t)pool->heads * kStateFloats * 4)
+    return DSA_ERR_INVALID_ARG;
+  if (x->qk_heads < 1 || pool->heads % x->qk_heads || (x->gate_dim != 1 && x->gate_dim != kDeltaDim))
+    return DSA_ERR_INVALID_ARG;
+  if (pool->heads > 4096 || rows > (1 << 24) || (int64_t)batch * pool->heads > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  if (batch == 0) return DSA_OK;
+  if (!slots_in || !slots_out || !aligned(slots_in, 4) || !aligned(slots_out, 4)) return DSA_ERR_INVALID_ARG;
+  if (rows == 0) return DSA_OK;
+  const bool wide = x->gate_dim == kDeltaDim;
+  if (!x->q || !x->k || !x->v || !x->gate || !x->beta || !out || !aligned(x->q, 16) || !aligned(x->k, 16) ||
+      !aligned(x->v, 16) || !aligned(x->gate, wide ? 16 : 4) || !aligned(x->beta, 4) || !aligned(out, 16))
+    return DSA_ERR_INVALID_ARG;
+  const int64_t qk = (int64_t)x->qk_heads * kDeltaDim, v = (int64_t)pool->heads * kDeltaDim;
+  if (x->ld_q < qk || x->ld_k < qk || x->ld_v < v || x->ld_gate < (int64_t)pool->heads * x->gate_dim ||
+      x->ld_beta < pool->heads || x->ld_q % 8 || x->ld_k % 8 || x->ld_v % 8 || (wide && x->ld_gate % 4))
+    return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+DeltaRows delta_rows(const dsa_state_pool_t& pool, const dsa_delta_rows_t& x) {
+  return DeltaRows{x.q,    x.k,    x.v,       x.gate,    x.beta,     x.ld_q,     x.ld_k,
+                   x.ld_v, x.ld_gate, x.ld_beta, pool.heads, x.qk_heads, x.gate_dim, x.scale};
+}
+
+}  // namespace
+
+dsa_status_t gated_delta_decode(const dsa_state_pool_t* pool, const dsa_delta_rows_t* x, int32_t batch,
+                                int32_t queries_per_seq, const int32_t* slots_in, const int32_t* slots_out,
+                                uint16_t* out, int32_t* dev_status, void* stream) {
+  if (queries_per_seq < 1 || !dev_status) return DSA_ERR_INVALID_ARG;
+  const dsa_status_t s = check_delta(pool, x, (int64_t)batch * queries_per_seq, batch, slots_in, slots_out, out);
+  if (s != DSA_OK || batch == 0) return s;
+  const DeltaSeqs seqs{static_cast<float*>(pool->base), pool->slot_stride / 4, pool->num_slots, batch,
+                       batch * queries_per_seq, queries_per_seq, nullptr, slots_in, slots_out, 1, dev_status};
+  return launch_delta_rows(delta_rows(*pool, *x), seqs, out, static_cast<cudaStream_t>(stream));
+}
+
+size_t gated_delta_prefill_workspace_size(int32_t rows, int32_t batch, int32_t heads) {
+  if (rows < 0 || batch < 0 || heads < 1) return 0;
+  return 256;
+}
+
+dsa_status_t gated_delta_prefill(const dsa_state_pool_t* pool, const dsa_delta_rows_t* x, const int32_t* row_starts,
+                                 int32_t batch, int32_t rows, const int32_t* slots_in, const int32_t* slots_out,
+                                 uint16_t* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                 void* stream) {
+  if (!dev_status) return DSA_ERR_INVALID_ARG;
+  const dsa_status_t s = check_delta(pool, x, rows, batch, slots_in, slots_out, out);
+  if (s != DSA_OK || batch == 0) return s;
+  if (!row_starts || !aligned(row_starts, 4)) return DSA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < gated_delta_prefill_workspace_size(rows, batch, pool->heads))
+    return DSA_ERR_WORKSPACE;
+  const DeltaSeqs seqs{static_cast<float*>(pool->base), pool->slot_stride / 4, pool->num_slots, batch, rows, 0,
+                       row_starts, slots_in, slots_out, 0, dev_status};
+  return launch_delta_rows(delta_rows(*pool, *x), seqs, out, static_cast<cudaStream_t>(stream));
 }
 
 dsa_status_t dsa_quantize_index_query(const uint16_t* q_bf16, const float* head_w, int32_t rows, uint8_t* q_index,

@@ -78,35 +78,18 @@ struct AppendArgs {
 // Named barrier 1 over the 128 threads that write one token (threads 0..127).
 __device__ __forceinline__ void bar_append() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// New token row nr = b * nq + j (token L_b - nq + j) by threads tid = 0..127;
-// `sync` is a barrier over those threads (uniform: every early return below
-// depends on nr alone).
+// Row nr of the new tokens into slot `slot` of block row r.
 template <typename Sync>
-__device__ __forceinline__ void append_row(const AppendArgs& a, int nr, int tid, float* warp_amax, Sync sync) {
+__device__ __forceinline__ void append_token(const AppendArgs& a, int nr, int r, int slot, int tid, float* warp_amax,
+                                             Sync sync) {
   uint8_t* latent_base = a.latent_base;
   uint8_t* index_base = a.index_base;
   const int64_t row_stride = a.row_stride;
-  const int32_t num_blocks = a.num_blocks, key_format = a.key_format, latent_format = a.latent_format;
+  const int32_t key_format = a.key_format, latent_format = a.latent_format;
   const float latent_scale = a.latent_scale;
-  const int32_t* block_table = a.block_table;
-  const int32_t max_blocks = a.max_blocks, nq = a.nq, cap = a.cap;
   const uint16_t* new_latent = a.new_latent;
   const uint16_t* new_key = a.new_key;
-  int32_t* status = a.status;
-  const int b = nr / nq, j = nr % nq, lane = tid & 31, wid = tid >> 5;
-  const int L = a.seq_lens[b];
-  if (L < 0 || L > cap) {
-    if (tid == 0) report(status, DSA_ERR_BOUNDS);
-    return;
-  }
-  const int t = L - nq + j;
-  if (t < 0) return;  // a context shorter than its new rows: nothing to write for this one
-  const int r = block_table[(int64_t)b * max_blocks + t / kBlock];
-  if (r < 0 || r >= num_blocks) {
-    if (tid == 0) report(status, DSA_ERR_BOUNDS);
-    return;
-  }
-  const int slot = t % kBlock;
+  const int lane = tid & 31, wid = tid >> 5;
   const uint16_t* lat = new_latent + (int64_t)nr * kLatent;
   if (latent_format == DSA_LATENT_FP8_E4M3) {
     // latent: 576 codes
@@ -159,10 +142,47 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int nr, int tid,
   }
 }
 
+// New token row nr = b * nq + j (token L_b - nq + j) by threads tid = 0..127;
+// `sync` is a barrier over those threads (uniform: every early return below
+// depends on nr alone).
+template <typename Sync>
+__device__ __forceinline__ void append_row(const AppendArgs& a, int nr, int tid, float* warp_amax, Sync sync) {
+  const int32_t num_blocks = a.num_blocks;
+  const int32_t* block_table = a.block_table;
+  const int32_t max_blocks = a.max_blocks, nq = a.nq, cap = a.cap;
+  int32_t* status = a.status;
+  const int b = nr / nq, j = nr % nq;
+  const int L = a.seq_lens[b];
+  if (L < 0 || L > cap) {
+    if (tid == 0) report(status, DSA_ERR_BOUNDS);
+    return;
+  }
+  const int t = L - nq + j;
+  if (t < 0) return;  // a context shorter than its new rows: nothing to write for this one
+  const int r = block_table[(int64_t)b * max_blocks + t / kBlock];
+  if (r < 0 || r >= num_blocks) {
+    if (tid == 0) report(status, DSA_ERR_BOUNDS);
+    return;
+  }
+  append_token(a, nr, r, t % kBlock, tid, warp_amax, sync);
+}
+
 // One CTA per new token row.
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
   __shared__ float warp_amax[kAppendThreads / 32];
   append_row(a, blockIdx.x, threadIdx.x, warp_amax, [] { __syncthreads(); });
+}
+
+// One CTA per new token row, its slot given: -1 is a padding row.
+__global__ void __launch_bounds__(kAppendThreads) cache_append_slots_kernel(const AppendArgs a, const int32_t* slots) {
+  __shared__ float warp_amax[kAppendThreads / 32];
+  const int s = slots[blockIdx.x];
+  if (s == -1) return;
+  if (s < 0 || s / kBlock >= a.num_blocks) {
+    if (threadIdx.x == 0) report(a.status, DSA_ERR_BOUNDS);
+    return;
+  }
+  append_token(a, blockIdx.x, s / kBlock, s % kBlock, threadIdx.x, warp_amax, [] { __syncthreads(); });
 }
 
 // One warp per (row, head): 128 elements, four per lane.
@@ -538,6 +558,17 @@ dsa_status_t launch_cache_append(const dsa_paged_cache_t& c, const dsa_batch_t& 
                      bt.queries_per_seq, cap, new_latent, new_key, status};
   count_launches(1);
   cache_append_kernel<<<rows, kAppendThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+dsa_status_t launch_cache_append_slots(const dsa_paged_cache_t& c, const int32_t* slots, int rows,
+                                       const uint16_t* new_latent, const uint16_t* new_key, int32_t* status,
+                                       cudaStream_t st) {
+  uint8_t* base = static_cast<uint8_t*>(c.base);
+  const AppendArgs a{base + c.latent_off, base + c.index_off, c.row_stride, c.num_blocks, c.key_format,
+                     c.latent_format, c.latent_scale, nullptr, 0, nullptr, 1, 0, new_latent, new_key, status};
+  count_launches(1);
+  cache_append_slots_kernel<<<rows, kAppendThreads, 0, st>>>(a, slots);
   return launch_status();
 }
 

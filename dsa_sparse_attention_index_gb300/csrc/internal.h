@@ -118,6 +118,15 @@ dsa_status_t launch_cache_evict(const dsa_paged_cache_t& src, const dsa_batch_t&
 dsa_status_t launch_wait_selftest(int64_t limit_ns, int32_t* status, cudaStream_t st);
 dsa_status_t launch_cache_append(const dsa_paged_cache_t& c, const dsa_batch_t& bt, const uint16_t* new_latent,
                                  const uint16_t* new_key, int32_t* status, cudaStream_t st);
+// The same writes into given slots (block row * 64 + place; -1: none), ragged batches.
+dsa_status_t launch_cache_append_slots(const dsa_paged_cache_t& c, const int32_t* slots, int rows,
+                                       const uint16_t* new_latent, const uint16_t* new_key, int32_t* status,
+                                       cudaStream_t st);
+// Pages and slots of a step's new tokens (slots.cu).
+dsa_status_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, int batch, const int32_t* free_blocks,
+                                 int free_capacity, const int32_t* free_count, int32_t* free_left, int num_blocks,
+                                 int32_t* table, int max_blocks, int32_t* seq_lens, int32_t* starts, int32_t* positions,
+                                 int32_t* slots, int max_rows, int32_t* status, cudaStream_t st);
 // The fused indexer front end: RMSNorm of c_q [rows][dim], the projection by
 // w_iq [4096][dim] (bf16), FP8 query codes and folded head weights, optional
 // fp32 projected values, and the new tokens into the cache; one launch.

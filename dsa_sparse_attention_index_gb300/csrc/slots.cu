@@ -1,0 +1,192 @@
+// slots.cu — where a step's new tokens go: pages off the free stack into the
+// block table, lengths, first rows, positions and cache slots.
+//
+// With c_i cached and n_i new tokens, request i has have_i = ceil(c_i / 64)
+// pages and needs need_i = ceil((c_i + n_i) / 64).  Its rows start at R_i =
+// sum_{j<i} n_j and its fresh pages come off the stack behind the F_i =
+// sum_{j<i} (need_j - have_j) pages of the requests before it.  Row r of
+// request i is position p = c_i + r - R_i on page j = p / 64: a page of the
+// table for j < have_i, else entry count - 1 - (F_i + j - have_i) of the stack.
+// The row with p % 64 = 0 is the only first one of a fresh page: it puts the
+// page into the table.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kSlotThreads = 1024;
+constexpr int kPer = 2;                             // requests a thread scans at once
+constexpr int kSlotTile = kSlotThreads * kPer;      // requests of a tile
+constexpr int kSlotRows = 4;                        // rows a thread places at once
+
+struct SlotArgs {
+  const int32_t *cached, *fresh;
+  int32_t batch;
+  const int32_t* free_blocks;
+  int32_t free_capacity;
+  const int32_t* free_count;
+  int32_t* free_left;
+  int32_t num_blocks;
+  int32_t* table;
+  int32_t max_blocks;
+  int32_t *seq_lens, *starts, *positions, *slots;
+  int32_t max_rows;
+  int32_t* status;
+};
+
+// Request i's lengths; one that does not fit its table row takes part with none.
+__device__ __forceinline__ int2 lengths_of(const SlotArgs& a, int i) {
+  const int c = a.cached[i], n = a.fresh[i];
+  if (c < 0 || n < 0 || (int64_t)c + n > (int64_t)a.max_blocks * kBlock) return make_int2(0, -1);
+  return make_int2(c, n);
+}
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
+
+// One cluster.  Every CTA scans the requests (a tile of 2,048 at a time, kept
+// in shared memory) and places its share of the rows; nothing that the caller
+// may pass as input and output at once (lengths, the stack's count) is written
+// before the whole cluster has read it.
+__global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotArgs a) {
+  namespace cg = cooperative_groups;
+  __shared__ int s_start[kSlotTile + 1], s_cached[kSlotTile], s_page[kSlotTile];
+  __shared__ long long s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  int count = *a.free_count;
+  if (count < 0 || count > a.free_capacity) {
+    if (cta == 0 && tid == 0) report(a.status, DSA_ERR_BOUNDS);
+    count = 0;
+  }
+  // this CTA's rows: whole groups of 4 rows a thread, in turns over the cluster
+  long long rows0 = 0, pages0 = 0;  // of the tiles before
+  for (int base = 0; base < a.batch; base += kSlotTile) {
+    // scan of (rows, pages), rows in the upper half: either sum of a tile stays below 2^42 and 2^36
+    int c[kPer], n[kPer];
+    long long rsum = 0, psum = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int i = base + tid * kPer + e;
+      c[e] = n[e] = 0;
+      if (i < a.batch) {
+        const int2 v = lengths_of(a, i);
+        if (v.y < 0 && cta == 0) report(a.status, DSA_ERR_BOUNDS);
+        c[e] = v.x, n[e] = max(v.y, 0);
+      }
+      rsum += n[e];
+      psum += pages_of(c[e] + n[e]) - pages_of(c[e]);
+    }
+    long long ri = rsum, pi = psum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long r = __shfl_up_sync(0xffffffffu, ri, o), p = __shfl_up_sync(0xffffffffu, pi, o);
+      if (lane >= o) ri += r, pi += p;
+    }
+    __shared__ long long s_warp2[32];
+    if (lane == 31) s_warp[wid] = ri, s_warp2[wid] = pi;
+    __syncthreads();
+    long long rt = s_warp[lane], pt = s_warp2[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long r = __shfl_up_sync(0xffffffffu, rt, o), p = __shfl_up_sync(0xffffffffu, pt, o);
+      if (lane >= o) rt += r, pt += p;
+    }
+    const long long rall = __shfl_sync(0xffffffffu, rt, 31), pall = __shfl_sync(0xffffffffu, pt, 31);
+    const long long rw = wid ? __shfl_sync(0xffffffffu, rt, wid - 1) : 0;
+    const long long pw = wid ? __shfl_sync(0xffffffffu, pt, wid - 1) : 0;
+    long long r = rows0 + rw + ri - rsum, p = pages0 + pw + pi - psum;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int j = tid * kPer + e;
+      s_start[j] = (int)min(r, (long long)a.max_rows);
+      s_cached[j] = c[e];
+      s_page[j] = (int)min(p, (long long)INT32_MAX);
+      if (cta == 0 && base + j < a.batch) a.starts[base + j] = s_start[j];
+      r += n[e];
+      p += pages_of(c[e] + n[e]) - pages_of(c[e]);
+    }
+    if (tid == kSlotThreads - 1) s_start[kSlotTile] = (int)min(r, (long long)a.max_rows);
+    __syncthreads();
+    // the tile's rows, four at a time, in turns over the cluster's threads
+    const int first = s_start[0], last = s_start[kSlotTile];
+    const int step = ctas * kSlotThreads * kSlotRows;
+    for (int g = first + (cta * kSlotThreads + tid) * kSlotRows; g < last; g += step) {
+      int lo = 0, hi = kSlotTile;  // the last request with start <= g: start[lo] <= g < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= g) lo = mid; else hi = mid;
+      }
+#pragma unroll
+      for (int e = 0; e < kSlotRows; ++e) {
+        const int row = g + e;
+        if (row >= last) break;
+        while (s_start[lo + 1] <= row) ++lo;
+        const int pos = s_cached[lo] + row - s_start[lo], j = pos / kBlock, have = pages_of(s_cached[lo]);
+        const int64_t entry = (int64_t)(base + lo) * a.max_blocks + j;
+        int page;
+        if (j < have) {
+          page = a.table[entry];
+        } else {
+          const long long at = (long long)count - 1 - ((long long)s_page[lo] + j - have);
+          page = at >= 0 ? a.free_blocks[at] : -1;
+        }
+        if (page < 0 || page >= a.num_blocks) {
+          report(a.status, DSA_ERR_BOUNDS);
+          page = -1;
+        } else if (j >= have && pos % kBlock == 0) {
+          a.table[entry] = page;
+        }
+        a.positions[row] = pos;
+        a.slots[row] = page < 0 ? -1 : page * kBlock + pos % kBlock;
+      }
+    }
+    rows0 += rall, pages0 += pall;
+    __syncthreads();
+  }
+  const int total = (int)min(rows0, (long long)a.max_rows);
+  for (int r = total + cta * kSlotThreads + tid; r < a.max_rows; r += ctas * kSlotThreads) a.positions[r] = a.slots[r] = -1;
+  if (ctas > 1) cg::this_cluster().sync();
+  for (int i = cta * kSlotThreads + tid; i < a.batch; i += ctas * kSlotThreads) {
+    const int2 v = lengths_of(a, i);
+    a.seq_lens[i] = v.y < 0 ? 0 : v.x + v.y;
+  }
+  if (cta == 0 && tid == 0) {
+    a.starts[a.batch] = total;
+    if (rows0 > a.max_rows || pages0 > count) report(a.status, DSA_ERR_BOUNDS);
+    *a.free_left = (int)max(0ll, (long long)count - pages0);
+  }
+}
+
+}  // namespace
+
+dsa_status_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, int batch, const int32_t* free_blocks,
+                                 int free_capacity, const int32_t* free_count, int32_t* free_left, int num_blocks,
+                                 int32_t* table, int max_blocks, int32_t* seq_lens, int32_t* starts, int32_t* positions,
+                                 int32_t* slots, int max_rows, int32_t* status, cudaStream_t st) {
+  const SlotArgs a{cached,     fresh,    batch,  free_blocks, free_capacity, free_count, free_left, num_blocks, table,
+                   max_blocks, seq_lens, starts, positions,   slots,         max_rows,   status};
+  const int ctas = max_rows > 4 * kSlotThreads * kSlotRows ? 8 : max_rows > kSlotThreads * kSlotRows ? 4 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSlotThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, assign_slots_kernel, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_status(e);
+  }
+  count_launches(1);
+  return launch_status();
+}
+
+}  // namespace dsa

@@ -27,6 +27,9 @@
  *   dsa_attention_mass       attention weight per cached token, added to a running total
  *   dsa_cache_evict          eviction by that total into fresh pages
  *   dsa_decode_step(_bf16)   the three stages fused on one stream
+ *   gated_delta_decode, gated_delta_prefill   the recurrent layers' gated delta rule over states by slot
+ *   dsa_assign_slots         pages and cache slots of a step's new tokens, from the requests' lengths
+ *   dsa_cache_append_slots   new tokens into given slots (ragged batches)
  *   dsa_cache_append, dsa_quantize_index_query   the step's front end
  *   dsa_index_frontend       the fused indexer front end (norm, projection,
  *                            FP8 query, new tokens into the cache)
@@ -74,6 +77,7 @@ extern "C" {
 #define DSA_MAX_TOPK 2048        /* top-k of the model; also the largest k accepted */
 #define DSA_MAX_QUERIES_PER_SEQ 2048 /* draft rows (1..4) or a prefill chunk (a multiple of 4) */
 #define DSA_TOPK_NOALLOC_MAX_ROWS 64  /* row limit of dsa_topk_noalloc */
+#define DSA_DELTA_DIM 128        /* key and value width of a gated delta head */
 #define DSA_DCP_MAX_SHARDS 8          /* shards of dsa_dcp_topk and dsa_dcp_sparse_mla */
 #define DSA_DCP_MAX_SHARD_TOKENS 65536 /* tokens of one row a shard may hold (16-bit local position) */
 
@@ -137,6 +141,30 @@ typedef struct dsa_batch {
                                   seq_len - (nq - 1) + j tokens (causal) */
   int32_t max_seq_len;         /* host-known upper bound of seq_lens; sizes grids and scores */
 } dsa_batch_t;
+
+/* The recurrent layers' states: slot s holds one sequence's, fp32 [heads][128 values][128 keys]
+ * at base + s * slot_stride; a pool of its own, or a part of the packed cache's block rows. */
+typedef struct dsa_state_pool {
+  void* base;              /* device address of slot 0's states; 128-byte aligned */
+  int64_t slot_stride;     /* bytes between slots; multiple of 128, at least heads * 65536 */
+  int32_t num_slots;
+  int32_t heads;           /* value heads */
+} dsa_state_pool_t;
+
+/* The rows of a gated delta layer.  Query and key head h * qk_heads / heads belong to value head
+ * h; ld_* are elements between rows, so the tensors may be parts of one projection's output. */
+typedef struct dsa_delta_rows {
+  const uint16_t* q;       /* device bf16 bits [rows][qk_heads][128]; 16-byte aligned, ld_q a multiple of 8 */
+  const uint16_t* k;       /* likewise */
+  const uint16_t* v;       /* device bf16 bits [rows][heads][128]; 16-byte aligned, ld_v a multiple of 8 */
+  const float* gate;       /* device fp32 log decay [rows][heads][gate_dim]; gate_dim 128: 16-byte aligned,
+                              ld_gate a multiple of 4 */
+  const float* beta;       /* device fp32 [rows][heads] */
+  int64_t ld_q, ld_k, ld_v, ld_gate, ld_beta;
+  int32_t qk_heads;        /* divides the pool's heads */
+  int32_t gate_dim;        /* 128: a decay per key channel; 1: one per head */
+  float scale;             /* of the queries */
+} dsa_delta_rows_t;
 
 /* Library and status helpers (host only; never fail). */
 int32_t dsa_api_version(void);
@@ -537,6 +565,85 @@ dsa_status_t dsa_decode_step_bf16(const dsa_paged_cache_t* cache, const dsa_batc
 dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_batch_t* batch,
                               const uint16_t* new_latent, const uint16_t* new_index_key,
                               int32_t* dev_status, void* stream);
+
+/*
+ * Where a step's new tokens go (no counterpart on the source pages, which say
+ * only that the block table and the cache slots are made before each step):
+ * from each request's cached and new tokens, on the device, so that a captured
+ * step builds its own table.  Request i with c cached and n new tokens has
+ * ceil(c / 64) pages in its row of block_table; the ceil((c + n) / 64) pages that it
+ * needs are completed from the top of the stack of free pages, request by
+ * request: page i of the step is free_blocks[free_count - 1 - i].  Then
+ *   seq_lens[i]   = c + n                        (what dsa_batch_t takes)
+ *   row_starts[i] = first row of request i, row_starts[batch] = all rows
+ *   positions[r]  = the row's token index in its request, c, c + 1, ...
+ *   slots[r]      = its physical cache row, table entry * 64 + position % 64
+ * and rows behind the last request get position and slot -1, up to max_rows.
+ * Neither the cached pages' entries nor the entries behind the new ones are touched.
+ *   cached_lens, new_lens  device int32 [batch]
+ *   free_blocks   device int32 [free_capacity];  free_count device int32, 0..free_capacity
+ *   free_left     device int32: the count that is left; may be free_count itself
+ *   block_table   device int32 [batch][max_blocks];  max_blocks up to 2^24, num_blocks up to 2^25
+ *   seq_lens      device int32 [batch]; may be cached_lens itself
+ *   row_starts    device int32 [batch + 1];  positions, slots device int32 [max_rows]
+ * A negative length, a request that does not fit its table row (it comes out
+ * with no rows and length 0), more rows than max_rows, more pages than the
+ * stack holds, or an entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS; slots
+ * without a page are -1.  One launch.
+ */
+dsa_status_t dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                              const int32_t* free_blocks, int32_t free_capacity, const int32_t* free_count,
+                              int32_t* free_left, int32_t num_blocks, int32_t* block_table, int32_t max_blocks,
+                              int32_t* seq_lens, int32_t* row_starts, int32_t* positions, int32_t* slots,
+                              int32_t max_rows, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_cache_append with the rows' slots given (as dsa_assign_slots makes them),
+ * for steps in which every request brings its own number of new tokens: row r
+ * goes to block row slots[r] / 64, place slots[r] % 64, in dsa_cache_append's
+ * encodings; a slot of -1 is a padding row.  A slot outside the pool raises
+ * DSA_ERR_BOUNDS and is not written.
+ *   slots          device int32 [rows], all different but for -1
+ *   new_latent     device bf16 bits [rows][576];  new_index_key device bf16 bits [rows][128]; 16-byte aligned
+ */
+dsa_status_t dsa_cache_append_slots(const dsa_paged_cache_t* cache, const int32_t* slots, int32_t rows,
+                                    const uint16_t* new_latent, const uint16_t* new_index_key,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * The gated delta rule of the hybrid model's recurrent layers (no counterpart
+ * on the source pages, which name these layers' state as the third kind in the
+ * packed cache).  Per value head, with the state S [128 values][128 keys] and
+ * row t of the sequence:
+ *   S~  = S diag(exp(gate_t))              (per key channel, or one decay per head)
+ *   u   = beta_t (v_t - S~ k_t)
+ *   S   = S~ + u k_t^T
+ *   out = scale * S q_t                     (bf16, round-to-nearest)
+ * in fp32.  A gate of -inf forgets the channel.
+ *
+ * gated_delta_decode: rows r = b * queries_per_seq + j, as in dsa_batch_t.
+ *   slots_in   device int32 [batch]: the slot of the state that sequence b starts from, or -1: zeros
+ *   slots_out  device int32 [batch][queries_per_seq]: where the state after row j goes, or -1:
+ *              nowhere.  With draft rows a slot for each, and the accepted one's goes on.
+ * gated_delta_prefill: row_starts device int32 [batch + 1], sequence b has the rows
+ * row_starts[b] .. row_starts[b + 1] - 1 (any number, none too), all within 0..rows; rows outside of
+ * them are not read and their outputs not touched.
+ *   slots_in   as above;  slots_out device int32 [batch]: where the last state goes, or -1
+ *   workspace  >= gated_delta_prefill_workspace_size(rows, batch, heads) bytes, 256-B aligned
+ * A slot in slots_out may be the same sequence's in slots_in; no other sequence of the
+ * call may use it.  out: device bf16 bits [rows][heads][128], 16-byte aligned.
+ * A slot outside the pool or row_starts that do not ascend within 0..rows raise
+ * DSA_ERR_BOUNDS; such a state counts as zeros or is not written, such a
+ * sequence is left out.
+ */
+dsa_status_t gated_delta_decode(const dsa_state_pool_t* pool, const dsa_delta_rows_t* x, int32_t batch,
+                                int32_t queries_per_seq, const int32_t* slots_in, const int32_t* slots_out,
+                                uint16_t* out, int32_t* dev_status, void* stream);
+size_t gated_delta_prefill_workspace_size(int32_t rows, int32_t batch, int32_t heads);
+dsa_status_t gated_delta_prefill(const dsa_state_pool_t* pool, const dsa_delta_rows_t* x, const int32_t* row_starts,
+                                 int32_t batch, int32_t rows, const int32_t* slots_in, const int32_t* slots_out,
+                                 uint16_t* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                 void* stream);
 
 /*
  * Indexer query in FP8 (Day-0 post, fused-decode section: the indexer's query
