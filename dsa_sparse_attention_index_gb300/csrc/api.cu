@@ -618,7 +618,7 @@ dsa_status_t gated_delta_decode(const dsa_state_pool_t* pool, const dsa_delta_ro
 
 size_t gated_delta_prefill_workspace_size(int32_t rows, int32_t batch, int32_t heads) {
   if (rows < 0 || batch < 0 || heads < 1) return 0;
-  return 256;
+  return delta_chunk_workspace_bytes(rows, batch, heads);
 }
 
 dsa_status_t gated_delta_prefill(const dsa_state_pool_t* pool, const dsa_delta_rows_t* x, const int32_t* row_starts,
@@ -634,7 +634,7 @@ dsa_status_t gated_delta_prefill(const dsa_state_pool_t* pool, const dsa_delta_r
     return DSA_ERR_WORKSPACE;
   const DeltaSeqs seqs{static_cast<float*>(pool->base), pool->slot_stride / 4, pool->num_slots, batch, rows, 0,
                        row_starts, slots_in, slots_out, 0, dev_status};
-  return launch_delta_rows(delta_rows(*pool, *x), seqs, out, static_cast<cudaStream_t>(stream));
+  return launch_delta_chunks(delta_rows(*pool, *x), seqs, out, workspace, static_cast<cudaStream_t>(stream));
 }
 
 dsa_status_t dsa_quantize_index_query(const uint16_t* q_bf16, const float* head_w, int32_t rows, uint8_t* q_index,

@@ -76,6 +76,9 @@ __device__ __forceinline__ float4 bf16x4_to_float4(uint2 v) {
                      __uint_as_float(v.y & 0xFFFF0000u));
 }
 
+// Row by row (delta.cu), and ragged prompts in chunks of 64 rows (delta_chunk.cu).
 dsa_status_t launch_delta_rows(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, cudaStream_t st);
+size_t delta_chunk_workspace_bytes(int rows, int batch, int heads);
+dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, void* workspace, cudaStream_t st);
 
 }  // namespace dsa

@@ -1,0 +1,1002 @@
+// delta_chunk.cu — the gated delta rule over prompts, 64 rows at once.
+//
+// For the rows i = 1..64 of a chunk behind the state S0, with P_i = prod_{s<=i}
+// a_s (a = exp(gate), by channel) and the decay D_ij = prod_{j<s<=i} a_s:
+//   A_ij = beta_i sum_d k_i k_j D_ij (j < i),   T = (I + A)^-1 diag(beta),
+//   R = V - (K P) S0^T,   U = T R,
+//   out = scale ((Q P) S0^T + B U),  B_ij = sum_d q_i k_j D_ij (j <= i),
+//   S = S0 diag(P_64) + U^T (K D_64)
+// which is the rule of delta.cu with its 64 steps solved as one triangular system.
+//
+// Two kernels.  delta_prepare_kernel: everything that does not depend on the
+// state, a CTA per chunk and head, into a record of operands laid out as the tensor
+// core reads them.  delta_chain_kernel: a CTA per sequence and head walks the
+// chunks; the state stays in registers in fp32.
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "delta.cuh"
+#include "internal.h"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kChunk = 64;
+constexpr int kTileHalf = kChunk * 128;                // 64 rows of 64 fp16 (128 bytes, 128-byte swizzle)
+constexpr int kTileBytes = 2 * kTileHalf;              // 64 rows x 128 channels
+// A record: K P (high and low parts), Q P, T (high and low), B, K D (high and low), then 256 floats.
+constexpr int kRecKp = 0;
+constexpr int kRecQp = kRecKp + 2 * kTileBytes;
+constexpr int kRecT = kRecQp + kTileBytes;
+constexpr int kRecB = kRecT + 2 * kTileHalf;
+constexpr int kRecKd = kRecB + kTileHalf;
+constexpr int kRecHead = kRecKd + 2 * kTileBytes;      // 106,496
+constexpr int kRecBytes = kRecHead + 1024;
+// floats of the record's head
+enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvT, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdMaxP, kHdP = 128 };
+
+struct ChunkArgs {
+  DeltaRows x;
+  DeltaSeqs s;
+  uint8_t* records;   // [rows / 64 + batch][heads]; chunk c of sequence b is number starts[b] / 64 + b + c
+  uint16_t* out;
+};
+
+// The power of two that brings a bound below 2^(top + 1).
+__device__ __forceinline__ float pow2_scale(float bound, int top) {
+  const int e = (int)((__float_as_uint(bound) >> 23) & 0xFFu) - 127;
+  return __uint_as_float((uint32_t)(max(-126, min(126, top - e)) + 127) << 23);
+}
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
+// Two fp32 in a register pair: one instruction for both.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, pack2(-1.f, -1.f), a); }
+__device__ __forceinline__ float reciprocal(float x) {   // within one unit in the last place
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 bf16x2_to_f32x2(uint32_t v) {
+  return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+// Two values as fp16: the upper 11 bits of each, and 11 bits of what they leave,
+// so 21 bits in all (the first part is cut, not rounded: that takes no way back
+// from fp16, and the rest holds its sign).
+__device__ __forceinline__ uint32_t f16x2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void split_f16(f32x2 v, uint32_t& hi, uint32_t& lo) {
+  const float2 f = unpack2(v);
+  const float hx = __uint_as_float(__float_as_uint(f.x) & 0xFFFFE000u), hy = __uint_as_float(__float_as_uint(f.y) & 0xFFFFE000u);
+  const float2 r = unpack2(sub2(v, pack2(hx, hy)));
+  hi = f16x2(hx, hy);
+  lo = f16x2(r.x, r.y);
+}
+// The same in bf16, whose range fits every factor of the decays: 16 bits.
+__device__ __forceinline__ uint32_t bf16x2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void split_bf16(f32x2 v, uint32_t& hi, uint32_t& lo) {
+  const float2 f = unpack2(v);
+  hi = bf16x2(f.x, f.y);
+  const float2 r = unpack2(sub2(v, bf16x2_to_f32x2(hi)));
+  lo = bf16x2(r.x, r.y);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t (&r)[2]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// ---------------------------------------------------------------- prepare
+constexpr int kPrepThreads = 256;
+constexpr int kPX = 0;                            // X = k L c in two parts and q L c: 64 rows x 256 bytes each
+constexpr int kPY = 3 * kChunk * 256;             // Y in two parts, 64 rows each
+constexpr int kLdA = kChunk + 4;                  // floats: rows start four banks apart
+constexpr int kPA = kPY + 2 * kChunk * 256;       // A, then (I + A)^-1, fp32 [64][68]
+constexpr int kPB = kPA + kChunk * kLdA * 4;    // B, fp16, the record's image
+constexpr int kPTab = kPB + kTileHalf;            // block products [4][128]
+constexpr int kPBeta = kPTab + 4 * kDeltaDim * 4;
+constexpr int kPMisc = kPBeta + kChunk * 4;
+constexpr int kPrepSmem = kPMisc + 128;
+static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
+
+// Offset of 16-byte piece c of row r in a tile of 256-byte rows: pieces are
+// exchanged so that eight rows' same piece lie in all banks.
+__device__ __forceinline__ uint32_t at256(int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); }
+
+// The 16 x 8 tile of X Y^T at rows x0 of X and y0 of Y, for keys (all four products
+// of the parts) and queries (two).
+__device__ __forceinline__ void tile_xy(uint32_t sm, int x0, int y0, float (&kk)[4], float (&qk)[4]) {
+  const int lane = threadIdx.x & 31;
+  const int ar = x0 + (lane & 15), ac = lane >> 4, br = y0 + (lane & 7), bc = (lane >> 3) & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    uint32_t xh[4], xl[4], xq[4], yh[2], yl[2];
+    const uint32_t a = at256(ar, 2 * ks + ac), b = at256(br, 2 * ks + bc);
+    ldsm4(sm + kPX + a, xh);
+    ldsm4(sm + kPX + kChunk * 256 + a, xl);
+    ldsm4(sm + kPX + 2 * kChunk * 256 + a, xq);
+    ldsm2(sm + kPY + b, yh);
+    ldsm2(sm + kPY + kChunk * 256 + b, yl);
+    mma_16x8x16(kk, xl, yl);
+    mma_16x8x16(kk, xl, yh);
+    mma_16x8x16(kk, xh, yl);
+    mma_16x8x16(kk, xh, yh);
+    mma_16x8x16(qk, xq, yl);
+    mma_16x8x16(qk, xq, yh);
+  }
+}
+
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// A 16 x 8 tile of sign * L R for fp32 matrices in shared memory: L's 16 rows, K columns; R's K
+// rows, 8 columns.  Each factor as two tf32 (22 bits), three products.
+template <int K>
+__device__ __forceinline__ void mul_tile(const float* L, int ldl, const float* R, int ldr, float* out, int ldo, float sign) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < K; k += 8) {
+    const float l[4] = {L[g * ldl + k + t], L[(g + 8) * ldl + k + t], L[g * ldl + k + t + 4], L[(g + 8) * ldl + k + t + 4]};
+    const float r[2] = {R[(k + t) * ldr + g], R[(k + t + 4) * ldr + g]};
+    uint32_t lh[4], ll[4], rh[2], rl[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lh[i] = tf32(l[i]), ll[i] = tf32(l[i] - __uint_as_float(lh[i]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rh[i] = tf32(r[i]), rl[i] = tf32(r[i] - __uint_as_float(rh[i]));
+    mma_16x8x8(d, ll, rh);
+    mma_16x8x8(d, lh, rl);
+    mma_16x8x8(d, lh, rh);
+  }
+  out[g * ldo + 2 * t] = sign * d[0], out[g * ldo + 2 * t + 1] = sign * d[1];
+  out[(g + 8) * ldo + 2 * t] = sign * d[2], out[(g + 8) * ldo + 2 * t + 1] = sign * d[3];
+}
+
+__device__ __forceinline__ float max_warp(float v) {  // of values >= 0
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const ChunkArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sm = smem_u32(smem);
+  const DeltaRows& x = p.x;
+  const int slot = blockIdx.x / x.heads, h = blockIdx.x % x.heads, hq = h / (x.heads / x.qk_heads);
+  const int tid = threadIdx.x, lane = tid & 31, warp = warp_number();
+
+  // the sequence whose chunk this is: the last b with starts[b] / 64 + b <= slot
+  int seq = 0, end = p.s.batch;
+  while (end - seq > 1) {
+    const int mid = (seq + end) >> 1;
+    if (p.s.starts[mid] / kChunk + mid <= slot) seq = mid; else end = mid;
+  }
+  int64_t row0;
+  int n;
+  if (!seq_rows(p.s, seq, &row0, &n)) return;
+  const int c = slot - (int)(row0 / kChunk + seq);
+  if (c < 0 || c * kChunk >= n) return;
+  row0 += c * kChunk;
+  n = min(n - c * kChunk, kChunk);
+  uint8_t* rec = p.records + (int64_t)blockIdx.x * kRecBytes;
+
+  float* tab = reinterpret_cast<float*>(smem + kPTab);
+  float* beta = reinterpret_cast<float*>(smem + kPBeta);
+  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: largest |k|, |q|, growth; unsafe lanes
+  float* A = reinterpret_cast<float*>(smem + kPA);
+  bool bad = false;
+
+  // ---- rows 16 I .. + 15, channels 2 q2 and 2 q2 + 1 of this thread
+  const int q2 = tid & 63, I = tid >> 6;
+  uint32_t kr[16], qr[16];
+  f32x2 a[16];
+  {
+    const uint16_t* kp = x.k + (row0 + 16 * I) * x.ld_k + hq * kDeltaDim + 2 * q2;
+    const uint16_t* qp = x.q + (row0 + 16 * I) * x.ld_q + hq * kDeltaDim + 2 * q2;
+    const float* gp = x.gate + (row0 + 16 * I) * x.ld_gate + (int64_t)h * x.gate_dim + (x.gate_dim == 1 ? 0 : 2 * q2);
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      kr[t] = qr[t] = 0u;
+      float gx = 0.f, gy = 0.f;
+      if (16 * I + t < n) {
+        kr[t] = __ldg(reinterpret_cast<const uint32_t*>(kp + t * x.ld_k));
+        qr[t] = __ldg(reinterpret_cast<const uint32_t*>(qp + t * x.ld_q));
+        if (x.gate_dim == 1) {
+          gx = gy = __ldg(gp + t * x.ld_gate);
+        } else {
+          const float2 g = __ldg(reinterpret_cast<const float2*>(gp + t * x.ld_gate));
+          gx = g.x, gy = g.y;
+        }
+      }
+      a[t] = pack2(gx, gy);
+    }
+  }
+  if (tid < kChunk) {
+    const float bt = tid < n ? __ldg(x.beta + (row0 + tid) * x.ld_beta + h) : 0.f;
+    beta[tid] = bt;
+    bad = !(fabsf(bt) <= 3.4e38f);
+  }
+  const f32x2 one = pack2(1.f, 1.f);
+  f32x2 block = one;
+  float grow = 1.f, amax = 0.f;
+  uint32_t km = 0, qm = 0;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    const float2 g = unpack2(a[t]);
+    const float ex = expf(g.x), ey = expf(g.y);
+    a[t] = pack2(ex, ey);
+    block = mul2(block, a[t]);
+    const float m = fmaxf(ex, ey);
+    bad |= g.x != g.x || g.y != g.y;   // (a maximum drops a NaN)
+    amax = fmaxf(amax, m);
+    grow *= fmaxf(1.f, m);
+    km = __vmaxu2(km, kr[t] & 0x7FFF7FFFu), qm = __vmaxu2(qm, qr[t] & 0x7FFF7FFFu);
+  }
+  bad |= !(amax <= 3.4e38f);
+  const float Bx = unpack2(block).x, By = unpack2(block).y;
+  tab[I * kDeltaDim + 2 * q2] = Bx, tab[I * kDeltaDim + 2 * q2 + 1] = By;
+  {
+    const float k1 = __uint_as_float(max(km & 0xFFFFu, km >> 16) << 16), q1 = __uint_as_float(max(qm & 0xFFFFu, qm >> 16) << 16);
+    bad |= !(k1 <= 3.4e38f) || !(q1 <= 3.4e38f) || !(grow <= 3.4e38f);
+    const bool unsafe = !(fminf(Bx, By) >= 7.6e-37f) || !(grow <= 1024.f);   // 2^-120, 2^10
+    const float mk = max_warp(bad ? 0.f : k1), mq = max_warp(bad ? 0.f : q1), mg = max_warp(bad ? 1.f : grow);
+    const uint32_t any = __ballot_sync(0xffffffffu, unsafe);
+    if (lane == 0) {
+      misc[warp] = mk, misc[8 + warp] = mq, misc[16 + warp] = mg;
+      reinterpret_cast<uint32_t*>(misc)[24 + warp] = any;
+    }
+  }
+  // the upper triangles stay zero
+  static_assert(kPB == kPA + kChunk * kLdA * 4, "A and B lie together");
+  for (int i = tid; i < (kChunk * kLdA * 4 + kTileHalf) / 16; i += kPrepThreads)
+    reinterpret_cast<uint4*>(smem + kPA)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+
+  float mk = 0.f, mq = 0.f, mg = 1.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) mk = fmaxf(mk, misc[w]), mq = fmaxf(mq, misc[8 + w]);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) mg *= fmaxf(misc[16 + 2 * b], misc[17 + 2 * b]);
+  const uint32_t* unsafe_w = reinterpret_cast<const uint32_t*>(misc) + 24;
+  const float scale = x.scale;
+  bad |= !(mg <= 1e30f) || !(mk <= 1e30f) || !(mq <= 1e30f) || !(mk * mk * mg <= 1e30f) ||
+         !(mk * mq * mg * fabsf(scale) <= 1e30f) || !(fabsf(scale) <= 1e30f);
+  // powers of two that bring the operands into fp16's range, from bounds: products of decays grow no further than mg
+  const float sc_k = pow2_scale(mk * mg, 14);                        // of K P and K D
+  const float sc_q = pow2_scale(mq * mg * fabsf(scale), 14);
+  const float sc_b = pow2_scale(mq * mk * mg * fabsf(scale) * 128.f, 14);
+
+  // ---- decays by channel, forward: K P, Q P, X
+  auto block_of = [&](int b) { return *reinterpret_cast<const f32x2*>(tab + b * kDeltaDim + 2 * q2); };
+  f32x2 pre = one, post = one;   // the decays of the blocks before and behind
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (b < I) pre = mul2(pre, block_of(b));
+    if (b > I) post = mul2(post, block_of(b));
+  }
+  // c^2 brings a block's product to about one; X carries c, Y its inverse
+  auto centre1 = [](float B) {
+    const int e = (int)((__float_as_uint(B) >> 23) & 0xFFu) - 127;
+    return __uint_as_float((uint32_t)(127 + max(-60, min(60, -(e / 2)))) << 23);
+  };
+  auto centre = [&](int b) {
+    const float2 v = unpack2(block_of(b));
+    return pack2(centre1(v.x), centre1(v.y));
+  };
+  auto uncentre = [&](int b) {
+    const float2 v = unpack2(centre(b));
+    return pack2(pow2_inverse(v.x), pow2_inverse(v.y));
+  };
+  // image offsets of channel pair q2 in rows of 128 bytes, 64 channels a block
+  const uint32_t img = (uint32_t)((q2 >> 5) * kTileHalf + (q2 & 31) * 4);
+  const uint32_t piece = (uint32_t)(q2 >> 2), in_piece = (uint32_t)(q2 & 3) * 4;
+  {
+    const f32x2 c = centre(I), pre_k = mul2(pre, pack2(sc_k, sc_k)), pre_q = mul2(pre, pack2(sc_q * scale, sc_q * scale)),
+                c_q = mul2(c, pack2(scale, scale));
+    f32x2 l = one;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const int r = 16 * I + t;
+      l = mul2(l, a[t]);
+      const f32x2 k = bf16x2_to_f32x2(kr[t]), ql = mul2(bf16x2_to_f32x2(qr[t]), l), w = mul2(l, c);
+      uint32_t hi2, lo2;
+      const uint32_t o = swz128(img + r * 128);
+      split_f16(mul2(k, mul2(l, pre_k)), hi2, lo2);
+      *reinterpret_cast<uint32_t*>(rec + kRecKp + o) = hi2;
+      *reinterpret_cast<uint32_t*>(rec + kRecKp + kTileBytes + o) = lo2;
+      const float2 qp = unpack2(mul2(ql, pre_q)), xq = unpack2(mul2(ql, c_q)), wf = unpack2(w);
+      *reinterpret_cast<uint32_t*>(rec + kRecQp + o) = f16x2(qp.x, qp.y);
+      const uint32_t s = at256(r, piece) + in_piece;
+      split_bf16(mul2(k, w), hi2, lo2);
+      *reinterpret_cast<uint32_t*>(smem + kPX + s) = hi2;
+      *reinterpret_cast<uint32_t*>(smem + kPX + kChunk * 256 + s) = lo2;
+      *reinterpret_cast<uint32_t*>(smem + kPX + 2 * kChunk * 256 + s) = bf16x2(xq.x, xq.y);
+      // Y of the block itself: k / (L c); no number where the block is not safe, and not used there
+      split_bf16(mul2(k, pack2(reciprocal(wf.x), reciprocal(wf.y))), hi2, lo2);
+      *reinterpret_cast<uint32_t*>(smem + kPY + s) = hi2;
+      *reinterpret_cast<uint32_t*>(smem + kPY + kChunk * 256 + s) = lo2;
+    }
+    if (I == 3) *reinterpret_cast<f32x2*>(rec + kRecHead + 4 * (kHdP + 2 * q2)) = mul2(pre, block);
+  }
+  // ---- backward: K D
+  {
+    f32x2 l = mul2(post, pack2(sc_k, sc_k));
+#pragma unroll
+    for (int t = 15; t >= 0; --t) {
+      uint32_t hi2, lo2;
+      const uint32_t o = swz128(img + (16 * I + t) * 128);
+      split_f16(mul2(bf16x2_to_f32x2(kr[t]), l), hi2, lo2);
+      *reinterpret_cast<uint32_t*>(rec + kRecKd + o) = hi2;
+      *reinterpret_cast<uint32_t*>(rec + kRecKd + kTileBytes + o) = lo2;
+      l = mul2(l, a[t]);
+    }
+  }
+  __syncthreads();
+
+  // ---- A and B within the blocks
+  auto put = [&](int i, int j, float kk, float qk) {
+    if (j < i) A[i * kLdA + j] = kk * beta[i];
+    if (j <= i) *reinterpret_cast<__half*>(smem + kPB + swz128((uint32_t)(i * 128 + j * 2))) = __float2half_rn(qk * sc_b);
+  };
+  auto put_tile = [&](int i0, int j0, const float (&kk)[4], const float (&qk)[4]) {
+    const int i = i0 + (lane >> 2), j = j0 + 2 * (lane & 3);
+    put(i, j, kk[0], qk[0]);
+    put(i, j + 1, kk[1], qk[1]);
+    put(i + 8, j, kk[2], qk[2]);
+    put(i + 8, j + 1, kk[3], qk[3]);
+  };
+  {
+    const int D = warp >> 1;
+    if ((unsafe_w[2 * D] | unsafe_w[2 * D + 1]) == 0u) {
+      float kk[4], qk[4];
+      tile_xy(sm, 16 * D, 16 * D + 8 * (warp & 1), kk, qk);
+      put_tile(16 * D, 16 * D + 8 * (warp & 1), kk, qk);
+    } else {
+      // decays that leave fp32's range within 16 rows: pair by pair, four channels a lane
+      for (int j = 16 * D + (warp & 1); j < min(16 * D + 16, n); j += 2) {
+        const uint2 kj = __ldg(reinterpret_cast<const uint2*>(x.k + (row0 + j) * x.ld_k + hq * kDeltaDim) + lane);
+        float4 y = bf16x4_to_float4(kj);
+        for (int i = j; i < min(16 * D + 16, n); ++i) {
+          if (i > j) {
+            float4 g;
+            if (x.gate_dim == 1) {
+              g.x = g.y = g.z = g.w = __ldg(x.gate + (row0 + i) * x.ld_gate + h);
+            } else {
+              g = __ldg(reinterpret_cast<const float4*>(x.gate + (row0 + i) * x.ld_gate + (int64_t)h * kDeltaDim) + lane);
+            }
+            y.x *= expf(g.x), y.y *= expf(g.y), y.z *= expf(g.z), y.w *= expf(g.w);
+          }
+          const float4 ki = bf16x4_to_float4(__ldg(reinterpret_cast<const uint2*>(x.k + (row0 + i) * x.ld_k + hq * kDeltaDim) + lane));
+          const float4 qi = bf16x4_to_float4(__ldg(reinterpret_cast<const uint2*>(x.q + (row0 + i) * x.ld_q + hq * kDeltaDim) + lane));
+          float kk = fmaf(y.w, ki.w, fmaf(y.z, ki.z, fmaf(y.y, ki.y, y.x * ki.x)));
+          float qk = fmaf(y.w, qi.w, fmaf(y.z, qi.z, fmaf(y.y, qi.y, y.x * qi.x)));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            kk += __shfl_xor_sync(0xffffffffu, kk, o);
+            qk += __shfl_xor_sync(0xffffffffu, qk, o);
+          }
+          if (lane == 0) put(i, j, kk, qk * scale);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // ---- between the blocks: columns 0..47 of rows 48..63, then those of rows 32..47 and 16..31
+  // Y at rows y0 .. + 15: k times the decay to the block's end, times l
+  auto put_y = [&](int y0, f32x2 l) {
+#pragma unroll
+    for (int t = 15; t >= 0; --t) {
+      uint32_t hi2, lo2;
+      split_bf16(mul2(bf16x2_to_f32x2(kr[t]), l), hi2, lo2);
+      const uint32_t s = at256(y0 + t, piece) + in_piece;
+      *reinterpret_cast<uint32_t*>(smem + kPY + s) = hi2;
+      *reinterpret_cast<uint32_t*>(smem + kPY + kChunk * 256 + s) = lo2;
+      l = mul2(l, a[t]);
+    }
+  };
+  if (I < 3) {
+    f32x2 l = uncentre(3);
+    if (I < 2) l = mul2(l, block_of(2));
+    if (I < 1) l = mul2(l, block_of(1));
+    put_y(16 * I, l);
+  }
+  __syncthreads();
+  if (warp < 6) {
+    float kk[4], qk[4];
+    tile_xy(sm, 48, 8 * warp, kk, qk);
+    put_tile(48, 8 * warp, kk, qk);
+  }
+  __syncthreads();
+  if (I < 2) put_y(16 * I, I == 0 ? mul2(uncentre(2), block_of(1)) : uncentre(2));   // for rows 32..47
+  if (I == 0) put_y(32, uncentre(1));
+  __syncthreads();
+  if (warp < 6) {
+    float kk[4], qk[4];
+    const int x0 = warp < 4 ? 32 : 16, y0 = warp < 4 ? 8 * warp : 32 + 8 * (warp - 4), j0 = warp < 4 ? y0 : y0 - 32;
+    tile_xy(sm, x0, y0, kk, qk);
+    put_tile(x0, j0, kk, qk);
+  }
+  __syncthreads();
+
+  // ---- (I + A)^-1, in A's place: the diagonal blocks by substitution, a thread a
+  // column; then twice [[T1, 0], [-T2 A21 T1, T2]], of 16 and of 32 rows
+  if (tid < kChunk) {
+    const int j = tid & 15;
+    float* D = A + (tid & 48) * (kLdA + 1);
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(D + i * kLdA + m);
+        s0 = fmaf(r.x, t[m], s0);
+        if (m + 1 < i) s1 = fmaf(r.y, t[m + 1], s1);
+        if (m + 2 < i) s0 = fmaf(r.z, t[m + 2], s0);
+        if (m + 3 < i) s1 = fmaf(r.w, t[m + 3], s1);
+      }
+      t[i] = i < j ? 0.f : i == j ? 1.f : -(s0 + s1);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) D[i * kLdA + j] = t[i];
+  }
+  __syncthreads();
+  float* tmp = reinterpret_cast<float*>(smem + kPX);   // [32][36]
+  constexpr int kLdT = 36;
+  if (warp < 4) {
+    const int d = 32 * (warp >> 1), cc = 8 * (warp & 1);
+    mul_tile<16>(A + (d + 16) * kLdA + d, kLdA, A + d * kLdA + d + cc, kLdA, tmp + (d >> 1) * kLdT + cc, kLdT, 1.f);
+  }
+  __syncthreads();
+  if (warp < 4) {
+    const int d = 32 * (warp >> 1), cc = 8 * (warp & 1);
+    mul_tile<16>(A + (d + 16) * (kLdA + 1), kLdA, tmp + (d >> 1) * kLdT + cc, kLdT, A + (d + 16) * kLdA + d + cc, kLdA, -1.f);
+  }
+  __syncthreads();
+  {
+    const int r = 16 * (warp >> 2), cc = 8 * (warp & 3);
+    mul_tile<32>(A + (32 + r) * kLdA, kLdA, A + cc, kLdA, tmp + r * kLdT + cc, kLdT, 1.f);
+    __syncthreads();
+    mul_tile<32>(A + (32 + r) * kLdA + 32, kLdA, tmp + cc, kLdT, A + (32 + r) * kLdA + cc, kLdA, -1.f);
+  }
+  __syncthreads();
+  // ---- T = (I + A)^-1 diag(beta) in two parts: a thread 16 columns of a row
+  {
+    const int i = tid >> 2, j0 = 16 * (tid & 3);
+    float t[16], m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 r = *reinterpret_cast<const float4*>(A + i * kLdA + j0 + j);
+      const float4 bj = *reinterpret_cast<const float4*>(beta + j0 + j);
+      t[j] = r.x * bj.x, t[j + 1] = r.y * bj.y, t[j + 2] = r.z * bj.z, t[j + 3] = r.w * bj.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      bad |= t[j] != t[j];
+      m = fmaxf(m, fabsf(t[j]));
+    }
+    bad |= !(m <= 1e30f);
+    m = max_warp(bad ? 0.f : m);
+    if (lane == 0) misc[warp] = m;
+    __syncthreads();
+    float mt = misc[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) mt = fmaxf(mt, misc[w]);
+    const float sc_t = pow2_scale(mt, 14);
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split_f16(mul2(pack2(t[2 * j], t[2 * j + 1]), pack2(sc_t, sc_t)), hi[j], lo[j]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t o = swz128((uint32_t)(i * 128 + 2 * j0 + 16 * j));
+      *reinterpret_cast<uint4*>(rec + kRecT + o) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+      *reinterpret_cast<uint4*>(rec + kRecT + kTileHalf + o) = make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+    }
+    if (tid == 0) {
+      float* hd = reinterpret_cast<float*>(rec + kRecHead);
+      hd[kHdInvKp] = pow2_inverse(sc_k), hd[kHdInvQp] = pow2_inverse(sc_q), hd[kHdInvT] = pow2_inverse(sc_t);
+      hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvKd] = pow2_inverse(sc_k);
+      // sums of a row's or a column's magnitudes, from above
+      hd[kHdSumKp] = 128.f * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg, hd[kHdMaxP] = mg;
+    }
+    for (int q = tid; q < kTileHalf / 16; q += kPrepThreads)
+      reinterpret_cast<uint4*>(rec + kRecB)[q] = reinterpret_cast<const uint4*>(smem + kPB)[q];
+  }
+  const int any = __syncthreads_or(bad);
+  if (tid == 0) reinterpret_cast<int*>(rec + kRecHead)[kHdBad] = any;
+}
+
+// ---------------------------------------------------------------- chain
+// Warps 0..7 hold the state: row v = 32 (w % 4) + lane of it, keys 64 (w / 4) ..
+// + 63, and turn each product into the next one's operand; warp 8 issues the MMAs,
+// warp 9 copies the records, two chunks deep.  All products are transposed, with
+// the 128 values on the tensor core's rows:
+//   R^T [v][t] = V^T - S (K P)^T   A = S in two fp16 parts from TMEM, times K P's two (three products)
+//   U^T = R^T T^T                  A = R in two parts
+//   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
+//   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
+// The parts of a row of S, R or U are times a power of two from a bound of it, so
+// that they keep 22 bits of its largest element whatever its size.
+constexpr int kChainThreads = 10 * 32;
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kColS = 0;       // keys 64 h ..: high parts in columns 64 h .. + 31, low parts behind them
+constexpr int kColAcc = 128;   // R, then U
+constexpr int kColParts = 192; // R's, then U's parts: high 32 columns, low 32
+constexpr int kColDs = 256;
+constexpr int kColO1 = 384, kColO2 = 448;
+constexpr int kCOffX = 2 * kRecBytes;                   // exchanged maxima [2 parities][4 kinds][2 halves][128]
+constexpr int kCOffRow = kCOffX + 2 * 4 * 2 * 128 * 4;  // a row's k, q, decay (two buffers) and partial sums, where rows go one by one
+constexpr int kCOffBars = kCOffRow + (2 * 3 * 128 + 3 * 2 * 128) * 4;
+constexpr int kCNumBars = 13;
+constexpr int kCOffMisc = kCOffBars + kCNumBars * 8;
+constexpr int kChainSmem = 1024 + kCOffMisc + 32;
+static_assert(kChainSmem <= 232448 && kRecBytes % 1024 == 0, "shared memory");
+
+__device__ __forceinline__ void bar_state() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool bar_state_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, 256, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t load_u16(const uint16_t* p) {
+  uint32_t r;
+  asm volatile("{\n .reg .u16 t;\n ld.global.nc.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_abs_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n .reg .b32 t;\n abs.f16x2 t, %2;\n max.f16x2 %0, %1, t;\n}\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const ChunkArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sm = smem_u32(smem);
+  const DeltaRows& x = p.x;
+  const int h = blockIdx.x % x.heads, b = blockIdx.x / x.heads, hq = h / (x.heads / x.qk_heads);
+  const int warp = warp_number(), lane = threadIdx.x & 31;
+  int64_t row0;
+  int n;
+  if (!seq_rows(p.s, b, &row0, &n)) return;
+  const int chunks = (n + kChunk - 1) / kChunk;
+  const uint8_t* rec = p.records + ((row0 / kChunk + b) * x.heads + h) * kRecBytes;
+  const int64_t rec_step = (int64_t)x.heads * kRecBytes;
+
+  const uint32_t bars = sm + kCOffBars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 16u + 8u * s; };
+  const uint32_t b_s = bars + 32, b_r = bars + 40, b_rp = bars + 48, b_u = bars + 56, b_up = bars + 64, b_ds = bars + 72,
+                 b_o = bars + 80, b_of = bars + 88, drain = bars + 96;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kCOffMisc + 4);
+  volatile int* by_rows = reinterpret_cast<volatile int*>(smem + kCOffMisc + 8);   // [2]: this chunk goes row by row
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 9);
+    }
+    for (uint32_t a : {b_r, b_u, b_ds, b_o, drain}) mbar_init(a, 1);
+    for (uint32_t a : {b_s, b_rp, b_up, b_of}) mbar_init(a, 8);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+  if (warp == kCopyWarp) {
+    bool ok = true;
+    int issued = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int s = c & 1;
+      if (c >= 2) ok = mbar_wait_warp(empty(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status);
+      if (!ok) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full(s), kRecBytes);
+        for (int i = 0; i < 4; ++i)
+          bulk_load(sm + s * kRecBytes + i * (kRecBytes / 4), rec + c * rec_step + i * (kRecBytes / 4), kRecBytes / 4, full(s));
+      }
+      __syncwarp();
+      ++issued;
+    }
+    // no copy is in flight at the exit, also after another role gave up
+    for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait_drain(full(c & 1), (c >> 1) & 1, 10000000ull);
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t kIdesc64 = make_idesc(kFmtF16, kFmtF16, 0, 0, 128, kChunk);
+    constexpr uint32_t kIdescDs = make_idesc(kFmtF16, kFmtF16, 0, 1, 128, kDeltaDim);
+    const uint64_t kdesc = smem_desc(sm, 16, 1024, kLayoutSw128);                  // K-major tiles
+    const uint64_t ndesc = smem_desc(sm + kRecKd, kTileHalf, 1024, kLayoutSw128);  // K D: 64 keys a block
+    const uint32_t k_hi = (uint32_t)(kdesc >> 32), n_hi = (uint32_t)(ndesc >> 32);
+    uint32_t f = 0;   // chunks that took the tensor core
+    for (int c = 0; c < chunks; ++c) {
+      const int s = c & 1;
+      const uint32_t k0 = (uint32_t)kdesc + s * (kRecBytes / 16), n0 = (uint32_t)ndesc + s * (kRecBytes / 16);
+      if (!mbar_wait_warp(full(s), (c >> 1) & 1, abort_flag, p.s.status)) break;
+      if (!mbar_wait_warp(b_s, c & 1, abort_flag, p.s.status)) break;
+      if (__any_sync(0xffffffffu, by_rows[s] != 0)) {
+        if (elect_one()) mbar_arrive(empty(s));
+        __syncwarp();
+        continue;
+      }
+      tc_fence_after();
+      auto product_s = [&](uint32_t d, int part, int tile, bool more) {   // A: the state's part, 128 keys
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16_tmem_a(tmem + d, tmem + kColS + 64 * (ks >> 2) + 32 * part + 8 * (ks & 3),
+                          desc64(k0 + (tile + (ks >> 2) * kTileHalf) / 16 + 2 * (ks & 3), k_hi), kIdesc64, more || ks ? 1u : 0u);
+      };
+      auto product_t = [&](uint32_t d, int part, int tile, bool more) {   // A: R's or U's part, 64 rows
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_tmem_a(tmem + d, tmem + kColParts + 32 * part + 8 * ks, desc64(k0 + tile / 16 + 2 * ks, k_hi), kIdesc64,
+                          more || ks ? 1u : 0u);
+      };
+      if (elect_one()) {
+        product_s(kColAcc, 1, kRecKp, false);
+        product_s(kColAcc, 0, kRecKp + kTileBytes, true);
+        product_s(kColAcc, 0, kRecKp, true);
+        mma_commit(b_r);
+      }
+      __syncwarp();
+      if (!mbar_wait_warp(b_rp, f & 1, abort_flag, p.s.status)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        product_t(kColAcc, 1, kRecT, false);
+        product_t(kColAcc, 0, kRecT + kTileHalf, true);
+        product_t(kColAcc, 0, kRecT, true);
+        mma_commit(b_u);
+      }
+      __syncwarp();
+      if (f > 0 && !mbar_wait_warp(b_of, (f - 1) & 1, abort_flag, p.s.status)) break;
+      tc_fence_after();
+      if (elect_one()) product_s(kColO1, 0, kRecQp, false);
+      __syncwarp();
+      if (!mbar_wait_warp(b_up, f & 1, abort_flag, p.s.status)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)   // low x high, high x low, high x high
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_tmem_a(tmem + kColDs, tmem + kColParts + (q == 0 ? 32 : 0) + 8 * ks,
+                            desc64(n0 + (q == 1 ? kTileBytes / 16 : 0) + ks * (16 * 128 / 16), n_hi), kIdescDs, q | ks ? 1u : 0u);
+        mma_commit(b_ds);
+        product_t(kColO2, 0, kRecB, false);
+        mma_commit(b_o);
+        mma_commit(empty(s));
+      }
+      __syncwarp();
+      ++f;
+    }
+    // every MMA completes before TMEM is released
+    if (elect_one()) {
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0, 10000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ state warps
+    // A wait that gave up leaves the loop running without waits (they return at
+    // once then): the warps meet at named barriers and none may be missing there.
+    const int half = warp >> 2, v = 32 * (warp & 3) + lane, tid = threadIdx.x;
+    const uint32_t quad = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    float* ex = reinterpret_cast<float*>(smem + kCOffX);
+    auto xchg = [&](int parity, int kind, int hf) -> float& { return ex[((parity * 4 + kind) * 2 + hf) * 128 + v]; };
+    enum { kMaxS, kMaxV, kMaxR, kMaxU };
+    float S[64];
+    {
+      const float* in = state_in(p.s, b, h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 t = in ? *reinterpret_cast<const float4*>(in + v * kDeltaDim + 64 * half + 4 * i)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[4 * i] = t.x, S[4 * i + 1] = t.y, S[4 * i + 2] = t.z, S[4 * i + 3] = t.w;
+      }
+    }
+    auto own_max = [&]() {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(S[i]));
+      return m;
+    };
+    // the chunk's values of this lane, rows 32 half .. + 31: apart until they are used, or the loads would be waited for
+    uint32_t vr[32];
+    auto load_v = [&](int c) {
+      // rows that are not there repeat the last one, so that no load stands in a branch; they are cleared where used
+      const uint16_t* vp = x.v + (row0 + c * kChunk) * x.ld_v + (int64_t)h * kDeltaDim + v;
+      const int last = min(kChunk, n - c * kChunk) - 1;
+      if (last == kChunk - 1) {
+        vp += 32 * half * x.ld_v;
+#pragma unroll
+        for (int t = 0; t < 32; ++t, vp += x.ld_v) vr[t] = load_u16(vp);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 32; ++t) vr[t] = load_u16(vp + min(32 * half + t, last) * x.ld_v);
+      }
+    };
+    if (chunks > 0) load_v(0);
+    xchg(1, kMaxS, half) = own_max();
+    bar_state();
+    float bound_s = fmaxf(xchg(1, kMaxS, 0), xchg(1, kMaxS, 1));
+    uint32_t f = 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      mbar_wait_warp(bar, parity, abort_flag, p.s.status);
+      tc_fence_after();
+    };
+    auto arrive = [&](uint32_t bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+
+    // the outputs of the last chunk that took the tensor core, behind the next one's first operand
+    int out_rows = 0, out_c = 0;
+    float out_f1 = 0.f, out_f2 = 0.f;
+    auto put_out = [&]() {
+      if (out_rows == 0) return;
+      wait(b_o, (f - 1) & 1);
+      uint32_t o1[32], o2[32];
+      tmem_ld32(quad + kColO1 + 32 * half, o1);
+      tmem_ld32(quad + kColO2 + 32 * half, o2);
+      tmem_ld_wait();
+      arrive(b_of);
+      const int64_t step = (int64_t)x.heads * kDeltaDim;
+      uint16_t* op = p.out + (row0 + out_c * kChunk + 32 * half) * step + (int64_t)h * kDeltaDim + v;
+      const int left = out_rows - 32 * half;
+#pragma unroll
+      for (int t = 0; t < 32; t += 2, op += 2 * step) {
+        const uint32_t o = bf16x2(fmaf(out_f1, __uint_as_float(o1[t]), out_f2 * __uint_as_float(o2[t])),
+                                  fmaf(out_f1, __uint_as_float(o1[t + 1]), out_f2 * __uint_as_float(o2[t + 1])));
+        if (t < left) op[0] = (uint16_t)o;
+        if (t + 1 < left) op[step] = (uint16_t)(o >> 16);
+      }
+      out_rows = 0;
+    };
+
+    for (int c = 0; c < chunks; ++c) {
+      const int s = c & 1;
+      const int rows = min(kChunk, n - c * kChunk);
+      const float* hd = reinterpret_cast<const float*>(smem + s * kRecBytes + kRecHead);
+      // ---- the state's parts
+      const float sc_s = pow2_scale(bound_s, 14);
+      const f32x2 sc_s2 = pack2(sc_s, sc_s);
+      uint32_t top = 0u;   // the largest high part: the state's largest value is within 2^-10 of it
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) split_f16(mul2(pack2(S[32 * g + 2 * i], S[32 * g + 2 * i + 1]), sc_s2), hi[i], lo[i]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max_abs_f16x2(top, hi[i]);
+        tmem_st16(quad + kColS + 64 * half + 16 * g, hi);
+        tmem_st16(quad + kColS + 64 * half + 32 + 16 * g, lo);
+      }
+      {
+        const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&top));
+        xchg(s, kMaxS, half) = fmaxf(m.x, m.y) * pow2_inverse(sc_s) * 1.001f;
+      }
+      uint32_t vmax = 0;
+#pragma unroll
+      for (int t = 0; t < 32; ++t) {
+        if (rows < kChunk && 32 * half + t >= rows) vr[t] = 0u;
+        vmax = max(vmax, vr[t] & 0x7FFFu);
+      }
+      xchg(s, kMaxV, half) = __uint_as_float(vmax << 16);
+      tmem_st_wait();
+      wait(full(s), (c >> 1) & 1);
+      const bool rowwise = bar_state_or(vmax >= 0x7F80u || reinterpret_cast<const int*>(hd)[kHdBad] != 0);
+      if (tid == 0) by_rows[s] = rowwise;
+      arrive(b_s);
+      put_out();
+      if (rowwise) {
+        // a value that is no number, or out of range, touches nothing of the rows before it: one row after another
+        float* rb = reinterpret_cast<float*>(smem + kCOffRow);       // [2][k, q, decay][128]
+        float* part = rb + 2 * 3 * 128;                              // [p, w, k q][2 halves][128]
+        for (int t = 0; t < rows; ++t) {
+          const int64_t row = row0 + c * kChunk + t;
+          float* r = rb + (t & 1) * 3 * 128;
+          if (tid < 128) {
+            r[tid] = bf16_to_float(__ldg(x.k + row * x.ld_k + hq * kDeltaDim + tid));
+            r[128 + tid] = bf16_to_float(__ldg(x.q + row * x.ld_q + hq * kDeltaDim + tid));
+            r[256 + tid] = expf(__ldg(x.gate + row * x.ld_gate + (x.gate_dim == 1 ? h : h * kDeltaDim + tid)));
+          }
+          bar_state();
+          float pk = 0.f, pq = 0.f, kq = 0.f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const int k = 64 * half + i;
+            S[i] *= r[256 + k];
+            pk = fmaf(S[i], r[k], pk), pq = fmaf(S[i], r[128 + k], pq), kq = fmaf(r[k], r[128 + k], kq);
+          }
+          part[half * 128 + v] = pk, part[256 + half * 128 + v] = pq, part[512 + half * 128 + v] = kq;
+          bar_state();
+          const float u = __ldg(x.beta + row * x.ld_beta + h) *
+                          (bf16_to_float(__ldg(x.v + row * x.ld_v + (int64_t)h * kDeltaDim + v)) - (part[v] + part[128 + v]));
+          const float o = x.scale * fmaf(u, part[512 + v] + part[640 + v], part[256 + v] + part[384 + v]);
+          if (half == 0) p.out[(row * x.heads + h) * kDeltaDim + v] = float_to_bf16(o);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) S[i] = fmaf(u, r[64 * half + i], S[i]);
+        }
+        if (c + 1 < chunks) load_v(c + 1);
+        bar_state();
+        xchg(s, kMaxS, half) = own_max();
+        if (lane == 0) mbar_arrive(empty(s));
+        bar_state();
+        bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1));
+        // the issuer has seen this chunk: its barrier must not complete twice ahead of it
+        wait(empty(s), (c >> 1) & 1);
+        continue;
+      }
+      const float inv_s = pow2_inverse(sc_s);
+      // ---- R
+      const float inv_kp = inv_s * hd[kHdInvKp], sum_kp = hd[kHdSumKp];
+      wait(b_r, f & 1);
+      const float bound_r = fmaxf(xchg(s, kMaxV, 0), xchg(s, kMaxV, 1)) + bound_s * sum_kp;
+      const float sc_r = pow2_scale(bound_r, 14);
+      {
+        uint32_t acc[32], hi[16], lo[16];
+        tmem_ld32(quad + kColAcc + 32 * half, acc);
+        tmem_ld_wait();
+        float m = 0.f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const f32x2 r = fma2(pack2(-inv_kp, -inv_kp), pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])),
+                               pack2(__uint_as_float(vr[2 * t] << 16), __uint_as_float(vr[2 * t + 1] << 16)));
+          const float2 rf = unpack2(r);
+          m = fmaxf(m, fmaxf(fabsf(rf.x), fabsf(rf.y)));
+          split_f16(mul2(r, pack2(sc_r, sc_r)), hi[t], lo[t]);
+        }
+        tmem_st16(quad + kColParts + 16 * half, hi);
+        tmem_st16(quad + kColParts + 32 + 16 * half, lo);
+        xchg(s, kMaxR, half) = m;
+        tmem_st_wait();
+        arrive(b_rp);
+      }
+      if (c + 1 < chunks) load_v(c + 1);
+      // ---- U
+      const float inv_t = pow2_inverse(sc_r) * hd[kHdInvT], sum_t = hd[kHdSumT];
+      wait(b_u, f & 1);
+      const float sc_u = pow2_scale(fmaxf(xchg(s, kMaxR, 0), xchg(s, kMaxR, 1)) * sum_t, 14);
+      {
+        uint32_t acc[32], hi[16], lo[16];
+        tmem_ld32(quad + kColAcc + 32 * half, acc);
+        tmem_ld_wait();
+        float m = 0.f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const f32x2 u = mul2(pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])), pack2(inv_t, inv_t));
+          const float2 uf = unpack2(u);
+          m = fmaxf(m, fmaxf(fabsf(uf.x), fabsf(uf.y)));
+          split_f16(mul2(u, pack2(sc_u, sc_u)), hi[t], lo[t]);
+        }
+        tmem_st16(quad + kColParts + 16 * half, hi);
+        tmem_st16(quad + kColParts + 32 + 16 * half, lo);
+        xchg(s, kMaxU, half) = m;
+        tmem_st_wait();
+        arrive(b_up);
+      }
+      // ---- the state behind the chunk
+      const float inv_u = pow2_inverse(sc_u), inv_kd = inv_u * hd[kHdInvKd], sum_kd = hd[kHdSumKd], max_p = hd[kHdMaxP];
+      const float inv_o1 = inv_s * hd[kHdInvQp], inv_o2 = inv_u * hd[kHdInvB];
+      wait(b_ds, f & 1);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t acc[32];
+        tmem_ld32(quad + kColDs + 64 * half + 32 * g, acc);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 d = *reinterpret_cast<const float4*>(hd + kHdP + 64 * half + 32 * g + 4 * i);
+          float* st = S + 32 * g + 4 * i;
+          st[0] = fmaf(st[0], d.x, inv_kd * __uint_as_float(acc[4 * i]));
+          st[1] = fmaf(st[1], d.y, inv_kd * __uint_as_float(acc[4 * i + 1]));
+          st[2] = fmaf(st[2], d.z, inv_kd * __uint_as_float(acc[4 * i + 2]));
+          st[3] = fmaf(st[3], d.w, inv_kd * __uint_as_float(acc[4 * i + 3]));
+        }
+      }
+      bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1)) * max_p + fmaxf(xchg(s, kMaxU, 0), xchg(s, kMaxU, 1)) * sum_kd;
+      if (lane == 0) mbar_arrive(empty(s));
+      out_rows = rows, out_c = c, out_f1 = inv_o1, out_f2 = inv_o2;
+      ++f;
+    }
+    put_out();
+    if (float* to = state_out(p.s, b, 0, h)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        *reinterpret_cast<float4*>(to + v * kDeltaDim + 64 * half + 4 * i) =
+            make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+size_t delta_chunk_workspace_bytes(int rows, int batch, int heads) {
+  return ((size_t)rows / kChunk + batch) * heads * kRecBytes;
+}
+
+dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, void* workspace, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};   // devices whose kernels may take their shared memory
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem + 1024);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (dev < 64) ready.fetch_or(1ull << dev);
+  }
+  const ChunkArgs a{x, s, static_cast<uint8_t*>(workspace), out};
+  const int64_t records = ((int64_t)s.rows / kChunk + s.batch) * x.heads;
+  if (s.rows > 0) {
+    delta_prepare_kernel<<<(unsigned)records, kPrepThreads, kPrepSmem + 1024, st>>>(a);
+    count_launches(1);
+  }
+  delta_chain_kernel<<<(unsigned)(s.batch * x.heads), kChainThreads, kChainSmem, st>>>(a);
+  count_launches(1);
+  return launch_status();
+}
+
+}  // namespace dsa

@@ -41,8 +41,8 @@ def check_state(got, want, rows, size):
     assert (off <= state_tolerance(rows, size)).all(), (off / size).max()
 
 
-def check_out(got, want, rows, size, q):
-    off, tol = (got.double() - want).abs(), out_tolerance(want, rows, size, q, SCALE)
+def check_out(got, want, rows, size, mass, q, chunked=True):
+    off, tol = (got.double() - want).abs(), out_tolerance(want, rows, size, mass, q, SCALE, chunked)
     assert (off <= tol).all(), (off / tol).max()
 
 
@@ -68,8 +68,8 @@ def test_decode(batch, nq, heads, qk, gate, apart):
     for b in range(batch):
         r = slice(b * nq, (b + 1) * nq)
         s0 = before[slots_in[b]] if slots_in[b] >= 0 else torch.zeros_like(before[0])
-        want, states, size = rule(q[r], k[r], v[r], g[r], beta[r], SCALE, s0)
-        check_out(out[r], want, nq, size, q[r])
+        want, states, size, mass = rule(q[r], k[r], v[r], g[r], beta[r], SCALE, s0)
+        check_out(out[r], want, nq, size, mass, q[r], chunked=False)
         for j in range(nq):
             if slots_out[b, j] >= 0:
                 check_state(pool[slots_out[b, j]], states[j], j + 1, size)
@@ -108,8 +108,8 @@ def test_prefill(lens, heads, qk, gate):
     for b, n in enumerate(lens):
         r = slice(first[b], first[b + 1])
         s0 = before[slots_in[b]] if slots_in[b] >= 0 else torch.zeros_like(before[0])
-        want, states, size = rule(q[r], k[r], v[r], g[r], beta[r], SCALE, s0)
-        check_out(out[r], want, n, size, q[r])
+        want, states, size, mass = rule(q[r], k[r], v[r], g[r], beta[r], SCALE, s0)
+        check_out(out[r], want, n, size, mass, q[r])
         if slots_out[b] >= 0:
             check_state(pool[slots_out[b]], states[-1] if n else s0.double(), n, size)
             written.add(int(slots_out[b]))
@@ -128,8 +128,8 @@ def run_one(x, pool, out, st):
     before = pool[0].clone()
     prefill(pool, x, ints(0, out.shape[0]), ints(0), ints(1), out, st)
     assert st.item() == 0
-    want, states, size = rule(*x, SCALE, before)
-    check_out(out, want, out.shape[0], size, x[0])
+    want, states, size, mass = rule(*x, SCALE, before)
+    check_out(out, want, out.shape[0], size, mass, x[0])
     check_state(pool[1], states[-1], out.shape[0], size)
     return want
 
@@ -192,14 +192,14 @@ def test_rows_before_a_bad_one_keep_their_values(where, bad):
     good = torch.empty_like(out)
     p2 = pool.clone()
     prefill(p2, x, ints(0, n), ints(0), ints(1), good, st)
-    want, _, size = rule(*x, SCALE, pool[0])
+    want, _, size, mass = rule(*x, SCALE, pool[0])
     t = x["q k v gate beta".split().index(where)]
     t.view(n, 2, -1)[at, 0, 0] = bad
     prefill(pool, x, ints(0, n), ints(0), ints(1), out, st)
     assert st.item() == 0
-    check_out(out[:at], want[:at], n, size, x[0][:at])
+    check_out(out[:at], want[:at], n, size, mass[:at], x[0][:at])
     assert torch.isfinite(out[:, 1]).all() and torch.equal(out[:, 1], good[:, 1])   # the other head
-    bad64, states, _ = rule(*x, SCALE, pool[0])
+    bad64, states, _, _ = rule(*x, SCALE, pool[0])
     assert torch.equal(torch.isnan(out[at:, 0]) | torch.isinf(out[at:, 0]), ~torch.isfinite(bad64[at:, 0]))
     assert torch.equal(torch.isfinite(pool[1]), torch.isfinite(states[-1]))
 
@@ -208,7 +208,7 @@ def test_prefill_in_pieces_is_prefill_at_once_and_decode_goes_on():
     """A prompt at once, in chunks of 100 rows, and its last rows as draft rows: the same states and outputs."""
     n, heads = 333, 8
     x, pool, out, st = one(n, heads, seed=21)
-    want, states, size = rule(*x, SCALE, pool[0])
+    want, states, size, mass = rule(*x, SCALE, pool[0])
     for lo in range(0, 330, 110):
         part = [t[lo:lo + 110] for t in x]
         o = out[lo:lo + 110]
@@ -216,7 +216,7 @@ def test_prefill_in_pieces_is_prefill_at_once_and_decode_goes_on():
     B.gated_delta_decode(B.StatePool(pool), B.DeltaRows(*(t[330:] for t in x), SCALE), 3, ints(1), ints(-1, -1, 1).view(1, 3),
                          out[330:], st)
     assert st.item() == 0
-    check_out(out, want, n, size, x[0])
+    check_out(out, want, n, size, mass, x[0])
     check_state(pool[1], states[-1], n, size)
 
 
@@ -231,9 +231,9 @@ def test_states_in_the_packed_pool():
     out, st = torch.zeros((2, heads, DIM), dtype=torch.bfloat16, device="cuda"), status()
     B.gated_delta_decode(B.StatePool(view), B.DeltaRows(*x, SCALE), 2, ints(2), ints(-1, 3).view(1, 2), out, st)
     assert st.item() == 0
-    want, states, size = rule(*x, SCALE, s0[2])
+    want, states, size, mass = rule(*x, SCALE, s0[2])
     check_state(view[3], states[1], 2, size)
-    check_out(out, want, 2, size, x[0])
+    check_out(out, want, 2, size, mass, x[0], chunked=False)
     view[3] = s0[3]
     assert torch.equal(raw, before)
 
@@ -264,7 +264,7 @@ def test_side_stream_and_graph():
     n, heads = 300, 4
     x, pool, out, st = one(n, heads, seed=31)
     before = pool.clone()
-    want, states, size = rule(*x, SCALE, pool[0])
+    want, states, size, mass = rule(*x, SCALE, pool[0])
     ws = B.workspace(B.gated_delta_prefill_workspace_size(n, 1, heads))
     starts, a, b, both = ints(0, n), ints(0), ints(1), ints(0, 1)
     step, next_out = B.DeltaRows(*(t[:2] for t in x), SCALE), torch.zeros_like(out[:2])
@@ -277,7 +277,7 @@ def test_side_stream_and_graph():
     side.wait_stream(torch.cuda.current_stream())
     calls(side)
     side.synchronize()
-    check_out(out, want, n, size, x[0])
+    check_out(out, want, n, size, mass, x[0])
     eager = out.clone(), next_out.clone(), pool.clone()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -244,9 +244,9 @@ def test_a_step_of_the_calls_together():
             B.gated_delta_decode(spool, data, 1, own, own.view(3, 1), out, st)
         for i in range(3):
             r = slice(first[i], first[i + 1])
-            want, after, size = rule(*(t[r] for t in x), scale, want_state[i])
+            want, after, size, mass = rule(*(t[r] for t in x), scale, want_state[i])
             if n[i]:
-                assert ((out[r].double() - want).abs() <= out_tolerance(want, 300, size, x[0][r], scale)).all()
+                assert ((out[r].double() - want).abs() <= out_tolerance(want, 300, size, mass, x[0][r], scale, step == 0)).all()
                 want_state[i] = after[-1]
             off = (states[i].double() - want_state[i]).flatten(1).norm(dim=1)
             assert (off <= state_tolerance(300, size)).all()
