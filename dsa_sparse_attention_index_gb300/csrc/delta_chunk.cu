@@ -26,7 +26,7 @@ namespace {
 constexpr int kChunk = 64;
 constexpr int kTileHalf = kChunk * 128;                // 64 rows of 64 fp16 (128 bytes, 128-byte swizzle)
 constexpr int kTileBytes = 2 * kTileHalf;              // 64 rows x 128 channels
-// A record: K P (high and low parts), Q P, T (high and low), B, K D (high and low), then 256 floats.
+// A record: K P (high and low parts), Q P, T (high and low), then B, K D (high and low), then the head's floats.
 constexpr int kRecKp = 0;
 constexpr int kRecQp = kRecKp + 2 * kTileBytes;
 constexpr int kRecT = kRecQp + kTileBytes;
@@ -34,8 +34,10 @@ constexpr int kRecB = kRecT + 2 * kTileHalf;
 constexpr int kRecKd = kRecB + kTileHalf;
 constexpr int kRecHead = kRecKd + 2 * kTileBytes;      // 106,496
 constexpr int kRecBytes = kRecHead + 1024;
+constexpr int kPart1 = kRecB, kPart2 = kRecHead - kRecB;   // what is read first, and last
 // floats of the record's head
-enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvT, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdMaxP, kHdP = 128 };
+enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvT, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdMaxP, kHdP = 16 };
+constexpr int kHeadBytes = 4 * (kHdP + kDeltaDim);
 
 struct ChunkArgs {
   DeltaRows x;
@@ -51,29 +53,13 @@ __device__ __forceinline__ float pow2_scale(float bound, int top) {
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
-// Two fp32 in a register pair: one instruction for both.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float x, float y) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, pack2(-1.f, -1.f), a); }
+// Two neighbouring channels.  (The packed fp32 instructions take fewer slots, but
+// the moves into register pairs cost more: chain 164 us with them, 145 without.)
+using f32x2 = float2;
+__device__ __forceinline__ f32x2 pack2(float x, float y) { return make_float2(x, y); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return make_float2(a.x - b.x, a.y - b.y); }
 __device__ __forceinline__ float reciprocal(float x) {   // within one unit in the last place
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -91,9 +77,9 @@ __device__ __forceinline__ uint32_t f16x2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ void split_f16(f32x2 v, uint32_t& hi, uint32_t& lo) {
-  const float2 f = unpack2(v);
+  const float2 f = v;
   const float hx = __uint_as_float(__float_as_uint(f.x) & 0xFFFFE000u), hy = __uint_as_float(__float_as_uint(f.y) & 0xFFFFE000u);
-  const float2 r = unpack2(sub2(v, pack2(hx, hy)));
+  const float2 r = sub2(v, pack2(hx, hy));
   hi = f16x2(hx, hy);
   lo = f16x2(r.x, r.y);
 }
@@ -103,9 +89,9 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ void split_bf16(f32x2 v, uint32_t& hi, uint32_t& lo) {
-  const float2 f = unpack2(v);
+  const float2 f = v;
   hi = bf16x2(f.x, f.y);
-  const float2 r = unpack2(sub2(v, bf16x2_to_f32x2(hi)));
+  const float2 r = sub2(v, bf16x2_to_f32x2(hi));
   lo = bf16x2(r.x, r.y);
 }
 
@@ -269,7 +255,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   uint32_t km = 0, qm = 0;
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
-    const float2 g = unpack2(a[t]);
+    const float2 g = a[t];
     const float ex = expf(g.x), ey = expf(g.y);
     a[t] = pack2(ex, ey);
     block = mul2(block, a[t]);
@@ -280,7 +266,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     km = __vmaxu2(km, kr[t] & 0x7FFF7FFFu), qm = __vmaxu2(qm, qr[t] & 0x7FFF7FFFu);
   }
   bad |= !(amax <= 3.4e38f);
-  const float Bx = unpack2(block).x, By = unpack2(block).y;
+  const float Bx = block.x, By = block.y;
   tab[I * kDeltaDim + 2 * q2] = Bx, tab[I * kDeltaDim + 2 * q2 + 1] = By;
   {
     const float k1 = __uint_as_float(max(km & 0xFFFFu, km >> 16) << 16), q1 = __uint_as_float(max(qm & 0xFFFFu, qm >> 16) << 16);
@@ -327,11 +313,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     return __uint_as_float((uint32_t)(127 + max(-60, min(60, -(e / 2)))) << 23);
   };
   auto centre = [&](int b) {
-    const float2 v = unpack2(block_of(b));
+    const float2 v = block_of(b);
     return pack2(centre1(v.x), centre1(v.y));
   };
   auto uncentre = [&](int b) {
-    const float2 v = unpack2(centre(b));
+    const float2 v = centre(b);
     return pack2(pow2_inverse(v.x), pow2_inverse(v.y));
   };
   // image offsets of channel pair q2 in rows of 128 bytes, 64 channels a block
@@ -351,7 +337,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       split_f16(mul2(k, mul2(l, pre_k)), hi2, lo2);
       *reinterpret_cast<uint32_t*>(rec + kRecKp + o) = hi2;
       *reinterpret_cast<uint32_t*>(rec + kRecKp + kTileBytes + o) = lo2;
-      const float2 qp = unpack2(mul2(ql, pre_q)), xq = unpack2(mul2(ql, c_q)), wf = unpack2(w);
+      const float2 qp = mul2(ql, pre_q), xq = mul2(ql, c_q), wf = w;
       *reinterpret_cast<uint32_t*>(rec + kRecQp + o) = f16x2(qp.x, qp.y);
       const uint32_t s = at256(r, piece) + in_piece;
       split_bf16(mul2(k, w), hi2, lo2);
@@ -565,20 +551,24 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 //   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
 // The parts of a row of S, R or U are times a power of two from a bound of it, so
 // that they keep 22 bits of its largest element whatever its size.
-constexpr int kChainThreads = 10 * 32;
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kChainThreads = 11 * 32;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kStoreWarp = 10;
 constexpr int kColS = 0;       // keys 64 h ..: high parts in columns 64 h .. + 31, low parts behind them
 constexpr int kColAcc = 128;   // R, then U
 constexpr int kColParts = 192; // R's, then U's parts: high 32 columns, low 32
 constexpr int kColDs = 256;
 constexpr int kColO1 = 384, kColO2 = 448;
-constexpr int kCOffX = 2 * kRecBytes;                   // exchanged maxima [2 parities][4 kinds][2 halves][128]
-constexpr int kCOffRow = kCOffX + 2 * 4 * 2 * 128 * 4;  // a row's k, q, decay (two buffers) and partial sums, where rows go one by one
-constexpr int kCOffBars = kCOffRow + (2 * 3 * 128 + 3 * 2 * 128) * 4;
-constexpr int kCNumBars = 13;
+constexpr int kRowBytes = kDeltaDim * 2;                // a row of values or outputs
+constexpr int kCOffPart2 = 2 * kPart1;                  // one buffer: its products come last in a chunk
+constexpr int kCOffV = kCOffPart2 + kPart2;
+constexpr int kCOffOut = kCOffV + 2 * kChunk * kRowBytes;
+constexpr int kCOffHead = kCOffOut + kChunk * kRowBytes;
+constexpr int kCOffX = kCOffHead + 2 * 640;             // exchanged maxima [2 parities][4 kinds][2 halves][128]
+constexpr int kCOffBars = kCOffX + 2 * 4 * 2 * 128 * 4;
+constexpr int kCNumBars = 21;
 constexpr int kCOffMisc = kCOffBars + kCNumBars * 8;
-constexpr int kChainSmem = 1024 + kCOffMisc + 32;
-static_assert(kChainSmem <= 232448 && kRecBytes % 1024 == 0, "shared memory");
+constexpr int kChainSmem = 1024 + kCOffMisc + 40;
+static_assert(kChainSmem <= 232448 && kPart1 % 1024 == 0 && kPart2 % 1024 == 0 && kHeadBytes <= 640, "shared memory");
 
 __device__ __forceinline__ void bar_state() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool bar_state_or(bool v) {
@@ -591,15 +581,14 @@ __device__ __forceinline__ bool bar_state_or(bool v) {
   return r != 0;
 }
 
-__device__ __forceinline__ uint32_t load_u16(const uint16_t* p) {
-  uint32_t r;
-  asm volatile("{\n .reg .u16 t;\n ld.global.nc.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n" : "=r"(r) : "l"(p));
-  return r;
-}
 __device__ __forceinline__ uint32_t max_abs_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("{\n .reg .b32 t;\n abs.f16x2 t, %2;\n max.f16x2 %0, %1, t;\n}\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ float max_of_f16x2(uint32_t v) {
+  const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return fmaxf(m.x, m.y);
 }
 
 __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const ChunkArgs p) {
@@ -617,20 +606,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
   const int64_t rec_step = (int64_t)x.heads * kRecBytes;
 
   const uint32_t bars = sm + kCOffBars;
-  auto full = [&](int s) { return bars + 8u * s; };
+  auto full = [&](int s) { return bars + 8u * s; };          // first part and head
   auto empty = [&](int s) { return bars + 16u + 8u * s; };
-  const uint32_t b_s = bars + 32, b_r = bars + 40, b_rp = bars + 48, b_u = bars + 56, b_up = bars + 64, b_ds = bars + 72,
-                 b_o = bars + 80, b_of = bars + 88, drain = bars + 96;
+  const uint32_t full2 = bars + 32, empty2 = bars + 40, b_s = bars + 48, b_r = bars + 56, b_rp = bars + 64, b_u = bars + 72,
+                 b_up = bars + 80, b_ds = bars + 88, b_o = bars + 96, b_of = bars + 104, out_full = bars + 112,
+                 out_free = bars + 120, drain = bars + 128;
+  auto full_v = [&](int s) { return bars + 136u + 8u * s; };
+  auto empty_v = [&](int s) { return bars + 152u + 8u * s; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kCOffMisc + 4);
-  volatile int* by_rows = reinterpret_cast<volatile int*>(smem + kCOffMisc + 8);   // [2]: this chunk goes row by row
+  volatile int* by_rows = reinterpret_cast<volatile int*>(smem + kCOffMisc + 8);    // [2]: this chunk goes row by row
+  volatile int* out_job = reinterpret_cast<volatile int*>(smem + kCOffMisc + 16);   // chunk and rows to store; 0 rows: no more
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 9);
+      mbar_init(full_v(s), 1);
+      mbar_init(empty_v(s), 8);
     }
-    for (uint32_t a : {b_r, b_u, b_ds, b_o, drain}) mbar_init(a, 1);
-    for (uint32_t a : {b_s, b_rp, b_up, b_of}) mbar_init(a, 8);
+    for (uint32_t a : {full2, empty2, b_r, b_u, b_ds, b_o, out_free, drain}) mbar_init(a, 1);
+    for (uint32_t a : {b_s, b_rp, b_up, b_of, out_full}) mbar_init(a, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -644,39 +639,75 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == kCopyWarp) {
+    // the values one chunk further ahead than the operands: they are looked at during the chunk before theirs
     bool ok = true;
-    int issued = 0;
-    for (int c = 0; c < chunks; ++c) {
+    int issued_v = 0, issued = 0, issued2 = 0;
+    auto copy_v = [&](int c) {
+      const int s = c & 1, rows = min(kChunk, n - c * kChunk);
+      if (c >= 2 && !mbar_wait_warp(empty_v(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status)) return false;
+      if (elect_one()) mbar_arrive_expect_tx(full_v(s), rows * kRowBytes);
+      __syncwarp();
+      for (int t = lane; t < rows; t += 32)
+        bulk_load(sm + kCOffV + (s * kChunk + t) * kRowBytes, x.v + (row0 + c * kChunk + t) * x.ld_v + (int64_t)h * kDeltaDim,
+                  kRowBytes, full_v(s));
+      __syncwarp();
+      ++issued_v;
+      return true;
+    };
+    if (chunks > 0) ok = copy_v(0);
+    for (int c = 0; c < chunks && ok; ++c) {
       const int s = c & 1;
+      const uint8_t* src = rec + c * rec_step;
       if (c >= 2) ok = mbar_wait_warp(empty(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status);
       if (!ok) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(full(s), kRecBytes);
-        for (int i = 0; i < 4; ++i)
-          bulk_load(sm + s * kRecBytes + i * (kRecBytes / 4), rec + c * rec_step + i * (kRecBytes / 4), kRecBytes / 4, full(s));
+        mbar_arrive_expect_tx(full(s), kPart1 + kHeadBytes);
+        for (int i = 0; i < 4; ++i) bulk_load(sm + s * kPart1 + i * (kPart1 / 4), src + i * (kPart1 / 4), kPart1 / 4, full(s));
+        bulk_load(sm + kCOffHead + s * 640, src + kRecHead, kHeadBytes, full(s));
       }
       __syncwarp();
       ++issued;
+      if (c + 1 < chunks) ok = copy_v(c + 1);
+      if (ok && c >= 1) ok = mbar_wait_warp(empty2, (c - 1) & 1, abort_flag, p.s.status);
+      if (!ok) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full2, kPart2);
+        for (int i = 0; i < 2; ++i) bulk_load(sm + kCOffPart2 + i * (kPart2 / 2), src + kRecB + i * (kPart2 / 2), kPart2 / 2, full2);
+      }
+      __syncwarp();
+      ++issued2;
     }
     // no copy is in flight at the exit, also after another role gave up
+    for (int c = max(0, issued_v - 2); c < issued_v; ++c) mbar_wait_drain(full_v(c & 1), (c >> 1) & 1, 10000000ull);
     for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait_drain(full(c & 1), (c >> 1) & 1, 10000000ull);
+    if (issued2 > 0) mbar_wait_drain(full2, (issued2 - 1) & 1, 10000000ull);
+  } else if (warp == kStoreWarp) {
+    for (uint32_t j = 0;; ++j) {
+      if (!mbar_wait_warp(out_full, j & 1, abort_flag, p.s.status)) break;
+      const int c = __shfl_sync(0xffffffffu, out_job[0], 0), rows = __shfl_sync(0xffffffffu, out_job[1], 0);
+      if (rows == 0) break;
+      // two rows at a time, 16 bytes a lane (bulk copies would stand in line behind the next operands')
+      const uint4* src = reinterpret_cast<const uint4*>(smem + kCOffOut) + lane;
+      uint16_t* dst = p.out + ((row0 + c * kChunk + (lane >> 4)) * x.heads + h) * kDeltaDim + 8 * (lane & 15);
+#pragma unroll 8
+      for (int t = 0; t < rows; t += 2)
+        if (t + (lane >> 4) < rows) *reinterpret_cast<uint4*>(dst + (int64_t)t * x.heads * kDeltaDim) = src[16 * t];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(out_free);
+    }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t kIdesc64 = make_idesc(kFmtF16, kFmtF16, 0, 0, 128, kChunk);
     constexpr uint32_t kIdescDs = make_idesc(kFmtF16, kFmtF16, 0, 1, 128, kDeltaDim);
     const uint64_t kdesc = smem_desc(sm, 16, 1024, kLayoutSw128);                  // K-major tiles
-    const uint64_t ndesc = smem_desc(sm + kRecKd, kTileHalf, 1024, kLayoutSw128);  // K D: 64 keys a block
+    const uint64_t bdesc = smem_desc(sm + kCOffPart2, 16, 1024, kLayoutSw128);     // B
+    const uint64_t ndesc = smem_desc(sm + kCOffPart2 + kTileHalf, kTileHalf, 1024, kLayoutSw128);  // K D: 64 keys a block
     const uint32_t k_hi = (uint32_t)(kdesc >> 32), n_hi = (uint32_t)(ndesc >> 32);
     uint32_t f = 0;   // chunks that took the tensor core
     for (int c = 0; c < chunks; ++c) {
       const int s = c & 1;
-      const uint32_t k0 = (uint32_t)kdesc + s * (kRecBytes / 16), n0 = (uint32_t)ndesc + s * (kRecBytes / 16);
+      const uint32_t k0 = (uint32_t)kdesc + s * (kPart1 / 16), b0 = (uint32_t)bdesc, n0 = (uint32_t)ndesc;
       if (!mbar_wait_warp(full(s), (c >> 1) & 1, abort_flag, p.s.status)) break;
       if (!mbar_wait_warp(b_s, c & 1, abort_flag, p.s.status)) break;
-      if (__any_sync(0xffffffffu, by_rows[s] != 0)) {
-        if (elect_one()) mbar_arrive(empty(s));
-        __syncwarp();
-        continue;
-      }
       tc_fence_after();
       auto product_s = [&](uint32_t d, int part, int tile, bool more) {   // A: the state's part, 128 keys
 #pragma unroll
@@ -684,10 +715,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
           mma_bf16_tmem_a(tmem + d, tmem + kColS + 64 * (ks >> 2) + 32 * part + 8 * (ks & 3),
                           desc64(k0 + (tile + (ks >> 2) * kTileHalf) / 16 + 2 * (ks & 3), k_hi), kIdesc64, more || ks ? 1u : 0u);
       };
-      auto product_t = [&](uint32_t d, int part, int tile, bool more) {   // A: R's or U's part, 64 rows
+      auto product_t = [&](uint32_t d, int part, uint32_t tile, bool more) {   // A: R's or U's part, 64 rows
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_tmem_a(tmem + d, tmem + kColParts + 32 * part + 8 * ks, desc64(k0 + tile / 16 + 2 * ks, k_hi), kIdesc64,
+          mma_bf16_tmem_a(tmem + d, tmem + kColParts + 32 * part + 8 * ks, desc64(tile + 2 * ks, k_hi), kIdesc64,
                           more || ks ? 1u : 0u);
       };
       if (elect_one()) {
@@ -697,19 +728,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         mma_commit(b_r);
       }
       __syncwarp();
-      if (!mbar_wait_warp(b_rp, f & 1, abort_flag, p.s.status)) break;
+      if (!mbar_wait_warp(b_rp, c & 1, abort_flag, p.s.status)) break;
+      if (__any_sync(0xffffffffu, by_rows[s] != 0)) {
+        // nothing of this chunk comes from the tensor core: its buffers go back
+        if (!mbar_wait_warp(full2, c & 1, abort_flag, p.s.status)) break;
+        if (elect_one()) {
+          mbar_arrive(empty(s));
+          mbar_arrive(empty2);
+        }
+        __syncwarp();
+        continue;
+      }
       tc_fence_after();
       if (elect_one()) {
-        product_t(kColAcc, 1, kRecT, false);
-        product_t(kColAcc, 0, kRecT + kTileHalf, true);
-        product_t(kColAcc, 0, kRecT, true);
+        product_t(kColAcc, 1, k0 + kRecT / 16, false);
+        product_t(kColAcc, 0, k0 + (kRecT + kTileHalf) / 16, true);
+        product_t(kColAcc, 0, k0 + kRecT / 16, true);
         mma_commit(b_u);
       }
       __syncwarp();
-      if (f > 0 && !mbar_wait_warp(b_of, (f - 1) & 1, abort_flag, p.s.status)) break;
-      tc_fence_after();
-      if (elect_one()) product_s(kColO1, 0, kRecQp, false);
-      __syncwarp();
+      if (!mbar_wait_warp(full2, c & 1, abort_flag, p.s.status)) break;
       if (!mbar_wait_warp(b_up, f & 1, abort_flag, p.s.status)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -720,9 +758,17 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
             mma_bf16_tmem_a(tmem + kColDs, tmem + kColParts + (q == 0 ? 32 : 0) + 8 * ks,
                             desc64(n0 + (q == 1 ? kTileBytes / 16 : 0) + ks * (16 * 128 / 16), n_hi), kIdescDs, q | ks ? 1u : 0u);
         mma_commit(b_ds);
-        product_t(kColO2, 0, kRecB, false);
+      }
+      __syncwarp();
+      // the outputs' products run while the state is updated
+      if (f > 0 && !mbar_wait_warp(b_of, (f - 1) & 1, abort_flag, p.s.status)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        product_s(kColO1, 0, kRecQp, false);
+        product_t(kColO2, 0, b0, false);
         mma_commit(b_o);
         mma_commit(empty(s));
+        mma_commit(empty2);
       }
       __syncwarp();
       ++f;
@@ -758,25 +804,23 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(S[i]));
       return m;
     };
-    // the chunk's values of this lane, rows 32 half .. + 31: apart until they are used, or the loads would be waited for
-    uint32_t vr[32];
-    auto load_v = [&](int c) {
-      // rows that are not there repeat the last one, so that no load stands in a branch; they are cleared where used
-      const uint16_t* vp = x.v + (row0 + c * kChunk) * x.ld_v + (int64_t)h * kDeltaDim + v;
-      const int last = min(kChunk, n - c * kChunk) - 1;
-      if (last == kChunk - 1) {
-        vp += 32 * half * x.ld_v;
-#pragma unroll
-        for (int t = 0; t < 32; ++t, vp += x.ld_v) vr[t] = load_u16(vp);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 32; ++t) vr[t] = load_u16(vp + min(32 * half + t, last) * x.ld_v);
-      }
-    };
-    if (chunks > 0) load_v(0);
     xchg(1, kMaxS, half) = own_max();
     bar_state();
     float bound_s = fmaxf(xchg(1, kMaxS, 0), xchg(1, kMaxS, 1));
+    float sc_s = 1.f;   // what the row of the state in registers is times
+    auto rescale = [&]() {
+      // another power of two only where the bound has left [2^4, 2^15): a row keeps 21 bits of its largest element
+      // down to a bound 2^10 above it.  The bound holds for the state before and behind a chunk, so neither overflows.
+      const float b = bound_s * sc_s;
+      const bool moved = !(b >= 16.f && b < 32768.f) && !(bound_s == 0.f && sc_s == 1.f);
+      if (__any_sync(0xffffffffu, moved)) {
+        const float to = !moved ? sc_s : bound_s == 0.f ? 1.f : pow2_scale(bound_s, 12), by = to * pow2_inverse(sc_s);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) S[i] *= by;
+        sc_s = to;
+      }
+    };
+    rescale();
     uint32_t f = 0;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       mbar_wait_warp(bar, parity, abort_flag, p.s.status);
@@ -788,68 +832,103 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       if (lane == 0) mbar_arrive(bar);
     };
 
+    // a chunk's values of this lane, rows 32 half .. + 31, two a register, and whether it goes row by row: read while
+    // the chunk before waits for its products
+    uint32_t vr[16], vmax = 0;
+    auto read_v = [&](int c) {
+      const int s = c & 1, left = min(kChunk, n - c * kChunk) - 32 * half;
+      wait(full_v(s), (c >> 1) & 1);
+      const uint16_t* vp = reinterpret_cast<const uint16_t*>(smem + kCOffV) + (s * kChunk + 32 * half) * kDeltaDim + v;
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        vr[t] = __byte_perm((uint32_t)vp[2 * t * kDeltaDim], (uint32_t)vp[(2 * t + 1) * kDeltaDim], 0x5410);
+      if (left < 32) {   // rows that are not there
+#pragma unroll
+        for (int t = 0; t < 16; ++t) vr[t] = 2 * t >= left ? 0u : 2 * t + 1 >= left ? vr[t] & 0xFFFFu : vr[t];
+      }
+    };
+    auto vote = [&](int c) {
+      const int s = c & 1;
+      uint32_t m = 0;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) m = __vmaxu2(m, vr[t] & 0x7FFF7FFFu);
+      vmax = max(m & 0xFFFFu, m >> 16);
+      xchg(s, kMaxV, half) = __uint_as_float(vmax << 16);
+      if (lane == 0) mbar_arrive(empty_v(s));
+      return bar_state_or(vmax >= 0x7F80u);
+    };
+    bool rowwise = false;   // a value of the chunk is no number
+    if (chunks > 0) {
+      read_v(0);
+      rowwise = vote(0);
+    }
+
     // the outputs of the last chunk that took the tensor core, behind the next one's first operand
     int out_rows = 0, out_c = 0;
     float out_f1 = 0.f, out_f2 = 0.f;
-    auto put_out = [&]() {
+    uint32_t jobs = 0;
+    auto put_out = [&](int q) {   // in two halves, each where the warps would wait
       if (out_rows == 0) return;
-      wait(b_o, (f - 1) & 1);
-      uint32_t o1[32], o2[32];
-      tmem_ld32(quad + kColO1 + 32 * half, o1);
-      tmem_ld32(quad + kColO2 + 32 * half, o2);
+      uint32_t o1[16], o2[16];
+      tmem_ld16(quad + kColO1 + 32 * half + 16 * q, o1);
+      tmem_ld16(quad + kColO2 + 32 * half + 16 * q, o2);
+      if (q == 0 && jobs > 0) wait(out_free, (jobs - 1) & 1);
       tmem_ld_wait();
-      arrive(b_of);
-      const int64_t step = (int64_t)x.heads * kDeltaDim;
-      uint16_t* op = p.out + (row0 + out_c * kChunk + 32 * half) * step + (int64_t)h * kDeltaDim + v;
-      const int left = out_rows - 32 * half;
+      if (q == 1) arrive(b_of);
+      uint16_t* op = reinterpret_cast<uint16_t*>(smem + kCOffOut) + (32 * half + 16 * q) * kDeltaDim + v;
 #pragma unroll
-      for (int t = 0; t < 32; t += 2, op += 2 * step) {
+      for (int t = 0; t < 16; t += 2) {
         const uint32_t o = bf16x2(fmaf(out_f1, __uint_as_float(o1[t]), out_f2 * __uint_as_float(o2[t])),
                                   fmaf(out_f1, __uint_as_float(o1[t + 1]), out_f2 * __uint_as_float(o2[t + 1])));
-        if (t < left) op[0] = (uint16_t)o;
-        if (t + 1 < left) op[step] = (uint16_t)(o >> 16);
+        op[t * kDeltaDim] = (uint16_t)o;
+        op[(t + 1) * kDeltaDim] = (uint16_t)(o >> 16);
       }
+      if (q == 0) return;
+      if (tid == 0) out_job[0] = out_c, out_job[1] = out_rows;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(out_full);
+      ++jobs;
       out_rows = 0;
     };
 
     for (int c = 0; c < chunks; ++c) {
       const int s = c & 1;
       const int rows = min(kChunk, n - c * kChunk);
-      const float* hd = reinterpret_cast<const float*>(smem + s * kRecBytes + kRecHead);
-      // ---- the state's parts
-      const float sc_s = pow2_scale(bound_s, 14);
-      const f32x2 sc_s2 = pack2(sc_s, sc_s);
+      const float* hd = reinterpret_cast<const float*>(smem + kCOffHead + s * 640);
+      // ---- the state's parts; the outputs' products, which read the last ones, are through
+      if (out_rows > 0) wait(b_o, (f - 1) & 1);
       uint32_t top = 0u;   // the largest high part: the state's largest value is within 2^-10 of it
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) split_f16(mul2(pack2(S[32 * g + 2 * i], S[32 * g + 2 * i + 1]), sc_s2), hi[i], lo[i]);
+        for (int i = 0; i < 16; ++i) split_f16(pack2(S[32 * g + 2 * i], S[32 * g + 2 * i + 1]), hi[i], lo[i]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = max_abs_f16x2(top, hi[i]);
         tmem_st16(quad + kColS + 64 * half + 16 * g, hi);
         tmem_st16(quad + kColS + 64 * half + 32 + 16 * g, lo);
       }
       {
-        const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&top));
-        xchg(s, kMaxS, half) = fmaxf(m.x, m.y) * pow2_inverse(sc_s) * 1.001f;
+        xchg(s, kMaxS, half) = max_of_f16x2(top) * pow2_inverse(sc_s) * 1.001f;
       }
-      uint32_t vmax = 0;
-#pragma unroll
-      for (int t = 0; t < 32; ++t) {
-        if (rows < kChunk && 32 * half + t >= rows) vr[t] = 0u;
-        vmax = max(vmax, vr[t] & 0x7FFFu);
-      }
-      xchg(s, kMaxV, half) = __uint_as_float(vmax << 16);
       tmem_st_wait();
-      wait(full(s), (c >> 1) & 1);
-      const bool rowwise = bar_state_or(vmax >= 0x7F80u || reinterpret_cast<const int*>(hd)[kHdBad] != 0);
-      if (tid == 0) by_rows[s] = rowwise;
       arrive(b_s);
-      put_out();
+      put_out(0);
+      wait(full(s), (c >> 1) & 1);
+      rowwise |= reinterpret_cast<const int*>(hd)[kHdBad] != 0;
+      if (tid == 0) by_rows[s] = rowwise;
+      wait(b_r, c & 1);
       if (rowwise) {
+        // back to the state itself
+        const float un = pow2_inverse(sc_s);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) S[i] *= un;
+        sc_s = 1.f;
         // a value that is no number, or out of range, touches nothing of the rows before it: one row after another
-        float* rb = reinterpret_cast<float*>(smem + kCOffRow);       // [2][k, q, decay][128]
+        put_out(1);
+        arrive(b_rp);
+        // in the place of operands that nothing reads now: a row's k, q and decay, two buffers, and partial sums
+        float* rb = reinterpret_cast<float*>(smem + s * kPart1);     // [2][k, q, decay][128]
         float* part = rb + 2 * 3 * 128;                              // [p, w, k q][2 halves][128]
         for (int t = 0; t < rows; ++t) {
           const int64_t row = row0 + c * kChunk + t;
@@ -876,68 +955,76 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
 #pragma unroll
           for (int i = 0; i < 64; ++i) S[i] = fmaf(u, r[64 * half + i], S[i]);
         }
-        if (c + 1 < chunks) load_v(c + 1);
         bar_state();
         xchg(s, kMaxS, half) = own_max();
+        fence_proxy_async_smem();   // copies write there again
+        __syncwarp();
         if (lane == 0) mbar_arrive(empty(s));
         bar_state();
         bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1));
-        // the issuer has seen this chunk: its barrier must not complete twice ahead of it
-        wait(empty(s), (c >> 1) & 1);
+        rescale();
+        if (c + 1 < chunks) {
+          read_v(c + 1);
+          rowwise = vote(c + 1);
+        }
         continue;
       }
       const float inv_s = pow2_inverse(sc_s);
       // ---- R
       const float inv_kp = inv_s * hd[kHdInvKp], sum_kp = hd[kHdSumKp];
-      wait(b_r, f & 1);
       const float bound_r = fmaxf(xchg(s, kMaxV, 0), xchg(s, kMaxV, 1)) + bound_s * sum_kp;
       const float sc_r = pow2_scale(bound_r, 14);
       {
         uint32_t acc[32], hi[16], lo[16];
         tmem_ld32(quad + kColAcc + 32 * half, acc);
         tmem_ld_wait();
-        float m = 0.f;
+        uint32_t top = 0u;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           const f32x2 r = fma2(pack2(-inv_kp, -inv_kp), pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])),
-                               pack2(__uint_as_float(vr[2 * t] << 16), __uint_as_float(vr[2 * t + 1] << 16)));
-          const float2 rf = unpack2(r);
-          m = fmaxf(m, fmaxf(fabsf(rf.x), fabsf(rf.y)));
+                               bf16x2_to_f32x2(vr[t]));
           split_f16(mul2(r, pack2(sc_r, sc_r)), hi[t], lo[t]);
+          top = max_abs_f16x2(top, hi[t]);
         }
         tmem_st16(quad + kColParts + 16 * half, hi);
         tmem_st16(quad + kColParts + 32 + 16 * half, lo);
-        xchg(s, kMaxR, half) = m;
+        xchg(s, kMaxR, half) = max_of_f16x2(top) * pow2_inverse(sc_r) * 1.001f;
         tmem_st_wait();
         arrive(b_rp);
       }
-      if (c + 1 < chunks) load_v(c + 1);
       // ---- U
       const float inv_t = pow2_inverse(sc_r) * hd[kHdInvT], sum_t = hd[kHdSumT];
+      put_out(1);
       wait(b_u, f & 1);
       const float sc_u = pow2_scale(fmaxf(xchg(s, kMaxR, 0), xchg(s, kMaxR, 1)) * sum_t, 14);
       {
         uint32_t acc[32], hi[16], lo[16];
         tmem_ld32(quad + kColAcc + 32 * half, acc);
         tmem_ld_wait();
-        float m = 0.f;
+        uint32_t top = 0u;
+        const float f_u = inv_t * sc_u;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          const f32x2 u = mul2(pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])), pack2(inv_t, inv_t));
-          const float2 uf = unpack2(u);
-          m = fmaxf(m, fmaxf(fabsf(uf.x), fabsf(uf.y)));
-          split_f16(mul2(u, pack2(sc_u, sc_u)), hi[t], lo[t]);
+          split_f16(mul2(pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])), pack2(f_u, f_u)), hi[t], lo[t]);
+          top = max_abs_f16x2(top, hi[t]);
         }
         tmem_st16(quad + kColParts + 16 * half, hi);
         tmem_st16(quad + kColParts + 32 + 16 * half, lo);
-        xchg(s, kMaxU, half) = m;
+        xchg(s, kMaxU, half) = max_of_f16x2(top) * pow2_inverse(sc_u) * 1.001f;
         tmem_st_wait();
         arrive(b_up);
       }
       // ---- the state behind the chunk
-      const float inv_u = pow2_inverse(sc_u), inv_kd = inv_u * hd[kHdInvKd], sum_kd = hd[kHdSumKd], max_p = hd[kHdMaxP];
+      const float inv_u = pow2_inverse(sc_u), sum_kd = hd[kHdSumKd], max_p = hd[kHdMaxP];
       const float inv_o1 = inv_s * hd[kHdInvQp], inv_o2 = inv_u * hd[kHdInvB];
+      if (c + 1 < chunks) {
+        read_v(c + 1);
+        rowwise = vote(c + 1);
+      }
       wait(b_ds, f & 1);
+      bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1)) * max_p + fmaxf(xchg(s, kMaxU, 0), xchg(s, kMaxU, 1)) * sum_kd;
+      rescale();
+      const float inv_kd = inv_u * hd[kHdInvKd] * sc_s;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t acc[32];
@@ -953,13 +1040,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
           st[3] = fmaf(st[3], d.w, inv_kd * __uint_as_float(acc[4 * i + 3]));
         }
       }
-      bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1)) * max_p + fmaxf(xchg(s, kMaxU, 0), xchg(s, kMaxU, 1)) * sum_kd;
       if (lane == 0) mbar_arrive(empty(s));
       out_rows = rows, out_c = c, out_f1 = inv_o1, out_f2 = inv_o2;
       ++f;
     }
-    put_out();
+    if (out_rows > 0) wait(b_o, (f - 1) & 1);
+    put_out(0);
+    put_out(1);
+    if (jobs > 0) wait(out_free, (jobs - 1) & 1);
+    if (tid == 0) out_job[1] = 0;
+    if (lane == 0) mbar_arrive(out_full);
     if (float* to = state_out(p.s, b, 0, h)) {
+      const float un = pow2_inverse(sc_s);
+#pragma unroll
+      for (int i = 0; i < 64; ++i) S[i] *= un;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         *reinterpret_cast<float4*>(to + v * kDeltaDim + 64 * half + 4 * i) =
