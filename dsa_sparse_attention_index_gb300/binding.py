@@ -489,36 +489,38 @@ def cache_append_slots(cache: PagedCache, slots, new_latent, new_index_key, stat
                                         _status(status), _stream(stream)), "dsa_cache_append_slots")
 
 
-@dataclass
+def _rows_of(name: str, t, shape, dtypes):
+    """Address and row stride of a tensor of this shape whose rows are contiguous but may lie apart."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or not t.is_cuda:
+        raise ValueError(f"{name}: expected {list(shape)} of {dtypes[0]} on the GPU, got {list(t.shape)} of {t.dtype}")
+    inner = 1
+    for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and stride != inner:
+            raise ValueError(f"{name}: rows must be contiguous, got strides {list(t.stride())}")
+        inner *= size
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else inner
+
+
+@dataclass(frozen=True)
 class StatePool:
     """The recurrent layers' states, fp32 [slots, heads, 128 values, 128 keys] on the GPU: a tensor of its own, or a
-    view into the packed cache's block rows (slots may lie apart)."""
+    view into the packed cache's block rows (slots may lie apart).  Its layout is read once, here."""
 
     states: torch.Tensor
 
-    def struct(self) -> StatePoolT:
+    def __post_init__(self):
         t = self.states
-        if t.dtype not in _F32 or t.dim() != 4 or t.shape[2:] != (DELTA_DIM, DELTA_DIM) or not t.is_cuda or (
-                t.shape[0] and not t[0].is_contiguous()):
-            raise ValueError(f"states: expected float32 [slots, heads, {DELTA_DIM}, {DELTA_DIM}] on the GPU, each slot "
-                             f"contiguous, got {list(t.shape)} of {t.dtype}")
-        stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * DELTA_DIM * DELTA_DIM
-        return StatePoolT(t.data_ptr(), 4 * stride, t.shape[0], t.shape[1])
+        if t.dim() != 4:
+            raise ValueError(f"states: expected [slots, heads, {DELTA_DIM}, {DELTA_DIM}], got {list(t.shape)}")
+        ptr, stride = _rows_of("states", t, (t.shape[0], t.shape[1], DELTA_DIM, DELTA_DIM), _F32)
+        object.__setattr__(self, "layout", StatePoolT(ptr, 4 * stride, t.shape[0], t.shape[1]))
 
 
-def _strided(name: str, t, shape, dtypes):
-    """The address and the row stride of a tensor whose rows are contiguous but may lie apart."""
-    if t.shape != shape or t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {list(shape)} of {dtypes[0]}, got {list(t.shape)} of {t.dtype}")
-    if not t.is_cuda or (t.shape[0] and not t[0].is_contiguous()):
-        raise ValueError(f"{name}: expected a CUDA tensor with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else 1 << 40
-
-
-@dataclass
+@dataclass(frozen=True)
 class DeltaRows:
     """The rows of a gated delta layer: q and k bf16 bits [rows, qk_heads, 128], v [rows, heads, 128], the log decays
-    gate fp32 [rows, heads, 128] (per key channel) or [rows, heads], beta fp32 [rows, heads].  Rows may lie apart."""
+    gate fp32 [rows, heads, 128] (per key channel) or [rows, heads], beta fp32 [rows, heads].  Rows may lie apart.  The
+    tensors' layouts are read once, here; their values at every call."""
 
     q: torch.Tensor
     k: torch.Tensor
@@ -527,38 +529,43 @@ class DeltaRows:
     beta: torch.Tensor
     scale: float
 
+    def __post_init__(self):
+        if self.q.dim() != 3 or self.v.dim() != 3:
+            raise ValueError(f"q and v: expected [rows, heads, {DELTA_DIM}], got {list(self.q.shape)}, {list(self.v.shape)}")
+        rows, heads, qk, wide = self.v.shape[0], self.v.shape[1], self.q.shape[1], self.gate.dim() == 3
+        got = [_rows_of("q", self.q, (rows, qk, DELTA_DIM), _BITS16), _rows_of("k", self.k, (rows, qk, DELTA_DIM), _BITS16),
+               _rows_of("v", self.v, (rows, heads, DELTA_DIM), _BITS16),
+               _rows_of("gate", self.gate, (rows, heads, DELTA_DIM) if wide else (rows, heads), _F32),
+               _rows_of("beta", self.beta, (rows, heads), _F32)]
+        at = {t.get_device() for t in (self.q, self.k, self.v, self.gate, self.beta)}
+        if len(at) != 1:
+            raise ValueError(f"the rows' tensors must be on one device, got {sorted(at)}")
+        object.__setattr__(self, "layout", DeltaRowsT(*(p for p, _ in got), *(ld for _, ld in got), qk,
+                                                      DELTA_DIM if wide else 1, float(self.scale)))
+
     @property
     def rows(self) -> int:
-        return int(self.v.shape[0])
-
-    def struct(self, heads: int) -> DeltaRowsT:
-        rows, qk = self.rows, self.q.shape[1] if self.q.dim() == 3 else 0
-        wide = self.gate.dim() == 3
-        got = [_strided("q", self.q, (rows, qk, DELTA_DIM), _BITS16), _strided("k", self.k, (rows, qk, DELTA_DIM), _BITS16),
-               _strided("v", self.v, (rows, heads, DELTA_DIM), _BITS16),
-               _strided("gate", self.gate, (rows, heads, DELTA_DIM) if wide else (rows, heads), _F32),
-               _strided("beta", self.beta, (rows, heads), _F32)]
-        return DeltaRowsT(*(p for p, _ in got), *(ld for _, ld in got), qk, DELTA_DIM if wide else 1, float(self.scale))
+        return self.v.shape[0]
 
 
 def _delta(pool: StatePool, x: DeltaRows, *others):
-    p = pool.struct()
-    _one_device(pool.states, x.q, x.k, x.v, x.gate, x.beta, *others)
-    return p, x.struct(p.heads)
+    if x.v.shape[1] != pool.layout.heads:
+        raise ValueError(f"rows of {x.v.shape[1]} heads and states of {pool.layout.heads}")
+    _one_device(pool.states, x.v, *others)
+    return ctypes.byref(pool.layout), ctypes.byref(x.layout), (x.v.shape[0], x.v.shape[1], DELTA_DIM)
 
 
 def gated_delta_decode(pool: StatePool, x: DeltaRows, queries_per_seq: int, slots_in, slots_out, out, status,
                        stream=None):
     """The gated delta rule for queries_per_seq rows a sequence: states from slots_in int32 [batch] (-1: zeros), the
     state after each row to slots_out int32 [batch, queries_per_seq] (-1: nowhere); out bf16 bits [rows, heads, 128]."""
-    p, r = _delta(pool, x, slots_in, slots_out, out, status)
+    p, r, shape = _delta(pool, x, slots_in, slots_out, out, status)
     batch, nq = slots_in.shape[0], int(queries_per_seq)
-    if x.rows != batch * nq:
-        raise ValueError(f"{x.rows} rows for {batch} sequences of {nq}")
-    _check(lib().gated_delta_decode(ctypes.byref(p), ctypes.byref(r), batch, nq, _want("slots_in", slots_in, (batch,), _I32),
-                                    _want("slots_out", slots_out, (batch, nq), _I32),
-                                    _want("out", out, (x.rows, p.heads, DELTA_DIM), _BITS16), _status(status),
-                                    _stream(stream)), "gated_delta_decode")
+    if shape[0] != batch * nq:
+        raise ValueError(f"{shape[0]} rows for {batch} sequences of {nq}")
+    _check(lib().gated_delta_decode(p, r, batch, nq, _want("slots_in", slots_in, (batch,), _I32),
+                                    _want("slots_out", slots_out, (batch, nq), _I32), _want("out", out, shape, _BITS16),
+                                    _status(status), _stream(stream)), "gated_delta_decode")
 
 
 def gated_delta_prefill_workspace_size(rows: int, batch: int, heads: int) -> int:
@@ -569,14 +576,13 @@ def gated_delta_prefill(pool: StatePool, x: DeltaRows, row_starts, slots_in, slo
                         stream=None):
     """The gated delta rule over ragged prompts: sequence b has the rows row_starts[b] .. row_starts[b + 1] - 1 (int32
     [batch + 1]); its state comes from slots_in[b] (-1: zeros) and goes to slots_out[b] (-1: nowhere)."""
-    p, r = _delta(pool, x, row_starts, slots_in, slots_out, out, workspace, status)
+    p, r, shape = _delta(pool, x, row_starts, slots_in, slots_out, out, workspace, status)
     batch = slots_in.shape[0]
-    _check(lib().gated_delta_prefill(ctypes.byref(p), ctypes.byref(r),
-                                     _want("row_starts", row_starts, (batch + 1,), _I32), batch, x.rows,
+    _check(lib().gated_delta_prefill(p, r, _want("row_starts", row_starts, (batch + 1,), _I32), batch, shape[0],
                                      _want("slots_in", slots_in, (batch,), _I32),
-                                     _want("slots_out", slots_out, (batch,), _I32),
-                                     _want("out", out, (x.rows, p.heads, DELTA_DIM), _BITS16), _ptr(workspace),
-                                     workspace.nbytes, _status(status), _stream(stream)), "gated_delta_prefill")
+                                     _want("slots_out", slots_out, (batch,), _I32), _want("out", out, shape, _BITS16),
+                                     _ptr(workspace), workspace.nbytes, _status(status), _stream(stream)),
+           "gated_delta_prefill")
 
 
 def quantize_index_query(q_bf16, head_w, q_index, head_w_out, stream=None):

@@ -173,16 +173,93 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
   append_row(a, blockIdx.x, threadIdx.x, warp_amax, [] { __syncthreads(); });
 }
 
-// One CTA per new token row, its slot given: -1 is a padding row.
-__global__ void __launch_bounds__(kAppendThreads) cache_append_slots_kernel(const AppendArgs a, const int32_t* slots) {
-  __shared__ float warp_amax[kAppendThreads / 32];
-  const int s = slots[blockIdx.x];
+// Two values as E4M3 codes, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float bf16_low(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// Eight bf16 over s as eight E4M3 codes.
+__device__ __forceinline__ uint2 e4m3x8(uint4 v, float s) {
+  return make_uint2(e4m3x2(bf16_low(v.x) / s, bf16_high(v.x) / s) | e4m3x2(bf16_low(v.y) / s, bf16_high(v.y) / s) << 16,
+                    e4m3x2(bf16_low(v.z) / s, bf16_high(v.z) / s) | e4m3x2(bf16_low(v.w) / s, bf16_high(v.w) / s) << 16);
+}
+
+// One warp per new token row, its slot given; -1 is a padding row.  append_token's
+// encodings, 16 bytes a load and nothing shared between warps: a row's reads are all
+// on their way before the first is used.  Bound by bytes: 16,385 rows, 34.7 MB.
+constexpr int kSlotWarps = 8;
+template <bool NV, bool KEY8>
+__global__ void __launch_bounds__(32 * kSlotWarps) cache_append_slots_kernel(const AppendArgs a, const int32_t* slots, int rows) {
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kSlotWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int s = __ldg(slots + row);
   if (s == -1) return;
   if (s < 0 || s / kBlock >= a.num_blocks) {
-    if (threadIdx.x == 0) report(a.status, DSA_ERR_BOUNDS);
+    if (lane == 0) report(a.status, DSA_ERR_BOUNDS);
     return;
   }
-  append_token(a, blockIdx.x, s / kBlock, s % kBlock, threadIdx.x, warp_amax, [] { __syncthreads(); });
+  const int slot = s % kBlock;
+  const int64_t block = (int64_t)(s / kBlock) * a.row_stride;
+  const uint4* lat = reinterpret_cast<const uint4*>(a.new_latent + (int64_t)row * kLatent);
+  const uint2 key = __ldg(reinterpret_cast<const uint2*>(a.new_key + (int64_t)row * kIdxDim) + lane);
+  if (!NV) {
+    constexpr int kRest = kLatent / 8 - 64;   // pieces of eight behind two a lane
+    uint2* dst = reinterpret_cast<uint2*>(a.latent_base + block + (int64_t)slot * kLatent);
+    const uint4 v0 = __ldg(lat + lane), v1 = __ldg(lat + 32 + lane);
+    const uint4 v2 = lane < kRest ? __ldg(lat + 64 + lane) : make_uint4(0, 0, 0, 0);
+    dst[lane] = e4m3x8(v0, a.latent_scale);
+    dst[32 + lane] = e4m3x8(v1, a.latent_scale);
+    if (lane < kRest) dst[64 + lane] = e4m3x8(v2, a.latent_scale);
+  } else {
+    // a lane a block of 16 dims
+    constexpr int kRec = kValue / 2 + kValue / 16 + (kLatent - kValue);
+    uint8_t* rec = a.latent_base + block + (int64_t)slot * kRec;
+    const uint4 v0 = __ldg(lat + 2 * lane), v1 = __ldg(lat + 2 * lane + 1);
+    const uint32_t tail = __ldg(reinterpret_cast<const uint32_t*>(a.new_latent + (int64_t)row * kLatent + kValue) + lane);
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_low(w[i])), fabsf(bf16_high(w[i]))));
+    const uint8_t sc = e4m3(amax / (6.0f * a.latent_scale));
+    const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sc, __NV_E4M3);
+    const float sdec = __half2float(*reinterpret_cast<const __half*>(&hr)), step = a.latent_scale * sdec;
+    uint32_t code[2] = {0u, 0u};
+    if (sdec > 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t two = ((uint32_t)__nv_cvt_float_to_fp4(bf16_low(w[i]) / step, __NV_E2M1, cudaRoundNearest) & 0xFu) |
+                             ((uint32_t)__nv_cvt_float_to_fp4(bf16_high(w[i]) / step, __NV_E2M1, cudaRoundNearest) & 0xFu) << 4;
+        code[i >> 2] |= two << (8 * (i & 3));
+      }
+    }
+    reinterpret_cast<uint2*>(rec)[lane] = make_uint2(code[0], code[1]);
+    rec[kValue / 2 + lane] = sc;
+    reinterpret_cast<uint16_t*>(rec + kValue / 2 + kValue / 16)[lane] =
+        (uint16_t)e4m3x2(bf16_low(tail) / a.latent_scale, bf16_high(tail) / a.latent_scale);
+  }
+  // index key: four elements a lane
+  const float x[4] = {bf16_low(key.x), bf16_high(key.x), bf16_low(key.y), bf16_high(key.y)};
+  float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+  uint8_t* page = a.index_base + block;
+  if (KEY8) {
+    amax = warp_max(amax);
+    const float ks = amax > 0.f ? amax / 448.0f : 1.0f;
+    reinterpret_cast<uint32_t*>(page + slot * kIdxDim)[lane] = e4m3x2(x[0] / ks, x[1] / ks) | e4m3x2(x[2] / ks, x[3] / ks) << 16;
+    if (lane == 0) *reinterpret_cast<float*>(page + kBlock * kIdxDim + 4 * slot) = ks;
+  } else {
+    // eight lanes a block of 32
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const uint32_t ebits = (__float_as_uint(amax) >> 23) & 0xFFu;
+    const int e = (amax > 0.f && ebits > 0) ? max(-127, min(127, (int)ebits - 127 - 2)) : -127;
+    uint32_t code = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      code |= ((uint32_t)__nv_cvt_float_to_fp4(ldexpf(x[i], -e), __NV_E2M1, cudaRoundNearest) & 0xFu) << (4 * i);
+    reinterpret_cast<uint16_t*>(page + slot * (kIdxDim / 2))[lane] = (uint16_t)code;
+    if ((lane & 7) == 0) page[kBlock * (kIdxDim / 2) + 4 * slot + lane / 8] = (uint8_t)(e + 127);
+  }
 }
 
 // One warp per (row, head): 128 elements, four per lane.
@@ -568,7 +645,10 @@ dsa_status_t launch_cache_append_slots(const dsa_paged_cache_t& c, const int32_t
   const AppendArgs a{base + c.latent_off, base + c.index_off, c.row_stride, c.num_blocks, c.key_format,
                      c.latent_format, c.latent_scale, nullptr, 0, nullptr, 1, 0, new_latent, new_key, status};
   count_launches(1);
-  cache_append_slots_kernel<<<rows, kAppendThreads, 0, st>>>(a, slots);
+  const bool nv = c.latent_format == DSA_LATENT_NVFP4, key8 = c.key_format == DSA_KEY_FP8_E4M3;
+  const auto kernel = nv ? (key8 ? cache_append_slots_kernel<true, true> : cache_append_slots_kernel<true, false>)
+                         : (key8 ? cache_append_slots_kernel<false, true> : cache_append_slots_kernel<false, false>);
+  kernel<<<(rows + kSlotWarps - 1) / kSlotWarps, 32 * kSlotWarps, 0, st>>>(a, slots, rows);
   return launch_status();
 }
 

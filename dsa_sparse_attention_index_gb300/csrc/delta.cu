@@ -6,8 +6,6 @@
 // so one pass over S~ gives both of its products, and S never leaves registers
 // between the rows of a call.  The rows v of S do not touch each other: a CTA
 // takes some of them, and a warp needs no other one.
-#include <algorithm>
-
 #include "common.cuh"
 #include "delta.cuh"
 #include "internal.h"
@@ -18,39 +16,34 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int R = 4;                                  // value rows a thread has a part of
+constexpr int kCtaRows = 4 * R * kWarps;              // 64: a CTA's value rows
+constexpr int kSplit = kDeltaDim / kCtaRows;
 
-// What a row brings for this thread's keys 4 l + 32 i .. + 3 (l = lane % 8) and its values.
-template <int R>
+// What a row brings for this thread's keys 4 l + 32 i .. + 3 (l = lane % 8) and its
+// values, as loaded: half the registers that the converted numbers would take.
 struct RowData {
-  float4 k[4], q[4], a[4];
-  float v[R];
-  float beta, kq;
+  uint2 k[4], q[4];
+  float4 g[4];   // one decay per head: g[0].x alone
+  uint16_t v[R];
+  float beta;
 };
 
-template <int R>
-__device__ __forceinline__ void load_row(const DeltaRows& x, int64_t row, int hq, int h, int l, int vrow, RowData<R>& d) {
+__device__ __forceinline__ void load_row(const DeltaRows& x, int64_t row, int hq, int h, int l, int vrow, RowData& d) {
   const uint2* kp = reinterpret_cast<const uint2*>(x.k + row * x.ld_k + hq * kDeltaDim) + l;
   const uint2* qp = reinterpret_cast<const uint2*>(x.q + row * x.ld_q + hq * kDeltaDim) + l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    d.k[i] = bf16x4_to_float4(__ldg(kp + 8 * i));
-    d.q[i] = bf16x4_to_float4(__ldg(qp + 8 * i));
-  }
   if (x.gate_dim == 1) {
-    const float a = expf(__ldg(x.gate + row * x.ld_gate + h));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d.a[i] = make_float4(a, a, a, a);
+    d.g[0].x = __ldg(x.gate + row * x.ld_gate + h);
   } else {
     const float4* gp = reinterpret_cast<const float4*>(x.gate + row * x.ld_gate + (int64_t)h * kDeltaDim) + l;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 g = __ldg(gp + 8 * i);
-      d.a[i] = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
-    }
+    for (int i = 0; i < 4; ++i) d.g[i] = __ldg(gp + 8 * i);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d.k[i] = __ldg(kp + 8 * i), d.q[i] = __ldg(qp + 8 * i);
   const uint16_t* vp = x.v + row * x.ld_v + (int64_t)h * kDeltaDim + vrow;
 #pragma unroll
-  for (int r = 0; r < R; ++r) d.v[r] = bf16_to_float(__ldg(vp + 4 * r));
+  for (int r = 0; r < R; ++r) d.v[r] = __ldg(vp + 4 * r);
   d.beta = __ldg(x.beta + row * x.ld_beta + h);
 }
 
@@ -64,15 +57,19 @@ __device__ __forceinline__ float sum8(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 4);
 }
 
-// Grid batch * heads * (128 / (16 R)): a CTA holds 16 R value rows of one
-// head's state, a warp 4 R of them; eight lanes share a row (16 keys each).
-template <int R>
-__global__ void __launch_bounds__(kThreads) delta_rows_kernel(const DeltaRows x, const DeltaSeqs s, uint16_t* out) {
-  constexpr int kSplit = kDeltaDim / (4 * R * kWarps);
+// Grid batch * heads * 2: a CTA holds 64 value rows of one head's state, a warp 16
+// of them; eight lanes share a row (16 keys each), so a product with the keys takes
+// three shuffles.  Bound by the states' bytes: with 64 registers of state a thread
+// and three CTAs an SM, 96 KB are on their way.  32 sequences x 96 heads read and
+// write 0.41 GB in 62.6 us (6.5 TB/s, 0.96 of the measured copy); two CTAs an SM
+// take 72, two rows a thread and five CTAs 67, one row a thread 90.  Few heads are
+// no faster in smaller parts (32 heads: 3.4 us either way).
+__global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows x, const DeltaSeqs s, uint16_t* out) {
   const int part = blockIdx.x % kSplit, bh = blockIdx.x / kSplit;
   const int h = bh % x.heads, b = bh / x.heads, hq = h / (x.heads / x.qk_heads);
   const int lane = threadIdx.x & 31, l = lane & 7;
-  const int vrow = part * (4 * R * kWarps) + (threadIdx.x >> 5) * 4 * R + (lane >> 3);  // this thread's rows: vrow + 4 r
+  const int vrow = part * kCtaRows + (threadIdx.x >> 5) * 4 * R + (lane >> 3);  // this thread's rows: vrow + 4 r
+  const int64_t at = (int64_t)vrow * kDeltaDim + 4 * l;
   int64_t row;
   int n;
   if (!seq_rows(s, b, &row, &n)) return;
@@ -83,69 +80,66 @@ __global__ void __launch_bounds__(kThreads) delta_rows_kernel(const DeltaRows x,
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      S[r][i] = in ? *reinterpret_cast<const float4*>(in + (vrow + 4 * r) * kDeltaDim + 4 * l + 32 * i)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      S[r][i] = in ? *reinterpret_cast<const float4*>(in + at + r * 4 * kDeltaDim + 32 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  auto store = [&](float* to) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(to + at + r * 4 * kDeltaDim + 32 * i) = S[r][i];
+  };
 
-  RowData<R> d;
-  if (n > 0) load_row<R>(x, row, hq, h, l, vrow, d);
+  RowData d;
+  if (n > 0) load_row(x, row, hq, h, l, vrow, d);
   for (int t = 0; t < n; ++t) {
-    RowData<R> next;
-    if (t + 1 < n) load_row<R>(x, row + t + 1, hq, h, l, vrow, next);
     float kq = 0.f, p[R], w[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) kq = dot4(d.k[i], d.q[i], kq);
-    kq = sum8(kq);
+    for (int r = 0; r < R; ++r) p[r] = w[r] = 0.f;
+    const float a1 = x.gate_dim == 1 ? expf(d.g[0].x) : 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      p[r] = w[r] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const float4 k = bf16x4_to_float4(d.k[i]), q = bf16x4_to_float4(d.q[i]);
+      const float4 a = x.gate_dim == 1 ? make_float4(a1, a1, a1, a1)
+                                       : make_float4(expf(d.g[i].x), expf(d.g[i].y), expf(d.g[i].z), expf(d.g[i].w));
+      kq = dot4(k, q, kq);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        S[r][i].x *= d.a[i].x, S[r][i].y *= d.a[i].y, S[r][i].z *= d.a[i].z, S[r][i].w *= d.a[i].w;
-        p[r] = dot4(S[r][i], d.k[i], p[r]);
-        w[r] = dot4(S[r][i], d.q[i], w[r]);
+      for (int r = 0; r < R; ++r) {
+        S[r][i].x *= a.x, S[r][i].y *= a.y, S[r][i].z *= a.z, S[r][i].w *= a.w;
+        p[r] = dot4(S[r][i], k, p[r]);
+        w[r] = dot4(S[r][i], q, w[r]);
       }
     }
+    kq = sum8(kq);
+    float u[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float u = d.beta * (d.v[r] - sum8(p[r]));
-      const float o = x.scale * fmaf(u, kq, sum8(w[r]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        S[r][i].x = fmaf(u, d.k[i].x, S[r][i].x), S[r][i].y = fmaf(u, d.k[i].y, S[r][i].y);
-        S[r][i].z = fmaf(u, d.k[i].z, S[r][i].z), S[r][i].w = fmaf(u, d.k[i].w, S[r][i].w);
-      }
+      u[r] = d.beta * (bf16_to_float(d.v[r]) - sum8(p[r]));
+      const float o = x.scale * fmaf(u[r], kq, sum8(w[r]));
       if (l == r) out[((row + t) * x.heads + h) * kDeltaDim + vrow + 4 * r] = float_to_bf16(o);
     }
-    if (s.per_row || t == n - 1) {
-      if (float* to = state_out(s, b, t, h)) {
+    uint2 kr[4];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+    for (int i = 0; i < 4; ++i) kr[i] = d.k[i];
+    if (t + 1 < n) load_row(x, row + t + 1, hq, h, l, vrow, d);   // on its way while the state is updated and stored
 #pragma unroll
-          for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(to + (vrow + 4 * r) * kDeltaDim + 4 * l + 32 * i) = S[r][i];
+    for (int i = 0; i < 4; ++i) {
+      const float4 k = bf16x4_to_float4(kr[i]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        S[r][i].x = fmaf(u[r], k.x, S[r][i].x), S[r][i].y = fmaf(u[r], k.y, S[r][i].y);
+        S[r][i].z = fmaf(u[r], k.z, S[r][i].z), S[r][i].w = fmaf(u[r], k.w, S[r][i].w);
       }
     }
-    d = next;
+    if (s.per_row || t == n - 1)
+      if (float* to = state_out(s, b, t, h)) store(to);
   }
-  if (n == 0 && !s.per_row) {
-    // a sequence without rows hands its state on
-    if (float* to = state_out(s, b, 0, h)) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(to + (vrow + 4 * r) * kDeltaDim + 4 * l + 32 * i) = S[r][i];
-    }
-  }
+  if (n == 0 && !s.per_row)   // a sequence without rows hands its state on
+    if (float* to = state_out(s, b, 0, h)) store(to);
 }
 
 }  // namespace
 
 dsa_status_t launch_delta_rows(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, cudaStream_t st) {
-  const int64_t heads = (int64_t)s.batch * x.heads;
-  if (heads * 2 >= 2 * num_sms()) {
-    delta_rows_kernel<4><<<(unsigned)(heads * 2), kThreads, 0, st>>>(x, s, out);
-  } else {
-    delta_rows_kernel<1><<<(unsigned)(heads * 8), kThreads, 0, st>>>(x, s, out);
-  }
+  delta_rows_kernel<<<(unsigned)((int64_t)s.batch * x.heads * kSplit), kThreads, 0, st>>>(x, s, out);
   count_launches(1);
   return launch_status();
 }
