@@ -20,10 +20,8 @@ namespace dsa {
 
 namespace {
 
-constexpr int kSlotThreads = 1024;
-constexpr int kPer = 2;                             // requests a thread scans at once
-constexpr int kSlotTile = kSlotThreads * kPer;      // requests of a tile
-constexpr int kSlotRows = 4;                        // rows a thread places at once
+constexpr int kPer = 2;         // requests a thread scans at once
+constexpr int kSlotRows = 4;    // rows a thread places at once: 16 bytes of positions, 16 of slots
 
 struct SlotArgs {
   const int32_t *cached, *fresh;
@@ -52,10 +50,12 @@ __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlock - 
 // in shared memory) and places its share of the rows; nothing that the caller
 // may pass as input and output at once (lengths, the stack's count) is written
 // before the whole cluster has read it.
+template <int kSlotThreads>
 __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotArgs a) {
   namespace cg = cooperative_groups;
+  constexpr int kSlotTile = kSlotThreads * kPer;   // requests of a tile
   __shared__ int s_start[kSlotTile + 1], s_cached[kSlotTile], s_page[kSlotTile];
-  __shared__ long long s_warp[32];
+  __shared__ long long s_warp[32], s_warp2[32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int cta = blockIdx.x, ctas = gridDim.x;
   int count = *a.free_count;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
     if (cta == 0 && tid == 0) report(a.status, DSA_ERR_BOUNDS);
     count = 0;
   }
-  // this CTA's rows: whole groups of 4 rows a thread, in turns over the cluster
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
   long long rows0 = 0, pages0 = 0;  // of the tiles before
   for (int base = 0; base < a.batch; base += kSlotTile) {
     // scan of (rows, pages), rows in the upper half: either sum of a tile stays below 2^42 and 2^36
@@ -87,10 +87,10 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
       const long long r = __shfl_up_sync(0xffffffffu, ri, o), p = __shfl_up_sync(0xffffffffu, pi, o);
       if (lane >= o) ri += r, pi += p;
     }
-    __shared__ long long s_warp2[32];
     if (lane == 31) s_warp[wid] = ri, s_warp2[wid] = pi;
     __syncthreads();
-    long long rt = s_warp[lane], pt = s_warp2[lane];
+    constexpr int kWarps = kSlotThreads / 32;
+    long long rt = lane < kWarps ? s_warp[lane] : 0, pt = lane < kWarps ? s_warp2[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long r = __shfl_up_sync(0xffffffffu, rt, o), p = __shfl_up_sync(0xffffffffu, pt, o);
@@ -115,34 +115,48 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
     // the tile's rows, four at a time, in turns over the cluster's threads
     const int first = s_start[0], last = s_start[kSlotTile];
     const int step = ctas * kSlotThreads * kSlotRows;
-    for (int g = first + (cta * kSlotThreads + tid) * kSlotRows; g < last; g += step) {
-      int lo = 0, hi = kSlotTile;  // the last request with start <= g: start[lo] <= g < start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_start[mid] <= g) lo = mid; else hi = mid;
-      }
+    for (int g = (first & ~(kSlotRows - 1)) + (cta * kSlotThreads + tid) * kSlotRows; g < last; g += step) {
+      const int r0 = max(g, first);
+      int lo = 0;   // the last request with start <= r0
+#pragma unroll
+      for (int w = kSlotTile / 2; w > 0; w >>= 1)
+        if (s_start[lo + w] <= r0) lo += w;
+      int pos[kSlotRows], page[kSlotRows];
+      int32_t* entry[kSlotRows];
 #pragma unroll
       for (int e = 0; e < kSlotRows; ++e) {
         const int row = g + e;
-        if (row >= last) break;
+        pos[e] = -1, page[e] = 0, entry[e] = nullptr;
+        if (row < first || row >= last) continue;
         while (s_start[lo + 1] <= row) ++lo;
-        const int pos = s_cached[lo] + row - s_start[lo], j = pos / kBlock, have = pages_of(s_cached[lo]);
-        const int64_t entry = (int64_t)(base + lo) * a.max_blocks + j;
-        int page;
-        if (j < have) {
-          page = a.table[entry];
-        } else {
-          const long long at = (long long)count - 1 - ((long long)s_page[lo] + j - have);
-          page = at >= 0 ? a.free_blocks[at] : -1;
-        }
-        if (page < 0 || page >= a.num_blocks) {
+        const int cached = s_cached[lo], have = pages_of(cached);
+        pos[e] = cached + row - s_start[lo];
+        const int j = pos[e] / kBlock;
+        int32_t* to = a.table + (int64_t)(base + lo) * a.max_blocks + j;
+        const long long at = (long long)count - 1 - ((long long)s_page[lo] + j - have);
+        const int32_t* from = j < have ? to : a.free_blocks + at;
+        page[e] = j < have || at >= 0 ? *from : -1;
+        if (j >= have && pos[e] % kBlock == 0) entry[e] = to;
+      }
+      int slot[kSlotRows];
+#pragma unroll
+      for (int e = 0; e < kSlotRows; ++e) {
+        slot[e] = -1;
+        if (pos[e] < 0) continue;
+        if ((unsigned)page[e] >= (unsigned)a.num_blocks) {
           report(a.status, DSA_ERR_BOUNDS);
-          page = -1;
-        } else if (j >= have && pos % kBlock == 0) {
-          a.table[entry] = page;
+          continue;
         }
-        a.positions[row] = pos;
-        a.slots[row] = page < 0 ? -1 : page * kBlock + pos % kBlock;
+        slot[e] = page[e] * kBlock + pos[e] % kBlock;
+        if (entry[e]) *entry[e] = page[e];
+      }
+      if (wide && g >= first && g + kSlotRows <= last) {
+        *reinterpret_cast<int4*>(a.positions + g) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(a.slots + g) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kSlotRows; ++e)
+          if (pos[e] >= 0) a.positions[g + e] = pos[e], a.slots[g + e] = slot[e];
       }
     }
     rows0 += rall, pages0 += pall;
@@ -170,17 +184,24 @@ dsa_status_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, in
                                  int32_t* slots, int max_rows, int32_t* status, cudaStream_t st) {
   const SlotArgs a{cached,     fresh,    batch,  free_blocks, free_capacity, free_count, free_left, num_blocks, table,
                    max_blocks, seq_lens, starts, positions,   slots,         max_rows,   status};
-  const int ctas = max_rows > 4 * kSlotThreads * kSlotRows ? 8 : max_rows > kSlotThreads * kSlotRows ? 4 : 1;
+  // one CTA for up to 4,096 rows, so that a decode step's few take no cluster; 16 for many
+  const bool small = max_rows <= 1024 && batch <= 1024;
+  const int ctas = max_rows > 8 * 4096 ? 16 : max_rows > 4096 ? 4 : 1;
+  const auto kernel = small ? assign_slots_kernel<256> : assign_slots_kernel<1024>;
+  if (ctas > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSlotThreads);
+  cfg.blockDim = dim3(small ? 256 : 1024);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, assign_slots_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_status(e);
