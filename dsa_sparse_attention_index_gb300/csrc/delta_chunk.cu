@@ -44,6 +44,7 @@ struct ChunkArgs {
   DeltaSeqs s;
   uint8_t* records;   // [rows / 64 + batch][heads]; chunk c of sequence b is number starts[b] / 64 + b + c
   uint16_t* out;
+  int resident;       // CTAs of the first kernel that run at once
 };
 
 // The power of two that brings a bound below 2^(top + 1).
@@ -63,6 +64,11 @@ __device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return make_float2(a.x
 __device__ __forceinline__ float reciprocal(float x) {   // within one unit in the last place
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {   // within 2^-22
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ f32x2 bf16x2_to_f32x2(uint32_t v) {
@@ -131,9 +137,10 @@ __device__ __forceinline__ uint32_t at256(int r, int c) { return (uint32_t)(r * 
 // of the parts) and queries (two).
 __device__ __forceinline__ void tile_xy(uint32_t sm, int x0, int y0, float (&kk)[4], float (&qk)[4]) {
   const int lane = threadIdx.x & 31;
+  float ll[4], lh[4], hl[4], ql[4];   // sums of their own: six short chains of products instead of two long ones
   const int ar = x0 + (lane & 15), ac = lane >> 4, br = y0 + (lane & 7), bc = (lane >> 3) & 1;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = 0.f;
+  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = ll[i] = lh[i] = hl[i] = ql[i] = 0.f;
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     uint32_t xh[4], xl[4], xq[4], yh[2], yl[2];
@@ -143,20 +150,17 @@ __device__ __forceinline__ void tile_xy(uint32_t sm, int x0, int y0, float (&kk)
     ldsm4(sm + kPX + 2 * kChunk * 256 + a, xq);
     ldsm2(sm + kPY + b, yh);
     ldsm2(sm + kPY + kChunk * 256 + b, yl);
-    mma_16x8x16(kk, xl, yl);
-    mma_16x8x16(kk, xl, yh);
-    mma_16x8x16(kk, xh, yl);
+    mma_16x8x16(ll, xl, yl);
+    mma_16x8x16(lh, xl, yh);
+    mma_16x8x16(hl, xh, yl);
     mma_16x8x16(kk, xh, yh);
-    mma_16x8x16(qk, xq, yl);
+    mma_16x8x16(ql, xq, yl);
     mma_16x8x16(qk, xq, yh);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) kk[i] += (lh[i] + hl[i]) + ll[i], qk[i] += ql[i];
 }
 
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -164,24 +168,26 @@ __device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4]
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // A 16 x 8 tile of sign * L R for fp32 matrices in shared memory: L's 16 rows, K columns; R's K
-// rows, 8 columns.  Each factor as two tf32 (22 bits), three products.
+// rows, 8 columns.  Each factor as two tf32 (the upper 11 bits and what they leave), three products.
 template <int K>
 __device__ __forceinline__ void mul_tile(const float* L, int ldl, const float* R, int ldr, float* out, int ldo, float sign) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  float d[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < K; k += 8) {
     const float l[4] = {L[g * ldl + k + t], L[(g + 8) * ldl + k + t], L[g * ldl + k + t + 4], L[(g + 8) * ldl + k + t + 4]};
     const float r[2] = {R[(k + t) * ldr + g], R[(k + t + 4) * ldr + g]};
     uint32_t lh[4], ll[4], rh[2], rl[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lh[i] = tf32(l[i]), ll[i] = tf32(l[i] - __uint_as_float(lh[i]));
+    for (int i = 0; i < 4; ++i) lh[i] = __float_as_uint(l[i]) & 0xFFFFE000u, ll[i] = __float_as_uint(l[i] - __uint_as_float(lh[i]));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) rh[i] = tf32(r[i]), rl[i] = tf32(r[i] - __uint_as_float(rh[i]));
-    mma_16x8x8(d, ll, rh);
-    mma_16x8x8(d, lh, rl);
+    for (int i = 0; i < 2; ++i) rh[i] = __float_as_uint(r[i]) & 0xFFFFE000u, rl[i] = __float_as_uint(r[i] - __uint_as_float(rh[i]));
+    mma_16x8x8(d2, ll, rh);
+    mma_16x8x8(d1, lh, rl);
     mma_16x8x8(d, lh, rh);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] += d1[i] + d2[i];
   out[g * ldo + 2 * t] = sign * d[0], out[g * ldo + 2 * t + 1] = sign * d[1];
   out[(g + 8) * ldo + 2 * t] = sign * d[2], out[(g + 8) * ldo + 2 * t + 1] = sign * d[3];
 }
@@ -190,27 +196,32 @@ __device__ __forceinline__ float max_warp(float v) {  // of values >= 0
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const ChunkArgs p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const uint32_t sm = smem_u32(smem);
-  const DeltaRows& x = p.x;
-  const int slot = blockIdx.x / x.heads, h = blockIdx.x % x.heads, hq = h / (x.heads / x.qk_heads);
-  const int tid = threadIdx.x, lane = tid & 31, warp = warp_number();
-
-  // the sequence whose chunk this is: the last b with starts[b] / 64 + b <= slot
+// First row and number of rows of record number `slot`'s chunk: of the last sequence b with starts[b] / 64 + b <= slot.
+__device__ __forceinline__ bool chunk_rows(const ChunkArgs& p, int slot, int64_t* row0, int* n) {
   int seq = 0, end = p.s.batch;
   while (end - seq > 1) {
     const int mid = (seq + end) >> 1;
     if (p.s.starts[mid] / kChunk + mid <= slot) seq = mid; else end = mid;
   }
+  if (!seq_rows(p.s, seq, row0, n)) return false;
+  const int c = slot - (int)(*row0 / kChunk + seq);
+  if (c < 0 || c * kChunk >= *n) return false;
+  *row0 += c * kChunk;
+  *n = min(*n - c * kChunk, kChunk);
+  return true;
+}
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+__global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const ChunkArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sm = smem_u32(smem);
+  const DeltaRows& x = p.x;
+  const int h = blockIdx.x % x.heads, hq = h / (x.heads / x.qk_heads);
+  const int tid = threadIdx.x, lane = tid & 31, warp = warp_number();
   int64_t row0;
-  int n;
-  if (!seq_rows(p.s, seq, &row0, &n)) return;
-  const int c = slot - (int)(row0 / kChunk + seq);
-  if (c < 0 || c * kChunk >= n) return;
-  row0 += c * kChunk;
-  n = min(n - c * kChunk, kChunk);
+  int n = 0;
+  if (!chunk_rows(p, blockIdx.x / x.heads, &row0, &n)) return;
   uint8_t* rec = p.records + (int64_t)blockIdx.x * kRecBytes;
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
@@ -226,22 +237,47 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   {
     const uint16_t* kp = x.k + (row0 + 16 * I) * x.ld_k + hq * kDeltaDim + 2 * q2;
     const uint16_t* qp = x.q + (row0 + 16 * I) * x.ld_q + hq * kDeltaDim + 2 * q2;
-    const float* gp = x.gate + (row0 + 16 * I) * x.ld_gate + (int64_t)h * x.gate_dim + (x.gate_dim == 1 ? 0 : 2 * q2);
+    const bool wide = x.gate_dim != 1;
+    const float* gp = x.gate + (row0 + 16 * I) * x.ld_gate + (int64_t)h * x.gate_dim + (wide ? 2 * q2 : 0);
+    const int left = n - 16 * I;   // rows of the block that are there
+    if (left >= 16) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      kr[t] = qr[t] = 0u;
-      float gx = 0.f, gy = 0.f;
-      if (16 * I + t < n) {
-        kr[t] = __ldg(reinterpret_cast<const uint32_t*>(kp + t * x.ld_k));
-        qr[t] = __ldg(reinterpret_cast<const uint32_t*>(qp + t * x.ld_q));
-        if (x.gate_dim == 1) {
-          gx = gy = __ldg(gp + t * x.ld_gate);
-        } else {
-          const float2 g = __ldg(reinterpret_cast<const float2*>(gp + t * x.ld_gate));
-          gx = g.x, gy = g.y;
+      for (int t = 0; t < 16; ++t, kp += x.ld_k, qp += x.ld_q) {
+        kr[t] = __ldg(reinterpret_cast<const uint32_t*>(kp));
+        qr[t] = __ldg(reinterpret_cast<const uint32_t*>(qp));
+      }
+      if (wide) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t, gp += x.ld_gate) a[t] = __ldg(reinterpret_cast<const float2*>(gp));
+      } else {
+#pragma unroll
+        for (int t = 0; t < 16; ++t, gp += x.ld_gate) a[t].x = a[t].y = __ldg(gp);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        kr[t] = qr[t] = 0u;
+        a[t] = make_float2(0.f, 0.f);
+        if (t < left) {
+          kr[t] = __ldg(reinterpret_cast<const uint32_t*>(kp + t * x.ld_k));
+          qr[t] = __ldg(reinterpret_cast<const uint32_t*>(qp + t * x.ld_q));
+          a[t].x = __ldg(gp + t * x.ld_gate);
+          a[t].y = wide ? __ldg(gp + t * x.ld_gate + 1) : a[t].x;
         }
       }
-      a[t] = pack2(gx, gy);
+    }
+  }
+  {
+    // the inputs of the chunk that will take this CTA's place, towards L2: four threads a row
+    const int64_t next = (int64_t)blockIdx.x + p.resident;
+    int64_t row1;
+    int n1 = 0;
+    if (next < gridDim.x && chunk_rows(p, (int)(next / x.heads), &row1, &n1) && (tid >> 2) < n1) {
+      const int h1 = (int)(next % x.heads), part = tid & 3;
+      const int64_t r = row1 + (tid >> 2);
+      const uint16_t* kq = (part & 1) ? x.q + r * x.ld_q : x.k + r * x.ld_k;
+      prefetch_line(kq + h1 / (x.heads / x.qk_heads) * kDeltaDim + 64 * (part >> 1));
+      if (x.gate_dim != 1) prefetch_line(x.gate + r * x.ld_gate + (int64_t)h1 * kDeltaDim + 32 * part);
     }
   }
   if (tid < kChunk) {
@@ -255,18 +291,17 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   uint32_t km = 0, qm = 0;
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
-    const float2 g = a[t];
-    const float ex = expf(g.x), ey = expf(g.y);
-    a[t] = pack2(ex, ey);
+    a[t].x = exp2_approx(a[t].x * 1.44269504088896341f), a[t].y = exp2_approx(a[t].y * 1.44269504088896341f);
     block = mul2(block, a[t]);
-    const float m = fmaxf(ex, ey);
-    bad |= g.x != g.x || g.y != g.y;   // (a maximum drops a NaN)
-    amax = fmaxf(amax, m);
-    grow *= fmaxf(1.f, m);
+    amax = fmaxf(amax, fmaxf(a[t].x, a[t].y));
     km = __vmaxu2(km, kr[t] & 0x7FFF7FFFu), qm = __vmaxu2(qm, qr[t] & 0x7FFF7FFFu);
   }
-  bad |= !(amax <= 3.4e38f);
+  if (amax > 1.f) {
+#pragma unroll
+    for (int t = 0; t < 16; ++t) grow *= fmaxf(1.f, fmaxf(a[t].x, a[t].y));
+  }
   const float Bx = block.x, By = block.y;
+  bad |= !(amax <= 3.4e38f) || !(Bx <= 3.4e38f) || !(By <= 3.4e38f);   // a decay that is no number makes its product none
   tab[I * kDeltaDim + 2 * q2] = Bx, tab[I * kDeltaDim + 2 * q2 + 1] = By;
   {
     const float k1 = __uint_as_float(max(km & 0xFFFFu, km >> 16) << 16), q1 = __uint_as_float(max(qm & 0xFFFFu, qm >> 16) << 16);
@@ -439,23 +474,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     tile_xy(sm, 48, 8 * warp, kk, qk);
     put_tile(48, 8 * warp, kk, qk);
   }
-  __syncthreads();
-  if (I < 2) put_y(16 * I, I == 0 ? mul2(uncentre(2), block_of(1)) : uncentre(2));   // for rows 32..47
-  if (I == 0) put_y(32, uncentre(1));
-  __syncthreads();
-  if (warp < 6) {
-    float kk[4], qk[4];
-    const int x0 = warp < 4 ? 32 : 16, y0 = warp < 4 ? 8 * warp : 32 + 8 * (warp - 4), j0 = warp < 4 ? y0 : y0 - 32;
-    tile_xy(sm, x0, y0, kk, qk);
-    put_tile(x0, j0, kk, qk);
-  }
-  __syncthreads();
-
-  // ---- (I + A)^-1, in A's place: the diagonal blocks by substitution, a thread a
-  // column; then twice [[T1, 0], [-T2 A21 T1, T2]], of 16 and of 32 rows
-  if (tid < kChunk) {
+  // meanwhile the inverses of I + A's diagonal blocks, in their place, by substitution: a thread a column
+  if (warp >= 6) {
     const int j = tid & 15;
-    float* D = A + (tid & 48) * (kLdA + 1);
+    float* D = A + (tid & 48) * (kLdA + 1);   // (threads 192..255)
     float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -475,6 +497,18 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     for (int i = 0; i < 16; ++i) D[i * kLdA + j] = t[i];
   }
   __syncthreads();
+  if (I < 2) put_y(16 * I, I == 0 ? mul2(uncentre(2), block_of(1)) : uncentre(2));   // for rows 32..47
+  if (I == 0) put_y(32, uncentre(1));
+  __syncthreads();
+  if (warp < 6) {
+    float kk[4], qk[4];
+    const int x0 = warp < 4 ? 32 : 16, y0 = warp < 4 ? 8 * warp : 32 + 8 * (warp - 4), j0 = warp < 4 ? y0 : y0 - 32;
+    tile_xy(sm, x0, y0, kk, qk);
+    put_tile(x0, j0, kk, qk);
+  }
+  __syncthreads();
+
+  // ---- (I + A)^-1, in A's place: from its diagonal blocks twice [[T1, 0], [-T2 A21 T1, T2]], of 16 and of 32 rows
   float* tmp = reinterpret_cast<float*>(smem + kPX);   // [32][36]
   constexpr int kLdT = 36;
   if (warp < 4) {
@@ -1082,7 +1116,7 @@ dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& s, uint16_
     if (e != cudaSuccess) return cuda_status(e);
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  const ChunkArgs a{x, s, static_cast<uint8_t*>(workspace), out};
+  const ChunkArgs a{x, s, static_cast<uint8_t*>(workspace), out, 2 * num_sms()};
   const int64_t records = ((int64_t)s.rows / kChunk + s.batch) * x.heads;
   if (s.rows > 0) {
     delta_prepare_kernel<<<(unsigned)records, kPrepThreads, kPrepSmem + 1024, st>>>(a);
