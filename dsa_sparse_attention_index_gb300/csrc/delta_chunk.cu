@@ -269,11 +269,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   }
   {
     // the inputs of the chunk that will take this CTA's place, towards L2: four threads a row
-    const int64_t next = (int64_t)blockIdx.x + p.resident;
+    const uint32_t next = blockIdx.x + (uint32_t)p.resident;
     int64_t row1;
     int n1 = 0;
-    if (next < gridDim.x && chunk_rows(p, (int)(next / x.heads), &row1, &n1) && (tid >> 2) < n1) {
-      const int h1 = (int)(next % x.heads), part = tid & 3;
+    if (next < gridDim.x && chunk_rows(p, (int)(next / (uint32_t)x.heads), &row1, &n1) && (tid >> 2) < n1) {
+      const int h1 = (int)(next % (uint32_t)x.heads), part = tid & 3;
       const int64_t r = row1 + (tid >> 2);
       const uint16_t* kq = (part & 1) ? x.q + r * x.ld_q : x.k + r * x.ld_k;
       prefetch_line(kq + h1 / (x.heads / x.qk_heads) * kDeltaDim + 64 * (part >> 1));
