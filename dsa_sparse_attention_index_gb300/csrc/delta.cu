@@ -72,7 +72,9 @@ __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows
   const int64_t at = (int64_t)vrow * kDeltaDim + 4 * l;
   int64_t row;
   int n;
+  grid_dep_launch();   // the kernel behind this one in a prompt call touches other sequences
   if (!seq_rows(s, b, &row, &n)) return;
+  if (s.starts && n > kFewRows) return;
 
   float4 S[R][4];
   const float* in = state_in(s, b, h);

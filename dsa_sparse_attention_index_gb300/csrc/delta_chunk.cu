@@ -203,7 +203,7 @@ __device__ __forceinline__ bool chunk_rows(const ChunkArgs& p, int slot, int64_t
     const int mid = (seq + end) >> 1;
     if (p.s.starts[mid] / kChunk + mid <= slot) seq = mid; else end = mid;
   }
-  if (!seq_rows(p.s, seq, row0, n)) return false;
+  if (!seq_rows(p.s, seq, row0, n) || *n <= kFewRows) return false;
   const int c = slot - (int)(*row0 / kChunk + seq);
   if (c < 0 || c * kChunk >= *n) return false;
   *row0 += c * kChunk;
@@ -221,7 +221,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   const int tid = threadIdx.x, lane = tid & 31, warp = warp_number();
   int64_t row0;
   int n = 0;
-  if (!chunk_rows(p, blockIdx.x / x.heads, &row0, &n)) return;
+  grid_dep_launch();   // the chain's first steps need nothing of this
+  if (!chunk_rows(p, blockIdx.x / x.heads, &row0, &n)) {
+    grid_dep_wait();
+    return;
+  }
   uint8_t* rec = p.records + (int64_t)blockIdx.x * kRecBytes;
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
@@ -572,6 +576,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   }
   const int any = __syncthreads_or(bad);
   if (tid == 0) reinterpret_cast<int*>(rec + kRecHead)[kHdBad] = any;
+  grid_dep_wait();   // what runs behind the chain runs behind the kernel before this one too
 }
 
 // ---------------------------------------------------------------- chain
@@ -585,7 +590,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 //   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
 // The parts of a row of S, R or U are times a power of two from a bound of it, so
 // that they keep 22 bits of its largest element whatever its size.
-constexpr int kChainThreads = 11 * 32;
+constexpr int kChainThreads = 12 * 32;   // three warpgroups: two of state warps, one of the rest (its last warp has no work)
+// Of the block's 384 x 168 registers the state warps take 200 a thread and leave 104 to the others: with 168 they spill.
+constexpr int kHelperRegs = 104, kStateRegs = 200;
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kStoreWarp = 10;
 constexpr int kColS = 0;       // keys 64 h ..: high parts in columns 64 h .. + 31, low parts behind them
 constexpr int kColAcc = 128;   // R, then U
@@ -634,7 +641,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
   const int warp = warp_number(), lane = threadIdx.x & 31;
   int64_t row0;
   int n;
-  if (!seq_rows(p.s, b, &row0, &n)) return;
+  if (!seq_rows(p.s, b, &row0, &n) || n <= kFewRows) {
+    grid_dep_wait();
+    return;
+  }
   const int chunks = (n + kChunk - 1) / kChunk;
   const uint8_t* rec = p.records + ((row0 / kChunk + b) * x.heads + h) * kRecBytes;
   const int64_t rec_step = (int64_t)x.heads * kRecBytes;
@@ -672,149 +682,155 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp == kCopyWarp) {
-    // the values one chunk further ahead than the operands: they are looked at during the chunk before theirs
-    bool ok = true;
-    int issued_v = 0, issued = 0, issued2 = 0;
-    auto copy_v = [&](int c) {
-      const int s = c & 1, rows = min(kChunk, n - c * kChunk);
-      if (c >= 2 && !mbar_wait_warp(empty_v(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status)) return false;
-      if (elect_one()) mbar_arrive_expect_tx(full_v(s), rows * kRowBytes);
-      __syncwarp();
-      for (int t = lane; t < rows; t += 32)
-        bulk_load(sm + kCOffV + (s * kChunk + t) * kRowBytes, x.v + (row0 + c * kChunk + t) * x.ld_v + (int64_t)h * kDeltaDim,
-                  kRowBytes, full_v(s));
-      __syncwarp();
-      ++issued_v;
-      return true;
-    };
-    if (chunks > 0) ok = copy_v(0);
-    for (int c = 0; c < chunks && ok; ++c) {
-      const int s = c & 1;
-      const uint8_t* src = rec + c * rec_step;
-      if (c >= 2) ok = mbar_wait_warp(empty(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status);
-      if (!ok) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full(s), kPart1 + kHeadBytes);
-        for (int i = 0; i < 4; ++i) bulk_load(sm + s * kPart1 + i * (kPart1 / 4), src + i * (kPart1 / 4), kPart1 / 4, full(s));
-        bulk_load(sm + kCOffHead + s * 640, src + kRecHead, kHeadBytes, full(s));
-      }
-      __syncwarp();
-      ++issued;
-      if (c + 1 < chunks) ok = copy_v(c + 1);
-      if (ok && c >= 1) ok = mbar_wait_warp(empty2, (c - 1) & 1, abort_flag, p.s.status);
-      if (!ok) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full2, kPart2);
-        for (int i = 0; i < 2; ++i) bulk_load(sm + kCOffPart2 + i * (kPart2 / 2), src + kRecB + i * (kPart2 / 2), kPart2 / 2, full2);
-      }
-      __syncwarp();
-      ++issued2;
-    }
-    // no copy is in flight at the exit, also after another role gave up
-    for (int c = max(0, issued_v - 2); c < issued_v; ++c) mbar_wait_drain(full_v(c & 1), (c >> 1) & 1, 10000000ull);
-    for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait_drain(full(c & 1), (c >> 1) & 1, 10000000ull);
-    if (issued2 > 0) mbar_wait_drain(full2, (issued2 - 1) & 1, 10000000ull);
-  } else if (warp == kStoreWarp) {
-    for (uint32_t j = 0;; ++j) {
-      if (!mbar_wait_warp(out_full, j & 1, abort_flag, p.s.status)) break;
-      const int c = __shfl_sync(0xffffffffu, out_job[0], 0), rows = __shfl_sync(0xffffffffu, out_job[1], 0);
-      if (rows == 0) break;
-      // two rows at a time, 16 bytes a lane (bulk copies would stand in line behind the next operands')
-      const uint4* src = reinterpret_cast<const uint4*>(smem + kCOffOut) + lane;
-      uint16_t* dst = p.out + ((row0 + c * kChunk + (lane >> 4)) * x.heads + h) * kDeltaDim + 8 * (lane & 15);
-#pragma unroll 8
-      for (int t = 0; t < rows; t += 2)
-        if (t + (lane >> 4) < rows) *reinterpret_cast<uint4*>(dst + (int64_t)t * x.heads * kDeltaDim) = src[16 * t];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(out_free);
-    }
-  } else if (warp == kMmaWarp) {
-    constexpr uint32_t kIdesc64 = make_idesc(kFmtF16, kFmtF16, 0, 0, 128, kChunk);
-    constexpr uint32_t kIdescDs = make_idesc(kFmtF16, kFmtF16, 0, 1, 128, kDeltaDim);
-    const uint64_t kdesc = smem_desc(sm, 16, 1024, kLayoutSw128);                  // K-major tiles
-    const uint64_t bdesc = smem_desc(sm + kCOffPart2, 16, 1024, kLayoutSw128);     // B
-    const uint64_t ndesc = smem_desc(sm + kCOffPart2 + kTileHalf, kTileHalf, 1024, kLayoutSw128);  // K D: 64 keys a block
-    const uint32_t k_hi = (uint32_t)(kdesc >> 32), n_hi = (uint32_t)(ndesc >> 32);
-    uint32_t f = 0;   // chunks that took the tensor core
-    for (int c = 0; c < chunks; ++c) {
-      const int s = c & 1;
-      const uint32_t k0 = (uint32_t)kdesc + s * (kPart1 / 16), b0 = (uint32_t)bdesc, n0 = (uint32_t)ndesc;
-      if (!mbar_wait_warp(full(s), (c >> 1) & 1, abort_flag, p.s.status)) break;
-      if (!mbar_wait_warp(b_s, c & 1, abort_flag, p.s.status)) break;
-      tc_fence_after();
-      auto product_s = [&](uint32_t d, int part, int tile, bool more) {   // A: the state's part, 128 keys
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_tmem_a(tmem + d, tmem + kColS + 64 * (ks >> 2) + 32 * part + 8 * (ks & 3),
-                          desc64(k0 + (tile + (ks >> 2) * kTileHalf) / 16 + 2 * (ks & 3), k_hi), kIdesc64, more || ks ? 1u : 0u);
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHelperRegs));
+    if (warp == kCopyWarp) {
+      // the values one chunk further ahead than the operands: they are looked at during the chunk before theirs
+      bool ok = true;
+      int issued_v = 0, issued = 0, issued2 = 0;
+      auto copy_v = [&](int c) {
+        const int s = c & 1, rows = min(kChunk, n - c * kChunk);
+        if (c >= 2 && !mbar_wait_warp(empty_v(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status)) return false;
+        if (elect_one()) mbar_arrive_expect_tx(full_v(s), rows * kRowBytes);
+        __syncwarp();
+        for (int t = lane; t < rows; t += 32)
+          bulk_load(sm + kCOffV + (s * kChunk + t) * kRowBytes, x.v + (row0 + c * kChunk + t) * x.ld_v + (int64_t)h * kDeltaDim,
+                    kRowBytes, full_v(s));
+        __syncwarp();
+        ++issued_v;
+        return true;
       };
-      auto product_t = [&](uint32_t d, int part, uint32_t tile, bool more) {   // A: R's or U's part, 64 rows
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_tmem_a(tmem + d, tmem + kColParts + 32 * part + 8 * ks, desc64(tile + 2 * ks, k_hi), kIdesc64,
-                          more || ks ? 1u : 0u);
-      };
-      if (elect_one()) {
-        product_s(kColAcc, 1, kRecKp, false);
-        product_s(kColAcc, 0, kRecKp + kTileBytes, true);
-        product_s(kColAcc, 0, kRecKp, true);
-        mma_commit(b_r);
-      }
-      __syncwarp();
-      if (!mbar_wait_warp(b_rp, c & 1, abort_flag, p.s.status)) break;
-      if (__any_sync(0xffffffffu, by_rows[s] != 0)) {
-        // nothing of this chunk comes from the tensor core: its buffers go back
-        if (!mbar_wait_warp(full2, c & 1, abort_flag, p.s.status)) break;
+      ok = copy_v(0);
+      grid_dep_wait();   // the records
+      for (int c = 0; c < chunks && ok; ++c) {
+        const int s = c & 1;
+        const uint8_t* src = rec + c * rec_step;
+        if (c >= 2) ok = mbar_wait_warp(empty(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status);
+        if (!ok) break;
         if (elect_one()) {
-          mbar_arrive(empty(s));
-          mbar_arrive(empty2);
+          mbar_arrive_expect_tx(full(s), kPart1 + kHeadBytes);
+          for (int i = 0; i < 4; ++i) bulk_load(sm + s * kPart1 + i * (kPart1 / 4), src + i * (kPart1 / 4), kPart1 / 4, full(s));
+          bulk_load(sm + kCOffHead + s * 640, src + kRecHead, kHeadBytes, full(s));
         }
         __syncwarp();
-        continue;
+        ++issued;
+        if (c + 1 < chunks) ok = copy_v(c + 1);
+        if (ok && c >= 1) ok = mbar_wait_warp(empty2, (c - 1) & 1, abort_flag, p.s.status);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full2, kPart2);
+          for (int i = 0; i < 2; ++i) bulk_load(sm + kCOffPart2 + i * (kPart2 / 2), src + kRecB + i * (kPart2 / 2), kPart2 / 2, full2);
+        }
+        __syncwarp();
+        ++issued2;
       }
-      tc_fence_after();
-      if (elect_one()) {
-        product_t(kColAcc, 1, k0 + kRecT / 16, false);
-        product_t(kColAcc, 0, k0 + (kRecT + kTileHalf) / 16, true);
-        product_t(kColAcc, 0, k0 + kRecT / 16, true);
-        mma_commit(b_u);
+      // no copy is in flight at the exit, also after another role gave up
+      for (int c = max(0, issued_v - 2); c < issued_v; ++c) mbar_wait_drain(full_v(c & 1), (c >> 1) & 1, 10000000ull);
+      for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait_drain(full(c & 1), (c >> 1) & 1, 10000000ull);
+      if (issued2 > 0) mbar_wait_drain(full2, (issued2 - 1) & 1, 10000000ull);
+    } else if (warp == kStoreWarp) {
+      for (uint32_t j = 0;; ++j) {
+        if (!mbar_wait_warp(out_full, j & 1, abort_flag, p.s.status)) break;
+        const int c = __shfl_sync(0xffffffffu, out_job[0], 0), rows = __shfl_sync(0xffffffffu, out_job[1], 0);
+        if (rows == 0) break;
+        // two rows at a time, 16 bytes a lane (bulk copies would stand in line behind the next operands')
+        const uint4* src = reinterpret_cast<const uint4*>(smem + kCOffOut) + lane;
+        uint16_t* dst = p.out + ((row0 + c * kChunk + (lane >> 4)) * x.heads + h) * kDeltaDim + 8 * (lane & 15);
+#pragma unroll 8
+        for (int t = 0; t < rows; t += 2)
+          if (t + (lane >> 4) < rows) *reinterpret_cast<uint4*>(dst + (int64_t)t * x.heads * kDeltaDim) = src[16 * t];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(out_free);
       }
-      __syncwarp();
-      if (!mbar_wait_warp(full2, c & 1, abort_flag, p.s.status)) break;
-      if (!mbar_wait_warp(b_up, f & 1, abort_flag, p.s.status)) break;
-      tc_fence_after();
-      if (elect_one()) {
+    } else if (warp == kMmaWarp) {
+      constexpr uint32_t kIdesc64 = make_idesc(kFmtF16, kFmtF16, 0, 0, 128, kChunk);
+      constexpr uint32_t kIdescDs = make_idesc(kFmtF16, kFmtF16, 0, 1, 128, kDeltaDim);
+      const uint64_t kdesc = smem_desc(sm, 16, 1024, kLayoutSw128);                  // K-major tiles
+      const uint64_t bdesc = smem_desc(sm + kCOffPart2, 16, 1024, kLayoutSw128);     // B
+      const uint64_t ndesc = smem_desc(sm + kCOffPart2 + kTileHalf, kTileHalf, 1024, kLayoutSw128);  // K D: 64 keys a block
+      const uint32_t k_hi = (uint32_t)(kdesc >> 32), n_hi = (uint32_t)(ndesc >> 32);
+      uint32_t f = 0;   // chunks that took the tensor core
+      for (int c = 0; c < chunks; ++c) {
+        const int s = c & 1;
+        const uint32_t k0 = (uint32_t)kdesc + s * (kPart1 / 16), b0 = (uint32_t)bdesc, n0 = (uint32_t)ndesc;
+        if (!mbar_wait_warp(full(s), (c >> 1) & 1, abort_flag, p.s.status)) break;
+        if (!mbar_wait_warp(b_s, c & 1, abort_flag, p.s.status)) break;
+        tc_fence_after();
+        auto product_s = [&](uint32_t d, int part, int tile, bool more) {   // A: the state's part, 128 keys
 #pragma unroll
-        for (int q = 0; q < 3; ++q)   // low x high, high x low, high x high
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_tmem_a(tmem + d, tmem + kColS + 64 * (ks >> 2) + 32 * part + 8 * (ks & 3),
+                            desc64(k0 + (tile + (ks >> 2) * kTileHalf) / 16 + 2 * (ks & 3), k_hi), kIdesc64, more || ks ? 1u : 0u);
+        };
+        auto product_t = [&](uint32_t d, int part, uint32_t tile, bool more) {   // A: R's or U's part, 64 rows
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_tmem_a(tmem + kColDs, tmem + kColParts + (q == 0 ? 32 : 0) + 8 * ks,
-                            desc64(n0 + (q == 1 ? kTileBytes / 16 : 0) + ks * (16 * 128 / 16), n_hi), kIdescDs, q | ks ? 1u : 0u);
-        mma_commit(b_ds);
+            mma_bf16_tmem_a(tmem + d, tmem + kColParts + 32 * part + 8 * ks, desc64(tile + 2 * ks, k_hi), kIdesc64,
+                            more || ks ? 1u : 0u);
+        };
+        if (elect_one()) {
+          product_s(kColAcc, 1, kRecKp, false);
+          product_s(kColAcc, 0, kRecKp + kTileBytes, true);
+          product_s(kColAcc, 0, kRecKp, true);
+          mma_commit(b_r);
+        }
+        __syncwarp();
+        if (!mbar_wait_warp(b_rp, c & 1, abort_flag, p.s.status)) break;
+        if (__any_sync(0xffffffffu, by_rows[s] != 0)) {
+          // nothing of this chunk comes from the tensor core: its buffers go back
+          if (!mbar_wait_warp(full2, c & 1, abort_flag, p.s.status)) break;
+          if (elect_one()) {
+            mbar_arrive(empty(s));
+            mbar_arrive(empty2);
+          }
+          __syncwarp();
+          continue;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          product_t(kColAcc, 1, k0 + kRecT / 16, false);
+          product_t(kColAcc, 0, k0 + (kRecT + kTileHalf) / 16, true);
+          product_t(kColAcc, 0, k0 + kRecT / 16, true);
+          mma_commit(b_u);
+        }
+        __syncwarp();
+        if (!mbar_wait_warp(full2, c & 1, abort_flag, p.s.status)) break;
+        if (!mbar_wait_warp(b_up, f & 1, abort_flag, p.s.status)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int q = 0; q < 3; ++q)   // low x high, high x low, high x high
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_tmem_a(tmem + kColDs, tmem + kColParts + (q == 0 ? 32 : 0) + 8 * ks,
+                              desc64(n0 + (q == 1 ? kTileBytes / 16 : 0) + ks * (16 * 128 / 16), n_hi), kIdescDs, q | ks ? 1u : 0u);
+          mma_commit(b_ds);
+        }
+        __syncwarp();
+        // the outputs' products run while the state is updated
+        if (f > 0 && !mbar_wait_warp(b_of, (f - 1) & 1, abort_flag, p.s.status)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          product_s(kColO1, 0, kRecQp, false);
+          product_t(kColO2, 0, b0, false);
+          mma_commit(b_o);
+          mma_commit(empty(s));
+          mma_commit(empty2);
+        }
+        __syncwarp();
+        ++f;
       }
-      __syncwarp();
-      // the outputs' products run while the state is updated
-      if (f > 0 && !mbar_wait_warp(b_of, (f - 1) & 1, abort_flag, p.s.status)) break;
-      tc_fence_after();
+      // every MMA completes before TMEM is released
       if (elect_one()) {
-        product_s(kColO1, 0, kRecQp, false);
-        product_t(kColO2, 0, b0, false);
-        mma_commit(b_o);
-        mma_commit(empty(s));
-        mma_commit(empty2);
+        mma_commit(drain);
+        mbar_wait_drain(drain, 0, 10000000ull);
       }
       __syncwarp();
-      ++f;
     }
-    // every MMA completes before TMEM is released
-    if (elect_one()) {
-      mma_commit(drain);
-      mbar_wait_drain(drain, 0, 10000000ull);
-    }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
     // ------------------------------------------------ state warps
+    grid_dep_wait();
     // A wait that gave up leaves the loop running without waits (they return at
     // once then): the warps meet at named barriers and none may be missing there.
     const int half = warp >> 2, v = 32 * (warp & 3) + lane, tid = threadIdx.x;
@@ -1113,17 +1129,34 @@ dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& s, uint16_
     cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem + 1024);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainSmem);
+    cudaFuncAttributes at = {};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, delta_chain_kernel);
     if (e != cudaSuccess) return cuda_status(e);
+    // the state warps would wait for registers that the block does not have
+    if (at.numRegs * kChainThreads < 128 * kHelperRegs + 256 * kStateRegs) return DSA_ERR_UNSUPPORTED;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
+  const dsa_status_t first = launch_delta_rows(x, s, out, st);
+  if (first != DSA_OK || s.rows <= kFewRows) return first;
   const ChunkArgs a{x, s, static_cast<uint8_t*>(workspace), out, 2 * num_sms()};
   const int64_t records = ((int64_t)s.rows / kChunk + s.batch) * x.heads;
-  if (s.rows > 0) {
-    delta_prepare_kernel<<<(unsigned)records, kPrepThreads, kPrepSmem + 1024, st>>>(a);
-    count_launches(1);
-  }
-  delta_chain_kernel<<<(unsigned)(s.batch * x.heads), kChainThreads, kChainSmem, st>>>(a);
-  count_launches(1);
+  // each may start while the one before it still runs
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)records);
+  cfg.blockDim = dim3(kPrepThreads);
+  cfg.dynamicSmemBytes = kPrepSmem + 1024;
+  count_launches(2);
+  if (cuda_status(cudaLaunchKernelEx(&cfg, delta_prepare_kernel, a)) != DSA_OK) return DSA_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)(s.batch * x.heads));
+  cfg.blockDim = dim3(kChainThreads);
+  cfg.dynamicSmemBytes = kChainSmem;
+  if (cuda_status(cudaLaunchKernelEx(&cfg, delta_chain_kernel, a)) != DSA_OK) return DSA_ERR_CUDA;
   return launch_status();
 }
 
