@@ -57,7 +57,35 @@ __device__ __forceinline__ float sum8(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 4);
 }
 
-// Grid batch * heads * 2: a CTA holds 64 value rows of one head's state, a warp 16
+// The long sequences of a prompt call, by one warp.
+__device__ __forceinline__ void list_long(const DeltaSeqs& s) {
+  const int lane = threadIdx.x;
+  int found = 0, chunks = 0;
+  for (int b0 = 0; b0 < s.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < s.batch) {
+      const int r0 = s.starts[b], r1 = s.starts[b + 1];
+      if (r0 >= 0 && r1 >= r0 && r1 <= s.rows) n = r1 - r0;   // reported where the sequence is left out
+    }
+    const int c = n > kFewRows ? (n + kChunk - 1) / kChunk : 0;
+    int before = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    const uint32_t any = __ballot_sync(0xffffffffu, c > 0);
+    const int at = found + __popc(any & ((1u << lane) - 1));
+    // starts that do not ascend can make more long sequences than there are rows for
+    if (c > 0 && at < s.many) s.index[1 + at] = b, s.index[1 + s.many + at] = chunks + before - c;
+    found += __popc(any);
+    chunks += __shfl_sync(0xffffffffu, before, 31);
+  }
+  if (lane == 0) s.index[0] = min(found, s.many);
+}
+
+// Grid batch * heads * 2 (and one CTA before them in a prompt call): a CTA holds 64 value rows of one head's state, a warp 16
 // of them; eight lanes share a row (16 keys each), so a product with the keys takes
 // three shuffles.  Bound by the states' bytes: with 64 registers of state a thread
 // and three CTAs an SM, 96 KB are on their way.  32 sequences x 96 heads read and
@@ -65,14 +93,19 @@ __device__ __forceinline__ float sum8(float v) {
 // take 72, two rows a thread and five CTAs 67, one row a thread 90.  Few heads are
 // no faster in smaller parts (32 heads: 3.4 us either way).
 __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows x, const DeltaSeqs s, uint16_t* out) {
-  const int part = blockIdx.x % kSplit, bh = blockIdx.x / kSplit;
+  if (s.index) {
+    if (blockIdx.x == 0) {   // first, so that it is done before the others
+      if (threadIdx.x < 32) list_long(s);
+      return;
+    }
+  }
+  const int cta = (int)blockIdx.x - (s.index ? 1 : 0), part = cta % kSplit, bh = cta / kSplit;
   const int h = bh % x.heads, b = bh / x.heads, hq = h / (x.heads / x.qk_heads);
   const int lane = threadIdx.x & 31, l = lane & 7;
   const int vrow = part * kCtaRows + (threadIdx.x >> 5) * 4 * R + (lane >> 3);  // this thread's rows: vrow + 4 r
   const int64_t at = (int64_t)vrow * kDeltaDim + 4 * l;
   int64_t row;
   int n;
-  grid_dep_launch();   // the kernel behind this one in a prompt call touches other sequences
   if (!seq_rows(s, b, &row, &n)) return;
   if (s.starts && n > kFewRows) return;
 
@@ -141,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows
 }  // namespace
 
 dsa_status_t launch_delta_rows(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, cudaStream_t st) {
-  delta_rows_kernel<<<(unsigned)((int64_t)s.batch * x.heads * kSplit), kThreads, 0, st>>>(x, s, out);
+  const int64_t ctas = (int64_t)s.batch * x.heads * kSplit + (s.index ? 1 : 0);
+  delta_rows_kernel<<<(unsigned)ctas, kThreads, 0, st>>>(x, s, out);
   count_launches(1);
   return launch_status();
 }

@@ -12,6 +12,7 @@ constexpr int kStateFloats = kDeltaDim * kDeltaDim;  // one head's state
 // few of them are there: one sequence of 96 heads 25-26 us, in rows 18.5 us for 16 rows, 25.9 for 24, 33 for 32;
 // 64 sequences 840 us, in rows 105 us for 1 row, 627 for 16, 911 for 24.
 constexpr int kFewRows = 20;
+constexpr int kChunk = 64;
 
 // dsa_delta_rows_t with the number of value heads.
 struct DeltaRows {
@@ -33,6 +34,10 @@ struct DeltaSeqs {
   const int32_t *slots_in, *slots_out;
   int32_t per_row;          // slots_out [batch][nq], a state after each row; else [batch], the last one
   int32_t* status;
+  // Prompt calls: the sequences of more than kFewRows rows, of which there can be `many`: their number, their indices
+  // [many], and the chunks of 64 rows of those before each [many].
+  int32_t* index;
+  int32_t many;
 };
 
 // First row and number of rows of sequence b; false where starts is not

@@ -23,7 +23,6 @@ namespace dsa {
 
 namespace {
 
-constexpr int kChunk = 64;
 constexpr int kTileHalf = kChunk * 128;                // 64 rows of 64 fp16 (128 bytes, 128-byte swizzle)
 constexpr int kTileBytes = 2 * kTileHalf;              // 64 rows x 128 channels
 // A record: K P (high and low parts), Q P, T (high and low), then B, K D (high and low), then the head's floats.
@@ -42,7 +41,8 @@ constexpr int kHeadBytes = 4 * (kHdP + kDeltaDim);
 struct ChunkArgs {
   DeltaRows x;
   DeltaSeqs s;
-  uint8_t* records;   // [rows / 64 + batch][heads]; chunk c of sequence b is number starts[b] / 64 + b + c
+  uint8_t* records;   // [chunks of the long sequences, one sequence after another][heads]
+  int32_t chunks;     // room for so many
   uint16_t* out;
   int resident;       // CTAs of the first kernel that run at once
 };
@@ -196,15 +196,17 @@ __device__ __forceinline__ float max_warp(float v) {  // of values >= 0
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// First row and number of rows of record number `slot`'s chunk: of the last sequence b with starts[b] / 64 + b <= slot.
+// First row and number of rows of record number `slot`'s chunk: of the last long sequence with no more chunks before it.
 __device__ __forceinline__ bool chunk_rows(const ChunkArgs& p, int slot, int64_t* row0, int* n) {
-  int seq = 0, end = p.s.batch;
-  while (end - seq > 1) {
-    const int mid = (seq + end) >> 1;
-    if (p.s.starts[mid] / kChunk + mid <= slot) seq = mid; else end = mid;
+  const int32_t* first = p.s.index + 1 + p.s.many;
+  int at = 0, end = p.s.index[0];
+  if (end == 0) return false;
+  while (end - at > 1) {
+    const int mid = (at + end) >> 1;
+    if (first[mid] <= slot) at = mid; else end = mid;
   }
-  if (!seq_rows(p.s, seq, row0, n) || *n <= kFewRows) return false;
-  const int c = slot - (int)(*row0 / kChunk + seq);
+  if (!seq_rows(p.s, p.s.index[1 + at], row0, n)) return false;
+  const int c = slot - first[at];
   if (c < 0 || c * kChunk >= *n) return false;
   *row0 += c * kChunk;
   *n = min(*n - c * kChunk, kChunk);
@@ -222,10 +224,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   int64_t row0;
   int n = 0;
   grid_dep_launch();   // the chain's first steps need nothing of this
-  if (!chunk_rows(p, blockIdx.x / x.heads, &row0, &n)) {
-    grid_dep_wait();
-    return;
-  }
+  if (!chunk_rows(p, blockIdx.x / x.heads, &row0, &n)) return;
   uint8_t* rec = p.records + (int64_t)blockIdx.x * kRecBytes;
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
@@ -576,7 +575,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   }
   const int any = __syncthreads_or(bad);
   if (tid == 0) reinterpret_cast<int*>(rec + kRecHead)[kHdBad] = any;
-  grid_dep_wait();   // what runs behind the chain runs behind the kernel before this one too
 }
 
 // ---------------------------------------------------------------- chain
@@ -637,16 +635,22 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sm = smem_u32(smem);
   const DeltaRows& x = p.x;
-  const int h = blockIdx.x % x.heads, b = blockIdx.x / x.heads, hq = h / (x.heads / x.qk_heads);
+  const int h = blockIdx.x % x.heads, at = blockIdx.x / x.heads, hq = h / (x.heads / x.qk_heads);
   const int warp = warp_number(), lane = threadIdx.x & 31;
+  // the list is of the kernel before the one that prepares the operands: complete when that one started
+  if (at >= __ldcg(p.s.index)) {
+    grid_dep_wait();
+    return;
+  }
+  const int b = __ldcg(p.s.index + 1 + at), slot = __ldcg(p.s.index + 1 + p.s.many + at);
   int64_t row0;
   int n;
-  if (!seq_rows(p.s, b, &row0, &n) || n <= kFewRows) {
+  if (!seq_rows(p.s, b, &row0, &n) || slot + (n + kChunk - 1) / kChunk > p.chunks) {   // (starts that do not ascend)
     grid_dep_wait();
     return;
   }
   const int chunks = (n + kChunk - 1) / kChunk;
-  const uint8_t* rec = p.records + ((row0 / kChunk + b) * x.heads + h) * kRecBytes;
+  const uint8_t* rec = p.records + ((int64_t)slot * x.heads + h) * kRecBytes;
   const int64_t rec_step = (int64_t)x.heads * kRecBytes;
 
   const uint32_t bars = sm + kCOffBars;
@@ -1117,11 +1121,18 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
 
 }  // namespace
 
+namespace {
+int long_sequences(int rows, int batch) { return std::min(batch, rows / (kFewRows + 1)); }
+int64_t long_chunks(int rows, int batch) { return (int64_t)rows / kChunk + long_sequences(rows, batch); }
+size_t list_bytes(int rows, int batch) { return ((size_t)(1 + 2 * long_sequences(rows, batch)) * 4 + 1023) & ~size_t(1023); }
+}  // namespace
+
 size_t delta_chunk_workspace_bytes(int rows, int batch, int heads) {
-  return ((size_t)rows / kChunk + batch) * heads * kRecBytes;
+  return list_bytes(rows, batch) + (size_t)long_chunks(rows, batch) * heads * kRecBytes;
 }
 
-dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, void* workspace, cudaStream_t st) {
+dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& seqs, uint16_t* out, void* workspace, cudaStream_t st) {
+  if (seqs.rows <= kFewRows) return launch_delta_rows(x, seqs, out, st);
   static std::atomic<uint64_t> ready{0};   // devices whose kernels may take their shared memory
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1136,24 +1147,26 @@ dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& s, uint16_
     if (at.numRegs * kChainThreads < 128 * kHelperRegs + 256 * kStateRegs) return DSA_ERR_UNSUPPORTED;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
+  DeltaSeqs s = seqs;
+  s.index = static_cast<int32_t*>(workspace);
+  s.many = long_sequences(s.rows, s.batch);
   const dsa_status_t first = launch_delta_rows(x, s, out, st);
-  if (first != DSA_OK || s.rows <= kFewRows) return first;
-  const ChunkArgs a{x, s, static_cast<uint8_t*>(workspace), out, 2 * num_sms()};
-  const int64_t records = ((int64_t)s.rows / kChunk + s.batch) * x.heads;
-  // each may start while the one before it still runs
+  if (first != DSA_OK) return first;
+  const int64_t chunks = long_chunks(s.rows, s.batch);
+  const ChunkArgs a{x, s, static_cast<uint8_t*>(workspace) + list_bytes(s.rows, s.batch), (int32_t)chunks, out, 2 * num_sms()};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)records);
+  cfg.gridDim = dim3((unsigned)(chunks * x.heads));
   cfg.blockDim = dim3(kPrepThreads);
   cfg.dynamicSmemBytes = kPrepSmem + 1024;
   count_launches(2);
   if (cuda_status(cudaLaunchKernelEx(&cfg, delta_prepare_kernel, a)) != DSA_OK) return DSA_ERR_CUDA;
-  cfg.gridDim = dim3((unsigned)(s.batch * x.heads));
+  cfg.attrs = &attr;   // the chain may start while operands are still prepared
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(s.many * x.heads));
   cfg.blockDim = dim3(kChainThreads);
   cfg.dynamicSmemBytes = kChainSmem;
   if (cuda_status(cudaLaunchKernelEx(&cfg, delta_chain_kernel, a)) != DSA_OK) return DSA_ERR_CUDA;

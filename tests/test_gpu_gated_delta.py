@@ -117,6 +117,31 @@ def test_prefill(lens, heads, qk, gate):
         assert torch.equal(pool[s], before[s])
 
 
+@pytest.mark.parametrize("batch", [33, 200])
+def test_prefill_of_many_sequences(batch):
+    """A mixed step: most sequences bring a row or two, some a prompt, some nothing."""
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.where(torch.rand(batch, generator=g) < 0.8, torch.randint(0, 3, (batch,), generator=g),
+                       torch.randint(15, 140, (batch,), generator=g)).tolist()
+    lens[5], lens[6], lens[7] = 20, 21, 0
+    rows, heads = sum(lens), 2
+    x = inputs(rows, heads, heads, seed=batch)
+    pool = pool_of(2 * batch, heads)
+    before = pool.clone()
+    slots_in = torch.randperm(batch, generator=g).to(torch.int32).cuda()
+    slots_out = (batch + torch.randperm(batch, generator=g)).to(torch.int32).cuda()
+    first = [sum(lens[:b]) for b in range(batch + 1)]
+    out, st = torch.zeros((rows, heads, DIM), dtype=torch.bfloat16, device="cuda"), status()
+    prefill(pool, x, ints(*first), slots_in, slots_out, out, st)
+    assert st.item() == 0
+    for b, n in enumerate(lens):
+        r = slice(first[b], first[b + 1])
+        s0 = before[slots_in[b]]
+        want, states, size, mass = rule(*(t[r] for t in x), SCALE, s0)
+        check_out(out[r], want, n, size, mass, x[0][r])
+        check_state(pool[slots_out[b]], states[-1] if n else s0.double(), n, size)
+
+
 def one(n, heads=2, seed=0, gate="channel"):
     x = inputs(n, heads, heads, gate, seed=seed)
     pool = pool_of(2, heads, seed=seed + 1)
