@@ -66,11 +66,6 @@ __device__ __forceinline__ float reciprocal(float x) {   // within one unit in t
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float exp2_approx(float x) {   // within 2^-22
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ f32x2 bf16x2_to_f32x2(uint32_t v) {
   return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
@@ -89,77 +84,29 @@ __device__ __forceinline__ void split_f16(f32x2 v, uint32_t& hi, uint32_t& lo) {
   hi = f16x2(hx, hy);
   lo = f16x2(r.x, r.y);
 }
-// The same in bf16, whose range fits every factor of the decays: 16 bits.
 __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void split_bf16(f32x2 v, uint32_t& hi, uint32_t& lo) {
-  const float2 f = v;
-  hi = bf16x2(f.x, f.y);
-  const float2 r = sub2(v, bf16x2_to_f32x2(hi));
-  lo = bf16x2(r.x, r.y);
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t (&r)[2]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
-}
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
 // ---------------------------------------------------------------- prepare
 constexpr int kPrepThreads = 256;
-constexpr int kPX = 0;                            // X = k L c in two parts and q L c: 64 rows x 256 bytes each
-constexpr int kPY = 3 * kChunk * 256;             // Y in two parts, 64 rows each
+constexpr int kPX = 0;                            // X = k L c, fp32: 64 rows x 512 bytes
+constexpr int kPQ = kPX + kChunk * 512;           // q L c, bf16: 64 rows x 256 bytes
+constexpr int kPY = kPQ + kChunk * 256;           // Y, fp32
 constexpr int kLdA = kChunk + 4;                  // floats: rows start four banks apart
-constexpr int kPA = kPY + 2 * kChunk * 256;       // A, then (I + A)^-1, fp32 [64][68]
+constexpr int kPA = kPY + kChunk * 512;           // A, then (I + A)^-1, fp32 [64][68]
 constexpr int kPB = kPA + kChunk * kLdA * 4;    // B, fp16, the record's image
 constexpr int kPTab = kPB + kTileHalf;            // block products [4][128]
-constexpr int kPBeta = kPTab + 4 * kDeltaDim * 4;
+constexpr int kPSum = kPTab + 4 * kDeltaDim * 4;  // sums of their logarithms
+constexpr int kPBeta = kPSum + 4 * kDeltaDim * 4;
 constexpr int kPMisc = kPBeta + kChunk * 4;
 constexpr int kPrepSmem = kPMisc + 128;
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
-// Offset of 16-byte piece c of row r in a tile of 256-byte rows: pieces are
-// exchanged so that eight rows' same piece lie in all banks.
+// Offset of eight channels c of row r in rows of 512 bytes of fp32 and of 256 bytes of
+// bf16: pieces are exchanged so that neighbouring rows' same piece lie in other banks.
+__device__ __forceinline__ uint32_t at512(int r, int c) { return (uint32_t)(r * 512 + ((c ^ (r & 7)) << 5)); }
 __device__ __forceinline__ uint32_t at256(int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); }
-
-// The 16 x 8 tile of X Y^T at rows x0 of X and y0 of Y, for keys (all four products
-// of the parts) and queries (two).
-__device__ __forceinline__ void tile_xy(uint32_t sm, int x0, int y0, float (&kk)[4], float (&qk)[4]) {
-  const int lane = threadIdx.x & 31;
-  float ll[4], lh[4], hl[4], ql[4];   // sums of their own: six short chains of products instead of two long ones
-  const int ar = x0 + (lane & 15), ac = lane >> 4, br = y0 + (lane & 7), bc = (lane >> 3) & 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = ll[i] = lh[i] = hl[i] = ql[i] = 0.f;
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
-    uint32_t xh[4], xl[4], xq[4], yh[2], yl[2];
-    const uint32_t a = at256(ar, 2 * ks + ac), b = at256(br, 2 * ks + bc);
-    ldsm4(sm + kPX + a, xh);
-    ldsm4(sm + kPX + kChunk * 256 + a, xl);
-    ldsm4(sm + kPX + 2 * kChunk * 256 + a, xq);
-    ldsm2(sm + kPY + b, yh);
-    ldsm2(sm + kPY + kChunk * 256 + b, yl);
-    mma_16x8x16(ll, xl, yl);
-    mma_16x8x16(lh, xl, yh);
-    mma_16x8x16(hl, xh, yl);
-    mma_16x8x16(kk, xh, yh);
-    mma_16x8x16(ql, xq, yl);
-    mma_16x8x16(qk, xq, yh);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) kk[i] += (lh[i] + hl[i]) + ll[i], qk[i] += ql[i];
-}
 
 __device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -167,8 +114,46 @@ __device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4]
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
+// fp32 as two tf32: the upper 11 bits and what they leave, 21 bits in all and fp32's range.
+__device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(v) & 0xFFFFE000u;
+  lo = __float_as_uint(v - __uint_as_float(hi));
+}
+
+// The 16 x 8 tile of X Y^T at rows x0 of X and y0 of Y, for keys (three products of the
+// parts) and queries (two).  A lane's two columns of a step of eight are neighbours: the
+// order of the channels in a sum is free.
+__device__ __forceinline__ void tile_xy(const uint8_t* smem, int x0, int y0, float (&kk)[4], float (&qk)[4]) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const uint8_t* X = smem + kPX;
+  const uint8_t* Q = smem + kPQ;
+  const uint8_t* Y = smem + kPY;
+  float lh[4], hl[4], ql[4];   // sums of their own: short chains of products
+#pragma unroll
+  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = lh[i] = hl[i] = ql[i] = 0.f;
+#pragma unroll 2
+  for (int c = 0; c < 16; ++c) {
+    const float2 xa = *reinterpret_cast<const float2*>(X + at512(x0 + g, c) + 8 * t);
+    const float2 xb = *reinterpret_cast<const float2*>(X + at512(x0 + g + 8, c) + 8 * t);
+    const float2 y = *reinterpret_cast<const float2*>(Y + at512(y0 + g, c) + 8 * t);
+    const uint32_t qa = *reinterpret_cast<const uint32_t*>(Q + at256(x0 + g, c) + 4 * t);
+    const uint32_t qb = *reinterpret_cast<const uint32_t*>(Q + at256(x0 + g + 8, c) + 4 * t);
+    uint32_t xh[4], xl[4], yh[2], yl[2];
+    split_tf32(xa.x, xh[0], xl[0]), split_tf32(xb.x, xh[1], xl[1]), split_tf32(xa.y, xh[2], xl[2]), split_tf32(xb.y, xh[3], xl[3]);
+    split_tf32(y.x, yh[0], yl[0]), split_tf32(y.y, yh[1], yl[1]);
+    const uint32_t q[4] = {qa << 16, qb << 16, qa & 0xFFFF0000u, qb & 0xFFFF0000u};
+    mma_16x8x8(lh, xl, yh);
+    mma_16x8x8(hl, xh, yl);
+    mma_16x8x8(kk, xh, yh);
+    mma_16x8x8(ql, q, yl);
+    mma_16x8x8(qk, q, yh);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) kk[i] += lh[i] + hl[i], qk[i] += ql[i];
+}
+
 // A 16 x 8 tile of sign * L R for fp32 matrices in shared memory: L's 16 rows, K columns; R's K
-// rows, 8 columns.  Each factor as two tf32 (the upper 11 bits and what they leave), three products.
+// rows, 8 columns.  Each factor as two tf32, three products.
 template <int K>
 __device__ __forceinline__ void mul_tile(const float* L, int ldl, const float* R, int ldr, float* out, int ldo, float sign) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
@@ -179,9 +164,9 @@ __device__ __forceinline__ void mul_tile(const float* L, int ldl, const float* R
     const float r[2] = {R[(k + t) * ldr + g], R[(k + t + 4) * ldr + g]};
     uint32_t lh[4], ll[4], rh[2], rl[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lh[i] = __float_as_uint(l[i]) & 0xFFFFE000u, ll[i] = __float_as_uint(l[i] - __uint_as_float(lh[i]));
+    for (int i = 0; i < 4; ++i) split_tf32(l[i], lh[i], ll[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) rh[i] = __float_as_uint(r[i]) & 0xFFFFE000u, rl[i] = __float_as_uint(r[i] - __uint_as_float(rh[i]));
+    for (int i = 0; i < 2; ++i) split_tf32(r[i], rh[i], rl[i]);
     mma_16x8x8(d2, ll, rh);
     mma_16x8x8(d1, lh, rl);
     mma_16x8x8(d, lh, rh);
@@ -289,12 +274,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     bad = !(fabsf(bt) <= 3.4e38f);
   }
   const f32x2 one = pack2(1.f, 1.f);
-  f32x2 block = one;
+  f32x2 block = one, sum = make_float2(0.f, 0.f);
   float grow = 1.f, amax = 0.f;
   uint32_t km = 0, qm = 0;
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
-    a[t].x = exp2_approx(a[t].x * 1.44269504088896341f), a[t].y = exp2_approx(a[t].y * 1.44269504088896341f);
+    sum.x += a[t].x, sum.y += a[t].y;
+    a[t].x = expf(a[t].x), a[t].y = expf(a[t].y);
     block = mul2(block, a[t]);
     amax = fmaxf(amax, fmaxf(a[t].x, a[t].y));
     km = __vmaxu2(km, kr[t] & 0x7FFF7FFFu), qm = __vmaxu2(qm, qr[t] & 0x7FFF7FFFu);
@@ -306,6 +292,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   const float Bx = block.x, By = block.y;
   bad |= !(amax <= 3.4e38f) || !(Bx <= 3.4e38f) || !(By <= 3.4e38f);   // a decay that is no number makes its product none
   tab[I * kDeltaDim + 2 * q2] = Bx, tab[I * kDeltaDim + 2 * q2 + 1] = By;
+  *reinterpret_cast<f32x2*>(smem + kPSum + 4 * (I * kDeltaDim + 2 * q2)) = sum;
   {
     const float k1 = __uint_as_float(max(km & 0xFFFFu, km >> 16) << 16), q1 = __uint_as_float(max(qm & 0xFFFFu, qm >> 16) << 16);
     bad |= !(k1 <= 3.4e38f) || !(q1 <= 3.4e38f) || !(grow <= 3.4e38f);
@@ -377,17 +364,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       *reinterpret_cast<uint32_t*>(rec + kRecKp + kTileBytes + o) = lo2;
       const float2 qp = mul2(ql, pre_q), xq = mul2(ql, c_q), wf = w;
       *reinterpret_cast<uint32_t*>(rec + kRecQp + o) = f16x2(qp.x, qp.y);
-      const uint32_t s = at256(r, piece) + in_piece;
-      split_bf16(mul2(k, w), hi2, lo2);
-      *reinterpret_cast<uint32_t*>(smem + kPX + s) = hi2;
-      *reinterpret_cast<uint32_t*>(smem + kPX + kChunk * 256 + s) = lo2;
-      *reinterpret_cast<uint32_t*>(smem + kPX + 2 * kChunk * 256 + s) = bf16x2(xq.x, xq.y);
+      const uint32_t s = at512(r, piece) + 2 * in_piece;
+      *reinterpret_cast<f32x2*>(smem + kPX + s) = mul2(k, w);
+      *reinterpret_cast<uint32_t*>(smem + kPQ + at256(r, piece) + in_piece) = bf16x2(xq.x, xq.y);
       // Y of the block itself: k / (L c); no number where the block is not safe, and not used there
-      split_bf16(mul2(k, pack2(reciprocal(wf.x), reciprocal(wf.y))), hi2, lo2);
-      *reinterpret_cast<uint32_t*>(smem + kPY + s) = hi2;
-      *reinterpret_cast<uint32_t*>(smem + kPY + kChunk * 256 + s) = lo2;
+      *reinterpret_cast<f32x2*>(smem + kPY + s) = mul2(k, pack2(reciprocal(wf.x), reciprocal(wf.y)));
     }
-    if (I == 3) *reinterpret_cast<f32x2*>(rec + kRecHead + 4 * (kHdP + 2 * q2)) = mul2(pre, block);
+    if (I == 3) {
+      // the chunk's decay from the sum of the logarithms: the state is multiplied by it chunk after chunk, and a product
+      // of 64 rounded factors a chunk costs a slow channel 1e-6 in a thousand rows
+      f32x2 all = sum;
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        const f32x2 g = *reinterpret_cast<const f32x2*>(smem + kPSum + 4 * (b * kDeltaDim + 2 * q2));
+        all.x += g.x, all.y += g.y;
+      }
+      *reinterpret_cast<f32x2*>(rec + kRecHead + 4 * (kHdP + 2 * q2)) = make_float2(expf(all.x), expf(all.y));
+    }
   }
   // ---- backward: K D
   {
@@ -420,7 +413,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     const int D = warp >> 1;
     if ((unsafe_w[2 * D] | unsafe_w[2 * D + 1]) == 0u) {
       float kk[4], qk[4];
-      tile_xy(sm, 16 * D, 16 * D + 8 * (warp & 1), kk, qk);
+      tile_xy(smem, 16 * D, 16 * D + 8 * (warp & 1), kk, qk);
       put_tile(16 * D, 16 * D + 8 * (warp & 1), kk, qk);
     } else {
       // decays that leave fp32's range within 16 rows: pair by pair, four channels a lane
@@ -457,11 +450,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   auto put_y = [&](int y0, f32x2 l) {
 #pragma unroll
     for (int t = 15; t >= 0; --t) {
-      uint32_t hi2, lo2;
-      split_bf16(mul2(bf16x2_to_f32x2(kr[t]), l), hi2, lo2);
-      const uint32_t s = at256(y0 + t, piece) + in_piece;
-      *reinterpret_cast<uint32_t*>(smem + kPY + s) = hi2;
-      *reinterpret_cast<uint32_t*>(smem + kPY + kChunk * 256 + s) = lo2;
+      *reinterpret_cast<f32x2*>(smem + kPY + at512(y0 + t, piece) + 2 * in_piece) = mul2(bf16x2_to_f32x2(kr[t]), l);
       l = mul2(l, a[t]);
     }
   };
@@ -474,7 +463,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   __syncthreads();
   if (warp < 6) {
     float kk[4], qk[4];
-    tile_xy(sm, 48, 8 * warp, kk, qk);
+    tile_xy(smem, 48, 8 * warp, kk, qk);
     put_tile(48, 8 * warp, kk, qk);
   }
   // meanwhile the inverses of I + A's diagonal blocks, in their place, by substitution: a thread a column
@@ -506,7 +495,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   if (warp < 6) {
     float kk[4], qk[4];
     const int x0 = warp < 4 ? 32 : 16, y0 = warp < 4 ? 8 * warp : 32 + 8 * (warp - 4), j0 = warp < 4 ? y0 : y0 - 32;
-    tile_xy(sm, x0, y0, kk, qk);
+    tile_xy(smem, x0, y0, kk, qk);
     put_tile(x0, j0, kk, qk);
   }
   __syncthreads();
