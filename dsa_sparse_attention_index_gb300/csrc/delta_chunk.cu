@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   for (int b = 0; b < 4; ++b) mg *= fmaxf(misc[16 + 2 * b], misc[17 + 2 * b]);
   const uint32_t* unsafe_w = reinterpret_cast<const uint32_t*>(misc) + 24;
   const float scale = x.scale;
-  bad |= !(mg <= 1e30f) || !(mk <= 1e30f) || !(mq <= 1e30f) || !(mk * mk * mg <= 1e30f) ||
+  // (growth by more than 2^10 would leave the other channels too few bits of the common power of two)
+  bad |= !(mg <= 1024.f) || !(mk <= 1e30f) || !(mq <= 1e30f) || !(mk * mk * mg <= 1e30f) ||
          !(mk * mq * mg * fabsf(scale) <= 1e30f) || !(fabsf(scale) <= 1e30f);
   // powers of two that bring the operands into fp16's range, from bounds: products of decays grow no further than mg
   const float sc_k = pow2_scale(mk * mg, 14);                        // of K P and K D
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       bad |= t[j] != t[j];
       m = fmaxf(m, fabsf(t[j]));
     }
-    bad |= !(m <= 1e30f);
+    bad |= !(m <= 1e12f);   // keys much longer than one: the rows go one by one
     m = max_warp(bad ? 0.f : m);
     if (lane == 0) misc[warp] = m;
     __syncthreads();

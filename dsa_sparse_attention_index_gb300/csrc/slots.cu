@@ -10,6 +10,7 @@
 // The row with p % 64 = 0 is the only first one of a fresh page: it puts the
 // page into the table.
 #include <algorithm>
+#include <atomic>
 
 #include <cooperative_groups.h>
 
@@ -46,6 +47,10 @@ __device__ __forceinline__ int2 lengths_of(const SlotArgs& a, int i) {
 }
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
 
+// Bound by a chain of latencies: lengths, scan, search, page, store (64 requests: 3.8
+// us in a graph, of which a launch takes 2.3), and with many rows by the search and
+// the page's address, 16 bytes of positions and of slots a thread and turn (2,048
+// requests, 262,144 rows: 14.4 us in 16 CTAs; row by row in 8 CTAs 26).
 // One cluster.  Every CTA scans the requests (a tile of 2,048 at a time, kept
 // in shared memory) and places its share of the rows; nothing that the caller
 // may pass as input and output at once (lengths, the stack's count) is written
@@ -66,7 +71,7 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
   const bool wide = ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
   long long rows0 = 0, pages0 = 0;  // of the tiles before
   for (int base = 0; base < a.batch; base += kSlotTile) {
-    // scan of (rows, pages), rows in the upper half: either sum of a tile stays below 2^42 and 2^36
+    // scans of rows and of pages, in 64 bits: lengths go up to 2^30
     int c[kPer], n[kPer];
     long long rsum = 0, psum = 0;
 #pragma unroll
@@ -176,6 +181,30 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
   }
 }
 
+// CTAs of the largest cluster that the current device can schedule, 16 or 8 (asked once per device).
+int most_ctas() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
+  int n = 0;
+  if (cudaFuncSetAttribute(assign_slots_kernel<1024>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 16, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(1024);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, assign_slots_kernel<1024>, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  n = n > 0 ? 16 : 8;
+  if (dev >= 0 && dev < 64) known[dev] = n;
+  return n;
+}
+
 }  // namespace
 
 dsa_status_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, int batch, const int32_t* free_blocks,
@@ -184,14 +213,10 @@ dsa_status_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, in
                                  int32_t* slots, int max_rows, int32_t* status, cudaStream_t st) {
   const SlotArgs a{cached,     fresh,    batch,  free_blocks, free_capacity, free_count, free_left, num_blocks, table,
                    max_blocks, seq_lens, starts, positions,   slots,         max_rows,   status};
-  // one CTA for up to 4,096 rows, so that a decode step's few take no cluster; 16 for many
+  // one CTA for up to 4,096 rows, so that a decode step's few take no cluster; 16 for many where they can be scheduled
   const bool small = max_rows <= 1024 && batch <= 1024;
-  const int ctas = max_rows > 8 * 4096 ? 16 : max_rows > 4096 ? 4 : 1;
+  const int ctas = max_rows > 8 * 4096 ? most_ctas() : max_rows > 4096 ? 4 : 1;
   const auto kernel = small ? assign_slots_kernel<256> : assign_slots_kernel<1024>;
-  if (ctas > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(small ? 256 : 1024);
@@ -201,12 +226,8 @@ dsa_status_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, in
   at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_status(e);
-  }
   count_launches(1);
+  if (cuda_status(cudaLaunchKernelEx(&cfg, kernel, a)) != DSA_OK) return DSA_ERR_CUDA;
   return launch_status();
 }
 

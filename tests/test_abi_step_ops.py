@@ -118,3 +118,85 @@ def test_binding_assign(calls):
         with pytest.raises(ValueError):
             go(**bad)
     assert calls.calls == 2
+
+
+class Rows(Tensor):
+    """A stand-in with strides: `apart` more elements between rows."""
+
+    def __init__(self, shape, dtype, apart=0, cuda=True, order=None):
+        super().__init__(shape, dtype)
+        self.is_cuda, inner, strides = cuda, 1, []
+        for size in reversed(shape[1:]):
+            strides.append(inner)
+            inner *= size
+        self._strides = order or (inner + apart, *reversed(strides))
+
+    def stride(self, i=None):
+        return self._strides if i is None else self._strides[i]
+
+
+def layer(rows=6, qk=2, heads=4, wide=True, **kw):
+    bf, f32 = torch.bfloat16, torch.float32
+    t = dict(q=Rows((rows, qk, 128), bf, 64), k=Rows((rows, qk, 128), bf), v=Rows((rows, heads, 128), bf),
+             gate=Rows((rows, heads, 128) if wide else (rows, heads), f32), beta=Rows((rows, heads), f32, 3), scale=0.5)
+    return B.DeltaRows(**{**t, **kw})
+
+
+def test_binding_descriptors():
+    x = layer().layout
+    assert (x.ld_q, x.ld_k, x.ld_v, x.ld_gate, x.ld_beta, x.qk_heads, x.gate_dim) == (320, 256, 512, 512, 7, 2, 128)
+    assert layer(wide=False).layout.gate_dim == 1 and layer(rows=1).layout.ld_q == 256
+    bf, f32 = torch.bfloat16, torch.float32
+    for bad in (dict(q=Rows((6, 2, 64), bf)), dict(q=Rows((6, 256), bf)), dict(k=Rows((5, 2, 128), bf)),
+                dict(v=Rows((6, 4, 128), f32)), dict(gate=Rows((6, 4, 64), f32)), dict(beta=Rows((6, 3), f32)),
+                dict(gate=Rows((6, 4, 128), bf)), dict(v=Rows((6, 4, 128), bf, cuda=False)),
+                dict(k=Rows((6, 2, 128), bf, order=(256, 1, 2)))):
+        with pytest.raises(ValueError):
+            layer(**bad)
+    p = B.StatePool(Rows((5, 4, 128, 128), f32, 32)).layout
+    assert (p.slot_stride, p.num_slots, p.heads) == (4 * (4 * 16384 + 32), 5, 4)
+    for bad in (Rows((5, 4, 128, 64), f32), Rows((5, 4, 16384), f32), Rows((5, 4, 128, 128), bf),
+                Rows((5, 4, 128, 128), f32, cuda=False), Rows((5, 4, 128, 128), f32, order=(65536, 16384, 1, 128))):
+        with pytest.raises(ValueError):
+            B.StatePool(bad)
+
+
+def test_binding_gated_delta(calls):
+    f32, bf = torch.float32, torch.bfloat16
+    pool, x, out, ws = B.StatePool(Rows((9, 4, 128, 128), f32)), layer(), Tensor((6, 4, 128), bf), Tensor((99,), torch.uint8)
+
+    def decode(pool=pool, x=x, nq=3, slots_in=i32(2), slots_out=i32(2, 3), out=out, status=i32(1)):
+        B.gated_delta_decode(pool, x, nq, slots_in, slots_out, out, status)
+
+    def prefill(pool=pool, x=x, starts=i32(3), slots_in=i32(2), slots_out=i32(2), out=out, ws=ws, status=i32(1)):
+        B.gated_delta_prefill(pool, x, starts, slots_in, slots_out, out, ws, status)
+
+    decode()
+    prefill()
+    assert calls.calls == 2
+    other = B.StatePool(Rows((9, 8, 128, 128), f32))
+    for bad in (dict(nq=2), dict(slots_out=i32(2, 2)), dict(slots_in=Tensor((2,), torch.int64)), dict(pool=other),
+                dict(out=Tensor((6, 4, 128), f32)), dict(out=Tensor((5, 4, 128), bf)), dict(status=i32(0))):
+        with pytest.raises(ValueError):
+            decode(**bad)
+    for bad in (dict(starts=i32(2)), dict(slots_out=i32(2, 1)), dict(slots_in=i32(3)), dict(pool=other),
+                dict(out=Tensor((6, 3, 128), bf)), dict(starts=Tensor((3,), torch.int64))):
+        with pytest.raises(ValueError):
+            prefill(**bad)
+    assert calls.calls == 2
+
+
+def test_binding_append_slots(calls):
+    bf = torch.bfloat16
+    cache = B.PagedCache(Tensor((3, 45312), torch.uint8), 45312, 0, 36864, B.KEY_FP8_E4M3, 1.0)
+
+    def go(cache=cache, slots=i32(4), lat=Tensor((4, 576), bf), key=Tensor((4, 128), bf), status=i32(1)):
+        B.cache_append_slots(cache, slots, lat, key, status)
+
+    go()
+    small = B.PagedCache(Tensor((3, 45000), torch.uint8), 45312, 0, 36864, B.KEY_FP8_E4M3, 1.0)
+    for bad in (dict(lat=Tensor((3, 576), bf)), dict(key=Tensor((4, 64), bf)), dict(slots=Tensor((4,), torch.int64)),
+                dict(cache=small), dict(lat=Tensor((4, 576), torch.float32))):
+        with pytest.raises(ValueError):
+            go(**bad)
+    assert calls.calls == 1

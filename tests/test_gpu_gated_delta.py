@@ -159,7 +159,7 @@ def run_one(x, pool, out, st):
     return want
 
 
-@pytest.mark.parametrize("what", ["none", "reset", "rare reset", "fast", "very fast", "mixed", "growing"])
+@pytest.mark.parametrize("what", ["none", "reset", "rare reset", "fast", "very fast", "mixed", "growing", "growing fast"])
 def test_decays(what):
     n = 150
     x, pool, out, st = one(n, seed=5)
@@ -178,12 +178,15 @@ def test_decays(what):
         g.fill_(-40.0)
     elif what == "mixed":
         g[:] = torch.where(torch.rand(g.shape, device="cuda") < 0.3, -30 * torch.rand(g.shape, device="cuda"), g)
-    else:
+    elif what == "growing":
         g[:, :, ::2] = 0.01
+    else:
+        g[30:90] = 0.2
     run_one(x, pool, out, st)
 
 
-@pytest.mark.parametrize("what", ["beta 0", "beta 1", "beta 2", "one key", "zero keys", "two keys", "large values", "tiny"])
+@pytest.mark.parametrize("what", ["beta 0", "beta 1", "beta 2", "one key", "zero keys", "two keys", "large values", "tiny",
+                                  "long keys"])
 def test_extremes(what):
     n = 140
     x, pool, out, st = one(n, seed=9)
@@ -203,6 +206,9 @@ def test_extremes(what):
     elif what == "large values":
         v.mul_(2.0 ** 100)
         pool.mul_(2.0 ** 100)
+    elif what == "long keys":      # |k| = 8: beta |k|^2 is what counts
+        k.mul_(8.0)
+        beta.mul_(1.0 / 64)
     else:
         v.mul_(2.0 ** -60)
         pool.mul_(2.0 ** -60)
@@ -317,3 +323,46 @@ def test_side_stream_and_graph():
         assert st.item() == 0
         for got, kept in zip((out, next_out, pool), eager):
             assert torch.equal(got, kept)
+
+
+def test_a_sequence_does_not_depend_on_its_batch():
+    """Alone, among others and on two streams at once: the same bits."""
+    lens, heads = [150, 7, 333, 64, 21], 3
+    rows, first = sum(lens), [sum([150, 7, 333, 64, 21][:b]) for b in range(6)]
+    x = inputs(rows, heads, heads, seed=77)
+    pool = pool_of(2 * len(lens), heads)
+    before = pool.clone()
+    slots = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    out, st = torch.zeros((rows, heads, DIM), dtype=torch.bfloat16, device="cuda"), status()
+    prefill(pool, x, ints(*first), slots, slots + len(lens), out, st)
+    streams, alone = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        part = [t[first[b]:first[b + 1]].clone() for t in x]
+        p, o = before[b:b + 1].repeat(2, 1, 1, 1), torch.zeros((n, heads, DIM), dtype=torch.bfloat16, device="cuda")
+        args = part, p, o, ints(0, n), ints(0), ints(1)
+        ws = B.workspace(B.gated_delta_prefill_workspace_size(n, 1, heads))
+        alone.append((args, ws))
+    torch.cuda.synchronize()
+    for i, ((part, p, o, starts, a, b), ws) in enumerate(alone):
+        B.gated_delta_prefill(B.StatePool(p), B.DeltaRows(*part, SCALE), starts, a, b, o, ws, st, streams[i % 2])
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for b, ((_, p, o, *_), _) in enumerate(alone):
+        assert torch.equal(o, out[first[b]:first[b + 1]]) and torch.equal(p[1], pool[len(lens) + b])
+
+
+def test_slots_beyond_4_gib():
+    heads, apart = 1, (5 << 30) // 4
+    raw = torch.zeros(apart + heads * DIM * DIM, device="cuda")
+    pool = raw.as_strided((2, heads, DIM, DIM), (apart, DIM * DIM, DIM, 1))
+    pool.copy_(pool_of(2, heads))
+    s0 = pool[1].clone()
+    x, out, st = inputs(100, heads, heads, seed=8), torch.zeros((100, heads, DIM), dtype=torch.bfloat16, device="cuda"), status()
+    want, states, size, mass = rule(*x, SCALE, s0)
+    prefill(pool, [t[:97] for t in x], ints(0, 97), ints(1), ints(1), out[:97], st)
+    B.gated_delta_decode(B.StatePool(pool), B.DeltaRows(*(t[97:] for t in x), SCALE), 3, ints(1), ints(-1, -1, 1).view(1, 3),
+                         out[97:], st)
+    assert st.item() == 0
+    check_out(out, want, 100, size, mass, x[0])
+    check_state(pool[1], states[-1], 100, size)

@@ -87,6 +87,14 @@ def test_assign(mix, pad):
     s.check()
 
 
+@pytest.mark.parametrize("mix", ["page ends", "prompts", "2049"])
+def test_assign_into_buffers_off_a_16_byte_boundary(mix):
+    s = Step(*MIXES[mix])
+    s.pos, s.slots = (torch.full((t.numel() + 3,), -9, dtype=torch.int32, device="cuda")[3:] for t in (s.pos, s.slots))
+    s.call()
+    s.check()
+
+
 def test_assign_of_an_empty_batch():
     s = Step([3], [1], pad=6)
     none = s.c[:0]
