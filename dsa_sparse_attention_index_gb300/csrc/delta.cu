@@ -63,9 +63,10 @@ __device__ __forceinline__ void list_long(const DeltaSeqs& s) {
   int found = 0, chunks = 0;
   for (int b0 = 0; b0 < s.batch; b0 += 32) {
     const int b = b0 + lane;
-    int n = 0;
+    int n = 0, r0 = 0;
     if (b < s.batch) {
-      const int r0 = s.starts[b], r1 = s.starts[b + 1];
+      r0 = s.starts[b];
+      const int r1 = s.starts[b + 1];
       if (r0 >= 0 && r1 >= r0 && r1 <= s.rows) n = r1 - r0;   // reported where the sequence is left out
     }
     const int c = n > kFewRows ? (n + kChunk - 1) / kChunk : 0;
@@ -78,11 +79,11 @@ __device__ __forceinline__ void list_long(const DeltaSeqs& s) {
     const uint32_t any = __ballot_sync(0xffffffffu, c > 0);
     const int at = found + __popc(any & ((1u << lane) - 1));
     // starts that do not ascend can make more long sequences than there are rows for
-    if (c > 0 && at < s.many) s.index[1 + at] = b, s.index[1 + s.many + at] = chunks + before - c;
+    if (c > 0 && at < s.many) s.index[1 + at] = make_int4(r0, n, chunks + before - c, b);
     found += __popc(any);
     chunks += __shfl_sync(0xffffffffu, before, 31);
   }
-  if (lane == 0) s.index[0] = min(found, s.many);
+  if (lane == 0) s.index[0].x = min(found, s.many);
 }
 
 // Grid batch * heads * 2 (and one CTA before them in a prompt call): a CTA holds 64 value rows of one head's state, a warp 16

@@ -34,9 +34,9 @@ struct DeltaSeqs {
   const int32_t *slots_in, *slots_out;
   int32_t per_row;          // slots_out [batch][nq], a state after each row; else [batch], the last one
   int32_t* status;
-  // Prompt calls: the sequences of more than kFewRows rows, of which there can be `many`: their number, their indices
-  // [many], and the chunks of 64 rows of those before each [many].
-  int32_t* index;
+  // Prompt calls: the sequences of more than kFewRows rows, of which there can be `many`: their number in the first
+  // entry, then for each its first row, its rows, the chunks of 64 rows of those before it, and its index.
+  int4* index;
   int32_t many;
 };
 

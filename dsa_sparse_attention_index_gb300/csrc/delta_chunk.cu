@@ -183,18 +183,17 @@ __device__ __forceinline__ float max_warp(float v) {  // of values >= 0
 
 // First row and number of rows of record number `slot`'s chunk: of the last long sequence with no more chunks before it.
 __device__ __forceinline__ bool chunk_rows(const ChunkArgs& p, int slot, int64_t* row0, int* n) {
-  const int32_t* first = p.s.index + 1 + p.s.many;
-  int at = 0, end = p.s.index[0];
+  int at = 0, end = p.s.index[0].x;
   if (end == 0) return false;
   while (end - at > 1) {
     const int mid = (at + end) >> 1;
-    if (first[mid] <= slot) at = mid; else end = mid;
+    if (p.s.index[1 + mid].z <= slot) at = mid; else end = mid;
   }
-  if (!seq_rows(p.s, p.s.index[1 + at], row0, n)) return false;
-  const int c = slot - first[at];
-  if (c < 0 || c * kChunk >= *n) return false;
-  *row0 += c * kChunk;
-  *n = min(*n - c * kChunk, kChunk);
+  const int4 seq = p.s.index[1 + at];
+  const int c = slot - seq.z;
+  if (c < 0 || c * kChunk >= seq.y) return false;
+  *row0 = seq.x + c * kChunk;
+  *n = min(seq.y - c * kChunk, kChunk);
   return true;
 }
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -628,18 +627,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
   const int h = blockIdx.x % x.heads, at = blockIdx.x / x.heads, hq = h / (x.heads / x.qk_heads);
   const int warp = warp_number(), lane = threadIdx.x & 31;
   // the list is of the kernel before the one that prepares the operands: complete when that one started
-  if (at >= __ldcg(p.s.index)) {
+  const int4 seq = at < __ldcg(&p.s.index[0].x) ? __ldcg(p.s.index + 1 + at) : make_int4(0, 0, 0, 0);
+  const int64_t row0 = seq.x;
+  const int n = seq.y, slot = seq.z, b = seq.w, chunks = (n + kChunk - 1) / kChunk;
+  if (n == 0 || slot + chunks > p.chunks) {   // (starts that do not ascend can make more chunks than there is room for)
     grid_dep_wait();
     return;
   }
-  const int b = __ldcg(p.s.index + 1 + at), slot = __ldcg(p.s.index + 1 + p.s.many + at);
-  int64_t row0;
-  int n;
-  if (!seq_rows(p.s, b, &row0, &n) || slot + (n + kChunk - 1) / kChunk > p.chunks) {   // (starts that do not ascend)
-    grid_dep_wait();
-    return;
-  }
-  const int chunks = (n + kChunk - 1) / kChunk;
   const uint8_t* rec = p.records + ((int64_t)slot * x.heads + h) * kRecBytes;
   const int64_t rec_step = (int64_t)x.heads * kRecBytes;
 
@@ -1114,7 +1108,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
 namespace {
 int long_sequences(int rows, int batch) { return std::min(batch, rows / (kFewRows + 1)); }
 int64_t long_chunks(int rows, int batch) { return (int64_t)rows / kChunk + long_sequences(rows, batch); }
-size_t list_bytes(int rows, int batch) { return ((size_t)(1 + 2 * long_sequences(rows, batch)) * 4 + 1023) & ~size_t(1023); }
+size_t list_bytes(int rows, int batch) { return ((size_t)(1 + long_sequences(rows, batch)) * 16 + 1023) & ~size_t(1023); }
 }  // namespace
 
 size_t delta_chunk_workspace_bytes(int rows, int batch, int heads) {
@@ -1138,7 +1132,7 @@ dsa_status_t launch_delta_chunks(const DeltaRows& x, const DeltaSeqs& seqs, uint
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
   DeltaSeqs s = seqs;
-  s.index = static_cast<int32_t*>(workspace);
+  s.index = static_cast<int4*>(workspace);
   s.many = long_sequences(s.rows, s.batch);
   const dsa_status_t first = launch_delta_rows(x, s, out, st);
   if (first != DSA_OK) return first;
