@@ -11,7 +11,8 @@
 // Two kernels.  delta_prepare_kernel: everything that does not depend on the
 // state, a CTA per chunk and head, into a record of operands laid out as the tensor
 // core reads them.  delta_chain_kernel: a CTA per sequence and head walks the
-// chunks; the state stays in registers in fp32.
+// chunks; the state stays in registers in fp32.  2,048 rows of 96 heads: 184 us and
+// 135 us (row by row 5,478 us).
 #include <algorithm>
 #include <atomic>
 
@@ -54,8 +55,8 @@ __device__ __forceinline__ float pow2_scale(float bound, int top) {
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
-// Two neighbouring channels.  (The packed fp32 instructions take fewer slots, but
-// the moves into register pairs cost more: chain 164 us with them, 145 without.)
+// Two neighbouring channels.  (The packed fp32 instructions take fewer slots, but the
+// moves into register pairs cost more: a chain of 32 chunks 164 us with them, 145 without.)
 using f32x2 = float2;
 __device__ __forceinline__ f32x2 pack2(float x, float y) { return make_float2(x, y); }
 __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) { return make_float2(a.x * b.x, a.y * b.y); }
@@ -89,6 +90,22 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // ---------------------------------------------------------------- prepare
+// A thread has two channels of 16 rows: k, q and the decays in registers, running
+// products of the decays forward (K P, Q P, X) and backward (K D, Y).  A and B by
+// blocks of 16 rows, X Y^T:
+//   within a block       X_i = k_i L_i c,  Y_j = k_j / (L_j c), L the decays from the block's
+//                        start, c a power of two that centres them by channel: what a pair
+//                        gets is a quotient of products of 16 factors at most.  A block whose
+//                        decays leave 2^-120 .. 2^10 is computed pair by pair instead.
+//   between two blocks   Y_j = k_j times the decays from row j to the start of X's block, all
+//                        products of factors: nothing underflows that should not
+// The factors are fp32, cut into two tf32 on the way into the mma: three products, 21
+// bits.  (Two bf16 parts were 6 % faster and left states 7 to 10e-7 off instead of 4
+// to 5e-7.)  The inverse of I + A goes by blocks: the diagonal ones by substitution, a
+// thread a column, while other warps still make tiles, then two levels of products.
+// What bounds it: 36,770 warp instructions a chunk and head at 2.2 a cycle; its
+// memory traffic could go at twice the rate.  16 warps an SM, as registers and
+// shared memory allow; 512 threads a CTA or 16-byte pieces a thread were slower.
 constexpr int kPrepThreads = 256;
 constexpr int kPX = 0;                            // X = k L c, fp32: 64 rows x 512 bytes
 constexpr int kPQ = kPX + kChunk * 512;           // q L c, bf16: 64 rows x 256 bytes
@@ -569,14 +586,22 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 // ---------------------------------------------------------------- chain
 // Warps 0..7 hold the state: row v = 32 (w % 4) + lane of it, keys 64 (w / 4) ..
 // + 63, and turn each product into the next one's operand; warp 8 issues the MMAs,
-// warp 9 copies the records, two chunks deep.  All products are transposed, with
-// the 128 values on the tensor core's rows:
+// warp 9 copies the operands, two chunks deep, warp 10 stores the outputs.  All
+// products are transposed, with the 128 values on the tensor core's rows:
 //   R^T [v][t] = V^T - S (K P)^T   A = S in two fp16 parts from TMEM, times K P's two (three products)
 //   U^T = R^T T^T                  A = R in two parts
 //   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
 //   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
 // The parts of a row of S, R or U are times a power of two from a bound of it, so
-// that they keep 22 bits of its largest element whatever its size.
+// that they keep 21 bits of its largest element whatever its size.  The bounds come
+// from maxima that the two warps of a row exchange one step later, so they may be
+// loose: fp16's exponents leave room for 2^18.
+// Where something in a chunk is no finite number, or leaves the powers' range, its rows
+// go one by one: the zeros of T and B would carry a NaN to the rows before it.
+// What bounds it: a chain of latencies, 7,700 cycles a chunk, of which the tensor pipe
+// works 2,200: three products that wait for each other, their way through TMEM, and the
+// conversions between them (S 940 cycles, R 680, U 530, the update 780).  Outputs are
+// converted while R is made, the next values read while the update is.
 constexpr int kChainThreads = 12 * 32;   // three warpgroups: two of state warps, one of the rest (its last warp has no work)
 // Of the block's 384 x 168 registers the state warps take 200 a thread and leave 104 to the others: with 168 they spill.
 constexpr int kHelperRegs = 104, kStateRegs = 200;
