@@ -142,19 +142,21 @@ __device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) 
 // order of the channels in a sum is free.
 __device__ __forceinline__ void tile_xy(const uint8_t* smem, int x0, int y0, float (&kk)[4], float (&qk)[4]) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-  const uint8_t* X = smem + kPX;
-  const uint8_t* Q = smem + kPQ;
-  const uint8_t* Y = smem + kPY;
+  // rows x0 + g, x0 + g + 8 and y0 + g: the same place in a row's exchanged pieces (x0 and y0 are multiples of eight)
+  const uint8_t* X = smem + kPX + (x0 + g) * 512 + 8 * t;
+  const uint8_t* Q = smem + kPQ + (x0 + g) * 256 + 4 * t;
+  const uint8_t* Y = smem + kPY + (y0 + g) * 512 + 8 * t;
   float lh[4], hl[4], ql[4];   // sums of their own: short chains of products
 #pragma unroll
   for (int i = 0; i < 4; ++i) kk[i] = qk[i] = lh[i] = hl[i] = ql[i] = 0.f;
-#pragma unroll 2
+#pragma unroll 8
   for (int c = 0; c < 16; ++c) {
-    const float2 xa = *reinterpret_cast<const float2*>(X + at512(x0 + g, c) + 8 * t);
-    const float2 xb = *reinterpret_cast<const float2*>(X + at512(x0 + g + 8, c) + 8 * t);
-    const float2 y = *reinterpret_cast<const float2*>(Y + at512(y0 + g, c) + 8 * t);
-    const uint32_t qa = *reinterpret_cast<const uint32_t*>(Q + at256(x0 + g, c) + 4 * t);
-    const uint32_t qb = *reinterpret_cast<const uint32_t*>(Q + at256(x0 + g + 8, c) + 4 * t);
+    const int piece = c ^ g;
+    const float2 xa = *reinterpret_cast<const float2*>(X + 32 * piece);
+    const float2 xb = *reinterpret_cast<const float2*>(X + 32 * piece + 8 * 512);
+    const float2 y = *reinterpret_cast<const float2*>(Y + 32 * piece);
+    const uint32_t qa = *reinterpret_cast<const uint32_t*>(Q + 16 * piece);
+    const uint32_t qb = *reinterpret_cast<const uint32_t*>(Q + 16 * piece + 8 * 256);
     uint32_t xh[4], xl[4], yh[2], yl[2];
     split_tf32(xa.x, xh[0], xl[0]), split_tf32(xb.x, xh[1], xl[1]), split_tf32(xa.y, xh[2], xl[2]), split_tf32(xb.y, xh[3], xl[3]);
     split_tf32(y.x, yh[0], yl[0]), split_tf32(y.y, yh[1], yl[1]);
@@ -419,12 +421,17 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     if (j < i) A[i * kLdA + j] = kk * beta[i];
     if (j <= i) *reinterpret_cast<__half*>(smem + kPB + swz128((uint32_t)(i * 128 + j * 2))) = __float2half_rn(qk * sc_b);
   };
+  // a tile's lane has two neighbours of rows g and g + 8; above the diagonal there are zeros
   auto put_tile = [&](int i0, int j0, const float (&kk)[4], const float (&qk)[4]) {
-    const int i = i0 + (lane >> 2), j = j0 + 2 * (lane & 3);
-    put(i, j, kk[0], qk[0]);
-    put(i, j + 1, kk[1], qk[1]);
-    put(i + 8, j, kk[2], qk[2]);
-    put(i + 8, j + 1, kk[3], qk[3]);
+    const int j = j0 + 2 * (lane & 3);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = i0 + (lane >> 2) + 8 * e;
+      const float b = beta[i];
+      *reinterpret_cast<float2*>(A + i * kLdA + j) = make_float2(j < i ? kk[2 * e] * b : 0.f, j + 1 < i ? kk[2 * e + 1] * b : 0.f);
+      *reinterpret_cast<uint32_t*>(smem + kPB + swz128((uint32_t)(i * 128 + j * 2))) =
+          f16x2(j <= i ? qk[2 * e] * sc_b : 0.f, j + 1 <= i ? qk[2 * e + 1] * sc_b : 0.f);
+    }
   };
   {
     const int D = warp >> 1;
