@@ -110,6 +110,7 @@ constexpr int kPrepThreads = 256;
 constexpr int kPX = 0;                            // X = k L c, fp32: 64 rows x 512 bytes
 constexpr int kPQ = kPX + kChunk * 512;           // q L c, bf16: 64 rows x 256 bytes
 constexpr int kPY = kPQ + kChunk * 256;           // Y, fp32
+constexpr int kPartHalf = kChunk * 256;           // X and Y as two fp16 parts, one behind the other
 constexpr int kLdA = kChunk + 4;                  // floats: rows start four banks apart
 constexpr int kPA = kPY + kChunk * 512;           // A, then (I + A)^-1, fp32 [64][68]
 constexpr int kPB = kPA + kChunk * kLdA * 4;    // B, fp16, the record's image
@@ -169,6 +170,50 @@ __device__ __forceinline__ void tile_xy(const uint8_t* smem, int x0, int y0, flo
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) kk[i] += lh[i] + hl[i], qk[i] += ql[i];
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// 16 x 16 of X Y^T from fp16 parts, X and Y as [2 parts][64][128], queries [64][128]: for two different blocks.
+__device__ __forceinline__ void tile_parts(uint32_t sm, int x0, int y0, float (&kk)[2][4], float (&qk)[2][4]) {
+  const int lane = threadIdx.x & 31, r = lane & 7;
+  const uint32_t X = sm + kPX + (x0 + (lane & 15)) * 256, Y = sm + kPY + (lane >> 4) * kPartHalf + (y0 + r) * 256;
+  const uint32_t px = (uint32_t)((r ^ (lane >> 4)) << 4), py = (uint32_t)((r ^ ((lane >> 3) & 1)) << 4);
+  float kl[2][4], ql[2][4];   // products with a low part
+#pragma unroll
+  for (int i = 0; i < 8; ++i) kk[i >> 2][i & 3] = qk[i >> 2][i & 3] = kl[i >> 2][i & 3] = ql[i >> 2][i & 3] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < 8; ++c) {
+    uint32_t xh[4], xl[4], q[4], y[2][4];   // y: two pieces of the high part, two of the low one
+    const uint32_t ax = X + (px ^ (c << 5)), ay = Y + (py ^ (c << 5));
+    load_matrices(xh, ax);
+    load_matrices(xl, ax + kPartHalf);
+    load_matrices(q, ax + (kPQ - kPX));
+    load_matrices(y[0], ay);
+    load_matrices(y[1], ay + 8 * 256);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mma_16x8x16(kl[e], xl, y[e][0], y[e][1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mma_16x8x16(kk[e], xh, y[e][0], y[e][1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mma_16x8x16(ql[e], q, y[e][2], y[e][3]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mma_16x8x16(qk[e], q, y[e][0], y[e][1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mma_16x8x16(kl[e], xh, y[e][2], y[e][3]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) kk[i >> 2][i & 3] += kl[i >> 2][i & 3], qk[i >> 2][i & 3] += ql[i >> 2][i & 3];
 }
 
 // A 16 x 8 tile of sign * L R for fp32 matrices in shared memory: L's 16 rows, K columns; R's K
@@ -360,10 +405,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     const float2 v = block_of(b);
     return pack2(centre1(v.x), centre1(v.y));
   };
-  auto uncentre = [&](int b) {
-    const float2 v = centre(b);
-    return pack2(pow2_inverse(v.x), pow2_inverse(v.y));
-  };
   // image offsets of channel pair q2 in rows of 128 bytes, 64 channels a block
   const uint32_t img = (uint32_t)((q2 >> 5) * kTileHalf + (q2 & 31) * 4);
   const uint32_t piece = (uint32_t)(q2 >> 2), in_piece = (uint32_t)(q2 & 3) * 4;
@@ -469,26 +510,54 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     }
   }
   __syncthreads();
-  // ---- between the blocks: columns 0..47 of rows 48..63, then those of rows 32..47 and 16..31
+  // ---- between the blocks.  Rows 32..63 meet columns 0..31 at the start of row 32, rows 48..63 meet 32..47 at that of
+  // row 48, rows 16..31 meet 0..15 at that of row 16: decays up to there in Y, from there in X
   // Y at rows y0 .. + 15: k times the decay to the block's end, times l
   auto put_y = [&](int y0, f32x2 l) {
+    l = mul2(l, pack2(sc_k, sc_k));
 #pragma unroll
     for (int t = 15; t >= 0; --t) {
-      *reinterpret_cast<f32x2*>(smem + kPY + at512(y0 + t, piece) + 2 * in_piece) = mul2(bf16x2_to_f32x2(kr[t]), l);
+      uint32_t hi2, lo2;
+      split_f16(mul2(bf16x2_to_f32x2(kr[t]), l), hi2, lo2);
+      uint8_t* to = smem + kPY + at256(y0 + t, piece) + in_piece;
+      *reinterpret_cast<uint32_t*>(to) = hi2;
+      *reinterpret_cast<uint32_t*>(to + kPartHalf) = lo2;
       l = mul2(l, a[t]);
     }
   };
-  if (I < 3) {
-    f32x2 l = uncentre(3);
-    if (I < 2) l = mul2(l, block_of(2));
-    if (I < 1) l = mul2(l, block_of(1));
-    put_y(16 * I, l);
-  }
+  // X at rows x0 .. + 15: k and q times l and the decays from the block's start
+  auto put_x = [&](int x0, f32x2 l) {
+    const float sq = sc_q * scale;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      l = mul2(l, a[t]);
+      uint32_t hi2, lo2;
+      split_f16(mul2(bf16x2_to_f32x2(kr[t]), mul2(l, pack2(sc_k, sc_k))), hi2, lo2);
+      const f32x2 xq = mul2(bf16x2_to_f32x2(qr[t]), mul2(l, pack2(sq, sq)));
+      const uint32_t o = at256(x0 + t, piece) + in_piece;
+      *reinterpret_cast<uint32_t*>(smem + kPX + o) = hi2;
+      *reinterpret_cast<uint32_t*>(smem + kPX + kPartHalf + o) = lo2;
+      *reinterpret_cast<uint32_t*>(smem + kPQ + o) = f16x2(xq.x, xq.y);
+    }
+  };
+  // two pieces of work for every thread; X's free rows 0..15 hold rows 48..63 once more
+#pragma unroll 1
+  for (int e = 0; e < (I == 3 ? 2 : I > 0); ++e) put_x(e ? 0 : 16 * I, e ? block_of(2) : one);
+#pragma unroll 1
+  for (int e = 0; e < (I == 0 ? 2 : I < 3); ++e) put_y(e ? 48 : 16 * I, I == 0 && e == 0 ? block_of(1) : one);
   __syncthreads();
   if (warp < 6) {
-    float kk[4], qk[4];
-    tile_xy(smem, 48, 8 * warp, kk, qk);
-    put_tile(48, 8 * warp, kk, qk);
+    // blocks (1, 0), (2, 0), (2, 1), (3, 0), (3, 1), (3, 2)
+    const int bi = warp == 0 ? 1 : warp < 3 ? 2 : 3, bj = warp == 0 ? 0 : warp < 3 ? warp - 1 : warp - 3;
+    float kk[2][4], qk[2][4];
+    tile_parts(sm, warp == 3 || warp == 4 ? 0 : 16 * bi, warp == 0 ? 48 : 16 * bj, kk, qk);
+    const float ik = pow2_inverse(sc_k), iq = pow2_inverse(sc_q);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kk[e][i] = kk[e][i] * ik * ik, qk[e][i] = qk[e][i] * ik * iq;   // (ik * ik may leave fp32's range)
+      put_tile(16 * bi, 16 * bj + 8 * e, kk[e], qk[e]);
+    }
   }
   // meanwhile the inverses of I + A's diagonal blocks, in their place, by substitution: a thread a column
   if (warp >= 6) {
@@ -513,17 +582,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     for (int i = 0; i < 16; ++i) D[i * kLdA + j] = t[i];
   }
   __syncthreads();
-  if (I < 2) put_y(16 * I, I == 0 ? mul2(uncentre(2), block_of(1)) : uncentre(2));   // for rows 32..47
-  if (I == 0) put_y(32, uncentre(1));
-  __syncthreads();
-  if (warp < 6) {
-    float kk[4], qk[4];
-    const int x0 = warp < 4 ? 32 : 16, y0 = warp < 4 ? 8 * warp : 32 + 8 * (warp - 4), j0 = warp < 4 ? y0 : y0 - 32;
-    tile_xy(smem, x0, y0, kk, qk);
-    put_tile(x0, j0, kk, qk);
-  }
-  __syncthreads();
-
   // ---- (I + A)^-1, in A's place: from its diagonal blocks twice [[T1, 0], [-T2 A21 T1, T2]], of 16 and of 32 rows
   float* tmp = reinterpret_cast<float*>(smem + kPX);   // [32][36]
   constexpr int kLdT = 36;
