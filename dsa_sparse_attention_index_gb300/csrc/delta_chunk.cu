@@ -118,7 +118,7 @@ constexpr int kPTab = kPB + kTileHalf;            // block products [4][128]
 constexpr int kPSum = kPTab + 4 * kDeltaDim * 4;  // sums of their logarithms
 constexpr int kPBeta = kPSum + 4 * kDeltaDim * 4;
 constexpr int kPMisc = kPBeta + kChunk * 4;
-constexpr int kPrepSmem = kPMisc + 128;
+constexpr int kPrepSmem = kPMisc + 256;
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
 // Offset of eight channels c of row r in rows of 512 bytes of fp32 and of 256 bytes of
@@ -245,6 +245,12 @@ __device__ __forceinline__ float max_warp(float v) {  // of values >= 0
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // no number if one of them is none
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // First row and number of rows of record number `slot`'s chunk: of the last long sequence with no more chunks before it.
 __device__ __forceinline__ bool chunk_rows(const ChunkArgs& p, int slot, int64_t* row0, int* n) {
   int at = 0, end = p.s.index[0].x;
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
   float* beta = reinterpret_cast<float*>(smem + kPBeta);
-  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: largest |k|, |q|, growth; unsafe lanes
+  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: largest |k|, |q|, growth; unsafe lanes; largest |beta|, |T|
   float* A = reinterpret_cast<float*>(smem + kPA);
   bool bad = false;
 
@@ -335,6 +341,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     const float bt = tid < n ? __ldg(x.beta + (row0 + tid) * x.ld_beta + h) : 0.f;
     beta[tid] = bt;
     bad = !(fabsf(bt) <= 3.4e38f);
+    const float mb = max_warp(bad ? 0.f : fabsf(bt));
+    if (lane == 0) misc[32 + warp] = mb;
   }
   const f32x2 one = pack2(1.f, 1.f);
   f32x2 block = one, sum = make_float2(0.f, 0.f);
@@ -387,6 +395,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   const float sc_k = pow2_scale(mk * mg, 14);                        // of K P and K D
   const float sc_q = pow2_scale(mq * mg * fabsf(scale), 14);
   const float sc_b = pow2_scale(mq * mk * mg * fabsf(scale) * 128.f, 14);
+  // of T, whose diagonal is beta: room for 2^11 times its largest; the parts' last bit is 2^-27 of that
+  const float sc_t = pow2_scale(fmaxf(misc[32], misc[33]), 3);
 
   // ---- decays by channel, forward: K P, Q P, X
   auto block_of = [&](int b) { return *reinterpret_cast<const f32x2*>(tab + b * kDeltaDim + 2 * q2); };
@@ -588,6 +598,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   if (warp < 4) {
     const int d = 32 * (warp >> 1), cc = 8 * (warp & 1);
     mul_tile<16>(A + (d + 16) * kLdA + d, kLdA, A + d * kLdA + d + cc, kLdA, tmp + (d >> 1) * kLdT + cc, kLdT, 1.f);
+  } else {
+#pragma unroll
+    for (int q = tid - 128; q < kTileHalf / 16; q += 128)
+      reinterpret_cast<uint4*>(rec + kRecB)[q] = reinterpret_cast<const uint4*>(smem + kPB)[q];
   }
   __syncthreads();
   if (warp < 4) {
@@ -613,18 +627,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       t[j] = r.x * bj.x, t[j + 1] = r.y * bj.y, t[j + 2] = r.z * bj.z, t[j + 3] = r.w * bj.w;
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      bad |= t[j] != t[j];
-      m = fmaxf(m, fabsf(t[j]));
-    }
-    bad |= !(m <= 1e12f);   // keys much longer than one: the rows go one by one
+    for (int j = 0; j < 16; ++j) m = max_nan(m, fabsf(t[j]));
+    bad |= !(m * sc_t <= 32768.f);   // no number, or keys much longer than one: the rows go one by one
     m = max_warp(bad ? 0.f : m);
-    if (lane == 0) misc[warp] = m;
-    __syncthreads();
-    float mt = misc[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) mt = fmaxf(mt, misc[w]);
-    const float sc_t = pow2_scale(mt, 14);
+    if (lane == 0) misc[40 + warp] = m;
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) split_f16(mul2(pack2(t[2 * j], t[2 * j + 1]), pack2(sc_t, sc_t)), hi[j], lo[j]);
@@ -634,18 +640,19 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       *reinterpret_cast<uint4*>(rec + kRecT + o) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
       *reinterpret_cast<uint4*>(rec + kRecT + kTileHalf + o) = make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
     }
-    if (tid == 0) {
-      float* hd = reinterpret_cast<float*>(rec + kRecHead);
-      hd[kHdInvKp] = pow2_inverse(sc_k), hd[kHdInvQp] = pow2_inverse(sc_q), hd[kHdInvT] = pow2_inverse(sc_t);
-      hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvKd] = pow2_inverse(sc_k);
-      // sums of a row's or a column's magnitudes, from above
-      hd[kHdSumKp] = 128.f * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg, hd[kHdMaxP] = mg;
-    }
-    for (int q = tid; q < kTileHalf / 16; q += kPrepThreads)
-      reinterpret_cast<uint4*>(rec + kRecB)[q] = reinterpret_cast<const uint4*>(smem + kPB)[q];
   }
   const int any = __syncthreads_or(bad);
-  if (tid == 0) reinterpret_cast<int*>(rec + kRecHead)[kHdBad] = any;
+  if (tid == 0) {
+    float mt = misc[40];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) mt = fmaxf(mt, misc[40 + w]);
+    float* hd = reinterpret_cast<float*>(rec + kRecHead);
+    reinterpret_cast<int*>(hd)[kHdBad] = any;
+    hd[kHdInvKp] = pow2_inverse(sc_k), hd[kHdInvQp] = pow2_inverse(sc_q), hd[kHdInvT] = pow2_inverse(sc_t);
+    hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvKd] = pow2_inverse(sc_k);
+    // sums of a row's or a column's magnitudes, from above
+    hd[kHdSumKp] = 128.f * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg, hd[kHdMaxP] = mg;
+  }
 }
 
 // ---------------------------------------------------------------- chain
