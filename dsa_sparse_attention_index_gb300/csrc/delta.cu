@@ -81,7 +81,8 @@ __device__ __forceinline__ void list_long(const DeltaSeqs& s) {
     // starts that do not ascend can make more long sequences than there are rows for
     if (c > 0 && at < s.many) s.index[1 + at] = make_int4(r0, n, chunks + before - c, b);
     found += __popc(any);
-    chunks += __shfl_sync(0xffffffffu, before, 31);
+    // (overlapping ones could also count past 32 bits; there is no room for any that begin so far behind)
+    chunks = min(chunks + __shfl_sync(0xffffffffu, before, 31), 1 << 30);
   }
   if (lane == 0) s.index[0].x = min(found, s.many);
 }

@@ -289,6 +289,21 @@ def test_bad_slots_and_starts_are_reported():
     assert st.item() == B.ERR_BOUNDS
 
 
+def test_overlapping_sequences_whose_chunks_exceed_32_bits_are_reported():
+    rows, batch = 1_800_000, 154_000    # every other sequence has all rows: 77,000 x 28,125 chunks > 2^31
+    x = [torch.zeros((rows, 1, DIM), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    x += [torch.zeros((rows, 1), device="cuda"), torch.zeros((rows, 1), device="cuda")]
+    pool, st = pool_of(2, 1), status()
+    before = pool.clone()
+    starts = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    starts[1::2] = rows
+    none = torch.full((batch,), -1, dtype=torch.int32, device="cuda")
+    out = torch.ones((rows, 1, DIM), dtype=torch.bfloat16, device="cuda")
+    prefill(pool, x, starts, none, none, out, st)
+    assert st.item() == B.ERR_BOUNDS
+    assert torch.equal(pool, before) and (out == 0).all()
+
+
 def test_side_stream_and_graph():
     """A prompt and the next token of two sequences, eagerly on a side stream, then captured and replayed over other
     workspace contents: the same bits."""
