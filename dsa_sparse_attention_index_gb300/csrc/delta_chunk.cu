@@ -11,8 +11,8 @@
 // Two kernels.  delta_prepare_kernel: everything that does not depend on the
 // state, a CTA per chunk and head, into a record of operands laid out as the tensor
 // core reads them.  delta_chain_kernel: a CTA per sequence and head walks the
-// chunks; the state stays in registers in fp32.  2,048 rows of 96 heads: 183 us and
-// 135 us (row by row 5,478 us).
+// chunks; the state stays in registers in fp32.  2,048 rows of 96 heads: 168 us and
+// 134 us (row by row 5,478 us).
 #include <algorithm>
 #include <atomic>
 
@@ -97,15 +97,19 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 //                        start, c a power of two that centres them by channel: what a pair
 //                        gets is a quotient of products of 16 factors at most.  A block whose
 //                        decays leave 2^-120 .. 2^10 is computed pair by pair instead.
-//   between two blocks   Y_j = k_j times the decays from row j to the start of X's block, all
-//                        products of factors: nothing underflows that should not
-// The factors are fp32, cut into two tf32 on the way into the mma: three products, 21
-// bits.  (Two bf16 parts were 6 % faster and left states 7 to 10e-7 off instead of 4
-// to 5e-7.)  The inverse of I + A goes by blocks: the diagonal ones by substitution, a
-// thread a column, while other warps still make tiles, then two levels of products.
-// What bounds it: 36,770 warp instructions a chunk and head at 2.2 a cycle; its
-// memory traffic could go at twice the rate.  16 warps an SM, as registers and
-// shared memory allow; 512 threads a CTA or 16-byte pieces a thread were slower.
+//   between two blocks   Y_j = k_j times the decays from row j to an anchor, X_i = k_i times those from there, all
+//                        products of factors: nothing underflows that should not.  Three anchors
+//                        (the starts of rows 16, 32 and 48) let X and Y stand in shared memory at once.
+// Within a block the factors are fp32, since a quotient's factors may be large, cut into two tf32 on
+// the way into the mma; between blocks they are two fp16 times a power of two, made once.
+// Three products either way, 21 bits.  (Two bf16 parts everywhere left states 7 to 10e-7
+// off instead of 4 to 5e-7; tf32 everywhere took 5 % longer.)  The inverse of I + A goes by
+// blocks: the diagonal ones by substitution, a thread a column, while other warps make
+// tiles, then two levels of products.
+// What bounds it: 33,200 warp instructions a chunk and head at 2.0 a cycle, nine phases that wait for
+// each other's warps; its memory traffic could go at twice the rate.  16 warps an SM, as registers and
+// shared memory allow; 512 threads a CTA or 16-byte pieces a thread were slower, and
+// so was K D made by the warps that the inverse leaves idle (312 us for 302 in all).
 constexpr int kPrepThreads = 256;
 constexpr int kPX = 0;                            // X = k L c, fp32: 64 rows x 512 bytes
 constexpr int kPQ = kPX + kChunk * 512;           // q L c, bf16: 64 rows x 256 bytes
