@@ -612,7 +612,7 @@ dsa_status_t gated_delta_decode(const dsa_state_pool_t* pool, const dsa_delta_ro
   const dsa_status_t s = check_delta(pool, x, (int64_t)batch * queries_per_seq, batch, slots_in, slots_out, out);
   if (s != DSA_OK || batch == 0) return s;
   const DeltaSeqs seqs{static_cast<float*>(pool->base), pool->slot_stride / 4, pool->num_slots, batch,
-                       batch * queries_per_seq, queries_per_seq, nullptr, slots_in, slots_out, 1, dev_status, nullptr, 0};
+                       batch * queries_per_seq, queries_per_seq, nullptr, slots_in, slots_out, dev_status, nullptr, 0};
   return launch_delta_rows(delta_rows(*pool, *x), seqs, out, static_cast<cudaStream_t>(stream));
 }
 
@@ -633,7 +633,7 @@ dsa_status_t gated_delta_prefill(const dsa_state_pool_t* pool, const dsa_delta_r
       workspace_bytes < gated_delta_prefill_workspace_size(rows, batch, pool->heads))
     return DSA_ERR_WORKSPACE;
   const DeltaSeqs seqs{static_cast<float*>(pool->base), pool->slot_stride / 4, pool->num_slots, batch, rows, 0,
-                       row_starts, slots_in, slots_out, 0, dev_status, nullptr, 0};
+                       row_starts, slots_in, slots_out, dev_status, nullptr, 0};
   return launch_delta_chunks(delta_rows(*pool, *x), seqs, out, workspace, static_cast<cudaStream_t>(stream));
 }
 

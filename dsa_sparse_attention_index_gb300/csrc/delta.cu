@@ -120,25 +120,30 @@ __device__ __forceinline__ void list_long(const DeltaSeqs& s) {
 // of them; eight lanes share a row (16 keys each), so a product with the keys takes
 // three shuffles.  Bound by the states' bytes: with 64 registers of state a thread
 // and three CTAs an SM, 96 KB are on their way.  32 sequences x 96 heads read and
-// write 0.41 GB in 62.6 us (6.5 TB/s, 0.96 of the measured copy); two CTAs an SM
+// write 0.41 GB in 61.4 us (6.6 TB/s, 0.97 of the measured copy); two CTAs an SM
 // take 72, two rows a thread and five CTAs 67, one row a thread 90.  Few heads are
-// no faster in smaller parts (32 heads: 3.4 us either way).
+// no faster in smaller parts (32 heads: 3.2 us).  Prompt calls have an instance of their own:
+// with their ranges and list in it decode takes 168 registers for 152, and 1 to 8 % longer.
+template <bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows x, const DeltaSeqs s, uint16_t* out) {
-  if (s.index) {
-    if (blockIdx.x == 0) {   // first, so that it is done before the others
-      if (threadIdx.x < 32) list_long(s);
-      return;
-    }
+  const bool lists = PROMPT && s.index;
+  if (lists && blockIdx.x == 0) {   // first, so that it is done before the others
+    if (threadIdx.x < 32) list_long(s);
+    return;
   }
-  const int cta = (int)blockIdx.x - (s.index ? 1 : 0), part = cta % kSplit, bh = cta / kSplit;
+  const int cta = (int)blockIdx.x - (lists ? 1 : 0), part = cta % kSplit, bh = cta / kSplit;
   const int h = bh % x.heads, b = bh / x.heads, hq = h / (x.heads / x.qk_heads);
   const int lane = threadIdx.x & 31, l = lane & 7;
   const int vrow = part * kCtaRows + (threadIdx.x >> 5) * 4 * R + (lane >> 3);  // this thread's rows: vrow + 4 r
   const int64_t at = (int64_t)vrow * kDeltaDim + 4 * l;
   int64_t row;
   int n;
-  if (!seq_rows(s, b, &row, &n)) return;
-  if (s.starts && n > kFewRows) return;
+  if (PROMPT) {
+    if (!seq_rows(s, b, &row, &n)) return;
+  } else {
+    row = (int64_t)b * s.nq, n = s.nq;
+  }
+  if (PROMPT && n > kFewRows) return;
 
   float4 S[R][4];
   const float* in = state_in(s, b, h);
@@ -195,10 +200,10 @@ __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows
         S[r][i].z = fmaf(u[r], k.z, S[r][i].z), S[r][i].w = fmaf(u[r], k.w, S[r][i].w);
       }
     }
-    if (s.per_row || t == n - 1)
+    if (!PROMPT || t == n - 1)
       if (float* to = state_out(s, b, t, h)) store(to);
   }
-  if (n == 0 && !s.per_row)   // a sequence without rows hands its state on
+  if (PROMPT && n == 0)   // a sequence without rows hands its state on
     if (float* to = state_out(s, b, 0, h)) store(to);
 }
 
@@ -206,7 +211,11 @@ __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows
 
 dsa_status_t launch_delta_rows(const DeltaRows& x, const DeltaSeqs& s, uint16_t* out, cudaStream_t st) {
   const int64_t ctas = (int64_t)s.batch * x.heads * kSplit + (s.index ? 1 : 0);
-  delta_rows_kernel<<<(unsigned)ctas, kThreads, 0, st>>>(x, s, out);
+  if (s.starts) {
+    delta_rows_kernel<true><<<(unsigned)ctas, kThreads, 0, st>>>(x, s, out);
+  } else {
+    delta_rows_kernel<false><<<(unsigned)ctas, kThreads, 0, st>>>(x, s, out);
+  }
   count_launches(1);
   return launch_status();
 }

@@ -31,8 +31,7 @@ struct DeltaSeqs {
   int32_t num_slots;
   int32_t batch, rows, nq;
   const int32_t* starts;
-  const int32_t *slots_in, *slots_out;
-  int32_t per_row;          // slots_out [batch][nq], a state after each row; else [batch], the last one
+  const int32_t *slots_in, *slots_out;   // out: [batch][nq], a state after each row; with starts [batch], the last one
   int32_t* status;
   // Prompt calls: the sequences of more than kFewRows rows, of which there can be `many`: their number in the first
   // entry, then for each its first row, its rows, the chunks of 64 rows of those before it, and its index.
@@ -40,13 +39,9 @@ struct DeltaSeqs {
   int32_t many;
 };
 
-// First row and number of rows of sequence b; false where starts is not
+// First row and number of rows of a prompt call's sequence b; false where starts is not
 // ascending within 0..rows (such a sequence is left out).
 __device__ __forceinline__ bool seq_rows(const DeltaSeqs& s, int b, int64_t* row, int* n) {
-  if (!s.starts) {
-    *row = (int64_t)b * s.nq, *n = s.nq;
-    return true;
-  }
   const int r0 = s.starts[b], r1 = s.starts[b + 1];
   if (r0 < 0 || r1 < r0 || r1 > s.rows) {
     if (threadIdx.x == 0) report(s.status, DSA_ERR_BOUNDS);
@@ -69,7 +64,7 @@ __device__ __forceinline__ const float* state_in(const DeltaSeqs& s, int b, int 
 
 // Where the state after row t goes; null: nowhere.
 __device__ __forceinline__ float* state_out(const DeltaSeqs& s, int b, int t, int h) {
-  const int slot = s.slots_out[s.per_row ? b * s.nq + t : b];
+  const int slot = s.slots_out[s.starts ? b : b * s.nq + t];
   if (slot == -1) return nullptr;
   if (slot < 0 || slot >= s.num_slots) {
     if (threadIdx.x == 0) report(s.status, DSA_ERR_BOUNDS);
