@@ -36,7 +36,7 @@ constexpr int kRecHead = kRecKd + 2 * kTileBytes;      // 106,496
 constexpr int kRecBytes = kRecHead + 1024;
 constexpr int kPart1 = kRecB, kPart2 = kRecHead - kRecB;   // what is read first, and last
 // floats of the record's head
-enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvT, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdMaxP, kHdP = 16 };
+enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvT, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16 };
 constexpr int kHeadBytes = 4 * (kHdP + kDeltaDim);
 
 struct ChunkArgs {
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     hd[kHdInvKp] = pow2_inverse(sc_k), hd[kHdInvQp] = pow2_inverse(sc_q), hd[kHdInvT] = pow2_inverse(sc_t);
     hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvKd] = pow2_inverse(sc_k);
     // sums of a row's or a column's magnitudes, from above
-    hd[kHdSumKp] = 128.f * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg, hd[kHdMaxP] = mg;
+    hd[kHdSumKp] = 128.f * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg;
   }
 }
 
@@ -668,10 +668,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 //   U^T = R^T T^T                  A = R in two parts
 //   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
 //   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
-// The parts of a row of S, R or U are times a power of two from a bound of it, so
-// that they keep 21 bits of its largest element whatever its size.  The bounds come
-// from maxima that the two warps of a row exchange one step later, so they may be
-// loose: fp16's exponents leave room for 2^18.
+// The parts of a row of S, R or U are times a power of two, so that they keep 21 bits of
+// its largest element whatever its size: of S from the row's largest element itself, which the
+// two warps of a row exchange before they split it (a bound carried from chunk to chunk would
+// not see a state decay, and its parts would be lost: 0 to 2 % of a call); of R and U from bounds made of maxima
+// that they exchange one step later, which may be loose: fp16's exponents leave room for 2^18.
 // Where something in a chunk is no finite number, or leaves the powers' range, its rows
 // go one by one: the zeros of T and B would carry a NaN to the rows before it.
 // What bounds it: a chain of latencies, 7,700 cycles a chunk, of which the tensor pipe
@@ -692,13 +693,15 @@ constexpr int kCOffPart2 = 2 * kPart1;                  // one buffer: its produ
 constexpr int kCOffV = kCOffPart2 + kPart2;
 constexpr int kCOffOut = kCOffV + 2 * kChunk * kRowBytes;
 constexpr int kCOffHead = kCOffOut + kChunk * kRowBytes;
-constexpr int kCOffX = kCOffHead + 2 * 640;             // exchanged maxima [2 parities][4 kinds][2 halves][128]
-constexpr int kCOffBars = kCOffX + 2 * 4 * 2 * 128 * 4;
+constexpr int kCOffX = kCOffHead + 2 * 640;             // exchanged maxima [2 parities][3 kinds][2 halves][128]
+constexpr int kCOffBars = kCOffX + 2 * 3 * 2 * 128 * 4;
 constexpr int kCNumBars = 21;
 constexpr int kCOffMisc = kCOffBars + kCNumBars * 8;
 constexpr int kChainSmem = 1024 + kCOffMisc + 40;
 static_assert(kChainSmem <= 232448 && kPart1 % 1024 == 0 && kPart2 % 1024 == 0 && kHeadBytes <= 640, "shared memory");
 
+// The two warps that share 32 value rows of the state.
+__device__ __forceinline__ void bar_pair(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory"); }
 __device__ __forceinline__ void bar_state() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool bar_state_or(bool v) {
   uint32_t r;
@@ -925,8 +928,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
     const int half = warp >> 2, v = 32 * (warp & 3) + lane, tid = threadIdx.x;
     const uint32_t quad = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float* ex = reinterpret_cast<float*>(smem + kCOffX);
-    auto xchg = [&](int parity, int kind, int hf) -> float& { return ex[((parity * 4 + kind) * 2 + hf) * 128 + v]; };
-    enum { kMaxS, kMaxV, kMaxR, kMaxU };
+    auto xchg = [&](int parity, int kind, int hf) -> float& { return ex[((parity * 3 + kind) * 2 + hf) * 128 + v]; };
+    enum { kMaxS, kMaxV, kMaxR };
     float S[64];
     {
       const float* in = state_in(p.s, b, h);
@@ -937,29 +940,25 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         S[4 * i] = t.x, S[4 * i + 1] = t.y, S[4 * i + 2] = t.z, S[4 * i + 3] = t.w;
       }
     }
-    auto own_max = [&]() {
+    float sc_s = 1.f;     // what the row of the state in registers is times
+    float bound_s = 0.f;  // the row's largest element
+    auto measure = [&](int parity) {
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(S[i]));
-      return m;
-    };
-    xchg(1, kMaxS, half) = own_max();
-    bar_state();
-    float bound_s = fmaxf(xchg(1, kMaxS, 0), xchg(1, kMaxS, 1));
-    float sc_s = 1.f;   // what the row of the state in registers is times
-    auto rescale = [&]() {
-      // another power of two only where the bound has left [2^4, 2^15): a row keeps 21 bits of its largest element
-      // down to a bound 2^10 above it.  The bound holds for the state before and behind a chunk, so neither overflows.
-      const float b = bound_s * sc_s;
-      const bool moved = !(b >= 16.f && b < 32768.f) && !(bound_s == 0.f && sc_s == 1.f);
+      for (int i = 0; i < 64; i += 2) m = fmaxf(fmaxf(m, fabsf(S[i])), fabsf(S[i + 1]));
+      xchg(parity, kMaxS, half) = m;
+      bar_pair(warp & 3);
+      m = fmaxf(xchg(parity, kMaxS, 0), xchg(parity, kMaxS, 1));
+      bound_s = m * pow2_inverse(sc_s);
+      // another power of two only where the largest element has left [2^4, 2^15): 21 bits of it down to 2^4
+      const bool moved = m > 0.f && !(m >= 16.f && m < 32768.f);
       if (__any_sync(0xffffffffu, moved)) {
-        const float to = !moved ? sc_s : bound_s == 0.f ? 1.f : pow2_scale(bound_s, 12), by = to * pow2_inverse(sc_s);
+        const float by = moved ? fminf(pow2_scale(bound_s, 12) * pow2_inverse(sc_s), 0x1p126f) : 1.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) S[i] *= by;
-        sc_s = to;
+        sc_s *= by;
       }
     };
-    rescale();
     uint32_t f = 0;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       mbar_wait_warp(bar, parity, abort_flag, p.s.status);
@@ -1035,20 +1034,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       const int rows = min(kChunk, n - c * kChunk);
       const float* hd = reinterpret_cast<const float*>(smem + kCOffHead + s * 640);
       // ---- the state's parts; the outputs' products, which read the last ones, are through
+      measure(s);
       if (out_rows > 0) wait(b_o, (f - 1) & 1);
-      uint32_t top = 0u;   // the largest high part: the state's largest value is within 2^-10 of it
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) split_f16(pack2(S[32 * g + 2 * i], S[32 * g + 2 * i + 1]), hi[i], lo[i]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max_abs_f16x2(top, hi[i]);
         tmem_st16(quad + kColS + 64 * half + 16 * g, hi);
         tmem_st16(quad + kColS + 64 * half + 32 + 16 * g, lo);
-      }
-      {
-        xchg(s, kMaxS, half) = max_of_f16x2(top) * pow2_inverse(sc_s) * 1.001f;
       }
       tmem_st_wait();
       arrive(b_s);
@@ -1095,13 +1089,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
           for (int i = 0; i < 64; ++i) S[i] = fmaf(u, r[64 * half + i], S[i]);
         }
         bar_state();
-        xchg(s, kMaxS, half) = own_max();
         fence_proxy_async_smem();   // copies write there again
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(s));
-        bar_state();
-        bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1));
-        rescale();
         if (c + 1 < chunks) {
           read_v(c + 1);
           rowwise = vote(c + 1);
@@ -1140,29 +1130,32 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         uint32_t acc[32], hi[16], lo[16];
         tmem_ld32(quad + kColAcc + 32 * half, acc);
         tmem_ld_wait();
-        uint32_t top = 0u;
         const float f_u = inv_t * sc_u;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           split_f16(mul2(pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])), pack2(f_u, f_u)), hi[t], lo[t]);
-          top = max_abs_f16x2(top, hi[t]);
         }
         tmem_st16(quad + kColParts + 16 * half, hi);
         tmem_st16(quad + kColParts + 32 + 16 * half, lo);
-        xchg(s, kMaxU, half) = max_of_f16x2(top) * pow2_inverse(sc_u) * 1.001f;
         tmem_st_wait();
         arrive(b_up);
       }
       // ---- the state behind the chunk
-      const float inv_u = pow2_inverse(sc_u), sum_kd = hd[kHdSumKd], max_p = hd[kHdMaxP];
+      const float inv_u = pow2_inverse(sc_u);
       const float inv_o1 = inv_s * hd[kHdInvQp], inv_o2 = inv_u * hd[kHdInvB];
       if (c + 1 < chunks) {
         read_v(c + 1);
         rowwise = vote(c + 1);
       }
       wait(b_ds, f & 1);
-      bound_s = fmaxf(xchg(s, kMaxS, 0), xchg(s, kMaxS, 1)) * max_p + fmaxf(xchg(s, kMaxU, 0), xchg(s, kMaxU, 1)) * sum_kd;
-      rescale();
+      // a state that is nothing beside its update: in a smaller power of two, for the sum to stay in fp32's range
+      const float most = 32768.f * inv_u * hd[kHdSumKd];
+      if (__any_sync(0xffffffffu, most * sc_s > 0x1p100f)) {
+        const float to = most * sc_s > 0x1p100f ? pow2_scale(most, 12) : sc_s, by = to * pow2_inverse(sc_s);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) S[i] *= by;
+        sc_s = to;
+      }
       const float inv_kd = inv_u * hd[kHdInvKd] * sc_s;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {

@@ -1,0 +1,79 @@
+"""gated_delta_prefill where the numbers of a sequence differ widely in size."""
+import math
+
+import pytest
+import torch
+
+from dsa_sparse_attention_index_gb300 import binding as B
+from plain_delta import DIM, inputs, out_tolerance, rule, state_tolerance
+
+pytestmark = pytest.mark.gpu
+SCALE = DIM ** -0.5
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def state(heads, seed=1):
+    return 0.3 * torch.randn((1, heads, DIM, DIM), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def prefill(x, s0, scale=SCALE):
+    """(outputs, last state) of one sequence."""
+    rows, heads = x[2].shape[:2]
+    pool, out, st = torch.cat([s0, torch.zeros_like(s0)]), torch.zeros((rows, heads, DIM), dtype=torch.bfloat16, device="cuda"), ints(0)
+    ws = B.workspace(B.gated_delta_prefill_workspace_size(rows, 1, heads))
+    B.gated_delta_prefill(B.StatePool(pool), B.DeltaRows(*x, scale), ints(0, rows), ints(0), ints(1), out, ws, st)
+    assert st.item() == 0
+    return out, pool[1]
+
+
+def norms(s):
+    return s.double().flatten(1).norm(dim=1)
+
+
+# Six operands meet a state in 64 rows (S, K P, R, T, U, K D).  Each is two fp16 parts of 11 bits: what the second leaves is at
+# most 2^-22 of the number, and the product of two second parts, which is left out, at most 2^-20 of a product; counted together
+# as 2^-21 for each operand, relative to the state, since the updates (beta |k|^2 <= 1) and the decays do not enlarge it.
+BITS = 6 * 2.0 ** -21
+
+
+def check_bits(got, want, size):
+    off = norms(got.double() - want) / size
+    assert (off <= BITS).all(), off / BITS
+
+
+def check_out(out, want, rows, size, mass, q, scale=SCALE):
+    off, tol = (out.double() - want).abs(), out_tolerance(want, rows, size, mass, q, scale, True)
+    assert (off <= tol).all(), (off / tol).max()
+
+
+@pytest.mark.parametrize("gate,beta", [(-0.41, 1e-16), (-0.5, 0.5), (-1.2, 0.5), (-0.5, 1e-12)])
+def test_state_that_decayed_without_updates(gate, beta):
+    """64 rows take a state down by 2^-38 to 2^-111 and bring nothing; the next rows act on what is left of it."""
+    x, s0 = inputs(256, 2, 2, seed=43), state(2)
+    q, k, v, g, b = x
+    g[:64], g[64:] = gate, 0.0
+    b[:64], b[64:] = 0.0, beta
+    if beta > 1e-3:
+        v[64:] = 0.0                # beta erases
+    out, last = prefill(x, s0)
+    want, states, _, _ = rule(*x, SCALE, s0[0])
+    left = [norms(s) for s in states[63:]]
+    assert torch.isfinite(last).all() and torch.isfinite(out).all()
+    check_bits(last, states[-1], torch.stack(left).amax(0))
+    # outputs behind the decay, relative to what is left: half a bf16 step and the operands' 11 bits
+    tol = 2.0 ** -8 * want[64:].abs() + 2.0 ** -8 * SCALE * q[64:].double().norm(dim=2)[..., None] * torch.stack(left).amax(0)[None, :, None]
+    assert ((out[64:].double() - want[64:]).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-36, 0.0])
+def test_states_that_are_nothing_beside_their_updates(size):
+    x, s0 = inputs(200, 2, 2, seed=49), size * state(2)
+    x[2][:64] *= 1e-30
+    x[2][64:] *= 1e8
+    out, last = prefill(x, s0)
+    want, states, grown, mass = rule(*x, SCALE, s0[0])
+    check_bits(last, states[-1], grown)
+    check_out(out, want, 200, grown, mass, x[0])
