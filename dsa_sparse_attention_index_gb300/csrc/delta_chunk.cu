@@ -2,11 +2,15 @@
 //
 // For the rows i = 1..64 of a chunk behind the state S0, with P_i = prod_{s<=i}
 // a_s (a = exp(gate), by channel) and the decay D_ij = prod_{j<s<=i} a_s:
-//   A_ij = beta_i sum_d k_i k_j D_ij (j < i),   T = (I + A)^-1 diag(beta),
-//   R = V - (K P) S0^T,   U = T R,
+//   A_ij = beta_i sum_d k_i k_j D_ij (j < i),   T = (I + A)^-1,
+//   R = diag(beta) (V - (K P) S0^T),   U = T R,
 //   out = scale ((Q P) S0^T + B U),  B_ij = sum_d q_i k_j D_ij (j <= i),
 //   S = S0 diag(P_64) + U^T (K D_64)
 // which is the rule of delta.cu with its 64 steps solved as one triangular system.
+// It is the same rule for a key k / s with the value v / s and beta s^2, so every row
+// is taken with the power of two s that brings its key's largest element into [1, 2):
+// rows whose keys differ in length by any factor share the chunk's powers of two
+// without loss, and with beta in R, T's diagonal is one whatever beta is.
 //
 // Two kernels.  delta_prepare_kernel: everything that does not depend on the
 // state, a CTA per chunk and head, into a record of operands laid out as the tensor
@@ -26,7 +30,7 @@ namespace {
 
 constexpr int kTileHalf = kChunk * 128;                // 64 rows of 64 fp16 (128 bytes, 128-byte swizzle)
 constexpr int kTileBytes = 2 * kTileHalf;              // 64 rows x 128 channels
-// A record: K P (high and low parts), Q P, T (high and low), then B, K D (high and low), then the head's floats.
+// A record: beta K P (high and low parts), Q P, T (high and low), then B, K D (high and low), then the head's floats.
 constexpr int kRecKp = 0;
 constexpr int kRecQp = kRecKp + 2 * kTileBytes;
 constexpr int kRecT = kRecQp + kTileBytes;
@@ -36,8 +40,10 @@ constexpr int kRecHead = kRecKd + 2 * kTileBytes;      // 106,496
 constexpr int kRecBytes = kRecHead + 1024;
 constexpr int kPart1 = kRecB, kPart2 = kRecHead - kRecB;   // what is read first, and last
 // floats of the record's head
-enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvT, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16 };
-constexpr int kHeadBytes = 4 * (kHdP + kDeltaDim);
+enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16, kHdV = kHdP + kDeltaDim };
+constexpr int kHeadBytes = 4 * (kHdV + kChunk);   // (V: what a row's value is times)
+// T's power of two: its diagonal is one, so 2^11 of room above it, and the parts' last bit is 2^-28.
+constexpr float kScaleT = 8.f;
 
 struct ChunkArgs {
   DeltaRows x;
@@ -122,7 +128,9 @@ constexpr int kPTab = kPB + kTileHalf;            // block products [4][128]
 constexpr int kPSum = kPTab + 4 * kDeltaDim * 4;  // sums of their logarithms
 constexpr int kPBeta = kPSum + 4 * kDeltaDim * 4;
 constexpr int kPMisc = kPBeta + kChunk * 4;
-constexpr int kPrepSmem = kPMisc + 256;
+constexpr int kPRowMax = kPMisc + 256;            // [2 halves of the channels][64 rows]: largest |k| and |q|, as bf16
+constexpr int kPKeyScale = kPRowMax + 2 * kChunk * 4;   // [64]: what a row's key is times, twice as bf16
+constexpr int kPrepSmem = kPKeyScale + kChunk * 4;
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
 // Offset of eight channels c of row r in rows of 512 bytes of fp32 and of 256 bytes of
@@ -245,6 +253,10 @@ __device__ __forceinline__ void mul_tile(const float* L, int ldl, const float* R
   out[(g + 8) * ldo + 2 * t] = sign * d[2], out[(g + 8) * ldo + 2 * t + 1] = sign * d[3];
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ float max_warp(float v) {  // of values >= 0
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
@@ -287,7 +299,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
   float* beta = reinterpret_cast<float*>(smem + kPBeta);
-  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: largest |k|, |q|, growth; unsafe lanes; largest |beta|, |T|
+  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: (8) largest |q|, growth; unsafe lanes; largest |beta|, |T|
   float* A = reinterpret_cast<float*>(smem + kPA);
   bool bad = false;
 
@@ -341,24 +353,52 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       if (x.gate_dim != 1) prefetch_line(x.gate + r * x.ld_gate + (int64_t)h1 * kDeltaDim + 32 * part);
     }
   }
+  uint32_t* rowmax = reinterpret_cast<uint32_t*>(smem + kPRowMax);
+  uint32_t* key_scale = reinterpret_cast<uint32_t*>(smem + kPKeyScale);
+  const float bt = tid < kChunk && tid < n ? __ldg(x.beta + (row0 + tid) * x.ld_beta + h) : 0.f;
+  {
+    // a row's largest |k| (low half) and |q| (high half) over this warp's 64 channels: lanes hand half of their rows on
+    uint32_t m[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const uint32_t ka = kr[t] & 0x7FFF7FFFu, qa = qr[t] & 0x7FFF7FFFu;
+      m[t] = __vmaxu2(__byte_perm(ka, qa, 0x5410), __byte_perm(ka, qa, 0x7632));
+    }
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) {
+      const bool up = lane & (2 * w);
+#pragma unroll
+      for (int i = 0; i < w; ++i) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? m[i] : m[i + w], 2 * w);
+        m[i] = __vmaxu2(up ? m[i + w] : m[i], other);
+      }
+    }
+    m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    if ((lane & 1) == 0) rowmax[(warp & 1) * kChunk + 16 * I + (lane >> 1)] = m[0];
+  }
+  __syncthreads();
   if (tid < kChunk) {
-    const float bt = tid < n ? __ldg(x.beta + (row0 + tid) * x.ld_beta + h) : 0.f;
-    beta[tid] = bt;
-    bad = !(fabsf(bt) <= 3.4e38f);
-    const float mb = max_warp(bad ? 0.f : fabsf(bt));
-    if (lane == 0) misc[32 + warp] = mb;
+    const uint32_t m = __vmaxu2(rowmax[tid], rowmax[kChunk + tid]), kb = m & 0xFFFFu, qb = m >> 16;
+    uint32_t ke = kb >> 7;   // the exponent of the row's key
+    bad = kb >= 0x7F80u || qb >= 0x7F80u || (kb != 0u && (ke < 27u || ke > 227u));   // beyond 2^-100 .. 2^100 row by row
+    if (kb == 0u || bad) ke = 127u;
+    key_scale[tid] = (254u - ke) * (128u * 0x10001u);
+    const float length = __uint_as_float(ke << 23), bv = bt * length, bk = bv * length;
+    bad |= !(fabsf(bv) <= 0x1p20f) || !(fabsf(bk) <= 0x1p20f);
+    beta[tid] = bk;
+    reinterpret_cast<float*>(rec + kRecHead)[kHdV + tid] = bv;
+    const float mb = max_warp(bad ? 0.f : fabsf(bk)), mq = max_warp(bad ? 0.f : __uint_as_float(qb << 16));
+    if (lane == 0) misc[32 + warp] = mb, misc[8 + warp] = mq;
   }
   const f32x2 one = pack2(1.f, 1.f);
   f32x2 block = one, sum = make_float2(0.f, 0.f);
   float grow = 1.f, amax = 0.f;
-  uint32_t km = 0, qm = 0;
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
     sum.x += a[t].x, sum.y += a[t].y;
     a[t].x = expf(a[t].x), a[t].y = expf(a[t].y);
     block = mul2(block, a[t]);
     amax = fmaxf(amax, fmaxf(a[t].x, a[t].y));
-    km = __vmaxu2(km, kr[t] & 0x7FFF7FFFu), qm = __vmaxu2(qm, qr[t] & 0x7FFF7FFFu);
   }
   if (amax > 1.f) {
 #pragma unroll
@@ -369,13 +409,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   tab[I * kDeltaDim + 2 * q2] = Bx, tab[I * kDeltaDim + 2 * q2 + 1] = By;
   *reinterpret_cast<f32x2*>(smem + kPSum + 4 * (I * kDeltaDim + 2 * q2)) = sum;
   {
-    const float k1 = __uint_as_float(max(km & 0xFFFFu, km >> 16) << 16), q1 = __uint_as_float(max(qm & 0xFFFFu, qm >> 16) << 16);
-    bad |= !(k1 <= 3.4e38f) || !(q1 <= 3.4e38f) || !(grow <= 3.4e38f);
+    bad |= !(grow <= 3.4e38f);
     const bool unsafe = !(fminf(Bx, By) >= 7.6e-37f) || !(grow <= 1024.f);   // 2^-120, 2^10
-    const float mk = max_warp(bad ? 0.f : k1), mq = max_warp(bad ? 0.f : q1), mg = max_warp(bad ? 1.f : grow);
+    const float mg = max_warp(bad ? 1.f : grow);
     const uint32_t any = __ballot_sync(0xffffffffu, unsafe);
     if (lane == 0) {
-      misc[warp] = mk, misc[8 + warp] = mq, misc[16 + warp] = mg;
+      misc[16 + warp] = mg;
       reinterpret_cast<uint32_t*>(misc)[24 + warp] = any;
     }
   }
@@ -385,22 +424,26 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     reinterpret_cast<uint4*>(smem + kPA)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
-  float mk = 0.f, mq = 0.f, mg = 1.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) mk = fmaxf(mk, misc[w]), mq = fmaxf(mq, misc[8 + w]);
+  constexpr float mk = 2.f;   // the largest element of a key, as the rows are taken
+  const float mq = fmaxf(misc[8], misc[9]), mb = fmaxf(misc[32], misc[33]);
+  float mg = 1.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) mg *= fmaxf(misc[16 + 2 * b], misc[17 + 2 * b]);
   const uint32_t* unsafe_w = reinterpret_cast<const uint32_t*>(misc) + 24;
   const float scale = x.scale;
   // (growth by more than 2^10 would leave the other channels too few bits of the common power of two)
-  bad |= !(mg <= 1024.f) || !(mk <= 1e30f) || !(mq <= 1e30f) || !(mk * mk * mg <= 1e30f) ||
-         !(mk * mq * mg * fabsf(scale) <= 1e30f) || !(fabsf(scale) <= 1e30f);
+  bad |= !(mg <= 1024.f) || !(mq <= 1e30f) || !(mk * mq * mg * fabsf(scale) <= 1e30f) || !(fabsf(scale) <= 1e30f);
   // powers of two that bring the operands into fp16's range, from bounds: products of decays grow no further than mg
-  const float sc_k = pow2_scale(mk * mg, 14);                        // of K P and K D
+  const float sc_k = pow2_scale(mk * mg, 14);                        // of K D
+  const float sc_kp = pow2_scale(mb * mk * mg, 14);                  // of beta K P
   const float sc_q = pow2_scale(mq * mg * fabsf(scale), 14);
   const float sc_b = pow2_scale(mq * mk * mg * fabsf(scale) * 128.f, 14);
-  // of T, whose diagonal is beta: room for 2^11 times its largest; the parts' last bit is 2^-27 of that
-  const float sc_t = pow2_scale(fmaxf(misc[32], misc[33]), 3);
+#pragma unroll
+  for (int t = 0; t < 16; t += 4) {
+    const uint4 by = *reinterpret_cast<const uint4*>(key_scale + 16 * I + t);
+    kr[t] = mul_bf16x2(kr[t], by.x), kr[t + 1] = mul_bf16x2(kr[t + 1], by.y);
+    kr[t + 2] = mul_bf16x2(kr[t + 2], by.z), kr[t + 3] = mul_bf16x2(kr[t + 3], by.w);
+  }
 
   // ---- decays by channel, forward: K P, Q P, X
   auto block_of = [&](int b) { return *reinterpret_cast<const f32x2*>(tab + b * kDeltaDim + 2 * q2); };
@@ -423,7 +466,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   const uint32_t img = (uint32_t)((q2 >> 5) * kTileHalf + (q2 & 31) * 4);
   const uint32_t piece = (uint32_t)(q2 >> 2), in_piece = (uint32_t)(q2 & 3) * 4;
   {
-    const f32x2 c = centre(I), pre_k = mul2(pre, pack2(sc_k, sc_k)), pre_q = mul2(pre, pack2(sc_q * scale, sc_q * scale)),
+    const f32x2 c = centre(I), pre_k = mul2(pre, pack2(sc_kp, sc_kp)), pre_q = mul2(pre, pack2(sc_q * scale, sc_q * scale)),
                 c_q = mul2(c, pack2(scale, scale));
     f32x2 l = one;
 #pragma unroll
@@ -433,7 +476,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       const f32x2 k = bf16x2_to_f32x2(kr[t]), ql = mul2(bf16x2_to_f32x2(qr[t]), l), w = mul2(l, c);
       uint32_t hi2, lo2;
       const uint32_t o = swz128(img + r * 128);
-      split_f16(mul2(k, mul2(l, pre_k)), hi2, lo2);
+      const float b = beta[r];
+      split_f16(mul2(mul2(k, pack2(b, b)), mul2(l, pre_k)), hi2, lo2);
       *reinterpret_cast<uint32_t*>(rec + kRecKp + o) = hi2;
       *reinterpret_cast<uint32_t*>(rec + kRecKp + kTileBytes + o) = lo2;
       const float2 qp = mul2(ql, pre_q), xq = mul2(ql, c_q), wf = w;
@@ -499,6 +543,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       for (int j = 16 * D + (warp & 1); j < min(16 * D + 16, n); j += 2) {
         const uint2 kj = __ldg(reinterpret_cast<const uint2*>(x.k + (row0 + j) * x.ld_k + hq * kDeltaDim) + lane);
         float4 y = bf16x4_to_float4(kj);
+        const float by = __uint_as_float(key_scale[j] & 0xFFFF0000u);
+        y.x *= by, y.y *= by, y.z *= by, y.w *= by;
         for (int i = j; i < min(16 * D + 16, n); ++i) {
           if (i > j) {
             float4 g;
@@ -518,7 +564,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
             kk += __shfl_xor_sync(0xffffffffu, kk, o);
             qk += __shfl_xor_sync(0xffffffffu, qk, o);
           }
-          if (lane == 0) put(i, j, kk, qk * scale);
+          if (lane == 0) put(i, j, kk * __uint_as_float(key_scale[i] & 0xFFFF0000u), qk * scale);
         }
       }
     }
@@ -620,24 +666,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     mul_tile<32>(A + (32 + r) * kLdA + 32, kLdA, tmp + cc, kLdT, A + (32 + r) * kLdA + cc, kLdA, -1.f);
   }
   __syncthreads();
-  // ---- T = (I + A)^-1 diag(beta) in two parts: a thread 16 columns of a row
+  // ---- T = (I + A)^-1 in two parts: a thread 16 columns of a row
   {
     const int i = tid >> 2, j0 = 16 * (tid & 3);
     float t[16], m = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       const float4 r = *reinterpret_cast<const float4*>(A + i * kLdA + j0 + j);
-      const float4 bj = *reinterpret_cast<const float4*>(beta + j0 + j);
-      t[j] = r.x * bj.x, t[j + 1] = r.y * bj.y, t[j + 2] = r.z * bj.z, t[j + 3] = r.w * bj.w;
+      t[j] = r.x, t[j + 1] = r.y, t[j + 2] = r.z, t[j + 3] = r.w;
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) m = max_nan(m, fabsf(t[j]));
-    bad |= !(m * sc_t <= 32768.f);   // no number, or keys much longer than one: the rows go one by one
+    bad |= !(m * kScaleT <= 32768.f);   // no number, or beta |k|^2 much larger than one: the rows go one by one
     m = max_warp(bad ? 0.f : m);
     if (lane == 0) misc[40 + warp] = m;
     uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) split_f16(mul2(pack2(t[2 * j], t[2 * j + 1]), pack2(sc_t, sc_t)), hi[j], lo[j]);
+    for (int j = 0; j < 8; ++j) split_f16(mul2(pack2(t[2 * j], t[2 * j + 1]), pack2(kScaleT, kScaleT)), hi[j], lo[j]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t o = swz128((uint32_t)(i * 128 + 2 * j0 + 16 * j));
@@ -652,10 +697,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     for (int w = 1; w < 8; ++w) mt = fmaxf(mt, misc[40 + w]);
     float* hd = reinterpret_cast<float*>(rec + kRecHead);
     reinterpret_cast<int*>(hd)[kHdBad] = any;
-    hd[kHdInvKp] = pow2_inverse(sc_k), hd[kHdInvQp] = pow2_inverse(sc_q), hd[kHdInvT] = pow2_inverse(sc_t);
+    hd[kHdInvKp] = pow2_inverse(sc_kp), hd[kHdInvQp] = pow2_inverse(sc_q);
     hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvKd] = pow2_inverse(sc_k);
     // sums of a row's or a column's magnitudes, from above
-    hd[kHdSumKp] = 128.f * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg;
+    hd[kHdSumKp] = 128.f * mb * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg;
   }
 }
 
@@ -664,7 +709,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 // + 63, and turn each product into the next one's operand; warp 8 issues the MMAs,
 // warp 9 copies the operands, two chunks deep, warp 10 stores the outputs.  All
 // products are transposed, with the 128 values on the tensor core's rows:
-//   R^T [v][t] = V^T - S (K P)^T   A = S in two fp16 parts from TMEM, times K P's two (three products)
+//   R^T [v][t] = (V^T - S (K P)^T) diag(beta)   A = S in two fp16 parts from TMEM, times beta K P's two (three products)
 //   U^T = R^T T^T                  A = R in two parts
 //   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
 //   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
@@ -693,12 +738,13 @@ constexpr int kCOffPart2 = 2 * kPart1;                  // one buffer: its produ
 constexpr int kCOffV = kCOffPart2 + kPart2;
 constexpr int kCOffOut = kCOffV + 2 * kChunk * kRowBytes;
 constexpr int kCOffHead = kCOffOut + kChunk * kRowBytes;
-constexpr int kCOffX = kCOffHead + 2 * 640;             // exchanged maxima [2 parities][3 kinds][2 halves][128]
+constexpr int kCHead = 832;                             // bytes of a head's buffer
+constexpr int kCOffX = kCOffHead + 2 * kCHead;             // exchanged maxima [2 parities][3 kinds][2 halves][128]
 constexpr int kCOffBars = kCOffX + 2 * 3 * 2 * 128 * 4;
 constexpr int kCNumBars = 21;
 constexpr int kCOffMisc = kCOffBars + kCNumBars * 8;
 constexpr int kChainSmem = 1024 + kCOffMisc + 40;
-static_assert(kChainSmem <= 232448 && kPart1 % 1024 == 0 && kPart2 % 1024 == 0 && kHeadBytes <= 640, "shared memory");
+static_assert(kChainSmem <= 232448 && kPart1 % 1024 == 0 && kPart2 % 1024 == 0 && kHeadBytes <= kCHead && kHeadBytes <= kRecBytes - kRecHead, "shared memory");
 
 // The two warps that share 32 value rows of the state.
 __device__ __forceinline__ void bar_pair(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory"); }
@@ -802,7 +848,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         if (elect_one()) {
           mbar_arrive_expect_tx(full(s), kPart1 + kHeadBytes);
           for (int i = 0; i < 4; ++i) bulk_load(sm + s * kPart1 + i * (kPart1 / 4), src + i * (kPart1 / 4), kPart1 / 4, full(s));
-          bulk_load(sm + kCOffHead + s * 640, src + kRecHead, kHeadBytes, full(s));
+          bulk_load(sm + kCOffHead + s * kCHead, src + kRecHead, kHeadBytes, full(s));
         }
         __syncwarp();
         ++issued;
@@ -972,7 +1018,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
 
     // a chunk's values of this lane, rows 32 half .. + 31, two a register, and whether it goes row by row: read while
     // the chunk before waits for its products
-    uint32_t vr[16], vmax = 0;
+    uint32_t vr[16];
     auto read_v = [&](int c) {
       const int s = c & 1, left = min(kChunk, n - c * kChunk) - 32 * half;
       wait(full_v(s), (c >> 1) & 1);
@@ -990,12 +1036,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       uint32_t m = 0;
 #pragma unroll
       for (int t = 0; t < 16; ++t) m = __vmaxu2(m, vr[t] & 0x7FFF7FFFu);
-      vmax = max(m & 0xFFFFu, m >> 16);
-      xchg(s, kMaxV, half) = __uint_as_float(vmax << 16);
       if (lane == 0) mbar_arrive(empty_v(s));
-      return bar_state_or(vmax >= 0x7F80u);
+      return bar_state_or(max(m & 0xFFFFu, m >> 16) >= 0x7480u);   // 2^106: times what a row's value is times within fp32's range
     };
-    bool rowwise = false;   // a value of the chunk is no number
+    bool rowwise = false;   // a value of the chunk is no number, or a very large one
     if (chunks > 0) {
       read_v(0);
       rowwise = vote(0);
@@ -1032,7 +1076,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
     for (int c = 0; c < chunks; ++c) {
       const int s = c & 1;
       const int rows = min(kChunk, n - c * kChunk);
-      const float* hd = reinterpret_cast<const float*>(smem + kCOffHead + s * 640);
+      const float* hd = reinterpret_cast<const float*>(smem + kCOffHead + s * kCHead);
       // ---- the state's parts; the outputs' products, which read the last ones, are through
       measure(s);
       if (out_rows > 0) wait(b_o, (f - 1) & 1);
@@ -1050,6 +1094,17 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       wait(full(s), (c >> 1) & 1);
       rowwise |= reinterpret_cast<const int*>(hd)[kHdBad] != 0;
       if (tid == 0) by_rows[s] = rowwise;
+      const float* row_v = hd + kHdV + 32 * half;   // what these rows' values are times
+      if (!rowwise) {
+        float m = 0.f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const float2 by = *reinterpret_cast<const float2*>(row_v + 2 * t), r = mul2(bf16x2_to_f32x2(vr[t]), by);
+          m = fmaxf(fmaxf(m, fabsf(r.x)), fabsf(r.y));
+        }
+        xchg(s, kMaxV, half) = m;
+        bar_pair(warp & 3);
+      }
       wait(b_r, c & 1);
       if (rowwise) {
         // back to the state itself
@@ -1111,7 +1166,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           const f32x2 r = fma2(pack2(-inv_kp, -inv_kp), pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])),
-                               bf16x2_to_f32x2(vr[t]));
+                               mul2(bf16x2_to_f32x2(vr[t]), *reinterpret_cast<const float2*>(row_v + 2 * t)));
           split_f16(mul2(r, pack2(sc_r, sc_r)), hi[t], lo[t]);
           top = max_abs_f16x2(top, hi[t]);
         }
@@ -1122,7 +1177,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         arrive(b_rp);
       }
       // ---- U
-      const float inv_t = pow2_inverse(sc_r) * hd[kHdInvT], sum_t = hd[kHdSumT];
+      const float inv_t = pow2_inverse(sc_r) * (1.f / kScaleT), sum_t = hd[kHdSumT];
       put_out(1);
       wait(b_u, f & 1);
       const float sc_u = pow2_scale(fmaxf(xchg(s, kMaxR, 0), xchg(s, kMaxR, 1)) * sum_t, 14);

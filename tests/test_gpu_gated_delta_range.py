@@ -49,6 +49,32 @@ def check_out(out, want, rows, size, mass, q, scale=SCALE):
     assert (off <= tol).all(), (off / tol).max()
 
 
+@pytest.mark.parametrize("length", [1e2, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("at", [[63], [20, 21, 100]], ids=str)
+def test_long_keys_among_ordinary_ones(length, at):
+    """beta |k|^2 = 1 whatever the key's length: the update is of the state's size."""
+    x, s0 = inputs(130, 2, 2, seed=41), state(2)
+    q, k, v, g, beta = x
+    k[at] = (k[at].float() * length).to(torch.bfloat16)
+    beta[at] = 1 / k[at].float().square().sum(2)
+    out, last = prefill(x, s0)
+    want, states, size, mass = rule(*x, SCALE, s0[0])
+    check_bits(last, states[-1], torch.stack([norms(s) for s in states]).amax(0))
+    check_out(out, want, 130, size, mass, q)
+
+
+@pytest.mark.parametrize("length", [1e3, 1e5])
+def test_long_values_with_small_betas(length):
+    x, s0 = inputs(130, 2, 2, seed=42), state(2)
+    q, k, v, g, beta = x
+    at = [17, 63, 90]
+    v[at] = (v[at].float() * length).to(torch.bfloat16)
+    beta[at] = 1 / length
+    out, last = prefill(x, s0)
+    want, states, _, _ = rule(*x, SCALE, s0[0])
+    check_bits(last, states[-1], torch.stack([norms(s) for s in states]).amax(0))
+
+
 @pytest.mark.parametrize("gate,beta", [(-0.41, 1e-16), (-0.5, 0.5), (-1.2, 0.5), (-0.5, 1e-12)])
 def test_state_that_decayed_without_updates(gate, beta):
     """64 rows take a state down by 2^-38 to 2^-111 and bring nothing; the next rows act on what is left of it."""
