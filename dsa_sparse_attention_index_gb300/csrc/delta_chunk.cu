@@ -10,7 +10,9 @@
 // It is the same rule for a key k / s with the value v / s and beta s^2, so every row
 // is taken with the power of two s that brings its key's largest element into [1, 2):
 // rows whose keys differ in length by any factor share the chunk's powers of two
-// without loss, and with beta in R, T's diagonal is one whatever beta is.
+// without loss, and with beta in R, T's diagonal is one whatever beta is.  Queries are
+// taken likewise, the scale as a number in [1, 2): a row's outputs, rounded to bf16, are
+// multiplied by the powers of two that its query and the scale lost.
 //
 // Two kernels.  delta_prepare_kernel: everything that does not depend on the
 // state, a CTA per chunk and head, into a record of operands laid out as the tensor
@@ -37,11 +39,11 @@ constexpr int kRecT = kRecQp + kTileBytes;
 constexpr int kRecB = kRecT + 2 * kTileHalf;
 constexpr int kRecKd = kRecB + kTileHalf;
 constexpr int kRecHead = kRecKd + 2 * kTileBytes;      // 106,496
-constexpr int kRecBytes = kRecHead + 1024;
+constexpr int kRecBytes = kRecHead + 1152;
 constexpr int kPart1 = kRecB, kPart2 = kRecHead - kRecB;   // what is read first, and last
 // floats of the record's head
-enum : int { kHdBad = 0, kHdInvKp, kHdInvQp, kHdInvB, kHdInvKd, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16, kHdV = kHdP + kDeltaDim };
-constexpr int kHeadBytes = 4 * (kHdV + kChunk);   // (V: what a row's value is times)
+enum : int { kHdBad = 0, kHdInvKp, kHdInvB, kHdInvK, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16, kHdV = kHdP + kDeltaDim, kHdO = kHdV + kChunk };
+constexpr int kHeadBytes = 4 * (kHdO + kChunk);   // (V, O: what a row's value and its outputs are times; O twice as bf16)
 // T's power of two: its diagonal is one, so 2^11 of room above it, and the parts' last bit is 2^-28.
 constexpr float kScaleT = 8.f;
 
@@ -129,8 +131,8 @@ constexpr int kPSum = kPTab + 4 * kDeltaDim * 4;  // sums of their logarithms
 constexpr int kPBeta = kPSum + 4 * kDeltaDim * 4;
 constexpr int kPMisc = kPBeta + kChunk * 4;
 constexpr int kPRowMax = kPMisc + 256;            // [2 halves of the channels][64 rows]: largest |k| and |q|, as bf16
-constexpr int kPKeyScale = kPRowMax + 2 * kChunk * 4;   // [64]: what a row's key is times, twice as bf16
-constexpr int kPrepSmem = kPKeyScale + kChunk * 4;
+constexpr int kPRowScale = kPRowMax + 2 * kChunk * 4;   // [64] keys, [64] queries: what a row's is times, twice as bf16
+constexpr int kPrepSmem = kPRowScale + 2 * kChunk * 4;
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
 // Offset of eight channels c of row r in rows of 512 bytes of fp32 and of 256 bytes of
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
   float* beta = reinterpret_cast<float*>(smem + kPBeta);
-  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: (8) largest |q|, growth; unsafe lanes; largest |beta|, |T|
+  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: (16) growth; (24) unsafe lanes; (32) largest |beta|; (40) largest |T|
   float* A = reinterpret_cast<float*>(smem + kPA);
   bool bad = false;
 
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     }
   }
   uint32_t* rowmax = reinterpret_cast<uint32_t*>(smem + kPRowMax);
-  uint32_t* key_scale = reinterpret_cast<uint32_t*>(smem + kPKeyScale);
+  uint32_t *key_scale = reinterpret_cast<uint32_t*>(smem + kPRowScale), *query_scale = key_scale + kChunk;
   const float bt = tid < kChunk && tid < n ? __ldg(x.beta + (row0 + tid) * x.ld_beta + h) : 0.f;
   {
     // a row's largest |k| (low half) and |q| (high half) over this warp's 64 channels: lanes hand half of their rows on
@@ -379,16 +381,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   __syncthreads();
   if (tid < kChunk) {
     const uint32_t m = __vmaxu2(rowmax[tid], rowmax[kChunk + tid]), kb = m & 0xFFFFu, qb = m >> 16;
-    uint32_t ke = kb >> 7;   // the exponent of the row's key
-    bad = kb >= 0x7F80u || qb >= 0x7F80u || (kb != 0u && (ke < 27u || ke > 227u));   // beyond 2^-100 .. 2^100 row by row
+    uint32_t ke = kb >> 7, qe = qb >> 7;   // the exponents of the row's key and query
+    bad = (kb != 0u && (ke < 27u || ke > 227u)) || (qb != 0u && (qe < 27u || qe > 227u));   // beyond 2^-100 .. 2^100 row by row
     if (kb == 0u || bad) ke = 127u;
-    key_scale[tid] = (254u - ke) * (128u * 0x10001u);
+    if (qb == 0u || bad) qe = 127u;
+    key_scale[tid] = (254u - ke) * (128u * 0x10001u), query_scale[tid] = (254u - qe) * (128u * 0x10001u);
     const float length = __uint_as_float(ke << 23), bv = bt * length, bk = bv * length;
-    bad |= !(fabsf(bv) <= 0x1p20f) || !(fabsf(bk) <= 0x1p20f);
+    // the power of two of query and scale; of a row without outputs (a zero query or scale) any
+    const int se = (int)((__float_as_uint(x.scale) >> 23) & 0xFFu);
+    int oe = (int)qe + se - 127;
+    if (qb == 0u || x.scale == 0.f) oe = 127;
+    bad |= !(fabsf(bv) <= 0x1p20f) || !(fabsf(bk) <= 0x1p20f) || oe < 1 || oe > 254 || se == 255 || (se == 0 && x.scale != 0.f);
     beta[tid] = bk;
-    reinterpret_cast<float*>(rec + kRecHead)[kHdV + tid] = bv;
-    const float mb = max_warp(bad ? 0.f : fabsf(bk)), mq = max_warp(bad ? 0.f : __uint_as_float(qb << 16));
-    if (lane == 0) misc[32 + warp] = mb, misc[8 + warp] = mq;
+    float* hd = reinterpret_cast<float*>(rec + kRecHead);
+    hd[kHdV + tid] = bv;
+    reinterpret_cast<uint32_t*>(hd)[kHdO + tid] = (uint32_t)oe * (128u * 0x10001u);
+    const float mb = max_warp(bad ? 0.f : fabsf(bk));
+    if (lane == 0) misc[32 + warp] = mb;
   }
   const f32x2 one = pack2(1.f, 1.f);
   f32x2 block = one, sum = make_float2(0.f, 0.f);
@@ -424,25 +433,25 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     reinterpret_cast<uint4*>(smem + kPA)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
-  constexpr float mk = 2.f;   // the largest element of a key, as the rows are taken
-  const float mq = fmaxf(misc[8], misc[9]), mb = fmaxf(misc[32], misc[33]);
+  constexpr float mk = 2.f;   // the largest element of a key or a query, as the rows are taken
+  const float mb = fmaxf(misc[32], misc[33]);
   float mg = 1.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) mg *= fmaxf(misc[16 + 2 * b], misc[17 + 2 * b]);
   const uint32_t* unsafe_w = reinterpret_cast<const uint32_t*>(misc) + 24;
-  const float scale = x.scale;
   // (growth by more than 2^10 would leave the other channels too few bits of the common power of two)
-  bad |= !(mg <= 1024.f) || !(mq <= 1e30f) || !(mk * mq * mg * fabsf(scale) <= 1e30f) || !(fabsf(scale) <= 1e30f);
+  bad |= !(mg <= 1024.f);
   // powers of two that bring the operands into fp16's range, from bounds: products of decays grow no further than mg
-  const float sc_k = pow2_scale(mk * mg, 14);                        // of K D
+  const float sc_k = pow2_scale(mk * mg, 14);                        // of K D and Q P
   const float sc_kp = pow2_scale(mb * mk * mg, 14);                  // of beta K P
-  const float sc_q = pow2_scale(mq * mg * fabsf(scale), 14);
-  const float sc_b = pow2_scale(mq * mk * mg * fabsf(scale) * 128.f, 14);
+  const float sc_b = pow2_scale(mk * mk * mg * 128.f, 14);
 #pragma unroll
   for (int t = 0; t < 16; t += 4) {
-    const uint4 by = *reinterpret_cast<const uint4*>(key_scale + 16 * I + t);
-    kr[t] = mul_bf16x2(kr[t], by.x), kr[t + 1] = mul_bf16x2(kr[t + 1], by.y);
-    kr[t + 2] = mul_bf16x2(kr[t + 2], by.z), kr[t + 3] = mul_bf16x2(kr[t + 3], by.w);
+    const uint4 ks = *reinterpret_cast<const uint4*>(key_scale + 16 * I + t), qs = *reinterpret_cast<const uint4*>(query_scale + 16 * I + t);
+    kr[t] = mul_bf16x2(kr[t], ks.x), kr[t + 1] = mul_bf16x2(kr[t + 1], ks.y);
+    kr[t + 2] = mul_bf16x2(kr[t + 2], ks.z), kr[t + 3] = mul_bf16x2(kr[t + 3], ks.w);
+    qr[t] = mul_bf16x2(qr[t], qs.x), qr[t + 1] = mul_bf16x2(qr[t + 1], qs.y);
+    qr[t + 2] = mul_bf16x2(qr[t + 2], qs.z), qr[t + 3] = mul_bf16x2(qr[t + 3], qs.w);
   }
 
   // ---- decays by channel, forward: K P, Q P, X
@@ -466,8 +475,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   const uint32_t img = (uint32_t)((q2 >> 5) * kTileHalf + (q2 & 31) * 4);
   const uint32_t piece = (uint32_t)(q2 >> 2), in_piece = (uint32_t)(q2 & 3) * 4;
   {
-    const f32x2 c = centre(I), pre_k = mul2(pre, pack2(sc_kp, sc_kp)), pre_q = mul2(pre, pack2(sc_q * scale, sc_q * scale)),
-                c_q = mul2(c, pack2(scale, scale));
+    const f32x2 c = centre(I), pre_k = mul2(pre, pack2(sc_kp, sc_kp)), pre_q = mul2(pre, pack2(sc_k, sc_k));
     f32x2 l = one;
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       split_f16(mul2(mul2(k, pack2(b, b)), mul2(l, pre_k)), hi2, lo2);
       *reinterpret_cast<uint32_t*>(rec + kRecKp + o) = hi2;
       *reinterpret_cast<uint32_t*>(rec + kRecKp + kTileBytes + o) = lo2;
-      const float2 qp = mul2(ql, pre_q), xq = mul2(ql, c_q), wf = w;
+      const float2 qp = mul2(ql, pre_q), xq = mul2(ql, c), wf = w;
       *reinterpret_cast<uint32_t*>(rec + kRecQp + o) = f16x2(qp.x, qp.y);
       const uint32_t s = at512(r, piece) + 2 * in_piece;
       *reinterpret_cast<f32x2*>(smem + kPX + s) = mul2(k, w);
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
             kk += __shfl_xor_sync(0xffffffffu, kk, o);
             qk += __shfl_xor_sync(0xffffffffu, qk, o);
           }
-          if (lane == 0) put(i, j, kk * __uint_as_float(key_scale[i] & 0xFFFF0000u), qk * scale);
+          if (lane == 0) put(i, j, kk * __uint_as_float(key_scale[i] & 0xFFFF0000u), qk * __uint_as_float(query_scale[i] & 0xFFFF0000u));
         }
       }
     }
@@ -587,13 +595,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   };
   // X at rows x0 .. + 15: k and q times l and the decays from the block's start
   auto put_x = [&](int x0, f32x2 l) {
-    const float sq = sc_q * scale;
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
       l = mul2(l, a[t]);
       uint32_t hi2, lo2;
-      split_f16(mul2(bf16x2_to_f32x2(kr[t]), mul2(l, pack2(sc_k, sc_k))), hi2, lo2);
-      const f32x2 xq = mul2(bf16x2_to_f32x2(qr[t]), mul2(l, pack2(sq, sq)));
+      const f32x2 ls = mul2(l, pack2(sc_k, sc_k));
+      split_f16(mul2(bf16x2_to_f32x2(kr[t]), ls), hi2, lo2);
+      const f32x2 xq = mul2(bf16x2_to_f32x2(qr[t]), ls);
       const uint32_t o = at256(x0 + t, piece) + in_piece;
       *reinterpret_cast<uint32_t*>(smem + kPX + o) = hi2;
       *reinterpret_cast<uint32_t*>(smem + kPX + kPartHalf + o) = lo2;
@@ -611,11 +619,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     const int bi = warp == 0 ? 1 : warp < 3 ? 2 : 3, bj = warp == 0 ? 0 : warp < 3 ? warp - 1 : warp - 3;
     float kk[2][4], qk[2][4];
     tile_parts(sm, warp == 3 || warp == 4 ? 0 : 16 * bi, warp == 0 ? 48 : 16 * bj, kk, qk);
-    const float ik = pow2_inverse(sc_k), iq = pow2_inverse(sc_q);
+    const float ik = pow2_inverse(sc_k);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) kk[e][i] = kk[e][i] * ik * ik, qk[e][i] = qk[e][i] * ik * iq;   // (ik * ik may leave fp32's range)
+      for (int i = 0; i < 4; ++i) kk[e][i] = kk[e][i] * ik * ik, qk[e][i] = qk[e][i] * ik * ik;
       put_tile(16 * bi, 16 * bj + 8 * e, kk[e], qk[e]);
     }
   }
@@ -697,8 +705,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     for (int w = 1; w < 8; ++w) mt = fmaxf(mt, misc[40 + w]);
     float* hd = reinterpret_cast<float*>(rec + kRecHead);
     reinterpret_cast<int*>(hd)[kHdBad] = any;
-    hd[kHdInvKp] = pow2_inverse(sc_kp), hd[kHdInvQp] = pow2_inverse(sc_q);
-    hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvKd] = pow2_inverse(sc_k);
+    hd[kHdInvKp] = pow2_inverse(sc_kp), hd[kHdInvB] = pow2_inverse(sc_b), hd[kHdInvK] = pow2_inverse(sc_k);
     // sums of a row's or a column's magnitudes, from above
     hd[kHdSumKp] = 128.f * mb * mk * mg, hd[kHdSumT] = 64.f * mt, hd[kHdSumKd] = 64.f * mk * mg;
   }
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 //   R^T [v][t] = (V^T - S (K P)^T) diag(beta)   A = S in two fp16 parts from TMEM, times beta K P's two (three products)
 //   U^T = R^T T^T                  A = R in two parts
 //   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
-//   out^T = S (Q P)^T + U^T B^T    one product each: the high parts' 11 bits are more than bf16 keeps
+//   out^T = S (Q P)^T + U^T B^T    times a power of two a row; one product each: the high parts' 11 bits are more than bf16 keeps
 // The parts of a row of S, R or U are times a power of two, so that they keep 21 bits of
 // its largest element whatever its size: of S from the row's largest element itself, which the
 // two warps of a row exchange before they split it (a bound carried from chunk to chunk would
@@ -738,9 +745,10 @@ constexpr int kCOffPart2 = 2 * kPart1;                  // one buffer: its produ
 constexpr int kCOffV = kCOffPart2 + kPart2;
 constexpr int kCOffOut = kCOffV + 2 * kChunk * kRowBytes;
 constexpr int kCOffHead = kCOffOut + kChunk * kRowBytes;
-constexpr int kCHead = 832;                             // bytes of a head's buffer
+constexpr int kCHead = 1088;                            // bytes of a head's buffer
 constexpr int kCOffX = kCOffHead + 2 * kCHead;             // exchanged maxima [2 parities][3 kinds][2 halves][128]
-constexpr int kCOffBars = kCOffX + 2 * 3 * 2 * 128 * 4;
+constexpr int kCOffRow = kCOffX + 2 * 3 * 2 * 128 * 4;  // [2][64]: what the rows' outputs are times
+constexpr int kCOffBars = kCOffRow + 2 * kChunk * 4;
 constexpr int kCNumBars = 21;
 constexpr int kCOffMisc = kCOffBars + kCNumBars * 8;
 constexpr int kChainSmem = 1024 + kCOffMisc + 40;
@@ -874,9 +882,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         // two rows at a time, 16 bytes a lane (bulk copies would stand in line behind the next operands')
         const uint4* src = reinterpret_cast<const uint4*>(smem + kCOffOut) + lane;
         uint16_t* dst = p.out + ((row0 + c * kChunk + (lane >> 4)) * x.heads + h) * kDeltaDim + 8 * (lane & 15);
+        const uint32_t* by = reinterpret_cast<const uint32_t*>(smem + kCOffRow) + (c & 1) * kChunk + (lane >> 4);
 #pragma unroll 8
         for (int t = 0; t < rows; t += 2)
-          if (t + (lane >> 4) < rows) *reinterpret_cast<uint4*>(dst + (int64_t)t * x.heads * kDeltaDim) = src[16 * t];
+          if (t + (lane >> 4) < rows) {
+            const uint4 o = src[16 * t];
+            const uint32_t f = by[t];
+            *reinterpret_cast<uint4*>(dst + (int64_t)t * x.heads * kDeltaDim) =
+                make_uint4(mul_bf16x2(o.x, f), mul_bf16x2(o.y, f), mul_bf16x2(o.z, f), mul_bf16x2(o.w, f));
+          }
         __syncwarp();
         if (lane == 0) mbar_arrive(out_free);
       }
@@ -1048,6 +1062,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
     // the outputs of the last chunk that took the tensor core, behind the next one's first operand
     int out_rows = 0, out_c = 0;
     float out_f1 = 0.f, out_f2 = 0.f;
+    const float scale = x.scale == 0.f ? 0.f : __uint_as_float((__float_as_uint(x.scale) & 0x807FFFFFu) | 0x3F800000u);
     uint32_t jobs = 0;
     auto put_out = [&](int q) {   // in two halves, each where the warps would wait
       if (out_rows == 0) return;
@@ -1115,6 +1130,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         // a value that is no number, or out of range, touches nothing of the rows before it: one row after another
         put_out(1);
         arrive(b_rp);
+        if (jobs > 0) wait(out_free, (jobs - 1) & 1);   // the rows' powers of two of the chunk before are overwritten by the next one
         // in the place of operands that nothing reads now: a row's k, q and decay, two buffers, and partial sums
         float* rb = reinterpret_cast<float*>(smem + s * kPart1);     // [2][k, q, decay][128]
         float* part = rb + 2 * 3 * 128;                              // [p, w, k q][2 halves][128]
@@ -1179,6 +1195,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       // ---- U
       const float inv_t = pow2_inverse(sc_r) * (1.f / kScaleT), sum_t = hd[kHdSumT];
       put_out(1);
+      // for the store warp, which hears of it from all warps; it is through with the chunk before the last one, whose place this takes
+      if (tid < kChunk) reinterpret_cast<uint32_t*>(smem + kCOffRow)[s * kChunk + tid] = reinterpret_cast<const uint32_t*>(hd)[kHdO + tid];
       wait(b_u, f & 1);
       const float sc_u = pow2_scale(fmaxf(xchg(s, kMaxR, 0), xchg(s, kMaxR, 1)) * sum_t, 14);
       {
@@ -1197,7 +1215,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       }
       // ---- the state behind the chunk
       const float inv_u = pow2_inverse(sc_u);
-      const float inv_o1 = inv_s * hd[kHdInvQp], inv_o2 = inv_u * hd[kHdInvB];
+      const float inv_o1 = inv_s * hd[kHdInvK] * scale, inv_o2 = inv_u * hd[kHdInvB] * scale;
       if (c + 1 < chunks) {
         read_v(c + 1);
         rowwise = vote(c + 1);
@@ -1211,7 +1229,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         for (int i = 0; i < 64; ++i) S[i] *= by;
         sc_s = to;
       }
-      const float inv_kd = inv_u * hd[kHdInvKd] * sc_s;
+      const float inv_kd = inv_u * hd[kHdInvK] * sc_s;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t acc[32];

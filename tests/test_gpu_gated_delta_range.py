@@ -103,3 +103,36 @@ def test_states_that_are_nothing_beside_their_updates(size):
     want, states, grown, mass = rule(*x, SCALE, s0[0])
     check_bits(last, states[-1], grown)
     check_out(out, want, 200, grown, mass, x[0])
+
+
+@pytest.mark.parametrize("length", [1e15, 1e22, 1e26])
+def test_large_queries_where_a_block_decays(length):
+    """A channel that keeps its size for 15 rows and then falls by 2^-115."""
+    x, s0 = inputs(130, 2, 2, seed=44), state(2)
+    q, k, v, g, beta = x
+    q.copy_((q.float() * length).to(torch.bfloat16))
+    g[:, :, 3] = -0.001
+    g[15::16, :, 3] = -79.0
+    out, last = prefill(x, s0)
+    want, states, size, mass = rule(*x, SCALE, s0[0])
+    check_out(out, want, 130, size, mass, q)
+    check_bits(last, states[-1], size)
+
+
+@pytest.mark.parametrize("power", [-20, -30, -40, -60])
+def test_small_queries_among_ordinary_ones(power):
+    """A row's outputs are relative to its own query."""
+    x, s0 = inputs(130, 2, 2, seed=45), state(2)
+    x[0][::3] *= 2.0 ** power
+    out, last = prefill(x, s0)
+    want, states, size, mass = rule(*x, SCALE, s0[0])
+    check_out(out, want, 130, size, mass, x[0])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.25, 1e20, 1e-20, -1e-3])
+def test_scales(scale):
+    x, s0 = inputs(130, 2, 2, seed=46), state(2)
+    out, last = prefill(x, s0, scale)
+    want, states, size, mass = rule(*x, scale, s0[0])
+    check_out(out, want, 130, size, mass, x[0], scale)
+    check_bits(last, states[-1], size)
