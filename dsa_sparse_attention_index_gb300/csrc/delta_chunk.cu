@@ -93,6 +93,15 @@ __device__ __forceinline__ void split_f16(f32x2 v, uint32_t& hi, uint32_t& lo) {
   hi = f16x2(hx, hy);
   lo = f16x2(r.x, r.y);
 }
+// The same with the first part rounded to nearest, where it is also used alone (cut ones would make
+// the outputs 3.5e-4 too small).
+__device__ __forceinline__ void split_f16_rn(f32x2 v, uint32_t& hi, uint32_t& lo) {
+  hi = f16x2(v.x, v.y);
+  f32x2 r;   // v - hi without a way back to fp32 (2,048 rows of 96 heads: 326 us for 329)
+  asm("{\n .reg .f16 a, b, m;\n mov.b32 {a, b}, %2;\n mov.b16 m, 0xBC00;\n fma.rn.f32.f16 %0, a, m, %3;\n fma.rn.f32.f16 %1, b, m, %4;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "r"(hi), "f"(v.x), "f"(v.y));
+  lo = f16x2(r.x, r.y);
+}
 __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -719,7 +728,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 //   R^T [v][t] = (V^T - S (K P)^T) diag(beta)   A = S in two fp16 parts from TMEM, times beta K P's two (three products)
 //   U^T = R^T T^T                  A = R in two parts
 //   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
-//   out^T = S (Q P)^T + U^T B^T    times a power of two a row; one product each: the high parts' 11 bits are more than bf16 keeps
+//   out^T = S (Q P)^T + U^T B^T    times a power of two a row; one product each: the high parts' 11 bits, rounded, are more than bf16 keeps
 // The parts of a row of S, R or U are times a power of two, so that they keep 21 bits of
 // its largest element whatever its size: of S from the row's largest element itself, which the
 // two warps of a row exchange before they split it (a bound carried from chunk to chunk would
@@ -1099,7 +1108,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       for (int g = 0; g < 2; ++g) {
         uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) split_f16(pack2(S[32 * g + 2 * i], S[32 * g + 2 * i + 1]), hi[i], lo[i]);
+        for (int i = 0; i < 16; ++i) split_f16_rn(pack2(S[32 * g + 2 * i], S[32 * g + 2 * i + 1]), hi[i], lo[i]);
         tmem_st16(quad + kColS + 64 * half + 16 * g, hi);
         tmem_st16(quad + kColS + 64 * half + 32 + 16 * g, lo);
       }
@@ -1206,7 +1215,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
         const float f_u = inv_t * sc_u;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          split_f16(mul2(pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])), pack2(f_u, f_u)), hi[t], lo[t]);
+          split_f16_rn(mul2(pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])), pack2(f_u, f_u)), hi[t], lo[t]);
         }
         tmem_st16(quad + kColParts + 16 * half, hi);
         tmem_st16(quad + kColParts + 32 + 16 * half, lo);

@@ -1,4 +1,4 @@
-"""gated_delta_prefill where the numbers of a sequence differ widely in size."""
+"""gated_delta_prefill where the numbers of a sequence differ widely in size, and how exact it is."""
 import math
 
 import pytest
@@ -136,3 +136,13 @@ def test_scales(scale):
     want, states, size, mass = rule(*x, scale, s0[0])
     check_out(out, want, 130, size, mass, x[0], scale)
     check_bits(last, states[-1], size)
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_outputs_have_no_bias(gate):
+    """Over a million outputs.  A rounding to nearest has no bias, and to bf16 a relative error of 1.7e-3 rms, so the factor
+    that fits the outputs best is within 2e-6 of one; operands cut to 11 bits instead of rounded make it 3.5e-4 smaller."""
+    x, s0 = inputs(2048, 4, 4, gate, seed=50), state(4)
+    out, last = prefill(x, s0)
+    want = rule(*x, SCALE, s0[0])[0]
+    assert abs(float((out.double() * want).sum() / want.square().sum()) - 1) <= 2.0 ** -15
