@@ -119,7 +119,8 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 //                        (the starts of rows 16, 32 and 48) let X and Y stand in shared memory at once.
 // Within a block the factors are fp32, since a quotient's factors may be large, cut into two tf32 on
 // the way into the mma; between blocks they are two fp16 times a power of two, made once.
-// Three products either way, 21 bits.  (Two bf16 parts everywhere left states 7 to 10e-7
+// Three products either way, 21 bits; the queries one factor of 11 bits, rounded (as bf16 in the blocks
+// they put outputs 2.0e-3 off instead of 1.7e-3, which is bf16's own rounding).  (Two bf16 parts everywhere left states 7 to 10e-7
 // off instead of 4 to 5e-7; tf32 everywhere took 5 % longer.)  The inverse of I + A goes by
 // blocks: the diagonal ones by substitution, a thread a column, while other warps make
 // tiles, then two levels of products.
@@ -129,11 +130,11 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 // so was K D made by the warps that the inverse leaves idle (312 us for 302 in all).
 constexpr int kPrepThreads = 256;
 constexpr int kPX = 0;                            // X = k L c, fp32: 64 rows x 512 bytes
-constexpr int kPQ = kPX + kChunk * 512;           // q L c, bf16: 64 rows x 256 bytes
+constexpr int kPQ = kPX + kChunk * 512;           // q L c, tf32: 64 rows x 256 bytes of the upper halves
 constexpr int kPY = kPQ + kChunk * 256;           // Y, fp32
 constexpr int kPartHalf = kChunk * 256;           // X and Y as two fp16 parts, one behind the other
 constexpr int kLdA = kChunk + 4;                  // floats: rows start four banks apart
-constexpr int kPA = kPY + kChunk * 512;           // A, then (I + A)^-1, fp32 [64][68]
+constexpr int kPA = kPY + kChunk * 512;           // the lower halves of q L c, then A, then (I + A)^-1, fp32 [64][68]
 constexpr int kPB = kPA + kChunk * kLdA * 4;    // B, fp16, the record's image
 constexpr int kPTab = kPB + kTileHalf;            // block products [4][128]
 constexpr int kPSum = kPTab + 4 * kDeltaDim * 4;  // sums of their logarithms
@@ -142,6 +143,7 @@ constexpr int kPMisc = kPBeta + kChunk * 4;
 constexpr int kPRowMax = kPMisc + 256;            // [2 halves of the channels][64 rows]: largest |k| and |q|, as bf16
 constexpr int kPRowScale = kPRowMax + 2 * kChunk * 4;   // [64] keys, [64] queries: what a row's is times, twice as bf16
 constexpr int kPrepSmem = kPRowScale + 2 * kChunk * 4;
+static_assert(kChunk * 256 <= kChunk * kLdA * 4, "the lower halves in A's place");
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
 // Offset of eight channels c of row r in rows of 512 bytes of fp32 and of 256 bytes of
@@ -154,6 +156,11 @@ __device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4]
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t tf32_rn(float v) {   // to nearest, ties away from zero
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+  return r;
 }
 // fp32 as two tf32: the upper 11 bits and what they leave, 21 bits in all and fp32's range.
 __device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) {
@@ -184,7 +191,9 @@ __device__ __forceinline__ void tile_xy(const uint8_t* smem, int x0, int y0, flo
     uint32_t xh[4], xl[4], yh[2], yl[2];
     split_tf32(xa.x, xh[0], xl[0]), split_tf32(xb.x, xh[1], xl[1]), split_tf32(xa.y, xh[2], xl[2]), split_tf32(xb.y, xh[3], xl[3]);
     split_tf32(y.x, yh[0], yl[0]), split_tf32(y.y, yh[1], yl[1]);
-    const uint32_t q[4] = {qa << 16, qb << 16, qa & 0xFFFF0000u, qb & 0xFFFF0000u};
+    const uint32_t la = *reinterpret_cast<const uint32_t*>(Q + 16 * piece + (kPA - kPQ));
+    const uint32_t lb = *reinterpret_cast<const uint32_t*>(Q + 16 * piece + 8 * 256 + (kPA - kPQ));
+    const uint32_t q[4] = {__byte_perm(la, qa, 0x5410), __byte_perm(lb, qb, 0x5410), __byte_perm(la, qa, 0x7632), __byte_perm(lb, qb, 0x7632)};
     mma_16x8x8(lh, xl, yh);
     mma_16x8x8(hl, xh, yl);
     mma_16x8x8(kk, xh, yh);
@@ -436,10 +445,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       reinterpret_cast<uint32_t*>(misc)[24 + warp] = any;
     }
   }
-  // the upper triangles stay zero
-  static_assert(kPB == kPA + kChunk * kLdA * 4, "A and B lie together");
-  for (int i = tid; i < (kChunk * kLdA * 4 + kTileHalf) / 16; i += kPrepThreads)
-    reinterpret_cast<uint4*>(smem + kPA)[i] = make_uint4(0, 0, 0, 0);
+  // B's upper triangle stays zero
+  for (int i = tid; i < kTileHalf / 16; i += kPrepThreads) reinterpret_cast<uint4*>(smem + kPB)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
   constexpr float mk = 2.f;   // the largest element of a key or a query, as the rows are taken
@@ -501,7 +508,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       *reinterpret_cast<uint32_t*>(rec + kRecQp + o) = f16x2(qp.x, qp.y);
       const uint32_t s = at512(r, piece) + 2 * in_piece;
       *reinterpret_cast<f32x2*>(smem + kPX + s) = mul2(k, w);
-      *reinterpret_cast<uint32_t*>(smem + kPQ + at256(r, piece) + in_piece) = bf16x2(xq.x, xq.y);
+      const uint32_t qx = tf32_rn(xq.x), qy = tf32_rn(xq.y), oq = at256(r, piece) + in_piece;
+      *reinterpret_cast<uint32_t*>(smem + kPQ + oq) = __byte_perm(qx, qy, 0x7632);
+      *reinterpret_cast<uint32_t*>(smem + kPA + oq) = __byte_perm(qx, qy, 0x5410);
       // Y of the block itself: k / (L c); no number where the block is not safe, and not used there
       *reinterpret_cast<f32x2*>(smem + kPY + s) = mul2(k, pack2(reciprocal(wf.x), reciprocal(wf.y)));
     }
@@ -549,13 +558,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
           f16x2(j <= i ? qk[2 * e] * sc_b : 0.f, j + 1 <= i ? qk[2 * e + 1] * sc_b : 0.f);
     }
   };
+  const int D = warp >> 1;   // this warp's diagonal block
+  const bool safe = (unsafe_w[2 * D] | unsafe_w[2 * D + 1]) == 0u;
+  float dk[4], dq[4];
+  if (safe) tile_xy(smem, 16 * D, 16 * D + 8 * (warp & 1), dk, dq);
+  __syncthreads();
+  // (now that nothing reads the queries' lower halves) A and B within the blocks, and zeros right of A's diagonal blocks
   {
-    const int D = warp >> 1;
-    if ((unsafe_w[2 * D] | unsafe_w[2 * D + 1]) == 0u) {
-      float kk[4], qk[4];
-      tile_xy(smem, 16 * D, 16 * D + 8 * (warp & 1), kk, qk);
-      put_tile(16 * D, 16 * D + 8 * (warp & 1), kk, qk);
+    for (int i = tid; i < 6 * 64; i += kPrepThreads) {
+      const int blk = i >> 6, r = (i >> 2) & 15, br = blk < 3 ? 0 : blk < 5 ? 1 : 2, bc = blk < 3 ? blk + 1 : blk < 5 ? blk - 1 : 3;
+      *reinterpret_cast<float4*>(A + (16 * br + r) * kLdA + 16 * bc + 4 * (i & 3)) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (safe) {
+      put_tile(16 * D, 16 * D + 8 * (warp & 1), dk, dq);
     } else {
+      // rows that are not there stay zero
+      *reinterpret_cast<float4*>(A + (16 * D + ((tid & 63) >> 2)) * kLdA + 16 * D + 4 * (tid & 3)) = make_float4(0.f, 0.f, 0.f, 0.f);
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + D) : "memory");
       // decays that leave fp32's range within 16 rows: pair by pair, four channels a lane
       for (int j = 16 * D + (warp & 1); j < min(16 * D + 16, n); j += 2) {
         const uint2 kj = __ldg(reinterpret_cast<const uint2*>(x.k + (row0 + j) * x.ld_k + hq * kDeltaDim) + lane);
@@ -586,7 +605,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       }
     }
   }
-  __syncthreads();
   // ---- between the blocks.  Rows 32..63 meet columns 0..31 at the start of row 32, rows 48..63 meet 32..47 at that of
   // row 48, rows 16..31 meet 0..15 at that of row 16: decays up to there in Y, from there in X
   // Y at rows y0 .. + 15: k times the decay to the block's end, times l
