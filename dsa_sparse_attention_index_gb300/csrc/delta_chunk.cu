@@ -1077,6 +1077,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       uint32_t m = 0;
 #pragma unroll
       for (int t = 0; t < 16; ++t) m = __vmaxu2(m, vr[t] & 0x7FFF7FFFu);
+      __syncwarp();   // all lanes have read what the next copy overwrites
       if (lane == 0) mbar_arrive(empty_v(s));
       return bar_state_or(max(m & 0xFFFFu, m >> 16) >= 0x7480u);   // 2^106: times what a row's value is times within fp32's range
     };
@@ -1272,6 +1273,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
           st[3] = fmaf(st[3], d.w, inv_kd * __uint_as_float(acc[4 * i + 3]));
         }
       }
+      __syncwarp();   // likewise
       if (lane == 0) mbar_arrive(empty(s));
       out_rows = rows, out_c = c, out_f1 = inv_o1, out_f2 = inv_o2;
       ++f;
@@ -1281,6 +1283,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
     put_out(1);
     if (jobs > 0) wait(out_free, (jobs - 1) & 1);
     if (tid == 0) out_job[1] = 0;
+    __syncwarp();
     if (lane == 0) mbar_arrive(out_full);
     if (float* to = state_out(p.s, b, 0, h)) {
       const float un = pow2_inverse(sc_s);
