@@ -9,6 +9,11 @@
 // table for j < have_i, else entry count - 1 - (F_i + j - have_i) of the stack.
 // The row with p % 64 = 0 is the only first one of a fresh page: it puts the
 // page into the table.
+//
+// A step may not fit.  The rows of the one request `cut` at max_rows, and of those
+// behind it, are not placed, and their pages stay on the stack.  Where the stack ends
+// within the pages of the request `dry`, it and those behind it have rows without a page.
+// Lengths count the tokens that have a place, so a table row is whole up to its length.
 #include <algorithm>
 #include <atomic>
 
@@ -69,6 +74,11 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
     count = 0;
   }
   const bool wide = ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
+  // what the one thread finds that scans the request: of `cut` the request, its rows that are placed and all pages up to
+  // there; of `dry` the request and its pages
+  __shared__ int s_cut, s_cut_rows, s_dry, s_dry_pages;
+  __shared__ long long s_cut_pages;
+  if (tid == 0) s_cut = s_dry = INT32_MAX;   // (the first tile's scan is before any other write)
   long long rows0 = 0, pages0 = 0;  // of the tiles before
   for (int base = 0; base < a.batch; base += kSlotTile) {
     // scans of rows and of pages, in 64 bits: lengths go up to 2^30
@@ -112,8 +122,14 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
       s_cached[j] = c[e];
       s_page[j] = (int)min(p, (long long)INT32_MAX);
       if (cta == 0 && base + j < a.batch) a.starts[base + j] = s_start[j];
+      const int have = pages_of(c[e]), need = pages_of(c[e] + n[e]);
+      if (r <= a.max_rows && r + n[e] > a.max_rows) {
+        s_cut = base + j, s_cut_rows = (int)(a.max_rows - r);
+        s_cut_pages = p + pages_of(c[e] + s_cut_rows) - have;
+      }
+      if (p <= count && p + need - have > count) s_dry = base + j, s_dry_pages = have + (int)(count - p);
       r += n[e];
-      p += pages_of(c[e] + n[e]) - pages_of(c[e]);
+      p += need - have;
     }
     if (tid == kSlotThreads - 1) s_start[kSlotTile] = (int)min(r, (long long)a.max_rows);
     __syncthreads();
@@ -172,12 +188,16 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
   if (ctas > 1) cg::this_cluster().sync();
   for (int i = cta * kSlotThreads + tid; i < a.batch; i += ctas * kSlotThreads) {
     const int2 v = lengths_of(a, i);
-    a.seq_lens[i] = v.y < 0 ? 0 : v.x + v.y;
+    int len = v.y < 0 ? 0 : v.x + v.y;
+    if (i >= s_cut) len = v.x + (i == s_cut ? s_cut_rows : 0);
+    if (i >= s_dry) len = (int)min((long long)len, (long long)kBlock * (i == s_dry ? s_dry_pages : pages_of(v.x)));
+    a.seq_lens[i] = len;
   }
   if (cta == 0 && tid == 0) {
     a.starts[a.batch] = total;
-    if (rows0 > a.max_rows || pages0 > count) report(a.status, DSA_ERR_BOUNDS);
-    *a.free_left = (int)max(0ll, (long long)count - pages0);
+    const long long taken = s_cut == INT32_MAX ? pages0 : s_cut_pages;
+    if (rows0 > a.max_rows || taken > count) report(a.status, DSA_ERR_BOUNDS);
+    *a.free_left = (int)max(0ll, (long long)count - taken);
   }
 }
 

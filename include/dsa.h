@@ -574,7 +574,7 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_batch_t*
  * ceil(c / 64) pages in its row of block_table; the ceil((c + n) / 64) pages that it
  * needs are completed from the top of the stack of free pages, request by
  * request: page i of the step is free_blocks[free_count - 1 - i].  Then
- *   seq_lens[i]   = c + n                        (what dsa_batch_t takes)
+ *   seq_lens[i]   = c + n                        (what dsa_batch_t takes; fewer in a step that does not fit)
  *   row_starts[i] = first row of request i, row_starts[batch] = all rows
  *   positions[r]  = the row's token index in its request, c, c + 1, ...
  *   slots[r]      = its physical cache row, table entry * 64 + position % 64
@@ -588,8 +588,12 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_batch_t*
  *   row_starts    device int32 [batch + 1];  positions, slots device int32 [max_rows]
  * A negative length, a request that does not fit its table row (it comes out
  * with no rows and length 0), more rows than max_rows, more pages than the
- * stack holds, or an entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS; slots
- * without a page are -1.  One launch.
+ * stack holds, or an entry outside 0..num_blocks-1 raises DSA_ERR_BOUNDS.  A step
+ * that does not fit is taken as far as it goes, so that lengths and count in place
+ * stay those of a whole table: rows beyond max_rows are not placed and take no page;
+ * rows for which the stack has no page keep their position with a slot of -1; and
+ * seq_lens counts the tokens that have a place.  The caller brings the others again.
+ * One launch.
  */
 dsa_status_t dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
                               const int32_t* free_blocks, int32_t free_capacity, const int32_t* free_count,
