@@ -501,26 +501,47 @@ def _rows_of(name: str, t, shape, dtypes):
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else inner
 
 
+class _Descriptor:
+    """A descriptor's `layout`, made from its tensors and made again once one of them has another address, shape or
+    strides (resized, set_() or with new .data); `seen` is of the tensors that it was made from."""
+
+    def __post_init__(self):
+        self.read()
+
+    def read(self):
+        seen = self.places()
+        if getattr(self, "seen", None) != seen:
+            layout = self.describe()
+            object.__setattr__(self, "layout", layout)
+            object.__setattr__(self, "seen", seen)
+        return self.layout
+
+
 @dataclass(frozen=True)
-class StatePool:
+class StatePool(_Descriptor):
     """The recurrent layers' states, fp32 [slots, heads, 128 values, 128 keys] on the GPU: a tensor of its own, or a
-    view into the packed cache's block rows (slots may lie apart).  Its layout is read once, here."""
+    view into the packed cache's block rows (slots may lie apart)."""
 
     states: torch.Tensor
 
-    def __post_init__(self):
+    def places(self):
+        t = self.states
+        return t.data_ptr(), t.shape, t.stride()
+
+    def describe(self):
         t = self.states
         if t.dim() != 4:
             raise ValueError(f"states: expected [slots, heads, {DELTA_DIM}, {DELTA_DIM}], got {list(t.shape)}")
         ptr, stride = _rows_of("states", t, (t.shape[0], t.shape[1], DELTA_DIM, DELTA_DIM), _F32)
-        object.__setattr__(self, "layout", StatePoolT(ptr, 4 * stride, t.shape[0], t.shape[1]))
+        return StatePoolT(ptr, 4 * stride, t.shape[0], t.shape[1])
 
 
 @dataclass(frozen=True)
-class DeltaRows:
+class DeltaRows(_Descriptor):
     """The rows of a gated delta layer: q and k bf16 bits [rows, qk_heads, 128], v [rows, heads, 128], the log decays
-    gate fp32 [rows, heads, 128] (per key channel) or [rows, heads], beta fp32 [rows, heads].  Rows may lie apart.  The
-    tensors' layouts are read once, here; their values at every call."""
+    gate fp32 [rows, heads, 128] (per key channel) or [rows, heads], beta fp32 [rows, heads].  Rows may lie apart.
+    Making one takes longer than a decode call (its tensors' layouts are checked), so keep it where the tensors stay;
+    what they hold is read at every call."""
 
     q: torch.Tensor
     k: torch.Tensor
@@ -529,7 +550,12 @@ class DeltaRows:
     beta: torch.Tensor
     scale: float
 
-    def __post_init__(self):
+    def places(self):
+        q, k, v, g, b = self.q, self.k, self.v, self.gate, self.beta
+        return (q.data_ptr(), q.shape, q.stride(), k.data_ptr(), k.shape, k.stride(), v.data_ptr(), v.shape, v.stride(),
+                g.data_ptr(), g.shape, g.stride(), b.data_ptr(), b.shape, b.stride())
+
+    def describe(self):
         if self.q.dim() != 3 or self.v.dim() != 3:
             raise ValueError(f"q and v: expected [rows, heads, {DELTA_DIM}], got {list(self.q.shape)}, {list(self.v.shape)}")
         rows, heads, qk, wide = self.v.shape[0], self.v.shape[1], self.q.shape[1], self.gate.dim() == 3
@@ -540,8 +566,7 @@ class DeltaRows:
         at = {t.get_device() for t in (self.q, self.k, self.v, self.gate, self.beta)}
         if len(at) != 1:
             raise ValueError(f"the rows' tensors must be on one device, got {sorted(at)}")
-        object.__setattr__(self, "layout", DeltaRowsT(*(p for p, _ in got), *(ld for _, ld in got), qk,
-                                                      DELTA_DIM if wide else 1, float(self.scale)))
+        return DeltaRowsT(*(p for p, _ in got), *(ld for _, ld in got), qk, DELTA_DIM if wide else 1, float(self.scale))
 
     @property
     def rows(self) -> int:
@@ -549,10 +574,11 @@ class DeltaRows:
 
 
 def _delta(pool: StatePool, x: DeltaRows, *others):
-    if x.v.shape[1] != pool.layout.heads:
-        raise ValueError(f"rows of {x.v.shape[1]} heads and states of {pool.layout.heads}")
+    states, layout = pool.read(), x.read()
+    if x.v.shape[1] != states.heads:
+        raise ValueError(f"rows of {x.v.shape[1]} heads and states of {states.heads}")
     _one_device(pool.states, x.v, *others)
-    return ctypes.byref(pool.layout), ctypes.byref(x.layout), (x.v.shape[0], x.v.shape[1], DELTA_DIM)
+    return ctypes.byref(states), ctypes.byref(layout), (x.v.shape[0], x.v.shape[1], DELTA_DIM)
 
 
 def gated_delta_decode(pool: StatePool, x: DeltaRows, queries_per_seq: int, slots_in, slots_out, out, status,

@@ -1,4 +1,5 @@
-"""gated_delta_prefill where the numbers of a sequence differ widely in size, and how exact it is."""
+"""gated_delta_prefill where the numbers of a sequence differ widely in size, how exact it is, and descriptors over storage that
+changes."""
 import math
 
 import pytest
@@ -136,6 +137,23 @@ def test_scales(scale):
     want, states, size, mass = rule(*x, scale, s0[0])
     check_out(out, want, 130, size, mass, x[0], scale)
     check_bits(last, states[-1], size)
+
+
+def test_descriptors_follow_tensors_that_get_other_storage():
+    x, s0 = inputs(40, 2, 2, seed=51), state(2)
+    y, s1 = inputs(40, 2, 2, seed=52), state(2, seed=9)
+    pool, rows = torch.cat([s0, torch.zeros_like(s0)]), B.DeltaRows(*x, SCALE)
+    states, out, st = B.StatePool(pool), torch.zeros((40, 2, DIM), dtype=torch.bfloat16, device="cuda"), ints(0)
+    ws = B.workspace(B.gated_delta_prefill_workspace_size(40, 1, 2))
+    for new, first in ((x, s0), (y, s1)):
+        for t, n in zip(x, new):
+            t.data = n.clone()
+        pool.data = torch.cat([first, torch.zeros_like(first)])
+        B.gated_delta_prefill(states, rows, ints(0, 40), ints(0), ints(1), out, ws, st)
+        want, after, size, mass = rule(*new, SCALE, first[0])
+        assert st.item() == 0
+        check_out(out, want, 40, size, mass, new[0])
+        check_bits(pool[1], after[-1], size)
 
 
 @pytest.mark.parametrize("gate", ["channel", "head"])
