@@ -1,5 +1,10 @@
-"""gated_delta_prefill where the numbers of a sequence differ widely in size, how exact it is, and descriptors over storage that
-changes."""
+"""gated_delta_prefill where the rows of a chunk differ widely in size, and how
+many bits it keeps: long keys and values with small betas among ordinary rows,
+states that decay by many powers of two, large and small queries, scales,
+states that are no finite numbers, the paths beside the tensor cores for one
+decay a head and for shared query and key heads, and states and outputs held to
+the operands' bits instead of to a bound that grows with the rows; descriptors
+over storage that changes."""
 import math
 
 import pytest
@@ -37,6 +42,8 @@ def norms(s):
 # Six operands meet a state in 64 rows (S, K P, R, T, U, K D).  Each is two fp16 parts of 11 bits: what the second leaves is at
 # most 2^-22 of the number, and the product of two second parts, which is left out, at most 2^-20 of a product; counted together
 # as 2^-21 for each operand, relative to the state, since the updates (beta |k|^2 <= 1) and the decays do not enlarge it.
+# (An emulation of the chunks on these inputs stays within 0.06 of it; without any one of the cross products of first and
+# second parts it is 13 to 137 times over it.)
 BITS = 6 * 2.0 ** -21
 
 
@@ -139,6 +146,48 @@ def test_scales(scale):
     check_bits(last, states[-1], size)
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("rows", [10, 130])
+def test_states_that_are_no_numbers(bad, rows):
+    """Their value row is lost, the others are not."""
+    x, s0 = inputs(rows, 2, 2, seed=47), state(2)
+    good, good_last = prefill(x, s0)
+    s0[0, 1, 77, 5] = bad
+    out, last = prefill(x, s0)
+    keep = torch.ones((2, DIM), dtype=torch.bool, device="cuda")
+    keep[1, 77] = False
+    assert not torch.isfinite(out[:, 1, 77]).any() and not torch.isfinite(last[1, 77]).any()
+    assert torch.equal(out[:, keep], good[:, keep]) and torch.equal(last[keep], good_last[keep])
+
+
+@pytest.mark.parametrize("heads,qk,gate", [(2, 2, "head"), (6, 2, "channel"), (6, 2, "head")])
+@pytest.mark.parametrize("what", ["fast", "resets", "growing", "nan", "inf"])
+def test_paths_beside_the_tensor_cores(heads, qk, gate, what):
+    """Decays that leave a block's range, and chunks that go row by row: one decay a head, shared queries and keys."""
+    n, at = 150, 77
+    x, s0 = inputs(n, heads, qk, gate, seed=48), state(heads)
+    q, k, v, g, beta = x
+    if what == "fast":
+        g.fill_(-8.0)
+        g[:, ::2] = -0.01
+    elif what == "resets":
+        g[::7] = -math.inf
+    elif what == "growing":
+        g[30:90] = 0.2
+    elif what == "nan":
+        v[at, 1, 9] = math.nan
+    else:
+        beta[at, 1] = math.inf
+    out, last = prefill(x, s0)
+    want, states, size, mass = rule(*x, SCALE, s0[0])
+    if what in ("nan", "inf"):
+        check_out(out[:at], want[:at], n, rule(*(t[:at] for t in x), SCALE, s0[0])[2], mass[:at], q[:at])
+        assert torch.equal(torch.isfinite(out), torch.isfinite(want)) and torch.equal(torch.isfinite(last), torch.isfinite(states[-1]))
+    else:
+        check_out(out, want, n, size, mass, q)
+        assert (norms(last.double() - states[-1]) <= state_tolerance(n, size)).all()
+
+
 def test_descriptors_follow_tensors_that_get_other_storage():
     x, s0 = inputs(40, 2, 2, seed=51), state(2)
     y, s1 = inputs(40, 2, 2, seed=52), state(2, seed=9)
@@ -154,6 +203,15 @@ def test_descriptors_follow_tensors_that_get_other_storage():
         assert st.item() == 0
         check_out(out, want, 40, size, mass, new[0])
         check_bits(pool[1], after[-1], size)
+
+
+@pytest.mark.parametrize("rows,heads,qk,gate", [(n, 4, qk, gate) for n in (21, 64, 65, 130, 333, 2085)
+                                                for qk, gate in ((4, "channel"), (2, "head"))] + [(16385, 1, 1, "channel")])
+def test_states_keep_the_operands_bits(rows, heads, qk, gate):
+    x, s0 = inputs(rows, heads, qk, gate, seed=rows), state(heads)
+    out, last = prefill(x, s0)
+    want, states, size, mass = rule(*x, SCALE, s0[0])
+    check_bits(last, states[-1], size)
 
 
 @pytest.mark.parametrize("gate", ["channel", "head"])
