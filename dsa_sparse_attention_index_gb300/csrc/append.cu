@@ -54,6 +54,26 @@ __device__ __forceinline__ uint8_t e4m3(float x) {
   return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
+// The encodings' rules, once for all kernels of this file.
+__device__ __forceinline__ uint32_t e2m1(float x) {
+  return (uint32_t)__nv_cvt_float_to_fp4(x, __NV_E2M1, cudaRoundNearest) & 0xFu;
+}
+// Scale of a vector in FP8.
+__device__ __forceinline__ float fp8_scale(float amax) { return amax > 0.f ? amax / 448.0f : 1.0f; }
+// Exponent of 32 elements in MXFP4; floor(log2 amax) + 127 are a normal amax's exponent bits.
+__device__ __forceinline__ int mxfp4_exponent(float amax) {
+  const uint32_t ebits = (__float_as_uint(amax) >> 23) & 0xFFu;
+  return (amax > 0.f && ebits > 0) ? max(-127, min(127, (int)ebits - 127 - 2)) : -127;
+}
+// Scale code of 16 latents in NVFP4, and what they are divided by (0: their codes are 0).
+__device__ __forceinline__ uint8_t nvfp4_scale(float amax, float latent_scale, float* step) {
+  const uint8_t sc = e4m3(amax / (6.0f * latent_scale));
+  const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sc, __NV_E4M3);
+  const float dec = __half2float(*reinterpret_cast<const __half*>(&hr));
+  *step = dec > 0.f ? latent_scale * dec : 0.f;
+  return sc;
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -78,10 +98,29 @@ struct AppendArgs {
 // Named barrier 1 over the 128 threads that write one token (threads 0..127).
 __device__ __forceinline__ void bar_append() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Row nr of the new tokens into slot `slot` of block row r.
+// New token row nr = b * nq + j (token L_b - nq + j) by threads tid = 0..127;
+// `sync` is a barrier over those threads (uniform: every early return below
+// depends on nr alone).
 template <typename Sync>
-__device__ __forceinline__ void append_token(const AppendArgs& a, int nr, int r, int slot, int tid, float* warp_amax,
-                                             Sync sync) {
+__device__ __forceinline__ void append_row(const AppendArgs& a, int nr, int tid, float* warp_amax, Sync sync) {
+  const int32_t num_blocks = a.num_blocks;
+  const int32_t* block_table = a.block_table;
+  const int32_t max_blocks = a.max_blocks, nq = a.nq, cap = a.cap;
+  int32_t* status = a.status;
+  const int b = nr / nq, j = nr % nq;
+  const int L = a.seq_lens[b];
+  if (L < 0 || L > cap) {
+    if (tid == 0) report(status, DSA_ERR_BOUNDS);
+    return;
+  }
+  const int t = L - nq + j;
+  if (t < 0) return;  // a context shorter than its new rows: nothing to write for this one
+  const int r = block_table[(int64_t)b * max_blocks + t / kBlock];
+  if (r < 0 || r >= num_blocks) {
+    if (tid == 0) report(status, DSA_ERR_BOUNDS);
+    return;
+  }
+  const int slot = t % kBlock;
   uint8_t* latent_base = a.latent_base;
   uint8_t* index_base = a.index_base;
   const int64_t row_stride = a.row_stride;
@@ -105,14 +144,11 @@ __device__ __forceinline__ void append_token(const AppendArgs& a, int nr, int r,
     float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint8_t sc = e4m3(amax / (6.0f * latent_scale));
-    const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sc, __NV_E4M3);
-    const float sdec = __half2float(*reinterpret_cast<const __half*>(&hr));
-    const float step = latent_scale * sdec;
+    float step;
+    const uint8_t sc = nvfp4_scale(amax, latent_scale, &step);
     uint32_t code[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      code[q] = sdec > 0.f ? (uint32_t)__nv_cvt_float_to_fp4(v[q] / step, __NV_E2M1, cudaRoundNearest) & 0xFu : 0u;
+    for (int q = 0; q < 4; ++q) code[q] = step != 0.f ? e2m1(v[q] / step) : 0u;
     const uint16_t two = (uint16_t)((code[0] | (code[1] << 4)) | ((code[2] | (code[3] << 4)) << 8));
     *reinterpret_cast<uint16_t*>(rec + 2 * tid) = two;
     if ((tid & 3) == 0) rec[kValue / 2 + tid / 4] = sc;
@@ -127,44 +163,18 @@ __device__ __forceinline__ void append_token(const AppendArgs& a, int nr, int r,
     if (lane == 0) warp_amax[wid] = wm;
     sync();
     const float amax = fmaxf(fmaxf(warp_amax[0], warp_amax[1]), fmaxf(warp_amax[2], warp_amax[3]));
-    const float s = amax > 0.f ? amax / 448.0f : 1.0f;
+    const float s = fp8_scale(amax);
     page[(int64_t)slot * kIdxDim + tid] = e4m3(x / s);
     if (tid == 0) *reinterpret_cast<float*>(page + kBlock * kIdxDim + 4 * slot) = s;
   } else {
     // warp wid = 32-element block wid
     const float amax = warp_max(fabsf(x));
-    const uint32_t ebits = (__float_as_uint(amax) >> 23) & 0xFFu;  // floor(log2 amax) + 127 for normal amax
-    const int e = (amax > 0.f && ebits > 0) ? max(-127, min(127, (int)ebits - 127 - 2)) : -127;
-    const uint32_t code = (uint32_t)__nv_cvt_float_to_fp4(ldexpf(x, -e), __NV_E2M1, cudaRoundNearest) & 0xFu;
+    const int e = mxfp4_exponent(amax);
+    const uint32_t code = e2m1(ldexpf(x, -e));
     const uint32_t hi = __shfl_down_sync(0xffffffffu, code, 1);  // element 2i in the low nibble of byte i
     if ((lane & 1) == 0) page[(int64_t)slot * (kIdxDim / 2) + 16 * wid + lane / 2] = (uint8_t)(code | (hi << 4));
     if (lane == 0) page[kBlock * (kIdxDim / 2) + 4 * slot + wid] = (uint8_t)(e + 127);
   }
-}
-
-// New token row nr = b * nq + j (token L_b - nq + j) by threads tid = 0..127;
-// `sync` is a barrier over those threads (uniform: every early return below
-// depends on nr alone).
-template <typename Sync>
-__device__ __forceinline__ void append_row(const AppendArgs& a, int nr, int tid, float* warp_amax, Sync sync) {
-  const int32_t num_blocks = a.num_blocks;
-  const int32_t* block_table = a.block_table;
-  const int32_t max_blocks = a.max_blocks, nq = a.nq, cap = a.cap;
-  int32_t* status = a.status;
-  const int b = nr / nq, j = nr % nq;
-  const int L = a.seq_lens[b];
-  if (L < 0 || L > cap) {
-    if (tid == 0) report(status, DSA_ERR_BOUNDS);
-    return;
-  }
-  const int t = L - nq + j;
-  if (t < 0) return;  // a context shorter than its new rows: nothing to write for this one
-  const int r = block_table[(int64_t)b * max_blocks + t / kBlock];
-  if (r < 0 || r >= num_blocks) {
-    if (tid == 0) report(status, DSA_ERR_BOUNDS);
-    return;
-  }
-  append_token(a, nr, r, t % kBlock, tid, warp_amax, sync);
 }
 
 // One CTA per new token row.
@@ -185,7 +195,7 @@ __device__ __forceinline__ uint2 e4m3x8(uint4 v, float s) {
                     e4m3x2(bf16_low(v.z) / s, bf16_high(v.z) / s) | e4m3x2(bf16_low(v.w) / s, bf16_high(v.w) / s) << 16);
 }
 
-// One warp per new token row, its slot given; -1 is a padding row.  append_token's
+// One warp per new token row, its slot given; -1 is a padding row.  append_row's
 // encodings, 16 bytes a load and nothing shared between warps: a row's reads are all
 // on their way before the first is used.  16,385 rows (34.7 MB): 10.3 us in a graph,
 // a CTA a row took 25.7; bound by the correctly rounded divisions, then bytes.
@@ -222,15 +232,13 @@ __global__ void __launch_bounds__(32 * kSlotWarps) cache_append_slots_kernel(con
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_low(w[i])), fabsf(bf16_high(w[i]))));
-    const uint8_t sc = e4m3(amax / (6.0f * a.latent_scale));
-    const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sc, __NV_E4M3);
-    const float sdec = __half2float(*reinterpret_cast<const __half*>(&hr)), step = a.latent_scale * sdec;
+    float step;
+    const uint8_t sc = nvfp4_scale(amax, a.latent_scale, &step);
     uint32_t code[2] = {0u, 0u};
-    if (sdec > 0.f) {
+    if (step != 0.f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t two = ((uint32_t)__nv_cvt_float_to_fp4(bf16_low(w[i]) / step, __NV_E2M1, cudaRoundNearest) & 0xFu) |
-                             ((uint32_t)__nv_cvt_float_to_fp4(bf16_high(w[i]) / step, __NV_E2M1, cudaRoundNearest) & 0xFu) << 4;
+        const uint32_t two = e2m1(bf16_low(w[i]) / step) | e2m1(bf16_high(w[i]) / step) << 4;
         code[i >> 2] |= two << (8 * (i & 3));
       }
     }
@@ -245,19 +253,18 @@ __global__ void __launch_bounds__(32 * kSlotWarps) cache_append_slots_kernel(con
   uint8_t* page = a.index_base + block;
   if (KEY8) {
     amax = warp_max(amax);
-    const float ks = amax > 0.f ? amax / 448.0f : 1.0f;
+    const float ks = fp8_scale(amax);
     reinterpret_cast<uint32_t*>(page + slot * kIdxDim)[lane] = e4m3x2(x[0] / ks, x[1] / ks) | e4m3x2(x[2] / ks, x[3] / ks) << 16;
     if (lane == 0) *reinterpret_cast<float*>(page + kBlock * kIdxDim + 4 * slot) = ks;
   } else {
     // eight lanes a block of 32
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const uint32_t ebits = (__float_as_uint(amax) >> 23) & 0xFFu;
-    const int e = (amax > 0.f && ebits > 0) ? max(-127, min(127, (int)ebits - 127 - 2)) : -127;
+    const int e = mxfp4_exponent(amax);
     uint32_t code = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      code |= ((uint32_t)__nv_cvt_float_to_fp4(ldexpf(x[i], -e), __NV_E2M1, cudaRoundNearest) & 0xFu) << (4 * i);
+      code |= e2m1(ldexpf(x[i], -e)) << (4 * i);
     reinterpret_cast<uint16_t*>(page + slot * (kIdxDim / 2))[lane] = (uint16_t)code;
     if ((lane & 7) == 0) page[kBlock * (kIdxDim / 2) + 4 * slot + lane / 8] = (uint8_t)(e + 127);
   }
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(128)
   const float x[4] = {bf16_bits_to_float((uint16_t)(v.x & 0xFFFFu)), bf16_bits_to_float((uint16_t)(v.x >> 16)),
                       bf16_bits_to_float((uint16_t)(v.y & 0xFFFFu)), bf16_bits_to_float((uint16_t)(v.y >> 16))};
   const float amax = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-  const float s = amax > 0.f ? amax / 448.0f : 1.0f;
+  const float s = fp8_scale(amax);
   const uint32_t c = (uint32_t)e4m3(x[0] / s) | ((uint32_t)e4m3(x[1] / s) << 8) | ((uint32_t)e4m3(x[2] / s) << 16) |
                      ((uint32_t)e4m3(x[3] / s) << 24);
   reinterpret_cast<uint32_t*>(codes + rh * kIdxDim)[lane] = c;
@@ -601,16 +608,15 @@ __global__ void __launch_bounds__(kFeThreads, 2)
         // clamped to [-127, 127] (-127 for an all-zero block), codes
         // e2m1(q 2^-E), as the MXFP4 keys are written; the head weight as given
         const float am = amax_s[eq * 16 + i];
-        const uint32_t ebits = (__float_as_uint(am) >> 23) & 0xFFu;  // floor(log2 amax) + 127 for normal amax
-        const int e = (am > 0.f && ebits > 0) ? max(-127, min(127, (int)ebits - 127 - 2)) : -127;
-        const uint32_t code = (uint32_t)__nv_cvt_float_to_fp4(ldexpf(v[i], -e), __NV_E2M1, cudaRoundNearest) & 0xFu;
+        const int e = mxfp4_exponent(am);
+        const uint32_t code = e2m1(ldexpf(v[i], -e));
         const uint32_t hi = __shfl_down_sync(0xffffffffu, code, 1);  // element 2i in the low nibble of byte i
         if ((lane & 1) == 0) p.q_index[rh * (kIdxDim / 2) + d / 2] = (uint8_t)(code | (hi << 4));
         if (lane == 0) p.q_index[(int64_t)p.rows * kIdxHeads * (kIdxDim / 2) + rh * 4 + quarter] = (uint8_t)(e + 127);
         if (t == r) p.head_w_out[rh] = hw_t;
       } else {
         const float amax = fmaxf(fmaxf(amax_s[i], amax_s[16 + i]), fmaxf(amax_s[32 + i], amax_s[48 + i]));
-        const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
+        const float sc = fp8_scale(amax);
         p.q_index[rh * kIdxDim + d] = e4m3(v[i] / sc);
         if (t == r) p.head_w_out[rh] = hw_t * sc;
       }
