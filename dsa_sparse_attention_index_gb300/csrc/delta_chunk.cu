@@ -2,15 +2,15 @@
 //
 // For the rows i = 1..64 of a chunk behind the state S0, with P_i = prod_{s<=i}
 // a_s (a = exp(gate), by channel) and the decay D_ij = prod_{j<s<=i} a_s:
-//   A_ij = beta_i sum_d k_i k_j D_ij (j < i),   T = (I + A)^-1,
-//   R = diag(beta) (V - (K P) S0^T),   U = T R,
+//   A_ij = beta_i sum_d k_i k_j D_ij (j < i),   T = (I + A)^-1 diag(m),
+//   R = diag(p) (V - (K P) S0^T),   U = T R,   beta = m p, p a power of two, m in [1, 2)
 //   out = scale ((Q P) S0^T + B U),  B_ij = sum_d q_i k_j D_ij (j <= i),
 //   S = S0 diag(P_64) + U^T (K D_64)
 // which is the rule of delta.cu with its 64 steps solved as one triangular system.
 // It is the same rule for a key k / s with the value v / s and beta s^2, so every row
 // is taken with the power of two s that brings its key's largest element into [1, 2):
 // rows whose keys differ in length by any factor share the chunk's powers of two
-// without loss, and with beta in R, T's diagonal is one whatever beta is.  Queries are
+// without loss, and with p in R, T's diagonal is one to two whatever beta is.  Queries are
 // taken likewise, the scale as a number in [1, 2): a row's outputs, rounded to bf16, are
 // multiplied by the powers of two that its query and the scale lost.
 //
@@ -32,19 +32,21 @@ namespace {
 
 constexpr int kTileHalf = kChunk * 128;                // 64 rows of 64 fp16 (128 bytes, 128-byte swizzle)
 constexpr int kTileBytes = 2 * kTileHalf;              // 64 rows x 128 channels
-// A record: beta K P (high and low parts), Q P, T (high and low), then B, K D (high and low), then the head's floats.
+// A record: p K P (high and low parts), Q P, T (high and low), then B, K D (high and low), then the head's floats.
 constexpr int kRecKp = 0;
 constexpr int kRecQp = kRecKp + 2 * kTileBytes;
 constexpr int kRecT = kRecQp + kTileBytes;
 constexpr int kRecB = kRecT + 2 * kTileHalf;
 constexpr int kRecKd = kRecB + kTileHalf;
 constexpr int kRecHead = kRecKd + 2 * kTileBytes;      // 106,496
-constexpr int kRecBytes = kRecHead + 1152;
+constexpr int kRecBytes = kRecHead + 1024;
 constexpr int kPart1 = kRecB, kPart2 = kRecHead - kRecB;   // what is read first, and last
 // floats of the record's head
-enum : int { kHdBad = 0, kHdInvKp, kHdInvB, kHdInvK, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16, kHdV = kHdP + kDeltaDim, kHdO = kHdV + kChunk };
-constexpr int kHeadBytes = 4 * (kHdO + kChunk);   // (V, O: what a row's value and its outputs are times; O twice as bf16)
-// T's power of two: its diagonal is one, so 2^11 of room above it, and the parts' last bit is 2^-28.
+enum : int { kHdBad = 0, kHdInvKp, kHdInvB, kHdInvK, kHdSumKp, kHdSumT, kHdSumKd, kHdP = 16, kHdV = kHdP + kDeltaDim, kHdO = kHdV + kChunk / 2 };
+// (V, O: the powers of two that a row's value and its outputs are times, as bf16; V a row's, O its twice)
+constexpr int kHeadBytes = 4 * (kHdO + kChunk);
+constexpr int kHeadVBytes = 2 * kChunk;
+// T's power of two: its diagonal is one to two, so 2^11 of room above it, and the parts' last bit is 2^-28.
 constexpr float kScaleT = 8.f;
 
 struct ChunkArgs {
@@ -142,7 +144,9 @@ constexpr int kPBeta = kPSum + 4 * kDeltaDim * 4;
 constexpr int kPMisc = kPBeta + kChunk * 4;
 constexpr int kPRowMax = kPMisc + 256;            // [2 halves of the channels][64 rows]: largest |k| and |q|, as bf16
 constexpr int kPRowScale = kPRowMax + 2 * kChunk * 4;   // [64] keys, [64] queries: what a row's is times, twice as bf16
-constexpr int kPrepSmem = kPRowScale + 2 * kChunk * 4;
+constexpr int kPBetaM = kPRowScale + 2 * kChunk * 4;    // [64]: m
+constexpr int kPBetaP = kPBetaM + kChunk * 4;           // [64]: p
+constexpr int kPrepSmem = kPBetaP + kChunk * 4;
 static_assert(kChunk * 256 <= kChunk * kLdA * 4, "the lower halves in A's place");
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 
   float* tab = reinterpret_cast<float*>(smem + kPTab);
   float* beta = reinterpret_cast<float*>(smem + kPBeta);
-  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: (16) growth; (24) unsafe lanes; (32) largest |beta|; (40) largest |T|
+  float* misc = reinterpret_cast<float*>(smem + kPMisc);   // per warp: (16) growth; (24) unsafe lanes; (32) largest p; (40) largest |T|
   float* A = reinterpret_cast<float*>(smem + kPA);
   bool bad = false;
 
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   }
   uint32_t* rowmax = reinterpret_cast<uint32_t*>(smem + kPRowMax);
   uint32_t *key_scale = reinterpret_cast<uint32_t*>(smem + kPRowScale), *query_scale = key_scale + kChunk;
+  float *beta_m = reinterpret_cast<float*>(smem + kPBetaM), *beta_p = reinterpret_cast<float*>(smem + kPBetaP);
   const float bt = tid < kChunk && tid < n ? __ldg(x.beta + (row0 + tid) * x.ld_beta + h) : 0.f;
   {
     // a row's largest |k| (low half) and |q| (high half) over this warp's 64 channels: lanes hand half of their rows on
@@ -404,17 +409,22 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     if (kb == 0u || bad) ke = 127u;
     if (qb == 0u || bad) qe = 127u;
     key_scale[tid] = (254u - ke) * (128u * 0x10001u), query_scale[tid] = (254u - qe) * (128u * 0x10001u);
-    const float length = __uint_as_float(ke << 23), bv = bt * length, bk = bv * length;
+    // of the key's length and beta: A's beta, K P's p and the values' power of two (a beta of 0 leaves nothing of its row)
+    const float length = __uint_as_float(ke << 23), bv = bt * length;
+    const uint32_t be = (__float_as_uint(bv) >> 23) & 0xFFu;
+    const float pv = __uint_as_float(be << 23), pk = pv * length;
     // the power of two of query and scale; of a row without outputs (a zero query or scale) any
     const int se = (int)((__float_as_uint(x.scale) >> 23) & 0xFFu);
     int oe = (int)qe + se - 127;
     if (qb == 0u || x.scale == 0.f) oe = 127;
-    bad |= !(fabsf(bv) <= 0x1p20f) || !(fabsf(bk) <= 0x1p20f) || oe < 1 || oe > 254 || se == 255 || (se == 0 && x.scale != 0.f);
-    beta[tid] = bk;
+    bad |= (be == 0u && bv != 0.f) || !(fabsf(bv) <= 0x1p60f) || !(pk <= 0x1p60f) || oe < 1 || oe > 254 || se == 255 || (se == 0 && x.scale != 0.f);
+    beta[tid] = bv * length;
+    beta_p[tid] = pk;
+    beta_m[tid] = be == 0u ? 1.f : __uint_as_float((__float_as_uint(bv) & 0x807FFFFFu) | 0x3F800000u);
     float* hd = reinterpret_cast<float*>(rec + kRecHead);
-    hd[kHdV + tid] = bv;
+    reinterpret_cast<uint16_t*>(hd + kHdV)[tid] = (uint16_t)(be << 7);
     reinterpret_cast<uint32_t*>(hd)[kHdO + tid] = (uint32_t)oe * (128u * 0x10001u);
-    const float mb = max_warp(bad ? 0.f : fabsf(bk));
+    const float mb = max_warp(bad ? 0.f : pk);
     if (lane == 0) misc[32 + warp] = mb;
   }
   const f32x2 one = pack2(1.f, 1.f);
@@ -459,7 +469,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   bad |= !(mg <= 1024.f);
   // powers of two that bring the operands into fp16's range, from bounds: products of decays grow no further than mg
   const float sc_k = pow2_scale(mk * mg, 14);                        // of K D and Q P
-  const float sc_kp = pow2_scale(mb * mk * mg, 14);                  // of beta K P
+  const float sc_kp = pow2_scale(mb * mk * mg, 14);                  // of p K P
   const float sc_b = pow2_scale(mk * mk * mg * 128.f, 14);
 #pragma unroll
   for (int t = 0; t < 16; t += 4) {
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       const f32x2 k = bf16x2_to_f32x2(kr[t]), ql = mul2(bf16x2_to_f32x2(qr[t]), l), w = mul2(l, c);
       uint32_t hi2, lo2;
       const uint32_t o = swz128(img + r * 128);
-      const float b = beta[r];
+      const float b = beta_p[r];
       split_f16(mul2(mul2(k, pack2(b, b)), mul2(l, pre_k)), hi2, lo2);
       *reinterpret_cast<uint32_t*>(rec + kRecKp + o) = hi2;
       *reinterpret_cast<uint32_t*>(rec + kRecKp + kTileBytes + o) = lo2;
@@ -701,14 +711,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     mul_tile<32>(A + (32 + r) * kLdA + 32, kLdA, tmp + cc, kLdT, A + (32 + r) * kLdA + cc, kLdA, -1.f);
   }
   __syncthreads();
-  // ---- T = (I + A)^-1 in two parts: a thread 16 columns of a row
+  // ---- T = (I + A)^-1 diag(m) in two parts: a thread 16 columns of a row
   {
     const int i = tid >> 2, j0 = 16 * (tid & 3);
     float t[16], m = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       const float4 r = *reinterpret_cast<const float4*>(A + i * kLdA + j0 + j);
-      t[j] = r.x, t[j + 1] = r.y, t[j + 2] = r.z, t[j + 3] = r.w;
+      const float4 bj = *reinterpret_cast<const float4*>(beta_m + j0 + j);
+      t[j] = r.x * bj.x, t[j + 1] = r.y * bj.y, t[j + 2] = r.z * bj.z, t[j + 3] = r.w * bj.w;
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) m = max_nan(m, fabsf(t[j]));
@@ -743,7 +754,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 // + 63, and turn each product into the next one's operand; warp 8 issues the MMAs,
 // warp 9 copies the operands, two chunks deep, warp 10 stores the outputs.  All
 // products are transposed, with the 128 values on the tensor core's rows:
-//   R^T [v][t] = (V^T - S (K P)^T) diag(beta)   A = S in two fp16 parts from TMEM, times beta K P's two (three products)
+//   R^T [v][t] = (V^T - S (K P)^T) diag(p)   A = S in two fp16 parts from TMEM, times p K P's two (three products)
 //   U^T = R^T T^T                  A = R in two parts
 //   dS  = U^T (K D)                A = U in two parts; K D as it lies (MN-major)
 //   out^T = S (Q P)^T + U^T B^T    times a power of two a row; one product each: the high parts' 11 bits, rounded, are more than bf16 keeps
@@ -772,10 +783,11 @@ constexpr int kCOffPart2 = 2 * kPart1;                  // one buffer: its produ
 constexpr int kCOffV = kCOffPart2 + kPart2;
 constexpr int kCOffOut = kCOffV + 2 * kChunk * kRowBytes;
 constexpr int kCOffHead = kCOffOut + kChunk * kRowBytes;
-constexpr int kCHead = 1088;                            // bytes of a head's buffer
+constexpr int kCHead = (kHeadBytes + 127) & ~127;       // bytes of a head's buffer
 constexpr int kCOffX = kCOffHead + 2 * kCHead;             // exchanged maxima [2 parities][3 kinds][2 halves][128]
 constexpr int kCOffRow = kCOffX + 2 * 3 * 2 * 128 * 4;  // [2][64]: what the rows' outputs are times
-constexpr int kCOffBars = kCOffRow + 2 * kChunk * 4;
+constexpr int kCOffRowV = kCOffRow + 2 * kChunk * 4;    // [2][64] bf16: what the rows' values are times
+constexpr int kCOffBars = kCOffRowV + 2 * kHeadVBytes;
 constexpr int kCNumBars = 21;
 constexpr int kCOffMisc = kCOffBars + kCNumBars * 8;
 constexpr int kChainSmem = 1024 + kCOffMisc + 40;
@@ -864,7 +876,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       auto copy_v = [&](int c) {
         const int s = c & 1, rows = min(kChunk, n - c * kChunk);
         if (c >= 2 && !mbar_wait_warp(empty_v(s), ((c >> 1) & 1) ^ 1, abort_flag, p.s.status)) return false;
-        if (elect_one()) mbar_arrive_expect_tx(full_v(s), rows * kRowBytes);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full_v(s), rows * kRowBytes + kHeadVBytes);
+          if (c > 0) bulk_load(sm + kCOffRowV + s * kHeadVBytes, rec + c * rec_step + kRecHead + 4 * kHdV, kHeadVBytes, full_v(s));
+        }
         __syncwarp();
         for (int t = lane; t < rows; t += 32)
           bulk_load(sm + kCOffV + (s * kChunk + t) * kRowBytes, x.v + (row0 + c * kChunk + t) * x.ld_v + (int64_t)h * kDeltaDim,
@@ -875,6 +890,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       };
       ok = copy_v(0);
       grid_dep_wait();   // the records
+      if (elect_one()) bulk_load(sm + kCOffRowV, rec + kRecHead + 4 * kHdV, kHeadVBytes, full_v(0));
+      __syncwarp();
       for (int c = 0; c < chunks && ok; ++c) {
         const int s = c & 1;
         const uint8_t* src = rec + c * rec_step;
@@ -1063,10 +1080,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
     auto read_v = [&](int c) {
       const int s = c & 1, left = min(kChunk, n - c * kChunk) - 32 * half;
       wait(full_v(s), (c >> 1) & 1);
+      const uint32_t* by = reinterpret_cast<const uint32_t*>(smem + kCOffRowV + s * kHeadVBytes) + 16 * half;
       const uint16_t* vp = reinterpret_cast<const uint16_t*>(smem + kCOffV) + (s * kChunk + 32 * half) * kDeltaDim + v;
 #pragma unroll
       for (int t = 0; t < 16; ++t)
-        vr[t] = __byte_perm((uint32_t)vp[2 * t * kDeltaDim], (uint32_t)vp[(2 * t + 1) * kDeltaDim], 0x5410);
+        vr[t] = mul_bf16x2(__byte_perm((uint32_t)vp[2 * t * kDeltaDim], (uint32_t)vp[(2 * t + 1) * kDeltaDim], 0x5410), by[t]);
       if (left < 32) {   // rows that are not there
 #pragma unroll
         for (int t = 0; t < 16; ++t) vr[t] = 2 * t >= left ? 0u : 2 * t + 1 >= left ? vr[t] & 0xFFFFu : vr[t];
@@ -1077,11 +1095,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       uint32_t m = 0;
 #pragma unroll
       for (int t = 0; t < 16; ++t) m = __vmaxu2(m, vr[t] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+      xchg(s, kMaxV, half) = __uint_as_float(m << 16);
       __syncwarp();   // all lanes have read what the next copy overwrites
       if (lane == 0) mbar_arrive(empty_v(s));
-      return bar_state_or(max(m & 0xFFFFu, m >> 16) >= 0x7480u);   // 2^106: times what a row's value is times within fp32's range
+      return bar_state_or(m >= 0x7F80u);
     };
-    bool rowwise = false;   // a value of the chunk is no number, or a very large one
+    bool rowwise = false;   // a value of the chunk is no number, or not in bf16's range as it is taken
     if (chunks > 0) {
       read_v(0);
       rowwise = vote(0);
@@ -1137,17 +1157,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
       wait(full(s), (c >> 1) & 1);
       rowwise |= reinterpret_cast<const int*>(hd)[kHdBad] != 0;
       if (tid == 0) by_rows[s] = rowwise;
-      const float* row_v = hd + kHdV + 32 * half;   // what these rows' values are times
-      if (!rowwise) {
-        float m = 0.f;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const float2 by = *reinterpret_cast<const float2*>(row_v + 2 * t), r = mul2(bf16x2_to_f32x2(vr[t]), by);
-          m = fmaxf(fmaxf(m, fabsf(r.x)), fabsf(r.y));
-        }
-        xchg(s, kMaxV, half) = m;
-        bar_pair(warp & 3);
-      }
       wait(b_r, c & 1);
       if (rowwise) {
         // back to the state itself
@@ -1210,7 +1219,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Chu
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           const f32x2 r = fma2(pack2(-inv_kp, -inv_kp), pack2(__uint_as_float(acc[2 * t]), __uint_as_float(acc[2 * t + 1])),
-                               mul2(bf16x2_to_f32x2(vr[t]), *reinterpret_cast<const float2*>(row_v + 2 * t)));
+                               bf16x2_to_f32x2(vr[t]));
           split_f16(mul2(r, pack2(sc_r, sc_r)), hi[t], lo[t]);
           top = max_abs_f16x2(top, hi[t]);
         }
