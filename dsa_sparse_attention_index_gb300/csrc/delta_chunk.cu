@@ -409,18 +409,19 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
     if (kb == 0u || bad) ke = 127u;
     if (qb == 0u || bad) qe = 127u;
     key_scale[tid] = (254u - ke) * (128u * 0x10001u), query_scale[tid] = (254u - qe) * (128u * 0x10001u);
-    // of the key's length and beta: A's beta, K P's p and the values' power of two (a beta of 0 leaves nothing of its row)
+    // of the key's length and beta: A's beta, K P's p and the values' power of two (a beta of 0 leaves nothing of its row,
+    // one below 2^-126 has a smaller m)
     const float length = __uint_as_float(ke << 23), bv = bt * length;
-    const uint32_t be = (__float_as_uint(bv) >> 23) & 0xFFu;
+    const uint32_t be = bv == 0.f ? 0u : max(1u, (__float_as_uint(bv) >> 23) & 0xFFu);
     const float pv = __uint_as_float(be << 23), pk = pv * length;
     // the power of two of query and scale; of a row without outputs (a zero query or scale) any
     const int se = (int)((__float_as_uint(x.scale) >> 23) & 0xFFu);
     int oe = (int)qe + se - 127;
     if (qb == 0u || x.scale == 0.f) oe = 127;
-    bad |= (be == 0u && bv != 0.f) || !(fabsf(bv) <= 0x1p60f) || !(pk <= 0x1p60f) || oe < 1 || oe > 254 || se == 255 || (se == 0 && x.scale != 0.f);
+    bad |= !(fabsf(bv) <= 0x1p60f) || !(pk <= 0x1p60f) || oe < 1 || oe > 254 || se == 255 || (se == 0 && x.scale != 0.f);
     beta[tid] = bv * length;
     beta_p[tid] = pk;
-    beta_m[tid] = be == 0u ? 1.f : __uint_as_float((__float_as_uint(bv) & 0x807FFFFFu) | 0x3F800000u);
+    beta_m[tid] = bv * __uint_as_float((254u - be) << 23);
     float* hd = reinterpret_cast<float*>(rec + kRecHead);
     reinterpret_cast<uint16_t*>(hd + kHdV)[tid] = (uint16_t)(be << 7);
     reinterpret_cast<uint32_t*>(hd)[kHdO + tid] = (uint32_t)oe * (128u * 0x10001u);

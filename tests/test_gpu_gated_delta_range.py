@@ -71,6 +71,20 @@ def test_long_keys_among_ordinary_ones(length, at):
     check_out(out, want, 130, size, mass, q)
 
 
+@pytest.mark.parametrize("beta", [1e-38, 1e-40, 1e-45, -0.5, 0.0])
+@pytest.mark.parametrize("length", [1.0, 1e-15, 1e15])
+def test_betas_at_the_ends_of_their_range(beta, length):
+    """Every third row: betas below the normal numbers, negative ones, and none; beside keys of any length."""
+    x, s0 = inputs(130, 2, 2, seed=53), state(2)
+    q, k, v, g, b = x
+    k[1::5] = (k[1::5].float() * length).to(torch.bfloat16)
+    b[1::5] *= length ** -2
+    b[::3] = beta if beta > -0.1 else beta * b[::3].sign() / k[::3].float().square().sum(2).clamp(min=1.0)
+    out, last = prefill(x, s0)
+    want, states, size, mass = rule(*x, SCALE, s0[0])
+    check_bits(last, states[-1], torch.stack([norms(s) for s in states]).amax(0))
+
+
 @pytest.mark.parametrize("length", [1e3, 1e5])
 def test_long_values_with_small_betas(length):
     x, s0 = inputs(130, 2, 2, seed=42), state(2)
