@@ -132,11 +132,11 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 // so was K D made by the warps that the inverse leaves idle (312 us for 302 in all).
 constexpr int kPrepThreads = 256;
 constexpr int kPX = 0;                            // X = k L c, fp32: 64 rows x 512 bytes
-constexpr int kPQ = kPX + kChunk * 512;           // q L c, tf32: 64 rows x 256 bytes of the upper halves
-constexpr int kPY = kPQ + kChunk * 256;           // Y, fp32
+constexpr int kPY = kPX + kChunk * 512;           // Y, fp32
+constexpr int kPQ = kPY + kChunk * 512;           // q L c, tf32: 64 rows x 512 bytes, of which the second half in A's place
 constexpr int kPartHalf = kChunk * 256;           // X and Y as two fp16 parts, one behind the other
 constexpr int kLdA = kChunk + 4;                  // floats: rows start four banks apart
-constexpr int kPA = kPY + kChunk * 512;           // the lower halves of q L c, then A, then (I + A)^-1, fp32 [64][68]
+constexpr int kPA = kPQ + kChunk * 256;           // A, then (I + A)^-1, fp32 [64][68]
 constexpr int kPB = kPA + kChunk * kLdA * 4;    // B, fp16, the record's image
 constexpr int kPTab = kPB + kTileHalf;            // block products [4][128]
 constexpr int kPSum = kPTab + 4 * kDeltaDim * 4;  // sums of their logarithms
@@ -147,7 +147,7 @@ constexpr int kPRowScale = kPRowMax + 2 * kChunk * 4;   // [64] keys, [64] queri
 constexpr int kPBetaM = kPRowScale + 2 * kChunk * 4;    // [64]: m
 constexpr int kPBetaP = kPBetaM + kChunk * 4;           // [64]: p
 constexpr int kPrepSmem = kPBetaP + kChunk * 4;
-static_assert(kChunk * 256 <= kChunk * kLdA * 4, "the lower halves in A's place");
+static_assert(kChunk * 256 <= kChunk * kLdA * 4, "queries in A's place");
 static_assert(2 * (kPrepSmem + 2048) <= 233472, "two CTAs per SM");
 
 // Offset of eight channels c of row r in rows of 512 bytes of fp32 and of 256 bytes of
@@ -179,7 +179,7 @@ __device__ __forceinline__ void tile_xy(const uint8_t* smem, int x0, int y0, flo
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   // rows x0 + g, x0 + g + 8 and y0 + g: the same place in a row's exchanged pieces (x0 and y0 are multiples of eight)
   const uint8_t* X = smem + kPX + (x0 + g) * 512 + 8 * t;
-  const uint8_t* Q = smem + kPQ + (x0 + g) * 256 + 4 * t;
+  const uint8_t* Q = smem + kPQ + (x0 + g) * 512 + 8 * t;
   const uint8_t* Y = smem + kPY + (y0 + g) * 512 + 8 * t;
   float lh[4], hl[4], ql[4];   // sums of their own: short chains of products
 #pragma unroll
@@ -190,14 +190,12 @@ __device__ __forceinline__ void tile_xy(const uint8_t* smem, int x0, int y0, flo
     const float2 xa = *reinterpret_cast<const float2*>(X + 32 * piece);
     const float2 xb = *reinterpret_cast<const float2*>(X + 32 * piece + 8 * 512);
     const float2 y = *reinterpret_cast<const float2*>(Y + 32 * piece);
-    const uint32_t qa = *reinterpret_cast<const uint32_t*>(Q + 16 * piece);
-    const uint32_t qb = *reinterpret_cast<const uint32_t*>(Q + 16 * piece + 8 * 256);
+    const uint2 qa = *reinterpret_cast<const uint2*>(Q + 32 * piece);
+    const uint2 qb = *reinterpret_cast<const uint2*>(Q + 32 * piece + 8 * 512);
     uint32_t xh[4], xl[4], yh[2], yl[2];
     split_tf32(xa.x, xh[0], xl[0]), split_tf32(xb.x, xh[1], xl[1]), split_tf32(xa.y, xh[2], xl[2]), split_tf32(xb.y, xh[3], xl[3]);
     split_tf32(y.x, yh[0], yl[0]), split_tf32(y.y, yh[1], yl[1]);
-    const uint32_t la = *reinterpret_cast<const uint32_t*>(Q + 16 * piece + (kPA - kPQ));
-    const uint32_t lb = *reinterpret_cast<const uint32_t*>(Q + 16 * piece + 8 * 256 + (kPA - kPQ));
-    const uint32_t q[4] = {__byte_perm(la, qa, 0x5410), __byte_perm(lb, qb, 0x5410), __byte_perm(la, qa, 0x7632), __byte_perm(lb, qb, 0x7632)};
+    const uint32_t q[4] = {qa.x, qb.x, qa.y, qb.y};
     mma_16x8x8(lh, xl, yh);
     mma_16x8x8(hl, xh, yl);
     mma_16x8x8(kk, xh, yh);
@@ -519,9 +517,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
       *reinterpret_cast<uint32_t*>(rec + kRecQp + o) = f16x2(qp.x, qp.y);
       const uint32_t s = at512(r, piece) + 2 * in_piece;
       *reinterpret_cast<f32x2*>(smem + kPX + s) = mul2(k, w);
-      const uint32_t qx = tf32_rn(xq.x), qy = tf32_rn(xq.y), oq = at256(r, piece) + in_piece;
-      *reinterpret_cast<uint32_t*>(smem + kPQ + oq) = __byte_perm(qx, qy, 0x7632);
-      *reinterpret_cast<uint32_t*>(smem + kPA + oq) = __byte_perm(qx, qy, 0x5410);
+      *reinterpret_cast<uint2*>(smem + kPQ + s) = make_uint2(tf32_rn(xq.x), tf32_rn(xq.y));
       // Y of the block itself: k / (L c); no number where the block is not safe, and not used there
       *reinterpret_cast<f32x2*>(smem + kPY + s) = mul2(k, pack2(reciprocal(wf.x), reciprocal(wf.y)));
     }
@@ -574,7 +570,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
   float dk[4], dq[4];
   if (safe) tile_xy(smem, 16 * D, 16 * D + 8 * (warp & 1), dk, dq);
   __syncthreads();
-  // (now that nothing reads the queries' lower halves) A and B within the blocks, and zeros right of A's diagonal blocks
+  // (now that nothing reads the queries) A and B within the blocks, and zeros right of A's diagonal blocks
   {
     for (int i = tid; i < 6 * 64; i += kPrepThreads) {
       const int blk = i >> 6, r = (i >> 2) & 15, br = blk < 3 ? 0 : blk < 5 ? 1 : 2, bc = blk < 3 ? blk + 1 : blk < 5 ? blk - 1 : 3;
