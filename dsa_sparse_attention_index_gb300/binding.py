@@ -502,8 +502,9 @@ def _rows_of(name: str, t, shape, dtypes):
 
 
 class _Descriptor:
-    """A descriptor's `layout`, made from its tensors and made again once one of them has another address, shape or
-    strides (resized, set_() or with new .data); `seen` is of the tensors that it was made from."""
+    """A descriptor's `layout`, made from its tensors and made again, with all checks, once one of them has another
+    address (resized, set_() or with new .data), or the rows' number has changed; a tensor's other sizes and its strides
+    have to stay as long as its address does (looking at all of them takes 2 us a call).  `seen`: what it was made from."""
 
     def __post_init__(self):
         self.read()
@@ -525,8 +526,7 @@ class StatePool(_Descriptor):
     states: torch.Tensor
 
     def places(self):
-        t = self.states
-        return t.data_ptr(), t.shape, t.stride()
+        return self.states.data_ptr(), self.states.shape
 
     def describe(self):
         t = self.states
@@ -551,9 +551,8 @@ class DeltaRows(_Descriptor):
     scale: float
 
     def places(self):
-        q, k, v, g, b = self.q, self.k, self.v, self.gate, self.beta
-        return (q.data_ptr(), q.shape, q.stride(), k.data_ptr(), k.shape, k.stride(), v.data_ptr(), v.shape, v.stride(),
-                g.data_ptr(), g.shape, g.stride(), b.data_ptr(), b.shape, b.stride())
+        return (self.q.data_ptr(), self.k.data_ptr(), self.v.data_ptr(), self.gate.data_ptr(), self.beta.data_ptr(),
+                self.v.shape)
 
     def describe(self):
         if self.q.dim() != 3 or self.v.dim() != 3:

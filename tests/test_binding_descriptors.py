@@ -82,12 +82,22 @@ def test_tensors_that_no_longer_fit_are_refused(library, call, name):
     states, t = things()
     pool, x = B.StatePool(states), layer(**t)
     call(pool, x)
-    t[name].move(shape=(5, *NAMES[name][1:]))
+    t[name].move(1 << 30, shape=(5, *NAMES[name][1:]))
     with pytest.raises(ValueError):
         call(pool, x)
-    t[name].move(shape=NAMES[name])
+    t[name].move(1 << 31, shape=NAMES[name])
     call(pool, x)
-    t[name].move(strides=tuple(2 * s for s in t[name].stride()))
+    t[name].move(1 << 32, strides=tuple(2 * s for s in t[name].stride()))
+    with pytest.raises(ValueError):
+        call(pool, x)
+
+
+@pytest.mark.parametrize("call", [decode, prefill])
+def test_rows_that_grow_in_place_are_refused(library, call):
+    """Values of a buffer with room for more rows, the others without."""
+    states, t = things()
+    pool, x = B.StatePool(states), layer(**t)
+    t["v"].move(shape=(12, 4, 128))
     with pytest.raises(ValueError):
         call(pool, x)
 
