@@ -197,7 +197,7 @@ __device__ __forceinline__ uint2 e4m3x8(uint4 v, float s) {
 
 // One warp per new token row, its slot given; -1 is a padding row.  append_row's
 // encodings, 16 bytes a load and nothing shared between warps: a row's reads are all
-// on their way before the first is used.  16,385 rows (34.7 MB): 10.3 us in a graph,
+// on their way before the first is used.  16,385 rows (34.7 MB): 9.4 us in a graph,
 // a CTA a row took 25.7; bound by the correctly rounded divisions, then bytes.
 constexpr int kSlotWarps = 8;
 template <bool NV, bool KEY8>

@@ -122,7 +122,7 @@ __device__ __forceinline__ void list_long(const DeltaSeqs& s) {
 // and three CTAs an SM, 96 KB are on their way.  32 sequences x 96 heads read and
 // write 0.41 GB in 61.4 us (6.6 TB/s, 0.97 of the measured copy); two CTAs an SM
 // take 72, two rows a thread and five CTAs 67, one row a thread 90.  Few heads are
-// no faster in smaller parts (32 heads: 3.2 us).  Prompt calls have an instance of their own:
+// no faster in smaller parts (32 heads: 2.8 us).  Prompt calls have an instance of their own:
 // with their ranges and list in it decode takes 168 registers for 152, and 1 to 8 % longer.
 template <bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 3) delta_rows_kernel(const DeltaRows x, const DeltaSeqs s, uint16_t* out) {

@@ -17,8 +17,8 @@
 // Two kernels.  delta_prepare_kernel: everything that does not depend on the
 // state, a CTA per chunk and head, into a record of operands laid out as the tensor
 // core reads them.  delta_chain_kernel: a CTA per sequence and head walks the
-// chunks; the state stays in registers in fp32.  2,048 rows of 96 heads: 168 us and
-// 134 us (row by row 5,478 us).
+// chunks; the state stays in registers in fp32.  2,048 rows of 96 heads: 177 us and
+// 143 us (row by row 5,478 us).
 #include <algorithm>
 #include <atomic>
 
@@ -123,10 +123,10 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 // the way into the mma; between blocks they are two fp16 times a power of two, made once.
 // Three products either way, 21 bits; the queries one factor of 11 bits, rounded (as bf16 in the blocks
 // they put outputs 2.0e-3 off instead of 1.7e-3, which is bf16's own rounding).  (Two bf16 parts everywhere left states 7 to 10e-7
-// off instead of 4 to 5e-7; tf32 everywhere took 5 % longer.)  The inverse of I + A goes by
+// off instead of 4 to 6e-7; tf32 everywhere took 5 % longer.)  The inverse of I + A goes by
 // blocks: the diagonal ones by substitution, a thread a column, while other warps make
 // tiles, then two levels of products.
-// What bounds it: 33,200 warp instructions a chunk and head at 2.0 a cycle, nine phases that wait for
+// What bounds it: 34,800 warp instructions a chunk and head at 2.1 a cycle, ten phases that wait for
 // each other's warps; its memory traffic could go at twice the rate.  16 warps an SM, as registers and
 // shared memory allow; 512 threads a CTA or 16-byte pieces a thread were slower, and
 // so was K D made by the warps that the inverse leaves idle (312 us for 302 in all).
@@ -758,13 +758,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prepare_kernel(const Ch
 // The parts of a row of S, R or U are times a power of two, so that they keep 21 bits of
 // its largest element whatever its size: of S from the row's largest element itself, which the
 // two warps of a row exchange before they split it (a bound carried from chunk to chunk would
-// not see a state decay, and its parts would be lost: 0 to 2 % of a call); of R and U from bounds made of maxima
+// not see a state decay, and its parts would be lost; 5 us of 2,048 rows); of R and U from bounds made of maxima
 // that they exchange one step later, which may be loose: fp16's exponents leave room for 2^18.
 // Where something in a chunk is no finite number, or leaves the powers' range, its rows
 // go one by one: the zeros of T and B would carry a NaN to the rows before it.
-// What bounds it: a chain of latencies, 7,700 cycles a chunk, of which the tensor pipe
+// What bounds it: a chain of latencies, 7,300 to 7,600 cycles a chunk, of which the tensor pipe
 // works 2,200: three products that wait for each other, their way through TMEM, and the
-// conversions between them (S 940 cycles, R 680, U 530, the update 780).  Outputs are
+// conversions between them (S 660 cycles and 370 for its largest element, R 740, U 450, the update 940).  Outputs are
 // converted while R is made, the next values read while the update is.
 constexpr int kChainThreads = 12 * 32;   // three warpgroups: two of state warps, one of the rest (its last warp has no work)
 // Of the block's 384 x 168 registers the state warps take 200 a thread and leave 104 to the others: with 168 they spill.

@@ -52,10 +52,10 @@ __device__ __forceinline__ int2 lengths_of(const SlotArgs& a, int i) {
 }
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
 
-// Bound by a chain of latencies: lengths, scan, search, page, store (64 requests: 3.8
+// Bound by a chain of latencies: lengths, scan, search, page, store (64 requests: 3.9
 // us in a graph, of which a launch takes 2.3), and with many rows by the search and
 // the page's address, 16 bytes of positions and of slots a thread and turn (2,048
-// requests, 262,144 rows: 14.4 us in 16 CTAs; row by row in 8 CTAs 26).
+// requests, 262,144 rows: 14.7 us in 16 CTAs; row by row in 8 CTAs 26).
 // One cluster.  Every CTA scans the requests (a tile of 2,048 at a time, kept
 // in shared memory) and places its share of the rows; nothing that the caller
 // may pass as input and output at once (lengths, the stack's count) is written

@@ -624,7 +624,7 @@ dsa_status_t dsa_cache_append_slots(const dsa_paged_cache_t* cache, const int32_
  *   S   = S~ + u k_t^T
  *   out = scale * S q_t                     (bf16, round-to-nearest)
  * in fp32.  A gate of -inf forgets the channel.  The state needs |beta| |k|^2 <= 2 and
- * gates of at most 0 to stay bounded; nothing else is asked of them.
+ * gates of at most 0 to stay bounded; nothing else is asked of them, and rows may differ in size by any factor.
  *
  * gated_delta_decode: rows r = b * queries_per_seq + j, as in dsa_batch_t.
  *   slots_in   device int32 [batch]: the slot of the state that sequence b starts from, or -1: zeros
@@ -637,11 +637,11 @@ dsa_status_t dsa_cache_append_slots(const dsa_paged_cache_t* cache, const int32_
  *   workspace  >= gated_delta_prefill_workspace_size(rows, batch, heads) bytes, 256-B aligned:
  *              105 KB a head for every 64 rows (2,048 rows of 96 heads: 0.33 GB)
  * Sequences of more than 20 rows are taken 64 rows at a time on the tensor cores, with
- * operands of 21 bits, so that states keep fp32's accuracy (after 2,048 rows 5e-7 of their norm,
- * where one row after another gives 1.4e-6); their outputs' products take 11 bits and one bf16
- * factor, beside the output's own rounding.  Where a value in 64 rows is no finite number
- * or the numbers leave fp32's range, these rows of the head go one by one, so that rows before a
- * NaN keep their values.  Three launches (one for up to 20 rows); decode: one.
+ * operands of 21 bits, so that states keep fp32's accuracy (after 2,048 rows 4 to 6e-7 of their norm,
+ * where one row after another gives up to 1.6e-6), relative to the largest state of the 64 rows; their
+ * outputs' products take 11 bits, rounded, beside the output's own rounding to bf16.  Where a value in 64 rows
+ * is no finite number or the numbers leave the range of the powers of two that they are taken with, these rows
+ * of the head go one by one, so that rows before a NaN keep their values.  Three launches (one for up to 20 rows); decode: one.
  * A slot in slots_out may be the same sequence's in slots_in; no other sequence of the
  * call may use it.  out: device bf16 bits [rows][heads][128], 16-byte aligned.
  * A slot outside the pool or row_starts that do not ascend within 0..rows raise
